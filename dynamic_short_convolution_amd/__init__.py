@@ -13,6 +13,8 @@ from .ops import (  # noqa: F401
     dynconv_bwd_workspace_size,
     dynconv_cache_fill,
     dynconv_decode_step,
+    dynconv_delta_fwd,
+    dynconv_delta_step,
     dynconv_fwd,
     dynconv_gemm_fwd,
     dynconv_gemm_lowrank_fwd,
@@ -21,5 +23,6 @@ from .ops import (  # noqa: F401
     dynconv_lowrank_decode_step,
     dynconv_lowrank_fwd,
     new_cache,
+    new_delta_state,
 )
 from ._lib import DynconvError, load  # noqa: F401

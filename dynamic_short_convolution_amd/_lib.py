@@ -50,6 +50,9 @@ EXPORTS = (
     "dynconv_lowrank_bwd_ex",
     "dynconv_lowrank_bwd_ex_workspace_size",
     "dynconv_lowrank_decode_step_ex",
+    "dynconv_delta_fwd",
+    "dynconv_delta_fwd_workspace_size",
+    "dynconv_delta_step",
 )
 
 # Bytes of the per-GPU scratch array of dynconv_bwd_ex_noalloc (DYNCONV_NOALLOC_SCRATCH_BYTES).
@@ -138,6 +141,15 @@ _SIGNATURES["dynconv_lowrank_decode_step_ex"] = (
     ctypes.c_int)
 _SIGNATURES["dynconv_cache_fill_varlen"] = (
     _SIGNATURES["dynconv_cache_fill"][0][:2] + [_vp, _i64p] + _SIGNATURES["dynconv_cache_fill"][0][2:], ctypes.c_int)
+# gated delta rule: (pointer, strides) pairs, then sizes, scale, eps, dtype
+_f32 = ctypes.c_float
+_delta_in = [_vp, _i64p] * 7  # q, k, v, g, beta, seq_idx, state_in
+_delta_sizes = [_i64] * 6     # B, T, Hk, Hv, dk, dv
+_SIGNATURES["dynconv_delta_fwd"] = (
+    _delta_in + [_vp, _i64p] * 2 + _delta_sizes + [_f32, _f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int)
+_SIGNATURES["dynconv_delta_fwd_workspace_size"] = (_delta_sizes + [ctypes.c_int], _sz)
+_SIGNATURES["dynconv_delta_step"] = (
+    [_vp, _i64p] * 7 + [_i64] * 5 + [_f32, _f32, ctypes.c_int, _vp], ctypes.c_int)
 
 _lib = None
 

@@ -28,6 +28,11 @@ SOURCES = [
     "dynconv_lowrank_fast.hip",
     "dynconv_decode.hip",
     "dynconv_gemm.hip",
+    "dynconv_delta_abi.hip",
+    "dynconv_delta.hip",
+    "dynconv_delta_f32.hip",
+    "dynconv_delta_bf16.hip",
+    "dynconv_delta_f16.hip",
 ]
 
 # -packed-fp32-ops: no v_pk_{add,mul,fma}_f32 are generated from ordinary float code.

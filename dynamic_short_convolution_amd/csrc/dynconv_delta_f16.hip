@@ -1,0 +1,8 @@
+// Gated delta rule kernels for f16 storage.
+#include "dynconv_delta_kernels.hpp"
+
+namespace dynconv {
+
+hipError_t delta_fwd_f16(const DeltaParams& p, hipStream_t s) { return delta::delta_fwd_et<f16_t>(p, s); }
+
+}  // namespace dynconv

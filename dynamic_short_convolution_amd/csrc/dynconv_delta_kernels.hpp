@@ -1,0 +1,770 @@
+// Chunked gated delta rule, gfx950. Per value head, with a_t = exp(g_t) and unit or raw q, k:
+//
+//   S_t = a_t S_{t-1} + k_t u_t^T,  u_t = beta_t (v_t - a_t S_{t-1}^T k_t),  o_t = scale S_t^T q_t.
+//
+// Over a chunk of 64 tokens with G_i the sum of g up to token i, Gam_ij = exp(G_i - G_j) for
+// i >= j, E_i = exp(G_i), D_j = exp(G_63 - G_j), gamma = exp(G_63) and S0 the state before it:
+//
+//   A_ij = beta_i Gam_ij k_i.k_j (i > j),   T = (I + A)^-1,
+//   Z = V - E (K S0),   U = T (beta Z),
+//   O = scale (E (Q S0) + (Gam o Q K^T) U),   S1 = gamma S0 + K^T (D U).
+//
+// A document start (packed sequences), or a decay so small that exp(g) is 0 in float32, cuts
+// every path across it: Gam_ij, E_i, D_j and gamma are 0 where one lies between.
+//
+// Work split. T, the only part with a serial inner dependence, does not involve the state: one
+// workgroup per (sequence, head, chunk) forms it (k_delta_prep). The state is carried by
+// k_delta_scan, one wave per 16 value columns: a matrix-core result holds rows 4q .. 4q+3 of
+// column lane % 16, which is what the next product takes as its right operand once the
+// contraction index is taken in the order (4q .. 4q+3 of one 16-row tile, then of the next);
+// so S0, Z, U and S1 of a wave's columns stay in its registers from product to product, and
+// only K, Q, T (left operands, shared by the workgroup's waves) pass through LDS.
+//
+// Precision. The matrix cores take bf16; a float32 operand enters as three terms of 8 bits
+// (mantissa split by truncation, exactly x = x0 + x1 + x2), a float16 one as two, a bf16 one
+// as itself, and the products of terms whose orders add up to more than 2 (below 2^-24 of the
+// result) are left out. That holds states and sums at float32 accuracy at 2.7 times the rate
+// of the float32 matrix instructions (6 products for two float32 operands, 3 for a bf16 one).
+// Products that only reach 16-bit results keep the terms up to order 1 (2^-16).
+#pragma once
+
+#include "dynconv_common.hpp"
+#include "dynconv_delta_internal.hpp"
+
+namespace dynconv {
+namespace delta {
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+
+constexpr int C = kDeltaChunk;
+
+template <typename ET>
+struct Store;  // terms of a stored element, and of an operand that only reaches stored results
+template <>
+struct Store<bf16_t> {
+  static constexpr int NT = 1, NP = 2;
+};
+template <>
+struct Store<f16_t> {
+  static constexpr int NT = 2, NP = 2;
+};
+template <>
+struct Store<float> {
+  static constexpr int NT = 3, NP = 3;
+};
+
+// N terms of 8 values each: values 0..3 of the first 16-row tile, 4..7 of the second.
+template <int N>
+struct Frag {
+  u32x4 t[N];
+};
+
+// c += sum over terms (i, j) with i + j <= L of a_i b_j.
+template <int L, int NA, int NB>
+__device__ __forceinline__ void mma(f32x4_t& c, const Frag<NA>& a, const Frag<NB>& b) {
+#pragma unroll
+  for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = NB - 1; j >= 0; --j)
+      if (i + j <= L)
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a.t[i]),
+                                                    __builtin_bit_cast(bf16x8_t, b.t[j]), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t top2(float lo, float hi) {  // upper halves of two floats
+  return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
+__device__ __forceinline__ float below(float x) {  // x without its first 8 significant bits, exact
+  return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+}
+
+template <int N>
+__device__ __forceinline__ Frag<N> split8(f32x4_t a, f32x4_t b) {
+  Frag<N> f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    f.t[n] = u32x4{top2(a[0], a[1]), top2(a[2], a[3]), top2(b[0], b[1]), top2(b[2], b[3])};
+    if (n + 1 < N) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        a[e] = below(a[e]);
+        b[e] = below(b[e]);
+      }
+    }
+  }
+  return f;
+}
+
+// Left operand of tile row0 .. row0+15 from a row-major LDS matrix: contraction over columns
+// col0 .. col0+31 in fragment order. Planes (terms) lie `plane` elements apart.
+template <int N>
+__device__ __forceinline__ Frag<N> rowfrag(const uint16_t* m, int ld, int plane, int row0, int col0) {
+  const int lane = threadIdx.x & 63;
+  const uint16_t* p = m + (row0 + (lane & 15)) * ld + col0 + 4 * (lane >> 4);
+  Frag<N> f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const u32x2 a = *reinterpret_cast<const u32x2*>(p + n * plane);
+    const u32x2 b = *reinterpret_cast<const u32x2*>(p + n * plane + 16);
+    f.t[n] = u32x4{a[0], a[1], b[0], b[1]};
+  }
+  return f;
+}
+
+// The transposed operand: index col0 + lane % 16, contraction over rows row0 .. row0+31. A
+// 16-lane group's transposing read returns to lane i element i % 4 of what lanes i / 4 + 4e
+// loaded, so lane j loads row 4q + j / 4, columns 4 (j % 4) .. + 3.
+template <int N>
+__device__ __forceinline__ Frag<N> colfrag(const uint16_t* m, int ld, int plane, int row0, int col0) {
+  const int lane = threadIdx.x & 63;
+  const int q = lane >> 4, j = lane & 15;
+  const uint16_t* p = m + (row0 + 4 * q + (j >> 2)) * ld + col0 + 4 * (j & 3);
+  Frag<N> f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + n * plane));
+    const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + n * plane + 16 * ld));
+    const u32x2 ua = __builtin_bit_cast(u32x2, a), ub = __builtin_bit_cast(u32x2, b);
+    f.t[n] = u32x4{ua[0], ua[1], ub[0], ub[1]};
+  }
+  return f;
+}
+
+// LDS image of a lower-triangular matrix: rows 0..31 of 40 elements (32 used), rows 32..63 of 72.
+constexpr int kTrapLds = 32 * 40 + 32 * 72;
+__device__ __forceinline__ constexpr int trap_off(int i) { return i < 32 ? i * 40 : 1280 + (i - 32) * 72; }
+template <int N>
+__device__ __forceinline__ Frag<N> trap_row(const uint16_t* m, int tile, int kb) {  // kb <= tile / 2
+  return tile < 2 ? rowfrag<N>(m, 40, kTrapLds, 16 * tile, 0) : rowfrag<N>(m + 1280, 72, kTrapLds, 16 * tile - 32, 32 * kb);
+}
+template <int N>
+__device__ __forceinline__ Frag<N> trap_col(const uint16_t* m, int tile, int kb) {  // kb >= tile / 2
+  return kb == 0 ? colfrag<N>(m, 40, kTrapLds, 0, 16 * tile) : colfrag<N>(m + 1280, 72, kTrapLds, 0, 16 * tile);
+}
+// The same for an upper-triangular matrix: rows 0..31 of 72 (64 used), rows 32..63 of 40
+// (columns 32..63).
+__device__ __forceinline__ constexpr int utrap_off(int i, int j) {
+  return i < 32 ? i * 72 + j : 2304 + (i - 32) * 40 + j - 32;
+}
+template <int N>
+__device__ __forceinline__ Frag<N> utrap_row(const uint16_t* m, int tile, int kb) {  // kb >= tile / 2
+  return tile < 2 ? rowfrag<N>(m, 72, kTrapLds, 16 * tile, 32 * kb) : rowfrag<N>(m + 2304, 40, kTrapLds, 16 * tile - 32, 0);
+}
+
+// Writes 4 consecutive elements' N terms.
+template <int N>
+__device__ __forceinline__ void put4(uint16_t* p, int plane, f32x4_t x) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    *reinterpret_cast<u32x2*>(p + n * plane) = u32x2{top2(x[0], x[1]), top2(x[2], x[3])};
+    if (n + 1 < N) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = below(x[e]);
+    }
+  }
+}
+
+template <typename ET>
+__device__ __forceinline__ float ldf(const void* p, int64_t i) {
+  if constexpr (sizeof(ET) == 2) {
+    return Cvt<ET>::of_bits(static_cast<const uint16_t*>(p)[i]);
+  } else {
+    return static_cast<const float*>(p)[i];
+  }
+}
+template <typename ET>
+__device__ __forceinline__ void stf(void* p, int64_t i, float v) {
+  if constexpr (sizeof(ET) == 2) {
+    static_cast<uint16_t*>(p)[i] = Cvt<ET>::bits(v);
+  } else {
+    static_cast<float*>(p)[i] = v;
+  }
+}
+
+// 8 consecutive stored elements of a row, as loaded (zeros past `n` elements).
+template <typename ET>
+struct Raw8 {
+  u32x4 w[sizeof(ET) / 2];
+};
+template <typename ET>
+__device__ __forceinline__ Raw8<ET> load8(const void* base, int64_t off, int n, int vec) {
+  Raw8<ET> r;
+  if (n >= 8 && vec) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const ET*>(base) + off);
+#pragma unroll
+    for (int i = 0; i < int(sizeof(ET) / 2); ++i) r.w[i] = p[i];
+  } else {
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      e[i] = 0;
+      if (i < n) {
+        if constexpr (sizeof(ET) == 2) {
+          e[i] = static_cast<const uint16_t*>(base)[off + i];
+        } else {
+          e[i] = static_cast<const uint32_t*>(base)[off + i];
+        }
+      }
+    }
+    if constexpr (sizeof(ET) == 2) {
+      r.w[0] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+    } else {
+      r.w[0] = u32x4{e[0], e[1], e[2], e[3]};
+      r.w[1] = u32x4{e[4], e[5], e[6], e[7]};
+    }
+  }
+  return r;
+}
+template <typename ET>
+__device__ __forceinline__ void floats8(const Raw8<ET>& r, f32x4_t& a, f32x4_t& b) {
+  if constexpr (sizeof(ET) == 2) {
+    a = f32x4_t{Cvt<ET>::lo(r.w[0][0]), Cvt<ET>::hi(r.w[0][0]), Cvt<ET>::lo(r.w[0][1]), Cvt<ET>::hi(r.w[0][1])};
+    b = f32x4_t{Cvt<ET>::lo(r.w[0][2]), Cvt<ET>::hi(r.w[0][2]), Cvt<ET>::lo(r.w[0][3]), Cvt<ET>::hi(r.w[0][3])};
+  } else {
+    a = __builtin_bit_cast(f32x4_t, r.w[0]);
+    b = __builtin_bit_cast(f32x4_t, r.w[1]);
+  }
+}
+// Its terms, 16 bytes each.
+template <typename ET>
+__device__ __forceinline__ Frag<Store<ET>::NT> terms8(const Raw8<ET>& r) {
+  if constexpr (Store<ET>::NT == 1) {
+    Frag<1> f;
+    f.t[0] = r.w[0];
+    return f;
+  } else {
+    f32x4_t a, b;
+    floats8<ET>(r, a, b);
+    return split8<Store<ET>::NT>(a, b);
+  }
+}
+
+// A [64][DK] tile of q or k rows: loads into registers, then stores its terms to LDS.
+template <typename ET, int DK, int NTHR>
+struct Tile {
+  static constexpr int LD = DK + 8, PLANE = C * LD, N = C * DK / 8 / NTHR;
+  static_assert(C * DK / 8 % NTHR == 0, "whole passes");
+  Raw8<ET> r[N];
+  // `base`: the sequence's and head's first element; rows s1 apart; `rows` valid rows, `cols` valid columns.
+  __device__ __forceinline__ void load(const void* base, int64_t s1, int t0, int rows, int cols, int vec) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int idx = int(threadIdx.x) + i * NTHR;
+      const int row = idx / (DK / 8), col = idx % (DK / 8) * 8;
+      const int n = row < rows ? cols - col : 0;
+      r[i] = load8<ET>(base, int64_t(t0 + row) * s1 + col, n, vec);
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* m) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int idx = int(threadIdx.x) + i * NTHR;
+      const int row = idx / (DK / 8), col = idx % (DK / 8) * 8;
+      const Frag<Store<ET>::NT> f = terms8<ET>(r[i]);
+#pragma unroll
+      for (int n = 0; n < Store<ET>::NT; ++n) *reinterpret_cast<u32x4*>(m + n * PLANE + row * LD + col) = f.t[n];
+    }
+  }
+};
+
+// T's three planes of a chunk, through registers into the padded LDS image.
+template <int NTHR>
+struct TrapTile {
+  static constexpr int TOTAL = 3 * kTrapElems / 8, N = (TOTAL + NTHR - 1) / NTHR;
+  u32x4 r[N];
+  __device__ __forceinline__ void load(const uint16_t* src) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int idx = int(threadIdx.x) + i * NTHR;
+      r[i] = u32x4{0u, 0u, 0u, 0u};
+      if (idx < TOTAL) r[i] = reinterpret_cast<const u32x4*>(src)[idx];
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* m) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int idx = int(threadIdx.x) + i * NTHR;
+      if (idx >= TOTAL) continue;
+      const int plane = idx / (kTrapElems / 8), e = idx % (kTrapElems / 8);
+      const int off = e < 128 ? (e >> 2) * 40 + (e & 3) * 8 : 1280 + ((e - 128) >> 3) * 72 + (e & 7) * 8;
+      *reinterpret_cast<u32x4*>(m + plane * kTrapLds + off) = r[i];
+    }
+  }
+};
+
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
+
+// exp(G_i - G_j), 0 across a document start. The cumulated logarithms are pairs of floats, so
+// the difference keeps float32 accuracy relative to itself, not to the sums.
+__device__ __forceinline__ float gam(float ghi_i, float glo_i, int n_i, float ghi_j, float glo_j, int n_j) {
+  const float d = (ghi_i - ghi_j) + (glo_i - glo_j);
+  return n_i == n_j ? fast_exp(d) : 0.f;
+}
+
+__device__ __forceinline__ f32x4_t ld4(const float* p) { return *reinterpret_cast<const f32x4_t*>(p); }
+__device__ __forceinline__ f32x4_t zero4() { return f32x4_t{0.f, 0.f, 0.f, 0.f}; }
+
+// The 10 tiles on and below the diagonal, in rows.
+__device__ __forceinline__ void tile_of(int t, int& ti, int& tj) {
+  ti = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3;
+  tj = t - ti * (ti + 1) / 2;
+}
+
+// ---------------------------------------------------------------------------------
+// T = (I + A)^-1 and the per-token factors of one chunk
+// ---------------------------------------------------------------------------------
+
+constexpr int kInvLd = 68;
+
+template <typename ET, int DK>
+struct PrepLds {
+  static constexpr int K = 0;
+  static constexpr int A = K + Store<ET>::NT * Tile<ET, DK, 256>::PLANE * 2;
+  static constexpr int T = A + C * kInvLd * 4;
+  static constexpr int TOK = T + C * kInvLd * 4;
+  static constexpr int BYTES = TOK + kTokArrays * C * 4;
+};
+
+// The inverse in float32: each wave inverts one 16 x 16 diagonal block by forward substitution
+// (one column per lane), then block diagonal d = 1, 2, 3 follows as
+// T_ij = -T_ii sum_{j <= k < i} A_ik T_kj on the float32 matrix instructions, whose result
+// layout is again their right operand's.
+template <typename ET, int DK>
+__global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
+  using L = PrepLds<ET, DK>;
+  using TK = Tile<ET, DK, 256>;
+  extern __shared__ __align__(16) char lds[];
+  uint16_t* sK = reinterpret_cast<uint16_t*>(lds + L::K);
+  float* sA = reinterpret_cast<float*>(lds + L::A);
+  float* sT = reinterpret_cast<float*>(lds + L::T);
+  float* tok = reinterpret_cast<float*>(lds + L::TOK);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q = lane >> 4, n16 = lane & 15;
+  const int64_t ci = blockIdx.x;
+  const int c = int(ci % p.nC);
+  const int hv = int(ci / p.nC % p.Hv);
+  const int b = int(ci / p.nC / p.Hv);
+  const int hk = hv / p.group;
+  const int t0 = c * C, rows = min(C, p.T - t0);
+
+  TK tk;
+  tk.load(static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2, p.ks1, t0, rows, p.dkn, p.veck);
+  auto norms = [&](const TK& t, float* out) {
+#pragma unroll
+    for (int i = 0; i < TK::N; ++i) {
+      f32x4_t x, y;
+      floats8<ET>(t.r[i], x, y);
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s += x[e] * x[e] + y[e] * y[e];
+#pragma unroll
+      for (int m = 1; m < DK / 8; m <<= 1) s += __shfl_xor(s, m);
+      const int idx = tid + i * 256;
+      if (idx % (DK / 8) == 0) out[idx / (DK / 8)] = p.eps < 0.f ? 1.f : 1.f / sqrtf(s + p.eps);
+    }
+  };
+  norms(tk, tok + kTokRk * C);
+  tk.store(sK);
+  {
+    TK tq;
+    tq.load(static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2, p.qs1, t0, rows, p.dkn, p.vecq);
+    norms(tq, tok + kTokRq * C);
+  }
+  if (wave == 0) {
+    const int t = t0 + lane;
+    float g = 0.f, bt = 0.f;
+    bool cut = false;
+    if (lane < rows) {
+      g = p.g[b * p.gs0 + t * p.gs1 + hv * p.gs2];
+      bt = ldf<ET>(p.beta, b * p.bs0 + t * p.bs1 + hv * p.bs2);
+      if (p.seg != nullptr && t > 0) {
+        const int32_t* sg = p.seg + b * p.ss0;
+        cut = sg[t * p.ss1] != sg[(t - 1) * p.ss1];
+      }
+      // exp(-128) is 0 in float32: such a token keeps nothing of what came before it
+      if (g <= -128.f) cut = true;
+      if (cut) g = 0.f;
+    }
+    const unsigned long long mask = __ballot(cut);
+    const int cnt = __popcll(mask & ((2ull << lane) - 1ull));
+    double G = g;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const double o = __shfl_up(G, m);
+      if (lane >= m) G += o;
+    }
+    const double GC = __shfl(G, 63);
+    const int cntC = __popcll(mask);
+    const float hi = float(G);
+    tok[kTokGhi * C + lane] = hi;
+    tok[kTokGlo * C + lane] = float(G - double(hi));
+    tok[kTokE * C + lane] = cnt == 0 ? expf(hi) : 0.f;
+    tok[kTokD * C + lane] = cnt == cntC ? expf(float(GC - G)) : 0.f;
+    tok[kTokN * C + lane] = __int_as_float(cnt);
+    tok[kTokBeta * C + lane] = bt;
+  }
+  __syncthreads();
+
+  // A, tile by tile: rows i = 4q .. 4q+3, column j = lane % 16
+  for (int t = wave; t < 10; t += 4) {
+    int ti, tj;
+    tile_of(t, ti, tj);
+    f32x4_t acc = zero4();
+#pragma unroll
+    for (int kb = 0; kb < DK / 32; ++kb) {
+      const auto fa = rowfrag<Store<ET>::NT>(sK, TK::LD, TK::PLANE, 16 * ti, 32 * kb);
+      const auto fb = rowfrag<Store<ET>::NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb);
+      mma<2>(acc, fa, fb);
+    }
+    const int j = 16 * tj + n16;
+    const float gh = tok[kTokGhi * C + j], gl = tok[kTokGlo * C + j], rkj = tok[kTokRk * C + j];
+    const int nj = __float_as_int(tok[kTokN * C + j]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = 16 * ti + 4 * q + r;
+      float a = 0.f;
+      if (i > j) {
+        a = acc[r] * rkj * tok[kTokRk * C + i] * tok[kTokBeta * C + i] *
+            gam(tok[kTokGhi * C + i], tok[kTokGlo * C + i], __float_as_int(tok[kTokN * C + i]), gh, gl, nj);
+      }
+      sA[i * kInvLd + j] = a;
+    }
+  }
+  __syncthreads();
+  {
+    const float* a = sA + 16 * wave * kInvLd + 16 * wave;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s = i == n16 ? 1.f : 0.f;
+#pragma unroll
+      for (int k = 0; k < i; ++k) s -= a[i * kInvLd + k] * x[k];
+      x[i] = s;
+    }
+    if (q == 0) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sT[(16 * wave + i) * kInvLd + 16 * wave + n16] = x[i];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int d = 1; d < 4; ++d) {
+    if (wave < 4 - d) {
+      const int tj = wave, ti = wave + d;
+      f32x4_t acc = zero4();
+      for (int k = tj; k < ti; ++k) {
+        const f32x4_t a = ld4(sA + (16 * ti + n16) * kInvLd + 16 * k + 4 * q);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], sT[(16 * k + 4 * q + r) * kInvLd + 16 * tj + n16], acc, 0, 0, 0);
+      }
+      const f32x4_t a = ld4(sT + (16 * ti + n16) * kInvLd + 16 * ti + 4 * q);
+      f32x4_t res = zero4();
+#pragma unroll
+      for (int r = 0; r < 4; ++r) res = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], acc[r], res, 0, 0, 0);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sT[(16 * ti + 4 * q + r) * kInvLd + 16 * tj + n16] = -res[r];
+    }
+    __syncthreads();
+  }
+  uint16_t* wT = p.wT + ci * (3 * kTrapElems);
+  for (int e = tid; e < kTrapElems / 8; e += 256) {
+    const int row = e < 128 ? e >> 2 : 32 + ((e - 128) >> 3);
+    const int col = e < 128 ? (e & 3) * 8 : (e & 7) * 8;
+    f32x4_t x = zero4(), y = zero4();
+    if ((col >> 4) <= (row >> 4)) {
+      x = ld4(sT + row * kInvLd + col);
+      y = ld4(sT + row * kInvLd + col + 4);
+    }
+    const Frag<3> f = split8<3>(x, y);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) reinterpret_cast<u32x4*>(wT + n * kTrapElems)[e] = f.t[n];
+  }
+  float* wTok = p.wTok + ci * (kTokArrays * C);
+  for (int e = tid; e < kTokArrays * C / 4; e += 256)
+    reinterpret_cast<f32x4_t*>(wTok)[e] = reinterpret_cast<const f32x4_t*>(tok)[e];
+}
+
+// ---------------------------------------------------------------------------------
+// Forward scan over the chunks of one (sequence, value head), 16 columns per wave
+// ---------------------------------------------------------------------------------
+
+template <typename ET, int DK, bool STATES>
+struct ScanLds {
+  static constexpr int NT = Store<ET>::NT, NP = Store<ET>::NP;
+  static constexpr int K = 0;
+  static constexpr int Q = K + NT * Tile<ET, DK, 64>::PLANE * 2;
+  static constexpr int T = Q + (STATES ? 0 : NT * Tile<ET, DK, 64>::PLANE * 2);
+  static constexpr int P = T + 3 * kTrapLds * 2;
+  static constexpr int TOK = P + (STATES ? 0 : NP * kTrapLds * 2);
+  static constexpr int BYTES = TOK + kTokArrays * C * 4;
+};
+
+__device__ __forceinline__ int delta_cols(const DeltaParams& p, int nw) { return (p.nCG + nw - 1) / nw; }
+
+// The 16 values of a wave's column in a chunk: token 16 mt + 4 q + r in v[4 mt + r].
+template <typename ET>
+__device__ __forceinline__ void load_cols(float* v, const void* base, int64_t s1, int t0, int T, int col, bool ok) {
+  const int q = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int t = t0 + 16 * (e >> 2) + 4 * q + (e & 3);
+    v[e] = 0.f;
+    if (ok && t < T) v[e] = ldf<ET>(base, t * s1 + col);
+  }
+}
+template <typename ET>
+__device__ __forceinline__ void store_cols(const f32x4_t* v, void* base, int64_t s1, int t0, int T, int col, bool ok) {
+  const int q = (threadIdx.x & 63) >> 4;
+  if (!ok) return;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int t = t0 + 16 * (e >> 2) + 4 * q + (e & 3);
+    if (t < T) stf<ET>(base, t * s1 + col, v[e >> 2][e & 3]);
+  }
+}
+
+// State rows 16 i + 4 q + r of a column, from and to [dk][dv] float32.
+template <int DK>
+__device__ __forceinline__ void load_state(f32x4_t* S, const float* src, int64_t s2, int dkn, int col, bool ok) {
+  const int q = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * i + 4 * q + r;
+      S[i][r] = (src != nullptr && ok && row < dkn) ? src[row * s2 + col] : 0.f;
+    }
+}
+template <int DK>
+__device__ __forceinline__ void store_state(const f32x4_t* S, float* dst, int64_t s2, int dkn, int col, bool ok) {
+  const int q = (threadIdx.x & 63) >> 4;
+  if (dst == nullptr || !ok) return;
+#pragma unroll
+  for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * i + 4 * q + r;
+      if (row < dkn) dst[row * s2 + col] = S[i][r];
+    }
+}
+
+// Images of a wave's [rows x 16] matrix in fragment order: 32 bytes per lane and 32 rows.
+template <int N>
+__device__ __forceinline__ void store_image(const f32x4_t* x, float* dst) {
+  f32x4_t* d = reinterpret_cast<f32x4_t*>(dst) + 2 * (threadIdx.x & 63);
+#pragma unroll
+  for (int i = 0; i < N; ++i) d[128 * (i >> 1) + (i & 1)] = x[i];
+}
+template <int N>
+__device__ __forceinline__ void load_image(f32x4_t* x, const float* src) {
+  const f32x4_t* d = reinterpret_cast<const f32x4_t*>(src) + 2 * (threadIdx.x & 63);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = d[128 * (i >> 1) + (i & 1)];
+}
+
+// STATES: only carries the state and stores it before each chunk (for the backward).
+template <typename ET, int DK, int NW, bool STATES>
+__global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) {
+  using L = ScanLds<ET, DK, STATES>;
+  constexpr int NT = L::NT, NP = L::NP, NTHR = 64 * NW, KB = DK / 32;
+  using TK = Tile<ET, DK, NTHR>;
+  extern __shared__ __align__(16) char lds[];
+  uint16_t* sK = reinterpret_cast<uint16_t*>(lds + L::K);
+  uint16_t* sQ = reinterpret_cast<uint16_t*>(lds + L::Q);
+  uint16_t* sT = reinterpret_cast<uint16_t*>(lds + L::T);
+  uint16_t* sP = reinterpret_cast<uint16_t*>(lds + L::P);
+  float* tok = reinterpret_cast<float*>(lds + L::TOK);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q = lane >> 4, n16 = lane & 15;
+  const int ncb = delta_cols(p, NW);
+  const uint32_t bid = xcd_logical_block(blockIdx.x, gridDim.x);
+  const int cg = int(bid % ncb) * NW + wave;
+  const int64_t bh = bid / ncb;
+  const int hv = int(bh % p.Hv), b = int(bh / p.Hv), hk = hv / p.group;
+  const int col = cg * kDeltaCols + n16;
+  const bool ok = col < p.dvn;
+  const ET* kbase = static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2;
+  const ET* qbase = static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2;
+  const ET* vbase = static_cast<const ET*>(p.v) + b * p.vs0 + hv * p.vs2;
+  ET* obase = STATES ? nullptr : static_cast<ET*>(p.out) + b * p.os0 + hv * p.os2;
+
+  f32x4_t S[DK / 16];
+  load_state<DK>(S, p.state_in == nullptr ? nullptr : p.state_in + b * p.sis0 + hv * p.sis1, p.sis2, p.dkn, col, ok);
+
+  if constexpr (!STATES) {
+    // the tiles above the diagonal that a 32-wide contraction block still reads
+    for (int e = tid; e < NP * 128; e += NTHR) {
+      const int n = e >> 7, row = (e >> 2) & 31, part = e & 3;
+      const int i = row < 16 ? row : row + 16, j = (row < 16 ? 16 : 48) + 4 * part;
+      *reinterpret_cast<u32x2*>(sP + n * kTrapLds + trap_off(i) + j) = u32x2{0u, 0u};
+    }
+  }
+
+  TK tk, tq;
+  TrapTile<NTHR> tt;
+  f32x4_t ttok[(kTokArrays * C / 4 + NTHR - 1) / NTHR];
+  float vn[16];
+  auto fetch = [&](int c) {
+    const int t0 = c * C, rows = min(C, p.T - t0);
+    tk.load(kbase, p.ks1, t0, rows, p.dkn, p.veck);
+    if constexpr (!STATES) tq.load(qbase, p.qs1, t0, rows, p.dkn, p.vecq);
+    tt.load(p.wT + (bh * p.nC + c) * (3 * kTrapElems));
+    const f32x4_t* w = reinterpret_cast<const f32x4_t*>(p.wTok + (bh * p.nC + c) * (kTokArrays * C));
+#pragma unroll
+    for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i)
+      if (tid + i * NTHR < kTokArrays * C / 4) ttok[i] = w[tid + i * NTHR];
+    load_cols<ET>(vn, vbase, p.vs1, t0, p.T, col, ok);
+  };
+  if (p.nC > 0) fetch(0);
+  for (int c = 0; c < p.nC; ++c) {
+    __syncthreads();  // every wave is done with the previous chunk's tiles
+    tk.store(sK);
+    if constexpr (!STATES) tq.store(sQ);
+    tt.store(sT);
+#pragma unroll
+    for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i)
+      if (tid + i * NTHR < kTokArrays * C / 4) reinterpret_cast<f32x4_t*>(tok)[tid + i * NTHR] = ttok[i];
+    float v[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = vn[e];
+    __syncthreads();
+    if (c + 1 < p.nC) fetch(c + 1);
+
+    if constexpr (!STATES) {
+      // P = scale Gam o Q K^T: tiles transposed (rows j, column i), so a lane holds four
+      // neighbours of one row of P
+      for (int t = wave; t < 10; t += NW) {
+        int ti, tj;
+        tile_of(t, ti, tj);
+        f32x4_t acc = zero4();
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+          mma<NP - 1>(acc, rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb),
+                      rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb));
+        const int i = 16 * ti + n16, j0 = 16 * tj + 4 * q;
+        const float gh = tok[kTokGhi * C + i], gl = tok[kTokGlo * C + i], rqi = tok[kTokRq * C + i] * p.scale;
+        const int ni = __float_as_int(tok[kTokN * C + i]);
+        const f32x4_t ghj = ld4(tok + kTokGhi * C + j0), glj = ld4(tok + kTokGlo * C + j0);
+        const f32x4_t nj = ld4(tok + kTokN * C + j0), rkj = ld4(tok + kTokRk * C + j0);
+        f32x4_t x;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          x[r] = j0 + r <= i ? acc[r] * rqi * rkj[r] * gam(gh, gl, ni, ghj[r], glj[r], __float_as_int(nj[r])) : 0.f;
+        put4<NP>(sP + trap_off(i) + j0, kTrapLds, x);
+      }
+    } else if (cg < p.nCG) {
+      store_image<DK / 16>(S, p.wS + ((bh * p.nC + c) * p.nCG + cg) * (DK * 16));
+    }
+
+    Frag<3> sf[KB];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(S[2 * kb], S[2 * kb + 1]);
+    f32x4_t z[4];  // beta (v - E K S0)
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+      f32x4_t acc = zero4();
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) mma<2>(acc, rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * mt, 32 * kb), sf[kb]);
+      const int t = 16 * mt + 4 * q;
+      const f32x4_t e = ld4(tok + kTokE * C + t), rk = ld4(tok + kTokRk * C + t), be = ld4(tok + kTokBeta * C + t);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) z[mt][r] = be[r] * (v[4 * mt + r] - e[r] * rk[r] * acc[r]);
+    }
+    f32x4_t u[4];
+    {
+      const Frag<3> zf[2] = {split8<3>(z[0], z[1]), split8<3>(z[2], z[3])};
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        u[mt] = zero4();
+#pragma unroll
+        for (int kb = 0; kb <= mt / 2; ++kb) mma<2>(u[mt], trap_row<3>(sT, mt, kb), zf[kb]);
+      }
+    }
+    f32x4_t o[4];
+    if constexpr (!STATES) {
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        o[mt] = zero4();
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) mma<NP - 1>(o[mt], rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * mt, 32 * kb), sf[kb]);
+        const int t = 16 * mt + 4 * q;
+        const f32x4_t e = ld4(tok + kTokE * C + t), rq = ld4(tok + kTokRq * C + t);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[mt][r] *= e[r] * rq[r] * p.scale;
+      }
+    }
+    {
+      f32x4_t d[4];
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        const int t = 16 * mt + 4 * q;
+        const f32x4_t dd = ld4(tok + kTokD * C + t), rk = ld4(tok + kTokRk * C + t);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) d[mt][r] = u[mt][r] * dd[r] * rk[r];
+      }
+      const Frag<3> df[2] = {split8<3>(d[0], d[1]), split8<3>(d[2], d[3])};
+      const float gamma = tok[kTokE * C + C - 1];
+#pragma unroll
+      for (int i = 0; i < DK / 16; ++i) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[i][r] *= gamma;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) mma<2>(S[i], colfrag<NT>(sK, TK::LD, TK::PLANE, 32 * kb, 16 * i), df[kb]);
+      }
+    }
+    if constexpr (!STATES) {
+      __syncthreads();  // P is complete
+      const Frag<NP> uf[2] = {split8<NP>(u[0], u[1]), split8<NP>(u[2], u[3])};
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int kb = 0; kb <= mt / 2; ++kb) mma<NP - 1>(o[mt], trap_row<NP>(sP, mt, kb), uf[kb]);
+      store_cols<ET>(o, obase, p.os1, c * C, p.T, col, ok);
+    }
+  }
+  if constexpr (!STATES)
+    store_state<DK>(S, p.state_out == nullptr ? nullptr : p.state_out + b * p.sos0 + hv * p.sos1, p.sos2, p.dkn, col, ok);
+}
+
+template <typename KernelT>
+hipError_t launch_delta(KernelT kernel, int64_t blocks, int threads, int lds_bytes, const DeltaParams& p,
+                        hipStream_t s) {
+  if (lds_bytes > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kernel, dim3(unsigned(blocks)), dim3(unsigned(threads)), unsigned(lds_bytes), s, p);
+  return hipGetLastError();
+}
+
+template <typename ET, int DK>
+hipError_t delta_prep_launch(const DeltaParams& p, hipStream_t s) {
+  if (p.nC == 0) return hipSuccess;
+  return launch_delta(k_delta_prep<ET, DK>, int64_t(p.B) * p.Hv * p.nC, 256, PrepLds<ET, DK>::BYTES, p, s);
+}
+
+template <typename ET, int DK, bool STATES>
+hipError_t delta_scan_launch(const DeltaParams& p, hipStream_t s) {
+  constexpr int NW = 4;
+  const int64_t blocks = int64_t(p.B) * p.Hv * ((p.nCG + NW - 1) / NW);
+  return launch_delta(k_delta_scan<ET, DK, NW, STATES>, blocks, 64 * NW, ScanLds<ET, DK, STATES>::BYTES, p, s);
+}
+
+template <typename ET, int DK>
+hipError_t delta_fwd_dk(const DeltaParams& p, hipStream_t s) {
+  const hipError_t e = delta_prep_launch<ET, DK>(p, s);
+  return e != hipSuccess ? e : delta_scan_launch<ET, DK, false>(p, s);
+}
+
+template <typename ET>
+hipError_t delta_fwd_et(const DeltaParams& p, hipStream_t s) {
+  return delta_dk_pad(p.dkn) == 64 ? delta_fwd_dk<ET, 64>(p, s) : delta_fwd_dk<ET, 128>(p, s);
+}
+
+}  // namespace delta
+}  // namespace dynconv

@@ -6,6 +6,7 @@ current stream, nothing else.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -422,3 +423,102 @@ def dynconv_lowrank_decode_step(x, z, U, bias, cache, t: int, W: int, out=None, 
         _stream(dev))
     _lib.check("dynconv_lowrank_decode_step", st)
     return y
+
+
+# ----------------------------------------------------------------------------------
+# Gated delta rule: the recurrence behind the convolved q, k, v
+# ----------------------------------------------------------------------------------
+
+
+def _on(dev):
+    """Makes dev the current device for a launch (its stream belongs to it)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _sp(t):
+    """(pointer, strides) of a tensor, or two NULLs."""
+    return (_ptr(t), _lib.strides(t.stride())) if t is not None else (None, None)
+
+
+def _delta_shapes(q, k, v, g, beta, token: bool):
+    """Checks the operands of a gated delta rule call; returns (lead, Hk, Hv, dk, dv) with
+    lead = (B, T), or (B,) for one token."""
+    n = 3 if token else 4
+    lead_name = "[B, Hk, dk]" if token else "[B, T, Hk, dk]"
+    if q.dim() != n:
+        raise ValueError(f"q must be {lead_name}; got shape {list(q.shape)}")
+    if v.dim() != n:
+        raise ValueError(f"v must be {lead_name.replace('k', 'v')}; got shape {list(v.shape)}")
+    lead, (Hk, dk), (Hv, dv) = tuple(q.shape[:-2]), tuple(q.shape[-2:]), tuple(v.shape[-2:])
+    if Hk < 1 or Hv % Hk != 0:
+        raise ValueError(f"the {Hv} value heads must be a multiple of the {Hk} key heads")
+    _dtype_code(q)
+    _expect("k", k, (*lead, Hk, dk), q.dtype)
+    _expect("v", v, (*lead, Hv, dv), q.dtype)
+    _expect("g", g, (*lead, Hv), torch.float32)
+    _expect("beta", beta, (*lead, Hv), q.dtype)
+    return lead, Hk, Hv, dk, dv
+
+
+def _delta_consts(scale, qk_norm_eps, dk: int):
+    if qk_norm_eps is not None and not qk_norm_eps >= 0.0:
+        raise ValueError(f"qk_norm_eps = {qk_norm_eps} must be at least 0, or None")
+    return (float(dk) ** -0.5 if dk and scale is None else float(scale or 0.0)), (
+        -1.0 if qk_norm_eps is None else float(qk_norm_eps))
+
+
+def new_delta_state(B: int, Hv: int, dk: int, dv: int, device) -> torch.Tensor:
+    """A zeroed float32 [B, Hv, dk, dv] state of the gated delta rule."""
+    return torch.zeros((B, Hv, dk, dv), dtype=torch.float32, device=device)
+
+
+def dynconv_delta_fwd(q, k, v, g, beta, scale: float | None = None, qk_norm_eps: float | None = None, seq_idx=None,
+                      state=None, want_state: bool = False, out=None, state_out=None):
+    """o [B,T,Hv,dv] of the gated delta rule on q, k [B,T,Hk,dk], v [B,T,Hv,dv], log decays g
+    (float32 [B,T,Hv]) and write strengths beta [B,T,Hv]:
+
+        S_t = e^{g_t} S_{t-1} + k_t (beta_t (v_t - e^{g_t} S_{t-1}^T k_t))^T,  o_t = scale S_t^T q_t,
+
+    scale = dk^-0.5 by default, key head h // (Hv // Hk) for value head h. With qk_norm_eps,
+    q and k are divided by sqrt(|.|^2 + qk_norm_eps) first. With seq_idx (int32 [B,T]) the
+    state restarts from zero at every document start. state: the float32 [B,Hv,dk,dv] state
+    before token 0 (default zero). With want_state, or a state_out to write (which may be
+    state itself), returns (o, state after token T-1)."""
+    (B, T), Hk, Hv, dk, dv = _delta_shapes(q, k, v, g, beta, False)
+    scale, eps = _delta_consts(scale, qk_norm_eps, dk)
+    _expect("state", state, (B, Hv, dk, dv), torch.float32)
+    _expect("state_out", state_out, (B, Hv, dk, dv), torch.float32)
+    _expect("out", out, (B, T, Hv, dv), q.dtype)
+    dev = _require_device(q, k, v, g, beta, seq_idx, state, out, state_out)
+    seg = _seg_args(seq_idx, B, T) if seq_idx is not None else (None, None)
+    o = torch.empty((B, T, Hv, dv), dtype=q.dtype, device=dev) if out is None else out
+    if want_state and state_out is None:
+        state_out = torch.empty((B, Hv, dk, dv), dtype=torch.float32, device=dev)
+    lib = _lib.load()
+    code = _dtype_code(q)
+    ws_bytes = int(lib.dynconv_delta_fwd_workspace_size(B, T, Hk, Hv, dk, dv, code))
+    work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    with _on(dev):
+        st = lib.dynconv_delta_fwd(*_sp(q), *_sp(k), *_sp(v), *_sp(g), *_sp(beta), *seg, *_sp(state), *_sp(o),
+                                   *_sp(state_out), B, T, Hk, Hv, dk, dv, scale, eps, code, _ptr(work), ws_bytes,
+                                   _stream(dev))
+    _lib.check("dynconv_delta_fwd", st)
+    return o if state_out is None else (o, state_out)
+
+
+def dynconv_delta_step(q, k, v, g, beta, state, scale: float | None = None, qk_norm_eps: float | None = None, out=None):
+    """o [B,Hv,dv] of one token of every sequence (q, k [B,Hk,dk], v [B,Hv,dv], g float32 and
+    beta [B,Hv]); state (float32 [B,Hv,dk,dv]) is updated in place."""
+    (B,), Hk, Hv, dk, dv = _delta_shapes(q, k, v, g, beta, True)
+    scale, eps = _delta_consts(scale, qk_norm_eps, dk)
+    if state is None:
+        raise ValueError("a state [B, Hv, dk, dv] is required")
+    _expect("state", state, (B, Hv, dk, dv), torch.float32)
+    _expect("out", out, (B, Hv, dv), q.dtype)
+    dev = _require_device(q, k, v, g, beta, state, out)
+    o = torch.empty((B, Hv, dv), dtype=q.dtype, device=dev) if out is None else out
+    with _on(dev):
+        st = _lib.load().dynconv_delta_step(*_sp(q), *_sp(k), *_sp(v), *_sp(g), *_sp(beta), *_sp(state), *_sp(o), B,
+                                            Hk, Hv, dk, dv, scale, eps, _dtype_code(q), _stream(dev))
+    _lib.check("dynconv_delta_step", st)
+    return o

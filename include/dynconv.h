@@ -363,6 +363,52 @@ dynconv_status dynconv_cache_fill_varlen(const void* x, const int64_t* xs, const
                                          void* cache, const int64_t* cs, int64_t B, int64_t T, int64_t D, int32_t W,
                                          dynconv_dtype dtype, void* stream);
 
+/*
+ * Gated delta rule: the recurrence that consumes the convolved q, k, v in linear-attention
+ * models (the reading note's linear-attention experiments put the dynamic convolution in
+ * Gated DeltaNet). Per sequence b and value head h, with a_t = exp(g[b,t,h]), the key head
+ * h / (Hv/Hk) shared by Hv/Hk consecutive value heads, and a float32 state S [dk, dv]:
+ *   u_t = beta_t (v_t - a_t S_{t-1}^T k_t),  S_t = a_t S_{t-1} + k_t u_t^T,
+ *   o_t = scale S_t^T q_t.
+ *   q, k   [B,T,Hk,dk], v, o [B,T,Hv,dv] of `dtype`, strides s[0..3], s[3] == 1
+ *   beta   [B,T,Hv] of `dtype`, g float32 [B,T,Hv] (log decay, normally <= 0), strides s[0..2]
+ *   qk_norm_eps >= 0: q and k are divided by sqrt(|.|^2 + qk_norm_eps) first; < 0: as given
+ *   seq_idx  int32 [B,T] (strides ss[0..1]) or NULL: the state is reset to zero before a
+ *            token whose id differs from the token's before it (document starts of packed
+ *            rows); the initial state belongs to the first document of a row, the final
+ *            state to the last
+ *   state_in   float32 [B,Hv,dk,dv] (strides [0..3], last 1) or NULL (zero)
+ *   state_out  the same, overwritten with the state after token T-1, or NULL; may be
+ *              state_in itself (same strides). T == 0 copies the state.
+ * A token with beta = 0 and g = 0 leaves the state as it is (padding behind a sequence).
+ * g <= -128 counts as a decay to exactly zero (exp of it is 0 in float32).
+ * Limits (DYNCONV_ERR_UNSUPPORTED otherwise): dk <= 128, dv <= 65536; strides >= 0. Inputs
+ * and outputs need element alignment; rows of q, k that allow 16-byte loads are read so.
+ * Needs dynconv_delta_fwd_workspace_size(...) bytes of workspace. Run-to-run deterministic.
+ */
+dynconv_status dynconv_delta_fwd(const void* q, const int64_t* qs, const void* k, const int64_t* ks, const void* v,
+                                 const int64_t* vs, const float* g, const int64_t* gs, const void* beta,
+                                 const int64_t* bs, const int32_t* seq_idx, const int64_t* ss, const float* state_in,
+                                 const int64_t* sis, void* o, const int64_t* os, float* state_out, const int64_t* sos,
+                                 int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, float scale,
+                                 float qk_norm_eps, dynconv_dtype dtype, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+size_t dynconv_delta_fwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
+                                        dynconv_dtype dtype);
+
+/*
+ * One decoding step of the gated delta rule: one token of every sequence, the state updated
+ * in place (equal to dynconv_delta_fwd with T = 1).
+ *   q, k [B,Hk,dk], v, o [B,Hv,dv] strides s[0..2] (s[2] == 1), g, beta [B,Hv] strides
+ *   s[0..1], state float32 [B,Hv,dk,dv] strides sts[0..3] (sts[3] == 1).
+ */
+dynconv_status dynconv_delta_step(const void* q, const int64_t* qs, const void* k, const int64_t* ks, const void* v,
+                                  const int64_t* vs, const float* g, const int64_t* gs, const void* beta,
+                                  const int64_t* bs, float* state, const int64_t* sts, void* o, const int64_t* os,
+                                  int64_t B, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, float scale,
+                                  float qk_norm_eps, dynconv_dtype dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
