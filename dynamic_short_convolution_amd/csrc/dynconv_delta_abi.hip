@@ -81,8 +81,7 @@ dynconv_status take_inputs(DeltaParams* p, const void* q, const int64_t* qs, con
     p->vs0 = vs[0], p->vs1 = vs[1], p->vs2 = vs[2];
     p->gs0 = gs[0], p->gs1 = gs[1], p->gs2 = gs[2];
     p->bs0 = bs[0], p->bs1 = bs[1], p->bs2 = bs[2];
-    p->vecq = wide(q, qs, 4, eq, eb);
-    p->veck = wide(k, ks, 4, eq, eb);
+    p->vec = dk % 8 == 0 && wide(q, qs, 4, eq, eb) && wide(k, ks, 4, eq, eb);
   }
   if (state_in != nullptr) {
     if ((st = check_tensor(state_in, sis, 4, est, 4, true, false)) != DYNCONV_OK) return st;

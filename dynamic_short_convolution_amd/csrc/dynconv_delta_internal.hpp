@@ -43,7 +43,7 @@ struct DeltaParams {
   int64_t sis0, sis1, sis2, sos0, sos1, sos2, dsos0, dsos1, dsos2, dsis0, dsis1, dsis2;
   int32_t B, T, Hk, Hv, group, dkn, dvn;  // dkn, dvn: key and value head widths
   int32_t nC, nCG;                        // chunks per sequence, 16-column groups of a value head
-  int32_t vecq, veck, vecdo;              // 16-byte loads of q, k, dO rows
+  int32_t vec;                            // rows of q and k allow 16-byte loads
   float scale, eps;                       // eps < 0: q and k as they are
   // workspace
   uint16_t* wT;   // [chunk][3][kTrapElems]: (I + A)^-1 in three 8-bit terms

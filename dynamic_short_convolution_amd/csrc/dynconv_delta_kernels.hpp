@@ -184,31 +184,37 @@ __device__ __forceinline__ void stf(void* p, int64_t i, float v) {
   }
 }
 
-// 8 consecutive stored elements of a row, as loaded (zeros past `n` elements).
+// 8 consecutive stored elements of a row, as loaded; elements from `n` on read as zero. Every
+// load is issued whatever n is, from a clamped address (`off` is of an existing element, of
+// whose row `n0` follow): a branch around a load would make each wait for the one before.
 template <typename ET>
 struct Raw8 {
   u32x4 w[sizeof(ET) / 2];
 };
-template <typename ET>
-__device__ __forceinline__ Raw8<ET> load8(const void* base, int64_t off, int n, int vec) {
+template <typename ET, bool VEC>
+__device__ __forceinline__ Raw8<ET> load8(const void* base, int64_t off, int n, int n0) {
   Raw8<ET> r;
-  if (n >= 8 && vec) {
+  if constexpr (VEC) {  // n is 8 or at most 0
     const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const ET*>(base) + off);
 #pragma unroll
     for (int i = 0; i < int(sizeof(ET) / 2); ++i) r.w[i] = p[i];
+    if (n <= 0) {
+#pragma unroll
+      for (int i = 0; i < int(sizeof(ET) / 2); ++i) r.w[i] = u32x4{0u, 0u, 0u, 0u};
+    }
   } else {
     uint32_t e[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      e[i] = 0;
-      if (i < n) {
-        if constexpr (sizeof(ET) == 2) {
-          e[i] = static_cast<const uint16_t*>(base)[off + i];
-        } else {
-          e[i] = static_cast<const uint32_t*>(base)[off + i];
-        }
+      const int64_t at = off + min(i, n0 - 1);
+      if constexpr (sizeof(ET) == 2) {
+        e[i] = static_cast<const uint16_t*>(base)[at];
+      } else {
+        e[i] = static_cast<const uint32_t*>(base)[at];
       }
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = i < n ? e[i] : 0u;
     if constexpr (sizeof(ET) == 2) {
       r.w[0] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
     } else {
@@ -243,19 +249,21 @@ __device__ __forceinline__ Frag<Store<ET>::NT> terms8(const Raw8<ET>& r) {
 }
 
 // A [64][DK] tile of q or k rows: loads into registers, then stores its terms to LDS.
-template <typename ET, int DK, int NTHR>
+template <typename ET, int DK, int NTHR, bool VEC>
 struct Tile {
   static constexpr int LD = DK + 8, PLANE = C * LD, N = C * DK / 8 / NTHR;
   static_assert(C * DK / 8 % NTHR == 0, "whole passes");
   Raw8<ET> r[N];
-  // `base`: the sequence's and head's first element; rows s1 apart; `rows` valid rows, `cols` valid columns.
-  __device__ __forceinline__ void load(const void* base, int64_t s1, int t0, int rows, int cols, int vec) {
+  // `base`: the sequence's and head's first element; rows s1 apart; `rows` >= 1 valid rows,
+  // `cols` valid columns (a multiple of 8 with VEC).
+  __device__ __forceinline__ void load(const void* base, int64_t s1, int t0, int rows, int cols) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int idx = int(threadIdx.x) + i * NTHR;
       const int row = idx / (DK / 8), col = idx % (DK / 8) * 8;
-      const int n = row < rows ? cols - col : 0;
-      r[i] = load8<ET>(base, int64_t(t0 + row) * s1 + col, n, vec);
+      const int c = col < cols ? col : 0;
+      const int n = row < rows && col < cols ? cols - col : 0;
+      r[i] = load8<ET, VEC>(base, int64_t(t0 + min(row, rows - 1)) * s1 + c, n, cols - c);
     }
   }
   __device__ __forceinline__ void store(uint16_t* m) const {
@@ -279,8 +287,7 @@ struct TrapTile {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int idx = int(threadIdx.x) + i * NTHR;
-      r[i] = u32x4{0u, 0u, 0u, 0u};
-      if (idx < TOTAL) r[i] = reinterpret_cast<const u32x4*>(src)[idx];
+      r[i] = reinterpret_cast<const u32x4*>(src)[min(idx, TOTAL - 1)];
     }
   }
   __device__ __forceinline__ void store(uint16_t* m) const {
@@ -322,7 +329,7 @@ constexpr int kInvLd = 68;
 template <typename ET, int DK>
 struct PrepLds {
   static constexpr int K = 0;
-  static constexpr int A = K + Store<ET>::NT * Tile<ET, DK, 256>::PLANE * 2;
+  static constexpr int A = K + Store<ET>::NT * Tile<ET, DK, 64, true>::PLANE * 2;
   static constexpr int T = A + C * kInvLd * 4;
   static constexpr int TOK = T + C * kInvLd * 4;
   static constexpr int BYTES = TOK + kTokArrays * C * 4;
@@ -332,10 +339,10 @@ struct PrepLds {
 // (one column per lane), then block diagonal d = 1, 2, 3 follows as
 // T_ij = -T_ii sum_{j <= k < i} A_ik T_kj on the float32 matrix instructions, whose result
 // layout is again their right operand's.
-template <typename ET, int DK>
+template <typename ET, int DK, bool VEC>
 __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
   using L = PrepLds<ET, DK>;
-  using TK = Tile<ET, DK, 256>;
+  using TK = Tile<ET, DK, 256, VEC>;
   extern __shared__ __align__(16) char lds[];
   uint16_t* sK = reinterpret_cast<uint16_t*>(lds + L::K);
   float* sA = reinterpret_cast<float*>(lds + L::A);
@@ -351,7 +358,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
   const int t0 = c * C, rows = min(C, p.T - t0);
 
   TK tk;
-  tk.load(static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2, p.ks1, t0, rows, p.dkn, p.veck);
+  tk.load(static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2, p.ks1, t0, rows, p.dkn);
   auto norms = [&](const TK& t, float* out) {
 #pragma unroll
     for (int i = 0; i < TK::N; ++i) {
@@ -370,7 +377,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
   tk.store(sK);
   {
     TK tq;
-    tq.load(static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2, p.qs1, t0, rows, p.dkn, p.vecq);
+    tq.load(static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2, p.qs1, t0, rows, p.dkn);
     norms(tq, tok + kTokRq * C);
   }
   if (wave == 0) {
@@ -496,8 +503,8 @@ template <typename ET, int DK, bool STATES>
 struct ScanLds {
   static constexpr int NT = Store<ET>::NT, NP = Store<ET>::NP;
   static constexpr int K = 0;
-  static constexpr int Q = K + NT * Tile<ET, DK, 64>::PLANE * 2;
-  static constexpr int T = Q + (STATES ? 0 : NT * Tile<ET, DK, 64>::PLANE * 2);
+  static constexpr int Q = K + NT * Tile<ET, DK, 64, true>::PLANE * 2;
+  static constexpr int T = Q + (STATES ? 0 : NT * Tile<ET, DK, 64, true>::PLANE * 2);
   static constexpr int P = T + 3 * kTrapLds * 2;
   static constexpr int TOK = P + (STATES ? 0 : NP * kTrapLds * 2);
   static constexpr int BYTES = TOK + kTokArrays * C * 4;
@@ -512,8 +519,8 @@ __device__ __forceinline__ void load_cols(float* v, const void* base, int64_t s1
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const int t = t0 + 16 * (e >> 2) + 4 * q + (e & 3);
-    v[e] = 0.f;
-    if (ok && t < T) v[e] = ldf<ET>(base, t * s1 + col);
+    const float x = ldf<ET>(base, min(t, T - 1) * s1 + (ok ? col : 0));
+    v[e] = ok && t < T ? x : 0.f;
   }
 }
 template <typename ET>
@@ -567,11 +574,11 @@ __device__ __forceinline__ void load_image(f32x4_t* x, const float* src) {
 }
 
 // STATES: only carries the state and stores it before each chunk (for the backward).
-template <typename ET, int DK, int NW, bool STATES>
+template <typename ET, int DK, int NW, bool STATES, bool VEC>
 __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) {
   using L = ScanLds<ET, DK, STATES>;
   constexpr int NT = L::NT, NP = L::NP, NTHR = 64 * NW, KB = DK / 32;
-  using TK = Tile<ET, DK, NTHR>;
+  using TK = Tile<ET, DK, NTHR, VEC>;
   extern __shared__ __align__(16) char lds[];
   uint16_t* sK = reinterpret_cast<uint16_t*>(lds + L::K);
   uint16_t* sQ = reinterpret_cast<uint16_t*>(lds + L::Q);
@@ -610,13 +617,13 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
   float vn[16];
   auto fetch = [&](int c) {
     const int t0 = c * C, rows = min(C, p.T - t0);
-    tk.load(kbase, p.ks1, t0, rows, p.dkn, p.veck);
-    if constexpr (!STATES) tq.load(qbase, p.qs1, t0, rows, p.dkn, p.vecq);
+    tk.load(kbase, p.ks1, t0, rows, p.dkn);
+    if constexpr (!STATES) tq.load(qbase, p.qs1, t0, rows, p.dkn);
     tt.load(p.wT + (bh * p.nC + c) * (3 * kTrapElems));
     const f32x4_t* w = reinterpret_cast<const f32x4_t*>(p.wTok + (bh * p.nC + c) * (kTokArrays * C));
 #pragma unroll
     for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i)
-      if (tid + i * NTHR < kTokArrays * C / 4) ttok[i] = w[tid + i * NTHR];
+      ttok[i] = w[min(tid + i * NTHR, kTokArrays * C / 4 - 1)];
     load_cols<ET>(vn, vbase, p.vs1, t0, p.T, col, ok);
   };
   if (p.nC > 0) fetch(0);
@@ -742,28 +749,29 @@ hipError_t launch_delta(KernelT kernel, int64_t blocks, int threads, int lds_byt
   return hipGetLastError();
 }
 
-template <typename ET, int DK>
+template <typename ET, int DK, bool VEC>
 hipError_t delta_prep_launch(const DeltaParams& p, hipStream_t s) {
   if (p.nC == 0) return hipSuccess;
-  return launch_delta(k_delta_prep<ET, DK>, int64_t(p.B) * p.Hv * p.nC, 256, PrepLds<ET, DK>::BYTES, p, s);
+  return launch_delta(k_delta_prep<ET, DK, VEC>, int64_t(p.B) * p.Hv * p.nC, 256, PrepLds<ET, DK>::BYTES, p, s);
 }
 
-template <typename ET, int DK, bool STATES>
+template <typename ET, int DK, bool STATES, bool VEC>
 hipError_t delta_scan_launch(const DeltaParams& p, hipStream_t s) {
   constexpr int NW = 4;
   const int64_t blocks = int64_t(p.B) * p.Hv * ((p.nCG + NW - 1) / NW);
-  return launch_delta(k_delta_scan<ET, DK, NW, STATES>, blocks, 64 * NW, ScanLds<ET, DK, STATES>::BYTES, p, s);
+  return launch_delta(k_delta_scan<ET, DK, NW, STATES, VEC>, blocks, 64 * NW, ScanLds<ET, DK, STATES>::BYTES, p, s);
 }
 
-template <typename ET, int DK>
+template <typename ET, int DK, bool VEC>
 hipError_t delta_fwd_dk(const DeltaParams& p, hipStream_t s) {
-  const hipError_t e = delta_prep_launch<ET, DK>(p, s);
-  return e != hipSuccess ? e : delta_scan_launch<ET, DK, false>(p, s);
+  const hipError_t e = delta_prep_launch<ET, DK, VEC>(p, s);
+  return e != hipSuccess ? e : delta_scan_launch<ET, DK, false, VEC>(p, s);
 }
 
 template <typename ET>
 hipError_t delta_fwd_et(const DeltaParams& p, hipStream_t s) {
-  return delta_dk_pad(p.dkn) == 64 ? delta_fwd_dk<ET, 64>(p, s) : delta_fwd_dk<ET, 128>(p, s);
+  if (p.vec) return delta_dk_pad(p.dkn) == 64 ? delta_fwd_dk<ET, 64, true>(p, s) : delta_fwd_dk<ET, 128, true>(p, s);
+  return delta_dk_pad(p.dkn) == 64 ? delta_fwd_dk<ET, 64, false>(p, s) : delta_fwd_dk<ET, 128, false>(p, s);
 }
 
 }  // namespace delta
