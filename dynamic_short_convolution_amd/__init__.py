@@ -13,6 +13,7 @@ from .ops import (  # noqa: F401
     dynconv_bwd_workspace_size,
     dynconv_cache_fill,
     dynconv_decode_step,
+    dynconv_delta_bwd,
     dynconv_delta_fwd,
     dynconv_delta_step,
     dynconv_fwd,

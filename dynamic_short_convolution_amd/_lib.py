@@ -52,6 +52,8 @@ EXPORTS = (
     "dynconv_lowrank_decode_step_ex",
     "dynconv_delta_fwd",
     "dynconv_delta_fwd_workspace_size",
+    "dynconv_delta_bwd",
+    "dynconv_delta_bwd_workspace_size",
     "dynconv_delta_step",
 )
 
@@ -148,6 +150,9 @@ _delta_sizes = [_i64] * 6     # B, T, Hk, Hv, dk, dv
 _SIGNATURES["dynconv_delta_fwd"] = (
     _delta_in + [_vp, _i64p] * 2 + _delta_sizes + [_f32, _f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int)
 _SIGNATURES["dynconv_delta_fwd_workspace_size"] = (_delta_sizes + [ctypes.c_int], _sz)
+_SIGNATURES["dynconv_delta_bwd"] = (  # + dO, dstate_out; dq, dk, dv, dg, dbeta, dstate_in
+    _delta_in + [_vp, _i64p] * 8 + _delta_sizes + [_f32, _f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int)
+_SIGNATURES["dynconv_delta_bwd_workspace_size"] = (_delta_sizes + [ctypes.c_int], _sz)
 _SIGNATURES["dynconv_delta_step"] = (
     [_vp, _i64p] * 7 + [_i64] * 5 + [_f32, _f32, ctypes.c_int, _vp], ctypes.c_int)
 

@@ -157,6 +157,69 @@ dynconv_status dynconv_delta_fwd(const void* q, const int64_t* qs, const void* k
   return e == hipSuccess ? DYNCONV_OK : record_hip_error(e);
 }
 
+size_t dynconv_delta_bwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
+                                        dynconv_dtype dtype) {
+  if (check_sizes(B, T, Hk, Hv, dk, dv, dtype) != DYNCONV_OK || empty(B, Hv, dk, dv) || T == 0) return 0;
+  return delta_workspace(B, T, Hv, dk, dv, true);
+}
+
+dynconv_status dynconv_delta_bwd(const void* q, const int64_t* qs, const void* k, const int64_t* ks, const void* v,
+                                 const int64_t* vs, const float* g, const int64_t* gs, const void* beta,
+                                 const int64_t* bs, const int32_t* seq_idx, const int64_t* ss, const float* state_in,
+                                 const int64_t* sis, const void* dO, const int64_t* dos, const float* dstate_out,
+                                 const int64_t* dsos, void* dq, const int64_t* dqs, void* dk_, const int64_t* dks,
+                                 void* dv_, const int64_t* dvs, float* dg, const int64_t* dgs, void* dbeta,
+                                 const int64_t* dbs, float* dstate_in, const int64_t* dsis, int64_t B, int64_t T,
+                                 int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, float scale, float qk_norm_eps,
+                                 dynconv_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  dynconv_status st = check_sizes(B, T, Hk, Hv, dk, dv, dtype);
+  if (st != DYNCONV_OK) return st;
+  if (empty(B, Hv, dk, dv) || T == 0) return DYNCONV_OK;
+  DeltaParams p{};
+  st = take_inputs(&p, q, qs, k, ks, v, vs, g, gs, beta, bs, seq_idx, ss, state_in, sis, B, T, Hk, Hv, dk, dv, scale,
+                   qk_norm_eps, dtype);
+  if (st != DYNCONV_OK) return st;
+  const int eb = elem_bytes(dtype);
+  const int64_t eq[4] = {B, T, Hk, dk}, ev[4] = {B, T, Hv, dv}, eg[3] = {B, T, Hv}, est[4] = {B, Hv, dk, dv};
+  if ((st = check_tensor(dO, dos, 4, ev, eb, true, false)) != DYNCONV_OK) return st;
+  if ((st = check_tensor(dq, dqs, 4, eq, eb, true, true)) != DYNCONV_OK) return st;
+  if ((st = check_tensor(dk_, dks, 4, eq, eb, true, true)) != DYNCONV_OK) return st;
+  if ((st = check_tensor(dv_, dvs, 4, ev, eb, true, true)) != DYNCONV_OK) return st;
+  if ((st = check_tensor(dg, dgs, 3, eg, 4, false, true)) != DYNCONV_OK) return st;
+  if ((st = check_tensor(dbeta, dbs, 3, eg, eb, false, true)) != DYNCONV_OK) return st;
+  p.dO = dO, p.dq = dq, p.dk = dk_, p.dv = dv_, p.dg = dg, p.dbeta = dbeta;
+  p.dos0 = dos[0], p.dos1 = dos[1], p.dos2 = dos[2];
+  p.dqs0 = dqs[0], p.dqs1 = dqs[1], p.dqs2 = dqs[2];
+  p.dks0 = dks[0], p.dks1 = dks[1], p.dks2 = dks[2];
+  p.dvs0 = dvs[0], p.dvs1 = dvs[1], p.dvs2 = dvs[2];
+  p.dgs0 = dgs[0], p.dgs1 = dgs[1], p.dgs2 = dgs[2];
+  p.dbs0 = dbs[0], p.dbs1 = dbs[1], p.dbs2 = dbs[2];
+  p.vecdo = dv % 8 == 0 && wide(dO, dos, 4, ev, eb);
+  if (dstate_out != nullptr) {
+    if ((st = check_tensor(dstate_out, dsos, 4, est, 4, true, false)) != DYNCONV_OK) return st;
+    p.dstate_out = dstate_out;
+    p.dsos0 = dsos[0], p.dsos1 = dsos[1], p.dsos2 = dsos[2];
+  }
+  if (dstate_in != nullptr) {
+    if ((st = check_tensor(dstate_in, dsis, 4, est, 4, true, true)) != DYNCONV_OK) return st;
+    p.dstate = dstate_in;
+    p.dsis0 = dsis[0], p.dsis1 = dsis[1], p.dsis2 = dsis[2];
+  }
+  const void* outs[6] = {dq, dk_, dv_, dg, dbeta, dstate_in};
+  for (int i = 0; i < 6; ++i) {
+    if (any_equal(outs[i], {q, k, v, g, beta, seq_idx, state_in, dO, dstate_out})) return DYNCONV_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (outs[i] != nullptr && outs[i] == outs[j]) return DYNCONV_ERR_INVALID_ARG;
+  }
+  if (workspace == nullptr || workspace_bytes < delta_workspace(B, T, Hv, dk, dv, true)) return DYNCONV_ERR_WORKSPACE;
+  delta_carve(&p, workspace, true);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipError_t e = dtype == DYNCONV_BF16  ? delta_bwd_bf16(p, s)
+                       : dtype == DYNCONV_F16 ? delta_bwd_f16(p, s)
+                                              : delta_bwd_f32(p, s);
+  return e == hipSuccess ? DYNCONV_OK : record_hip_error(e);
+}
+
 dynconv_status dynconv_delta_step(const void* q, const int64_t* qs, const void* k, const int64_t* ks, const void* v,
                                   const int64_t* vs, const float* g, const int64_t* gs, const void* beta,
                                   const int64_t* bs, float* state, const int64_t* sts, void* o, const int64_t* os,

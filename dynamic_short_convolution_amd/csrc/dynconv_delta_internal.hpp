@@ -44,6 +44,7 @@ struct DeltaParams {
   int32_t B, T, Hk, Hv, group, dkn, dvn;  // dkn, dvn: key and value head widths
   int32_t nC, nCG;                        // chunks per sequence, 16-column groups of a value head
   int32_t vec;                            // rows of q and k allow 16-byte loads
+  int32_t vecdo;                          // rows of dO do
   float scale, eps;                       // eps < 0: q and k as they are
   // workspace
   uint16_t* wT;   // [chunk][3][kTrapElems]: (I + A)^-1 in three 8-bit terms

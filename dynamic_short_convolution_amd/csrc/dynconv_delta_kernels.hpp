@@ -737,6 +737,602 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
     store_state<DK>(S, p.state_out == nullptr ? nullptr : p.state_out + b * p.sos0 + hv * p.sos1, p.sos2, p.dkn, col, ok);
 }
 
+// ---------------------------------------------------------------------------------
+// Backward: reverse scan of the state's gradient, 16 columns per wave
+// ---------------------------------------------------------------------------------
+//
+// With dS1 the gradient of the state after the chunk and dO that of the outputs:
+//   dU  = P^T dO + D (K dS1),   dR = T^T dU,   dV = dZ = beta dR,
+//   dS0 = gamma dS1 + scale Q^T (E dO) - K^T (beta E dR),
+// all of them column by column, like the forward. S0 (stored by the STATES scan) gives back
+// Z = V - E (K S0) and U = T (beta Z). What contracts over value columns (dq, dk, the pair
+// terms of dg and dbeta) is left to k_delta_grad, which gets U, dR and dS1 from here and the
+// sums over a wave's columns of
+//   into_i = dO_i.(scale E Q S0)_i - dZ_i.(E K S0)_i,  out_j = U_j.(D K dS1)_j,  dR_i.Z_i
+// and gamma <S0, dS1>.
+
+template <typename ET, int DK>
+struct BackLds {
+  static constexpr int NT = Store<ET>::NT;
+  static constexpr int K = 0;
+  static constexpr int Q = K + NT * Tile<ET, DK, 64, true>::PLANE * 2;
+  static constexpr int T = Q + NT * Tile<ET, DK, 64, true>::PLANE * 2;
+  static constexpr int P = T + 3 * kTrapLds * 2;
+  static constexpr int TOK = P + 3 * kTrapLds * 2;
+  static constexpr int BYTES = TOK + kTokArrays * C * 4;
+};
+
+// Sum over the 16 lanes of a group (DPP operand modifiers), in every lane.
+__device__ __forceinline__ float sum16(float x) {
+  auto add = [](float v, float o) { return v + o; };
+  x = add(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0xB1, 0xf, 0xf, true)));   // lane ^ 1
+  x = add(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x4E, 0xf, 0xf, true)));   // lane ^ 2
+  x = add(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x141, 0xf, 0xf, true)));  // mirror of 8
+  x = add(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x140, 0xf, 0xf, true)));  // mirror of 16
+  return x;
+}
+
+template <typename ET, int DK, int NW, bool VEC>
+__global__ __launch_bounds__(64 * NW, 1) void k_delta_back(const DeltaParams p) {
+  using L = BackLds<ET, DK>;
+  constexpr int NT = L::NT, NTHR = 64 * NW, KB = DK / 32;
+  using TK = Tile<ET, DK, NTHR, VEC>;
+  extern __shared__ __align__(16) char lds[];
+  uint16_t* sK = reinterpret_cast<uint16_t*>(lds + L::K);
+  uint16_t* sQ = reinterpret_cast<uint16_t*>(lds + L::Q);
+  uint16_t* sT = reinterpret_cast<uint16_t*>(lds + L::T);
+  uint16_t* sP = reinterpret_cast<uint16_t*>(lds + L::P);
+  float* tok = reinterpret_cast<float*>(lds + L::TOK);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q = lane >> 4, n16 = lane & 15;
+  const int ncb = delta_cols(p, NW);
+  const uint32_t bid = xcd_logical_block(blockIdx.x, gridDim.x);
+  const int cg = int(bid % ncb) * NW + wave;
+  const bool live = cg < p.nCG;  // a wave past the last column group still stages tiles
+  const int64_t bh = bid / ncb;
+  const int hv = int(bh % p.Hv), b = int(bh / p.Hv), hk = hv / p.group;
+  const int col = cg * kDeltaCols + n16;
+  const bool ok = col < p.dvn;
+  const ET* kbase = static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2;
+  const ET* qbase = static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2;
+  const ET* vbase = static_cast<const ET*>(p.v) + b * p.vs0 + hv * p.vs2;
+  const ET* dobase = static_cast<const ET*>(p.dO) + b * p.dos0 + hv * p.dos2;
+  ET* dvbase = static_cast<ET*>(p.dv) + b * p.dvs0 + hv * p.dvs2;
+
+  f32x4_t dS[DK / 16];
+  load_state<DK>(dS, p.dstate_out == nullptr ? nullptr : p.dstate_out + b * p.dsos0 + hv * p.dsos1, p.dsos2, p.dkn, col,
+                 ok);
+  // the tiles below the diagonal of P^T that a 32-wide contraction block still reads
+  for (int e = tid; e < 3 * 128; e += NTHR) {
+    const int n = e >> 7, row = (e >> 2) & 31, part = e & 3;
+    const int i = row < 16 ? row + 16 : row + 32, j = (row < 16 ? 0 : 32) + 4 * part;
+    *reinterpret_cast<u32x2*>(sP + n * kTrapLds + utrap_off(i, j)) = u32x2{0u, 0u};
+  }
+
+  TK tk, tq;
+  TrapTile<NTHR> tt;
+  f32x4_t ttok[(kTokArrays * C / 4 + NTHR - 1) / NTHR];
+  float vn[16], don[16];
+  auto fetch = [&](int c) {
+    const int t0 = c * C, rows = min(C, p.T - t0);
+    tk.load(kbase, p.ks1, t0, rows, p.dkn);
+    tq.load(qbase, p.qs1, t0, rows, p.dkn);
+    tt.load(p.wT + (bh * p.nC + c) * (3 * kTrapElems));
+    const f32x4_t* w = reinterpret_cast<const f32x4_t*>(p.wTok + (bh * p.nC + c) * (kTokArrays * C));
+#pragma unroll
+    for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i) ttok[i] = w[min(tid + i * NTHR, kTokArrays * C / 4 - 1)];
+    load_cols<ET>(vn, vbase, p.vs1, t0, p.T, col, ok);
+    load_cols<ET>(don, dobase, p.dos1, t0, p.T, col, ok);
+  };
+  fetch(p.nC - 1);
+  for (int c = p.nC - 1; c >= 0; --c) {
+    const int64_t ci = bh * p.nC + c;
+    const int64_t cim = ci * p.nCG + (live ? cg : 0);
+    __syncthreads();  // every wave is done with the previous chunk's tiles
+    tk.store(sK);
+    tq.store(sQ);
+    tt.store(sT);
+#pragma unroll
+    for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i)
+      if (tid + i * NTHR < kTokArrays * C / 4) reinterpret_cast<f32x4_t*>(tok)[tid + i * NTHR] = ttok[i];
+    f32x4_t v[4], dO[4], S0[DK / 16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      v[e >> 2][e & 3] = vn[e];
+      dO[e >> 2][e & 3] = don[e];
+    }
+    load_image<DK / 16>(S0, p.wS + cim * (DK * 16));
+    __syncthreads();
+    if (c > 0) fetch(c - 1);
+
+    // P^T: tiles of P = scale Gam o Q K^T (rows i, column j), four neighbours of a row of P^T
+    for (int t = wave; t < 10; t += NW) {
+      int ti, tj;
+      tile_of(t, ti, tj);
+      f32x4_t acc = zero4();
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+        mma<2>(acc, rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb),
+               rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb));
+      const int j = 16 * tj + n16, i0 = 16 * ti + 4 * q;
+      const float gh = tok[kTokGhi * C + j], gl = tok[kTokGlo * C + j], rkj = tok[kTokRk * C + j] * p.scale;
+      const int nj = __float_as_int(tok[kTokN * C + j]);
+      const f32x4_t ghi = ld4(tok + kTokGhi * C + i0), gli = ld4(tok + kTokGlo * C + i0);
+      const f32x4_t ni = ld4(tok + kTokN * C + i0), rqi = ld4(tok + kTokRq * C + i0);
+      f32x4_t x;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        x[r] = j <= i0 + r ? acc[r] * rkj * rqi[r] * gam(ghi[r], gli[r], __float_as_int(ni[r]), gh, gl, nj) : 0.f;
+      put4<3>(sP + utrap_off(j, i0), kTrapLds, x);
+    }
+
+    if (live) store_image<DK / 16>(dS, p.wdS + cim * (DK * 16));
+    f32x4_t KdS[4];  // D (K dS1)
+    {
+      Frag<3> sf[KB];
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(dS[2 * kb], dS[2 * kb + 1]);
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        f32x4_t acc = zero4();
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) mma<2>(acc, rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * mt, 32 * kb), sf[kb]);
+        const int t = 16 * mt + 4 * q;
+        const f32x4_t d = ld4(tok + kTokD * C + t), rk = ld4(tok + kTokRk * C + t);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) KdS[mt][r] = acc[r] * d[r] * rk[r];
+      }
+    }
+    f32x4_t KS[4], QS[4];  // E (K S0), scale E (Q S0)
+    {
+      Frag<3> sf[KB];
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(S0[2 * kb], S0[2 * kb + 1]);
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        f32x4_t a = zero4(), o = zero4();
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          mma<2>(a, rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * mt, 32 * kb), sf[kb]);
+          mma<2>(o, rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * mt, 32 * kb), sf[kb]);
+        }
+        const int t = 16 * mt + 4 * q;
+        const f32x4_t e = ld4(tok + kTokE * C + t), rk = ld4(tok + kTokRk * C + t), rq = ld4(tok + kTokRq * C + t);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          KS[mt][r] = a[r] * e[r] * rk[r];
+          QS[mt][r] = o[r] * e[r] * rq[r] * p.scale;
+        }
+      }
+    }
+    f32x4_t z[4], u[4];
+    {
+      f32x4_t bz[4];
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        z[mt] = v[mt] - KS[mt];
+        bz[mt] = z[mt] * ld4(tok + kTokBeta * C + 16 * mt + 4 * q);
+      }
+      const Frag<3> zf[2] = {split8<3>(bz[0], bz[1]), split8<3>(bz[2], bz[3])};
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        u[mt] = zero4();
+#pragma unroll
+        for (int kb = 0; kb <= mt / 2; ++kb) mma<2>(u[mt], trap_row<3>(sT, mt, kb), zf[kb]);
+      }
+    }
+    if (live) store_image<4>(u, p.wU + cim * (C * kDeltaCols));
+    __syncthreads();  // P^T is complete
+    f32x4_t dR[4];
+    {
+      f32x4_t dU[4];
+      const Frag<NT> of[2] = {split8<NT>(dO[0], dO[1]), split8<NT>(dO[2], dO[3])};
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        dU[mt] = KdS[mt];
+#pragma unroll
+        for (int kb = mt / 2; kb < 2; ++kb) mma<2>(dU[mt], utrap_row<3>(sP, mt, kb), of[kb]);
+      }
+      const Frag<3> uf[2] = {split8<3>(dU[0], dU[1]), split8<3>(dU[2], dU[3])};
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        dR[mt] = zero4();
+#pragma unroll
+        for (int kb = mt / 2; kb < 2; ++kb) mma<2>(dR[mt], trap_col<3>(sT, mt, kb), uf[kb]);
+      }
+    }
+    if (live) store_image<4>(dR, p.wR + cim * (C * kDeltaCols));
+    f32x4_t dz[4];
+    float* dot = p.wDot + cim * (4 * C);
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+      const int t = 16 * mt + 4 * q;
+      dz[mt] = dR[mt] * ld4(tok + kTokBeta * C + t);
+      f32x4_t into, out, rz;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        into[r] = sum16(dO[mt][r] * QS[mt][r] - dz[mt][r] * KS[mt][r]);
+        out[r] = sum16(KdS[mt][r] * u[mt][r]);
+        rz[r] = sum16(dR[mt][r] * z[mt][r]);
+      }
+      if (live && n16 == 0) {
+        *reinterpret_cast<f32x4_t*>(dot + t) = into;
+        *reinterpret_cast<f32x4_t*>(dot + C + t) = out;
+        *reinterpret_cast<f32x4_t*>(dot + 2 * C + t) = rz;
+      }
+    }
+    store_cols<ET>(dz, dvbase, p.dvs1, c * C, p.T, col, ok);
+    const float gamma = tok[kTokE * C + C - 1];
+    {
+      float h = 0.f;
+#pragma unroll
+      for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h += S0[i][r] * dS[i][r];
+      h = sum16(h);
+      h += __shfl_xor(h, 16);
+      h += __shfl_xor(h, 32);
+      if (live && lane == 0) dot[3 * C] = gamma * h;
+    }
+    {
+      f32x4_t eo[4], er[4];
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        const int t = 16 * mt + 4 * q;
+        const f32x4_t e = ld4(tok + kTokE * C + t), rk = ld4(tok + kTokRk * C + t), rq = ld4(tok + kTokRq * C + t);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          eo[mt][r] = dO[mt][r] * e[r] * rq[r] * p.scale;
+          er[mt][r] = -(dz[mt][r] * e[r] * rk[r]);
+        }
+      }
+      const Frag<3> of[2] = {split8<3>(eo[0], eo[1]), split8<3>(eo[2], eo[3])};
+      const Frag<3> rf[2] = {split8<3>(er[0], er[1]), split8<3>(er[2], er[3])};
+#pragma unroll
+      for (int i = 0; i < DK / 16; ++i) {
+        dS[i] *= gamma;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          mma<2>(dS[i], colfrag<NT>(sQ, TK::LD, TK::PLANE, 32 * kb, 16 * i), of[kb]);
+          mma<2>(dS[i], colfrag<NT>(sK, TK::LD, TK::PLANE, 32 * kb, 16 * i), rf[kb]);
+        }
+      }
+    }
+  }
+  store_state<DK>(dS, p.dstate == nullptr ? nullptr : p.dstate + b * p.dsis0 + hv * p.dsis1, p.dsis2, p.dkn, col, ok);
+}
+
+// ---------------------------------------------------------------------------------
+// Backward: dq, dk, dg, dbeta of one chunk and key head
+// ---------------------------------------------------------------------------------
+//
+// Over the value columns (32 at a time, staged from the scan's images):
+//   dP = scale dO U^T,  F = dR U^T  (dA = -F),  dO S0^T,  U dS1^T,  dR S0^T,
+// then with Y = rq rk Gam o dP (i >= j), Yk = -beta rk rk Gam o F (i > j) and raw q, k:
+//   dq' = rq scale E (dO S0^T) + Y K
+//   dk' = rk (D (U dS1^T) - beta E (dR S0^T)) + Y^T Q + (Yk + Yk^T) K
+// are rq dq and rk dk in terms of the normalised rows; the norm's own gradient takes their
+// part along q (k) away: dq = dq' - rq q (rq q.dq'). The decay's gradient adds up all paths
+// that cross a token, dg_t = sum_{i >= t > j} X_ij + sum_{i >= t} into_i + sum_{j < t} out_j
+// + gamma <S0, dS1> with X = Y o Q K^T + Yk o K K^T, from row and column sums of the same
+// products, so that pairs on one side of t cancel exactly; the cumulative sums are in 64 bits.
+
+template <typename ET, int DK>
+struct GradLds {
+  static constexpr int NT = Store<ET>::NT, NP = Store<ET>::NP;
+  static constexpr int ULD = C + 8, OLD = 40, SLD = DK + 8;
+  static constexpr int UPL = 32 * ULD, OPL = C * OLD, SPL = 32 * SLD;
+  // first part: staged operands of 32 value columns
+  static constexpr int U = 0;
+  static constexpr int R = U + 3 * UPL * 2;
+  static constexpr int O = R + 3 * UPL * 2;
+  static constexpr int S = O + NT * OPL * 2;
+  static constexpr int G = S + NP * SPL * 2;
+  static constexpr int END1 = G + NP * SPL * 2;
+  // second part, in the same place
+  static constexpr int K = 0;
+  static constexpr int Q = K + NT * Tile<ET, DK, 64, true>::PLANE * 2;
+  static constexpr int Y = Q + NT * Tile<ET, DK, 64, true>::PLANE * 2;
+  static constexpr int YK = Y + NP * kTrapLds * 2;
+  static constexpr int END2 = YK + NP * kTrapLds * 2;
+  static constexpr int TOK = END1 > END2 ? END1 : END2;
+  static constexpr int SUM = TOK + kTokArrays * C * 4;  // row, column and beta sums [3][4][64]
+  static constexpr int BYTES = SUM + 3 * 4 * C * 4;
+};
+
+// Stages rows [16 half .. +15] of a [columns][index] matrix from an image of NB blocks of 32 indices.
+template <int N, int NB>
+__device__ __forceinline__ void stage_image(uint16_t* m, int ld, int plane, const float* src, bool have) {
+  for (int e = threadIdx.x; e < NB * 64 * 2; e += 256) {
+    const int kb = e >> 7, l = (e >> 1) & 63, h = e & 1;
+    const f32x4_t x = have ? reinterpret_cast<const f32x4_t*>(src)[e] : zero4();
+    put4<N>(m + (l & 15) * ld + 32 * kb + 16 * h + 4 * (l >> 4), plane, x);
+  }
+}
+
+template <typename ET, int DK, bool VEC>
+__global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
+  using L = GradLds<ET, DK>;
+  constexpr int NT = L::NT, NP = L::NP, LV = NP - 1, KB = DK / 32, NN = DK / 64;
+  using TK = Tile<ET, DK, 256, VEC>;
+  extern __shared__ __align__(16) char lds[];
+  uint16_t* sU = reinterpret_cast<uint16_t*>(lds + L::U);
+  uint16_t* sR = reinterpret_cast<uint16_t*>(lds + L::R);
+  uint16_t* sO = reinterpret_cast<uint16_t*>(lds + L::O);
+  uint16_t* sS = reinterpret_cast<uint16_t*>(lds + L::S);
+  uint16_t* sG = reinterpret_cast<uint16_t*>(lds + L::G);
+  uint16_t* sK = reinterpret_cast<uint16_t*>(lds + L::K);
+  uint16_t* sQ = reinterpret_cast<uint16_t*>(lds + L::Q);
+  uint16_t* sY = reinterpret_cast<uint16_t*>(lds + L::Y);
+  uint16_t* sYk = reinterpret_cast<uint16_t*>(lds + L::YK);
+  float* tok = reinterpret_cast<float*>(lds + L::TOK);
+  float* sum = reinterpret_cast<float*>(lds + L::SUM);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q = lane >> 4, n16 = lane & 15;
+  const int64_t id = blockIdx.x;
+  const int c = int(id % p.nC);
+  const int hk = int(id / p.nC % p.Hk);
+  const int b = int(id / p.nC / p.Hk);
+  const int t0 = c * C, rows = min(C, p.T - t0);
+  const int dt0 = wave * NN;  // first of this wave's 16-wide tiles of dk columns
+
+  f32x4_t aq[4][NN], ak[4][NN];
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+    for (int n = 0; n < NN; ++n) aq[mt][n] = ak[mt][n] = zero4();
+
+  for (int gh = 0; gh < p.group; ++gh) {
+    const int hv = hk * p.group + gh;
+    const int64_t ci = (int64_t(b) * p.Hv + hv) * p.nC + c;
+    const ET* dobase = static_cast<const ET*>(p.dO) + b * p.dos0 + hv * p.dos2;
+    f32x4_t dP[3], F[3];
+#pragma unroll
+    for (int s = 0; s < 3; ++s) dP[s] = F[s] = zero4();
+    f32x4_t os[4][NN], ug[4][NN], rs[4][NN];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int n = 0; n < NN; ++n) os[mt][n] = ug[mt][n] = rs[mt][n] = zero4();
+
+    for (int cb = 0; cb < p.nCG; cb += 2) {
+      __syncthreads();  // the previous contents are read
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool have = cb + h < p.nCG;
+        const int64_t cim = ci * p.nCG + (have ? cb + h : cb);
+        stage_image<3, 2>(sU + 16 * h * L::ULD, L::ULD, L::UPL, p.wU + cim * (C * kDeltaCols), have);
+        stage_image<3, 2>(sR + 16 * h * L::ULD, L::ULD, L::UPL, p.wR + cim * (C * kDeltaCols), have);
+        stage_image<NP, KB>(sS + 16 * h * L::SLD, L::SLD, L::SPL, p.wS + cim * (DK * 16), have);
+        stage_image<NP, KB>(sG + 16 * h * L::SLD, L::SLD, L::SPL, p.wdS + cim * (DK * 16), have);
+      }
+      {
+        const int row = tid >> 2, cc = (tid & 3) * 8, c0 = cb * kDeltaCols + cc;
+        const int cs = c0 < p.dvn ? c0 : 0;
+        const int n = row < rows && c0 < p.dvn ? p.dvn - c0 : 0;
+        const int64_t off = int64_t(t0 + min(row, rows - 1)) * p.dos1 + cs;
+        const Raw8<ET> r = p.vecdo ? load8<ET, true>(dobase, off, n, p.dvn - cs) : load8<ET, false>(dobase, off, n, p.dvn - cs);
+        const Frag<NT> f = terms8<ET>(r);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) *reinterpret_cast<u32x4*>(sO + i * L::OPL + row * L::OLD + cc) = f.t[i];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < 3; ++s) {
+        const int t = wave + 4 * s;
+        if (t < 10) {
+          int ti, tj;
+          tile_of(t, ti, tj);
+          const auto fu = colfrag<3>(sU, L::ULD, L::UPL, 0, 16 * tj);
+          mma<2>(dP[s], fu, rowfrag<NT>(sO, L::OLD, L::OPL, 16 * ti, 0));
+          mma<2>(F[s], fu, colfrag<3>(sR, L::ULD, L::UPL, 0, 16 * ti));
+        }
+      }
+      Frag<NP> fs[NN], fg[NN];
+#pragma unroll
+      for (int n = 0; n < NN; ++n) {
+        fs[n] = colfrag<NP>(sS, L::SLD, L::SPL, 0, 16 * (dt0 + n));
+        fg[n] = colfrag<NP>(sG, L::SLD, L::SPL, 0, 16 * (dt0 + n));
+      }
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        const auto fo = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * mt, 0);
+        const auto fu = colfrag<NP>(sU, L::ULD, L::UPL, 0, 16 * mt);
+        const auto fr = colfrag<NP>(sR, L::ULD, L::UPL, 0, 16 * mt);
+#pragma unroll
+        for (int n = 0; n < NN; ++n) {
+          mma<LV>(os[mt][n], fo, fs[n]);
+          mma<LV>(ug[mt][n], fu, fg[n]);
+          mma<LV>(rs[mt][n], fr, fs[n]);
+        }
+      }
+    }
+    __syncthreads();
+    {
+      TK tk, tq;
+      tk.load(static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2, p.ks1, t0, rows, p.dkn);
+      tq.load(static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2, p.qs1, t0, rows, p.dkn);
+      if (tid < kTokArrays * C / 4)
+        reinterpret_cast<f32x4_t*>(tok)[tid] = reinterpret_cast<const f32x4_t*>(p.wTok + ci * (kTokArrays * C))[tid];
+      // tiles above the diagonal that a 32-wide block reads, and sums of tiles that do not exist
+      for (int e = tid; e < 2 * NP * 128; e += 256) {
+        const int n = e >> 7, row = (e >> 2) & 31, part = e & 3;
+        const int i = row < 16 ? row : row + 16, j = (row < 16 ? 16 : 48) + 4 * part;
+        *reinterpret_cast<u32x2*>((n < NP ? sY + n * kTrapLds : sYk + (n - NP) * kTrapLds) + trap_off(i) + j) = u32x2{0u, 0u};
+      }
+      for (int e = tid; e < 3 * 4 * C; e += 256) sum[e] = 0.f;
+      tk.store(sK);
+      tq.store(sQ);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+      const int t = wave + 4 * s;
+      if (t < 10) {
+        int ti, tj;
+        tile_of(t, ti, tj);
+        f32x4_t qk = zero4(), kk = zero4();
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          const auto fj = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb);
+          mma<2>(qk, fj, rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb));
+          mma<2>(kk, fj, rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * ti, 32 * kb));
+        }
+        const int i = 16 * ti + n16, j0 = 16 * tj + 4 * q;
+        const float ghi = tok[kTokGhi * C + i], glo = tok[kTokGlo * C + i], rki = tok[kTokRk * C + i];
+        const float rqi = tok[kTokRq * C + i], be = tok[kTokBeta * C + i];
+        const int ni = __float_as_int(tok[kTokN * C + i]);
+        const f32x4_t ghj = ld4(tok + kTokGhi * C + j0), glj = ld4(tok + kTokGlo * C + j0);
+        const f32x4_t nj = ld4(tok + kTokN * C + j0), rkj = ld4(tok + kTokRk * C + j0);
+        f32x4_t y, yk;
+        float xi = 0.f, bi = 0.f, xj[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int j = j0 + r;
+          const float gm = j <= i ? gam(ghi, glo, ni, ghj[r], glj[r], __float_as_int(nj[r])) * rkj[r] : 0.f;
+          y[r] = p.scale * rqi * gm * dP[s][r];
+          const float f = j < i ? -(rki * gm * F[s][r]) : 0.f;
+          yk[r] = be * f;
+          const float x = j < i ? y[r] * qk[r] + yk[r] * kk[r] : 0.f;
+          xi += x;
+          xj[r] = x;
+          bi += f * kk[r];
+        }
+        put4<NP>(sY + trap_off(i) + j0, kTrapLds, y);
+        put4<NP>(sYk + trap_off(i) + j0, kTrapLds, yk);
+        xi += __shfl_xor(xi, 16);
+        bi += __shfl_xor(bi, 16);
+        xi += __shfl_xor(xi, 32);
+        bi += __shfl_xor(bi, 32);
+        if (q == 0) {
+          sum[tj * C + i] = xi;
+          sum[8 * C + tj * C + i] = bi;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) xj[r] = sum16(xj[r]);
+        if (n16 == 0) *reinterpret_cast<f32x4_t*>(sum + 4 * C + ti * C + j0) = f32x4_t{xj[0], xj[1], xj[2], xj[3]};
+      }
+    }
+    __syncthreads();
+    if (wave == 0) {  // dg and dbeta, one token per lane
+      float into = 0.f, out = 0.f, rz = 0.f, through = 0.f;
+      for (int g = 0; g < p.nCG; ++g) {
+        const float* dot = p.wDot + (ci * p.nCG + g) * (4 * C);
+        into += dot[lane];
+        out += dot[C + lane];
+        rz += dot[2 * C + lane];
+        through += dot[3 * C];
+      }
+      double ahead = out, behind = into;
+      float db = rz;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        ahead += double(sum[4 * C + s * C + lane]) - double(sum[s * C + lane]);
+        db += sum[8 * C + s * C + lane];
+      }
+      const double own = ahead;
+#pragma unroll
+      for (int m = 1; m < 64; m <<= 1) {
+        const double a = __shfl_up(ahead, m), h = __shfl_down(behind, m);
+        if (lane >= m) ahead += a;
+        if (lane + m < 64) behind += h;
+      }
+      const int n = __float_as_int(tok[kTokN * C + lane]);
+      const int before = lane == 0 ? 0 : __float_as_int(tok[kTokN * C + lane - 1]);
+      const float dg = n != before ? 0.f : float(ahead - own + behind + double(through));
+      if (lane < rows) {
+        p.dg[b * p.dgs0 + (t0 + lane) * p.dgs1 + hv * p.dgs2] = dg;
+        stf<ET>(p.dbeta, b * p.dbs0 + (t0 + lane) * p.dbs1 + hv * p.dbs2, db);
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+      const int t = 16 * mt + 4 * q;
+      const f32x4_t e = ld4(tok + kTokE * C + t), d = ld4(tok + kTokD * C + t), be = ld4(tok + kTokBeta * C + t);
+      const f32x4_t rk = ld4(tok + kTokRk * C + t), rq = ld4(tok + kTokRq * C + t);
+#pragma unroll
+      for (int n = 0; n < NN; ++n) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          aq[mt][n][r] += rq[r] * p.scale * e[r] * os[mt][n][r];
+          ak[mt][n][r] += rk[r] * (d[r] * ug[mt][n][r] - be[r] * e[r] * rs[mt][n][r]);
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          const int dc = 16 * (dt0 + n);
+          if (kb <= mt / 2) {
+            const auto fk = colfrag<NT>(sK, TK::LD, TK::PLANE, 32 * kb, dc);
+            mma<LV>(aq[mt][n], trap_row<NP>(sY, mt, kb), fk);
+            mma<LV>(ak[mt][n], trap_row<NP>(sYk, mt, kb), fk);
+          }
+          if (kb >= mt / 2) {
+            mma<LV>(ak[mt][n], trap_col<NP>(sY, mt, kb), colfrag<NT>(sQ, TK::LD, TK::PLANE, 32 * kb, dc));
+            mma<LV>(ak[mt][n], trap_col<NP>(sYk, mt, kb), colfrag<NT>(sK, TK::LD, TK::PLANE, 32 * kb, dc));
+          }
+        }
+      }
+    }
+  }
+
+  // the norms' own gradients, then out; q and k of the last head are still in LDS
+  auto element = [&](const uint16_t* m, int t, int d) {
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) x += __uint_as_float(uint32_t(m[i * TK::PLANE + t * TK::LD + d]) << 16);
+    return x;
+  };
+  const bool unit = p.eps >= 0.f;
+  if (unit) {
+    __syncthreads();
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * mt + 4 * q + r;
+        float a = 0.f, k = 0.f;
+#pragma unroll
+        for (int n = 0; n < NN; ++n) {
+          a += aq[mt][n][r] * element(sQ, t, 16 * (dt0 + n) + n16);
+          k += ak[mt][n][r] * element(sK, t, 16 * (dt0 + n) + n16);
+        }
+        a = sum16(a);
+        k = sum16(k);
+        if (n16 == 0) {
+          sum[wave * C + t] = a;
+          sum[4 * C + wave * C + t] = k;
+        }
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 16 * mt + 4 * q + r;
+      float pq = 0.f, pk = 0.f;
+      if (unit) {
+        const float rq = tok[kTokRq * C + t], rk = tok[kTokRk * C + t];
+        pq = rq * rq * (sum[t] + sum[C + t] + sum[2 * C + t] + sum[3 * C + t]);
+        pk = rk * rk * (sum[4 * C + t] + sum[5 * C + t] + sum[6 * C + t] + sum[7 * C + t]);
+      }
+#pragma unroll
+      for (int n = 0; n < NN; ++n) {
+        const int d = 16 * (dt0 + n) + n16;
+        float a = aq[mt][n][r], k = ak[mt][n][r];
+        if (unit) {
+          a -= pq * element(sQ, t, d);
+          k -= pk * element(sK, t, d);
+        }
+        if (t < rows && d < p.dkn) {
+          stf<ET>(p.dq, b * p.dqs0 + (t0 + t) * p.dqs1 + hk * p.dqs2 + d, a);
+          stf<ET>(p.dk, b * p.dks0 + (t0 + t) * p.dks1 + hk * p.dks2 + d, k);
+        }
+      }
+    }
+  }
+}
+
 template <typename KernelT>
 hipError_t launch_delta(KernelT kernel, int64_t blocks, int threads, int lds_bytes, const DeltaParams& p,
                         hipStream_t s) {
@@ -772,6 +1368,24 @@ template <typename ET>
 hipError_t delta_fwd_et(const DeltaParams& p, hipStream_t s) {
   if (p.vec) return delta_dk_pad(p.dkn) == 64 ? delta_fwd_dk<ET, 64, true>(p, s) : delta_fwd_dk<ET, 128, true>(p, s);
   return delta_dk_pad(p.dkn) == 64 ? delta_fwd_dk<ET, 64, false>(p, s) : delta_fwd_dk<ET, 128, false>(p, s);
+}
+
+template <typename ET, int DK, bool VEC>
+hipError_t delta_bwd_dk(const DeltaParams& p, hipStream_t s) {
+  hipError_t e = delta_prep_launch<ET, DK, VEC>(p, s);
+  if (e == hipSuccess) e = delta_scan_launch<ET, DK, true, VEC>(p, s);
+  constexpr int NW = 4;
+  const int64_t blocks = int64_t(p.B) * p.Hv * ((p.nCG + NW - 1) / NW);
+  if (e == hipSuccess) e = launch_delta(k_delta_back<ET, DK, NW, VEC>, blocks, 64 * NW, BackLds<ET, DK>::BYTES, p, s);
+  if (e == hipSuccess)
+    e = launch_delta(k_delta_grad<ET, DK, VEC>, int64_t(p.B) * p.Hk * p.nC, 256, GradLds<ET, DK>::BYTES, p, s);
+  return e;
+}
+
+template <typename ET>
+hipError_t delta_bwd_et(const DeltaParams& p, hipStream_t s) {
+  if (p.vec) return delta_dk_pad(p.dkn) == 64 ? delta_bwd_dk<ET, 64, true>(p, s) : delta_bwd_dk<ET, 128, true>(p, s);
+  return delta_dk_pad(p.dkn) == 64 ? delta_bwd_dk<ET, 64, false>(p, s) : delta_bwd_dk<ET, 128, false>(p, s);
 }
 
 }  // namespace delta

@@ -506,6 +506,42 @@ def dynconv_delta_fwd(q, k, v, g, beta, scale: float | None = None, qk_norm_eps:
     return o if state_out is None else (o, state_out)
 
 
+def dynconv_delta_bwd(q, k, v, g, beta, do, scale: float | None = None, qk_norm_eps: float | None = None, seq_idx=None,
+                      state=None, dstate_out=None, need_dstate: bool = False):
+    """(dq, dk, dv, dg, dbeta, dstate) of <do, o> (+ <dstate_out, final state> with the float32
+    [B,Hv,dk,dv] gradient of the state after the last token) for dynconv_delta_fwd with the
+    same arguments; dg is float32, dstate (float32, the gradient of `state`) None unless
+    need_dstate. The states are recomputed, nothing is kept from the forward."""
+    (B, T), Hk, Hv, dk, dv = _delta_shapes(q, k, v, g, beta, False)
+    scale, eps = _delta_consts(scale, qk_norm_eps, dk)
+    _expect("do", do, (B, T, Hv, dv), q.dtype)
+    _expect("state", state, (B, Hv, dk, dv), torch.float32)
+    _expect("dstate_out", dstate_out, (B, Hv, dk, dv), torch.float32)
+    dev = _require_device(q, k, v, g, beta, do, seq_idx, state, dstate_out)
+    seg = _seg_args(seq_idx, B, T) if seq_idx is not None else (None, None)
+
+    def new(shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+    dq, dk_ = new((B, T, Hk, dk), q.dtype), new((B, T, Hk, dk), q.dtype)
+    dv_, dg, dbeta = new((B, T, Hv, dv), q.dtype), new((B, T, Hv), torch.float32), new((B, T, Hv), q.dtype)
+    dstate = None
+    if need_dstate:  # without tokens the state's gradient passes through
+        dstate = new((B, Hv, dk, dv), torch.float32) if T else (
+            torch.zeros((B, Hv, dk, dv), dtype=torch.float32, device=dev) if dstate_out is None else dstate_out.clone())
+    lib = _lib.load()
+    code = _dtype_code(q)
+    ws_bytes = int(lib.dynconv_delta_bwd_workspace_size(B, T, Hk, Hv, dk, dv, code))
+    work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    with _on(dev):
+        st = lib.dynconv_delta_bwd(*_sp(q), *_sp(k), *_sp(v), *_sp(g), *_sp(beta), *seg, *_sp(state), *_sp(do),
+                                   *_sp(dstate_out), *_sp(dq), *_sp(dk_), *_sp(dv_), *_sp(dg), *_sp(dbeta),
+                                   *_sp(dstate), B, T, Hk, Hv, dk, dv, scale, eps, code, _ptr(work), ws_bytes,
+                                   _stream(dev))
+    _lib.check("dynconv_delta_bwd", st)
+    return dq, dk_, dv_, dg, dbeta, dstate
+
+
 def dynconv_delta_step(q, k, v, g, beta, state, scale: float | None = None, qk_norm_eps: float | None = None, out=None):
     """o [B,Hv,dv] of one token of every sequence (q, k [B,Hk,dk], v [B,Hv,dv], g float32 and
     beta [B,Hv]); state (float32 [B,Hv,dk,dv]) is updated in place."""

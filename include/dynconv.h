@@ -398,6 +398,30 @@ size_t dynconv_delta_fwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_
                                         dynconv_dtype dtype);
 
 /*
+ * Backward of dynconv_delta_fwd given dO = dL/do [B,T,Hv,dv] and, optionally, the gradient of
+ * the final state (dstate_out float32 [B,Hv,dk,dv], or NULL): the exact adjoints
+ *   dq, dk    [B,T,Hk,dk] (through the normalisation; summed over the value heads of a key head)
+ *   dv        [B,T,Hv,dv], dbeta [B,T,Hv] of `dtype`
+ *   dg        float32 [B,T,Hv] (0 at a document start and where exp(g) is 0)
+ *   dstate_in float32 [B,Hv,dk,dv], the gradient of the initial state, or NULL to skip.
+ * States are recomputed from the inputs; nothing is kept from the forward. Needs
+ * dynconv_delta_bwd_workspace_size(...) bytes (per 64 tokens and value head about 20 KiB +
+ * (8 dk' + 0.5 KiB + 1 KiB) dv with dk' = 64 or 128). T == 0 is a no-op.
+ */
+dynconv_status dynconv_delta_bwd(const void* q, const int64_t* qs, const void* k, const int64_t* ks, const void* v,
+                                 const int64_t* vs, const float* g, const int64_t* gs, const void* beta,
+                                 const int64_t* bs, const int32_t* seq_idx, const int64_t* ss, const float* state_in,
+                                 const int64_t* sis, const void* dO, const int64_t* dos, const float* dstate_out,
+                                 const int64_t* dsos, void* dq, const int64_t* dqs, void* dk_, const int64_t* dks,
+                                 void* dv_, const int64_t* dvs, float* dg, const int64_t* dgs, void* dbeta,
+                                 const int64_t* dbs, float* dstate_in, const int64_t* dsis, int64_t B, int64_t T,
+                                 int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, float scale, float qk_norm_eps,
+                                 dynconv_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+size_t dynconv_delta_bwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
+                                        dynconv_dtype dtype);
+
+/*
  * One decoding step of the gated delta rule: one token of every sequence, the state updated
  * in place (equal to dynconv_delta_fwd with T = 1).
  *   q, k [B,Hk,dk], v, o [B,Hv,dv] strides s[0..2] (s[2] == 1), g, beta [B,Hv] strides
