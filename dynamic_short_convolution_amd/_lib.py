@@ -55,6 +55,9 @@ EXPORTS = (
     "dynconv_delta_bwd",
     "dynconv_delta_bwd_workspace_size",
     "dynconv_delta_step",
+    "dynconv_norm_fwd",
+    "dynconv_norm_bwd",
+    "dynconv_norm_bwd_workspace_size",
 )
 
 # Bytes of the per-GPU scratch array of dynconv_bwd_ex_noalloc (DYNCONV_NOALLOC_SCRATCH_BYTES).
@@ -155,6 +158,13 @@ _SIGNATURES["dynconv_delta_bwd"] = (  # + dO, dstate_out; dq, dk, dv, dg, dbeta,
 _SIGNATURES["dynconv_delta_bwd_workspace_size"] = (_delta_sizes + [ctypes.c_int], _sz)
 _SIGNATURES["dynconv_delta_step"] = (
     [_vp, _i64p] * 7 + [_i64] * 5 + [_f32, _f32, ctypes.c_int, _vp], ctypes.c_int)
+_SIGNATURES["dynconv_norm_fwd"] = (
+    [_vp, _i64p, _vp, _vp, _i64p, _vp, _i64p, _i32, _f32, _vp, _i64p, _vp, _i64p, _i64, _i64, _i64, _i64, _f32,
+     ctypes.c_int, _vp], ctypes.c_int)
+_SIGNATURES["dynconv_norm_bwd"] = (
+    [_vp, _i64p, _vp, _vp, _i64p, _vp, _i64p, _vp, _i64p, _i32, _f32, _vp, _i64p, _vp, _i64p, _vp, _vp, _i64p, _i64,
+     _i64, _i64, _i64, _f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int)
+_SIGNATURES["dynconv_norm_bwd_workspace_size"] = ([_i64] * 4 + [ctypes.c_int], _sz)
 
 _lib = None
 

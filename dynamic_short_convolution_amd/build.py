@@ -33,6 +33,7 @@ SOURCES = [
     "dynconv_delta_f32.hip",
     "dynconv_delta_bf16.hip",
     "dynconv_delta_f16.hip",
+    "dynconv_norm.hip",
 ]
 
 # -packed-fp32-ops: no v_pk_{add,mul,fma}_f32 are generated from ordinary float code.

@@ -558,3 +558,91 @@ def dynconv_delta_step(q, k, v, g, beta, state, scale: float | None = None, qk_n
                                             Hk, Hv, dk, dv, scale, eps, _dtype_code(q), _stream(dev))
     _lib.check("dynconv_delta_step", st)
     return o
+
+
+# ----------------------------------------------------------------------------------
+# RMS norm with a weight, a SiLU gate and a scaled residual
+# ----------------------------------------------------------------------------------
+
+_NORM_RESIDUAL = {None: 0, "before": 1, "after": 2}
+
+
+def _norm_shape(x):
+    if not 1 <= x.dim() <= 4:
+        raise ValueError(f"x must have 1 to 4 dimensions; got shape {list(x.shape)}")
+    return (1,) * (4 - x.dim()) + tuple(x.shape)
+
+
+def _sp4(t):
+    """(pointer, four strides) of a tensor of up to 4 dimensions, or two NULLs."""
+    return (_ptr(t), _lib.strides([0] * (4 - t.dim()) + list(t.stride()))) if t is not None else (None, None)
+
+
+def _norm_weight(weight, x):
+    if weight is None:
+        return
+    _expect("weight", weight, (x.shape[-1],), x.dtype)
+    if weight.numel() > 1 and weight.stride(0) != 1:
+        raise ValueError("weight must be contiguous")
+
+
+def dynconv_norm_fwd(x, weight=None, gate=None, residual=None, residual_scale: float = 1.0, residual_at: str = "before",
+                     eps: float = 1e-6, out=None, out_h=None):
+    """y = x / sqrt(mean(x^2) + eps) * weight * silu(gate) over the last dimension of x (1 to 4
+    dimensions; weight [D] and gate, of x's shape, are optional).
+
+    With a residual (x's shape) and residual_at="before", h = residual + residual_scale * x
+    takes x's place, and (y, h) is returned; with "after", y = residual + residual_scale * (...)."""
+    shape = _norm_shape(x)
+    code = _dtype_code(x)
+    if residual_at not in ("before", "after"):
+        raise ValueError(f"residual_at is 'before' or 'after'; got {residual_at!r}")
+    before = residual is not None and residual_at == "before"
+    _norm_weight(weight, x)
+    for name, t in (("gate", gate), ("residual", residual), ("out", out), ("out_h", out_h)):
+        _expect(name, t, x.shape, x.dtype)
+    if out_h is not None and not before:
+        raise ValueError("out_h goes with a residual before the norm")
+    dev = _require_device(x, weight, gate, residual, out, out_h)
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+    h = (torch.empty(x.shape, dtype=x.dtype, device=dev) if out_h is None else out_h) if before else None
+    with _on(dev):
+        st = _lib.load().dynconv_norm_fwd(*_sp4(x), _ptr(weight), *_sp4(gate), *_sp4(residual),
+                                          int(residual_at == "after"), float(residual_scale), *_sp4(y), *_sp4(h),
+                                          *shape, float(eps), code, _stream(dev))
+    _lib.check("dynconv_norm_fwd", st)
+    return (y, h) if before else y
+
+
+def dynconv_norm_bwd(x, weight, dy, gate=None, dh=None, residual_scale: float = 1.0, residual_at: str | None = None,
+                     eps: float = 1e-6):
+    """(dx, dresidual, dweight, dgate) of <dy, y> for dynconv_norm_fwd, None where there is no
+    such input. x is what was normalised: the forward's x or, with residual_at="before", its h
+    (dh is then the gradient of h from its other uses). residual_at=None: no residual; with
+    "after" the residual's gradient is dy itself and None is returned in its place. dweight is
+    float32 [D]."""
+    shape = _norm_shape(x)
+    code = _dtype_code(x)
+    if residual_at not in _NORM_RESIDUAL:
+        raise ValueError(f"residual_at is 'before', 'after' or None; got {residual_at!r}")
+    if dh is not None and residual_at != "before":
+        raise ValueError("dh goes with a residual before the norm")
+    _norm_weight(weight, x)
+    for name, t in (("dy", dy), ("gate", gate), ("dh", dh)):
+        _expect(name, t, x.shape, x.dtype)
+    dev = _require_device(x, weight, dy, gate, dh)
+
+    def new():
+        return torch.empty(x.shape, dtype=x.dtype, device=dev)
+
+    dx, dres, dgate = new(), new() if residual_at == "before" else None, new() if gate is not None else None
+    dw = torch.empty((x.shape[-1],), dtype=torch.float32, device=dev) if weight is not None else None
+    lib = _lib.load()
+    ws_bytes = int(lib.dynconv_norm_bwd_workspace_size(*shape, code)) if dw is not None else 0
+    work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    with _on(dev):
+        st = lib.dynconv_norm_bwd(*_sp4(x), _ptr(weight), *_sp4(gate), *_sp4(dy), *_sp4(dh),
+                                  _NORM_RESIDUAL[residual_at], float(residual_scale), *_sp4(dx), *_sp4(dres), _ptr(dw),
+                                  *_sp4(dgate), *shape, float(eps), code, _ptr(work), ws_bytes, _stream(dev))
+    _lib.check("dynconv_norm_bwd", st)
+    return dx, dres, dw, dgate

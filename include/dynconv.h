@@ -433,6 +433,49 @@ dynconv_status dynconv_delta_step(const void* q, const int64_t* qs, const void* 
                                   int64_t B, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, float scale,
                                   float qk_norm_eps, dynconv_dtype dtype, void* stream);
 
+/*
+ * RMS norm over the last dimension with a weight, a SiLU gate and a scaled residual: the norm
+ * behind the gated delta rule (per head, gated) and the norms before and after a block.
+ *   n = x / sqrt(mean(x^2) + eps),  y = n * weight * silu(gate)
+ * With a residual and residual_after == 0 (the norm before a block, fused with the addition):
+ *   h = residual + residual_scale * x, rounded to `dtype` and written, takes x's place.
+ * With a residual and residual_after != 0 (the norm after a block):
+ *   y = residual + residual_scale * n * weight * silu(gate).
+ *   x, gate, residual, y, h  [n0,n1,n2,D] of `dtype`, strides s[0..3] (elements, >= 0, s[3] == 1);
+ *                            gate and residual may be NULL; h is required (and only used)
+ *                            with a residual before
+ *   weight                   [D] of `dtype`, contiguous, or NULL (ones)
+ * Any D up to 2^24; element alignment (rows that allow 16-byte accesses use them). Sums are
+ * float32. y and h may not be an input or each other (DYNCONV_ERR_INVALID_ARG).
+ */
+dynconv_status dynconv_norm_fwd(const void* x, const int64_t* xs, const void* weight, const void* gate,
+                                const int64_t* gs, const void* residual, const int64_t* rs, int32_t residual_after,
+                                float residual_scale, void* y, const int64_t* ys, void* h, const int64_t* hs, int64_t n0,
+                                int64_t n1, int64_t n2, int64_t D, float eps, dynconv_dtype dtype, void* stream);
+
+enum { DYNCONV_NORM_NO_RESIDUAL = 0, DYNCONV_NORM_RESIDUAL_BEFORE = 1, DYNCONV_NORM_RESIDUAL_AFTER = 2 };
+
+/*
+ * Backward of dynconv_norm_fwd given dy:
+ *   x          what was normalised: the forward's x, or its h with the residual before
+ *   dh         gradient of h from its other uses, or NULL (residual before only)
+ *   dx         gradient of the forward's x
+ *   dresidual  gradient of the residual (before only), or NULL to skip. With the residual
+ *              after it is dy itself and not written.
+ *   dweight    float32 [D], overwritten, or NULL to skip; needs
+ *              dynconv_norm_bwd_workspace_size(...) bytes of workspace (fixed-order partial
+ *              sums, run-to-run deterministic). Without rows it is zero.
+ *   dgate      gradient of the gate; required with a gate
+ */
+dynconv_status dynconv_norm_bwd(const void* x, const int64_t* xs, const void* weight, const void* gate,
+                                const int64_t* gs, const void* dy, const int64_t* dys, const void* dh,
+                                const int64_t* dhs, int32_t residual_at, float residual_scale, void* dx,
+                                const int64_t* dxs, void* dresidual, const int64_t* drs, float* dweight, void* dgate,
+                                const int64_t* dgs, int64_t n0, int64_t n1, int64_t n2, int64_t D, float eps,
+                                dynconv_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+size_t dynconv_norm_bwd_workspace_size(int64_t n0, int64_t n1, int64_t n2, int64_t D, dynconv_dtype dtype);
+
 #ifdef __cplusplus
 }
 #endif
