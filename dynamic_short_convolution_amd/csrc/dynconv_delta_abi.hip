@@ -28,6 +28,11 @@ dynconv_status check_tensor(const void* p, const int64_t* s, int n, const int64_
   return DYNCONV_OK;
 }
 
+// The kernels address a chunk's 64 rows with 32-bit byte offsets: token strides (s[1]) stay
+// below this many elements.
+constexpr int64_t kDeltaMaxTokenStride = int64_t(1) << 22;
+bool far_tokens(const int64_t* s, int64_t T) { return T > 1 && s[1] >= kDeltaMaxTokenStride; }
+
 // Whether rows of the last dimension can be read in 16-byte pieces.
 int wide(const void* p, const int64_t* s, int n, const int64_t* e, int eb) {
   if (!aligned(p, 16)) return 0;
@@ -68,6 +73,7 @@ dynconv_status take_inputs(DeltaParams* p, const void* q, const int64_t* qs, con
     if ((st = check_tensor(v, vs, 4, ev, eb, true, false)) != DYNCONV_OK) return st;
     if ((st = check_tensor(g, gs, 3, eg, 4, false, false)) != DYNCONV_OK) return st;
     if ((st = check_tensor(beta, bs, 3, eg, eb, false, false)) != DYNCONV_OK) return st;
+    if (far_tokens(qs, T) || far_tokens(ks, T) || far_tokens(vs, T)) return DYNCONV_ERR_UNSUPPORTED;
     if (seg != nullptr) {
       if (ss == nullptr) return DYNCONV_ERR_INVALID_ARG;
       if (ss[0] < 0 || ss[1] < 0 || !aligned(seg, 4)) return DYNCONV_ERR_UNSUPPORTED;
@@ -131,6 +137,7 @@ dynconv_status dynconv_delta_fwd(const void* q, const int64_t* qs, const void* k
   const int64_t ev[4] = {B, T, Hv, dv}, est[4] = {B, Hv, dk, dv};
   if (T > 0) {
     if ((st = check_tensor(o, os, 4, ev, elem_bytes(dtype), true, true)) != DYNCONV_OK) return st;
+    if (far_tokens(os, T)) return DYNCONV_ERR_UNSUPPORTED;
     p.out = o;
     p.os0 = os[0], p.os1 = os[1], p.os2 = os[2];
   }
@@ -187,6 +194,7 @@ dynconv_status dynconv_delta_bwd(const void* q, const int64_t* qs, const void* k
   if ((st = check_tensor(dv_, dvs, 4, ev, eb, true, true)) != DYNCONV_OK) return st;
   if ((st = check_tensor(dg, dgs, 3, eg, 4, false, true)) != DYNCONV_OK) return st;
   if ((st = check_tensor(dbeta, dbs, 3, eg, eb, false, true)) != DYNCONV_OK) return st;
+  if (far_tokens(dos, T) || far_tokens(dvs, T)) return DYNCONV_ERR_UNSUPPORTED;
   p.dO = dO, p.dq = dq, p.dk = dk_, p.dv = dv_, p.dg = dg, p.dbeta = dbeta;
   p.dos0 = dos[0], p.dos1 = dos[1], p.dos2 = dos[2];
   p.dqs0 = dqs[0], p.dqs1 = dqs[1], p.dqs2 = dqs[2];
@@ -194,7 +202,7 @@ dynconv_status dynconv_delta_bwd(const void* q, const int64_t* qs, const void* k
   p.dvs0 = dvs[0], p.dvs1 = dvs[1], p.dvs2 = dvs[2];
   p.dgs0 = dgs[0], p.dgs1 = dgs[1], p.dgs2 = dgs[2];
   p.dbs0 = dbs[0], p.dbs1 = dbs[1], p.dbs2 = dbs[2];
-  p.vecdo = dv % 8 == 0 && wide(dO, dos, 4, ev, eb);
+  p.vec = p.vec && dv % 8 == 0 && wide(dO, dos, 4, ev, eb);
   if (dstate_out != nullptr) {
     if ((st = check_tensor(dstate_out, dsos, 4, est, 4, true, false)) != DYNCONV_OK) return st;
     p.dstate_out = dstate_out;

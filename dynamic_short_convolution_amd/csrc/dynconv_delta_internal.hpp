@@ -14,6 +14,8 @@ constexpr int kDeltaMaxDk = 128;    // widest key head
 constexpr int kDeltaMaxDv = 65536;  // widest value head
 constexpr int kDeltaCols = 16;      // value columns of one wave
 
+constexpr int kDeltaDots = 5;        // per-token sums of a wave's columns in the backward
+
 // Lower-triangular 64 x 64 matrices keep rows 0..31 in 32 columns and rows 32..63 in 64.
 constexpr int kTrapElems = 32 * 32 + 32 * 64;
 constexpr int kTokArrays = 8;  // per chunk and value head: float[64] each, in this order
@@ -43,8 +45,7 @@ struct DeltaParams {
   int64_t sis0, sis1, sis2, sos0, sos1, sos2, dsos0, dsos1, dsos2, dsis0, dsis1, dsis2;
   int32_t B, T, Hk, Hv, group, dkn, dvn;  // dkn, dvn: key and value head widths
   int32_t nC, nCG;                        // chunks per sequence, 16-column groups of a value head
-  int32_t vec;                            // rows of q and k allow 16-byte loads
-  int32_t vecdo;                          // rows of dO do
+  int32_t vec;                            // rows of q, k (and dO) allow 16-byte loads
   float scale, eps;                       // eps < 0: q and k as they are
   // workspace
   uint16_t* wT;   // [chunk][3][kTrapElems]: (I + A)^-1 in three 8-bit terms
@@ -53,7 +54,7 @@ struct DeltaParams {
   float* wdS;     // the same, gradient of the state after the chunk
   float* wU;      // [chunk][nCG][1024]: u, in fragment order
   float* wR;      // the same, gradient of beta * (v - decayed prediction)
-  float* wDot;    // [chunk][nCG][4][64]: sums over the group's columns
+  float* wDot;    // [chunk][nCG][kDeltaDots][64]: sums over the group's columns
 };
 
 constexpr int delta_dk_pad(int dk) { return dk <= 64 ? 64 : 128; }

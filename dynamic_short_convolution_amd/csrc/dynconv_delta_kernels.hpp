@@ -62,6 +62,11 @@ struct Frag {
   u32x4 t[N];
 };
 
+// Keeps the scheduler from moving anything across: products are written with the next
+// fragments' LDS reads ahead of the current ones' matrix instructions, and left alone the
+// scheduler sinks every read to its use (read, wait 130 cycles, 3 matrix instructions, ...).
+#define DELTA_FENCE() __builtin_amdgcn_sched_barrier(0)
+
 // c += sum over terms (i, j) with i + j <= L of a_i b_j.
 template <int L, int NA, int NB>
 __device__ __forceinline__ void mma(f32x4_t& c, const Frag<NA>& a, const Frag<NB>& b) {
@@ -72,6 +77,21 @@ __device__ __forceinline__ void mma(f32x4_t& c, const Frag<NA>& a, const Frag<NB
       if (i + j <= L)
         c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a.t[i]),
                                                     __builtin_bit_cast(bf16x8_t, b.t[j]), c, 0, 0, 0);
+}
+
+// The same for M tiles with one right operand, tiles innermost (independent accumulators).
+template <int L, int M, int NA, int NB>
+__device__ __forceinline__ void mma_tiles(f32x4_t* c, const Frag<NA>* a, const Frag<NB>& b) {
+#pragma unroll
+  for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = NB - 1; j >= 0; --j)
+      if (i + j <= L) {
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+          c[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a[m].t[i]),
+                                                         __builtin_bit_cast(bf16x8_t, b.t[j]), c[m], 0, 0, 0);
+      }
 }
 
 __device__ __forceinline__ uint32_t top2(float lo, float hi) {  // upper halves of two floats
@@ -98,30 +118,35 @@ __device__ __forceinline__ Frag<N> split8(f32x4_t a, f32x4_t b) {
   return f;
 }
 
-// Left operand of tile row0 .. row0+15 from a row-major LDS matrix: contraction over columns
-// col0 .. col0+31 in fragment order. Planes (terms) lie `plane` elements apart.
+// Row-major LDS matrices keep each 32-column block in fragment order: columns 4q .. 4q+3 at
+// place 8q, columns 16 + 4q .. at place 8q + 4, so a left operand's 8 values are one 16-byte
+// read. Place of column c (the first of 4 when c is a multiple of 4).
+__device__ __forceinline__ constexpr int place(int c) {
+  return (c & ~31) + 2 * (c & 12) + ((c & 16) >> 2) + (c & 3);
+}
+
+// Left operand of tile row0 .. row0+15: contraction over columns col0 .. col0+31. Planes
+// (terms) lie `plane` elements apart.
 template <int N>
 __device__ __forceinline__ Frag<N> rowfrag(const uint16_t* m, int ld, int plane, int row0, int col0) {
   const int lane = threadIdx.x & 63;
-  const uint16_t* p = m + (row0 + (lane & 15)) * ld + col0 + 4 * (lane >> 4);
+  const uint16_t* p = m + (row0 + (lane & 15)) * ld + col0 + 8 * (lane >> 4);
   Frag<N> f;
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const u32x2 a = *reinterpret_cast<const u32x2*>(p + n * plane);
-    const u32x2 b = *reinterpret_cast<const u32x2*>(p + n * plane + 16);
-    f.t[n] = u32x4{a[0], a[1], b[0], b[1]};
-  }
+  for (int n = 0; n < N; ++n) f.t[n] = *reinterpret_cast<const u32x4*>(p + n * plane);
   return f;
 }
 
-// The transposed operand: index col0 + lane % 16, contraction over rows row0 .. row0+31. A
-// 16-lane group's transposing read returns to lane i element i % 4 of what lanes i / 4 + 4e
-// loaded, so lane j loads row 4q + j / 4, columns 4 (j % 4) .. + 3.
-template <int N>
+// The transposed operand: index col0 + lane % 16 (col0 a multiple of 16), contraction over rows
+// row0 .. row0+31. A 16-lane group's transposing read returns to lane i element i % 4 of what
+// lanes i / 4 + 4e loaded, so lane j loads row 4q + j / 4, columns 4 (j % 4) .. + 3 of the
+// tile. PLAIN: the matrix' columns are in their own order.
+template <int N, bool PLAIN = false>
 __device__ __forceinline__ Frag<N> colfrag(const uint16_t* m, int ld, int plane, int row0, int col0) {
   const int lane = threadIdx.x & 63;
   const int q = lane >> 4, j = lane & 15;
-  const uint16_t* p = m + (row0 + 4 * q + (j >> 2)) * ld + col0 + 4 * (j & 3);
+  const int c = PLAIN ? col0 + 4 * (j & 3) : place(col0) + 8 * (j & 3);
+  const uint16_t* p = m + (row0 + 4 * q + (j >> 2)) * ld + c;
   Frag<N> f;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
@@ -131,6 +156,63 @@ __device__ __forceinline__ Frag<N> colfrag(const uint16_t* m, int ld, int plane,
     f.t[n] = u32x4{ua[0], ua[1], ub[0], ub[1]};
   }
   return f;
+}
+
+// acc[m] += rows 16m .. 16m+15 of a [64][32 KB] matrix times b, m = 0..3. `f` holds the
+// fragments of block 0; those of block kb + 1 are read while block kb's products run, and
+// `next` issues the following product's reads before the last ones.
+template <int L, int KB, int NA, int NB, typename Next>
+__device__ __forceinline__ void row_product(f32x4_t* acc, Frag<NA>* f, const uint16_t* m, int ld, int plane,
+                                            const Frag<NB>* b, Next next) {
+  Frag<NA> g[2][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) g[0][i] = f[i];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    if (kb + 1 < KB) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[(kb + 1) & 1][i] = rowfrag<NA>(m, ld, plane, 16 * i, 32 * (kb + 1));
+    } else {
+      next();
+    }
+    DELTA_FENCE();
+    mma_tiles<L, 4>(acc, g[kb & 1], b[kb]);
+    DELTA_FENCE();
+  }
+}
+template <int NA>
+__device__ __forceinline__ void row_load(Frag<NA>* f, const uint16_t* m, int ld, int plane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = rowfrag<NA>(m, ld, plane, 16 * i, 0);
+}
+
+// acc[i] += transposed rows of a [64][16 N] matrix times b: acc[i] takes columns 16i .. 16i+15,
+// contraction over the 64 rows. Two column tiles at a time, the next two's reads ahead.
+template <int NA>
+__device__ __forceinline__ void col_load(Frag<NA>* f, const uint16_t* m, int ld, int plane, int i0) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) f[2 * kb + i] = colfrag<NA>(m, ld, plane, 32 * kb, 16 * (i0 + i));
+}
+template <int L, int N, int NA, int NB, typename Next>
+__device__ __forceinline__ void col_product(f32x4_t* acc, Frag<NA>* f, const uint16_t* m, int ld, int plane,
+                                            const Frag<NB>* b, Next next) {
+  Frag<NA> g[2][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) g[0][i] = f[i];
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    if (i + 2 < N) {
+      col_load<NA>(g[(i / 2 + 1) & 1], m, ld, plane, i + 2);
+    } else {
+      next();
+    }
+    DELTA_FENCE();
+    mma_tiles<L, 2>(acc + i, g[(i / 2) & 1], b[0]);
+    mma_tiles<L, 2>(acc + i, g[(i / 2) & 1] + 2, b[1]);
+    DELTA_FENCE();
+  }
 }
 
 // LDS image of a lower-triangular matrix: rows 0..31 of 40 elements (32 used), rows 32..63 of 72.
@@ -152,6 +234,45 @@ __device__ __forceinline__ constexpr int utrap_off(int i, int j) {
 template <int N>
 __device__ __forceinline__ Frag<N> utrap_row(const uint16_t* m, int tile, int kb) {  // kb >= tile / 2
   return tile < 2 ? rowfrag<N>(m, 72, kTrapLds, 16 * tile, 32 * kb) : rowfrag<N>(m + 2304, 40, kTrapLds, 16 * tile - 32, 0);
+}
+
+// Triangular products over the 64-row contraction, fragments of both blocks at once.
+template <int N>
+struct Trap {
+  Frag<N> a[4], b[2];  // block 0 (or the block that all 4 tiles have), and the other two tiles'
+};
+// lower: tiles 0..3 of block 0, tiles 2, 3 of block 1
+template <int N>
+__device__ __forceinline__ void trap_load(Trap<N>& t, const uint16_t* m) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t.a[i] = trap_row<N>(m, i, 0);
+  t.b[0] = trap_row<N>(m, 2, 1);
+  t.b[1] = trap_row<N>(m, 3, 1);
+}
+template <int L, int N, int NB>
+__device__ __forceinline__ void trap_product(f32x4_t* acc, const Trap<N>& t, const Frag<NB>* x) {
+  mma_tiles<L, 4>(acc, t.a, x[0]);
+  mma_tiles<L, 2>(acc + 2, t.b, x[1]);
+}
+// upper (a transposed lower one, or an upper image): tiles 0..3 of block 1, tiles 0, 1 of block 0
+template <int N>
+__device__ __forceinline__ void trap_load_t(Trap<N>& t, const uint16_t* m) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t.a[i] = trap_col<N>(m, i, 1);
+  t.b[0] = trap_col<N>(m, 0, 0);
+  t.b[1] = trap_col<N>(m, 1, 0);
+}
+template <int N>
+__device__ __forceinline__ void utrap_load(Trap<N>& t, const uint16_t* m) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t.a[i] = utrap_row<N>(m, i, 1);
+  t.b[0] = utrap_row<N>(m, 0, 0);
+  t.b[1] = utrap_row<N>(m, 1, 0);
+}
+template <int L, int N, int NB>
+__device__ __forceinline__ void utrap_product(f32x4_t* acc, const Trap<N>& t, const Frag<NB>* x) {
+  mma_tiles<L, 4>(acc, t.a, x[1]);
+  mma_tiles<L, 2>(acc, t.b, x[0]);
 }
 
 // Writes 4 consecutive elements' N terms.
@@ -184,37 +305,57 @@ __device__ __forceinline__ void stf(void* p, int64_t i, float v) {
   }
 }
 
-// 8 consecutive stored elements of a row, as loaded; elements from `n` on read as zero. Every
-// load is issued whatever n is, from a clamped address (`off` is of an existing element, of
-// whose row `n0` follow): a branch around a load would make each wait for the one before.
+// Global rows of a chunk go through buffer instructions: a uniform descriptor per chunk and
+// 32-bit byte offsets (the ABI bounds token strides so that 64 rows stay below 2^31 bytes).
+// Rows and columns that do not exist get the offset kNowhere: such loads return 0 and such
+// stores are dropped, without a branch (a branch around a load makes each wait for the one
+// before).
+constexpr uint32_t kNowhere = 0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rsrc(const void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, int(kNowhere), 0x00027000);
+}
+template <typename ET>
+__device__ __forceinline__ float buf_ld(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  if constexpr (sizeof(ET) == 2) {
+    return Cvt<ET>::of_bits(uint16_t(__builtin_amdgcn_raw_buffer_load_b16(r, int(off), 0, 0)));
+  } else {
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, int(off), 0, 0));
+  }
+}
+template <typename ET>
+__device__ __forceinline__ void buf_st(__amdgpu_buffer_rsrc_t r, uint32_t off, float v) {
+  if constexpr (sizeof(ET) == 2) {
+    __builtin_amdgcn_raw_buffer_store_b16(Cvt<ET>::bits(v), r, int(off), 0, 0);
+  } else {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, int(off), 0, 0);
+  }
+}
+
+// 8 consecutive stored elements of a row, as loaded; elements from `n` on read as zero (VEC: n
+// is at least 8 or at most 0).
 template <typename ET>
 struct Raw8 {
   u32x4 w[sizeof(ET) / 2];
 };
 template <typename ET, bool VEC>
-__device__ __forceinline__ Raw8<ET> load8(const void* base, int64_t off, int n, int n0) {
+__device__ __forceinline__ Raw8<ET> load8(__amdgpu_buffer_rsrc_t rs, uint32_t off, int n) {
   Raw8<ET> r;
-  if constexpr (VEC) {  // n is 8 or at most 0
-    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const ET*>(base) + off);
+  if constexpr (VEC) {
+    const uint32_t o = n > 0 ? off : kNowhere;
 #pragma unroll
-    for (int i = 0; i < int(sizeof(ET) / 2); ++i) r.w[i] = p[i];
-    if (n <= 0) {
-#pragma unroll
-      for (int i = 0; i < int(sizeof(ET) / 2); ++i) r.w[i] = u32x4{0u, 0u, 0u, 0u};
-    }
+    for (int i = 0; i < int(sizeof(ET) / 2); ++i)
+      r.w[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, int(o), 16 * i, 0);
   } else {
     uint32_t e[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t at = off + min(i, n0 - 1);
+      const uint32_t o = i < n ? off + i * uint32_t(sizeof(ET)) : kNowhere;
       if constexpr (sizeof(ET) == 2) {
-        e[i] = static_cast<const uint16_t*>(base)[at];
+        e[i] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(rs, int(o), 0, 0));
       } else {
-        e[i] = static_cast<const uint32_t*>(base)[at];
+        e[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, int(o), 0, 0);
       }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = i < n ? e[i] : 0u;
     if constexpr (sizeof(ET) == 2) {
       r.w[0] = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
     } else {
@@ -254,17 +395,17 @@ struct Tile {
   static constexpr int LD = DK + 8, PLANE = C * LD, N = C * DK / 8 / NTHR;
   static_assert(C * DK / 8 % NTHR == 0, "whole passes");
   Raw8<ET> r[N];
-  // `base`: the sequence's and head's first element; rows s1 apart; `rows` >= 1 valid rows,
-  // `cols` valid columns (a multiple of 8 with VEC).
-  __device__ __forceinline__ void load(const void* base, int64_t s1, int t0, int rows, int cols) {
+  // `base`: the chunk's first element; rows s1 apart; `rows` valid rows, `cols` valid columns
+  // (a multiple of 8 with VEC).
+  __device__ __forceinline__ void load(const ET* base, int64_t s1, int rows, int cols) {
+    const __amdgpu_buffer_rsrc_t rs = chunk_rsrc(base);
+    constexpr int STEP = NTHR / (DK / 8);
+    const int row = int(threadIdx.x) / (DK / 8), col = int(threadIdx.x) % (DK / 8) * 8;
+    const uint32_t pitch = uint32_t(s1) * uint32_t(sizeof(ET));
+    const uint32_t off = uint32_t(row) * pitch + uint32_t(col) * uint32_t(sizeof(ET));
+    const int n = cols - col;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int idx = int(threadIdx.x) + i * NTHR;
-      const int row = idx / (DK / 8), col = idx % (DK / 8) * 8;
-      const int c = col < cols ? col : 0;
-      const int n = row < rows && col < cols ? cols - col : 0;
-      r[i] = load8<ET, VEC>(base, int64_t(t0 + min(row, rows - 1)) * s1 + c, n, cols - c);
-    }
+    for (int i = 0; i < N; ++i) r[i] = load8<ET, VEC>(rs, off + i * STEP * pitch, row + i * STEP < rows ? n : 0);
   }
   __device__ __forceinline__ void store(uint16_t* m) const {
 #pragma unroll
@@ -272,8 +413,12 @@ struct Tile {
       const int idx = int(threadIdx.x) + i * NTHR;
       const int row = idx / (DK / 8), col = idx % (DK / 8) * 8;
       const Frag<Store<ET>::NT> f = terms8<ET>(r[i]);
+      uint16_t* p = m + row * LD + place(col);  // columns col + 4 .. are 8 places on
 #pragma unroll
-      for (int n = 0; n < Store<ET>::NT; ++n) *reinterpret_cast<u32x4*>(m + n * PLANE + row * LD + col) = f.t[n];
+      for (int n = 0; n < Store<ET>::NT; ++n) {
+        *reinterpret_cast<u32x2*>(p + n * PLANE) = u32x2{f.t[n][0], f.t[n][1]};
+        *reinterpret_cast<u32x2*>(p + n * PLANE + 8) = u32x2{f.t[n][2], f.t[n][3]};
+      }
     }
   }
 };
@@ -312,6 +457,11 @@ __device__ __forceinline__ float gam(float ghi_i, float glo_i, int n_i, float gh
 }
 
 __device__ __forceinline__ f32x4_t ld4(const float* p) { return *reinterpret_cast<const f32x4_t*>(p); }
+// A per-token array's values at this lane's rows 16 mt + 4 q .. + 3.
+__device__ __forceinline__ void tok_load(f32x4_t* x, const float* arr) {
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt) x[mt] = ld4(arr + 16 * mt + 4 * ((threadIdx.x & 63) >> 4));
+}
 __device__ __forceinline__ f32x4_t zero4() { return f32x4_t{0.f, 0.f, 0.f, 0.f}; }
 
 // The 10 tiles on and below the diagonal, in rows.
@@ -358,7 +508,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
   const int t0 = c * C, rows = min(C, p.T - t0);
 
   TK tk;
-  tk.load(static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2, p.ks1, t0, rows, p.dkn);
+  tk.load(static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2 + t0 * p.ks1, p.ks1, rows, p.dkn);
   auto norms = [&](const TK& t, float* out) {
 #pragma unroll
     for (int i = 0; i < TK::N; ++i) {
@@ -377,7 +527,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
   tk.store(sK);
   {
     TK tq;
-    tq.load(static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2, p.qs1, t0, rows, p.dkn);
+    tq.load(static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2 + t0 * p.qs1, p.qs1, rows, p.dkn);
     norms(tq, tok + kTokRq * C);
   }
   if (wave == 0) {
@@ -480,12 +630,11 @@ __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
   uint16_t* wT = p.wT + ci * (3 * kTrapElems);
   for (int e = tid; e < kTrapElems / 8; e += 256) {
     const int row = e < 128 ? e >> 2 : 32 + ((e - 128) >> 3);
-    const int col = e < 128 ? (e & 3) * 8 : (e & 7) * 8;
+    // the 8 values at places 8 k .. of the row, in fragment order; zeros above the diagonal tiles
+    const int k = e < 128 ? e & 3 : (e - 128) & 7, col = 32 * (k >> 2) + 4 * (k & 3);
     f32x4_t x = zero4(), y = zero4();
-    if ((col >> 4) <= (row >> 4)) {
-      x = ld4(sT + row * kInvLd + col);
-      y = ld4(sT + row * kInvLd + col + 4);
-    }
+    if ((col >> 4) <= (row >> 4)) x = ld4(sT + row * kInvLd + col);
+    if ((col >> 4) + 1 <= (row >> 4)) y = ld4(sT + row * kInvLd + col + 16);
     const Frag<3> f = split8<3>(x, y);
 #pragma unroll
     for (int n = 0; n < 3; ++n) reinterpret_cast<u32x4*>(wT + n * kTrapElems)[e] = f.t[n];
@@ -513,24 +662,29 @@ struct ScanLds {
 __device__ __forceinline__ int delta_cols(const DeltaParams& p, int nw) { return (p.nCG + nw - 1) / nw; }
 
 // The 16 values of a wave's column in a chunk: token 16 mt + 4 q + r in v[4 mt + r].
+// `base`: the chunk's first element, `rows` its tokens.
 template <typename ET>
-__device__ __forceinline__ void load_cols(float* v, const void* base, int64_t s1, int t0, int T, int col, bool ok) {
+__device__ __forceinline__ void load_cols(float* v, const ET* base, int64_t s1, int rows, int col, bool ok) {
   const int q = (threadIdx.x & 63) >> 4;
+  const __amdgpu_buffer_rsrc_t rs = chunk_rsrc(base);
+  const uint32_t pitch = uint32_t(s1) * uint32_t(sizeof(ET)), o0 = 4u * q * pitch + uint32_t(col) * uint32_t(sizeof(ET));
+  const int left = ok ? rows - 4 * q : 0;
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
-    const int t = t0 + 16 * (e >> 2) + 4 * q + (e & 3);
-    const float x = ldf<ET>(base, min(t, T - 1) * s1 + (ok ? col : 0));
-    v[e] = ok && t < T ? x : 0.f;
+    const int t = 16 * (e >> 2) + (e & 3);
+    v[e] = buf_ld<ET>(rs, t < left ? o0 + uint32_t(t) * pitch : kNowhere);
   }
 }
 template <typename ET>
-__device__ __forceinline__ void store_cols(const f32x4_t* v, void* base, int64_t s1, int t0, int T, int col, bool ok) {
+__device__ __forceinline__ void store_cols(const f32x4_t* v, ET* base, int64_t s1, int rows, int col, bool ok) {
   const int q = (threadIdx.x & 63) >> 4;
-  if (!ok) return;
+  const __amdgpu_buffer_rsrc_t rs = chunk_rsrc(base);
+  const uint32_t pitch = uint32_t(s1) * uint32_t(sizeof(ET)), o0 = 4u * q * pitch + uint32_t(col) * uint32_t(sizeof(ET));
+  const int left = ok ? rows - 4 * q : 0;
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
-    const int t = t0 + 16 * (e >> 2) + 4 * q + (e & 3);
-    if (t < T) stf<ET>(base, t * s1 + col, v[e >> 2][e & 3]);
+    const int t = 16 * (e >> 2) + (e & 3);
+    buf_st<ET>(rs, t < left ? o0 + uint32_t(t) * pitch : kNowhere, v[e >> 2][e & 3]);
   }
 }
 
@@ -607,24 +761,22 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
     for (int e = tid; e < NP * 128; e += NTHR) {
       const int n = e >> 7, row = (e >> 2) & 31, part = e & 3;
       const int i = row < 16 ? row : row + 16, j = (row < 16 ? 16 : 48) + 4 * part;
-      *reinterpret_cast<u32x2*>(sP + n * kTrapLds + trap_off(i) + j) = u32x2{0u, 0u};
+      *reinterpret_cast<u32x2*>(sP + n * kTrapLds + trap_off(i) + place(j)) = u32x2{0u, 0u};
     }
   }
 
   TK tk, tq;
   TrapTile<NTHR> tt;
   f32x4_t ttok[(kTokArrays * C / 4 + NTHR - 1) / NTHR];
-  float vn[16];
   auto fetch = [&](int c) {
-    const int t0 = c * C, rows = min(C, p.T - t0);
-    tk.load(kbase, p.ks1, t0, rows, p.dkn);
-    if constexpr (!STATES) tq.load(qbase, p.qs1, t0, rows, p.dkn);
+    const int64_t t0 = int64_t(c) * C;
+    const int rows = min(C, p.T - int(t0));
+    tk.load(kbase + t0 * p.ks1, p.ks1, rows, p.dkn);
+    if constexpr (!STATES) tq.load(qbase + t0 * p.qs1, p.qs1, rows, p.dkn);
     tt.load(p.wT + (bh * p.nC + c) * (3 * kTrapElems));
     const f32x4_t* w = reinterpret_cast<const f32x4_t*>(p.wTok + (bh * p.nC + c) * (kTokArrays * C));
 #pragma unroll
-    for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i)
-      ttok[i] = w[min(tid + i * NTHR, kTokArrays * C / 4 - 1)];
-    load_cols<ET>(vn, vbase, p.vs1, t0, p.T, col, ok);
+    for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i) ttok[i] = w[min(tid + i * NTHR, kTokArrays * C / 4 - 1)];
   };
   if (p.nC > 0) fetch(0);
   for (int c = 0; c < p.nC; ++c) {
@@ -636,101 +788,113 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
     for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i)
       if (tid + i * NTHR < kTokArrays * C / 4) reinterpret_cast<f32x4_t*>(tok)[tid + i * NTHR] = ttok[i];
     float v[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = vn[e];
+    {
+      const int64_t t0 = int64_t(c) * C;
+      load_cols<ET>(v, vbase + t0 * p.vs1, p.vs1, min(C, p.T - int(t0)), col, ok);
+    }
     __syncthreads();
-    if (c + 1 < p.nC) fetch(c + 1);
 
     if constexpr (!STATES) {
       // P = scale Gam o Q K^T: tiles transposed (rows j, column i), so a lane holds four
       // neighbours of one row of P
-      for (int t = wave; t < 10; t += NW) {
-        int ti, tj;
-        tile_of(t, ti, tj);
-        f32x4_t acc = zero4();
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-          mma<NP - 1>(acc, rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb),
-                      rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb));
-        const int i = 16 * ti + n16, j0 = 16 * tj + 4 * q;
-        const float gh = tok[kTokGhi * C + i], gl = tok[kTokGlo * C + i], rqi = tok[kTokRq * C + i] * p.scale;
-        const int ni = __float_as_int(tok[kTokN * C + i]);
-        const f32x4_t ghj = ld4(tok + kTokGhi * C + j0), glj = ld4(tok + kTokGlo * C + j0);
-        const f32x4_t nj = ld4(tok + kTokN * C + j0), rkj = ld4(tok + kTokRk * C + j0);
-        f32x4_t x;
+      for (int s = 0; s < (10 + NW - 1) / NW; ++s) {
+        const int t = wave + s * NW;
+        if (t < 10) {
+          int ti, tj;
+          tile_of(t, ti, tj);
+          Frag<NT> fj[KB], fi[KB];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          x[r] = j0 + r <= i ? acc[r] * rqi * rkj[r] * gam(gh, gl, ni, ghj[r], glj[r], __float_as_int(nj[r])) : 0.f;
-        put4<NP>(sP + trap_off(i) + j0, kTrapLds, x);
+          for (int kb = 0; kb < KB; ++kb) {
+            fj[kb] = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb);
+            fi[kb] = rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb);
+          }
+          const int i = 16 * ti + n16, j0 = 16 * tj + 4 * q;
+          const float gh = tok[kTokGhi * C + i], gl = tok[kTokGlo * C + i], rqi = tok[kTokRq * C + i] * p.scale;
+          const int ni = __float_as_int(tok[kTokN * C + i]);
+          const f32x4_t ghj = ld4(tok + kTokGhi * C + j0), glj = ld4(tok + kTokGlo * C + j0);
+          const f32x4_t nj = ld4(tok + kTokN * C + j0), rkj = ld4(tok + kTokRk * C + j0);
+          DELTA_FENCE();
+          f32x4_t acc[2] = {zero4(), zero4()};
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) mma<NP - 1>(acc[kb & 1], fj[kb], fi[kb]);
+          f32x4_t x;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            x[r] = j0 + r <= i ? (acc[0][r] + acc[1][r]) * rqi * rkj[r] *
+                                     gam(gh, gl, ni, ghj[r], glj[r], __float_as_int(nj[r]))
+                               : 0.f;
+          put4<NP>(sP + trap_off(i) + place(j0), kTrapLds, x);
+        }
       }
     } else if (cg < p.nCG) {
       store_image<DK / 16>(S, p.wS + ((bh * p.nC + c) * p.nCG + cg) * (DK * 16));
     }
 
-    Frag<3> sf[KB];
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(S[2 * kb], S[2 * kb + 1]);
-    f32x4_t z[4];  // beta (v - E K S0)
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      f32x4_t acc = zero4();
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) mma<2>(acc, rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * mt, 32 * kb), sf[kb]);
-      const int t = 16 * mt + 4 * q;
-      const f32x4_t e = ld4(tok + kTokE * C + t), rk = ld4(tok + kTokRk * C + t), be = ld4(tok + kTokBeta * C + t);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) z[mt][r] = be[r] * (v[4 * mt + r] - e[r] * rk[r] * acc[r]);
-    }
-    f32x4_t u[4];
+    f32x4_t z[4] = {zero4(), zero4(), zero4(), zero4()};  // beta (v - E K S0)
+    f32x4_t o[4] = {zero4(), zero4(), zero4(), zero4()};  // scale E (Q S0), then all of the output
     {
-      const Frag<3> zf[2] = {split8<3>(z[0], z[1]), split8<3>(z[2], z[3])};
+      Frag<NT> fk[4];
+      f32x4_t te[4], tr[4], tb[4];
+      row_load<NT>(fk, sK, TK::LD, TK::PLANE);
+      Frag<3> sf[KB];
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        u[mt] = zero4();
-#pragma unroll
-        for (int kb = 0; kb <= mt / 2; ++kb) mma<2>(u[mt], trap_row<3>(sT, mt, kb), zf[kb]);
-      }
-    }
-    f32x4_t o[4];
-    if constexpr (!STATES) {
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        o[mt] = zero4();
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) mma<NP - 1>(o[mt], rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * mt, 32 * kb), sf[kb]);
-        const int t = 16 * mt + 4 * q;
-        const f32x4_t e = ld4(tok + kTokE * C + t), rq = ld4(tok + kTokRq * C + t);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[mt][r] *= e[r] * rq[r] * p.scale;
-      }
-    }
-    {
-      f32x4_t d[4];
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        const int t = 16 * mt + 4 * q;
-        const f32x4_t dd = ld4(tok + kTokD * C + t), rk = ld4(tok + kTokRk * C + t);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) d[mt][r] = u[mt][r] * dd[r] * rk[r];
-      }
-      const Frag<3> df[2] = {split8<3>(d[0], d[1]), split8<3>(d[2], d[3])};
-      const float gamma = tok[kTokE * C + C - 1];
-#pragma unroll
-      for (int i = 0; i < DK / 16; ++i) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) S[i][r] *= gamma;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) mma<2>(S[i], colfrag<NT>(sK, TK::LD, TK::PLANE, 32 * kb, 16 * i), df[kb]);
-      }
-    }
-    if constexpr (!STATES) {
-      __syncthreads();  // P is complete
-      const Frag<NP> uf[2] = {split8<NP>(u[0], u[1]), split8<NP>(u[2], u[3])};
+      for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(S[2 * kb], S[2 * kb + 1]);
+      row_product<2, KB>(z, fk, sK, TK::LD, TK::PLANE, sf, [&] {
+        if constexpr (!STATES) row_load<NT>(fk, sQ, TK::LD, TK::PLANE);
+        tok_load(te, tok + kTokE * C);
+        tok_load(tr, tok + kTokRk * C);
+        tok_load(tb, tok + kTokBeta * C);
+      });
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-        for (int kb = 0; kb <= mt / 2; ++kb) mma<NP - 1>(o[mt], trap_row<NP>(sP, mt, kb), uf[kb]);
-      store_cols<ET>(o, obase, p.os1, c * C, p.T, col, ok);
+        for (int r = 0; r < 4; ++r) z[mt][r] = tb[mt][r] * (v[4 * mt + r] - te[mt][r] * tr[mt][r] * z[mt][r]);
+      if constexpr (!STATES) {
+        Frag<NP> so[KB];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int n = 0; n < NP; ++n) so[kb].t[n] = sf[kb].t[n];
+        row_product<NP - 1, KB>(o, fk, sQ, TK::LD, TK::PLANE, so, [&] { tok_load(tr, tok + kTokRq * C); });
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) o[mt] *= te[mt] * tr[mt] * p.scale;
+      }
+    }
+    f32x4_t u[4] = {zero4(), zero4(), zero4(), zero4()};
+    const float gamma = tok[kTokE * C + C - 1];
+    f32x4_t td[4], trk[4];
+    {
+      Trap<3> ft;
+      trap_load(ft, sT);
+      const Frag<3> zf[2] = {split8<3>(z[0], z[1]), split8<3>(z[2], z[3])};
+      tok_load(td, tok + kTokD * C);
+      tok_load(trk, tok + kTokRk * C);
+      DELTA_FENCE();
+      trap_product<2>(u, ft, zf);
+      DELTA_FENCE();
+    }
+    if (c + 1 < p.nC) fetch(c + 1);
+    {
+      Frag<NT> fc[4];
+      col_load<NT>(fc, sK, TK::LD, TK::PLANE, 0);
+      f32x4_t d[4];
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) d[mt] = u[mt] * td[mt] * trk[mt];
+      const Frag<3> df[2] = {split8<3>(d[0], d[1]), split8<3>(d[2], d[3])};
+#pragma unroll
+      for (int i = 0; i < DK / 16; ++i) S[i] *= gamma;
+      col_product<2, DK / 16>(S, fc, sK, TK::LD, TK::PLANE, df, [] {});
+    }
+    if constexpr (!STATES) {
+      const Frag<NP> uf[2] = {split8<NP>(u[0], u[1]), split8<NP>(u[2], u[3])};
+      __syncthreads();  // P is complete
+      Trap<NP> fp;
+      trap_load(fp, sP);
+      DELTA_FENCE();
+      trap_product<NP - 1>(o, fp, uf);
+      const int64_t t0 = int64_t(c) * C;
+      store_cols<ET>(o, obase + t0 * p.os1, p.os1, min(C, p.T - int(t0)), col, ok);
     }
   }
   if constexpr (!STATES)
@@ -748,7 +912,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
 // Z = V - E (K S0) and U = T (beta Z). What contracts over value columns (dq, dk, the pair
 // terms of dg and dbeta) is left to k_delta_grad, which gets U, dR and dS1 from here and the
 // sums over a wave's columns of
-//   into_i = dO_i.(scale E Q S0)_i - dZ_i.(E K S0)_i,  out_j = U_j.(D K dS1)_j,  dR_i.Z_i
+//   dO_i.(scale E Q S0)_i,  out_j = U_j.(D K dS1)_j,  dR_i.Z_i,  dZ_i.(E K S0)_i
 // and gamma <S0, dS1>.
 
 template <typename ET, int DK>
@@ -806,23 +970,21 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_back(const DeltaParams p) 
   for (int e = tid; e < 3 * 128; e += NTHR) {
     const int n = e >> 7, row = (e >> 2) & 31, part = e & 3;
     const int i = row < 16 ? row + 16 : row + 32, j = (row < 16 ? 0 : 32) + 4 * part;
-    *reinterpret_cast<u32x2*>(sP + n * kTrapLds + utrap_off(i, j)) = u32x2{0u, 0u};
+    *reinterpret_cast<u32x2*>(sP + n * kTrapLds + utrap_off(i, place(j))) = u32x2{0u, 0u};
   }
 
   TK tk, tq;
   TrapTile<NTHR> tt;
   f32x4_t ttok[(kTokArrays * C / 4 + NTHR - 1) / NTHR];
-  float vn[16], don[16];
   auto fetch = [&](int c) {
-    const int t0 = c * C, rows = min(C, p.T - t0);
-    tk.load(kbase, p.ks1, t0, rows, p.dkn);
-    tq.load(qbase, p.qs1, t0, rows, p.dkn);
+    const int64_t t0 = int64_t(c) * C;
+    const int rows = min(C, p.T - int(t0));
+    tk.load(kbase + t0 * p.ks1, p.ks1, rows, p.dkn);
+    tq.load(qbase + t0 * p.qs1, p.qs1, rows, p.dkn);
     tt.load(p.wT + (bh * p.nC + c) * (3 * kTrapElems));
     const f32x4_t* w = reinterpret_cast<const f32x4_t*>(p.wTok + (bh * p.nC + c) * (kTokArrays * C));
 #pragma unroll
     for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i) ttok[i] = w[min(tid + i * NTHR, kTokArrays * C / 4 - 1)];
-    load_cols<ET>(vn, vbase, p.vs1, t0, p.T, col, ok);
-    load_cols<ET>(don, dobase, p.dos1, t0, p.T, col, ok);
   };
   fetch(p.nC - 1);
   for (int c = p.nC - 1; c >= 0; --c) {
@@ -835,136 +997,57 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_back(const DeltaParams p) 
 #pragma unroll
     for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i)
       if (tid + i * NTHR < kTokArrays * C / 4) reinterpret_cast<f32x4_t*>(tok)[tid + i * NTHR] = ttok[i];
-    f32x4_t v[4], dO[4], S0[DK / 16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      v[e >> 2][e & 3] = vn[e];
-      dO[e >> 2][e & 3] = don[e];
-    }
+    f32x4_t S0[DK / 16];
     load_image<DK / 16>(S0, p.wS + cim * (DK * 16));
+    float v[16], dO[16];
+    const int64_t t0 = int64_t(c) * C;
+    const int rows = min(C, p.T - int(t0));
+    load_cols<ET>(v, vbase + t0 * p.vs1, p.vs1, rows, col, ok);
+    load_cols<ET>(dO, dobase + t0 * p.dos1, p.dos1, rows, col, ok);
     __syncthreads();
-    if (c > 0) fetch(c - 1);
 
     // P^T: tiles of P = scale Gam o Q K^T (rows i, column j), four neighbours of a row of P^T
-    for (int t = wave; t < 10; t += NW) {
-      int ti, tj;
-      tile_of(t, ti, tj);
-      f32x4_t acc = zero4();
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-        mma<2>(acc, rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb),
-               rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb));
-      const int j = 16 * tj + n16, i0 = 16 * ti + 4 * q;
-      const float gh = tok[kTokGhi * C + j], gl = tok[kTokGlo * C + j], rkj = tok[kTokRk * C + j] * p.scale;
-      const int nj = __float_as_int(tok[kTokN * C + j]);
-      const f32x4_t ghi = ld4(tok + kTokGhi * C + i0), gli = ld4(tok + kTokGlo * C + i0);
-      const f32x4_t ni = ld4(tok + kTokN * C + i0), rqi = ld4(tok + kTokRq * C + i0);
-      f32x4_t x;
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        x[r] = j <= i0 + r ? acc[r] * rkj * rqi[r] * gam(ghi[r], gli[r], __float_as_int(ni[r]), gh, gl, nj) : 0.f;
-      put4<3>(sP + utrap_off(j, i0), kTrapLds, x);
-    }
-
-    if (live) store_image<DK / 16>(dS, p.wdS + cim * (DK * 16));
-    f32x4_t KdS[4];  // D (K dS1)
-    {
-      Frag<3> sf[KB];
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(dS[2 * kb], dS[2 * kb + 1]);
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        f32x4_t acc = zero4();
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) mma<2>(acc, rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * mt, 32 * kb), sf[kb]);
-        const int t = 16 * mt + 4 * q;
-        const f32x4_t d = ld4(tok + kTokD * C + t), rk = ld4(tok + kTokRk * C + t);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) KdS[mt][r] = acc[r] * d[r] * rk[r];
-      }
-    }
-    f32x4_t KS[4], QS[4];  // E (K S0), scale E (Q S0)
-    {
-      Frag<3> sf[KB];
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(S0[2 * kb], S0[2 * kb + 1]);
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        f32x4_t a = zero4(), o = zero4();
+    for (int s = 0; s < (10 + NW - 1) / NW; ++s) {
+      const int t = wave + s * NW;
+      if (t < 10) {
+        int ti, tj;
+        tile_of(t, ti, tj);
+        Frag<NT> fj[KB], fi[KB];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-          mma<2>(a, rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * mt, 32 * kb), sf[kb]);
-          mma<2>(o, rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * mt, 32 * kb), sf[kb]);
+          fi[kb] = rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb);
+          fj[kb] = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb);
         }
-        const int t = 16 * mt + 4 * q;
-        const f32x4_t e = ld4(tok + kTokE * C + t), rk = ld4(tok + kTokRk * C + t), rq = ld4(tok + kTokRq * C + t);
+        const int j = 16 * tj + n16, i0 = 16 * ti + 4 * q;
+        const float gh = tok[kTokGhi * C + j], gl = tok[kTokGlo * C + j], rkj = tok[kTokRk * C + j] * p.scale;
+        const int nj = __float_as_int(tok[kTokN * C + j]);
+        const f32x4_t ghi = ld4(tok + kTokGhi * C + i0), gli = ld4(tok + kTokGlo * C + i0);
+        const f32x4_t ni = ld4(tok + kTokN * C + i0), rqi = ld4(tok + kTokRq * C + i0);
+        DELTA_FENCE();
+        f32x4_t acc[2] = {zero4(), zero4()};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          KS[mt][r] = a[r] * e[r] * rk[r];
-          QS[mt][r] = o[r] * e[r] * rq[r] * p.scale;
-        }
+        for (int kb = 0; kb < KB; ++kb) mma<2>(acc[kb & 1], fi[kb], fj[kb]);
+        f32x4_t x;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          x[r] = j <= i0 + r ? (acc[0][r] + acc[1][r]) * rkj * rqi[r] *
+                                   gam(ghi[r], gli[r], __float_as_int(ni[r]), gh, gl, nj)
+                             : 0.f;
+        put4<3>(sP + utrap_off(j, place(i0)), kTrapLds, x);
       }
     }
-    f32x4_t z[4], u[4];
-    {
-      f32x4_t bz[4];
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        z[mt] = v[mt] - KS[mt];
-        bz[mt] = z[mt] * ld4(tok + kTokBeta * C + 16 * mt + 4 * q);
-      }
-      const Frag<3> zf[2] = {split8<3>(bz[0], bz[1]), split8<3>(bz[2], bz[3])};
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        u[mt] = zero4();
-#pragma unroll
-        for (int kb = 0; kb <= mt / 2; ++kb) mma<2>(u[mt], trap_row<3>(sT, mt, kb), zf[kb]);
-      }
-    }
-    if (live) store_image<4>(u, p.wU + cim * (C * kDeltaCols));
-    __syncthreads();  // P^T is complete
-    f32x4_t dR[4];
-    {
-      f32x4_t dU[4];
-      const Frag<NT> of[2] = {split8<NT>(dO[0], dO[1]), split8<NT>(dO[2], dO[3])};
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        dU[mt] = KdS[mt];
-#pragma unroll
-        for (int kb = mt / 2; kb < 2; ++kb) mma<2>(dU[mt], utrap_row<3>(sP, mt, kb), of[kb]);
-      }
-      const Frag<3> uf[2] = {split8<3>(dU[0], dU[1]), split8<3>(dU[2], dU[3])};
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        dR[mt] = zero4();
-#pragma unroll
-        for (int kb = mt / 2; kb < 2; ++kb) mma<2>(dR[mt], trap_col<3>(sT, mt, kb), uf[kb]);
-      }
-    }
-    if (live) store_image<4>(dR, p.wR + cim * (C * kDeltaCols));
-    f32x4_t dz[4];
-    float* dot = p.wDot + cim * (4 * C);
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      const int t = 16 * mt + 4 * q;
-      dz[mt] = dR[mt] * ld4(tok + kTokBeta * C + t);
-      f32x4_t into, out, rz;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        into[r] = sum16(dO[mt][r] * QS[mt][r] - dz[mt][r] * KS[mt][r]);
-        out[r] = sum16(KdS[mt][r] * u[mt][r]);
-        rz[r] = sum16(dR[mt][r] * z[mt][r]);
-      }
-      if (live && n16 == 0) {
-        *reinterpret_cast<f32x4_t*>(dot + t) = into;
-        *reinterpret_cast<f32x4_t*>(dot + C + t) = out;
-        *reinterpret_cast<f32x4_t*>(dot + 2 * C + t) = rz;
-      }
-    }
-    store_cols<ET>(dz, dvbase, p.dvs1, c * C, p.T, col, ok);
+
     const float gamma = tok[kTokE * C + C - 1];
+    float* dot = p.wDot + cim * (kDeltaDots * C);
+    f32x4_t KdS[4] = {zero4(), zero4(), zero4(), zero4()};  // D (K dS1)
+    f32x4_t KS[4] = {zero4(), zero4(), zero4(), zero4()};   // E (K S0)
+    f32x4_t ta[4], tb[4];  // token factors, read anew where they are used: registers are scarce here
     {
-      float h = 0.f;
+      Frag<NT> fk[4];
+      row_load<NT>(fk, sK, TK::LD, TK::PLANE);
+      if (live) store_image<DK / 16>(dS, p.wdS + cim * (DK * 16));
+      float h = 0.f;  // <S0, dS1>
 #pragma unroll
       for (int i = 0; i < DK / 16; ++i)
 #pragma unroll
@@ -972,31 +1055,112 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_back(const DeltaParams p) 
       h = sum16(h);
       h += __shfl_xor(h, 16);
       h += __shfl_xor(h, 32);
-      if (live && lane == 0) dot[3 * C] = gamma * h;
-    }
-    {
-      f32x4_t eo[4], er[4];
+      if (live && lane == 0) dot[4 * C] = gamma * h;
+      Frag<3> sf[KB];
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(dS[2 * kb], dS[2 * kb + 1]);
+      row_product<2, KB>(KdS, fk, sK, TK::LD, TK::PLANE, sf, [&] {
+        row_load<NT>(fk, sK, TK::LD, TK::PLANE);
+        tok_load(ta, tok + kTokD * C);
+        tok_load(tb, tok + kTokRk * C);
+      });
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) KdS[mt] *= ta[mt] * tb[mt];
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(S0[2 * kb], S0[2 * kb + 1]);
+      row_product<2, KB>(KS, fk, sK, TK::LD, TK::PLANE, sf, [&] {
+        row_load<NT>(fk, sQ, TK::LD, TK::PLANE);
+        tok_load(ta, tok + kTokE * C);
+      });
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) KS[mt] *= ta[mt] * tb[mt];
+      f32x4_t QS[4] = {zero4(), zero4(), zero4(), zero4()};
+      row_product<2, KB>(QS, fk, sQ, TK::LD, TK::PLANE, sf, [&] { tok_load(tb, tok + kTokRq * C); });
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
-        const int t = 16 * mt + 4 * q;
-        const f32x4_t e = ld4(tok + kTokE * C + t), rk = ld4(tok + kTokRk * C + t), rq = ld4(tok + kTokRq * C + t);
+        f32x4_t x;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = sum16(dO[4 * mt + r] * (QS[mt][r] * ta[mt][r] * tb[mt][r] * p.scale));
+        if (live && n16 == 0) *reinterpret_cast<f32x4_t*>(dot + 16 * mt + 4 * q) = x;
+      }
+    }
+    f32x4_t z[4];
+    {
+      f32x4_t u[4] = {zero4(), zero4(), zero4(), zero4()};
+      Trap<3> ft;
+      tok_load(tb, tok + kTokBeta * C);
+      trap_load(ft, sT);
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z[mt][r] = v[4 * mt + r] - KS[mt][r];
+      const Frag<3> zf[2] = {split8<3>(z[0] * tb[0], z[1] * tb[1]), split8<3>(z[2] * tb[2], z[3] * tb[3])};
+      DELTA_FENCE();
+      trap_product<2>(u, ft, zf);
+      if (live) store_image<4>(u, p.wU + cim * (C * kDeltaCols));
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        f32x4_t x;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = sum16(KdS[mt][r] * u[mt][r]);
+        if (live && n16 == 0) *reinterpret_cast<f32x4_t*>(dot + C + 16 * mt + 4 * q) = x;
+      }
+    }
+    __syncthreads();  // P^T is complete
+    f32x4_t dR[4] = {zero4(), zero4(), zero4(), zero4()};
+    {
+      Trap<3> ft;
+      utrap_load(ft, sP);
+      const Frag<NT> of[2] = {split8<NT>(f32x4_t{dO[0], dO[1], dO[2], dO[3]}, f32x4_t{dO[4], dO[5], dO[6], dO[7]}),
+                              split8<NT>(f32x4_t{dO[8], dO[9], dO[10], dO[11]}, f32x4_t{dO[12], dO[13], dO[14], dO[15]})};
+      DELTA_FENCE();
+      utrap_product<2>(KdS, ft, of);  // dU
+      DELTA_FENCE();
+      trap_load_t(ft, sT);
+      const Frag<3> uf[2] = {split8<3>(KdS[0], KdS[1]), split8<3>(KdS[2], KdS[3])};
+      DELTA_FENCE();
+      utrap_product<2>(dR, ft, uf);
+      tok_load(ta, tok + kTokE * C);
+      tok_load(tb, tok + kTokBeta * C);
+      DELTA_FENCE();
+    }
+    if (live) store_image<4>(dR, p.wR + cim * (C * kDeltaCols));
+    if (c > 0) fetch(c - 1);
+    {
+      Frag<NT> fc[4];
+      col_load<NT>(fc, sK, TK::LD, TK::PLANE, 0);
+      f32x4_t dz[4], tc[4];
+      tok_load(tc, tok + kTokRk * C);
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        f32x4_t x, y;
+        dz[mt] = dR[mt] * tb[mt];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          eo[mt][r] = dO[mt][r] * e[r] * rq[r] * p.scale;
-          er[mt][r] = -(dz[mt][r] * e[r] * rk[r]);
+          x[r] = sum16(dR[mt][r] * z[mt][r]);
+          y[r] = sum16(dz[mt][r] * KS[mt][r]);
+        }
+        if (live && n16 == 0) {
+          *reinterpret_cast<f32x4_t*>(dot + 2 * C + 16 * mt + 4 * q) = x;
+          *reinterpret_cast<f32x4_t*>(dot + 3 * C + 16 * mt + 4 * q) = y;
         }
       }
-      const Frag<3> of[2] = {split8<3>(eo[0], eo[1]), split8<3>(eo[2], eo[3])};
-      const Frag<3> rf[2] = {split8<3>(er[0], er[1]), split8<3>(er[2], er[3])};
+      store_cols<ET>(dz, dvbase + t0 * p.dvs1, p.dvs1, rows, col, ok);
 #pragma unroll
-      for (int i = 0; i < DK / 16; ++i) {
-        dS[i] *= gamma;
+      for (int mt = 0; mt < 4; ++mt) dz[mt] = -(dz[mt] * ta[mt] * tc[mt]);
+      const Frag<3> rf[2] = {split8<3>(dz[0], dz[1]), split8<3>(dz[2], dz[3])};
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          mma<2>(dS[i], colfrag<NT>(sQ, TK::LD, TK::PLANE, 32 * kb, 16 * i), of[kb]);
-          mma<2>(dS[i], colfrag<NT>(sK, TK::LD, TK::PLANE, 32 * kb, 16 * i), rf[kb]);
-        }
-      }
+      for (int i = 0; i < DK / 16; ++i) dS[i] *= gamma;
+      col_product<2, DK / 16>(dS, fc, sK, TK::LD, TK::PLANE, rf, [&] {
+        col_load<NT>(fc, sQ, TK::LD, TK::PLANE, 0);
+        tok_load(tc, tok + kTokRq * C);
+      });
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) dz[mt][r] = dO[4 * mt + r] * (ta[mt][r] * tc[mt][r] * p.scale);
+      const Frag<3> of[2] = {split8<3>(dz[0], dz[1]), split8<3>(dz[2], dz[3])};
+      col_product<2, DK / 16>(dS, fc, sQ, TK::LD, TK::PLANE, of, [] {});
     }
   }
   store_state<DK>(dS, p.dstate == nullptr ? nullptr : p.dstate + b * p.dsis0 + hv * p.dsis1, p.dsis2, p.dkn, col, ok);
@@ -1014,7 +1178,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_back(const DeltaParams p) 
 // are rq dq and rk dk in terms of the normalised rows; the norm's own gradient takes their
 // part along q (k) away: dq = dq' - rq q (rq q.dq'). The decay's gradient adds up all paths
 // that cross a token, dg_t = sum_{i >= t > j} X_ij + sum_{i >= t} into_i + sum_{j < t} out_j
-// + gamma <S0, dS1> with X = Y o Q K^T + Yk o K K^T, from row and column sums of the same
+// + gamma <S0, dS1> with into = dO.(scale E Q S0) - dZ.(E K S0), X = Y o Q K^T + Yk o K K^T, from row and column sums of the same
 // products, so that pairs on one side of t cancel exactly; the cumulative sums are in 64 bits.
 
 template <typename ET, int DK>
@@ -1040,15 +1204,25 @@ struct GradLds {
   static constexpr int BYTES = SUM + 3 * 4 * C * 4;
 };
 
-// Stages rows [16 half .. +15] of a [columns][index] matrix from an image of NB blocks of 32 indices.
-template <int N, int NB>
-__device__ __forceinline__ void stage_image(uint16_t* m, int ld, int plane, const float* src, bool have) {
-  for (int e = threadIdx.x; e < NB * 64 * 2; e += 256) {
-    const int kb = e >> 7, l = (e >> 1) & 63, h = e & 1;
-    const f32x4_t x = have ? reinterpret_cast<const f32x4_t*>(src)[e] : zero4();
-    put4<N>(m + (l & 15) * ld + 32 * kb + 16 * h + 4 * (l >> 4), plane, x);
+// Image of 16 columns (NB blocks of 32 indices) through registers into rows of a
+// [columns][index] LDS matrix of N terms.
+template <int NB>
+struct ImageTile {
+  static constexpr int N = NB * 128 / 256;
+  f32x4_t r[N];
+  __device__ __forceinline__ void load(const float* src) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = reinterpret_cast<const f32x4_t*>(src)[threadIdx.x + 256 * i];
   }
-}
+  template <int NTERM>
+  __device__ __forceinline__ void store(uint16_t* m, int ld, int plane, bool have) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = threadIdx.x + 256 * i, kb = e >> 7, l = (e >> 1) & 63, h = e & 1;
+      put4<NTERM>(m + (l & 15) * ld + 32 * kb + 16 * h + 4 * (l >> 4), plane, have ? r[i] : zero4());
+    }
+  }
+};
 
 template <typename ET, int DK, bool VEC>
 __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
@@ -1085,7 +1259,7 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
   for (int gh = 0; gh < p.group; ++gh) {
     const int hv = hk * p.group + gh;
     const int64_t ci = (int64_t(b) * p.Hv + hv) * p.nC + c;
-    const ET* dobase = static_cast<const ET*>(p.dO) + b * p.dos0 + hv * p.dos2;
+    const ET* dobase = static_cast<const ET*>(p.dO) + b * p.dos0 + hv * p.dos2 + t0 * p.dos1;
     f32x4_t dP[3], F[3];
 #pragma unroll
     for (int s = 0; s < 3; ++s) dP[s] = F[s] = zero4();
@@ -1095,70 +1269,103 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
 #pragma unroll
       for (int n = 0; n < NN; ++n) os[mt][n] = ug[mt][n] = rs[mt][n] = zero4();
 
+    ImageTile<2> iu[2], ir[2];
+    ImageTile<KB> is[2], ig[2];
+    Raw8<ET> io;
+    auto fetch = [&](int cb) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t cim = ci * p.nCG + min(cb + h, p.nCG - 1);
+        iu[h].load(p.wU + cim * (C * kDeltaCols));
+        ir[h].load(p.wR + cim * (C * kDeltaCols));
+        is[h].load(p.wS + cim * (DK * 16));
+        ig[h].load(p.wdS + cim * (DK * 16));
+      }
+      const int row = tid >> 2, c0 = cb * kDeltaCols + (tid & 3) * 8;
+      const __amdgpu_buffer_rsrc_t rs = chunk_rsrc(dobase);
+      const uint32_t off = (uint32_t(row) * uint32_t(p.dos1) + uint32_t(c0)) * uint32_t(sizeof(ET));
+      const int n = row < rows ? p.dvn - c0 : 0;
+      if constexpr (VEC) {
+        io = load8<ET, true>(rs, off, n);
+      } else {
+        io = load8<ET, false>(rs, off, n);
+      }
+    };
+    fetch(0);
     for (int cb = 0; cb < p.nCG; cb += 2) {
       __syncthreads();  // the previous contents are read
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const bool have = cb + h < p.nCG;
-        const int64_t cim = ci * p.nCG + (have ? cb + h : cb);
-        stage_image<3, 2>(sU + 16 * h * L::ULD, L::ULD, L::UPL, p.wU + cim * (C * kDeltaCols), have);
-        stage_image<3, 2>(sR + 16 * h * L::ULD, L::ULD, L::UPL, p.wR + cim * (C * kDeltaCols), have);
-        stage_image<NP, KB>(sS + 16 * h * L::SLD, L::SLD, L::SPL, p.wS + cim * (DK * 16), have);
-        stage_image<NP, KB>(sG + 16 * h * L::SLD, L::SLD, L::SPL, p.wdS + cim * (DK * 16), have);
+        iu[h].template store<3>(sU + 16 * h * L::ULD, L::ULD, L::UPL, have);
+        ir[h].template store<3>(sR + 16 * h * L::ULD, L::ULD, L::UPL, have);
+        is[h].template store<NP>(sS + 16 * h * L::SLD, L::SLD, L::SPL, have);
+        ig[h].template store<NP>(sG + 16 * h * L::SLD, L::SLD, L::SPL, have);
       }
       {
-        const int row = tid >> 2, cc = (tid & 3) * 8, c0 = cb * kDeltaCols + cc;
-        const int cs = c0 < p.dvn ? c0 : 0;
-        const int n = row < rows && c0 < p.dvn ? p.dvn - c0 : 0;
-        const int64_t off = int64_t(t0 + min(row, rows - 1)) * p.dos1 + cs;
-        const Raw8<ET> r = p.vecdo ? load8<ET, true>(dobase, off, n, p.dvn - cs) : load8<ET, false>(dobase, off, n, p.dvn - cs);
-        const Frag<NT> f = terms8<ET>(r);
+        const Frag<NT> f = terms8<ET>(io);
+        uint16_t* o = sO + (tid >> 2) * L::OLD + place((tid & 3) * 8);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) *reinterpret_cast<u32x4*>(sO + i * L::OPL + row * L::OLD + cc) = f.t[i];
+        for (int i = 0; i < NT; ++i) {
+          *reinterpret_cast<u32x2*>(o + i * L::OPL) = u32x2{f.t[i][0], f.t[i][1]};
+          *reinterpret_cast<u32x2*>(o + i * L::OPL + 8) = u32x2{f.t[i][2], f.t[i][3]};
+        }
       }
       __syncthreads();
+      if (cb + 2 < p.nCG) fetch(cb + 2);
+      Frag<NP> fs[NN], fg[NN];
+#pragma unroll
+      for (int n = 0; n < NN; ++n) {
+        fs[n] = colfrag<NP, true>(sS, L::SLD, L::SPL, 0, 16 * (dt0 + n));
+        fg[n] = colfrag<NP, true>(sG, L::SLD, L::SPL, 0, 16 * (dt0 + n));
+      }
 #pragma unroll
       for (int s = 0; s < 3; ++s) {
         const int t = wave + 4 * s;
         if (t < 10) {
           int ti, tj;
           tile_of(t, ti, tj);
-          const auto fu = colfrag<3>(sU, L::ULD, L::UPL, 0, 16 * tj);
-          mma<2>(dP[s], fu, rowfrag<NT>(sO, L::OLD, L::OPL, 16 * ti, 0));
-          mma<2>(F[s], fu, colfrag<3>(sR, L::ULD, L::UPL, 0, 16 * ti));
+          const auto fu = colfrag<3, true>(sU, L::ULD, L::UPL, 0, 16 * tj);
+          const auto fo = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * ti, 0);
+          const auto fr = colfrag<3, true>(sR, L::ULD, L::UPL, 0, 16 * ti);
+          DELTA_FENCE();
+          mma<2>(dP[s], fu, fo);
+          mma<2>(F[s], fu, fr);
         }
       }
-      Frag<NP> fs[NN], fg[NN];
-#pragma unroll
-      for (int n = 0; n < NN; ++n) {
-        fs[n] = colfrag<NP>(sS, L::SLD, L::SPL, 0, 16 * (dt0 + n));
-        fg[n] = colfrag<NP>(sG, L::SLD, L::SPL, 0, 16 * (dt0 + n));
-      }
+      Frag<NT> fo[2];
+      Frag<NP> fu[2], fr[2];
+      auto read = [&](int mt) {
+        fo[mt & 1] = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * mt, 0);
+        fu[mt & 1] = colfrag<NP, true>(sU, L::ULD, L::UPL, 0, 16 * mt);
+        fr[mt & 1] = colfrag<NP, true>(sR, L::ULD, L::UPL, 0, 16 * mt);
+      };
+      read(0);
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
-        const auto fo = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * mt, 0);
-        const auto fu = colfrag<NP>(sU, L::ULD, L::UPL, 0, 16 * mt);
-        const auto fr = colfrag<NP>(sR, L::ULD, L::UPL, 0, 16 * mt);
+        if (mt < 3) read(mt + 1);
+        DELTA_FENCE();
 #pragma unroll
         for (int n = 0; n < NN; ++n) {
-          mma<LV>(os[mt][n], fo, fs[n]);
-          mma<LV>(ug[mt][n], fu, fg[n]);
-          mma<LV>(rs[mt][n], fr, fs[n]);
+          mma<LV>(os[mt][n], fo[mt & 1], fs[n]);
+          mma<LV>(ug[mt][n], fu[mt & 1], fg[n]);
+          mma<LV>(rs[mt][n], fr[mt & 1], fs[n]);
         }
+        DELTA_FENCE();
       }
     }
     __syncthreads();
     {
       TK tk, tq;
-      tk.load(static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2, p.ks1, t0, rows, p.dkn);
-      tq.load(static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2, p.qs1, t0, rows, p.dkn);
+      tk.load(static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2 + t0 * p.ks1, p.ks1, rows, p.dkn);
+      tq.load(static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2 + t0 * p.qs1, p.qs1, rows, p.dkn);
       if (tid < kTokArrays * C / 4)
         reinterpret_cast<f32x4_t*>(tok)[tid] = reinterpret_cast<const f32x4_t*>(p.wTok + ci * (kTokArrays * C))[tid];
       // tiles above the diagonal that a 32-wide block reads, and sums of tiles that do not exist
       for (int e = tid; e < 2 * NP * 128; e += 256) {
         const int n = e >> 7, row = (e >> 2) & 31, part = e & 3;
         const int i = row < 16 ? row : row + 16, j = (row < 16 ? 16 : 48) + 4 * part;
-        *reinterpret_cast<u32x2*>((n < NP ? sY + n * kTrapLds : sYk + (n - NP) * kTrapLds) + trap_off(i) + j) = u32x2{0u, 0u};
+        *reinterpret_cast<u32x2*>((n < NP ? sY + n * kTrapLds : sYk + (n - NP) * kTrapLds) + trap_off(i) + place(j)) = u32x2{0u, 0u};
       }
       for (int e = tid; e < 3 * 4 * C; e += 256) sum[e] = 0.f;
       tk.store(sK);
@@ -1172,11 +1379,20 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
         int ti, tj;
         tile_of(t, ti, tj);
         f32x4_t qk = zero4(), kk = zero4();
+        {
+          Frag<NT> fj[KB], fq[KB], fk[KB];
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          const auto fj = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb);
-          mma<2>(qk, fj, rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb));
-          mma<2>(kk, fj, rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * ti, 32 * kb));
+          for (int kb = 0; kb < KB; ++kb) {
+            fj[kb] = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb);
+            fq[kb] = rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb);
+            fk[kb] = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * ti, 32 * kb);
+          }
+          DELTA_FENCE();
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) {
+            mma<2>(qk, fj[kb], fq[kb]);
+            mma<2>(kk, fj[kb], fk[kb]);
+          }
         }
         const int i = 16 * ti + n16, j0 = 16 * tj + 4 * q;
         const float ghi = tok[kTokGhi * C + i], glo = tok[kTokGlo * C + i], rki = tok[kTokRk * C + i];
@@ -1198,8 +1414,8 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
           xj[r] = x;
           bi += f * kk[r];
         }
-        put4<NP>(sY + trap_off(i) + j0, kTrapLds, y);
-        put4<NP>(sYk + trap_off(i) + j0, kTrapLds, yk);
+        put4<NP>(sY + trap_off(i) + place(j0), kTrapLds, y);
+        put4<NP>(sYk + trap_off(i) + place(j0), kTrapLds, yk);
         xi += __shfl_xor(xi, 16);
         bi += __shfl_xor(bi, 16);
         xi += __shfl_xor(xi, 32);
@@ -1217,11 +1433,11 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
     if (wave == 0) {  // dg and dbeta, one token per lane
       float into = 0.f, out = 0.f, rz = 0.f, through = 0.f;
       for (int g = 0; g < p.nCG; ++g) {
-        const float* dot = p.wDot + (ci * p.nCG + g) * (4 * C);
-        into += dot[lane];
+        const float* dot = p.wDot + (ci * p.nCG + g) * (kDeltaDots * C);
+        into += dot[lane] - dot[3 * C + lane];
         out += dot[C + lane];
         rz += dot[2 * C + lane];
-        through += dot[3 * C];
+        through += dot[4 * C];
       }
       double ahead = out, behind = into;
       float db = rz;
@@ -1245,32 +1461,50 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
         stf<ET>(p.dbeta, b * p.dbs0 + (t0 + lane) * p.dbs1 + hv * p.dbs2, db);
       }
     }
+    Frag<NT> fk[2][NN], fq[2][NN];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int n = 0; n < NN; ++n) {
+        fk[kb][n] = colfrag<NT>(sK, TK::LD, TK::PLANE, 32 * kb, 16 * (dt0 + n));
+        fq[kb][n] = colfrag<NT>(sQ, TK::LD, TK::PLANE, 32 * kb, 16 * (dt0 + n));
+      }
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
       const int t = 16 * mt + 4 * q;
       const f32x4_t e = ld4(tok + kTokE * C + t), d = ld4(tok + kTokD * C + t), be = ld4(tok + kTokBeta * C + t);
       const f32x4_t rk = ld4(tok + kTokRk * C + t), rq = ld4(tok + kTokRq * C + t);
+      Frag<NP> yr[2], kr[2], yc[2], kc[2];
 #pragma unroll
-      for (int n = 0; n < NN; ++n) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          aq[mt][n][r] += rq[r] * p.scale * e[r] * os[mt][n][r];
-          ak[mt][n][r] += rk[r] * (d[r] * ug[mt][n][r] - be[r] * e[r] * rs[mt][n][r]);
+      for (int kb = 0; kb < 2; ++kb) {
+        if (kb <= mt / 2) {
+          yr[kb] = trap_row<NP>(sY, mt, kb);
+          kr[kb] = trap_row<NP>(sYk, mt, kb);
         }
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          const int dc = 16 * (dt0 + n);
-          if (kb <= mt / 2) {
-            const auto fk = colfrag<NT>(sK, TK::LD, TK::PLANE, 32 * kb, dc);
-            mma<LV>(aq[mt][n], trap_row<NP>(sY, mt, kb), fk);
-            mma<LV>(ak[mt][n], trap_row<NP>(sYk, mt, kb), fk);
-          }
-          if (kb >= mt / 2) {
-            mma<LV>(ak[mt][n], trap_col<NP>(sY, mt, kb), colfrag<NT>(sQ, TK::LD, TK::PLANE, 32 * kb, dc));
-            mma<LV>(ak[mt][n], trap_col<NP>(sYk, mt, kb), colfrag<NT>(sK, TK::LD, TK::PLANE, 32 * kb, dc));
-          }
+        if (kb >= mt / 2) {
+          yc[kb] = trap_col<NP>(sY, mt, kb);
+          kc[kb] = trap_col<NP>(sYk, mt, kb);
         }
       }
+      DELTA_FENCE();
+#pragma unroll
+      for (int n = 0; n < NN; ++n) {
+        aq[mt][n] += rq * p.scale * e * os[mt][n];
+        ak[mt][n] += rk * (d * ug[mt][n] - be * e * rs[mt][n]);
+      }
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int n = 0; n < NN; ++n) {
+          if (kb <= mt / 2) {
+            mma<LV>(aq[mt][n], yr[kb], fk[kb][n]);
+            mma<LV>(ak[mt][n], kr[kb], fk[kb][n]);
+          }
+          if (kb >= mt / 2) {
+            mma<LV>(ak[mt][n], yc[kb], fq[kb][n]);
+            mma<LV>(ak[mt][n], kc[kb], fk[kb][n]);
+          }
+        }
     }
   }
 
@@ -1278,7 +1512,7 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
   auto element = [&](const uint16_t* m, int t, int d) {
     float x = 0.f;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) x += __uint_as_float(uint32_t(m[i * TK::PLANE + t * TK::LD + d]) << 16);
+    for (int i = 0; i < NT; ++i) x += __uint_as_float(uint32_t(m[i * TK::PLANE + t * TK::LD + place(d)]) << 16);
     return x;
   };
   const bool unit = p.eps >= 0.f;
