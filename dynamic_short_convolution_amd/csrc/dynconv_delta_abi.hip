@@ -33,6 +33,9 @@ dynconv_status check_tensor(const void* p, const int64_t* s, int n, const int64_
 constexpr int64_t kDeltaMaxTokenStride = int64_t(1) << 22;
 bool far_tokens(const int64_t* s, int64_t T) { return T > 1 && s[1] >= kDeltaMaxTokenStride; }
 
+// Whether the rows of a chunk lie one behind the other (no token's row overlaps the next).
+bool apart(const int64_t* s, const int64_t* e) { return e[1] <= 1 || s[1] >= e[3]; }
+
 // Whether rows of the last dimension can be read in 16-byte pieces.
 int wide(const void* p, const int64_t* s, int n, const int64_t* e, int eb) {
   if (!aligned(p, 16)) return 0;
@@ -87,7 +90,8 @@ dynconv_status take_inputs(DeltaParams* p, const void* q, const int64_t* qs, con
     p->vs0 = vs[0], p->vs1 = vs[1], p->vs2 = vs[2];
     p->gs0 = gs[0], p->gs1 = gs[1], p->gs2 = gs[2];
     p->bs0 = bs[0], p->bs1 = bs[1], p->bs2 = bs[2];
-    p->vec = dk % 8 == 0 && wide(q, qs, 4, eq, eb) && wide(k, ks, 4, eq, eb);
+    p->vec = dk % 8 == 0 && wide(q, qs, 4, eq, eb) && wide(k, ks, 4, eq, eb) && apart(qs, eq) && apart(ks, eq) &&
+             apart(vs, ev);
   }
   if (state_in != nullptr) {
     if ((st = check_tensor(state_in, sis, 4, est, 4, true, false)) != DYNCONV_OK) return st;
@@ -138,6 +142,7 @@ dynconv_status dynconv_delta_fwd(const void* q, const int64_t* qs, const void* k
   if (T > 0) {
     if ((st = check_tensor(o, os, 4, ev, elem_bytes(dtype), true, true)) != DYNCONV_OK) return st;
     if (far_tokens(os, T)) return DYNCONV_ERR_UNSUPPORTED;
+    p.vec = p.vec && apart(os, ev);
     p.out = o;
     p.os0 = os[0], p.os1 = os[1], p.os2 = os[2];
   }
@@ -202,7 +207,7 @@ dynconv_status dynconv_delta_bwd(const void* q, const int64_t* qs, const void* k
   p.dvs0 = dvs[0], p.dvs1 = dvs[1], p.dvs2 = dvs[2];
   p.dgs0 = dgs[0], p.dgs1 = dgs[1], p.dgs2 = dgs[2];
   p.dbs0 = dbs[0], p.dbs1 = dbs[1], p.dbs2 = dbs[2];
-  p.vec = p.vec && dv % 8 == 0 && wide(dO, dos, 4, ev, eb);
+  p.vec = p.vec && dv % 8 == 0 && wide(dO, dos, 4, ev, eb) && apart(dos, ev) && apart(dvs, ev);
   if (dstate_out != nullptr) {
     if ((st = check_tensor(dstate_out, dsos, 4, est, 4, true, false)) != DYNCONV_OK) return st;
     p.dstate_out = dstate_out;

@@ -40,6 +40,7 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
 constexpr int C = kDeltaChunk;
+constexpr int kLdsBytes = 160 * 1024;
 
 template <typename ET>
 struct Store;  // terms of a stored element, and of an operand that only reaches stored results
@@ -187,13 +188,12 @@ __device__ __forceinline__ void row_load(Frag<NA>* f, const uint16_t* m, int ld,
 }
 
 // acc[i] += transposed rows of a [64][16 N] matrix times b: acc[i] takes columns 16i .. 16i+15,
-// contraction over the 64 rows. Two column tiles at a time, the next two's reads ahead.
+// contraction over the 64 rows. Four column tiles (independent accumulators) of one 32-row
+// block at a time, the next reads ahead.
 template <int NA>
-__device__ __forceinline__ void col_load(Frag<NA>* f, const uint16_t* m, int ld, int plane, int i0) {
+__device__ __forceinline__ void col_load(Frag<NA>* f, const uint16_t* m, int ld, int plane, int kb, int i0) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) f[2 * kb + i] = colfrag<NA>(m, ld, plane, 32 * kb, 16 * (i0 + i));
+  for (int i = 0; i < 4; ++i) f[i] = colfrag<NA>(m, ld, plane, 32 * kb, 16 * (i0 + i));
 }
 template <int L, int N, int NA, int NB, typename Next>
 __device__ __forceinline__ void col_product(f32x4_t* acc, Frag<NA>* f, const uint16_t* m, int ld, int plane,
@@ -202,38 +202,45 @@ __device__ __forceinline__ void col_product(f32x4_t* acc, Frag<NA>* f, const uin
 #pragma unroll
   for (int i = 0; i < 4; ++i) g[0][i] = f[i];
 #pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    if (i + 2 < N) {
-      col_load<NA>(g[(i / 2 + 1) & 1], m, ld, plane, i + 2);
+  for (int s = 0; s < N / 2; ++s) {  // step s: block s % 2 of tiles 4 (s / 2) ..
+    if (s + 1 < N / 2) {
+      col_load<NA>(g[(s + 1) & 1], m, ld, plane, (s + 1) & 1, (s + 1) / 2 * 4);
     } else {
       next();
     }
     DELTA_FENCE();
-    mma_tiles<L, 2>(acc + i, g[(i / 2) & 1], b[0]);
-    mma_tiles<L, 2>(acc + i, g[(i / 2) & 1] + 2, b[1]);
+    mma_tiles<L, 4>(acc + s / 2 * 4, g[s & 1], b[s & 1]);
     DELTA_FENCE();
   }
 }
 
-// LDS image of a lower-triangular matrix: rows 0..31 of 40 elements (32 used), rows 32..63 of 72.
-constexpr int kTrapLds = 32 * 40 + 32 * 72;
-__device__ __forceinline__ constexpr int trap_off(int i) { return i < 32 ? i * 40 : 1280 + (i - 32) * 72; }
+// A 16-byte read is served in passes of lanes 0-7 with 16-23, 8-15 with 24-31, ... over 256
+// bytes: 8 rows at two neighbouring 16-byte places. Row pitches are therefore an odd multiple
+// of 32 bytes (16 elements), which puts the 8 rows on the 8 even places.
+constexpr int kPad = 16;
+
+// LDS image of a lower-triangular matrix: rows 0..31 of 48 elements (32 used), rows 32..63 of 80.
+constexpr int kLdA = 32 + kPad, kLdB = 64 + kPad, kTrapLo = 32 * kLdA, kTrapHi = 32 * kLdB;
+constexpr int kTrapLds = kTrapLo + kTrapHi;
+__device__ __forceinline__ constexpr int trap_off(int i) { return i < 32 ? i * kLdA : kTrapLo + (i - 32) * kLdB; }
 template <int N>
 __device__ __forceinline__ Frag<N> trap_row(const uint16_t* m, int tile, int kb) {  // kb <= tile / 2
-  return tile < 2 ? rowfrag<N>(m, 40, kTrapLds, 16 * tile, 0) : rowfrag<N>(m + 1280, 72, kTrapLds, 16 * tile - 32, 32 * kb);
+  return tile < 2 ? rowfrag<N>(m, kLdA, kTrapLds, 16 * tile, 0)
+                  : rowfrag<N>(m + kTrapLo, kLdB, kTrapLds, 16 * tile - 32, 32 * kb);
 }
 template <int N>
 __device__ __forceinline__ Frag<N> trap_col(const uint16_t* m, int tile, int kb) {  // kb >= tile / 2
-  return kb == 0 ? colfrag<N>(m, 40, kTrapLds, 0, 16 * tile) : colfrag<N>(m + 1280, 72, kTrapLds, 0, 16 * tile);
+  return kb == 0 ? colfrag<N>(m, kLdA, kTrapLds, 0, 16 * tile) : colfrag<N>(m + kTrapLo, kLdB, kTrapLds, 0, 16 * tile);
 }
-// The same for an upper-triangular matrix: rows 0..31 of 72 (64 used), rows 32..63 of 40
+// The same for an upper-triangular matrix: rows 0..31 of 80 (64 used), rows 32..63 of 48
 // (columns 32..63).
 __device__ __forceinline__ constexpr int utrap_off(int i, int j) {
-  return i < 32 ? i * 72 + j : 2304 + (i - 32) * 40 + j - 32;
+  return i < 32 ? i * kLdB + j : kTrapHi + (i - 32) * kLdA + j - 32;
 }
 template <int N>
 __device__ __forceinline__ Frag<N> utrap_row(const uint16_t* m, int tile, int kb) {  // kb >= tile / 2
-  return tile < 2 ? rowfrag<N>(m, 72, kTrapLds, 16 * tile, 32 * kb) : rowfrag<N>(m + 2304, 40, kTrapLds, 16 * tile - 32, 0);
+  return tile < 2 ? rowfrag<N>(m, kLdB, kTrapLds, 16 * tile, 32 * kb)
+                  : rowfrag<N>(m + kTrapHi, kLdA, kTrapLds, 16 * tile - 32, 0);
 }
 
 // Triangular products over the 64-row contraction, fragments of both blocks at once.
@@ -307,12 +314,16 @@ __device__ __forceinline__ void stf(void* p, int64_t i, float v) {
 
 // Global rows of a chunk go through buffer instructions: a uniform descriptor per chunk and
 // 32-bit byte offsets (the ABI bounds token strides so that 64 rows stay below 2^31 bytes).
-// Rows and columns that do not exist get the offset kNowhere: such loads return 0 and such
-// stores are dropped, without a branch (a branch around a load makes each wait for the one
-// before).
+// Loads from outside the descriptor's range return 0 and stores to it are dropped, without a
+// branch (a branch around a load makes each wait for the one before) and without a mask per
+// row (16 of them held over a chunk spilled scalar registers): the range ends with the last
+// row that exists, and lanes of columns that do not start at kNowhere. VEC is only set when
+// rows do not overlap (token stride >= row length); the general form masks every element.
 constexpr uint32_t kNowhere = 0x80000000u;
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rsrc(const void* p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, int(kNowhere), 0x00027000);
+template <typename ET, bool VEC>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rsrc(const ET* p, int64_t s1, int rows, int cols) {
+  const int range = VEC ? int((uint32_t(rows - 1) * uint32_t(s1) + uint32_t(cols)) * uint32_t(sizeof(ET))) : int(kNowhere);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<ET*>(p), 0, range, 0x00027000);
 }
 template <typename ET>
 __device__ __forceinline__ float buf_ld(__amdgpu_buffer_rsrc_t r, uint32_t off) {
@@ -331,8 +342,8 @@ __device__ __forceinline__ void buf_st(__amdgpu_buffer_rsrc_t r, uint32_t off, f
   }
 }
 
-// 8 consecutive stored elements of a row, as loaded; elements from `n` on read as zero (VEC: n
-// is at least 8 or at most 0).
+// 8 consecutive stored elements of a row, as loaded; elements from `n` on read as zero (VEC:
+// `off` alone decides).
 template <typename ET>
 struct Raw8 {
   u32x4 w[sizeof(ET) / 2];
@@ -341,10 +352,9 @@ template <typename ET, bool VEC>
 __device__ __forceinline__ Raw8<ET> load8(__amdgpu_buffer_rsrc_t rs, uint32_t off, int n) {
   Raw8<ET> r;
   if constexpr (VEC) {
-    const uint32_t o = n > 0 ? off : kNowhere;
 #pragma unroll
     for (int i = 0; i < int(sizeof(ET) / 2); ++i)
-      r.w[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, int(o), 16 * i, 0);
+      r.w[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, int(off) + 16 * i, 0, 0);
   } else {
     uint32_t e[8];
 #pragma unroll
@@ -392,18 +402,19 @@ __device__ __forceinline__ Frag<Store<ET>::NT> terms8(const Raw8<ET>& r) {
 // A [64][DK] tile of q or k rows: loads into registers, then stores its terms to LDS.
 template <typename ET, int DK, int NTHR, bool VEC>
 struct Tile {
-  static constexpr int LD = DK + 8, PLANE = C * LD, N = C * DK / 8 / NTHR;
+  // (three planes of q and of k with the full padding would not leave room in LDS)
+  static constexpr int LD = DK + (Store<ET>::NT < 3 ? kPad : 8), PLANE = C * LD, N = C * DK / 8 / NTHR;
   static_assert(C * DK / 8 % NTHR == 0, "whole passes");
   Raw8<ET> r[N];
   // `base`: the chunk's first element; rows s1 apart; `rows` valid rows, `cols` valid columns
   // (a multiple of 8 with VEC).
   __device__ __forceinline__ void load(const ET* base, int64_t s1, int rows, int cols) {
-    const __amdgpu_buffer_rsrc_t rs = chunk_rsrc(base);
+    const __amdgpu_buffer_rsrc_t rs = chunk_rsrc<ET, VEC>(base, s1, rows, cols);
     constexpr int STEP = NTHR / (DK / 8);
     const int row = int(threadIdx.x) / (DK / 8), col = int(threadIdx.x) % (DK / 8) * 8;
     const uint32_t pitch = uint32_t(s1) * uint32_t(sizeof(ET));
-    const uint32_t off = uint32_t(row) * pitch + uint32_t(col) * uint32_t(sizeof(ET));
     const int n = cols - col;
+    const uint32_t off = n > 0 ? uint32_t(row) * pitch + uint32_t(col) * uint32_t(sizeof(ET)) : kNowhere;
 #pragma unroll
     for (int i = 0; i < N; ++i) r[i] = load8<ET, VEC>(rs, off + i * STEP * pitch, row + i * STEP < rows ? n : 0);
   }
@@ -441,7 +452,7 @@ struct TrapTile {
       const int idx = int(threadIdx.x) + i * NTHR;
       if (idx >= TOTAL) continue;
       const int plane = idx / (kTrapElems / 8), e = idx % (kTrapElems / 8);
-      const int off = e < 128 ? (e >> 2) * 40 + (e & 3) * 8 : 1280 + ((e - 128) >> 3) * 72 + (e & 7) * 8;
+      const int off = e < 128 ? (e >> 2) * kLdA + (e & 3) * 8 : kTrapLo + ((e - 128) >> 3) * kLdB + (e & 7) * 8;
       *reinterpret_cast<u32x4*>(m + plane * kTrapLds + off) = r[i];
     }
   }
@@ -493,6 +504,7 @@ template <typename ET, int DK, bool VEC>
 __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
   using L = PrepLds<ET, DK>;
   using TK = Tile<ET, DK, 256, VEC>;
+  static_assert(L::BYTES <= kLdsBytes, "LDS of a CU");
   extern __shared__ __align__(16) char lds[];
   uint16_t* sK = reinterpret_cast<uint16_t*>(lds + L::K);
   float* sA = reinterpret_cast<float*>(lds + L::A);
@@ -662,29 +674,31 @@ struct ScanLds {
 __device__ __forceinline__ int delta_cols(const DeltaParams& p, int nw) { return (p.nCG + nw - 1) / nw; }
 
 // The 16 values of a wave's column in a chunk: token 16 mt + 4 q + r in v[4 mt + r].
-// `base`: the chunk's first element, `rows` its tokens.
-template <typename ET>
-__device__ __forceinline__ void load_cols(float* v, const ET* base, int64_t s1, int rows, int col, bool ok) {
+// `base`: the chunk's first element, `rows` its tokens, `cols` the head's width.
+template <typename ET, bool VEC>
+__device__ __forceinline__ void load_cols(float* v, const ET* base, int64_t s1, int rows, int col, int cols) {
   const int q = (threadIdx.x & 63) >> 4;
-  const __amdgpu_buffer_rsrc_t rs = chunk_rsrc(base);
-  const uint32_t pitch = uint32_t(s1) * uint32_t(sizeof(ET)), o0 = 4u * q * pitch + uint32_t(col) * uint32_t(sizeof(ET));
-  const int left = ok ? rows - 4 * q : 0;
+  const __amdgpu_buffer_rsrc_t rs = chunk_rsrc<ET, VEC>(base, s1, rows, cols);
+  const uint32_t pitch = uint32_t(s1) * uint32_t(sizeof(ET));
+  const uint32_t o0 = col < cols ? 4u * q * pitch + uint32_t(col) * uint32_t(sizeof(ET)) : kNowhere;
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const int t = 16 * (e >> 2) + (e & 3);
-    v[e] = buf_ld<ET>(rs, t < left ? o0 + uint32_t(t) * pitch : kNowhere);
+    const uint32_t o = o0 + uint32_t(t) * pitch;
+    v[e] = buf_ld<ET>(rs, VEC || (col < cols && t + 4 * q < rows) ? o : kNowhere);
   }
 }
-template <typename ET>
-__device__ __forceinline__ void store_cols(const f32x4_t* v, ET* base, int64_t s1, int rows, int col, bool ok) {
+template <typename ET, bool VEC>
+__device__ __forceinline__ void store_cols(const f32x4_t* v, ET* base, int64_t s1, int rows, int col, int cols) {
   const int q = (threadIdx.x & 63) >> 4;
-  const __amdgpu_buffer_rsrc_t rs = chunk_rsrc(base);
-  const uint32_t pitch = uint32_t(s1) * uint32_t(sizeof(ET)), o0 = 4u * q * pitch + uint32_t(col) * uint32_t(sizeof(ET));
-  const int left = ok ? rows - 4 * q : 0;
+  const __amdgpu_buffer_rsrc_t rs = chunk_rsrc<ET, VEC>(base, s1, rows, cols);
+  const uint32_t pitch = uint32_t(s1) * uint32_t(sizeof(ET));
+  const uint32_t o0 = col < cols ? 4u * q * pitch + uint32_t(col) * uint32_t(sizeof(ET)) : kNowhere;
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const int t = 16 * (e >> 2) + (e & 3);
-    buf_st<ET>(rs, t < left ? o0 + uint32_t(t) * pitch : kNowhere, v[e >> 2][e & 3]);
+    const uint32_t o = o0 + uint32_t(t) * pitch;
+    buf_st<ET>(rs, VEC || (col < cols && t + 4 * q < rows) ? o : kNowhere, v[e >> 2][e & 3]);
   }
 }
 
@@ -733,6 +747,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
   using L = ScanLds<ET, DK, STATES>;
   constexpr int NT = L::NT, NP = L::NP, NTHR = 64 * NW, KB = DK / 32;
   using TK = Tile<ET, DK, NTHR, VEC>;
+  static_assert(L::BYTES <= kLdsBytes, "LDS of a CU");
   extern __shared__ __align__(16) char lds[];
   uint16_t* sK = reinterpret_cast<uint16_t*>(lds + L::K);
   uint16_t* sQ = reinterpret_cast<uint16_t*>(lds + L::Q);
@@ -790,7 +805,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
     float v[16];
     {
       const int64_t t0 = int64_t(c) * C;
-      load_cols<ET>(v, vbase + t0 * p.vs1, p.vs1, min(C, p.T - int(t0)), col, ok);
+      load_cols<ET, VEC>(v, vbase + t0 * p.vs1, p.vs1, min(C, p.T - int(t0)), col, p.dvn);
     }
     __syncthreads();
 
@@ -877,7 +892,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
     if (c + 1 < p.nC) fetch(c + 1);
     {
       Frag<NT> fc[4];
-      col_load<NT>(fc, sK, TK::LD, TK::PLANE, 0);
+      col_load<NT>(fc, sK, TK::LD, TK::PLANE, 0, 0);
       f32x4_t d[4];
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) d[mt] = u[mt] * td[mt] * trk[mt];
@@ -894,7 +909,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
       DELTA_FENCE();
       trap_product<NP - 1>(o, fp, uf);
       const int64_t t0 = int64_t(c) * C;
-      store_cols<ET>(o, obase + t0 * p.os1, p.os1, min(C, p.T - int(t0)), col, ok);
+      store_cols<ET, VEC>(o, obase + t0 * p.os1, p.os1, min(C, p.T - int(t0)), col, p.dvn);
     }
   }
   if constexpr (!STATES)
@@ -941,6 +956,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_back(const DeltaParams p) 
   using L = BackLds<ET, DK>;
   constexpr int NT = L::NT, NTHR = 64 * NW, KB = DK / 32;
   using TK = Tile<ET, DK, NTHR, VEC>;
+  static_assert(L::BYTES <= kLdsBytes, "LDS of a CU");
   extern __shared__ __align__(16) char lds[];
   uint16_t* sK = reinterpret_cast<uint16_t*>(lds + L::K);
   uint16_t* sQ = reinterpret_cast<uint16_t*>(lds + L::Q);
@@ -1002,8 +1018,8 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_back(const DeltaParams p) 
     float v[16], dO[16];
     const int64_t t0 = int64_t(c) * C;
     const int rows = min(C, p.T - int(t0));
-    load_cols<ET>(v, vbase + t0 * p.vs1, p.vs1, rows, col, ok);
-    load_cols<ET>(dO, dobase + t0 * p.dos1, p.dos1, rows, col, ok);
+    load_cols<ET, VEC>(v, vbase + t0 * p.vs1, p.vs1, rows, col, p.dvn);
+    load_cols<ET, VEC>(dO, dobase + t0 * p.dos1, p.dos1, rows, col, p.dvn);
     __syncthreads();
 
     // P^T: tiles of P = scale Gam o Q K^T (rows i, column j), four neighbours of a row of P^T
@@ -1128,7 +1144,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_back(const DeltaParams p) 
     if (c > 0) fetch(c - 1);
     {
       Frag<NT> fc[4];
-      col_load<NT>(fc, sK, TK::LD, TK::PLANE, 0);
+      col_load<NT>(fc, sK, TK::LD, TK::PLANE, 0, 0);
       f32x4_t dz[4], tc[4];
       tok_load(tc, tok + kTokRk * C);
 #pragma unroll
@@ -1145,14 +1161,14 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_back(const DeltaParams p) 
           *reinterpret_cast<f32x4_t*>(dot + 3 * C + 16 * mt + 4 * q) = y;
         }
       }
-      store_cols<ET>(dz, dvbase + t0 * p.dvs1, p.dvs1, rows, col, ok);
+      store_cols<ET, VEC>(dz, dvbase + t0 * p.dvs1, p.dvs1, rows, col, p.dvn);
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) dz[mt] = -(dz[mt] * ta[mt] * tc[mt]);
       const Frag<3> rf[2] = {split8<3>(dz[0], dz[1]), split8<3>(dz[2], dz[3])};
 #pragma unroll
       for (int i = 0; i < DK / 16; ++i) dS[i] *= gamma;
       col_product<2, DK / 16>(dS, fc, sK, TK::LD, TK::PLANE, rf, [&] {
-        col_load<NT>(fc, sQ, TK::LD, TK::PLANE, 0);
+        col_load<NT>(fc, sQ, TK::LD, TK::PLANE, 0, 0);
         tok_load(tc, tok + kTokRq * C);
       });
 #pragma unroll
@@ -1184,15 +1200,14 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_back(const DeltaParams p) 
 template <typename ET, int DK>
 struct GradLds {
   static constexpr int NT = Store<ET>::NT, NP = Store<ET>::NP;
-  static constexpr int ULD = C + 8, OLD = 40, SLD = DK + 8;
+  static constexpr int ULD = C + kPad, OLD = 32 + kPad, SLD = DK + kPad;
   static constexpr int UPL = 32 * ULD, OPL = C * OLD, SPL = 32 * SLD;
   // first part: staged operands of 32 value columns
   static constexpr int U = 0;
   static constexpr int R = U + 3 * UPL * 2;
   static constexpr int O = R + 3 * UPL * 2;
   static constexpr int S = O + NT * OPL * 2;
-  static constexpr int G = S + NP * SPL * 2;
-  static constexpr int END1 = G + NP * SPL * 2;
+  static constexpr int END1 = S + NP * SPL * 2;
   // second part, in the same place
   static constexpr int K = 0;
   static constexpr int Q = K + NT * Tile<ET, DK, 64, true>::PLANE * 2;
@@ -1229,12 +1244,12 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
   using L = GradLds<ET, DK>;
   constexpr int NT = L::NT, NP = L::NP, LV = NP - 1, KB = DK / 32, NN = DK / 64;
   using TK = Tile<ET, DK, 256, VEC>;
+  static_assert(L::BYTES <= kLdsBytes, "LDS of a CU");
   extern __shared__ __align__(16) char lds[];
   uint16_t* sU = reinterpret_cast<uint16_t*>(lds + L::U);
   uint16_t* sR = reinterpret_cast<uint16_t*>(lds + L::R);
   uint16_t* sO = reinterpret_cast<uint16_t*>(lds + L::O);
   uint16_t* sS = reinterpret_cast<uint16_t*>(lds + L::S);
-  uint16_t* sG = reinterpret_cast<uint16_t*>(lds + L::G);
   uint16_t* sK = reinterpret_cast<uint16_t*>(lds + L::K);
   uint16_t* sQ = reinterpret_cast<uint16_t*>(lds + L::Q);
   uint16_t* sY = reinterpret_cast<uint16_t*>(lds + L::Y);
@@ -1260,98 +1275,125 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
     const int hv = hk * p.group + gh;
     const int64_t ci = (int64_t(b) * p.Hv + hv) * p.nC + c;
     const ET* dobase = static_cast<const ET*>(p.dO) + b * p.dos0 + hv * p.dos2 + t0 * p.dos1;
-    f32x4_t dP[3], F[3];
+    f32x4_t dP[3], F[3], os[4][NN], rs[4][NN], ug[4][NN];
 #pragma unroll
     for (int s = 0; s < 3; ++s) dP[s] = F[s] = zero4();
-    f32x4_t os[4][NN], ug[4][NN], rs[4][NN];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-      for (int n = 0; n < NN; ++n) os[mt][n] = ug[mt][n] = rs[mt][n] = zero4();
-
-    ImageTile<2> iu[2], ir[2];
-    ImageTile<KB> is[2], ig[2];
-    Raw8<ET> io;
-    auto fetch = [&](int cb) {
+      for (int n = 0; n < NN; ++n) os[mt][n] = rs[mt][n] = ug[mt][n] = zero4();
+    {  // everything but U dS1^T
+      ImageTile<2> iu[2], ir[2];
+      ImageTile<KB> is[2];
+      Raw8<ET> io;
+      auto fetch = [&](int cb) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t cim = ci * p.nCG + min(cb + h, p.nCG - 1);
-        iu[h].load(p.wU + cim * (C * kDeltaCols));
-        ir[h].load(p.wR + cim * (C * kDeltaCols));
-        is[h].load(p.wS + cim * (DK * 16));
-        ig[h].load(p.wdS + cim * (DK * 16));
-      }
-      const int row = tid >> 2, c0 = cb * kDeltaCols + (tid & 3) * 8;
-      const __amdgpu_buffer_rsrc_t rs = chunk_rsrc(dobase);
-      const uint32_t off = (uint32_t(row) * uint32_t(p.dos1) + uint32_t(c0)) * uint32_t(sizeof(ET));
-      const int n = row < rows ? p.dvn - c0 : 0;
-      if constexpr (VEC) {
-        io = load8<ET, true>(rs, off, n);
-      } else {
-        io = load8<ET, false>(rs, off, n);
-      }
-    };
-    fetch(0);
-    for (int cb = 0; cb < p.nCG; cb += 2) {
-      __syncthreads();  // the previous contents are read
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool have = cb + h < p.nCG;
-        iu[h].template store<3>(sU + 16 * h * L::ULD, L::ULD, L::UPL, have);
-        ir[h].template store<3>(sR + 16 * h * L::ULD, L::ULD, L::UPL, have);
-        is[h].template store<NP>(sS + 16 * h * L::SLD, L::SLD, L::SPL, have);
-        ig[h].template store<NP>(sG + 16 * h * L::SLD, L::SLD, L::SPL, have);
-      }
-      {
-        const Frag<NT> f = terms8<ET>(io);
-        uint16_t* o = sO + (tid >> 2) * L::OLD + place((tid & 3) * 8);
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          *reinterpret_cast<u32x2*>(o + i * L::OPL) = u32x2{f.t[i][0], f.t[i][1]};
-          *reinterpret_cast<u32x2*>(o + i * L::OPL + 8) = u32x2{f.t[i][2], f.t[i][3]};
+        for (int h = 0; h < 2; ++h) {
+          const int64_t cim = ci * p.nCG + min(cb + h, p.nCG - 1);
+          iu[h].load(p.wU + cim * (C * kDeltaCols));
+          ir[h].load(p.wR + cim * (C * kDeltaCols));
+          is[h].load(p.wS + cim * (DK * 16));
         }
-      }
-      __syncthreads();
-      if (cb + 2 < p.nCG) fetch(cb + 2);
-      Frag<NP> fs[NN], fg[NN];
-#pragma unroll
-      for (int n = 0; n < NN; ++n) {
-        fs[n] = colfrag<NP, true>(sS, L::SLD, L::SPL, 0, 16 * (dt0 + n));
-        fg[n] = colfrag<NP, true>(sG, L::SLD, L::SPL, 0, 16 * (dt0 + n));
-      }
-#pragma unroll
-      for (int s = 0; s < 3; ++s) {
-        const int t = wave + 4 * s;
-        if (t < 10) {
-          int ti, tj;
-          tile_of(t, ti, tj);
-          const auto fu = colfrag<3, true>(sU, L::ULD, L::UPL, 0, 16 * tj);
-          const auto fo = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * ti, 0);
-          const auto fr = colfrag<3, true>(sR, L::ULD, L::UPL, 0, 16 * ti);
-          DELTA_FENCE();
-          mma<2>(dP[s], fu, fo);
-          mma<2>(F[s], fu, fr);
-        }
-      }
-      Frag<NT> fo[2];
-      Frag<NP> fu[2], fr[2];
-      auto read = [&](int mt) {
-        fo[mt & 1] = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * mt, 0);
-        fu[mt & 1] = colfrag<NP, true>(sU, L::ULD, L::UPL, 0, 16 * mt);
-        fr[mt & 1] = colfrag<NP, true>(sR, L::ULD, L::UPL, 0, 16 * mt);
+        const int row = tid >> 2, c0 = cb * kDeltaCols + (tid & 3) * 8;
+        const int n = row < rows ? p.dvn - c0 : 0;
+        const uint32_t off = (uint32_t(row) * uint32_t(p.dos1) + uint32_t(c0)) * uint32_t(sizeof(ET));
+        io = load8<ET, VEC>(chunk_rsrc<ET, VEC>(dobase, p.dos1, rows, p.dvn), n > 0 ? off : kNowhere, n);
       };
-      read(0);
+      fetch(0);
+      for (int cb = 0; cb < p.nCG; cb += 2) {
+        __syncthreads();  // the previous contents are read
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        if (mt < 3) read(mt + 1);
+        for (int h = 0; h < 2; ++h) {
+          const bool have = cb + h < p.nCG;
+          iu[h].template store<3>(sU + 16 * h * L::ULD, L::ULD, L::UPL, have);
+          ir[h].template store<3>(sR + 16 * h * L::ULD, L::ULD, L::UPL, have);
+          is[h].template store<NP>(sS + 16 * h * L::SLD, L::SLD, L::SPL, have);
+        }
+        {
+          const Frag<NT> f = terms8<ET>(io);
+          uint16_t* o = sO + (tid >> 2) * L::OLD + place((tid & 3) * 8);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            *reinterpret_cast<u32x2*>(o + i * L::OPL) = u32x2{f.t[i][0], f.t[i][1]};
+            *reinterpret_cast<u32x2*>(o + i * L::OPL + 8) = u32x2{f.t[i][2], f.t[i][3]};
+          }
+        }
+        __syncthreads();
+        if (cb + 2 < p.nCG) fetch(cb + 2);
+        Frag<NP> fs[NN];
+        Frag<NT> fo[4];
+        Frag<NP> fr[4];
+#pragma unroll
+        for (int n = 0; n < NN; ++n) fs[n] = colfrag<NP, true>(sS, L::SLD, L::SPL, 0, 16 * (dt0 + n));
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+          fo[mt] = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * mt, 0);
+          fr[mt] = colfrag<NP, true>(sR, L::ULD, L::UPL, 0, 16 * mt);
+        }
         DELTA_FENCE();
 #pragma unroll
         for (int n = 0; n < NN; ++n) {
-          mma<LV>(os[mt][n], fo[mt & 1], fs[n]);
-          mma<LV>(ug[mt][n], fu[mt & 1], fg[n]);
-          mma<LV>(rs[mt][n], fr[mt & 1], fs[n]);
+          f32x4_t x[4], y[4];
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) x[mt] = os[mt][n], y[mt] = rs[mt][n];
+          mma_tiles<LV, 4>(x, fo, fs[n]);
+          mma_tiles<LV, 4>(y, fr, fs[n]);
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) os[mt][n] = x[mt], rs[mt][n] = y[mt];
         }
+#pragma unroll
+        for (int s = 0; s < 3; ++s) {
+          const int t = wave + 4 * s;
+          if (t < 10) {
+            int ti, tj;
+            tile_of(t, ti, tj);
+            const auto fu = colfrag<3, true>(sU, L::ULD, L::UPL, 0, 16 * tj);
+            const auto fo1 = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * ti, 0);
+            const auto fr1 = colfrag<3, true>(sR, L::ULD, L::UPL, 0, 16 * ti);
+            DELTA_FENCE();
+            mma<2>(dP[s], fu, fo1);
+            mma<2>(F[s], fu, fr1);
+          }
+        }
+      }
+    }
+    {  // U dS1^T, in a loop of its own: fewer accumulators and less LDS at a time
+      ImageTile<2> iu[2];
+      ImageTile<KB> ig[2];
+      auto fetch = [&](int cb) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t cim = ci * p.nCG + min(cb + h, p.nCG - 1);
+          iu[h].load(p.wU + cim * (C * kDeltaCols));
+          ig[h].load(p.wdS + cim * (DK * 16));
+        }
+      };
+      fetch(0);
+      for (int cb = 0; cb < p.nCG; cb += 2) {
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bool have = cb + h < p.nCG;
+          iu[h].template store<NP>(sU + 16 * h * L::ULD, L::ULD, L::UPL, have);
+          ig[h].template store<NP>(sS + 16 * h * L::SLD, L::SLD, L::SPL, have);
+        }
+        __syncthreads();
+        if (cb + 2 < p.nCG) fetch(cb + 2);
+        Frag<NP> fg[NN], fu[4];
+#pragma unroll
+        for (int n = 0; n < NN; ++n) fg[n] = colfrag<NP, true>(sS, L::SLD, L::SPL, 0, 16 * (dt0 + n));
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) fu[mt] = colfrag<NP, true>(sU, L::ULD, L::UPL, 0, 16 * mt);
         DELTA_FENCE();
+#pragma unroll
+        for (int n = 0; n < NN; ++n) {
+          f32x4_t x[4];
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) x[mt] = ug[mt][n];
+          mma_tiles<LV, 4>(x, fu, fg[n]);
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) ug[mt][n] = x[mt];
+        }
       }
     }
     __syncthreads();
