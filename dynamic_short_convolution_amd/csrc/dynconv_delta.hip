@@ -23,7 +23,7 @@ DeltaSizes delta_sizes(int64_t B, int64_t T, int64_t Hv, int64_t dk, int64_t dv)
   z.tok = n * kTokArrays * kDeltaChunk * sizeof(float);
   z.S = n * nCG * size_t(delta_dk_pad(int(dk))) * kDeltaCols * sizeof(float);
   z.U = n * nCG * kDeltaChunk * kDeltaCols * sizeof(float);
-  z.dot = n * nCG * kDeltaDots * kDeltaChunk * sizeof(float);
+  z.dot = n * nCG * kDeltaChunk * sizeof(float);
   return z;  // every size is a multiple of kPiece
 }
 

@@ -55,7 +55,7 @@ dynconv_status check_sizes(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t
   const int64_t bh = B * Hv;
   const int64_t per = (T + kDeltaChunk - 1) / kDeltaChunk;
   const int64_t cols = (dv + kDeltaCols - 1) / kDeltaCols;
-  if (bh > INT32_MAX || (per > 0 && bh > INT32_MAX / per) || bh > INT32_MAX / cols) return DYNCONV_ERR_UNSUPPORTED;
+  if (bh > INT32_MAX || (per > 0 && bh > INT32_MAX / per) || 2 * bh > INT32_MAX / cols) return DYNCONV_ERR_UNSUPPORTED;
   return DYNCONV_OK;
 }
 

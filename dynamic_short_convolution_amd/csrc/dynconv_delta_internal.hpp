@@ -14,8 +14,6 @@ constexpr int kDeltaMaxDk = 128;    // widest key head
 constexpr int kDeltaMaxDv = 65536;  // widest value head
 constexpr int kDeltaCols = 16;      // value columns of one wave
 
-constexpr int kDeltaDots = 5;        // per-token sums of a wave's columns in the backward
-
 // Lower-triangular 64 x 64 matrices keep rows 0..31 in 32 columns and rows 32..63 in 64.
 constexpr int kTrapElems = 32 * 32 + 32 * 64;
 constexpr int kTokArrays = 8;  // per chunk and value head: float[64] each, in this order
@@ -54,7 +52,7 @@ struct DeltaParams {
   float* wdS;     // the same, gradient of the state after the chunk
   float* wU;      // [chunk][nCG][1024]: u, in fragment order
   float* wR;      // the same, gradient of beta * (v - decayed prediction)
-  float* wDot;    // [chunk][nCG][kDeltaDots][64]: sums over the group's columns
+  float* wDot;    // [chunk][nCG][64]: sums of dR o V over the group's columns
 };
 
 constexpr int delta_dk_pad(int dk) { return dk <= 64 ? 64 : 128; }

@@ -63,6 +63,16 @@ struct Frag {
   u32x4 t[N];
 };
 
+// The lane, as a value that the compiler cannot see through: addresses derived from it are
+// formed anew where they are used. Left alone, it hoists every lane-dependent LDS and memory
+// offset of a chunk's work out of the loop over chunks, and the registers that hold them over
+// all of it push the work's own values out.
+__device__ __forceinline__ int fresh_lane() {
+  int l = int(threadIdx.x & 63);
+  asm volatile("" : "+v"(l));
+  return l;
+}
+
 // Keeps the scheduler from moving anything across: products are written with the next
 // fragments' LDS reads ahead of the current ones' matrix instructions, and left alone the
 // scheduler sinks every read to its use (read, wait 130 cycles, 3 matrix instructions, ...).
@@ -129,9 +139,8 @@ __device__ __forceinline__ constexpr int place(int c) {
 // Left operand of tile row0 .. row0+15: contraction over columns col0 .. col0+31. Planes
 // (terms) lie `plane` elements apart.
 template <int N>
-__device__ __forceinline__ Frag<N> rowfrag(const uint16_t* m, int ld, int plane, int row0, int col0) {
-  const int lane = threadIdx.x & 63;
-  const uint16_t* p = m + (row0 + (lane & 15)) * ld + col0 + 8 * (lane >> 4);
+__device__ __forceinline__ Frag<N> rowfrag(const uint16_t* m, int ld, int plane, int row0, int col0, int ln) {
+  const uint16_t* p = m + (row0 + (ln & 15)) * ld + col0 + 8 * (ln >> 4);
   Frag<N> f;
 #pragma unroll
   for (int n = 0; n < N; ++n) f.t[n] = *reinterpret_cast<const u32x4*>(p + n * plane);
@@ -143,9 +152,8 @@ __device__ __forceinline__ Frag<N> rowfrag(const uint16_t* m, int ld, int plane,
 // lanes i / 4 + 4e loaded, so lane j loads row 4q + j / 4, columns 4 (j % 4) .. + 3 of the
 // tile. PLAIN: the matrix' columns are in their own order.
 template <int N, bool PLAIN = false>
-__device__ __forceinline__ Frag<N> colfrag(const uint16_t* m, int ld, int plane, int row0, int col0) {
-  const int lane = threadIdx.x & 63;
-  const int q = lane >> 4, j = lane & 15;
+__device__ __forceinline__ Frag<N> colfrag(const uint16_t* m, int ld, int plane, int row0, int col0, int ln) {
+  const int q = ln >> 4, j = ln & 15;
   const int c = PLAIN ? col0 + 4 * (j & 3) : place(col0) + 8 * (j & 3);
   const uint16_t* p = m + (row0 + 4 * q + (j >> 2)) * ld + c;
   Frag<N> f;
@@ -164,7 +172,7 @@ __device__ __forceinline__ Frag<N> colfrag(const uint16_t* m, int ld, int plane,
 // `next` issues the following product's reads before the last ones.
 template <int L, int KB, int NA, int NB, typename Next>
 __device__ __forceinline__ void row_product(f32x4_t* acc, Frag<NA>* f, const uint16_t* m, int ld, int plane,
-                                            const Frag<NB>* b, Next next) {
+                                            const Frag<NB>* b, Next next, int ln) {
   Frag<NA> g[2][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) g[0][i] = f[i];
@@ -172,7 +180,7 @@ __device__ __forceinline__ void row_product(f32x4_t* acc, Frag<NA>* f, const uin
   for (int kb = 0; kb < KB; ++kb) {
     if (kb + 1 < KB) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) g[(kb + 1) & 1][i] = rowfrag<NA>(m, ld, plane, 16 * i, 32 * (kb + 1));
+      for (int i = 0; i < 4; ++i) g[(kb + 1) & 1][i] = rowfrag<NA>(m, ld, plane, 16 * i, 32 * (kb + 1), ln);
     } else {
       next();
     }
@@ -182,29 +190,29 @@ __device__ __forceinline__ void row_product(f32x4_t* acc, Frag<NA>* f, const uin
   }
 }
 template <int NA>
-__device__ __forceinline__ void row_load(Frag<NA>* f, const uint16_t* m, int ld, int plane) {
+__device__ __forceinline__ void row_load(Frag<NA>* f, const uint16_t* m, int ld, int plane, int ln) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = rowfrag<NA>(m, ld, plane, 16 * i, 0);
+  for (int i = 0; i < 4; ++i) f[i] = rowfrag<NA>(m, ld, plane, 16 * i, 0, ln);
 }
 
 // acc[i] += transposed rows of a [64][16 N] matrix times b: acc[i] takes columns 16i .. 16i+15,
 // contraction over the 64 rows. Four column tiles (independent accumulators) of one 32-row
 // block at a time, the next reads ahead.
 template <int NA>
-__device__ __forceinline__ void col_load(Frag<NA>* f, const uint16_t* m, int ld, int plane, int kb, int i0) {
+__device__ __forceinline__ void col_load(Frag<NA>* f, const uint16_t* m, int ld, int plane, int kb, int i0, int ln) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = colfrag<NA>(m, ld, plane, 32 * kb, 16 * (i0 + i));
+  for (int i = 0; i < 4; ++i) f[i] = colfrag<NA>(m, ld, plane, 32 * kb, 16 * (i0 + i), ln);
 }
 template <int L, int N, int NA, int NB, typename Next>
 __device__ __forceinline__ void col_product(f32x4_t* acc, Frag<NA>* f, const uint16_t* m, int ld, int plane,
-                                            const Frag<NB>* b, Next next) {
+                                            const Frag<NB>* b, Next next, int ln) {
   Frag<NA> g[2][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) g[0][i] = f[i];
 #pragma unroll
   for (int s = 0; s < N / 2; ++s) {  // step s: block s % 2 of tiles 4 (s / 2) ..
     if (s + 1 < N / 2) {
-      col_load<NA>(g[(s + 1) & 1], m, ld, plane, (s + 1) & 1, (s + 1) / 2 * 4);
+      col_load<NA>(g[(s + 1) & 1], m, ld, plane, (s + 1) & 1, (s + 1) / 2 * 4, ln);
     } else {
       next();
     }
@@ -219,28 +227,29 @@ __device__ __forceinline__ void col_product(f32x4_t* acc, Frag<NA>* f, const uin
 // of 32 bytes (16 elements), which puts the 8 rows on the 8 even places.
 constexpr int kPad = 16;
 
-// LDS image of a lower-triangular matrix: rows 0..31 of 48 elements (32 used), rows 32..63 of 80.
-constexpr int kLdA = 32 + kPad, kLdB = 64 + kPad, kTrapLo = 32 * kLdA, kTrapHi = 32 * kLdB;
+// LDS image of a lower-triangular matrix: rows 0..31 of 40 elements (32 used), rows 32..63 of
+// 72 (the full padding would not let two workgroups of the backward scans share a CU's LDS).
+constexpr int kLdA = 32 + 8, kLdB = 64 + 8, kTrapLo = 32 * kLdA, kTrapHi = 32 * kLdB;
 constexpr int kTrapLds = kTrapLo + kTrapHi;
 __device__ __forceinline__ constexpr int trap_off(int i) { return i < 32 ? i * kLdA : kTrapLo + (i - 32) * kLdB; }
 template <int N>
-__device__ __forceinline__ Frag<N> trap_row(const uint16_t* m, int tile, int kb) {  // kb <= tile / 2
-  return tile < 2 ? rowfrag<N>(m, kLdA, kTrapLds, 16 * tile, 0)
-                  : rowfrag<N>(m + kTrapLo, kLdB, kTrapLds, 16 * tile - 32, 32 * kb);
+__device__ __forceinline__ Frag<N> trap_row(const uint16_t* m, int tile, int kb, int ln) {  // kb <= tile / 2
+  return tile < 2 ? rowfrag<N>(m, kLdA, kTrapLds, 16 * tile, 0, ln)
+                  : rowfrag<N>(m + kTrapLo, kLdB, kTrapLds, 16 * tile - 32, 32 * kb, ln);
 }
 template <int N>
-__device__ __forceinline__ Frag<N> trap_col(const uint16_t* m, int tile, int kb) {  // kb >= tile / 2
-  return kb == 0 ? colfrag<N>(m, kLdA, kTrapLds, 0, 16 * tile) : colfrag<N>(m + kTrapLo, kLdB, kTrapLds, 0, 16 * tile);
+__device__ __forceinline__ Frag<N> trap_col(const uint16_t* m, int tile, int kb, int ln) {  // kb >= tile / 2
+  return kb == 0 ? colfrag<N>(m, kLdA, kTrapLds, 0, 16 * tile, ln) : colfrag<N>(m + kTrapLo, kLdB, kTrapLds, 0, 16 * tile, ln);
 }
-// The same for an upper-triangular matrix: rows 0..31 of 80 (64 used), rows 32..63 of 48
+// The same for an upper-triangular matrix: rows 0..31 of 72 (64 used), rows 32..63 of 40
 // (columns 32..63).
 __device__ __forceinline__ constexpr int utrap_off(int i, int j) {
   return i < 32 ? i * kLdB + j : kTrapHi + (i - 32) * kLdA + j - 32;
 }
 template <int N>
-__device__ __forceinline__ Frag<N> utrap_row(const uint16_t* m, int tile, int kb) {  // kb >= tile / 2
-  return tile < 2 ? rowfrag<N>(m, kLdB, kTrapLds, 16 * tile, 32 * kb)
-                  : rowfrag<N>(m + kTrapHi, kLdA, kTrapLds, 16 * tile - 32, 0);
+__device__ __forceinline__ Frag<N> utrap_row(const uint16_t* m, int tile, int kb, int ln) {  // kb >= tile / 2
+  return tile < 2 ? rowfrag<N>(m, kLdB, kTrapLds, 16 * tile, 32 * kb, ln)
+                  : rowfrag<N>(m + kTrapHi, kLdA, kTrapLds, 16 * tile - 32, 0, ln);
 }
 
 // Triangular products over the 64-row contraction, fragments of both blocks at once.
@@ -250,11 +259,11 @@ struct Trap {
 };
 // lower: tiles 0..3 of block 0, tiles 2, 3 of block 1
 template <int N>
-__device__ __forceinline__ void trap_load(Trap<N>& t, const uint16_t* m) {
+__device__ __forceinline__ void trap_load(Trap<N>& t, const uint16_t* m, int ln) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) t.a[i] = trap_row<N>(m, i, 0);
-  t.b[0] = trap_row<N>(m, 2, 1);
-  t.b[1] = trap_row<N>(m, 3, 1);
+  for (int i = 0; i < 4; ++i) t.a[i] = trap_row<N>(m, i, 0, ln);
+  t.b[0] = trap_row<N>(m, 2, 1, ln);
+  t.b[1] = trap_row<N>(m, 3, 1, ln);
 }
 template <int L, int N, int NB>
 __device__ __forceinline__ void trap_product(f32x4_t* acc, const Trap<N>& t, const Frag<NB>* x) {
@@ -263,18 +272,18 @@ __device__ __forceinline__ void trap_product(f32x4_t* acc, const Trap<N>& t, con
 }
 // upper (a transposed lower one, or an upper image): tiles 0..3 of block 1, tiles 0, 1 of block 0
 template <int N>
-__device__ __forceinline__ void trap_load_t(Trap<N>& t, const uint16_t* m) {
+__device__ __forceinline__ void trap_load_t(Trap<N>& t, const uint16_t* m, int ln) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) t.a[i] = trap_col<N>(m, i, 1);
-  t.b[0] = trap_col<N>(m, 0, 0);
-  t.b[1] = trap_col<N>(m, 1, 0);
+  for (int i = 0; i < 4; ++i) t.a[i] = trap_col<N>(m, i, 1, ln);
+  t.b[0] = trap_col<N>(m, 0, 0, ln);
+  t.b[1] = trap_col<N>(m, 1, 0, ln);
 }
 template <int N>
-__device__ __forceinline__ void utrap_load(Trap<N>& t, const uint16_t* m) {
+__device__ __forceinline__ void utrap_load(Trap<N>& t, const uint16_t* m, int ln) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) t.a[i] = utrap_row<N>(m, i, 1);
-  t.b[0] = utrap_row<N>(m, 0, 0);
-  t.b[1] = utrap_row<N>(m, 1, 0);
+  for (int i = 0; i < 4; ++i) t.a[i] = utrap_row<N>(m, i, 1, ln);
+  t.b[0] = utrap_row<N>(m, 0, 0, ln);
+  t.b[1] = utrap_row<N>(m, 1, 0, ln);
 }
 template <int L, int N, int NB>
 __device__ __forceinline__ void utrap_product(f32x4_t* acc, const Trap<N>& t, const Frag<NB>* x) {
@@ -408,20 +417,20 @@ struct Tile {
   Raw8<ET> r[N];
   // `base`: the chunk's first element; rows s1 apart; `rows` valid rows, `cols` valid columns
   // (a multiple of 8 with VEC).
-  __device__ __forceinline__ void load(const ET* base, int64_t s1, int rows, int cols) {
+  __device__ __forceinline__ void load(const ET* base, int64_t s1, int rows, int cols, int tid) {
     const __amdgpu_buffer_rsrc_t rs = chunk_rsrc<ET, VEC>(base, s1, rows, cols);
     constexpr int STEP = NTHR / (DK / 8);
-    const int row = int(threadIdx.x) / (DK / 8), col = int(threadIdx.x) % (DK / 8) * 8;
+    const int row = tid / (DK / 8), col = tid % (DK / 8) * 8;
     const uint32_t pitch = uint32_t(s1) * uint32_t(sizeof(ET));
     const int n = cols - col;
     const uint32_t off = n > 0 ? uint32_t(row) * pitch + uint32_t(col) * uint32_t(sizeof(ET)) : kNowhere;
 #pragma unroll
     for (int i = 0; i < N; ++i) r[i] = load8<ET, VEC>(rs, off + i * STEP * pitch, row + i * STEP < rows ? n : 0);
   }
-  __device__ __forceinline__ void store(uint16_t* m) const {
+  __device__ __forceinline__ void store(uint16_t* m, int tid) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int idx = int(threadIdx.x) + i * NTHR;
+      const int idx = tid + i * NTHR;
       const int row = idx / (DK / 8), col = idx % (DK / 8) * 8;
       const Frag<Store<ET>::NT> f = terms8<ET>(r[i]);
       uint16_t* p = m + row * LD + place(col);  // columns col + 4 .. are 8 places on
@@ -434,22 +443,35 @@ struct Tile {
   }
 };
 
+// Pointers that come out of the parameter block as generic ones, said to be global: a generic
+// ("flat") load also counts as an LDS access, and every LDS wait would wait for it.
+template <typename T>
+using global_t = __attribute__((address_space(1))) T;
+template <typename T>
+__device__ __forceinline__ const global_t<T>* in_global(const void* p) {
+  return (const global_t<T>*)p;
+}
+template <typename T>
+__device__ __forceinline__ global_t<T>* in_global(void* p) {
+  return (global_t<T>*)p;
+}
+
 // T's three planes of a chunk, through registers into the padded LDS image.
 template <int NTHR>
 struct TrapTile {
   static constexpr int TOTAL = 3 * kTrapElems / 8, N = (TOTAL + NTHR - 1) / NTHR;
   u32x4 r[N];
-  __device__ __forceinline__ void load(const uint16_t* src) {
+  __device__ __forceinline__ void load(const uint16_t* src, int tid) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int idx = int(threadIdx.x) + i * NTHR;
-      r[i] = reinterpret_cast<const u32x4*>(src)[min(idx, TOTAL - 1)];
+      const int idx = tid + i * NTHR;
+      r[i] = in_global<u32x4>(src)[min(idx, TOTAL - 1)];
     }
   }
-  __device__ __forceinline__ void store(uint16_t* m) const {
+  __device__ __forceinline__ void store(uint16_t* m, int tid) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int idx = int(threadIdx.x) + i * NTHR;
+      const int idx = tid + i * NTHR;
       if (idx >= TOTAL) continue;
       const int plane = idx / (kTrapElems / 8), e = idx % (kTrapElems / 8);
       const int off = e < 128 ? (e >> 2) * kLdA + (e & 3) * 8 : kTrapLo + ((e - 128) >> 3) * kLdB + (e & 7) * 8;
@@ -469,9 +491,9 @@ __device__ __forceinline__ float gam(float ghi_i, float glo_i, int n_i, float gh
 
 __device__ __forceinline__ f32x4_t ld4(const float* p) { return *reinterpret_cast<const f32x4_t*>(p); }
 // A per-token array's values at this lane's rows 16 mt + 4 q .. + 3.
-__device__ __forceinline__ void tok_load(f32x4_t* x, const float* arr) {
+__device__ __forceinline__ void tok_load(f32x4_t* x, const float* arr, int ln) {
 #pragma unroll
-  for (int mt = 0; mt < 4; ++mt) x[mt] = ld4(arr + 16 * mt + 4 * ((threadIdx.x & 63) >> 4));
+  for (int mt = 0; mt < 4; ++mt) x[mt] = ld4(arr + 16 * mt + 4 * (ln >> 4));
 }
 __device__ __forceinline__ f32x4_t zero4() { return f32x4_t{0.f, 0.f, 0.f, 0.f}; }
 
@@ -511,7 +533,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
   float* sT = reinterpret_cast<float*>(lds + L::T);
   float* tok = reinterpret_cast<float*>(lds + L::TOK);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int q = lane >> 4, n16 = lane & 15;
+  const int q = lane >> 4, n16 = lane & 15, ln = lane;
   const int64_t ci = blockIdx.x;
   const int c = int(ci % p.nC);
   const int hv = int(ci / p.nC % p.Hv);
@@ -520,7 +542,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
   const int t0 = c * C, rows = min(C, p.T - t0);
 
   TK tk;
-  tk.load(static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2 + t0 * p.ks1, p.ks1, rows, p.dkn);
+  tk.load(static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2 + t0 * p.ks1, p.ks1, rows, p.dkn, tid);
   auto norms = [&](const TK& t, float* out) {
 #pragma unroll
     for (int i = 0; i < TK::N; ++i) {
@@ -536,10 +558,10 @@ __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
     }
   };
   norms(tk, tok + kTokRk * C);
-  tk.store(sK);
+  tk.store(sK, tid);
   {
     TK tq;
-    tq.load(static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2 + t0 * p.qs1, p.qs1, rows, p.dkn);
+    tq.load(static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2 + t0 * p.qs1, p.qs1, rows, p.dkn, tid);
     norms(tq, tok + kTokRq * C);
   }
   if (wave == 0) {
@@ -584,8 +606,8 @@ __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
     f32x4_t acc = zero4();
 #pragma unroll
     for (int kb = 0; kb < DK / 32; ++kb) {
-      const auto fa = rowfrag<Store<ET>::NT>(sK, TK::LD, TK::PLANE, 16 * ti, 32 * kb);
-      const auto fb = rowfrag<Store<ET>::NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb);
+      const auto fa = rowfrag<Store<ET>::NT>(sK, TK::LD, TK::PLANE, 16 * ti, 32 * kb, ln);
+      const auto fb = rowfrag<Store<ET>::NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb, ln);
       mma<2>(acc, fa, fb);
     }
     const int j = 16 * tj + n16;
@@ -676,8 +698,8 @@ __device__ __forceinline__ int delta_cols(const DeltaParams& p, int nw) { return
 // The 16 values of a wave's column in a chunk: token 16 mt + 4 q + r in v[4 mt + r].
 // `base`: the chunk's first element, `rows` its tokens, `cols` the head's width.
 template <typename ET, bool VEC>
-__device__ __forceinline__ void load_cols(float* v, const ET* base, int64_t s1, int rows, int col, int cols) {
-  const int q = (threadIdx.x & 63) >> 4;
+__device__ __forceinline__ void load_cols(float* v, const ET* base, int64_t s1, int rows, int col, int cols, int ln) {
+  const int q = ln >> 4;
   const __amdgpu_buffer_rsrc_t rs = chunk_rsrc<ET, VEC>(base, s1, rows, cols);
   const uint32_t pitch = uint32_t(s1) * uint32_t(sizeof(ET));
   const uint32_t o0 = col < cols ? 4u * q * pitch + uint32_t(col) * uint32_t(sizeof(ET)) : kNowhere;
@@ -689,8 +711,8 @@ __device__ __forceinline__ void load_cols(float* v, const ET* base, int64_t s1, 
   }
 }
 template <typename ET, bool VEC>
-__device__ __forceinline__ void store_cols(const f32x4_t* v, ET* base, int64_t s1, int rows, int col, int cols) {
-  const int q = (threadIdx.x & 63) >> 4;
+__device__ __forceinline__ void store_cols(const f32x4_t* v, ET* base, int64_t s1, int rows, int col, int cols, int ln) {
+  const int q = ln >> 4;
   const __amdgpu_buffer_rsrc_t rs = chunk_rsrc<ET, VEC>(base, s1, rows, cols);
   const uint32_t pitch = uint32_t(s1) * uint32_t(sizeof(ET));
   const uint32_t o0 = col < cols ? 4u * q * pitch + uint32_t(col) * uint32_t(sizeof(ET)) : kNowhere;
@@ -704,60 +726,52 @@ __device__ __forceinline__ void store_cols(const f32x4_t* v, ET* base, int64_t s
 
 // State rows 16 i + 4 q + r of a column, from and to [dk][dv] float32.
 template <int DK>
-__device__ __forceinline__ void load_state(f32x4_t* S, const float* src, int64_t s2, int dkn, int col, bool ok) {
-  const int q = (threadIdx.x & 63) >> 4;
+__device__ __forceinline__ void load_state(f32x4_t* S, const float* src, int64_t s2, int dkn, int col, bool ok, int ln) {
+  const int q = ln >> 4;
 #pragma unroll
   for (int i = 0; i < DK / 16; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 16 * i + 4 * q + r;
-      S[i][r] = (src != nullptr && ok && row < dkn) ? src[row * s2 + col] : 0.f;
+      S[i][r] = (src != nullptr && ok && row < dkn) ? in_global<float>(src)[row * s2 + col] : 0.f;
     }
 }
 template <int DK>
-__device__ __forceinline__ void store_state(const f32x4_t* S, float* dst, int64_t s2, int dkn, int col, bool ok) {
-  const int q = (threadIdx.x & 63) >> 4;
+__device__ __forceinline__ void store_state(const f32x4_t* S, float* dst, int64_t s2, int dkn, int col, bool ok, int ln) {
+  const int q = ln >> 4;
   if (dst == nullptr || !ok) return;
 #pragma unroll
   for (int i = 0; i < DK / 16; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 16 * i + 4 * q + r;
-      if (row < dkn) dst[row * s2 + col] = S[i][r];
+      if (row < dkn) in_global<float>(static_cast<void*>(dst))[row * s2 + col] = S[i][r];
     }
 }
 
 // Images of a wave's [rows x 16] matrix in fragment order: 32 bytes per lane and 32 rows.
 template <int N>
-__device__ __forceinline__ void store_image(const f32x4_t* x, float* dst) {
-  f32x4_t* d = reinterpret_cast<f32x4_t*>(dst) + 2 * (threadIdx.x & 63);
+__device__ __forceinline__ void store_image(const f32x4_t* x, float* dst, int ln) {
+  auto* d = in_global<f32x4_t>(static_cast<void*>(dst)) + 2 * ln;
 #pragma unroll
   for (int i = 0; i < N; ++i) d[128 * (i >> 1) + (i & 1)] = x[i];
 }
-template <int N>
-__device__ __forceinline__ void load_image(f32x4_t* x, const float* src) {
-  const f32x4_t* d = reinterpret_cast<const f32x4_t*>(src) + 2 * (threadIdx.x & 63);
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = d[128 * (i >> 1) + (i & 1)];
-}
-
-// STATES: only carries the state and stores it before each chunk (for the backward).
+// STATES: only carries the state, storing it before each chunk, and u (for the backward).
 template <typename ET, int DK, int NW, bool STATES, bool VEC>
-__global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) {
+__device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint32_t bid) {
   using L = ScanLds<ET, DK, STATES>;
   constexpr int NT = L::NT, NP = L::NP, NTHR = 64 * NW, KB = DK / 32;
   using TK = Tile<ET, DK, NTHR, VEC>;
   static_assert(L::BYTES <= kLdsBytes, "LDS of a CU");
-  extern __shared__ __align__(16) char lds[];
   uint16_t* sK = reinterpret_cast<uint16_t*>(lds + L::K);
   uint16_t* sQ = reinterpret_cast<uint16_t*>(lds + L::Q);
   uint16_t* sT = reinterpret_cast<uint16_t*>(lds + L::T);
   uint16_t* sP = reinterpret_cast<uint16_t*>(lds + L::P);
   float* tok = reinterpret_cast<float*>(lds + L::TOK);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int q = lane >> 4, n16 = lane & 15;
+  const int n16 = lane & 15;
+  const int q = lane >> 4, ln = lane;
   const int ncb = delta_cols(p, NW);
-  const uint32_t bid = xcd_logical_block(blockIdx.x, gridDim.x);
   const int cg = int(bid % ncb) * NW + wave;
   const int64_t bh = bid / ncb;
   const int hv = int(bh % p.Hv), b = int(bh / p.Hv), hk = hv / p.group;
@@ -769,7 +783,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
   ET* obase = STATES ? nullptr : static_cast<ET*>(p.out) + b * p.os0 + hv * p.os2;
 
   f32x4_t S[DK / 16];
-  load_state<DK>(S, p.state_in == nullptr ? nullptr : p.state_in + b * p.sis0 + hv * p.sis1, p.sis2, p.dkn, col, ok);
+  load_state<DK>(S, p.state_in == nullptr ? nullptr : p.state_in + b * p.sis0 + hv * p.sis1, p.sis2, p.dkn, col, ok, ln);
 
   if constexpr (!STATES) {
     // the tiles above the diagonal that a 32-wide contraction block still reads
@@ -783,29 +797,29 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
   TK tk, tq;
   TrapTile<NTHR> tt;
   f32x4_t ttok[(kTokArrays * C / 4 + NTHR - 1) / NTHR];
-  auto fetch = [&](int c) {
+  auto fetch = [&](int c, int tid) {
     const int64_t t0 = int64_t(c) * C;
     const int rows = min(C, p.T - int(t0));
-    tk.load(kbase + t0 * p.ks1, p.ks1, rows, p.dkn);
-    if constexpr (!STATES) tq.load(qbase + t0 * p.qs1, p.qs1, rows, p.dkn);
-    tt.load(p.wT + (bh * p.nC + c) * (3 * kTrapElems));
-    const f32x4_t* w = reinterpret_cast<const f32x4_t*>(p.wTok + (bh * p.nC + c) * (kTokArrays * C));
+    tk.load(kbase + t0 * p.ks1, p.ks1, rows, p.dkn, tid);
+    if constexpr (!STATES) tq.load(qbase + t0 * p.qs1, p.qs1, rows, p.dkn, tid);
+    tt.load(p.wT + (bh * p.nC + c) * (3 * kTrapElems), tid);
+    const auto* w = in_global<f32x4_t>(p.wTok + (bh * p.nC + c) * (kTokArrays * C));
 #pragma unroll
     for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i) ttok[i] = w[min(tid + i * NTHR, kTokArrays * C / 4 - 1)];
   };
-  if (p.nC > 0) fetch(0);
+  if (p.nC > 0) fetch(0, tid);
   for (int c = 0; c < p.nC; ++c) {
     __syncthreads();  // every wave is done with the previous chunk's tiles
-    tk.store(sK);
-    if constexpr (!STATES) tq.store(sQ);
-    tt.store(sT);
+    tk.store(sK, tid);
+    if constexpr (!STATES) tq.store(sQ, tid);
+    tt.store(sT, tid);
 #pragma unroll
     for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i)
       if (tid + i * NTHR < kTokArrays * C / 4) reinterpret_cast<f32x4_t*>(tok)[tid + i * NTHR] = ttok[i];
     float v[16];
     {
       const int64_t t0 = int64_t(c) * C;
-      load_cols<ET, VEC>(v, vbase + t0 * p.vs1, p.vs1, min(C, p.T - int(t0)), col, p.dvn);
+      load_cols<ET, VEC>(v, vbase + t0 * p.vs1, p.vs1, min(C, p.T - int(t0)), col, p.dvn, ln);
     }
     __syncthreads();
 
@@ -821,8 +835,8 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
           Frag<NT> fj[KB], fi[KB];
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb) {
-            fj[kb] = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb);
-            fi[kb] = rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb);
+            fj[kb] = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb, ln);
+            fi[kb] = rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb, ln);
           }
           const int i = 16 * ti + n16, j0 = 16 * tj + 4 * q;
           const float gh = tok[kTokGhi * C + i], gl = tok[kTokGlo * C + i], rqi = tok[kTokRq * C + i] * p.scale;
@@ -843,7 +857,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
         }
       }
     } else if (cg < p.nCG) {
-      store_image<DK / 16>(S, p.wS + ((bh * p.nC + c) * p.nCG + cg) * (DK * 16));
+      store_image<DK / 16>(S, p.wS + ((bh * p.nC + c) * p.nCG + cg) * (DK * 16), ln);
     }
 
     f32x4_t z[4] = {zero4(), zero4(), zero4(), zero4()};  // beta (v - E K S0)
@@ -851,16 +865,16 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
     {
       Frag<NT> fk[4];
       f32x4_t te[4], tr[4], tb[4];
-      row_load<NT>(fk, sK, TK::LD, TK::PLANE);
+      row_load<NT>(fk, sK, TK::LD, TK::PLANE, ln);
       Frag<3> sf[KB];
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(S[2 * kb], S[2 * kb + 1]);
       row_product<2, KB>(z, fk, sK, TK::LD, TK::PLANE, sf, [&] {
-        if constexpr (!STATES) row_load<NT>(fk, sQ, TK::LD, TK::PLANE);
-        tok_load(te, tok + kTokE * C);
-        tok_load(tr, tok + kTokRk * C);
-        tok_load(tb, tok + kTokBeta * C);
-      });
+        if constexpr (!STATES) row_load<NT>(fk, sQ, TK::LD, TK::PLANE, ln);
+        tok_load(te, tok + kTokE * C, ln);
+        tok_load(tr, tok + kTokRk * C, ln);
+        tok_load(tb, tok + kTokBeta * C, ln);
+      }, ln);
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
@@ -871,7 +885,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
           for (int n = 0; n < NP; ++n) so[kb].t[n] = sf[kb].t[n];
-        row_product<NP - 1, KB>(o, fk, sQ, TK::LD, TK::PLANE, so, [&] { tok_load(tr, tok + kTokRq * C); });
+        row_product<NP - 1, KB>(o, fk, sQ, TK::LD, TK::PLANE, so, [&] { tok_load(tr, tok + kTokRq * C, ln); }, ln);
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) o[mt] *= te[mt] * tr[mt] * p.scale;
       }
@@ -881,39 +895,48 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
     f32x4_t td[4], trk[4];
     {
       Trap<3> ft;
-      trap_load(ft, sT);
+      trap_load(ft, sT, ln);
       const Frag<3> zf[2] = {split8<3>(z[0], z[1]), split8<3>(z[2], z[3])};
-      tok_load(td, tok + kTokD * C);
-      tok_load(trk, tok + kTokRk * C);
+      tok_load(td, tok + kTokD * C, ln);
+      tok_load(trk, tok + kTokRk * C, ln);
       DELTA_FENCE();
       trap_product<2>(u, ft, zf);
       DELTA_FENCE();
     }
-    if (c + 1 < p.nC) fetch(c + 1);
+    if constexpr (STATES) {
+      if (cg < p.nCG) store_image<4>(u, p.wU + ((bh * p.nC + c) * p.nCG + cg) * (C * kDeltaCols), ln);
+    }
+    if (c + 1 < p.nC) fetch(c + 1, wave * 64 + ln);
     {
       Frag<NT> fc[4];
-      col_load<NT>(fc, sK, TK::LD, TK::PLANE, 0, 0);
+      col_load<NT>(fc, sK, TK::LD, TK::PLANE, 0, 0, ln);
       f32x4_t d[4];
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) d[mt] = u[mt] * td[mt] * trk[mt];
       const Frag<3> df[2] = {split8<3>(d[0], d[1]), split8<3>(d[2], d[3])};
 #pragma unroll
       for (int i = 0; i < DK / 16; ++i) S[i] *= gamma;
-      col_product<2, DK / 16>(S, fc, sK, TK::LD, TK::PLANE, df, [] {});
+      col_product<2, DK / 16>(S, fc, sK, TK::LD, TK::PLANE, df, [] {}, ln);
     }
     if constexpr (!STATES) {
       const Frag<NP> uf[2] = {split8<NP>(u[0], u[1]), split8<NP>(u[2], u[3])};
       __syncthreads();  // P is complete
       Trap<NP> fp;
-      trap_load(fp, sP);
+      trap_load(fp, sP, ln);
       DELTA_FENCE();
       trap_product<NP - 1>(o, fp, uf);
       const int64_t t0 = int64_t(c) * C;
-      store_cols<ET, VEC>(o, obase + t0 * p.os1, p.os1, min(C, p.T - int(t0)), col, p.dvn);
+      store_cols<ET, VEC>(o, obase + t0 * p.os1, p.os1, min(C, p.T - int(t0)), col, p.dvn, ln);
     }
   }
   if constexpr (!STATES)
-    store_state<DK>(S, p.state_out == nullptr ? nullptr : p.state_out + b * p.sos0 + hv * p.sos1, p.sos2, p.dkn, col, ok);
+    store_state<DK>(S, p.state_out == nullptr ? nullptr : p.state_out + b * p.sos0 + hv * p.sos1, p.sos2, p.dkn, col, ok, ln);
+}
+
+template <typename ET, int DK, int NW, bool VEC>
+__global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) {
+  extern __shared__ __align__(16) char lds[];
+  delta_scan<ET, DK, NW, false, VEC>(p, lds, xcd_logical_block(blockIdx.x, gridDim.x));
 }
 
 // ---------------------------------------------------------------------------------
@@ -923,12 +946,11 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) 
 // With dS1 the gradient of the state after the chunk and dO that of the outputs:
 //   dU  = P^T dO + D (K dS1),   dR = T^T dU,   dV = dZ = beta dR,
 //   dS0 = gamma dS1 + scale Q^T (E dO) - K^T (beta E dR),
-// all of them column by column, like the forward. S0 (stored by the STATES scan) gives back
-// Z = V - E (K S0) and U = T (beta Z). What contracts over value columns (dq, dk, the pair
-// terms of dg and dbeta) is left to k_delta_grad, which gets U, dR and dS1 from here and the
-// sums over a wave's columns of
-//   dO_i.(scale E Q S0)_i,  out_j = U_j.(D K dS1)_j,  dR_i.Z_i,  dZ_i.(E K S0)_i
-// and gamma <S0, dS1>.
+// all of them column by column, like the forward, and without the states: so this scan and the
+// one that carries the states run side by side in one launch, two waves on a SIMD (a lone wave
+// issues an instruction about every 5 cycles, two share the SIMD's issue at half that).
+// Everything that needs both is left to k_delta_grad, which gets U and S0 from the state scan,
+// dR, dS1 and the sums of dR o V over a wave's columns from here.
 
 template <typename ET, int DK>
 struct BackLds {
@@ -952,27 +974,23 @@ __device__ __forceinline__ float sum16(float x) {
 }
 
 template <typename ET, int DK, int NW, bool VEC>
-__global__ __launch_bounds__(64 * NW, 1) void k_delta_back(const DeltaParams p) {
+__device__ __forceinline__ void delta_back(const DeltaParams p, char* lds, uint32_t bid) {
   using L = BackLds<ET, DK>;
   constexpr int NT = L::NT, NTHR = 64 * NW, KB = DK / 32;
   using TK = Tile<ET, DK, NTHR, VEC>;
   static_assert(L::BYTES <= kLdsBytes, "LDS of a CU");
-  extern __shared__ __align__(16) char lds[];
   uint16_t* sK = reinterpret_cast<uint16_t*>(lds + L::K);
   uint16_t* sQ = reinterpret_cast<uint16_t*>(lds + L::Q);
   uint16_t* sT = reinterpret_cast<uint16_t*>(lds + L::T);
   uint16_t* sP = reinterpret_cast<uint16_t*>(lds + L::P);
   float* tok = reinterpret_cast<float*>(lds + L::TOK);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int q = lane >> 4, n16 = lane & 15;
+  int ln = lane;
   const int ncb = delta_cols(p, NW);
-  const uint32_t bid = xcd_logical_block(blockIdx.x, gridDim.x);
   const int cg = int(bid % ncb) * NW + wave;
   const bool live = cg < p.nCG;  // a wave past the last column group still stages tiles
   const int64_t bh = bid / ncb;
   const int hv = int(bh % p.Hv), b = int(bh / p.Hv), hk = hv / p.group;
-  const int col = cg * kDeltaCols + n16;
-  const bool ok = col < p.dvn;
   const ET* kbase = static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2;
   const ET* qbase = static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2;
   const ET* vbase = static_cast<const ET*>(p.v) + b * p.vs0 + hv * p.vs2;
@@ -980,8 +998,11 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_back(const DeltaParams p) 
   ET* dvbase = static_cast<ET*>(p.dv) + b * p.dvs0 + hv * p.dvs2;
 
   f32x4_t dS[DK / 16];
-  load_state<DK>(dS, p.dstate_out == nullptr ? nullptr : p.dstate_out + b * p.dsos0 + hv * p.dsos1, p.dsos2, p.dkn, col,
-                 ok);
+  {
+    const int col = cg * kDeltaCols + (lane & 15);
+    load_state<DK>(dS, p.dstate_out == nullptr ? nullptr : p.dstate_out + b * p.dsos0 + hv * p.dsos1, p.dsos2, p.dkn, col,
+                   col < p.dvn, ln);
+  }
   // the tiles below the diagonal of P^T that a 32-wide contraction block still reads
   for (int e = tid; e < 3 * 128; e += NTHR) {
     const int n = e >> 7, row = (e >> 2) & 31, part = e & 3;
@@ -992,34 +1013,34 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_back(const DeltaParams p) 
   TK tk, tq;
   TrapTile<NTHR> tt;
   f32x4_t ttok[(kTokArrays * C / 4 + NTHR - 1) / NTHR];
-  auto fetch = [&](int c) {
+  auto fetch = [&](int c, int tid) {
     const int64_t t0 = int64_t(c) * C;
     const int rows = min(C, p.T - int(t0));
-    tk.load(kbase + t0 * p.ks1, p.ks1, rows, p.dkn);
-    tq.load(qbase + t0 * p.qs1, p.qs1, rows, p.dkn);
-    tt.load(p.wT + (bh * p.nC + c) * (3 * kTrapElems));
-    const f32x4_t* w = reinterpret_cast<const f32x4_t*>(p.wTok + (bh * p.nC + c) * (kTokArrays * C));
+    tk.load(kbase + t0 * p.ks1, p.ks1, rows, p.dkn, tid);
+    tq.load(qbase + t0 * p.qs1, p.qs1, rows, p.dkn, tid);
+    tt.load(p.wT + (bh * p.nC + c) * (3 * kTrapElems), tid);
+    const auto* w = in_global<f32x4_t>(p.wTok + (bh * p.nC + c) * (kTokArrays * C));
 #pragma unroll
     for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i) ttok[i] = w[min(tid + i * NTHR, kTokArrays * C / 4 - 1)];
   };
-  fetch(p.nC - 1);
+  fetch(p.nC - 1, tid);
   for (int c = p.nC - 1; c >= 0; --c) {
-    const int64_t ci = bh * p.nC + c;
-    const int64_t cim = ci * p.nCG + (live ? cg : 0);
+    ln = fresh_lane();
+    const int tid = wave * 64 + ln, q = ln >> 4, n16 = ln & 15;
+    const int col = cg * kDeltaCols + n16;
+    const int64_t cim = (bh * p.nC + c) * p.nCG + (live ? cg : 0);
     __syncthreads();  // every wave is done with the previous chunk's tiles
-    tk.store(sK);
-    tq.store(sQ);
-    tt.store(sT);
+    tk.store(sK, tid);
+    tq.store(sQ, tid);
+    tt.store(sT, tid);
 #pragma unroll
     for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i)
       if (tid + i * NTHR < kTokArrays * C / 4) reinterpret_cast<f32x4_t*>(tok)[tid + i * NTHR] = ttok[i];
-    f32x4_t S0[DK / 16];
-    load_image<DK / 16>(S0, p.wS + cim * (DK * 16));
     float v[16], dO[16];
     const int64_t t0 = int64_t(c) * C;
     const int rows = min(C, p.T - int(t0));
-    load_cols<ET, VEC>(v, vbase + t0 * p.vs1, p.vs1, rows, col, p.dvn);
-    load_cols<ET, VEC>(dO, dobase + t0 * p.dos1, p.dos1, rows, col, p.dvn);
+    load_cols<ET, VEC>(dO, dobase + t0 * p.dos1, p.dos1, rows, col, p.dvn, ln);
+    load_cols<ET, VEC>(v, vbase + t0 * p.vs1, p.vs1, rows, col, p.dvn, ln);
     __syncthreads();
 
     // P^T: tiles of P = scale Gam o Q K^T (rows i, column j), four neighbours of a row of P^T
@@ -1032,8 +1053,8 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_back(const DeltaParams p) 
         Frag<NT> fj[KB], fi[KB];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-          fi[kb] = rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb);
-          fj[kb] = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb);
+          fi[kb] = rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb, ln);
+          fj[kb] = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb, ln);
         }
         const int j = 16 * tj + n16, i0 = 16 * ti + 4 * q;
         const float gh = tok[kTokGhi * C + j], gl = tok[kTokGlo * C + j], rkj = tok[kTokRk * C + j] * p.scale;
@@ -1054,152 +1075,115 @@ __global__ __launch_bounds__(64 * NW, 1) void k_delta_back(const DeltaParams p) 
       }
     }
 
+    ln = fresh_lane();
     const float gamma = tok[kTokE * C + C - 1];
-    float* dot = p.wDot + cim * (kDeltaDots * C);
-    f32x4_t KdS[4] = {zero4(), zero4(), zero4(), zero4()};  // D (K dS1)
-    f32x4_t KS[4] = {zero4(), zero4(), zero4(), zero4()};   // E (K S0)
+    f32x4_t dU[4] = {zero4(), zero4(), zero4(), zero4()};  // D (K dS1), then dU
     f32x4_t ta[4], tb[4];  // token factors, read anew where they are used: registers are scarce here
     {
       Frag<NT> fk[4];
-      row_load<NT>(fk, sK, TK::LD, TK::PLANE);
-      if (live) store_image<DK / 16>(dS, p.wdS + cim * (DK * 16));
-      float h = 0.f;  // <S0, dS1>
-#pragma unroll
-      for (int i = 0; i < DK / 16; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) h += S0[i][r] * dS[i][r];
-      h = sum16(h);
-      h += __shfl_xor(h, 16);
-      h += __shfl_xor(h, 32);
-      if (live && lane == 0) dot[4 * C] = gamma * h;
+      row_load<NT>(fk, sK, TK::LD, TK::PLANE, ln);
+      if (live) store_image<DK / 16>(dS, p.wdS + cim * (DK * 16), ln);
       Frag<3> sf[KB];
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(dS[2 * kb], dS[2 * kb + 1]);
-      row_product<2, KB>(KdS, fk, sK, TK::LD, TK::PLANE, sf, [&] {
-        row_load<NT>(fk, sK, TK::LD, TK::PLANE);
-        tok_load(ta, tok + kTokD * C);
-        tok_load(tb, tok + kTokRk * C);
-      });
+      row_product<2, KB>(dU, fk, sK, TK::LD, TK::PLANE, sf, [&] {
+        tok_load(ta, tok + kTokD * C, ln);
+        tok_load(tb, tok + kTokRk * C, ln);
+      }, ln);
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) KdS[mt] *= ta[mt] * tb[mt];
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(S0[2 * kb], S0[2 * kb + 1]);
-      row_product<2, KB>(KS, fk, sK, TK::LD, TK::PLANE, sf, [&] {
-        row_load<NT>(fk, sQ, TK::LD, TK::PLANE);
-        tok_load(ta, tok + kTokE * C);
-      });
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) KS[mt] *= ta[mt] * tb[mt];
-      f32x4_t QS[4] = {zero4(), zero4(), zero4(), zero4()};
-      row_product<2, KB>(QS, fk, sQ, TK::LD, TK::PLANE, sf, [&] { tok_load(tb, tok + kTokRq * C); });
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        f32x4_t x;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = sum16(dO[4 * mt + r] * (QS[mt][r] * ta[mt][r] * tb[mt][r] * p.scale));
-        if (live && n16 == 0) *reinterpret_cast<f32x4_t*>(dot + 16 * mt + 4 * q) = x;
-      }
-    }
-    f32x4_t z[4];
-    {
-      f32x4_t u[4] = {zero4(), zero4(), zero4(), zero4()};
-      Trap<3> ft;
-      tok_load(tb, tok + kTokBeta * C);
-      trap_load(ft, sT);
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) z[mt][r] = v[4 * mt + r] - KS[mt][r];
-      const Frag<3> zf[2] = {split8<3>(z[0] * tb[0], z[1] * tb[1]), split8<3>(z[2] * tb[2], z[3] * tb[3])};
-      DELTA_FENCE();
-      trap_product<2>(u, ft, zf);
-      if (live) store_image<4>(u, p.wU + cim * (C * kDeltaCols));
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
-        f32x4_t x;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = sum16(KdS[mt][r] * u[mt][r]);
-        if (live && n16 == 0) *reinterpret_cast<f32x4_t*>(dot + C + 16 * mt + 4 * q) = x;
-      }
+      for (int mt = 0; mt < 4; ++mt) dU[mt] *= ta[mt] * tb[mt];
     }
     __syncthreads();  // P^T is complete
+    ln = fresh_lane();
     f32x4_t dR[4] = {zero4(), zero4(), zero4(), zero4()};
     {
       Trap<3> ft;
-      utrap_load(ft, sP);
+      utrap_load(ft, sP, ln);
       const Frag<NT> of[2] = {split8<NT>(f32x4_t{dO[0], dO[1], dO[2], dO[3]}, f32x4_t{dO[4], dO[5], dO[6], dO[7]}),
                               split8<NT>(f32x4_t{dO[8], dO[9], dO[10], dO[11]}, f32x4_t{dO[12], dO[13], dO[14], dO[15]})};
       DELTA_FENCE();
-      utrap_product<2>(KdS, ft, of);  // dU
+      utrap_product<2>(dU, ft, of);
       DELTA_FENCE();
-      trap_load_t(ft, sT);
-      const Frag<3> uf[2] = {split8<3>(KdS[0], KdS[1]), split8<3>(KdS[2], KdS[3])};
+      trap_load_t(ft, sT, ln);
+      const Frag<3> uf[2] = {split8<3>(dU[0], dU[1]), split8<3>(dU[2], dU[3])};
       DELTA_FENCE();
       utrap_product<2>(dR, ft, uf);
-      tok_load(ta, tok + kTokE * C);
-      tok_load(tb, tok + kTokBeta * C);
+      tok_load(ta, tok + kTokE * C, ln);
+      tok_load(tb, tok + kTokBeta * C, ln);
       DELTA_FENCE();
     }
-    if (live) store_image<4>(dR, p.wR + cim * (C * kDeltaCols));
-    if (c > 0) fetch(c - 1);
+    ln = fresh_lane();
+    if (live) store_image<4>(dR, p.wR + cim * (C * kDeltaCols), ln);
+    if (c > 0) fetch(c - 1, wave * 64 + ln);
     {
       Frag<NT> fc[4];
-      col_load<NT>(fc, sK, TK::LD, TK::PLANE, 0, 0);
+      col_load<NT>(fc, sK, TK::LD, TK::PLANE, 0, 0, ln);
       f32x4_t dz[4], tc[4];
-      tok_load(tc, tok + kTokRk * C);
+      tok_load(tc, tok + kTokRk * C, ln);
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
-        f32x4_t x, y;
-        dz[mt] = dR[mt] * tb[mt];
+        f32x4_t x;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          x[r] = sum16(dR[mt][r] * z[mt][r]);
-          y[r] = sum16(dz[mt][r] * KS[mt][r]);
-        }
-        if (live && n16 == 0) {
-          *reinterpret_cast<f32x4_t*>(dot + 2 * C + 16 * mt + 4 * q) = x;
-          *reinterpret_cast<f32x4_t*>(dot + 3 * C + 16 * mt + 4 * q) = y;
-        }
+        for (int r = 0; r < 4; ++r) x[r] = sum16(dR[mt][r] * v[4 * mt + r]);
+        if (live && (ln & 15) == 0) *in_global<f32x4_t>(static_cast<void*>(p.wDot + cim * C + 16 * mt + 4 * (ln >> 4))) = x;
+        dz[mt] = dR[mt] * tb[mt];
       }
-      store_cols<ET, VEC>(dz, dvbase + t0 * p.dvs1, p.dvs1, rows, col, p.dvn);
+      store_cols<ET, VEC>(dz, dvbase + t0 * p.dvs1, p.dvs1, rows, cg * kDeltaCols + (ln & 15), p.dvn, ln);
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) dz[mt] = -(dz[mt] * ta[mt] * tc[mt]);
       const Frag<3> rf[2] = {split8<3>(dz[0], dz[1]), split8<3>(dz[2], dz[3])};
 #pragma unroll
       for (int i = 0; i < DK / 16; ++i) dS[i] *= gamma;
       col_product<2, DK / 16>(dS, fc, sK, TK::LD, TK::PLANE, rf, [&] {
-        col_load<NT>(fc, sQ, TK::LD, TK::PLANE, 0, 0);
-        tok_load(tc, tok + kTokRq * C);
-      });
+        col_load<NT>(fc, sQ, TK::LD, TK::PLANE, 0, 0, ln);
+        tok_load(tc, tok + kTokRq * C, ln);
+      }, ln);
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
         for (int r = 0; r < 4; ++r) dz[mt][r] = dO[4 * mt + r] * (ta[mt][r] * tc[mt][r] * p.scale);
       const Frag<3> of[2] = {split8<3>(dz[0], dz[1]), split8<3>(dz[2], dz[3])};
-      col_product<2, DK / 16>(dS, fc, sQ, TK::LD, TK::PLANE, of, [] {});
+      col_product<2, DK / 16>(dS, fc, sQ, TK::LD, TK::PLANE, of, [] {}, ln);
     }
   }
-  store_state<DK>(dS, p.dstate == nullptr ? nullptr : p.dstate + b * p.dsis0 + hv * p.dsis1, p.dsis2, p.dkn, col, ok);
+  const int col = cg * kDeltaCols + (ln & 15);
+  store_state<DK>(dS, p.dstate == nullptr ? nullptr : p.dstate + b * p.dsis0 + hv * p.dsis1, p.dsis2, p.dkn, col,
+                  col < p.dvn, ln);
+}
+
+// Both scans of the backward: the first half of the workgroups carries dS, the second S.
+template <typename ET, int DK, int NW, bool VEC>
+__global__ __launch_bounds__(64 * NW, Store<ET>::NT == 1 ? 2 : 1) void k_delta_scans(const DeltaParams p) {
+  extern __shared__ __align__(16) char lds[];
+  const uint32_t half = gridDim.x / 2;
+  if (blockIdx.x < half) {
+    delta_back<ET, DK, NW, VEC>(p, lds, xcd_logical_block(blockIdx.x, half));
+  } else {
+    delta_scan<ET, DK, NW, true, VEC>(p, lds, xcd_logical_block(blockIdx.x - half, half));
+  }
 }
 
 // ---------------------------------------------------------------------------------
 // Backward: dq, dk, dg, dbeta of one chunk and key head
 // ---------------------------------------------------------------------------------
 //
-// Over the value columns (32 at a time, staged from the scan's images):
-//   dP = scale dO U^T,  F = dR U^T  (dA = -F),  dO S0^T,  U dS1^T,  dR S0^T,
+// Over the value columns (32 at a time, staged from the scans' images):
+//   dP = scale dO U^T,  F = dR U^T  (dA = -F),  os = dO S0^T,  rs = dR S0^T,  ug = U dS1^T,
 // then with Y = rq rk Gam o dP (i >= j), Yk = -beta rk rk Gam o F (i > j) and raw q, k:
-//   dq' = rq scale E (dO S0^T) + Y K
-//   dk' = rk (D (U dS1^T) - beta E (dR S0^T)) + Y^T Q + (Yk + Yk^T) K
+//   dq' = rq scale E os + Y K
+//   dk' = rk (D ug - beta E rs) + Y^T Q + (Yk + Yk^T) K
 // are rq dq and rk dk in terms of the normalised rows; the norm's own gradient takes their
 // part along q (k) away: dq = dq' - rq q (rq q.dq'). The decay's gradient adds up all paths
 // that cross a token, dg_t = sum_{i >= t > j} X_ij + sum_{i >= t} into_i + sum_{j < t} out_j
-// + gamma <S0, dS1> with into = dO.(scale E Q S0) - dZ.(E K S0), X = Y o Q K^T + Yk o K K^T, from row and column sums of the same
-// products, so that pairs on one side of t cancel exactly; the cumulative sums are in 64 bits.
+// + gamma <S0, dS1> with X = Y o Q K^T + Yk o K K^T, from row and column sums of the same
+// products, so that pairs on one side of t cancel exactly, into = rq scale E (q.os) - beta E
+// rk (k.rs) and out = D rk (k.ug); the cumulative sums are in 64 bits. dbeta_i = dR_i.V_i -
+// E rk (k.rs)_i + sum_j dA_ij Gam k.k. What reaches dg keeps all terms (float32).
 
 template <typename ET, int DK>
 struct GradLds {
   static constexpr int NT = Store<ET>::NT, NP = Store<ET>::NP;
+  static constexpr int NW = DK / 16;  // waves: one 16-wide tile of key columns each
   static constexpr int ULD = C + kPad, OLD = 32 + kPad, SLD = DK + kPad;
   static constexpr int UPL = 32 * ULD, OPL = C * OLD, SPL = 32 * SLD;
   // first part: staged operands of 32 value columns
@@ -1207,7 +1191,7 @@ struct GradLds {
   static constexpr int R = U + 3 * UPL * 2;
   static constexpr int O = R + 3 * UPL * 2;
   static constexpr int S = O + NT * OPL * 2;
-  static constexpr int END1 = S + NP * SPL * 2;
+  static constexpr int END1 = S + 3 * SPL * 2;
   // second part, in the same place
   static constexpr int K = 0;
   static constexpr int Q = K + NT * Tile<ET, DK, 64, true>::PLANE * 2;
@@ -1215,35 +1199,45 @@ struct GradLds {
   static constexpr int YK = Y + NP * kTrapLds * 2;
   static constexpr int END2 = YK + NP * kTrapLds * 2;
   static constexpr int TOK = END1 > END2 ? END1 : END2;
-  static constexpr int SUM = TOK + kTokArrays * C * 4;  // row, column and beta sums [3][4][64]
-  static constexpr int BYTES = SUM + 3 * 4 * C * 4;
+  static constexpr int SUM = TOK + kTokArrays * C * 4;  // per-wave sums [3][NW][64] and <S0, dS1> [NW]
+  static constexpr int BYTES = SUM + 3 * NW * C * 4 + NW * 4;
 };
 
-// Image of 16 columns (NB blocks of 32 indices) through registers into rows of a
-// [columns][index] LDS matrix of N terms.
-template <int NB>
+// Images of two 16-column groups (NB blocks of 32 indices each) through registers into the 32
+// rows of a [columns][index] LDS matrix of N terms.
+template <int NB, int NTHR>
 struct ImageTile {
-  static constexpr int N = NB * 128 / 256;
+  static constexpr int N = 2 * NB * 128 / NTHR;
+  static_assert(2 * NB * 128 % NTHR == 0, "whole passes");
   f32x4_t r[N];
-  __device__ __forceinline__ void load(const float* src) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = reinterpret_cast<const f32x4_t*>(src)[threadIdx.x + 256 * i];
-  }
-  template <int NTERM>
-  __device__ __forceinline__ void store(uint16_t* m, int ld, int plane, bool have) const {
+  // `second`: whether the second group exists (it follows the first); if not, zeros.
+  __device__ __forceinline__ void load(const float* src, bool second, int tid) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int e = threadIdx.x + 256 * i, kb = e >> 7, l = (e >> 1) & 63, h = e & 1;
-      put4<NTERM>(m + (l & 15) * ld + 32 * kb + 16 * h + 4 * (l >> 4), plane, have ? r[i] : zero4());
+      const int e = tid + NTHR * i;
+      const bool have = e < NB * 128 || second;
+      const f32x4_t x = in_global<f32x4_t>(src)[have ? e : e - NB * 128];
+      r[i] = have ? x : zero4();
+    }
+  }
+  template <int NTERM>
+  __device__ __forceinline__ void store(uint16_t* m, int ld, int plane, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = tid + NTHR * i, g = e / (NB * 128), f = e % (NB * 128);
+      const int kb = f >> 7, l = (f >> 1) & 63, h = f & 1;
+      put4<NTERM>(m + (16 * g + (l & 15)) * ld + 32 * kb + 16 * h + 4 * (l >> 4), plane, r[i]);
     }
   }
 };
 
-template <typename ET, int DK, bool VEC>
-__global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
+// ONE: a single value head per key head (no sums to carry from head to head).
+template <typename ET, int DK, bool VEC, bool ONE>
+__global__ __launch_bounds__(4 * DK, 2) void k_delta_grad(const DeltaParams p) {
   using L = GradLds<ET, DK>;
-  constexpr int NT = L::NT, NP = L::NP, LV = NP - 1, KB = DK / 32, NN = DK / 64;
-  using TK = Tile<ET, DK, 256, VEC>;
+  constexpr int NT = L::NT, NP = L::NP, LV = NP - 1, KB = DK / 32, NW = L::NW, NTHR = 64 * NW;
+  constexpr int SLOTS = (10 + NW - 1) / NW;  // tiles of a triangle per wave
+  using TK = Tile<ET, DK, NTHR, VEC>;
   static_assert(L::BYTES <= kLdsBytes, "LDS of a CU");
   extern __shared__ __align__(16) char lds[];
   uint16_t* sU = reinterpret_cast<uint16_t*>(lds + L::U);
@@ -1257,59 +1251,71 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
   float* tok = reinterpret_cast<float*>(lds + L::TOK);
   float* sum = reinterpret_cast<float*>(lds + L::SUM);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int q = lane >> 4, n16 = lane & 15;
+  int ln = lane;
   const int64_t id = blockIdx.x;
   const int c = int(id % p.nC);
   const int hk = int(id / p.nC % p.Hk);
   const int b = int(id / p.nC / p.Hk);
   const int t0 = c * C, rows = min(C, p.T - t0);
-  const int dt0 = wave * NN;  // first of this wave's 16-wide tiles of dk columns
+  const int dc = 16 * wave;  // this wave's key columns
 
-  f32x4_t aq[4][NN], ak[4][NN];
+  f32x4_t aq[4], ak[4];
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-    for (int n = 0; n < NN; ++n) aq[mt][n] = ak[mt][n] = zero4();
+aq[mt] = ak[mt] = zero4();
 
-  for (int gh = 0; gh < p.group; ++gh) {
+  auto element = [&](const uint16_t* m, int t, int d) {
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) x += __uint_as_float(uint32_t(m[i * TK::PLANE + t * TK::LD + place(d)]) << 16);
+    return x;
+  };
+  for (int gh = 0; gh < (ONE ? 1 : p.group); ++gh) {
+    ln = fresh_lane();
+    const int tid = wave * 64 + ln, lane = ln, q = ln >> 4, n16 = ln & 15;
     const int hv = hk * p.group + gh;
     const int64_t ci = (int64_t(b) * p.Hv + hv) * p.nC + c;
     const ET* dobase = static_cast<const ET*>(p.dO) + b * p.dos0 + hv * p.dos2 + t0 * p.dos1;
-    f32x4_t dP[3], F[3], os[4][NN], rs[4][NN], ug[4][NN];
+    f32x4_t dP[SLOTS], F[SLOTS];
 #pragma unroll
-    for (int s = 0; s < 3; ++s) dP[s] = F[s] = zero4();
+    for (int s = 0; s < SLOTS; ++s) dP[s] = F[s] = zero4();
+    if (gh > 0) __syncthreads();  // the previous head's factors are read
+    if (tid < kTokArrays * C / 4)
+      reinterpret_cast<f32x4_t*>(tok)[tid] = reinterpret_cast<const f32x4_t*>(p.wTok + ci * (kTokArrays * C))[tid];
+    f32x4_t os[4], rs[4], ug[4];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-      for (int n = 0; n < NN; ++n) os[mt][n] = rs[mt][n] = ug[mt][n] = zero4();
-    {  // everything but U dS1^T
-      ImageTile<2> iu[2], ir[2];
-      ImageTile<KB> is[2];
+os[mt] = rs[mt] = ug[mt] = zero4();
+    float through = 0.f;  // <S0, dS1>
+    {
+      ImageTile<2, NTHR> iu, ir;
+      ImageTile<KB, NTHR> is, ig;
       Raw8<ET> io;
-      auto fetch = [&](int cb) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t cim = ci * p.nCG + min(cb + h, p.nCG - 1);
-          iu[h].load(p.wU + cim * (C * kDeltaCols));
-          ir[h].load(p.wR + cim * (C * kDeltaCols));
-          is[h].load(p.wS + cim * (DK * 16));
-        }
+      auto fetch = [&](int cb, int tid) {
+        const int64_t cim = ci * p.nCG + cb;
+        const bool second = cb + 1 < p.nCG;
+        iu.load(p.wU + cim * (C * kDeltaCols), second, tid);
+        ir.load(p.wR + cim * (C * kDeltaCols), second, tid);
+        is.load(p.wS + cim * (DK * 16), second, tid);
+        ig.load(p.wdS + cim * (DK * 16), second, tid);
         const int row = tid >> 2, c0 = cb * kDeltaCols + (tid & 3) * 8;
         const int n = row < rows ? p.dvn - c0 : 0;
         const uint32_t off = (uint32_t(row) * uint32_t(p.dos1) + uint32_t(c0)) * uint32_t(sizeof(ET));
         io = load8<ET, VEC>(chunk_rsrc<ET, VEC>(dobase, p.dos1, rows, p.dvn), n > 0 ? off : kNowhere, n);
       };
-      fetch(0);
+      fetch(0, tid);
       for (int cb = 0; cb < p.nCG; cb += 2) {
+        ln = fresh_lane();
+        const int tid = wave * 64 + ln;
         __syncthreads();  // the previous contents are read
+        iu.template store<3>(sU, L::ULD, L::UPL, tid);
+        ir.template store<3>(sR, L::ULD, L::UPL, tid);
+        is.template store<3>(sS, L::SLD, L::SPL, tid);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool have = cb + h < p.nCG;
-          iu[h].template store<3>(sU + 16 * h * L::ULD, L::ULD, L::UPL, have);
-          ir[h].template store<3>(sR + 16 * h * L::ULD, L::ULD, L::UPL, have);
-          is[h].template store<NP>(sS + 16 * h * L::SLD, L::SLD, L::SPL, have);
-        }
-        {
+        for (int i = 0; i < ImageTile<KB, NTHR>::N; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) through += is.r[i][e] * ig.r[i][e];
+        if (wave < 4) {  // 64 rows of 4 pieces
           const Frag<NT> f = terms8<ET>(io);
           uint16_t* o = sO + (tid >> 2) * L::OLD + place((tid & 3) * 8);
 #pragma unroll
@@ -1319,104 +1325,120 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
           }
         }
         __syncthreads();
-        if (cb + 2 < p.nCG) fetch(cb + 2);
-        Frag<NP> fs[NN];
-        Frag<NT> fo[4];
-        Frag<NP> fr[4];
+        const ImageTile<KB, NTHR> gg = ig;
+        if (cb + 2 < p.nCG) fetch(cb + 2, tid);
+        {
+          const auto fs = colfrag<3, true>(sS, L::SLD, L::SPL, 0, dc, ln);
+          Frag<NT> fo[4];
+          Frag<3> fr[4];
 #pragma unroll
-        for (int n = 0; n < NN; ++n) fs[n] = colfrag<NP, true>(sS, L::SLD, L::SPL, 0, 16 * (dt0 + n));
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-          fo[mt] = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * mt, 0);
-          fr[mt] = colfrag<NP, true>(sR, L::ULD, L::UPL, 0, 16 * mt);
-        }
-        DELTA_FENCE();
-#pragma unroll
-        for (int n = 0; n < NN; ++n) {
-          f32x4_t x[4], y[4];
-#pragma unroll
-          for (int mt = 0; mt < 4; ++mt) x[mt] = os[mt][n], y[mt] = rs[mt][n];
-          mma_tiles<LV, 4>(x, fo, fs[n]);
-          mma_tiles<LV, 4>(y, fr, fs[n]);
-#pragma unroll
-          for (int mt = 0; mt < 4; ++mt) os[mt][n] = x[mt], rs[mt][n] = y[mt];
+          for (int mt = 0; mt < 4; ++mt) {
+            fo[mt] = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * mt, 0, ln);
+            fr[mt] = colfrag<3, true>(sR, L::ULD, L::UPL, 0, 16 * mt, ln);
+          }
+          DELTA_FENCE();
+          mma_tiles<2, 4>(os, fo, fs);
+          mma_tiles<2, 4>(rs, fr, fs);
         }
 #pragma unroll
-        for (int s = 0; s < 3; ++s) {
-          const int t = wave + 4 * s;
+        for (int s = 0; s < SLOTS; ++s) {
+          const int t = wave + NW * s;
           if (t < 10) {
             int ti, tj;
             tile_of(t, ti, tj);
-            const auto fu = colfrag<3, true>(sU, L::ULD, L::UPL, 0, 16 * tj);
-            const auto fo1 = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * ti, 0);
-            const auto fr1 = colfrag<3, true>(sR, L::ULD, L::UPL, 0, 16 * ti);
+            const auto fu = colfrag<3, true>(sU, L::ULD, L::UPL, 0, 16 * tj, ln);
+            const auto fo1 = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * ti, 0, ln);
+            const auto fr1 = colfrag<3, true>(sR, L::ULD, L::UPL, 0, 16 * ti, ln);
             DELTA_FENCE();
             mma<2>(dP[s], fu, fo1);
             mma<2>(F[s], fu, fr1);
           }
         }
-      }
-    }
-    {  // U dS1^T, in a loop of its own: fewer accumulators and less LDS at a time
-      ImageTile<2> iu[2];
-      ImageTile<KB> ig[2];
-      auto fetch = [&](int cb) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t cim = ci * p.nCG + min(cb + h, p.nCG - 1);
-          iu[h].load(p.wU + cim * (C * kDeltaCols));
-          ig[h].load(p.wdS + cim * (DK * 16));
-        }
-      };
-      fetch(0);
-      for (int cb = 0; cb < p.nCG; cb += 2) {
+        __syncthreads();  // S0 is read: dS1 takes its place
+        gg.template store<3>(sS, L::SLD, L::SPL, tid);
         __syncthreads();
+        const auto fg = colfrag<3, true>(sS, L::SLD, L::SPL, 0, dc, ln);
+        Frag<3> fu[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool have = cb + h < p.nCG;
-          iu[h].template store<NP>(sU + 16 * h * L::ULD, L::ULD, L::UPL, have);
-          ig[h].template store<NP>(sS + 16 * h * L::SLD, L::SLD, L::SPL, have);
-        }
-        __syncthreads();
-        if (cb + 2 < p.nCG) fetch(cb + 2);
-        Frag<NP> fg[NN], fu[4];
-#pragma unroll
-        for (int n = 0; n < NN; ++n) fg[n] = colfrag<NP, true>(sS, L::SLD, L::SPL, 0, 16 * (dt0 + n));
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) fu[mt] = colfrag<NP, true>(sU, L::ULD, L::UPL, 0, 16 * mt);
+        for (int mt = 0; mt < 4; ++mt) fu[mt] = colfrag<3, true>(sU, L::ULD, L::UPL, 0, 16 * mt, ln);
         DELTA_FENCE();
-#pragma unroll
-        for (int n = 0; n < NN; ++n) {
-          f32x4_t x[4];
-#pragma unroll
-          for (int mt = 0; mt < 4; ++mt) x[mt] = ug[mt][n];
-          mma_tiles<LV, 4>(x, fu, fg[n]);
-#pragma unroll
-          for (int mt = 0; mt < 4; ++mt) ug[mt][n] = x[mt];
-        }
+        mma_tiles<2, 4>(ug, fu, fg);
       }
     }
+    through = sum16(through);
+    through += __shfl_xor(through, 16);
+    through += __shfl_xor(through, 32);
     __syncthreads();
     {
       TK tk, tq;
-      tk.load(static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2 + t0 * p.ks1, p.ks1, rows, p.dkn);
-      tq.load(static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2 + t0 * p.qs1, p.qs1, rows, p.dkn);
-      if (tid < kTokArrays * C / 4)
-        reinterpret_cast<f32x4_t*>(tok)[tid] = reinterpret_cast<const f32x4_t*>(p.wTok + ci * (kTokArrays * C))[tid];
+      tk.load(static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2 + t0 * p.ks1, p.ks1, rows, p.dkn, tid);
+      tq.load(static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2 + t0 * p.qs1, p.qs1, rows, p.dkn, tid);
       // tiles above the diagonal that a 32-wide block reads, and sums of tiles that do not exist
-      for (int e = tid; e < 2 * NP * 128; e += 256) {
+      for (int e = tid; e < 2 * NP * 128; e += NTHR) {
         const int n = e >> 7, row = (e >> 2) & 31, part = e & 3;
         const int i = row < 16 ? row : row + 16, j = (row < 16 ? 16 : 48) + 4 * part;
         *reinterpret_cast<u32x2*>((n < NP ? sY + n * kTrapLds : sYk + (n - NP) * kTrapLds) + trap_off(i) + place(j)) = u32x2{0u, 0u};
       }
-      for (int e = tid; e < 3 * 4 * C; e += 256) sum[e] = 0.f;
-      tk.store(sK);
-      tq.store(sQ);
+      tk.store(sK, tid);
+      tq.store(sQ, tid);
     }
     __syncthreads();
+    // q.os, k.rs and k.ug of every token over this wave's key columns, and os, rs, ug into dq', dk'
+    ln = fresh_lane();
 #pragma unroll
-    for (int s = 0; s < 3; ++s) {
-      const int t = wave + 4 * s;
+    for (int mt = 0; mt < 4; ++mt) {
+      const int t = 16 * mt + 4 * (ln >> 4);
+      const f32x4_t e = ld4(tok + kTokE * C + t), be = ld4(tok + kTokBeta * C + t), d = ld4(tok + kTokD * C + t);
+      const f32x4_t rk = ld4(tok + kTokRk * C + t), rq = ld4(tok + kTokRq * C + t);
+      f32x4_t a = zero4(), k1 = zero4(), k2 = zero4();
+{
+        os[mt] *= rq * p.scale * e;
+        rs[mt] *= rk * e;
+        ug[mt] *= rk * d;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float qe = element(sQ, t + r, dc + (ln & 15)), ke = element(sK, t + r, dc + (ln & 15));
+          a[r] += qe * os[mt][r];
+          k1[r] += ke * rs[mt][r];
+          k2[r] += ke * ug[mt][r];
+        }
+        aq[mt] += os[mt];
+        ak[mt] += ug[mt] - be * rs[mt];
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        a[r] = sum16(a[r]);
+        k1[r] = sum16(k1[r]);
+        k2[r] = sum16(k2[r]);
+      }
+      if ((ln & 15) == 0) {
+        *reinterpret_cast<f32x4_t*>(sum + wave * C + t) = a;
+        *reinterpret_cast<f32x4_t*>(sum + (NW + wave) * C + t) = k1;
+        *reinterpret_cast<f32x4_t*>(sum + (2 * NW + wave) * C + t) = k2;
+      }
+    }
+    if (ln == 0) sum[3 * NW * C + wave] = through;
+    __syncthreads();
+    float into = 0.f, out = 0.f, kr = 0.f;  // this lane's token, in wave 0
+    if (wave == 0) {
+      through = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) through += sum[3 * NW * C + w];
+      through *= tok[kTokE * C + C - 1];
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        into += sum[w * C + ln];
+        kr += sum[(NW + w) * C + ln];
+        out += sum[(2 * NW + w) * C + ln];
+      }
+      into -= tok[kTokBeta * C + ln] * kr;
+    }
+    __syncthreads();
+    for (int e = wave * 64 + ln; e < 3 * 4 * C; e += NTHR) sum[e] = 0.f;  // sums of tiles that do not exist
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      const int t = wave + NW * s;
       if (t < 10) {
         int ti, tj;
         tile_of(t, ti, tj);
@@ -1425,9 +1447,9 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
           Frag<NT> fj[KB], fq[KB], fk[KB];
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb) {
-            fj[kb] = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb);
-            fq[kb] = rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb);
-            fk[kb] = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * ti, 32 * kb);
+            fj[kb] = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb, ln);
+            fq[kb] = rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb, ln);
+            fk[kb] = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * ti, 32 * kb, ln);
           }
           DELTA_FENCE();
 #pragma unroll
@@ -1473,14 +1495,8 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
     }
     __syncthreads();
     if (wave == 0) {  // dg and dbeta, one token per lane
-      float into = 0.f, out = 0.f, rz = 0.f, through = 0.f;
-      for (int g = 0; g < p.nCG; ++g) {
-        const float* dot = p.wDot + (ci * p.nCG + g) * (kDeltaDots * C);
-        into += dot[lane] - dot[3 * C + lane];
-        out += dot[C + lane];
-        rz += dot[2 * C + lane];
-        through += dot[4 * C];
-      }
+      float rz = -kr;
+      for (int g = 0; g < p.nCG; ++g) rz += p.wDot[(ci * p.nCG + g) * C + lane];
       double ahead = out, behind = into;
       float db = rz;
 #pragma unroll
@@ -1503,60 +1519,47 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
         stf<ET>(p.dbeta, b * p.dbs0 + (t0 + lane) * p.dbs1 + hv * p.dbs2, db);
       }
     }
-    Frag<NT> fk[2][NN], fq[2][NN];
+    ln = fresh_lane();
+    Frag<NT> fk[2], fq[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int n = 0; n < NN; ++n) {
-        fk[kb][n] = colfrag<NT>(sK, TK::LD, TK::PLANE, 32 * kb, 16 * (dt0 + n));
-        fq[kb][n] = colfrag<NT>(sQ, TK::LD, TK::PLANE, 32 * kb, 16 * (dt0 + n));
+{
+        fk[kb] = colfrag<NT>(sK, TK::LD, TK::PLANE, 32 * kb, dc, ln);
+        fq[kb] = colfrag<NT>(sQ, TK::LD, TK::PLANE, 32 * kb, dc, ln);
       }
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
-      const int t = 16 * mt + 4 * q;
-      const f32x4_t e = ld4(tok + kTokE * C + t), d = ld4(tok + kTokD * C + t), be = ld4(tok + kTokBeta * C + t);
-      const f32x4_t rk = ld4(tok + kTokRk * C + t), rq = ld4(tok + kTokRq * C + t);
       Frag<NP> yr[2], kr[2], yc[2], kc[2];
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         if (kb <= mt / 2) {
-          yr[kb] = trap_row<NP>(sY, mt, kb);
-          kr[kb] = trap_row<NP>(sYk, mt, kb);
+          yr[kb] = trap_row<NP>(sY, mt, kb, ln);
+          kr[kb] = trap_row<NP>(sYk, mt, kb, ln);
         }
         if (kb >= mt / 2) {
-          yc[kb] = trap_col<NP>(sY, mt, kb);
-          kc[kb] = trap_col<NP>(sYk, mt, kb);
+          yc[kb] = trap_col<NP>(sY, mt, kb, ln);
+          kc[kb] = trap_col<NP>(sYk, mt, kb, ln);
         }
       }
       DELTA_FENCE();
 #pragma unroll
-      for (int n = 0; n < NN; ++n) {
-        aq[mt][n] += rq * p.scale * e * os[mt][n];
-        ak[mt][n] += rk * (d * ug[mt][n] - be * e * rs[mt][n]);
-      }
-#pragma unroll
       for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int n = 0; n < NN; ++n) {
+{
           if (kb <= mt / 2) {
-            mma<LV>(aq[mt][n], yr[kb], fk[kb][n]);
-            mma<LV>(ak[mt][n], kr[kb], fk[kb][n]);
+            mma<LV>(aq[mt], yr[kb], fk[kb]);
+            mma<LV>(ak[mt], kr[kb], fk[kb]);
           }
           if (kb >= mt / 2) {
-            mma<LV>(ak[mt][n], yc[kb], fq[kb][n]);
-            mma<LV>(ak[mt][n], kc[kb], fk[kb][n]);
+            mma<LV>(ak[mt], yc[kb], fq[kb]);
+            mma<LV>(ak[mt], kc[kb], fk[kb]);
           }
         }
     }
   }
 
   // the norms' own gradients, then out; q and k of the last head are still in LDS
-  auto element = [&](const uint16_t* m, int t, int d) {
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) x += __uint_as_float(uint32_t(m[i * TK::PLANE + t * TK::LD + place(d)]) << 16);
-    return x;
-  };
+  ln = fresh_lane();
+  const int q = ln >> 4, n16 = ln & 15;
   const bool unit = p.eps >= 0.f;
   if (unit) {
     __syncthreads();
@@ -1566,16 +1569,15 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
       for (int r = 0; r < 4; ++r) {
         const int t = 16 * mt + 4 * q + r;
         float a = 0.f, k = 0.f;
-#pragma unroll
-        for (int n = 0; n < NN; ++n) {
-          a += aq[mt][n][r] * element(sQ, t, 16 * (dt0 + n) + n16);
-          k += ak[mt][n][r] * element(sK, t, 16 * (dt0 + n) + n16);
+{
+          a += aq[mt][r] * element(sQ, t, dc + n16);
+          k += ak[mt][r] * element(sK, t, dc + n16);
         }
         a = sum16(a);
         k = sum16(k);
         if (n16 == 0) {
           sum[wave * C + t] = a;
-          sum[4 * C + wave * C + t] = k;
+          sum[(NW + wave) * C + t] = k;
         }
       }
     }
@@ -1589,13 +1591,17 @@ __global__ __launch_bounds__(256, 1) void k_delta_grad(const DeltaParams p) {
       float pq = 0.f, pk = 0.f;
       if (unit) {
         const float rq = tok[kTokRq * C + t], rk = tok[kTokRk * C + t];
-        pq = rq * rq * (sum[t] + sum[C + t] + sum[2 * C + t] + sum[3 * C + t]);
-        pk = rk * rk * (sum[4 * C + t] + sum[5 * C + t] + sum[6 * C + t] + sum[7 * C + t]);
-      }
 #pragma unroll
-      for (int n = 0; n < NN; ++n) {
-        const int d = 16 * (dt0 + n) + n16;
-        float a = aq[mt][n][r], k = ak[mt][n][r];
+        for (int w = 0; w < NW; ++w) {
+          pq += sum[w * C + t];
+          pk += sum[(NW + w) * C + t];
+        }
+        pq *= rq * rq;
+        pk *= rk * rk;
+      }
+{
+        const int d = dc + n16;
+        float a = aq[mt][r], k = ak[mt][r];
         if (unit) {
           a -= pq * element(sQ, t, d);
           k -= pk * element(sK, t, d);
@@ -1627,17 +1633,13 @@ hipError_t delta_prep_launch(const DeltaParams& p, hipStream_t s) {
   return launch_delta(k_delta_prep<ET, DK, VEC>, int64_t(p.B) * p.Hv * p.nC, 256, PrepLds<ET, DK>::BYTES, p, s);
 }
 
-template <typename ET, int DK, bool STATES, bool VEC>
-hipError_t delta_scan_launch(const DeltaParams& p, hipStream_t s) {
-  constexpr int NW = 4;
-  const int64_t blocks = int64_t(p.B) * p.Hv * ((p.nCG + NW - 1) / NW);
-  return launch_delta(k_delta_scan<ET, DK, NW, STATES, VEC>, blocks, 64 * NW, ScanLds<ET, DK, STATES>::BYTES, p, s);
-}
-
 template <typename ET, int DK, bool VEC>
 hipError_t delta_fwd_dk(const DeltaParams& p, hipStream_t s) {
+  constexpr int NW = 4;
   const hipError_t e = delta_prep_launch<ET, DK, VEC>(p, s);
-  return e != hipSuccess ? e : delta_scan_launch<ET, DK, false, VEC>(p, s);
+  if (e != hipSuccess) return e;
+  const int64_t blocks = int64_t(p.B) * p.Hv * ((p.nCG + NW - 1) / NW);
+  return launch_delta(k_delta_scan<ET, DK, NW, VEC>, blocks, 64 * NW, ScanLds<ET, DK, false>::BYTES, p, s);
 }
 
 template <typename ET>
@@ -1648,14 +1650,16 @@ hipError_t delta_fwd_et(const DeltaParams& p, hipStream_t s) {
 
 template <typename ET, int DK, bool VEC>
 hipError_t delta_bwd_dk(const DeltaParams& p, hipStream_t s) {
-  hipError_t e = delta_prep_launch<ET, DK, VEC>(p, s);
-  if (e == hipSuccess) e = delta_scan_launch<ET, DK, true, VEC>(p, s);
   constexpr int NW = 4;
+  hipError_t e = delta_prep_launch<ET, DK, VEC>(p, s);
+  if (e != hipSuccess) return e;
   const int64_t blocks = int64_t(p.B) * p.Hv * ((p.nCG + NW - 1) / NW);
-  if (e == hipSuccess) e = launch_delta(k_delta_back<ET, DK, NW, VEC>, blocks, 64 * NW, BackLds<ET, DK>::BYTES, p, s);
-  if (e == hipSuccess)
-    e = launch_delta(k_delta_grad<ET, DK, VEC>, int64_t(p.B) * p.Hk * p.nC, 256, GradLds<ET, DK>::BYTES, p, s);
-  return e;
+  constexpr int scan_lds = ScanLds<ET, DK, true>::BYTES, back_lds = BackLds<ET, DK>::BYTES;
+  e = launch_delta(k_delta_scans<ET, DK, NW, VEC>, 2 * blocks, 64 * NW, scan_lds > back_lds ? scan_lds : back_lds, p, s);
+  if (e != hipSuccess) return e;
+  const int64_t chunks = int64_t(p.B) * p.Hk * p.nC;
+  if (p.group == 1) return launch_delta(k_delta_grad<ET, DK, VEC, true>, chunks, 64 * GradLds<ET, DK>::NW, GradLds<ET, DK>::BYTES, p, s);
+  return launch_delta(k_delta_grad<ET, DK, VEC, false>, chunks, 64 * GradLds<ET, DK>::NW, GradLds<ET, DK>::BYTES, p, s);
 }
 
 template <typename ET>
