@@ -1183,7 +1183,7 @@ __global__ __launch_bounds__(64 * NW, Store<ET>::NT == 1 ? 2 : 1) void k_delta_s
 template <typename ET, int DK>
 struct GradLds {
   static constexpr int NT = Store<ET>::NT, NP = Store<ET>::NP;
-  static constexpr int NW = DK / 16;  // waves: one 16-wide tile of key columns each
+  static constexpr int NW = 4;  // waves, each with DK / 64 16-wide tiles of key columns
   static constexpr int ULD = C + kPad, OLD = 32 + kPad, SLD = DK + kPad;
   static constexpr int UPL = 32 * ULD, OPL = C * OLD, SPL = 32 * SLD;
   // first part: staged operands of 32 value columns
@@ -1233,9 +1233,9 @@ struct ImageTile {
 
 // ONE: a single value head per key head (no sums to carry from head to head).
 template <typename ET, int DK, bool VEC, bool ONE>
-__global__ __launch_bounds__(4 * DK, 2) void k_delta_grad(const DeltaParams p) {
+__global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delta_grad(const DeltaParams p) {
   using L = GradLds<ET, DK>;
-  constexpr int NT = L::NT, NP = L::NP, LV = NP - 1, KB = DK / 32, NW = L::NW, NTHR = 64 * NW;
+  constexpr int NT = L::NT, NP = L::NP, LV = NP - 1, KB = DK / 32, NN = DK / 64, NW = L::NW, NTHR = 64 * NW;
   constexpr int SLOTS = (10 + NW - 1) / NW;  // tiles of a triangle per wave
   using TK = Tile<ET, DK, NTHR, VEC>;
   static_assert(L::BYTES <= kLdsBytes, "LDS of a CU");
@@ -1257,12 +1257,13 @@ __global__ __launch_bounds__(4 * DK, 2) void k_delta_grad(const DeltaParams p) {
   const int hk = int(id / p.nC % p.Hk);
   const int b = int(id / p.nC / p.Hk);
   const int t0 = c * C, rows = min(C, p.T - t0);
-  const int dc = 16 * wave;  // this wave's key columns
+  const int dc = 16 * NN * wave;  // first of this wave's key columns
 
-  f32x4_t aq[4], ak[4];
+  f32x4_t aq[4][NN], ak[4][NN];
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt)
-aq[mt] = ak[mt] = zero4();
+#pragma unroll
+    for (int n = 0; n < NN; ++n) aq[mt][n] = ak[mt][n] = zero4();
 
   auto element = [&](const uint16_t* m, int t, int d) {
     float x = 0.f;
@@ -1282,10 +1283,11 @@ aq[mt] = ak[mt] = zero4();
     if (gh > 0) __syncthreads();  // the previous head's factors are read
     if (tid < kTokArrays * C / 4)
       reinterpret_cast<f32x4_t*>(tok)[tid] = reinterpret_cast<const f32x4_t*>(p.wTok + ci * (kTokArrays * C))[tid];
-    f32x4_t os[4], rs[4], ug[4];
+    f32x4_t os[4][NN], rs[4][NN], ug[4][NN];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
-os[mt] = rs[mt] = ug[mt] = zero4();
+#pragma unroll
+      for (int n = 0; n < NN; ++n) os[mt][n] = rs[mt][n] = ug[mt][n] = zero4();
     float through = 0.f;  // <S0, dS1>
     {
       ImageTile<2, NTHR> iu, ir;
@@ -1297,13 +1299,16 @@ os[mt] = rs[mt] = ug[mt] = zero4();
         iu.load(p.wU + cim * (C * kDeltaCols), second, tid);
         ir.load(p.wR + cim * (C * kDeltaCols), second, tid);
         is.load(p.wS + cim * (DK * 16), second, tid);
-        ig.load(p.wdS + cim * (DK * 16), second, tid);
         const int row = tid >> 2, c0 = cb * kDeltaCols + (tid & 3) * 8;
         const int n = row < rows ? p.dvn - c0 : 0;
         const uint32_t off = (uint32_t(row) * uint32_t(p.dos1) + uint32_t(c0)) * uint32_t(sizeof(ET));
         io = load8<ET, VEC>(chunk_rsrc<ET, VEC>(dobase, p.dos1, rows, p.dvn), n > 0 ? off : kNowhere, n);
       };
+      auto fetch_ds = [&](int cb, int tid) {
+        ig.load(p.wdS + (ci * p.nCG + cb) * (DK * 16), cb + 1 < p.nCG, tid);
+      };
       fetch(0, tid);
+      fetch_ds(0, tid);
       for (int cb = 0; cb < p.nCG; cb += 2) {
         ln = fresh_lane();
         const int tid = wave * 64 + ln;
@@ -1315,7 +1320,7 @@ os[mt] = rs[mt] = ug[mt] = zero4();
         for (int i = 0; i < ImageTile<KB, NTHR>::N; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) through += is.r[i][e] * ig.r[i][e];
-        if (wave < 4) {  // 64 rows of 4 pieces
+        {  // 64 rows of 4 pieces
           const Frag<NT> f = terms8<ET>(io);
           uint16_t* o = sO + (tid >> 2) * L::OLD + place((tid & 3) * 8);
 #pragma unroll
@@ -1325,20 +1330,28 @@ os[mt] = rs[mt] = ug[mt] = zero4();
           }
         }
         __syncthreads();
-        const ImageTile<KB, NTHR> gg = ig;
         if (cb + 2 < p.nCG) fetch(cb + 2, tid);
         {
-          const auto fs = colfrag<3, true>(sS, L::SLD, L::SPL, 0, dc, ln);
-          Frag<NT> fo[4];
-          Frag<3> fr[4];
+          Frag<3> fs[NN], fr[2];
+          Frag<NT> fo[2];
+          auto read = [&](int mt) {
+            fo[mt & 1] = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * mt, 0, ln);
+            fr[mt & 1] = colfrag<3, true>(sR, L::ULD, L::UPL, 0, 16 * mt, ln);
+          };
+#pragma unroll
+          for (int n = 0; n < NN; ++n) fs[n] = colfrag<3, true>(sS, L::SLD, L::SPL, 0, dc + 16 * n, ln);
+          read(0);
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt) {
-            fo[mt] = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * mt, 0, ln);
-            fr[mt] = colfrag<3, true>(sR, L::ULD, L::UPL, 0, 16 * mt, ln);
+            if (mt < 3) read(mt + 1);
+            DELTA_FENCE();
+#pragma unroll
+            for (int n = 0; n < NN; ++n) {
+              mma<2>(os[mt][n], fo[mt & 1], fs[n]);
+              mma<2>(rs[mt][n], fr[mt & 1], fs[n]);
+            }
+            DELTA_FENCE();
           }
-          DELTA_FENCE();
-          mma_tiles<2, 4>(os, fo, fs);
-          mma_tiles<2, 4>(rs, fr, fs);
         }
 #pragma unroll
         for (int s = 0; s < SLOTS; ++s) {
@@ -1355,14 +1368,23 @@ os[mt] = rs[mt] = ug[mt] = zero4();
           }
         }
         __syncthreads();  // S0 is read: dS1 takes its place
-        gg.template store<3>(sS, L::SLD, L::SPL, tid);
+        ig.template store<3>(sS, L::SLD, L::SPL, tid);
         __syncthreads();
-        const auto fg = colfrag<3, true>(sS, L::SLD, L::SPL, 0, dc, ln);
-        Frag<3> fu[4];
+        if (cb + 2 < p.nCG) fetch_ds(cb + 2, tid);
+        {
+          Frag<3> fg[NN], fu[2];
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) fu[mt] = colfrag<3, true>(sU, L::ULD, L::UPL, 0, 16 * mt, ln);
-        DELTA_FENCE();
-        mma_tiles<2, 4>(ug, fu, fg);
+          for (int n = 0; n < NN; ++n) fg[n] = colfrag<3, true>(sS, L::SLD, L::SPL, 0, dc + 16 * n, ln);
+          fu[0] = colfrag<3, true>(sU, L::ULD, L::UPL, 0, 0, ln);
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            if (mt < 3) fu[(mt + 1) & 1] = colfrag<3, true>(sU, L::ULD, L::UPL, 0, 16 * (mt + 1), ln);
+            DELTA_FENCE();
+#pragma unroll
+            for (int n = 0; n < NN; ++n) mma<2>(ug[mt][n], fu[mt & 1], fg[n]);
+            DELTA_FENCE();
+          }
+        }
       }
     }
     through = sum16(through);
@@ -1391,19 +1413,20 @@ os[mt] = rs[mt] = ug[mt] = zero4();
       const f32x4_t e = ld4(tok + kTokE * C + t), be = ld4(tok + kTokBeta * C + t), d = ld4(tok + kTokD * C + t);
       const f32x4_t rk = ld4(tok + kTokRk * C + t), rq = ld4(tok + kTokRq * C + t);
       f32x4_t a = zero4(), k1 = zero4(), k2 = zero4();
-{
-        os[mt] *= rq * p.scale * e;
-        rs[mt] *= rk * e;
-        ug[mt] *= rk * d;
+#pragma unroll
+      for (int n = 0; n < NN; ++n) {
+        os[mt][n] *= rq * p.scale * e;
+        rs[mt][n] *= rk * e;
+        ug[mt][n] *= rk * d;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float qe = element(sQ, t + r, dc + (ln & 15)), ke = element(sK, t + r, dc + (ln & 15));
-          a[r] += qe * os[mt][r];
-          k1[r] += ke * rs[mt][r];
-          k2[r] += ke * ug[mt][r];
+          const float qe = element(sQ, t + r, dc + 16 * n + (ln & 15)), ke = element(sK, t + r, dc + 16 * n + (ln & 15));
+          a[r] += qe * os[mt][n][r];
+          k1[r] += ke * rs[mt][n][r];
+          k2[r] += ke * ug[mt][n][r];
         }
-        aq[mt] += os[mt];
-        ak[mt] += ug[mt] - be * rs[mt];
+        aq[mt][n] += os[mt][n];
+        ak[mt][n] += ug[mt][n] - be * rs[mt][n];
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -1520,12 +1543,13 @@ os[mt] = rs[mt] = ug[mt] = zero4();
       }
     }
     ln = fresh_lane();
-    Frag<NT> fk[2], fq[2];
+    Frag<NT> fk[2][NN], fq[2][NN];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
-{
-        fk[kb] = colfrag<NT>(sK, TK::LD, TK::PLANE, 32 * kb, dc, ln);
-        fq[kb] = colfrag<NT>(sQ, TK::LD, TK::PLANE, 32 * kb, dc, ln);
+#pragma unroll
+      for (int n = 0; n < NN; ++n) {
+        fk[kb][n] = colfrag<NT>(sK, TK::LD, TK::PLANE, 32 * kb, dc + 16 * n, ln);
+        fq[kb][n] = colfrag<NT>(sQ, TK::LD, TK::PLANE, 32 * kb, dc + 16 * n, ln);
       }
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
@@ -1544,14 +1568,15 @@ os[mt] = rs[mt] = ug[mt] = zero4();
       DELTA_FENCE();
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
-{
+#pragma unroll
+        for (int n = 0; n < NN; ++n) {
           if (kb <= mt / 2) {
-            mma<LV>(aq[mt], yr[kb], fk[kb]);
-            mma<LV>(ak[mt], kr[kb], fk[kb]);
+            mma<LV>(aq[mt][n], yr[kb], fk[kb][n]);
+            mma<LV>(ak[mt][n], kr[kb], fk[kb][n]);
           }
           if (kb >= mt / 2) {
-            mma<LV>(ak[mt], yc[kb], fq[kb]);
-            mma<LV>(ak[mt], kc[kb], fk[kb]);
+            mma<LV>(ak[mt][n], yc[kb], fq[kb][n]);
+            mma<LV>(ak[mt][n], kc[kb], fk[kb][n]);
           }
         }
     }
@@ -1569,9 +1594,10 @@ os[mt] = rs[mt] = ug[mt] = zero4();
       for (int r = 0; r < 4; ++r) {
         const int t = 16 * mt + 4 * q + r;
         float a = 0.f, k = 0.f;
-{
-          a += aq[mt][r] * element(sQ, t, dc + n16);
-          k += ak[mt][r] * element(sK, t, dc + n16);
+#pragma unroll
+        for (int n = 0; n < NN; ++n) {
+          a += aq[mt][n][r] * element(sQ, t, dc + 16 * n + n16);
+          k += ak[mt][n][r] * element(sK, t, dc + 16 * n + n16);
         }
         a = sum16(a);
         k = sum16(k);
@@ -1599,9 +1625,10 @@ os[mt] = rs[mt] = ug[mt] = zero4();
         pq *= rq * rq;
         pk *= rk * rk;
       }
-{
-        const int d = dc + n16;
-        float a = aq[mt][r], k = ak[mt][r];
+#pragma unroll
+      for (int n = 0; n < NN; ++n) {
+        const int d = dc + 16 * n + n16;
+        float a = aq[mt][n][r], k = ak[mt][n][r];
         if (unit) {
           a -= pq * element(sQ, t, d);
           k -= pk * element(sK, t, d);
