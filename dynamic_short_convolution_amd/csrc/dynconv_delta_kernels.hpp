@@ -1207,26 +1207,24 @@ struct GradLds {
 // rows of a [columns][index] LDS matrix of N terms.
 template <int NB, int NTHR>
 struct ImageTile {
-  static constexpr int N = 2 * NB * 128 / NTHR;
-  static_assert(2 * NB * 128 % NTHR == 0, "whole passes");
+  static constexpr int G = NB * 128 / NTHR, N = 2 * G;  // pieces per thread of a group, and in all
+  static_assert(NB * 128 % NTHR == 0, "whole passes");
   f32x4_t r[N];
   // `second`: whether the second group exists (it follows the first); if not, zeros.
   __device__ __forceinline__ void load(const float* src, bool second, int tid) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int e = tid + NTHR * i;
-      const bool have = e < NB * 128 || second;
-      const f32x4_t x = in_global<f32x4_t>(src)[have ? e : e - NB * 128];
-      r[i] = have ? x : zero4();
+      const auto* base = in_global<char>(src) + (i < G || second ? i * NTHR * 16 : (i - G) * NTHR * 16);
+      r[i] = *(const global_t<f32x4_t>*)(base + uint32_t(tid) * 16u);
     }
   }
   template <int NTERM>
-  __device__ __forceinline__ void store(uint16_t* m, int ld, int plane, int tid) const {
+  __device__ __forceinline__ void store(uint16_t* m, int ld, int plane, bool second, int tid) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int e = tid + NTHR * i, g = e / (NB * 128), f = e % (NB * 128);
+      const int g = i / G, f = tid + NTHR * (i - g * G);
       const int kb = f >> 7, l = (f >> 1) & 63, h = f & 1;
-      put4<NTERM>(m + (16 * g + (l & 15)) * ld + 32 * kb + 16 * h + 4 * (l >> 4), plane, r[i]);
+      put4<NTERM>(m + (16 * g + (l & 15)) * ld + 32 * kb + 16 * h + 4 * (l >> 4), plane, i < G || second ? r[i] : zero4());
     }
   }
 };
@@ -1299,27 +1297,28 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
         iu.load(p.wU + cim * (C * kDeltaCols), second, tid);
         ir.load(p.wR + cim * (C * kDeltaCols), second, tid);
         is.load(p.wS + cim * (DK * 16), second, tid);
+        ig.load(p.wdS + cim * (DK * 16), second, tid);
         const int row = tid >> 2, c0 = cb * kDeltaCols + (tid & 3) * 8;
         const int n = row < rows ? p.dvn - c0 : 0;
         const uint32_t off = (uint32_t(row) * uint32_t(p.dos1) + uint32_t(c0)) * uint32_t(sizeof(ET));
         io = load8<ET, VEC>(chunk_rsrc<ET, VEC>(dobase, p.dos1, rows, p.dvn), n > 0 ? off : kNowhere, n);
       };
-      auto fetch_ds = [&](int cb, int tid) {
-        ig.load(p.wdS + (ci * p.nCG + cb) * (DK * 16), cb + 1 < p.nCG, tid);
-      };
-      fetch(0, tid);
-      fetch_ds(0, tid);
       for (int cb = 0; cb < p.nCG; cb += 2) {
         ln = fresh_lane();
         const int tid = wave * 64 + ln;
+        const bool second = cb + 1 < p.nCG;
+        // loaded here, not a block ahead: the registers that would take let the CU's other
+        // workgroup hide the latency instead
+        fetch(cb, tid);
         __syncthreads();  // the previous contents are read
-        iu.template store<3>(sU, L::ULD, L::UPL, tid);
-        ir.template store<3>(sR, L::ULD, L::UPL, tid);
-        is.template store<3>(sS, L::SLD, L::SPL, tid);
+        iu.template store<3>(sU, L::ULD, L::UPL, second, tid);
+        ir.template store<3>(sR, L::ULD, L::UPL, second, tid);
+        is.template store<3>(sS, L::SLD, L::SPL, second, tid);
 #pragma unroll
         for (int i = 0; i < ImageTile<KB, NTHR>::N; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) through += is.r[i][e] * ig.r[i][e];
+          for (int e = 0; e < 4; ++e)
+            if (i < ImageTile<KB, NTHR>::G || second) through += is.r[i][e] * ig.r[i][e];
         {  // 64 rows of 4 pieces
           const Frag<NT> f = terms8<ET>(io);
           uint16_t* o = sO + (tid >> 2) * L::OLD + place((tid & 3) * 8);
@@ -1330,7 +1329,6 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
           }
         }
         __syncthreads();
-        if (cb + 2 < p.nCG) fetch(cb + 2, tid);
         {
           Frag<3> fs[NN], fr[2];
           Frag<NT> fo[2];
@@ -1368,9 +1366,8 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
           }
         }
         __syncthreads();  // S0 is read: dS1 takes its place
-        ig.template store<3>(sS, L::SLD, L::SPL, tid);
+        ig.template store<3>(sS, L::SLD, L::SPL, second, tid);
         __syncthreads();
-        if (cb + 2 < p.nCG) fetch_ds(cb + 2, tid);
         {
           Frag<3> fg[NN], fu[2];
 #pragma unroll
