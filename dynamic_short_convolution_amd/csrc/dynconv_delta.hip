@@ -11,7 +11,7 @@ namespace {
 constexpr size_t kPiece = 256;  // alignment of the workspace's pieces
 
 struct DeltaSizes {
-  size_t T, tok, S, U, dot;
+  size_t T, tok, S, U, dot, end, M;
 };
 
 DeltaSizes delta_sizes(int64_t B, int64_t T, int64_t Hv, int64_t dk, int64_t dv) {
@@ -24,6 +24,14 @@ DeltaSizes delta_sizes(int64_t B, int64_t T, int64_t Hv, int64_t dk, int64_t dv)
   z.S = n * nCG * size_t(delta_dk_pad(int(dk))) * kDeltaCols * sizeof(float);
   z.U = n * nCG * kDeltaChunk * kDeltaCols * sizeof(float);
   z.dot = n * nCG * kDeltaChunk * sizeof(float);
+  const size_t len = size_t(delta_segment_length(B * Hv, int64_t(nC), int64_t(nCG)));
+  const size_t segs = size_t(B) * size_t(Hv) * ((nC + len - 1) / len);
+  const size_t pad = size_t(delta_dk_pad(int(dk)));
+  z.end = z.M = 0;
+  if (nC > len) {
+    z.end = segs * nCG * pad * kDeltaCols * sizeof(float);
+    z.M = segs * pad * pad * sizeof(float);
+  }
   return z;  // every size is a multiple of kPiece
 }
 
@@ -32,7 +40,7 @@ DeltaSizes delta_sizes(int64_t B, int64_t T, int64_t Hv, int64_t dk, int64_t dv)
 size_t delta_workspace(int64_t B, int64_t T, int64_t Hv, int64_t dk, int64_t dv, bool bwd) {
   const DeltaSizes z = delta_sizes(B, T, Hv, dk, dv);
   if (z.T == 0) return 0;
-  return kPiece + z.T + z.tok + (bwd ? 2 * z.S + 2 * z.U + z.dot : 0);
+  return kPiece + z.T + z.tok + z.end + z.M + (bwd ? z.end + 2 * z.S + 2 * z.U + z.dot : 0);
 }
 
 void delta_carve(DeltaParams* p, void* ws, bool bwd) {
@@ -45,7 +53,10 @@ void delta_carve(DeltaParams* p, void* ws, bool bwd) {
   };
   p->wT = reinterpret_cast<uint16_t*>(take(z.T));
   p->wTok = reinterpret_cast<float*>(take(z.tok));
+  p->wEnd = reinterpret_cast<float*>(take(z.end));
+  p->wM = reinterpret_cast<float*>(take(z.M));
   if (!bwd) return;
+  p->wBegin = reinterpret_cast<float*>(take(z.end));
   p->wS = reinterpret_cast<float*>(take(z.S));
   p->wdS = reinterpret_cast<float*>(take(z.S));
   p->wU = reinterpret_cast<float*>(take(z.U));

@@ -102,6 +102,8 @@ dynconv_status take_inputs(DeltaParams* p, const void* q, const int64_t* qs, con
   p->dkn = int32_t(dk), p->dvn = int32_t(dv);
   p->nC = int32_t((T + kDeltaChunk - 1) / kDeltaChunk);
   p->nCG = int32_t((dv + kDeltaCols - 1) / kDeltaCols);
+  p->segLen = delta_segment_length(B * Hv, p->nC, p->nCG);
+  p->nSeg = p->nC > 0 ? (p->nC + p->segLen - 1) / p->segLen : 1;
   p->scale = scale;
   p->eps = eps;
   return DYNCONV_OK;

@@ -43,6 +43,7 @@ struct DeltaParams {
   int64_t sis0, sis1, sis2, sos0, sos1, sos2, dsos0, dsos1, dsos2, dsis0, dsis1, dsis2;
   int32_t B, T, Hk, Hv, group, dkn, dvn;  // dkn, dvn: key and value head widths
   int32_t nC, nCG;                        // chunks per sequence, 16-column groups of a value head
+  int32_t nSeg, segLen;                   // segments of a sequence's chunks, chunks of one (the last may be shorter)
   int32_t vec;                            // rows of q, k (and dO) allow 16-byte loads
   float scale, eps;                       // eps < 0: q and k as they are
   // workspace
@@ -52,10 +53,25 @@ struct DeltaParams {
   float* wdS;     // the same, gradient of the state after the chunk
   float* wU;      // [chunk][nCG][1024]: u, in fragment order
   float* wR;      // the same, gradient of beta * (v - decayed prediction)
+  float* wEnd;    // [sequence and head][nSeg][nCG][DK * 16]: state at a segment's end, in fragment order
+  float* wBegin;  // the same, gradient at a segment's start
+  float* wM;      // [sequence and head][nSeg][DK][DK]: a segment's transition
   float* wDot;    // [chunk][nCG][64]: sums of dR o V over the group's columns
 };
 
 constexpr int delta_dk_pad(int dk) { return dk <= 64 ? 64 : 128; }
+
+// Segments that the scans cut a sequence's chunks into. They pay where one segment per sequence
+// and head leaves most of the 256 CUs idle: the first pass costs about what the second does, and
+// joining about 3 chunks' time per segment, so each gets at least 8 chunks and there are at
+// least 3 (B1 T32768, 16 heads of 128 x 128, bf16: SEGNOTE).
+constexpr int delta_segment_length(int64_t bh, int64_t nC, int64_t nCG) {
+  const int64_t blocks = bh * ((nCG + 3) / 4);
+  int64_t n = blocks > 0 ? 256 / blocks : 1;
+  if (n > nC / 8) n = nC / 8;
+  if (n < 3) return nC > 0 ? int(nC) : 1;
+  return int((nC + n - 1) / n);
+}
 
 // Workspace bytes of the two directions (0 for sizes outside the limits).
 size_t delta_workspace(int64_t B, int64_t T, int64_t Hv, int64_t dk, int64_t dv, bool bwd);

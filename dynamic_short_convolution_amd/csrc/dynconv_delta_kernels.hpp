@@ -756,9 +756,40 @@ __device__ __forceinline__ void store_image(const f32x4_t* x, float* dst, int ln
 #pragma unroll
   for (int i = 0; i < N; ++i) d[128 * (i >> 1) + (i & 1)] = x[i];
 }
-// STATES: only carries the state, storing it before each chunk, and u (for the backward).
-template <typename ET, int DK, int NW, bool STATES, bool VEC>
+template <int N>
+__device__ __forceinline__ void load_image(f32x4_t* x, const float* src, int ln) {
+  const auto* d = in_global<f32x4_t>(src) + 2 * ln;
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = d[128 * (i >> 1) + (i & 1)];
+}
+
+// Where a workgroup of a scan stands: its column block, segment of chunks, sequence and head.
+struct ScanAt {
+  int cb, seg;
+  int64_t bh;
+};
+__device__ __forceinline__ ScanAt scan_at(const DeltaParams& p, uint32_t bid, int ncb) {
+  ScanAt a;
+  a.cb = int(bid % ncb);
+  a.seg = int(bid / ncb % p.nSeg);
+  a.bh = bid / ncb / p.nSeg;
+  return a;
+}
+
+// What a scan leaves behind: outputs (kOutputs), the state before each chunk and u for the
+// backward (kStates), or the end state of its segment alone (kEnds).
+//
+// Segments. With few sequences and heads the chunks of one are cut into p.nSeg segments that
+// run at the same time. A segment's end state is M S + N in terms of its start state S: a first
+// pass (kEnds) carries the value columns from zero (N) and the columns of the unit matrix with
+// no values (M, dk more columns), k_delta_join adds the segments up one behind the other, and
+// the second pass starts every segment from its own state. The gradient's scan does the same
+// in reverse with the transposed M.
+enum { kOutputs = 0, kStates = 1, kEnds = 2 };
+
+template <typename ET, int DK, int NW, int MODE, bool VEC>
 __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint32_t bid) {
+  constexpr bool STATES = MODE != kOutputs;
   using L = ScanLds<ET, DK, STATES>;
   constexpr int NT = L::NT, NP = L::NP, NTHR = 64 * NW, KB = DK / 32;
   using TK = Tile<ET, DK, NTHR, VEC>;
@@ -772,10 +803,14 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
   const int n16 = lane & 15;
   const int q = lane >> 4, ln = lane;
   const int ncb = delta_cols(p, NW);
-  const int cg = int(bid % ncb) * NW + wave;
-  const int64_t bh = bid / ncb;
+  const ScanAt at = scan_at(p, bid, MODE == kEnds ? ncb + DK / kDeltaCols / NW : ncb);
+  const bool unit = at.cb >= ncb;  // columns of the unit matrix
+  if (MODE == kEnds && (at.seg + 1 == p.nSeg || (unit && at.seg == 0))) return;  // nothing starts from there
+  const int cg = (unit ? at.cb - ncb : at.cb) * NW + wave;
+  const int64_t bh = at.bh;
+  const int c0 = at.seg * p.segLen, c1 = min(p.nC, c0 + p.segLen);
   const int hv = int(bh % p.Hv), b = int(bh / p.Hv), hk = hv / p.group;
-  const int col = cg * kDeltaCols + n16;
+  const int col = unit ? p.dvn : cg * kDeltaCols + n16;  // no value column: values read as zero
   const bool ok = col < p.dvn;
   const ET* kbase = static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2;
   const ET* qbase = static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2;
@@ -783,7 +818,16 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
   ET* obase = STATES ? nullptr : static_cast<ET*>(p.out) + b * p.os0 + hv * p.os2;
 
   f32x4_t S[DK / 16];
-  load_state<DK>(S, p.state_in == nullptr ? nullptr : p.state_in + b * p.sis0 + hv * p.sis1, p.sis2, p.dkn, col, ok, ln);
+  if (at.seg == 0) {
+    load_state<DK>(S, p.state_in == nullptr ? nullptr : p.state_in + b * p.sis0 + hv * p.sis1, p.sis2, p.dkn, col, ok, ln);
+  } else if (MODE == kEnds) {
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[i][r] = unit && 16 * i + 4 * q + r == cg * kDeltaCols + n16 ? 1.f : 0.f;
+  } else {
+    load_image<DK / 16>(S, p.wEnd + ((bh * p.nSeg + at.seg - 1) * p.nCG + min(cg, p.nCG - 1)) * (DK * 16), ln);
+  }
 
   if constexpr (!STATES) {
     // the tiles above the diagonal that a 32-wide contraction block still reads
@@ -807,8 +851,8 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
 #pragma unroll
     for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i) ttok[i] = w[min(tid + i * NTHR, kTokArrays * C / 4 - 1)];
   };
-  if (p.nC > 0) fetch(0, tid);
-  for (int c = 0; c < p.nC; ++c) {
+  if (c1 > c0) fetch(c0, tid);
+  for (int c = c0; c < c1; ++c) {
     __syncthreads();  // every wave is done with the previous chunk's tiles
     tk.store(sK, tid);
     if constexpr (!STATES) tq.store(sQ, tid);
@@ -856,7 +900,7 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
           put4<NP>(sP + trap_off(i) + place(j0), kTrapLds, x);
         }
       }
-    } else if (cg < p.nCG) {
+    } else if (MODE == kStates && cg < p.nCG) {
       store_image<DK / 16>(S, p.wS + ((bh * p.nC + c) * p.nCG + cg) * (DK * 16), ln);
     }
 
@@ -903,10 +947,10 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
       trap_product<2>(u, ft, zf);
       DELTA_FENCE();
     }
-    if constexpr (STATES) {
+    if constexpr (MODE == kStates) {
       if (cg < p.nCG) store_image<4>(u, p.wU + ((bh * p.nC + c) * p.nCG + cg) * (C * kDeltaCols), ln);
     }
-    if (c + 1 < p.nC) fetch(c + 1, wave * 64 + ln);
+    if (c + 1 < c1) fetch(c + 1, wave * 64 + ln);
     {
       Frag<NT> fc[4];
       col_load<NT>(fc, sK, TK::LD, TK::PLANE, 0, 0, ln);
@@ -929,14 +973,24 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
       store_cols<ET, VEC>(o, obase + t0 * p.os1, p.os1, min(C, p.T - int(t0)), col, p.dvn, ln);
     }
   }
-  if constexpr (!STATES)
-    store_state<DK>(S, p.state_out == nullptr ? nullptr : p.state_out + b * p.sos0 + hv * p.sos1, p.sos2, p.dkn, col, ok, ln);
+  if constexpr (MODE == kOutputs) {
+    if (at.seg + 1 == p.nSeg)
+      store_state<DK>(S, p.state_out == nullptr ? nullptr : p.state_out + b * p.sos0 + hv * p.sos1, p.sos2, p.dkn, col, ok, ln);
+  }
+  if constexpr (MODE == kEnds) {
+    const int64_t seg = bh * p.nSeg + at.seg;
+    if (unit) {
+      store_state<DK>(S, p.wM + seg * (DK * DK), DK, DK, cg * kDeltaCols + n16, true, ln);
+    } else if (cg < p.nCG) {
+      store_image<DK / 16>(S, p.wEnd + (seg * p.nCG + cg) * (DK * 16), ln);
+    }
+  }
 }
 
 template <typename ET, int DK, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) {
   extern __shared__ __align__(16) char lds[];
-  delta_scan<ET, DK, NW, false, VEC>(p, lds, xcd_logical_block(blockIdx.x, gridDim.x));
+  delta_scan<ET, DK, NW, kOutputs, VEC>(p, lds, xcd_logical_block(blockIdx.x, gridDim.x));
 }
 
 // ---------------------------------------------------------------------------------
@@ -973,7 +1027,8 @@ __device__ __forceinline__ float sum16(float x) {
   return x;
 }
 
-template <typename ET, int DK, int NW, bool VEC>
+// ENDS: only the gradient at its segment's start, from zero at the segment's end.
+template <typename ET, int DK, int NW, bool ENDS, bool VEC>
 __device__ __forceinline__ void delta_back(const DeltaParams p, char* lds, uint32_t bid) {
   using L = BackLds<ET, DK>;
   constexpr int NT = L::NT, NTHR = 64 * NW, KB = DK / 32;
@@ -987,9 +1042,12 @@ __device__ __forceinline__ void delta_back(const DeltaParams p, char* lds, uint3
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int ln = lane;
   const int ncb = delta_cols(p, NW);
-  const int cg = int(bid % ncb) * NW + wave;
+  const ScanAt at = scan_at(p, bid, ncb);
+  if (ENDS && at.seg == 0) return;  // nothing ends there
+  const int cg = at.cb * NW + wave;
   const bool live = cg < p.nCG;  // a wave past the last column group still stages tiles
-  const int64_t bh = bid / ncb;
+  const int64_t bh = at.bh;
+  const int c0 = at.seg * p.segLen, c1 = min(p.nC, c0 + p.segLen);
   const int hv = int(bh % p.Hv), b = int(bh / p.Hv), hk = hv / p.group;
   const ET* kbase = static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2;
   const ET* qbase = static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2;
@@ -1000,8 +1058,15 @@ __device__ __forceinline__ void delta_back(const DeltaParams p, char* lds, uint3
   f32x4_t dS[DK / 16];
   {
     const int col = cg * kDeltaCols + (lane & 15);
-    load_state<DK>(dS, p.dstate_out == nullptr ? nullptr : p.dstate_out + b * p.dsos0 + hv * p.dsos1, p.dsos2, p.dkn, col,
-                   col < p.dvn, ln);
+    if (at.seg + 1 == p.nSeg) {
+      load_state<DK>(dS, p.dstate_out == nullptr ? nullptr : p.dstate_out + b * p.dsos0 + hv * p.dsos1, p.dsos2, p.dkn,
+                     col, col < p.dvn, ln);
+    } else if (ENDS) {
+#pragma unroll
+      for (int i = 0; i < DK / 16; ++i) dS[i] = zero4();
+    } else {
+      load_image<DK / 16>(dS, p.wBegin + ((bh * p.nSeg + at.seg + 1) * p.nCG + min(cg, p.nCG - 1)) * (DK * 16), ln);
+    }
   }
   // the tiles below the diagonal of P^T that a 32-wide contraction block still reads
   for (int e = tid; e < 3 * 128; e += NTHR) {
@@ -1023,8 +1088,8 @@ __device__ __forceinline__ void delta_back(const DeltaParams p, char* lds, uint3
 #pragma unroll
     for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i) ttok[i] = w[min(tid + i * NTHR, kTokArrays * C / 4 - 1)];
   };
-  fetch(p.nC - 1, tid);
-  for (int c = p.nC - 1; c >= 0; --c) {
+  fetch(c1 - 1, tid);
+  for (int c = c1 - 1; c >= c0; --c) {
     ln = fresh_lane();
     const int tid = wave * 64 + ln, q = ln >> 4, n16 = ln & 15;
     const int col = cg * kDeltaCols + n16;
@@ -1040,7 +1105,7 @@ __device__ __forceinline__ void delta_back(const DeltaParams p, char* lds, uint3
     const int64_t t0 = int64_t(c) * C;
     const int rows = min(C, p.T - int(t0));
     load_cols<ET, VEC>(dO, dobase + t0 * p.dos1, p.dos1, rows, col, p.dvn, ln);
-    load_cols<ET, VEC>(v, vbase + t0 * p.vs1, p.vs1, rows, col, p.dvn, ln);
+    if (!ENDS) load_cols<ET, VEC>(v, vbase + t0 * p.vs1, p.vs1, rows, col, p.dvn, ln);
     __syncthreads();
 
     // P^T: tiles of P = scale Gam o Q K^T (rows i, column j), four neighbours of a row of P^T
@@ -1082,7 +1147,7 @@ __device__ __forceinline__ void delta_back(const DeltaParams p, char* lds, uint3
     {
       Frag<NT> fk[4];
       row_load<NT>(fk, sK, TK::LD, TK::PLANE, ln);
-      if (live) store_image<DK / 16>(dS, p.wdS + cim * (DK * 16), ln);
+      if (!ENDS && live) store_image<DK / 16>(dS, p.wdS + cim * (DK * 16), ln);
       Frag<3> sf[KB];
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(dS[2 * kb], dS[2 * kb + 1]);
@@ -1113,8 +1178,8 @@ __device__ __forceinline__ void delta_back(const DeltaParams p, char* lds, uint3
       DELTA_FENCE();
     }
     ln = fresh_lane();
-    if (live) store_image<4>(dR, p.wR + cim * (C * kDeltaCols), ln);
-    if (c > 0) fetch(c - 1, wave * 64 + ln);
+    if (!ENDS && live) store_image<4>(dR, p.wR + cim * (C * kDeltaCols), ln);
+    if (c > c0) fetch(c - 1, wave * 64 + ln);
     {
       Frag<NT> fc[4];
       col_load<NT>(fc, sK, TK::LD, TK::PLANE, 0, 0, ln);
@@ -1122,13 +1187,15 @@ __device__ __forceinline__ void delta_back(const DeltaParams p, char* lds, uint3
       tok_load(tc, tok + kTokRk * C, ln);
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) {
-        f32x4_t x;
+        if constexpr (!ENDS) {
+          f32x4_t x;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = sum16(dR[mt][r] * v[4 * mt + r]);
-        if (live && (ln & 15) == 0) *in_global<f32x4_t>(static_cast<void*>(p.wDot + cim * C + 16 * mt + 4 * (ln >> 4))) = x;
+          for (int r = 0; r < 4; ++r) x[r] = sum16(dR[mt][r] * v[4 * mt + r]);
+          if (live && (ln & 15) == 0) *in_global<f32x4_t>(static_cast<void*>(p.wDot + cim * C + 16 * mt + 4 * (ln >> 4))) = x;
+        }
         dz[mt] = dR[mt] * tb[mt];
       }
-      store_cols<ET, VEC>(dz, dvbase + t0 * p.dvs1, p.dvs1, rows, cg * kDeltaCols + (ln & 15), p.dvn, ln);
+      if (!ENDS) store_cols<ET, VEC>(dz, dvbase + t0 * p.dvs1, p.dvs1, rows, cg * kDeltaCols + (ln & 15), p.dvn, ln);
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt) dz[mt] = -(dz[mt] * ta[mt] * tc[mt]);
       const Frag<3> rf[2] = {split8<3>(dz[0], dz[1]), split8<3>(dz[2], dz[3])};
@@ -1146,20 +1213,79 @@ __device__ __forceinline__ void delta_back(const DeltaParams p, char* lds, uint3
       col_product<2, DK / 16>(dS, fc, sQ, TK::LD, TK::PLANE, of, [] {}, ln);
     }
   }
-  const int col = cg * kDeltaCols + (ln & 15);
-  store_state<DK>(dS, p.dstate == nullptr ? nullptr : p.dstate + b * p.dsis0 + hv * p.dsis1, p.dsis2, p.dkn, col,
-                  col < p.dvn, ln);
+  if (ENDS) {
+    if (live) store_image<DK / 16>(dS, p.wBegin + ((bh * p.nSeg + at.seg) * p.nCG + cg) * (DK * 16), ln);
+  } else if (at.seg == 0) {
+    const int col = cg * kDeltaCols + (ln & 15);
+    store_state<DK>(dS, p.dstate == nullptr ? nullptr : p.dstate + b * p.dsis0 + hv * p.dsis1, p.dsis2, p.dkn, col,
+                    col < p.dvn, ln);
+  }
 }
 
-// Both scans of the backward: the first half of the workgroups carries dS, the second S.
-template <typename ET, int DK, int NW, bool VEC>
-__global__ __launch_bounds__(64 * NW, Store<ET>::NT == 1 ? 2 : 1) void k_delta_scans(const DeltaParams p) {
+// Both scans of the backward: the first `back` workgroups carry dS, the others S.
+template <typename ET, int DK, int NW, bool ENDS, bool VEC>
+__global__ __launch_bounds__(64 * NW, Store<ET>::NT == 1 ? 2 : 1) void k_delta_scans(const DeltaParams p, uint32_t back) {
   extern __shared__ __align__(16) char lds[];
-  const uint32_t half = gridDim.x / 2;
-  if (blockIdx.x < half) {
-    delta_back<ET, DK, NW, VEC>(p, lds, xcd_logical_block(blockIdx.x, half));
+  if (blockIdx.x < back) {
+    delta_back<ET, DK, NW, ENDS, VEC>(p, lds, xcd_logical_block(blockIdx.x, back));
   } else {
-    delta_scan<ET, DK, NW, true, VEC>(p, lds, xcd_logical_block(blockIdx.x - half, half));
+    delta_scan<ET, DK, NW, ENDS ? kEnds : kStates, VEC>(p, lds, xcd_logical_block(blockIdx.x - back, gridDim.x - back));
+  }
+}
+
+// The forward's first pass over segments.
+template <typename ET, int DK, int NW, bool VEC>
+__global__ __launch_bounds__(64 * NW, Store<ET>::NT == 1 ? 2 : 1) void k_delta_ends(const DeltaParams p) {
+  extern __shared__ __align__(16) char lds[];
+  delta_scan<ET, DK, NW, kEnds, VEC>(p, lds, xcd_logical_block(blockIdx.x, gridDim.x));
+}
+
+// Joins the segments of one (sequence, head), 16 columns per wave: wEnd[g] = M_g wEnd[g-1] +
+// wEnd[g] for g = 1 .. nSeg-2, in place, so that wEnd[g] is what segment g + 1 starts from. The
+// workgroups from `fwd` on do the same backwards with the transposed M on wBegin.
+template <int DK>
+__global__ __launch_bounds__(256, 1) void k_delta_join(const DeltaParams p, uint32_t fwd) {
+  constexpr int KB = DK / 32;
+  const int ln = threadIdx.x & 63, wave = threadIdx.x >> 6, q = ln >> 4, n16 = ln & 15;
+  const bool rev = blockIdx.x >= fwd;
+  const uint32_t bid = rev ? blockIdx.x - fwd : blockIdx.x;
+  const int ncb = delta_cols(p, 4);
+  const int cg = int(bid % ncb) * 4 + wave;
+  const int64_t bh = bid / ncb;
+  if (cg >= p.nCG) return;
+  float* w = rev ? p.wBegin : p.wEnd;
+  auto image = [&](int g) { return w + ((bh * p.nSeg + g) * p.nCG + cg) * (DK * 16); };
+  f32x4_t S[DK / 16];
+  load_image<DK / 16>(S, image(rev ? p.nSeg - 1 : 0), ln);
+  for (int s = 1; s + 1 < p.nSeg; ++s) {
+    const int g = rev ? p.nSeg - 1 - s : s;
+    const auto* M = in_global<float>(p.wM + (bh * p.nSeg + g) * (DK * DK));
+    Frag<3> sf[KB];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(S[2 * kb], S[2 * kb + 1]);
+    load_image<DK / 16>(S, image(g), ln);
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i) {
+      f32x4_t a[KB], b[KB];
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        if (!rev) {
+          const auto* row = M + (16 * i + n16) * DK + 32 * kb + 4 * q;
+          a[kb] = *(const global_t<f32x4_t>*)row;
+          b[kb] = *(const global_t<f32x4_t>*)(row + 16);
+        } else {
+          const auto* column = M + (32 * kb + 4 * q) * DK + 16 * i + n16;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            a[kb][r] = column[r * DK];
+            b[kb][r] = column[(16 + r) * DK];
+          }
+        }
+      }
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) mma<2>(S[i], split8<3>(a[kb], b[kb]), sf[kb]);
+    }
+    store_image<DK / 16>(S, image(g), ln);
   }
 }
 
@@ -1639,31 +1765,38 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
   }
 }
 
-template <typename KernelT>
-hipError_t launch_delta(KernelT kernel, int64_t blocks, int threads, int lds_bytes, const DeltaParams& p,
-                        hipStream_t s) {
+template <typename KernelT, typename... Args>
+hipError_t launch_delta(KernelT kernel, int64_t blocks, int threads, int lds_bytes, hipStream_t s, const Args&... args) {
   if (lds_bytes > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(kernel, dim3(unsigned(blocks)), dim3(unsigned(threads)), unsigned(lds_bytes), s, p);
+  hipLaunchKernelGGL(kernel, dim3(unsigned(blocks)), dim3(unsigned(threads)), unsigned(lds_bytes), s, args...);
   return hipGetLastError();
 }
 
 template <typename ET, int DK, bool VEC>
 hipError_t delta_prep_launch(const DeltaParams& p, hipStream_t s) {
   if (p.nC == 0) return hipSuccess;
-  return launch_delta(k_delta_prep<ET, DK, VEC>, int64_t(p.B) * p.Hv * p.nC, 256, PrepLds<ET, DK>::BYTES, p, s);
+  return launch_delta(k_delta_prep<ET, DK, VEC>, int64_t(p.B) * p.Hv * p.nC, 256, PrepLds<ET, DK>::BYTES, s, p);
 }
+
+constexpr int kScanWaves = 4;
 
 template <typename ET, int DK, bool VEC>
 hipError_t delta_fwd_dk(const DeltaParams& p, hipStream_t s) {
-  constexpr int NW = 4;
-  const hipError_t e = delta_prep_launch<ET, DK, VEC>(p, s);
+  constexpr int NW = kScanWaves;
+  hipError_t e = delta_prep_launch<ET, DK, VEC>(p, s);
   if (e != hipSuccess) return e;
-  const int64_t blocks = int64_t(p.B) * p.Hv * ((p.nCG + NW - 1) / NW);
-  return launch_delta(k_delta_scan<ET, DK, NW, VEC>, blocks, 64 * NW, ScanLds<ET, DK, false>::BYTES, p, s);
+  const int64_t bh = int64_t(p.B) * p.Hv, ncb = (p.nCG + NW - 1) / NW;
+  if (p.nSeg > 1) {
+    e = launch_delta(k_delta_ends<ET, DK, NW, VEC>, bh * p.nSeg * (ncb + DK / kDeltaCols / NW), 64 * NW,
+                     ScanLds<ET, DK, true>::BYTES, s, p);
+    if (e == hipSuccess && p.nSeg > 2) e = launch_delta(k_delta_join<DK>, bh * ncb, 256, 0, s, p, uint32_t(bh * ncb));
+    if (e != hipSuccess) return e;
+  }
+  return launch_delta(k_delta_scan<ET, DK, NW, VEC>, bh * p.nSeg * ncb, 64 * NW, ScanLds<ET, DK, false>::BYTES, s, p);
 }
 
 template <typename ET>
@@ -1674,16 +1807,24 @@ hipError_t delta_fwd_et(const DeltaParams& p, hipStream_t s) {
 
 template <typename ET, int DK, bool VEC>
 hipError_t delta_bwd_dk(const DeltaParams& p, hipStream_t s) {
-  constexpr int NW = 4;
+  constexpr int NW = kScanWaves;
+  constexpr int scan_lds = ScanLds<ET, DK, true>::BYTES, back_lds = BackLds<ET, DK>::BYTES;
+  constexpr int scans_lds = scan_lds > back_lds ? scan_lds : back_lds;
   hipError_t e = delta_prep_launch<ET, DK, VEC>(p, s);
   if (e != hipSuccess) return e;
-  const int64_t blocks = int64_t(p.B) * p.Hv * ((p.nCG + NW - 1) / NW);
-  constexpr int scan_lds = ScanLds<ET, DK, true>::BYTES, back_lds = BackLds<ET, DK>::BYTES;
-  e = launch_delta(k_delta_scans<ET, DK, NW, VEC>, 2 * blocks, 64 * NW, scan_lds > back_lds ? scan_lds : back_lds, p, s);
+  const int64_t bh = int64_t(p.B) * p.Hv, ncb = (p.nCG + NW - 1) / NW, blocks = bh * p.nSeg * ncb;
+  if (p.nSeg > 1) {
+    e = launch_delta(k_delta_scans<ET, DK, NW, true, VEC>, 2 * blocks + bh * p.nSeg * (DK / kDeltaCols / NW), 64 * NW,
+                     scans_lds, s, p, uint32_t(blocks));
+    if (e == hipSuccess && p.nSeg > 2) e = launch_delta(k_delta_join<DK>, 2 * bh * ncb, 256, 0, s, p, uint32_t(bh * ncb));
+    if (e != hipSuccess) return e;
+  }
+  e = launch_delta(k_delta_scans<ET, DK, NW, false, VEC>, 2 * blocks, 64 * NW, scans_lds, s, p, uint32_t(blocks));
   if (e != hipSuccess) return e;
   const int64_t chunks = int64_t(p.B) * p.Hk * p.nC;
-  if (p.group == 1) return launch_delta(k_delta_grad<ET, DK, VEC, true>, chunks, 64 * GradLds<ET, DK>::NW, GradLds<ET, DK>::BYTES, p, s);
-  return launch_delta(k_delta_grad<ET, DK, VEC, false>, chunks, 64 * GradLds<ET, DK>::NW, GradLds<ET, DK>::BYTES, p, s);
+  constexpr int threads = 64 * GradLds<ET, DK>::NW;
+  if (p.group == 1) return launch_delta(k_delta_grad<ET, DK, VEC, true>, chunks, threads, GradLds<ET, DK>::BYTES, s, p);
+  return launch_delta(k_delta_grad<ET, DK, VEC, false>, chunks, threads, GradLds<ET, DK>::BYTES, s, p);
 }
 
 template <typename ET>
