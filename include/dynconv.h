@@ -380,10 +380,14 @@ dynconv_status dynconv_cache_fill_varlen(const void* x, const int64_t* xs, const
  *   state_in   float32 [B,Hv,dk,dv] (strides [0..3], last 1) or NULL (zero)
  *   state_out  the same, overwritten with the state after token T-1, or NULL; may be
  *              state_in itself (same strides). T == 0 copies the state.
- * A token with beta = 0 and g = 0 leaves the state as it is (padding behind a sequence).
- * g <= -128 counts as a decay to exactly zero (exp of it is 0 in float32).
+ * A token with beta = 0 and g = 0 leaves the state as it is (padding behind a sequence, whose
+ * q, k, v have to be finite).
+ * g <= -128 counts as a decay to exactly zero (exp of it is 0 in float32). Tokens are worked
+ * on 64 at a time: a NaN or infinity among a head's inputs can reach every output of its
+ * 64-token chunk and of what follows, other documents included; other heads keep theirs.
  * Limits (DYNCONV_ERR_UNSUPPORTED otherwise): dk <= 128, dv <= 65536; strides >= 0, token
- * strides (s[1]) of q, k, v, o and their gradients below 2^22 elements. Inputs and outputs need element alignment; rows of q, k that allow 16-byte loads are read so.
+ * strides (s[1]) of q, k, v, o and their gradients below 2^22 elements. Inputs and outputs
+ * need element alignment; rows of q, k that allow 16-byte loads are read so.
  * Needs dynconv_delta_fwd_workspace_size(...) bytes of workspace. Run-to-run deterministic.
  */
 dynconv_status dynconv_delta_fwd(const void* q, const int64_t* qs, const void* k, const int64_t* ks, const void* v,
