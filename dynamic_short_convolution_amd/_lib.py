@@ -5,6 +5,7 @@ Loading fails loudly when the library has not been built: there is no CPU fallba
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdynconv.so")
@@ -203,9 +204,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
     return lib
 
 
+@functools.lru_cache(maxsize=4096)
+def _int64s(vals: tuple) -> ctypes.Array:
+    return (ctypes.c_int64 * len(vals))(*vals)
+
+
 def strides(vals) -> ctypes.Array:
-    arr = (ctypes.c_int64 * len(vals))(*[int(v) for v in vals])
-    return arr
+    """vals as the constant int64 array of a C call. One array serves every call with the same
+    values: building it took half of the time that a small call spends in Python."""
+    return _int64s(tuple(map(int, vals)))
 
 
 def check(fn: str, status: int) -> None:

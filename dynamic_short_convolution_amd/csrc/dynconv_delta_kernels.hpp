@@ -686,6 +686,8 @@ __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
 // Forward scan over the chunks of one (sequence, value head), 16 columns per wave
 // ---------------------------------------------------------------------------------
 
+constexpr int kScanWaves = 4;  // 16-column groups of a scan's workgroup
+
 template <typename ET, int DK, bool STATES>
 struct ScanLds {
   static constexpr int NT = Store<ET>::NT, NP = Store<ET>::NP;
@@ -694,7 +696,12 @@ struct ScanLds {
   static constexpr int T = Q + (STATES ? 0 : NT * Tile<ET, DK, 64, true>::PLANE * 2);
   static constexpr int P = T + 3 * kTrapLds * 2;
   static constexpr int TOK = P + (STATES ? 0 : NP * kTrapLds * 2);
-  static constexpr int BYTES = TOK + kTokArrays * C * 4;
+  // Two waves per 16 columns (see delta_scan) and what one hands the other: S0's and U's terms
+  static constexpr bool PAIR = !STATES && NT < 3;
+  static constexpr int HS = TOK + kTokArrays * C * 4, HSW = DK / 32 * NP * 1024;  // per wave
+  static constexpr int HU = HS + (PAIR ? kScanWaves * HSW : 0), HUW = 2 * NP * 1024;
+  static constexpr int BYTES = HU + (PAIR ? kScanWaves * HUW : 0);
+  static constexpr int THREADS = 64 * kScanWaves * (PAIR ? 2 : 1);
 };
 
 __device__ __forceinline__ int delta_cols(const DeltaParams& p, int nw) { return (p.nCG + nw - 1) / nw; }
@@ -753,18 +760,22 @@ __device__ __forceinline__ void store_state(const f32x4_t* S, float* dst, int64_
     }
 }
 
-// Images of a wave's [rows x 16] matrix in fragment order: 32 bytes per lane and 32 rows.
+// Images of a wave's [rows x 16] matrix: 16 bytes per lane and 16 rows, per 32 rows 128 such
+// pieces. Piece (column n, row group q, half h of the 32 rows) is at 32 (n / 4) + 16 h +
+// 4 (n % 4) + q: 16 neighbouring ones, taken by 16 lanes into an LDS matrix whose rows are
+// columns, 32 bytes modulo 128 apart, fall on all its banks.
+__device__ __forceinline__ int image_piece(int ln) { return 8 * (ln & 12) + 4 * (ln & 3) + (ln >> 4); }
 template <int N>
 __device__ __forceinline__ void store_image(const f32x4_t* x, float* dst, int ln) {
-  auto* d = in_global<f32x4_t>(static_cast<void*>(dst)) + 2 * ln;
+  auto* d = in_global<f32x4_t>(static_cast<void*>(dst)) + image_piece(ln);
 #pragma unroll
-  for (int i = 0; i < N; ++i) d[128 * (i >> 1) + (i & 1)] = x[i];
+  for (int i = 0; i < N; ++i) d[128 * (i >> 1) + 16 * (i & 1)] = x[i];
 }
 template <int N>
 __device__ __forceinline__ void load_image(f32x4_t* x, const float* src, int ln) {
-  const auto* d = in_global<f32x4_t>(src) + 2 * ln;
+  const auto* d = in_global<f32x4_t>(src) + image_piece(ln);
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = d[128 * (i >> 1) + (i & 1)];
+  for (int i = 0; i < N; ++i) x[i] = d[128 * (i >> 1) + 16 * (i & 1)];
 }
 
 // Where a workgroup of a scan stands: its column block, segment of chunks, sequence and head.
@@ -791,11 +802,29 @@ __device__ __forceinline__ ScanAt scan_at(const DeltaParams& p, uint32_t bid, in
 // in reverse with the transposed M.
 enum { kOutputs = 0, kStates = 1, kEnds = 2 };
 
+// Fragments handed from wave to wave through LDS, 16 bytes per lane and term.
+template <int N, int COUNT>
+__device__ __forceinline__ void hand_over(char* m, const Frag<N>* f, int ln) {
+#pragma unroll
+  for (int i = 0; i < COUNT; ++i)
+#pragma unroll
+    for (int n = 0; n < N; ++n) *reinterpret_cast<u32x4*>(m + (i * N + n) * 1024 + ln * 16) = f[i].t[n];
+}
+template <int N, int COUNT>
+__device__ __forceinline__ void take_over(Frag<N>* f, const char* m, int ln) {
+#pragma unroll
+  for (int i = 0; i < COUNT; ++i)
+#pragma unroll
+    for (int n = 0; n < N; ++n) f[i].t[n] = *reinterpret_cast<const u32x4*>(m + (i * N + n) * 1024 + ln * 16);
+}
+
 template <typename ET, int DK, int NW, int MODE, bool VEC>
 __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint32_t bid) {
   constexpr bool STATES = MODE != kOutputs;
   using L = ScanLds<ET, DK, STATES>;
-  constexpr int NT = L::NT, NP = L::NP, NTHR = 64 * NW, KB = DK / 32;
+  constexpr bool PAIR = L::PAIR;
+  constexpr int NT = L::NT, NP = L::NP, NTHR = L::THREADS, KB = DK / 32;
+  static_assert(NW == kScanWaves, "waves of the LDS layout");
   using TK = Tile<ET, DK, NTHR, VEC>;
   static_assert(L::BYTES <= kLdsBytes, "LDS of a CU");
   uint16_t* sK = reinterpret_cast<uint16_t*>(lds + L::K);
@@ -805,12 +834,14 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
   float* tok = reinterpret_cast<float*>(lds + L::TOK);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n16 = lane & 15;
-  const int q = lane >> 4, ln = lane;
+  const int q = lane >> 4;
+  int ln = lane;
   const int ncb = delta_cols(p, NW);
   const ScanAt at = scan_at(p, bid, MODE == kEnds ? ncb + DK / kDeltaCols / NW : ncb);
   const bool unit = at.cb >= ncb;  // columns of the unit matrix
   if (MODE == kEnds && (at.seg + 1 == p.nSeg || (unit && at.seg == 0))) return;  // nothing starts from there
-  const int cg = (unit ? at.cb - ncb : at.cb) * NW + wave;
+  const int cw = PAIR ? wave % NW : wave;
+  const int cg = (unit ? at.cb - ncb : at.cb) * NW + cw;
   const int64_t bh = at.bh;
   const int c0 = at.seg * p.segLen, c1 = min(p.nC, c0 + p.segLen);
   const int hv = int(bh % p.Hv), b = int(bh / p.Hv), hk = hv / p.group;
@@ -820,18 +851,6 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
   const ET* qbase = static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2;
   const ET* vbase = static_cast<const ET*>(p.v) + b * p.vs0 + hv * p.vs2;
   ET* obase = STATES ? nullptr : static_cast<ET*>(p.out) + b * p.os0 + hv * p.os2;
-
-  f32x4_t S[DK / 16];
-  if (at.seg == 0) {
-    load_state<DK>(S, p.state_in == nullptr ? nullptr : p.state_in + b * p.sis0 + hv * p.sis1, p.sis2, p.dkn, col, ok, ln);
-  } else if (MODE == kEnds) {
-#pragma unroll
-    for (int i = 0; i < DK / 16; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) S[i][r] = unit && 16 * i + 4 * q + r == cg * kDeltaCols + n16 ? 1.f : 0.f;
-  } else {
-    load_image<DK / 16>(S, p.wEnd + ((bh * p.nSeg + at.seg - 1) * p.nCG + min(cg, p.nCG - 1)) * (DK * 16), ln);
-  }
 
   if constexpr (!STATES) {
     // the tiles above the diagonal that a 32-wide contraction block still reads
@@ -855,15 +874,111 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
 #pragma unroll
     for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i) ttok[i] = w[min(tid + i * NTHR, kTokArrays * C / 4 - 1)];
   };
-  if (c1 > c0) fetch(c0, tid);
-  for (int c = c0; c < c1; ++c) {
-    __syncthreads();  // every wave is done with the previous chunk's tiles
+  auto stage = [&](int tid) {
     tk.store(sK, tid);
     if constexpr (!STATES) tq.store(sQ, tid);
     tt.store(sT, tid);
 #pragma unroll
     for (int i = 0; i * NTHR < kTokArrays * C / 4; ++i)
       if (tid + i * NTHR < kTokArrays * C / 4) reinterpret_cast<f32x4_t*>(tok)[tid + i * NTHR] = ttok[i];
+  };
+  // P = scale Gam o Q K^T: tiles transposed (rows j, column i), so a lane holds four neighbours
+  // of one row of P
+  auto pairs = [&] {
+    const int q = ln >> 4, n16 = ln & 15;
+#pragma unroll
+    for (int s = 0; s < (10 + NW - 1) / NW; ++s) {
+      const int t = cw + s * NW;
+      if (t < 10) {
+        int ti, tj;
+        tile_of(t, ti, tj);
+        Frag<NT> fj[KB], fi[KB];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          fj[kb] = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb, ln);
+          fi[kb] = rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb, ln);
+        }
+        const int i = 16 * ti + n16, j0 = 16 * tj + 4 * q;
+        const float gh = tok[kTokGhi * C + i], gl = tok[kTokGlo * C + i], rqi = tok[kTokRq * C + i] * p.scale;
+        const int ni = __float_as_int(tok[kTokN * C + i]);
+        const f32x4_t ghj = ld4(tok + kTokGhi * C + j0), glj = ld4(tok + kTokGlo * C + j0);
+        const f32x4_t nj = ld4(tok + kTokN * C + j0), rkj = ld4(tok + kTokRk * C + j0);
+        DELTA_FENCE();
+        f32x4_t acc[2] = {zero4(), zero4()};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) mma<NP - 1>(acc[kb & 1], fj[kb], fi[kb]);
+        f32x4_t x;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          x[r] = j0 + r <= i ? (acc[0][r] + acc[1][r]) * rqi * rkj[r] *
+                                   gam(gh, gl, ni, ghj[r], glj[r], __float_as_int(nj[r]))
+                             : 0.f;
+        put4<NP>(sP + trap_off(i) + place(j0), kTrapLds, x);
+      }
+    }
+  };
+  // o = scale E (Q S0), s0: its terms
+  auto from_state = [&](f32x4_t* o, Frag<NT>* fq, const Frag<NP>* s0) {
+    f32x4_t te[4], tr[4];
+    row_product<NP - 1, KB>(o, fq, sQ, TK::LD, TK::PLANE, s0, [&] {
+      tok_load(te, tok + kTokE * C, ln);
+      tok_load(tr, tok + kTokRq * C, ln);
+    }, ln);
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) o[mt] *= te[mt] * tr[mt] * p.scale;
+  };
+  // o += P U, and out
+  auto finish = [&](f32x4_t* o, const Frag<NP>* uf, int c) {
+    Trap<NP> fp;
+    trap_load(fp, sP, ln);
+    DELTA_FENCE();
+    trap_product<NP - 1>(o, fp, uf);
+    const int64_t t0 = int64_t(c) * C;
+    store_cols<ET, VEC>(o, obase + t0 * p.os1, p.os1, min(C, p.T - int(t0)), col, p.dvn, ln);
+  };
+
+  if (c1 > c0) fetch(c0, tid);
+  if constexpr (PAIR) {
+    if (wave >= NW) {
+      const char* hs = lds + L::HS + cw * L::HSW;
+      const char* hu = lds + L::HU + cw * L::HUW;
+      for (int c = c0; c < c1; ++c) {
+        ln = fresh_lane();
+        __syncthreads();  // every wave is done with the previous chunk's tiles
+        stage(wave * 64 + ln);
+        __syncthreads();
+        pairs();
+        if (c + 1 < c1) fetch(c + 1, wave * 64 + ln);
+        __syncthreads();  // P is complete, S0 and U are handed over
+        f32x4_t o[4] = {zero4(), zero4(), zero4(), zero4()};
+        Frag<NT> fq[4];
+        Frag<NP> s0[KB], uf[2];
+        row_load<NT>(fq, sQ, TK::LD, TK::PLANE, ln);
+        take_over<NP, KB>(s0, hs, ln);
+        from_state(o, fq, s0);
+        take_over<NP, 2>(uf, hu, ln);
+        finish(o, uf, c);
+      }
+      return;
+    }
+  }
+
+  f32x4_t S[DK / 16];
+  if (at.seg == 0) {
+    load_state<DK>(S, p.state_in == nullptr ? nullptr : p.state_in + b * p.sis0 + hv * p.sis1, p.sis2, p.dkn, col, ok, ln);
+  } else if (MODE == kEnds) {
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[i][r] = unit && 16 * i + 4 * q + r == cg * kDeltaCols + n16 ? 1.f : 0.f;
+  } else {
+    load_image<DK / 16>(S, p.wEnd + ((bh * p.nSeg + at.seg - 1) * p.nCG + min(cg, p.nCG - 1)) * (DK * 16), ln);
+  }
+
+  for (int c = c0; c < c1; ++c) {
+    ln = fresh_lane();
+    __syncthreads();  // every wave is done with the previous chunk's tiles
+    stage(wave * 64 + ln);
     float v[16];
     {
       const int64_t t0 = int64_t(c) * C;
@@ -871,45 +986,13 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
     }
     __syncthreads();
 
-    if constexpr (!STATES) {
-      // P = scale Gam o Q K^T: tiles transposed (rows j, column i), so a lane holds four
-      // neighbours of one row of P
-#pragma unroll
-      for (int s = 0; s < (10 + NW - 1) / NW; ++s) {
-        const int t = wave + s * NW;
-        if (t < 10) {
-          int ti, tj;
-          tile_of(t, ti, tj);
-          Frag<NT> fj[KB], fi[KB];
-#pragma unroll
-          for (int kb = 0; kb < KB; ++kb) {
-            fj[kb] = rowfrag<NT>(sK, TK::LD, TK::PLANE, 16 * tj, 32 * kb, ln);
-            fi[kb] = rowfrag<NT>(sQ, TK::LD, TK::PLANE, 16 * ti, 32 * kb, ln);
-          }
-          const int i = 16 * ti + n16, j0 = 16 * tj + 4 * q;
-          const float gh = tok[kTokGhi * C + i], gl = tok[kTokGlo * C + i], rqi = tok[kTokRq * C + i] * p.scale;
-          const int ni = __float_as_int(tok[kTokN * C + i]);
-          const f32x4_t ghj = ld4(tok + kTokGhi * C + j0), glj = ld4(tok + kTokGlo * C + j0);
-          const f32x4_t nj = ld4(tok + kTokN * C + j0), rkj = ld4(tok + kTokRk * C + j0);
-          DELTA_FENCE();
-          f32x4_t acc[2] = {zero4(), zero4()};
-#pragma unroll
-          for (int kb = 0; kb < KB; ++kb) mma<NP - 1>(acc[kb & 1], fj[kb], fi[kb]);
-          f32x4_t x;
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            x[r] = j0 + r <= i ? (acc[0][r] + acc[1][r]) * rqi * rkj[r] *
-                                     gam(gh, gl, ni, ghj[r], glj[r], __float_as_int(nj[r]))
-                               : 0.f;
-          put4<NP>(sP + trap_off(i) + place(j0), kTrapLds, x);
-        }
-      }
-    } else if (MODE == kStates && cg < p.nCG) {
+    if constexpr (!STATES && !PAIR) pairs();
+    if (MODE == kStates && cg < p.nCG) {
       store_image<DK / 16>(S, p.wS + ((bh * p.nC + c) * p.nCG + cg) * (DK * 16), ln);
     }
 
     f32x4_t z[4] = {zero4(), zero4(), zero4(), zero4()};  // beta (v - E K S0)
-    f32x4_t o[4] = {zero4(), zero4(), zero4(), zero4()};  // scale E (Q S0), then all of the output
+    f32x4_t o[4] = {zero4(), zero4(), zero4(), zero4()};  // the output, where no other wave forms it
     {
       Frag<NT> fk[4];
       f32x4_t te[4], tr[4], tb[4];
@@ -917,8 +1000,14 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
       Frag<3> sf[KB];
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(S[2 * kb], S[2 * kb + 1]);
+      Frag<NP> so[KB];
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int n = 0; n < NP; ++n) so[kb].t[n] = sf[kb].t[n];
+      if constexpr (PAIR) hand_over<NP, KB>(lds + L::HS + cw * L::HSW, so, ln);
       row_product<2, KB>(z, fk, sK, TK::LD, TK::PLANE, sf, [&] {
-        if constexpr (!STATES) row_load<NT>(fk, sQ, TK::LD, TK::PLANE, ln);
+        if constexpr (!STATES && !PAIR) row_load<NT>(fk, sQ, TK::LD, TK::PLANE, ln);
         tok_load(te, tok + kTokE * C, ln);
         tok_load(tr, tok + kTokRk * C, ln);
         tok_load(tb, tok + kTokBeta * C, ln);
@@ -927,16 +1016,7 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
       for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
         for (int r = 0; r < 4; ++r) z[mt][r] = tb[mt][r] * (v[4 * mt + r] - te[mt][r] * tr[mt][r] * z[mt][r]);
-      if constexpr (!STATES) {
-        Frag<NP> so[KB];
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-          for (int n = 0; n < NP; ++n) so[kb].t[n] = sf[kb].t[n];
-        row_product<NP - 1, KB>(o, fk, sQ, TK::LD, TK::PLANE, so, [&] { tok_load(tr, tok + kTokRq * C, ln); }, ln);
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) o[mt] *= te[mt] * tr[mt] * p.scale;
-      }
+      if constexpr (!STATES && !PAIR) from_state(o, fk, so);
     }
     f32x4_t u[4] = {zero4(), zero4(), zero4(), zero4()};
     const float gamma = tok[kTokE * C + C - 1];
@@ -954,6 +1034,12 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
     if constexpr (MODE == kStates) {
       if (cg < p.nCG) store_image<4>(u, p.wU + ((bh * p.nC + c) * p.nCG + cg) * (C * kDeltaCols), ln);
     }
+    const Frag<NP> uf[2] = {split8<NP>(u[0], u[1]), split8<NP>(u[2], u[3])};
+    if constexpr (PAIR) {
+      hand_over<NP, 2>(lds + L::HU + cw * L::HUW, uf, ln);
+      __syncthreads();
+    }
+    ln = fresh_lane();
     if (c + 1 < c1) fetch(c + 1, wave * 64 + ln);
     {
       Frag<NT> fc[4];
@@ -966,15 +1052,9 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
       for (int i = 0; i < DK / 16; ++i) S[i] *= gamma;
       col_product<2, DK / 16>(S, fc, sK, TK::LD, TK::PLANE, df, [] {}, ln);
     }
-    if constexpr (!STATES) {
-      const Frag<NP> uf[2] = {split8<NP>(u[0], u[1]), split8<NP>(u[2], u[3])};
+    if constexpr (!STATES && !PAIR) {
       __syncthreads();  // P is complete
-      Trap<NP> fp;
-      trap_load(fp, sP, ln);
-      DELTA_FENCE();
-      trap_product<NP - 1>(o, fp, uf);
-      const int64_t t0 = int64_t(c) * C;
-      store_cols<ET, VEC>(o, obase + t0 * p.os1, p.os1, min(C, p.T - int(t0)), col, p.dvn, ln);
+      finish(o, uf, c);
     }
   }
   if constexpr (MODE == kOutputs) {
@@ -992,7 +1072,7 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
 }
 
 template <typename ET, int DK, int NW, bool VEC>
-__global__ __launch_bounds__(64 * NW, 1) void k_delta_scan(const DeltaParams p) {
+__global__ __launch_bounds__((ScanLds<ET, DK, false>::THREADS), 1) void k_delta_scan(const DeltaParams p) {
   extern __shared__ __align__(16) char lds[];
   delta_scan<ET, DK, NW, kOutputs, VEC>(p, lds, xcd_logical_block(blockIdx.x, gridDim.x));
 }
@@ -1353,8 +1433,8 @@ struct ImageTile {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int g = i / G, f = tid + NTHR * (i - g * G);
-      const int kb = f >> 7, l = (f >> 1) & 63, h = f & 1;
-      put4<NTERM>(m + (16 * g + (l & 15)) * ld + 32 * kb + 16 * h + 4 * (l >> 4), plane, i < G || second ? r[i] : zero4());
+      const int kb = f >> 7, h = (f >> 4) & 1, n = (f >> 3 & 12) + (f >> 2 & 3), q = f & 3;
+      put4<NTERM>(m + (16 * g + n) * ld + 32 * kb + 16 * h + 4 * q, plane, i < G || second ? r[i] : zero4());
     }
   }
 };
@@ -1393,11 +1473,19 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
 #pragma unroll
     for (int n = 0; n < NN; ++n) aq[mt][n] = ak[mt][n] = zero4();
 
-  auto element = [&](const uint16_t* m, int t, int d) {
+  // Element 16 mt + 4 q + r of a column that `f` holds the rows 32 (mt / 2) .. of.
+  auto element = [&](const Frag<NT>& f, int mt, int r) {
     float x = 0.f;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) x += __uint_as_float(uint32_t(m[i * TK::PLANE + t * TK::LD + place(d)]) << 16);
+    for (int i = NT - 1; i >= 0; --i) {
+      const uint32_t w = f.t[i][2 * (mt & 1) + (r >> 1)];
+      x += __uint_as_float(r & 1 ? w & 0xffff0000u : w << 16);
+    }
     return x;
+  };
+  auto columns = [&](Frag<NT>* f, const uint16_t* m, int kb) {
+#pragma unroll
+    for (int n = 0; n < NN; ++n) f[n] = colfrag<NT>(m, TK::LD, TK::PLANE, 32 * kb, dc + 16 * n, ln);
   };
   for (int gh = 0; gh < (ONE ? 1 : p.group); ++gh) {
     ln = fresh_lane();
@@ -1534,8 +1622,13 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
     __syncthreads();
     // q.os, k.rs and k.ug of every token over this wave's key columns, and os, rs, ug into dq', dk'
     ln = fresh_lane();
+    Frag<NT> cq[NN], ck[NN];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
+      if (mt % 2 == 0) {
+        columns(cq, sQ, mt / 2);
+        columns(ck, sK, mt / 2);
+      }
       const int t = 16 * mt + 4 * (ln >> 4);
       const f32x4_t e = ld4(tok + kTokE * C + t), be = ld4(tok + kTokBeta * C + t), d = ld4(tok + kTokD * C + t);
       const f32x4_t rk = ld4(tok + kTokRk * C + t), rq = ld4(tok + kTokRq * C + t);
@@ -1547,7 +1640,7 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
         ug[mt][n] *= rk * d;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float qe = element(sQ, t + r, dc + 16 * n + (ln & 15)), ke = element(sK, t + r, dc + 16 * n + (ln & 15));
+          const float qe = element(cq[n], mt, r), ke = element(ck[n], mt, r);
           a[r] += qe * os[mt][n][r];
           k1[r] += ke * rs[mt][n][r];
           k2[r] += ke * ug[mt][n][r];
@@ -1672,12 +1765,10 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
     ln = fresh_lane();
     Frag<NT> fk[2][NN], fq[2][NN];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int n = 0; n < NN; ++n) {
-        fk[kb][n] = colfrag<NT>(sK, TK::LD, TK::PLANE, 32 * kb, dc + 16 * n, ln);
-        fq[kb][n] = colfrag<NT>(sQ, TK::LD, TK::PLANE, 32 * kb, dc + 16 * n, ln);
-      }
+    for (int kb = 0; kb < 2; ++kb) {
+      columns(fk[kb], sK, kb);
+      columns(fq[kb], sQ, kb);
+    }
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
       Frag<NP> yr[2], kr[2], yc[2], kc[2];
@@ -1713,18 +1804,23 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
   ln = fresh_lane();
   const int q = ln >> 4, n16 = ln & 15;
   const bool unit = p.eps >= 0.f;
+  Frag<NT> cq[NN], ck[NN];
   if (unit) {
     __syncthreads();
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
+      if (mt % 2 == 0) {
+        columns(cq, sQ, mt / 2);
+        columns(ck, sK, mt / 2);
+      }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = 16 * mt + 4 * q + r;
         float a = 0.f, k = 0.f;
 #pragma unroll
         for (int n = 0; n < NN; ++n) {
-          a += aq[mt][n][r] * element(sQ, t, dc + 16 * n + n16);
-          k += ak[mt][n][r] * element(sK, t, dc + 16 * n + n16);
+          a += aq[mt][n][r] * element(cq[n], mt, r);
+          k += ak[mt][n][r] * element(ck[n], mt, r);
         }
         a = sum16(a);
         k = sum16(k);
@@ -1738,6 +1834,10 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
   }
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt) {
+    if (unit && mt % 2 == 0) {
+      columns(cq, sQ, mt / 2);
+      columns(ck, sK, mt / 2);
+    }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 16 * mt + 4 * q + r;
@@ -1757,8 +1857,8 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
         const int d = dc + 16 * n + n16;
         float a = aq[mt][n][r], k = ak[mt][n][r];
         if (unit) {
-          a -= pq * element(sQ, t, d);
-          k -= pk * element(sK, t, d);
+          a -= pq * element(cq[n], mt, r);
+          k -= pk * element(ck[n], mt, r);
         }
         if (t < rows && d < p.dkn) {
           stf<ET>(p.dq, b * p.dqs0 + (t0 + t) * p.dqs1 + hk * p.dqs2 + d, a);
@@ -1786,8 +1886,6 @@ hipError_t delta_prep_launch(const DeltaParams& p, hipStream_t s) {
   return launch_delta(k_delta_prep<ET, DK, VEC>, int64_t(p.B) * p.Hv * p.nC, 256, PrepLds<ET, DK>::BYTES, s, p);
 }
 
-constexpr int kScanWaves = 4;
-
 template <typename ET, int DK, bool VEC>
 hipError_t delta_fwd_dk(const DeltaParams& p, hipStream_t s) {
   constexpr int NW = kScanWaves;
@@ -1800,7 +1898,8 @@ hipError_t delta_fwd_dk(const DeltaParams& p, hipStream_t s) {
     if (e == hipSuccess && p.nSeg > 2) e = launch_delta(k_delta_join<DK>, bh * ncb, 256, 0, s, p, uint32_t(bh * ncb));
     if (e != hipSuccess) return e;
   }
-  return launch_delta(k_delta_scan<ET, DK, NW, VEC>, bh * p.nSeg * ncb, 64 * NW, ScanLds<ET, DK, false>::BYTES, s, p);
+  return launch_delta(k_delta_scan<ET, DK, NW, VEC>, bh * p.nSeg * ncb, ScanLds<ET, DK, false>::THREADS,
+                      ScanLds<ET, DK, false>::BYTES, s, p);
 }
 
 template <typename ET>
