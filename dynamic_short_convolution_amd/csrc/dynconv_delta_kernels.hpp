@@ -1514,29 +1514,26 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
         const bool second = cb + 1 < p.nCG;
         iu.load(p.wU + cim * (C * kDeltaCols), second, tid);
         ir.load(p.wR + cim * (C * kDeltaCols), second, tid);
-        is.load(p.wS + cim * (DK * 16), second, tid);
-        ig.load(p.wdS + cim * (DK * 16), second, tid);
         const int row = tid >> 2, c0 = cb * kDeltaCols + (tid & 3) * 8;
         const int n = row < rows ? p.dvn - c0 : 0;
         const uint32_t off = (uint32_t(row) * uint32_t(p.dos1) + uint32_t(c0)) * uint32_t(sizeof(ET));
         io = load8<ET, VEC>(chunk_rsrc<ET, VEC>(dobase, p.dos1, rows, p.dvn), n > 0 ? off : kNowhere, n);
       };
+      auto fetch_states = [&](int cb, int tid) {
+        const int64_t cim = ci * p.nCG + cb;
+        const bool second = cb + 1 < p.nCG;
+        is.load(p.wS + cim * (DK * 16), second, tid);
+        ig.load(p.wdS + cim * (DK * 16), second, tid);
+      };
+      fetch(0, tid);
       for (int cb = 0; cb < p.nCG; cb += 2) {
         ln = fresh_lane();
         const int tid = wave * 64 + ln;
         const bool second = cb + 1 < p.nCG;
-        // loaded here, not a block ahead: the registers that would take let the CU's other
-        // workgroup hide the latency instead
-        fetch(cb, tid);
+        fetch_states(cb, tid);  // under way during the products of U, dR and dO
         __syncthreads();  // the previous contents are read
         iu.template store<3>(sU, L::ULD, L::UPL, second, tid);
         ir.template store<3>(sR, L::ULD, L::UPL, second, tid);
-        is.template store<3>(sS, L::SLD, L::SPL, second, tid);
-#pragma unroll
-        for (int i = 0; i < ImageTile<KB, NTHR>::N; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (i < ImageTile<KB, NTHR>::G || second) through += is.r[i][e] * ig.r[i][e];
         {  // 64 rows of 4 pieces
           const Frag<NT> f = terms8<ET>(io);
           uint16_t* o = sO + (tid >> 2) * L::OLD + place((tid & 3) * 8);
@@ -1546,6 +1543,27 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
             *reinterpret_cast<u32x2*>(o + i * L::OPL + 8) = u32x2{f.t[i][2], f.t[i][3]};
           }
         }
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+          const int t = wave + NW * s;
+          if (t < 10) {
+            int ti, tj;
+            tile_of(t, ti, tj);
+            const auto fu = colfrag<3, true>(sU, L::ULD, L::UPL, 0, 16 * tj, ln);
+            const auto fo1 = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * ti, 0, ln);
+            const auto fr1 = colfrag<3, true>(sR, L::ULD, L::UPL, 0, 16 * ti, ln);
+            DELTA_FENCE();
+            mma<2>(dP[s], fu, fo1);
+            mma<2>(F[s], fu, fr1);
+          }
+        }
+        is.template store<3>(sS, L::SLD, L::SPL, second, tid);
+#pragma unroll
+        for (int i = 0; i < ImageTile<KB, NTHR>::N; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (i < ImageTile<KB, NTHR>::G || second) through += is.r[i][e] * ig.r[i][e];
         __syncthreads();
         {
           Frag<3> fs[NN], fr[2];
@@ -1569,23 +1587,10 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
             DELTA_FENCE();
           }
         }
-#pragma unroll
-        for (int s = 0; s < SLOTS; ++s) {
-          const int t = wave + NW * s;
-          if (t < 10) {
-            int ti, tj;
-            tile_of(t, ti, tj);
-            const auto fu = colfrag<3, true>(sU, L::ULD, L::UPL, 0, 16 * tj, ln);
-            const auto fo1 = rowfrag<NT>(sO, L::OLD, L::OPL, 16 * ti, 0, ln);
-            const auto fr1 = colfrag<3, true>(sR, L::ULD, L::UPL, 0, 16 * ti, ln);
-            DELTA_FENCE();
-            mma<2>(dP[s], fu, fo1);
-            mma<2>(F[s], fu, fr1);
-          }
-        }
         __syncthreads();  // S0 is read: dS1 takes its place
         ig.template store<3>(sS, L::SLD, L::SPL, second, tid);
         __syncthreads();
+        if (cb + 2 < p.nCG) fetch(cb + 2, wave * 64 + fresh_lane());
         {
           Frag<3> fg[NN], fu[2];
 #pragma unroll
