@@ -212,7 +212,7 @@ def _int64s(vals: tuple) -> ctypes.Array:
 def strides(vals) -> ctypes.Array:
     """vals as the constant int64 array of a C call. One array serves every call with the same
     values: building it took half of the time that a small call spends in Python."""
-    return _int64s(tuple(map(int, vals)))
+    return _int64s(tuple(vals))
 
 
 def check(fn: str, status: int) -> None:

@@ -6,7 +6,6 @@ current stream, nothing else.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -75,7 +74,7 @@ def _expect(name: str, t, shape, dtype) -> None:
     bounds instead of being refused."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {list(shape)}; got {list(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype} but must be {dtype}")
@@ -430,14 +429,26 @@ def dynconv_lowrank_decode_step(x, z, U, bias, cache, t: int, W: int, out=None, 
 # ----------------------------------------------------------------------------------
 
 
-def _on(dev):
-    """Makes dev the current device for a launch (its stream belongs to it)."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+def _launch(fn: str, dev, *args) -> None:
+    """Calls a C entry point on dev's current stream, with dev as the current device."""
+    call = getattr(_lib.load(), fn)
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)  # current_stream() builds an object: 2 us
+    if torch._C._cuda_getDevice() == dev.index:
+        st = call(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = call(*args, stream)
+    if st != 0:
+        _lib.check(fn, st)
 
 
 def _sp(t):
     """(pointer, strides) of a tensor, or two NULLs."""
-    return (_ptr(t), _lib.strides(t.stride())) if t is not None else (None, None)
+    return (t.data_ptr(), _lib.strides(t.stride())) if t is not None else (None, None)
+
+
+def _dp(t):
+    return t.data_ptr() if t is not None else None
 
 
 def _delta_shapes(q, k, v, g, beta, token: bool):
@@ -449,14 +460,15 @@ def _delta_shapes(q, k, v, g, beta, token: bool):
         raise ValueError(f"q must be {lead_name}; got shape {list(q.shape)}")
     if v.dim() != n:
         raise ValueError(f"v must be {lead_name.replace('k', 'v')}; got shape {list(v.shape)}")
-    lead, (Hk, dk), (Hv, dv) = tuple(q.shape[:-2]), tuple(q.shape[-2:]), tuple(v.shape[-2:])
+    (*lead, Hk, dk), (Hv, dv) = q.shape, v.shape[-2:]
     if Hk < 1 or Hv % Hk != 0:
         raise ValueError(f"the {Hv} value heads must be a multiple of the {Hk} key heads")
     _dtype_code(q)
-    _expect("k", k, (*lead, Hk, dk), q.dtype)
-    _expect("v", v, (*lead, Hv, dv), q.dtype)
-    _expect("g", g, (*lead, Hv), torch.float32)
-    _expect("beta", beta, (*lead, Hv), q.dtype)
+    heads = (*lead, Hv)
+    _expect("k", k, q.shape, q.dtype)
+    _expect("v", v, (*heads, dv), q.dtype)
+    _expect("g", g, heads, torch.float32)
+    _expect("beta", beta, heads, q.dtype)
     return lead, Hk, Hv, dk, dv
 
 
@@ -494,15 +506,11 @@ def dynconv_delta_fwd(q, k, v, g, beta, scale: float | None = None, qk_norm_eps:
     o = torch.empty((B, T, Hv, dv), dtype=q.dtype, device=dev) if out is None else out
     if want_state and state_out is None:
         state_out = torch.empty((B, Hv, dk, dv), dtype=torch.float32, device=dev)
-    lib = _lib.load()
     code = _dtype_code(q)
-    ws_bytes = int(lib.dynconv_delta_fwd_workspace_size(B, T, Hk, Hv, dk, dv, code))
+    ws_bytes = int(_lib.load().dynconv_delta_fwd_workspace_size(B, T, Hk, Hv, dk, dv, code))
     work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
-    with _on(dev):
-        st = lib.dynconv_delta_fwd(*_sp(q), *_sp(k), *_sp(v), *_sp(g), *_sp(beta), *seg, *_sp(state), *_sp(o),
-                                   *_sp(state_out), B, T, Hk, Hv, dk, dv, scale, eps, code, _ptr(work), ws_bytes,
-                                   _stream(dev))
-    _lib.check("dynconv_delta_fwd", st)
+    _launch("dynconv_delta_fwd", dev, *_sp(q), *_sp(k), *_sp(v), *_sp(g), *_sp(beta), *seg, *_sp(state), *_sp(o),
+            *_sp(state_out), B, T, Hk, Hv, dk, dv, scale, eps, code, _dp(work), ws_bytes)
     return o if state_out is None else (o, state_out)
 
 
@@ -529,16 +537,12 @@ def dynconv_delta_bwd(q, k, v, g, beta, do, scale: float | None = None, qk_norm_
     if need_dstate:  # without tokens the state's gradient passes through
         dstate = new((B, Hv, dk, dv), torch.float32) if T else (
             torch.zeros((B, Hv, dk, dv), dtype=torch.float32, device=dev) if dstate_out is None else dstate_out.clone())
-    lib = _lib.load()
     code = _dtype_code(q)
-    ws_bytes = int(lib.dynconv_delta_bwd_workspace_size(B, T, Hk, Hv, dk, dv, code))
+    ws_bytes = int(_lib.load().dynconv_delta_bwd_workspace_size(B, T, Hk, Hv, dk, dv, code))
     work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
-    with _on(dev):
-        st = lib.dynconv_delta_bwd(*_sp(q), *_sp(k), *_sp(v), *_sp(g), *_sp(beta), *seg, *_sp(state), *_sp(do),
-                                   *_sp(dstate_out), *_sp(dq), *_sp(dk_), *_sp(dv_), *_sp(dg), *_sp(dbeta),
-                                   *_sp(dstate), B, T, Hk, Hv, dk, dv, scale, eps, code, _ptr(work), ws_bytes,
-                                   _stream(dev))
-    _lib.check("dynconv_delta_bwd", st)
+    _launch("dynconv_delta_bwd", dev, *_sp(q), *_sp(k), *_sp(v), *_sp(g), *_sp(beta), *seg, *_sp(state), *_sp(do),
+            *_sp(dstate_out), *_sp(dq), *_sp(dk_), *_sp(dv_), *_sp(dg), *_sp(dbeta), *_sp(dstate), B, T, Hk, Hv, dk,
+            dv, scale, eps, code, _dp(work), ws_bytes)
     return dq, dk_, dv_, dg, dbeta, dstate
 
 
@@ -553,10 +557,8 @@ def dynconv_delta_step(q, k, v, g, beta, state, scale: float | None = None, qk_n
     _expect("out", out, (B, Hv, dv), q.dtype)
     dev = _require_device(q, k, v, g, beta, state, out)
     o = torch.empty((B, Hv, dv), dtype=q.dtype, device=dev) if out is None else out
-    with _on(dev):
-        st = _lib.load().dynconv_delta_step(*_sp(q), *_sp(k), *_sp(v), *_sp(g), *_sp(beta), *_sp(state), *_sp(o), B,
-                                            Hk, Hv, dk, dv, scale, eps, _dtype_code(q), _stream(dev))
-    _lib.check("dynconv_delta_step", st)
+    _launch("dynconv_delta_step", dev, *_sp(q), *_sp(k), *_sp(v), *_sp(g), *_sp(beta), *_sp(state), *_sp(o), B, Hk, Hv,
+            dk, dv, scale, eps, _dtype_code(q))
     return o
 
 
@@ -570,12 +572,12 @@ _NORM_RESIDUAL = {None: 0, "before": 1, "after": 2}
 def _norm_shape(x):
     if not 1 <= x.dim() <= 4:
         raise ValueError(f"x must have 1 to 4 dimensions; got shape {list(x.shape)}")
-    return (1,) * (4 - x.dim()) + tuple(x.shape)
+    return (1,) * (4 - x.dim()) + x.shape
 
 
 def _sp4(t):
     """(pointer, four strides) of a tensor of up to 4 dimensions, or two NULLs."""
-    return (_ptr(t), _lib.strides([0] * (4 - t.dim()) + list(t.stride()))) if t is not None else (None, None)
+    return (t.data_ptr(), _lib.strides((0,) * (4 - t.dim()) + t.stride())) if t is not None else (None, None)
 
 
 def _norm_weight(weight, x):
@@ -606,11 +608,8 @@ def dynconv_norm_fwd(x, weight=None, gate=None, residual=None, residual_scale: f
     dev = _require_device(x, weight, gate, residual, out, out_h)
     y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
     h = (torch.empty(x.shape, dtype=x.dtype, device=dev) if out_h is None else out_h) if before else None
-    with _on(dev):
-        st = _lib.load().dynconv_norm_fwd(*_sp4(x), _ptr(weight), *_sp4(gate), *_sp4(residual),
-                                          int(residual_at == "after"), float(residual_scale), *_sp4(y), *_sp4(h),
-                                          *shape, float(eps), code, _stream(dev))
-    _lib.check("dynconv_norm_fwd", st)
+    _launch("dynconv_norm_fwd", dev, *_sp4(x), _dp(weight), *_sp4(gate), *_sp4(residual), int(residual_at == "after"),
+            float(residual_scale), *_sp4(y), *_sp4(h), *shape, float(eps), code)
     return (y, h) if before else y
 
 
@@ -637,12 +636,9 @@ def dynconv_norm_bwd(x, weight, dy, gate=None, dh=None, residual_scale: float = 
 
     dx, dres, dgate = new(), new() if residual_at == "before" else None, new() if gate is not None else None
     dw = torch.empty((x.shape[-1],), dtype=torch.float32, device=dev) if weight is not None else None
-    lib = _lib.load()
-    ws_bytes = int(lib.dynconv_norm_bwd_workspace_size(*shape, code)) if dw is not None else 0
+    ws_bytes = int(_lib.load().dynconv_norm_bwd_workspace_size(*shape, code)) if dw is not None else 0
     work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
-    with _on(dev):
-        st = lib.dynconv_norm_bwd(*_sp4(x), _ptr(weight), *_sp4(gate), *_sp4(dy), *_sp4(dh),
-                                  _NORM_RESIDUAL[residual_at], float(residual_scale), *_sp4(dx), *_sp4(dres), _ptr(dw),
-                                  *_sp4(dgate), *shape, float(eps), code, _ptr(work), ws_bytes, _stream(dev))
-    _lib.check("dynconv_norm_bwd", st)
+    _launch("dynconv_norm_bwd", dev, *_sp4(x), _dp(weight), *_sp4(gate), *_sp4(dy), *_sp4(dh),
+            _NORM_RESIDUAL[residual_at], float(residual_scale), *_sp4(dx), *_sp4(dres), _dp(dw), *_sp4(dgate), *shape,
+            float(eps), code, _dp(work), ws_bytes)
     return dx, dres, dw, dgate
