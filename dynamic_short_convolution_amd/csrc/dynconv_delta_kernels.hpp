@@ -1324,52 +1324,68 @@ __global__ __launch_bounds__(64 * NW, Store<ET>::NT == 1 ? 2 : 1) void k_delta_e
   delta_scan<ET, DK, NW, kEnds, VEC>(p, lds, xcd_logical_block(blockIdx.x, gridDim.x));
 }
 
-// Joins the segments of one (sequence, head), 16 columns per wave: wEnd[g] = M_g wEnd[g-1] +
-// wEnd[g] for g = 1 .. nSeg-2, in place, so that wEnd[g] is what segment g + 1 starts from. The
-// workgroups from `fwd` on do the same backwards with the transposed M on wBegin.
+// Joins the segments of one (sequence, head) for 16 columns: wEnd[g] = M_g wEnd[g-1] + wEnd[g]
+// for g = 1 .. nSeg-2, in place, so that wEnd[g] is what segment g + 1 starts from. The
+// workgroups from `fwd` on do the same backwards with the transposed M on wBegin. A wave owns 32
+// rows of the result and splits only their part of M into terms, which is most of a step's work
+// (one wave for all rows: 57 us for 8 segments of 16 heads of 128 x 128, in four 23).
 template <int DK>
-__global__ __launch_bounds__(256, 1) void k_delta_join(const DeltaParams p, uint32_t fwd) {
+__global__ __launch_bounds__(2 * DK) void k_delta_join(const DeltaParams p, uint32_t fwd) {
   constexpr int KB = DK / 32;
-  const int ln = threadIdx.x & 63, wave = threadIdx.x >> 6, q = ln >> 4, n16 = ln & 15;
+  __shared__ __align__(16) char terms[2][KB * 3 * 1024];
+  const int ln = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = ln >> 4, n16 = ln & 15;
   const bool rev = blockIdx.x >= fwd;
   const uint32_t bid = rev ? blockIdx.x - fwd : blockIdx.x;
-  const int ncb = delta_cols(p, 4);
-  const int cg = int(bid % ncb) * 4 + wave;
-  const int64_t bh = bid / ncb;
-  if (cg >= p.nCG) return;
+  const int cg = int(bid % p.nCG);
+  const int64_t bh = bid / p.nCG;
   float* w = rev ? p.wBegin : p.wEnd;
-  auto image = [&](int g) { return w + ((bh * p.nSeg + g) * p.nCG + cg) * (DK * 16); };
-  f32x4_t S[DK / 16];
-  load_image<DK / 16>(S, image(rev ? p.nSeg - 1 : 0), ln);
-  for (int s = 1; s + 1 < p.nSeg; ++s) {
-    const int g = rev ? p.nSeg - 1 - s : s;
-    const auto* M = in_global<float>(p.wM + (bh * p.nSeg + g) * (DK * DK));
-    Frag<3> sf[KB];
+  auto segment = [&](int s) { return rev ? p.nSeg - 1 - s : s; };
+  auto image = [&](int s) { return w + ((bh * p.nSeg + segment(s)) * p.nCG + cg) * (DK * 16) + wave * 512; };
+  // rows (columns, in reverse) 16 i .. of M, as left operands
+  struct Rows {
+    f32x4_t a[KB], b[KB];
+  };
+  auto load = [&](Rows& m, int s, int i) {
+    const auto* M = in_global<float>(p.wM + (bh * p.nSeg + segment(s)) * (DK * DK));
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(S[2 * kb], S[2 * kb + 1]);
-    load_image<DK / 16>(S, image(g), ln);
+    for (int kb = 0; kb < KB; ++kb) {
+      if (!rev) {
+        const auto* row = M + (16 * i + n16) * DK + 32 * kb + 4 * q;
+        m.a[kb] = *(const global_t<f32x4_t>*)row;
+        m.b[kb] = *(const global_t<f32x4_t>*)(row + 16);
+      } else {
+        const auto* column = M + (32 * kb + 4 * q) * DK + 16 * i + n16;
 #pragma unroll
-    for (int i = 0; i < DK / 16; ++i) {
-      f32x4_t a[KB], b[KB];
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        if (!rev) {
-          const auto* row = M + (16 * i + n16) * DK + 32 * kb + 4 * q;
-          a[kb] = *(const global_t<f32x4_t>*)row;
-          b[kb] = *(const global_t<f32x4_t>*)(row + 16);
-        } else {
-          const auto* column = M + (32 * kb + 4 * q) * DK + 16 * i + n16;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            a[kb][r] = column[r * DK];
-            b[kb][r] = column[(16 + r) * DK];
-          }
+        for (int r = 0; r < 4; ++r) {
+          m.a[kb][r] = column[r * DK];
+          m.b[kb][r] = column[(16 + r) * DK];
         }
       }
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) mma<2>(S[i], split8<3>(a[kb], b[kb]), sf[kb]);
     }
-    store_image<DK / 16>(S, image(g), ln);
+  };
+  Rows m[2];
+  f32x4_t S[2], next[2];
+  load_image<2>(S, image(0), ln);
+  load_image<2>(next, image(1), ln);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) load(m[i], 1, 2 * wave + i);
+  for (int s = 1; s + 1 < p.nSeg; ++s) {
+    const Frag<3> own = split8<3>(S[0], S[1]);
+    hand_over<3, 1>(terms[s & 1] + wave * 3072, &own, ln);
+    const int after = min(s + 1, p.nSeg - 2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) S[i] = next[i];
+    load_image<2>(next, image(after), ln);
+    __syncthreads();  // of the two buffers the other is free: its readers have come here
+    Frag<3> sf[KB];
+    take_over<3, KB>(sf, terms[s & 1], ln);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) mma<2>(S[i], split8<3>(m[i].a[kb], m[i].b[kb]), sf[kb]);
+      load(m[i], after, 2 * wave + i);
+    }
+    store_image<2>(S, image(s), ln);
   }
 }
 
@@ -1900,7 +1916,7 @@ hipError_t delta_fwd_dk(const DeltaParams& p, hipStream_t s) {
   if (p.nSeg > 1) {
     e = launch_delta(k_delta_ends<ET, DK, NW, VEC>, bh * p.nSeg * (ncb + DK / kDeltaCols / NW), 64 * NW,
                      ScanLds<ET, DK, true>::BYTES, s, p);
-    if (e == hipSuccess && p.nSeg > 2) e = launch_delta(k_delta_join<DK>, bh * ncb, 256, 0, s, p, uint32_t(bh * ncb));
+    if (e == hipSuccess && p.nSeg > 2) e = launch_delta(k_delta_join<DK>, bh * p.nCG, 2 * DK, 0, s, p, uint32_t(bh * p.nCG));
     if (e != hipSuccess) return e;
   }
   return launch_delta(k_delta_scan<ET, DK, NW, VEC>, bh * p.nSeg * ncb, ScanLds<ET, DK, false>::THREADS,
@@ -1924,7 +1940,7 @@ hipError_t delta_bwd_dk(const DeltaParams& p, hipStream_t s) {
   if (p.nSeg > 1) {
     e = launch_delta(k_delta_scans<ET, DK, NW, true, VEC>, 2 * blocks + bh * p.nSeg * (DK / kDeltaCols / NW), 64 * NW,
                      scans_lds, s, p, uint32_t(blocks));
-    if (e == hipSuccess && p.nSeg > 2) e = launch_delta(k_delta_join<DK>, 2 * bh * ncb, 256, 0, s, p, uint32_t(bh * ncb));
+    if (e == hipSuccess && p.nSeg > 2) e = launch_delta(k_delta_join<DK>, 2 * bh * p.nCG, 2 * DK, 0, s, p, uint32_t(bh * p.nCG));
     if (e != hipSuccess) return e;
   }
   e = launch_delta(k_delta_scans<ET, DK, NW, false, VEC>, 2 * blocks, 64 * NW, scans_lds, s, p, uint32_t(blocks));
