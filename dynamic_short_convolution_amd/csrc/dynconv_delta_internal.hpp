@@ -62,15 +62,18 @@ struct DeltaParams {
 constexpr int delta_dk_pad(int dk) { return dk <= 64 ? 64 : 128; }
 
 // Segments that the scans cut a sequence's chunks into. They pay where one segment per sequence
-// and head leaves most of the 256 CUs idle: the first pass costs about what the second does, and
-// joining about 3 chunks' time per segment, so each gets at least 8 chunks and there are at
-// least 3 (B1 T32768, 16 heads of 128 x 128, bf16: 2.50 ms in one
-// segment, 0.72 in 8).
+// and head leaves most of the 256 CUs idle: with n segments of nC / n chunks the two passes take
+// about 2 nC / n chunks' time, joining about a third of one per segment and the two more launches
+// one, which is least for n = sqrt(6 nC); a segment has at least 2 chunks, and from 8 chunks and
+// 3 segments on it is less than the nC of one pass (16 heads of 128 x 128, bf16, forward /
+// backward in us, one segment and as many as here: T 400 45 / 95 and 51 / 98, T 512 47 / 104 and
+// 47 / 91, T 1024 80 / 163 and 58 / 112, T 32768 forward 2500 and 694).
 constexpr int delta_segment_length(int64_t bh, int64_t nC, int64_t nCG) {
   const int64_t blocks = bh * ((nCG + 3) / 4);
   int64_t n = blocks > 0 ? 256 / blocks : 1;
-  if (n > nC / 8) n = nC / 8;
-  if (n < 3) return nC > 0 ? int(nC) : 1;
+  if (n > nC / 2) n = nC / 2;
+  while (n * n > 6 * nC) --n;
+  if (n < 3 || nC < 8) return nC > 0 ? int(nC) : 1;
   return int((nC + n - 1) / n);
 }
 

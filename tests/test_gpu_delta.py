@@ -125,6 +125,14 @@ def test_long_sequences_in_segments(shape, docs, dtype):
     check(args, seq=documents(8, B, T, docs) if docs else None, state=rand(5, B, Hv, dk, dv), dstate_out=rand(6, B, Hv, dk, dv))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T", [448, 449, 577])
+def test_shortest_segments(T, dtype):
+    """7 chunks (one segment), 8 (four of two) and 10 (four of two and the last of one)."""
+    args = make(31, 1, T, 1, 2, 40, 24, dtype, decay=0.05)
+    check(args, state=rand(32, 1, 2, 40, 24), dstate_out=rand(33, 1, 2, 40, 24))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_extreme_gates(dtype):
     """No write (beta 0), no decay, decays to zero (-inf, -1e30, below float32's exp), long sums
