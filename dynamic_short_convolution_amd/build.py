@@ -53,11 +53,11 @@ COMPILE_FLAGS = [
     "-amdgpu-mfma-vgpr-form",
 ]
 
-# Sources whose kernels use more than 256 registers are built without the last two flags: past
-# 256, the compiler's pass that moves VGPR-form matrix-core operands to accumulation registers
-# has crashed here, and gave wrong sums in one instantiation (float32, two value heads per key
-# head, unaligned rows). Within 256 registers the flags make no difference to these kernels;
-# the one that needs more, the forward scan, takes 368 us instead of 342 without them.
+# Sources with kernels of more than 256 registers are built without the last two flags: past 256,
+# the compiler's pass that moves VGPR-form matrix-core operands to accumulation registers has
+# crashed here, and gave wrong sums in one instantiation (float32, two value heads per key head,
+# unaligned rows). Within 256 registers, as in bfloat16, the flags change these kernels' times
+# by less than 2 %.
 PLAIN_MFMA_SOURCES = ("dynconv_delta_f32.hip", "dynconv_delta_bf16.hip", "dynconv_delta_f16.hip")
 
 

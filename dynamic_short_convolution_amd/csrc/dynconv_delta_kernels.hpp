@@ -1406,10 +1406,14 @@ __global__ __launch_bounds__(2 * DK) void k_delta_join(const DeltaParams p, uint
 // rk (k.rs) and out = D rk (k.ug); the cumulative sums are in 64 bits. dbeta_i = dR_i.V_i -
 // E rk (k.rs)_i + sum_j dA_ij Gam k.k. What reaches dg keeps all terms (float32).
 
-template <typename ET, int DK>
+template <typename ET, int DK, bool ONE>
 struct GradLds {
   static constexpr int NT = Store<ET>::NT, NP = Store<ET>::NP;
-  static constexpr int NW = 4;  // waves, each with DK / 64 16-wide tiles of key columns
+  // Waves, each with DK / NW key columns. Four, and two workgroups per CU, where registers (no
+  // sums over heads) and LDS (bf16) allow it, or 64 columns leave no more; else one workgroup of
+  // eight (2016 chunks and heads of 128, pairs of them on one key head, bf16: 245 us with four,
+  // 225 with eight).
+  static constexpr int NW = DK == 128 && !(NT == 1 && ONE) ? 8 : 4;
   static constexpr int ULD = C + kPad, OLD = 32 + kPad, SLD = DK + kPad;
   static constexpr int UPL = 32 * ULD, OPL = C * OLD, SPL = 32 * SLD;
   // first part: staged operands of 32 value columns
@@ -1433,14 +1437,15 @@ struct GradLds {
 // rows of a [columns][index] LDS matrix of N terms.
 template <int NB, int NTHR>
 struct ImageTile {
-  static constexpr int G = NB * 128 / NTHR, N = 2 * G;  // pieces per thread of a group, and in all
-  static_assert(NB * 128 % NTHR == 0, "whole passes");
+  static constexpr int P = NB * 128, N = 2 * P / NTHR;  // pieces of a group, and of a thread
+  static_assert(2 * P % NTHR == 0 && (P % NTHR == 0 || NTHR == 2 * P), "whole passes");
   f32x4_t r[N];
+  static __device__ __forceinline__ bool first(int i, int tid) { return i * NTHR + (NTHR > P ? tid : 0) < P; }
   // `second`: whether the second group exists (it follows the first); if not, zeros.
   __device__ __forceinline__ void load(const float* src, bool second, int tid) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const auto* base = in_global<char>(src) + (i < G || second ? i * NTHR * 16 : (i - G) * NTHR * 16);
+      const auto* base = in_global<char>(src) + (i * NTHR - (first(i, tid) || second ? 0 : P)) * 16;
       r[i] = *(const global_t<f32x4_t>*)(base + uint32_t(tid) * 16u);
     }
   }
@@ -1448,18 +1453,19 @@ struct ImageTile {
   __device__ __forceinline__ void store(uint16_t* m, int ld, int plane, bool second, int tid) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int g = i / G, f = tid + NTHR * (i - g * G);
+      const int g = first(i, tid) ? 0 : 1, f = tid + NTHR * i - P * g;
       const int kb = f >> 7, h = (f >> 4) & 1, n = (f >> 3 & 12) + (f >> 2 & 3), q = f & 3;
-      put4<NTERM>(m + (16 * g + n) * ld + 32 * kb + 16 * h + 4 * q, plane, i < G || second ? r[i] : zero4());
+      put4<NTERM>(m + (16 * g + n) * ld + 32 * kb + 16 * h + 4 * q, plane, g == 0 || second ? r[i] : zero4());
     }
   }
 };
 
 // ONE: a single value head per key head (no sums to carry from head to head).
 template <typename ET, int DK, bool VEC, bool ONE>
-__global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delta_grad(const DeltaParams p) {
-  using L = GradLds<ET, DK>;
-  constexpr int NT = L::NT, NP = L::NP, LV = NP - 1, KB = DK / 32, NN = DK / 64, NW = L::NW, NTHR = 64 * NW;
+__global__ __launch_bounds__((64 * GradLds<ET, DK, ONE>::NW), (Store<ET>::NT == 1 && ONE ? 2 : 1)) void k_delta_grad(
+    const DeltaParams p) {
+  using L = GradLds<ET, DK, ONE>;
+  constexpr int NT = L::NT, NP = L::NP, LV = NP - 1, KB = DK / 32, NW = L::NW, NN = DK / 16 / NW, NTHR = 64 * NW;
   constexpr int SLOTS = (10 + NW - 1) / NW;  // tiles of a triangle per wave
   using TK = Tile<ET, DK, NTHR, VEC>;
   static_assert(L::BYTES <= kLdsBytes, "LDS of a CU");
@@ -1531,7 +1537,7 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
         iu.load(p.wU + cim * (C * kDeltaCols), second, tid);
         ir.load(p.wR + cim * (C * kDeltaCols), second, tid);
         const int row = tid >> 2, c0 = cb * kDeltaCols + (tid & 3) * 8;
-        const int n = row < rows ? p.dvn - c0 : 0;
+        const int n = row < rows ? p.dvn - c0 : 0;  // (row 64 and on, of a workgroup of 512: none)
         const uint32_t off = (uint32_t(row) * uint32_t(p.dos1) + uint32_t(c0)) * uint32_t(sizeof(ET));
         io = load8<ET, VEC>(chunk_rsrc<ET, VEC>(dobase, p.dos1, rows, p.dvn), n > 0 ? off : kNowhere, n);
       };
@@ -1550,7 +1556,7 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
         __syncthreads();  // the previous contents are read
         iu.template store<3>(sU, L::ULD, L::UPL, second, tid);
         ir.template store<3>(sR, L::ULD, L::UPL, second, tid);
-        {  // 64 rows of 4 pieces
+        if (NTHR == 4 * C || tid < 4 * C) {  // 64 rows of 4 pieces
           const Frag<NT> f = terms8<ET>(io);
           uint16_t* o = sO + (tid >> 2) * L::OLD + place((tid & 3) * 8);
 #pragma unroll
@@ -1579,7 +1585,7 @@ __global__ __launch_bounds__(256, Store<ET>::NT == 1 && ONE ? 2 : 1) void k_delt
         for (int i = 0; i < ImageTile<KB, NTHR>::N; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (i < ImageTile<KB, NTHR>::G || second) through += is.r[i][e] * ig.r[i][e];
+            if (is.first(i, tid) || second) through += is.r[i][e] * ig.r[i][e];
         __syncthreads();
         {
           Frag<3> fs[NN], fr[2];
@@ -1946,9 +1952,10 @@ hipError_t delta_bwd_dk(const DeltaParams& p, hipStream_t s) {
   e = launch_delta(k_delta_scans<ET, DK, NW, false, VEC>, 2 * blocks, 64 * NW, scans_lds, s, p, uint32_t(blocks));
   if (e != hipSuccess) return e;
   const int64_t chunks = int64_t(p.B) * p.Hk * p.nC;
-  constexpr int threads = 64 * GradLds<ET, DK>::NW;
-  if (p.group == 1) return launch_delta(k_delta_grad<ET, DK, VEC, true>, chunks, threads, GradLds<ET, DK>::BYTES, s, p);
-  return launch_delta(k_delta_grad<ET, DK, VEC, false>, chunks, threads, GradLds<ET, DK>::BYTES, s, p);
+  using One = GradLds<ET, DK, true>;
+  using Group = GradLds<ET, DK, false>;
+  if (p.group == 1) return launch_delta(k_delta_grad<ET, DK, VEC, true>, chunks, 64 * One::NW, One::BYTES, s, p);
+  return launch_delta(k_delta_grad<ET, DK, VEC, false>, chunks, 64 * Group::NW, Group::BYTES, s, p);
 }
 
 template <typename ET>
