@@ -201,7 +201,7 @@ dynconv_status dynconv_delta_bwd(const void* q, const int64_t* qs, const void* k
   if ((st = check_tensor(dv_, dvs, 4, ev, eb, true, true)) != DYNCONV_OK) return st;
   if ((st = check_tensor(dg, dgs, 3, eg, 4, false, true)) != DYNCONV_OK) return st;
   if ((st = check_tensor(dbeta, dbs, 3, eg, eb, false, true)) != DYNCONV_OK) return st;
-  if (far_tokens(dos, T) || far_tokens(dvs, T)) return DYNCONV_ERR_UNSUPPORTED;
+  if (far_tokens(dos, T) || far_tokens(dvs, T) || far_tokens(dqs, T) || far_tokens(dks, T)) return DYNCONV_ERR_UNSUPPORTED;
   p.dO = dO, p.dq = dq, p.dk = dk_, p.dv = dv_, p.dg = dg, p.dbeta = dbeta;
   p.dos0 = dos[0], p.dos1 = dos[1], p.dos2 = dos[2];
   p.dqs0 = dqs[0], p.dqs1 = dqs[1], p.dqs2 = dqs[2];
@@ -209,7 +209,8 @@ dynconv_status dynconv_delta_bwd(const void* q, const int64_t* qs, const void* k
   p.dvs0 = dvs[0], p.dvs1 = dvs[1], p.dvs2 = dvs[2];
   p.dgs0 = dgs[0], p.dgs1 = dgs[1], p.dgs2 = dgs[2];
   p.dbs0 = dbs[0], p.dbs1 = dbs[1], p.dbs2 = dbs[2];
-  p.vec = p.vec && dv % 8 == 0 && wide(dO, dos, 4, ev, eb) && apart(dos, ev) && apart(dvs, ev);
+  p.vec = p.vec && dv % 8 == 0 && wide(dO, dos, 4, ev, eb) && apart(dos, ev) && apart(dvs, ev) &&
+          apart(dqs, eq) && apart(dks, eq);
   if (dstate_out != nullptr) {
     if ((st = check_tensor(dstate_out, dsos, 4, est, 4, true, false)) != DYNCONV_OK) return st;
     p.dstate_out = dstate_out;

@@ -1840,57 +1840,61 @@ __global__ __launch_bounds__((64 * GradLds<ET, DK, ONE>::NW), (Store<ET>::NT == 
         columns(cq, sQ, mt / 2);
         columns(ck, sK, mt / 2);
       }
+      f32x4_t a = zero4(), k = zero4();
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int t = 16 * mt + 4 * q + r;
-        float a = 0.f, k = 0.f;
 #pragma unroll
         for (int n = 0; n < NN; ++n) {
-          a += aq[mt][n][r] * element(cq[n], mt, r);
-          k += ak[mt][n][r] * element(ck[n], mt, r);
+          a[r] += aq[mt][n][r] * element(cq[n], mt, r);
+          k[r] += ak[mt][n][r] * element(ck[n], mt, r);
         }
-        a = sum16(a);
-        k = sum16(k);
-        if (n16 == 0) {
-          sum[wave * C + t] = a;
-          sum[(NW + wave) * C + t] = k;
-        }
+        a[r] = sum16(a[r]);
+        k[r] = sum16(k[r]);
+      }
+      if (n16 == 0) {
+        *reinterpret_cast<f32x4_t*>(sum + wave * C + 16 * mt + 4 * q) = a;
+        *reinterpret_cast<f32x4_t*>(sum + (NW + wave) * C + 16 * mt + 4 * q) = k;
       }
     }
     __syncthreads();
   }
+  const __amdgpu_buffer_rsrc_t outq = chunk_rsrc<ET, VEC>(
+      static_cast<ET*>(p.dq) + b * p.dqs0 + hk * p.dqs2 + t0 * p.dqs1, p.dqs1, rows, p.dkn);
+  const __amdgpu_buffer_rsrc_t outk = chunk_rsrc<ET, VEC>(
+      static_cast<ET*>(p.dk) + b * p.dks0 + hk * p.dks2 + t0 * p.dks1, p.dks1, rows, p.dkn);
+  const uint32_t pitchq = uint32_t(p.dqs1) * uint32_t(sizeof(ET)), pitchk = uint32_t(p.dks1) * uint32_t(sizeof(ET));
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt) {
-    if (unit && mt % 2 == 0) {
-      columns(cq, sQ, mt / 2);
-      columns(ck, sK, mt / 2);
+    f32x4_t pq = zero4(), pk = zero4();
+    if (unit) {
+      if (mt % 2 == 0) {
+        columns(cq, sQ, mt / 2);
+        columns(ck, sK, mt / 2);
+      }
+      const int t = 16 * mt + 4 * q;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        pq += ld4(sum + w * C + t);
+        pk += ld4(sum + (NW + w) * C + t);
+      }
+      const f32x4_t rq = ld4(tok + kTokRq * C + t), rk = ld4(tok + kTokRk * C + t);
+      pq *= rq * rq;
+      pk *= rk * rk;
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 16 * mt + 4 * q + r;
-      float pq = 0.f, pk = 0.f;
-      if (unit) {
-        const float rq = tok[kTokRq * C + t], rk = tok[kTokRk * C + t];
+    for (int n = 0; n < NN; ++n) {
+      const int d = dc + 16 * n + n16;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          pq += sum[w * C + t];
-          pk += sum[(NW + w) * C + t];
-        }
-        pq *= rq * rq;
-        pk *= rk * rk;
-      }
-#pragma unroll
-      for (int n = 0; n < NN; ++n) {
-        const int d = dc + 16 * n + n16;
+      for (int r = 0; r < 4; ++r) {
         float a = aq[mt][n][r], k = ak[mt][n][r];
         if (unit) {
-          a -= pq * element(cq[n], mt, r);
-          k -= pk * element(ck[n], mt, r);
+          a -= pq[r] * element(cq[n], mt, r);
+          k -= pk[r] * element(ck[n], mt, r);
         }
-        if (t < rows && d < p.dkn) {
-          stf<ET>(p.dq, b * p.dqs0 + (t0 + t) * p.dqs1 + hk * p.dqs2 + d, a);
-          stf<ET>(p.dk, b * p.dks0 + (t0 + t) * p.dks1 + hk * p.dks2 + d, k);
-        }
+        const int t = 16 * mt + r;  // + 4 q
+        const bool in = d < p.dkn && (VEC || t + 4 * q < rows);
+        buf_st<ET>(outq, in ? (4 * q + t) * pitchq + uint32_t(d) * uint32_t(sizeof(ET)) : kNowhere, a);
+        buf_st<ET>(outk, in ? (4 * q + t) * pitchk + uint32_t(d) * uint32_t(sizeof(ET)) : kNowhere, k);
       }
     }
   }

@@ -234,12 +234,12 @@ def test_delta_fwd_validation(lib, kw, status):
     assert fwd(lib, **kw) == status
 
 
-def bwd(lib, dO=DO, dos=None, dso=None, dq=DQ, dk_=DK_, dv_=DV_, dg=DG, db=DB, dsi=None, dqs=None, dgs=None, dvs=None, ws=None,
-        wsb=0, T=T_, si=None):
+def bwd(lib, dO=DO, dos=None, dso=None, dq=DQ, dk_=DK_, dv_=DV_, dg=DG, db=DB, dsi=None, dqs=None, dks=None, dgs=None, dvs=None,
+        ws=None, wsb=0, T=T_, si=None):
     ks, vv, gg, st = contig(B_, T_, HK, DKN), contig(B_, T_, HV, DVN), contig(B_, T_, HV), contig(B_, HV, DKN, DVN)
     return lib.dynconv_delta_bwd(
         Q, S(ks), K, S(ks), V, S(vv), G, S(gg), BETA, S(gg), None, None, si, S(st) if si else None, dO, S(dos or vv), dso,
-        S(st) if dso else None, dq, S(dqs or ks), dk_, S(ks), dv_, S(dvs or vv), dg, S(dgs or gg), db, S(gg), dsi,
+        S(st) if dso else None, dq, S(dqs or ks), dk_, S(dks or ks), dv_, S(dvs or vv), dg, S(dgs or gg), db, S(gg), dsi,
         S(st) if dsi else None, B_, T, HK, HV, DKN, DVN, 0.1, -1.0, BF16, ws, wsb, None)
 
 
@@ -259,6 +259,8 @@ def bwd(lib, dO=DO, dos=None, dso=None, dq=DQ, dk_=DK_, dv_=DV_, dg=DG, db=DB, d
         (dict(dgs=[T_ * HV, 0, 1]), INVALID),
         (dict(dos=[T_ << 22, 1 << 22, DVN, 1]), UNSUP),
         (dict(dvs=[T_ << 22, 1 << 22, DVN, 1]), UNSUP),
+        (dict(dqs=[T_ << 22, 1 << 22, DKN, 1]), UNSUP),
+        (dict(dks=[T_ << 22, 1 << 22, DKN, 1]), UNSUP),
         (dict(), WORKSPACE),
         (dict(T=0), OK),
     ],
