@@ -34,6 +34,8 @@ struct NormParams {
 int64_t norm_bwd_blocks(int64_t rows, int64_t D, dynconv_dtype dt, bool vec);
 // The most that norm_bwd_blocks returns for any alignment.
 int64_t norm_bwd_blocks_max(int64_t rows, int64_t D, dynconv_dtype dt);
+// out[D]: the sums over n partial rows.
+hipError_t norm_dweight(const float* part, int64_t n, int32_t D, float* out, hipStream_t s);
 hipError_t norm_fwd(const NormParams& p, dynconv_dtype dt, bool vec, hipStream_t s);
 hipError_t norm_bwd(const NormParams& p, dynconv_dtype dt, bool vec, hipStream_t s);
 
