@@ -53,7 +53,7 @@ struct DeltaParams {
   float* wdS;     // the same, gradient of the state after the chunk
   float* wU;      // [chunk][nCG][1024]: u, in fragment order
   float* wR;      // the same, gradient of beta * (v - decayed prediction)
-  float* wEnd;    // [sequence and head][nSeg][nCG][DK * 16]: state at a segment's end, in fragment order
+  float* wEnd;    // [sequence and head][nSeg][nCG][DK * 16]: state at a segment's end, in fragment order (last: initial)
   float* wBegin;  // the same, gradient at a segment's start
   float* wM;      // [sequence and head][nSeg][DK][DK]: a segment's transition
   float* wDot;    // [chunk][nCG][64]: sums of dR o V over the group's columns

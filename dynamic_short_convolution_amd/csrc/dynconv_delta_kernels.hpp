@@ -964,7 +964,7 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
   }
 
   f32x4_t S[DK / 16];
-  if (at.seg == 0) {
+  if (at.seg == 0 && (MODE == kEnds || p.nSeg == 1)) {
     load_state<DK>(S, p.state_in == nullptr ? nullptr : p.state_in + b * p.sis0 + hv * p.sis1, p.sis2, p.dkn, col, ok, ln);
   } else if (MODE == kEnds) {
 #pragma unroll
@@ -972,8 +972,14 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[i][r] = unit && 16 * i + 4 * q + r == cg * kDeltaCols + n16 ? 1.f : 0.f;
   } else {
-    load_image<DK / 16>(S, p.wEnd + ((bh * p.nSeg + at.seg - 1) * p.nCG + min(cg, p.nCG - 1)) * (DK * 16), ln);
+    // what the segment before ends in; for the first one the initial state, from where the first
+    // pass put it (no segment ends in the last place): another workgroup of this launch writes
+    // the final state, which may be in the initial one's memory
+    const int from = at.seg == 0 ? p.nSeg - 1 : at.seg - 1;
+    load_image<DK / 16>(S, p.wEnd + ((bh * p.nSeg + from) * p.nCG + min(cg, p.nCG - 1)) * (DK * 16), ln);
   }
+  if (MODE == kEnds && at.seg == 0 && cg < p.nCG)
+    store_image<DK / 16>(S, p.wEnd + ((bh * p.nSeg + p.nSeg - 1) * p.nCG + cg) * (DK * 16), ln);
 
   for (int c = c0; c < c1; ++c) {
     ln = fresh_lane();
