@@ -51,11 +51,14 @@ dynconv_status check_sizes(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t
   if (Hk == 0 || Hv % Hk != 0) return DYNCONV_ERR_INVALID_ARG;
   if (dk > kDeltaMaxDk || dv > kDeltaMaxDv) return DYNCONV_ERR_UNSUPPORTED;
   if (B > INT32_MAX || T > INT32_MAX - 65536 || Hv > INT32_MAX) return DYNCONV_ERR_UNSUPPORTED;
-  // workgroups per launch: one per (sequence, head, chunk) or (sequence, head, 16 columns)
+  // Workgroups per launch: one per (sequence, head, 32 columns), of up to 512 threads (a launch
+  // has fewer than 2^32), or per (sequence, head, chunk), where memory ends first: the forward's
+  // 2^24 of 256 threads need 340 GB of workspace, the backward's 2^23 of 512 more.
+  constexpr int64_t most = (int64_t(1) << 23) - 1;
   const int64_t bh = B * Hv;
   const int64_t per = (T + kDeltaChunk - 1) / kDeltaChunk;
-  const int64_t cols = (dv + kDeltaCols - 1) / kDeltaCols;
-  if (bh > INT32_MAX || (per > 0 && bh > INT32_MAX / per) || 2 * bh > INT32_MAX / cols) return DYNCONV_ERR_UNSUPPORTED;
+  const int64_t cols = (dv + 31) / 32;
+  if (bh > most || (per > 0 && bh > INT32_MAX / per) || bh > most / cols) return DYNCONV_ERR_UNSUPPORTED;
   return DYNCONV_OK;
 }
 

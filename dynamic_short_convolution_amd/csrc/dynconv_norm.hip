@@ -125,8 +125,8 @@ template <typename ET, int E, int LPR, int NV>
 __global__ __launch_bounds__(kThreads) void k_norm_fwd(const NormParams p) {
   __shared__ float red[4];
   const int lane = threadIdx.x % LPR;
-  const int64_t row = int64_t(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR;
-  if (row >= p.rows) return;  // whole rows; with 256 lanes the grid has exactly one each
+  const int64_t row = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR;
+  if (row >= p.rows) return;  // whole rows; with 256 lanes a whole workgroup
   const RowAt r = row_at(p, row);
   const int64_t ox = at(p.x, r), og = at(p.gate, r), orr = at(p.res, r), oy = at(p.y, r), oh = at(p.h, r);
   auto value = [&](float (&v)[E], int c) {  // what is normalised
@@ -436,7 +436,9 @@ int vec_elems(dynconv_dtype dt, bool vec) { return vec ? (dt == DYNCONV_F32 ? 4 
 template <typename ET, int E, int LPR, int NV>
 hipError_t launch(const NormParams& p, bool bwd, int64_t blocks, hipStream_t s) {
   if (!bwd) {
-    hipLaunchKernelGGL((k_norm_fwd<ET, E, LPR, NV>), dim3(unsigned(blocks)), dim3(kThreads), 0, s, p);
+    constexpr int64_t most = int64_t(1) << 23;  // a dimension of a launch has fewer than 2^32 threads
+    const dim3 grid(unsigned(blocks < most ? blocks : most), unsigned((blocks + most - 1) / most));
+    hipLaunchKernelGGL((k_norm_fwd<ET, E, LPR, NV>), grid, dim3(kThreads), 0, s, p);
   } else {
     const size_t lds = NV > 0 && LPR < kThreads ? size_t(kThreads / LPR) * size_t(p.D) * sizeof(float) : 0;
     hipLaunchKernelGGL((k_norm_bwd<ET, E, LPR, NV>), dim3(unsigned(blocks)), dim3(kThreads), lds, s, p);

@@ -461,8 +461,10 @@ def _delta_shapes(q, k, v, g, beta, token: bool):
     if v.dim() != n:
         raise ValueError(f"v must be {lead_name.replace('k', 'v')}; got shape {list(v.shape)}")
     (*lead, Hk, dk), (Hv, dv) = q.shape, v.shape[-2:]
-    if Hk < 1 or Hv % Hk != 0:
+    if Hk < 1 or Hv < 1 or Hv % Hk != 0:
         raise ValueError(f"the {Hv} value heads must be a multiple of the {Hk} key heads")
+    if dk < 1 or dv < 1:
+        raise ValueError(f"heads need at least one channel; got {dk} of q and k, {dv} of v")
     _dtype_code(q)
     heads = (*lead, Hv)
     _expect("k", k, q.shape, q.dtype)
@@ -475,8 +477,7 @@ def _delta_shapes(q, k, v, g, beta, token: bool):
 def _delta_consts(scale, qk_norm_eps, dk: int):
     if qk_norm_eps is not None and not qk_norm_eps >= 0.0:
         raise ValueError(f"qk_norm_eps = {qk_norm_eps} must be at least 0, or None")
-    return (float(dk) ** -0.5 if dk and scale is None else float(scale or 0.0)), (
-        -1.0 if qk_norm_eps is None else float(qk_norm_eps))
+    return (float(dk) ** -0.5 if scale is None else float(scale)), -1.0 if qk_norm_eps is None else float(qk_norm_eps)
 
 
 def new_delta_state(B: int, Hv: int, dk: int, dv: int, device) -> torch.Tensor:

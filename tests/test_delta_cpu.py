@@ -201,6 +201,8 @@ def fwd(lib, q=Q, qs=None, k=K, v=V, vs=None, g=G, gs=None, beta=BETA, seg=None,
         (dict(B=2**31), UNSUP),
         (dict(T=2**31), UNSUP),
         (dict(B=2**20, Hv=2**12, Hk=1, dk=16, dv=16), UNSUP),  # more workgroups than a grid holds
+        (dict(B=2**20, Hv=8, Hk=1), UNSUP),
+        (dict(B=2**14, Hv=8, Hk=1, dv=32 * 64), UNSUP),
         (dict(q=P(0)), INVALID),
         (dict(v=P(0)), INVALID),
         (dict(g=P(0)), INVALID),
@@ -382,6 +384,16 @@ def test_delta_binding_checks():
         dc.dynconv_delta_step(*one, torch.zeros(1, 4, 8, 16))
     with pytest.raises(ValueError):
         dc.dynconv_delta_step(q, k, v, g, b, torch.zeros(1, 4, 8, 16))
+
+
+@pytest.mark.parametrize("Hk,Hv,dk,dv", [(1, 1, 0, 8), (1, 1, 8, 0), (1, 0, 8, 8), (0, 0, 8, 8)])
+def test_delta_binding_refuses_empty_heads(Hk, Hv, dk, dv):
+    """They would leave outputs of the other sizes unwritten."""
+    q, v, g = torch.zeros(1, 3, Hk, dk), torch.zeros(1, 3, Hv, dv), torch.zeros(1, 3, Hv)
+    with pytest.raises(ValueError, match="heads"):
+        dc.dynconv_delta_fwd(q, q, v, g, g)
+    with pytest.raises(ValueError, match="heads"):
+        dc.dynconv_delta_bwd(q, q, v, g, g, v)
 
 
 def test_norm_binding_checks():

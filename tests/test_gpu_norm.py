@@ -161,6 +161,18 @@ def test_offsets_past_32_bits():
     assert torch.equal(dynconv_norm_fwd(x, out=out), dynconv_norm_fwd(x))
 
 
+def test_more_rows_than_one_dimension_of_a_launch():
+    """2^23 workgroups of 16 rows are one dimension's; the rows behind them are the second's."""
+    n = 2**27 + 37
+    x = torch.full((n, 1), 2.0, dtype=torch.bfloat16, device="cuda")
+    x[-37:, 0] = torch.arange(1, 38, device="cuda").to(torch.bfloat16)
+    y = dynconv_norm_fwd(x, eps=1.0)
+    part = x[-64:].double()
+    ref = part / (part * part + 1.0).sqrt()
+    assert bool(((y[-64:].double() - ref).abs() <= 2.0**-8 * ref).all())
+    assert bool((y[:-37] == y[0]).all())
+
+
 def test_captured_replayed_and_on_other_streams():
     x, z, w = rand(40, 3000, 128, dtype=torch.bfloat16), rand(41, 3000, 128, dtype=torch.bfloat16), rand(42, 128, dtype=torch.bfloat16)
 
