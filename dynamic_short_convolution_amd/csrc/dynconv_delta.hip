@@ -83,7 +83,8 @@ constexpr int kStepRows = kDeltaMaxDk / kStepRowThreads;
 // S'^T q = a S^T q + (k.q) u, so one pass over S gives both sums and S is read once, kept in
 // registers and written once. The state is the traffic (8 bytes per element against a few
 // bytes of everything else), so a workgroup takes 32 columns (128-byte row pieces) and every
-// thread issues its loads before anything else.
+// thread issues its loads before anything else. Bound by HBM: 99 us for 128 sequences of 32 heads
+// of 128 x 128, 5.4 TB/s; 5.6 us for one sequence of 16, of which nearly all is the launch.
 template <typename ET, bool VEC>
 __global__ __launch_bounds__(256) void k_delta_step(const DeltaStepParams p) {
   __shared__ float sq[kDeltaMaxDk], sk[kDeltaMaxDk], red[4][2][kStepCols], nrm[3];
