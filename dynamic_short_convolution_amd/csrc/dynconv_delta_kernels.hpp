@@ -546,8 +546,22 @@ __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
   const int hk = hv / p.group;
   const int t0 = c * C, rows = min(C, p.T - t0);
 
-  TK tk;
+  // every load that the first phase needs, before it waits for one
+  TK tk, tq;
   tk.load(static_cast<const ET*>(p.k) + b * p.ks0 + hk * p.ks2 + t0 * p.ks1, p.ks1, rows, p.dkn, tid);
+  if (p.eps >= 0.f)
+    tq.load(static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2 + t0 * p.qs1, p.qs1, rows, p.dkn, tid);
+  float g = 0.f, bt = 0.f;
+  bool cut = false;
+  if (wave == 0 && lane < rows) {
+    const int t = t0 + lane;
+    g = p.g[b * p.gs0 + t * p.gs1 + hv * p.gs2];
+    bt = ldf<ET>(p.beta, b * p.bs0 + t * p.bs1 + hv * p.bs2);
+    if (p.seg != nullptr && t > 0) {
+      const int32_t* sg = p.seg + b * p.ss0;
+      cut = sg[t * p.ss1] != sg[(t - 1) * p.ss1];
+    }
+  }
   auto norms = [&](const TK& t, float* out) {
 #pragma unroll
     for (int i = 0; i < TK::N; ++i) {
@@ -567,25 +581,12 @@ __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
   if (p.eps < 0.f) {
     if (tid < C) tok[kTokRq * C + tid] = 1.f;
   } else {
-    TK tq;
-    tq.load(static_cast<const ET*>(p.q) + b * p.qs0 + hk * p.qs2 + t0 * p.qs1, p.qs1, rows, p.dkn, tid);
     norms(tq, tok + kTokRq * C);
   }
   if (wave == 0) {
-    const int t = t0 + lane;
-    float g = 0.f, bt = 0.f;
-    bool cut = false;
-    if (lane < rows) {
-      g = p.g[b * p.gs0 + t * p.gs1 + hv * p.gs2];
-      bt = ldf<ET>(p.beta, b * p.bs0 + t * p.bs1 + hv * p.bs2);
-      if (p.seg != nullptr && t > 0) {
-        const int32_t* sg = p.seg + b * p.ss0;
-        cut = sg[t * p.ss1] != sg[(t - 1) * p.ss1];
-      }
-      // exp(-128) is 0 in float32: such a token keeps nothing of what came before it
-      if (g <= -128.f) cut = true;
-      if (cut) g = 0.f;
-    }
+    // exp(-128) is 0 in float32: such a token keeps nothing of what came before it
+    if (g <= -128.f) cut = true;
+    if (cut) g = 0.f;
     const unsigned long long mask = __ballot(cut);
     const int cnt = __popcll(mask & ((2ull << lane) - 1ull));
     double G = g;
@@ -1390,7 +1391,7 @@ __global__ __launch_bounds__(2 * DK) void k_delta_join(const DeltaParams p, uint
   for (int i = 0; i < 2; ++i) load(m[i], 1, 2 * wave + i);
   for (int s = 1; s + 1 < p.nSeg; ++s) {
     const Frag<3> own = split8<3>(S[0], S[1]);
-    hand_over<3, 1>(terms[s & 1] + wave * 3072, &own, ln);
+    hand_over<3, 1>(terms[s & 1] + wave * 3 * 1024, &own, ln);
     const int after = min(s + 1, p.nSeg - 2);
 #pragma unroll
     for (int i = 0; i < 2; ++i) S[i] = next[i];
