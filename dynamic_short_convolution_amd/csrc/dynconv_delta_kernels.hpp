@@ -1339,7 +1339,7 @@ __global__ __launch_bounds__(64 * NW, Store<ET>::NT == 1 ? 2 : 1) void k_delta_s
 
 // The forward's first pass over segments (T 32768, 16 heads: 320 us in 8 segments).
 template <typename ET, int DK, int NW, bool VEC>
-__global__ __launch_bounds__(64 * NW, Store<ET>::NT == 1 ? 2 : 1) void k_delta_ends(const DeltaParams p) {
+__global__ __launch_bounds__(64 * NW, 2) void k_delta_ends(const DeltaParams p) {
   extern __shared__ __align__(16) char lds[];
   delta_scan<ET, DK, NW, kEnds, VEC>(p, lds, xcd_logical_block(blockIdx.x, gridDim.x));
 }
