@@ -525,7 +525,7 @@ struct PrepLds {
 // (one column per lane), then block diagonal d = 1, 2, 3 follows as
 // T_ij = -T_ii sum_{j <= k < i} A_ik T_kj on the float32 matrix instructions, whose result
 // layout is again their right operand's. Bound by the latency of its short serial phases, which
-// the CU's other workgroups hide in part: 106 us for 8192 chunks, of which the 0.3 GB it moves
+// the CU's other workgroups hide in part: 102 us for 8192 chunks, of which the 0.3 GB it moves
 // would take 61 at the rate of a copy.
 template <typename ET, int DK, bool VEC>
 __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
@@ -811,7 +811,7 @@ __device__ __forceinline__ ScanAt scan_at(const DeltaParams& p, uint32_t bid, in
 // 128 x 128 has 8 such waves, so a batch that fills the chip has one per SIMD, and a lone wave
 // issues an instruction about every 5 cycles. The outputs do not feed the recurrence: where LDS
 // allows (16-bit storage), a second wave on the same SIMD forms P, Q S0 and P U from the terms of
-// S0 and U that the first leaves in LDS (B8 T4096, 16 heads, bf16: 368 us with one wave, 317 with
+// S0 and U that the first leaves in LDS (B8 T4096, 16 heads, bf16: 368 us with one wave, 312 with
 // two; 0.7 GB would take 146 at the rate of a copy). What bounds it now is the chain of a chunk
 // (barriers, the terms' splits between products): the vector units are busy for 46 % of the
 // time, LDS for 45 %, the matrix units for 31 %.
@@ -978,6 +978,7 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
     }
   }
 
+  if constexpr (PAIR) __builtin_amdgcn_s_setprio(1);  // the chain that sets the time (318 -> 312 us)
   f32x4_t S[DK / 16];
   if (at.seg == 0 && (MODE == kEnds || p.nSeg == 1)) {
     load_state<DK>(S, p.state_in == nullptr ? nullptr : p.state_in + b * p.sis0 + hv * p.sis1, p.sis2, p.dkn, col, ok, ln);
@@ -1328,7 +1329,7 @@ __device__ __forceinline__ void delta_back(const DeltaParams p, char* lds, uint3
 }
 
 // Both scans of the backward: the first `back` workgroups carry dS, the others S. At B8 T4096, 16
-// heads, bf16 714 us; they write 1.7 GB of images and read 0.65 GB, 490 us at the rate of a copy,
+// heads, bf16 697 us; they write 1.7 GB of images and read 0.65 GB, 490 us at the rate of a copy,
 // and the CU's vector units are busy for 39 % of the time, LDS for 31 %, the matrix units for 25 %.
 template <typename ET, int DK, int NW, bool ENDS, bool VEC>
 __global__ __launch_bounds__(64 * NW, Store<ET>::NT == 1 ? 2 : 1) void k_delta_scans(const DeltaParams p, uint32_t back) {
@@ -1483,7 +1484,7 @@ struct ImageTile {
   }
 };
 
-// ONE: a single value head per key head (no sums to carry from head to head). 653 us at B8 T4096,
+// ONE: a single value head per key head (no sums to carry from head to head). 651 us at B8 T4096,
 // 16 heads, bf16, for 1.3 GB (270 us at the rate of a copy): the images are read once, and what
 // bounds the kernel is the latency of its phases between barriers, with two waves per SIMD (the
 // five sums of 64 x 128 take most of the registers): vector units 43 % busy, LDS 33 %, matrix
