@@ -67,7 +67,7 @@ constexpr int delta_dk_pad(int dk) { return dk <= 64 ? 64 : 128; }
 // one, which is least for n = sqrt(6 nC); a segment has at least 2 chunks, and from 8 chunks and
 // 3 segments on it is less than the nC of one pass (16 heads of 128 x 128, bf16, forward /
 // backward in us, one segment and as many as here: T 400 45 / 95 and 51 / 98, T 512 47 / 104 and
-// 47 / 91, T 1024 80 / 163 and 58 / 112, T 32768 forward 2500 and 694).
+// 47 / 91, T 1024 80 / 163 and 58 / 112, T 32768 forward 2500 and 681).
 constexpr int delta_segment_length(int64_t bh, int64_t nC, int64_t nCG) {
   const int64_t blocks = bh * ((nCG + 3) / 4);
   int64_t n = blocks > 0 ? 256 / blocks : 1;

@@ -1329,7 +1329,7 @@ __device__ __forceinline__ void delta_back(const DeltaParams p, char* lds, uint3
 }
 
 // Both scans of the backward: the first `back` workgroups carry dS, the others S. At B8 T4096, 16
-// heads, bf16 697 us; they write 1.7 GB of images and read 0.65 GB, 490 us at the rate of a copy,
+// heads, bf16 703 us; they write 1.7 GB of images and read 0.6 GB, 480 us at the rate of a copy,
 // and the CU's vector units are busy for 39 % of the time, LDS for 31 %, the matrix units for 25 %.
 template <typename ET, int DK, int NW, bool ENDS, bool VEC>
 __global__ __launch_bounds__(64 * NW, Store<ET>::NT == 1 ? 2 : 1) void k_delta_scans(const DeltaParams p, uint32_t back) {
@@ -1341,7 +1341,7 @@ __global__ __launch_bounds__(64 * NW, Store<ET>::NT == 1 ? 2 : 1) void k_delta_s
   }
 }
 
-// The forward's first pass over segments (T 32768, 16 heads: 320 us in 8 segments).
+// The forward's first pass over segments (T 32768, 16 heads: 317 us in 8 segments).
 template <typename ET, int DK, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, 2) void k_delta_ends(const DeltaParams p) {
   extern __shared__ __align__(16) char lds[];
@@ -1484,8 +1484,8 @@ struct ImageTile {
   }
 };
 
-// ONE: a single value head per key head (no sums to carry from head to head). 651 us at B8 T4096,
-// 16 heads, bf16, for 1.3 GB (270 us at the rate of a copy): the images are read once, and what
+// ONE: a single value head per key head (no sums to carry from head to head). 611 to 651 us at B8
+// T4096, 16 heads, bf16, for 1.3 GB (270 us at the rate of a copy): the images are read once, and what
 // bounds the kernel is the latency of its phases between barriers, with two waves per SIMD (the
 // five sums of 64 x 128 take most of the registers): vector units 43 % busy, LDS 33 %, matrix
 // units 28 %.
