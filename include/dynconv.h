@@ -410,8 +410,9 @@ size_t dynconv_delta_fwd_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_
  *   dg        float32 [B,T,Hv] (0 at a document start and where exp(g) is 0)
  *   dstate_in float32 [B,Hv,dk,dv], the gradient of the initial state, or NULL to skip.
  * States are recomputed from the inputs; nothing is kept from the forward. Needs
- * dynconv_delta_bwd_workspace_size(...) bytes (per 64 tokens and value head about 20 KiB +
- * (8 dk' + 0.5 KiB + 1 KiB) dv with dk' = 64 or 128). T == 0 is a no-op.
+ * dynconv_delta_bwd_workspace_size(...) bytes (per 64 tokens and value head 20 KiB +
+ * (8 dk' + 528) dv, with dk rounded up to dk' = 64 or 128 and dv to a multiple of 16, and what
+ * the segments of long sequences take). T == 0 is a no-op.
  */
 dynconv_status dynconv_delta_bwd(const void* q, const int64_t* qs, const void* k, const int64_t* ks, const void* v,
                                  const int64_t* vs, const float* g, const int64_t* gs, const void* beta,
