@@ -8,8 +8,8 @@ convolution fused into its producing projection, dynconv_gemm_fwd and
 dynconv_gemm_lowrank_fwd. What consumes the convolved q, k, v in a linear-attention layer:
 the gated delta rule, dynconv_delta_fwd, dynconv_delta_bwd and the decoding step
 dynconv_delta_step (with new_delta_state), and the RMS norm with weight, SiLU gate and
-residual, dynconv_norm_fwd and dynconv_norm_bwd. Importing this package does not load the library; the first call does, and
-fails loudly if it has not been built.
+residual, dynconv_norm_fwd and dynconv_norm_bwd. Importing this package does not load the
+library; the first call does, and fails loudly if it has not been built.
 """
 from .ops import (  # noqa: F401
     dynconv_bwd,

@@ -444,7 +444,7 @@ def _launch(fn: str, dev, *args) -> None:
 
 def _sp(t):
     """(pointer, strides) of a tensor, or two NULLs."""
-    return (t.data_ptr(), _lib.strides(t.stride())) if t is not None else (None, None)
+    return (t.data_ptr(), _lib.const_strides(t.stride())) if t is not None else (None, None)
 
 
 def _dp(t):
@@ -578,7 +578,7 @@ def _norm_shape(x):
 
 def _sp4(t):
     """(pointer, four strides) of a tensor of up to 4 dimensions, or two NULLs."""
-    return (t.data_ptr(), _lib.strides((0,) * (4 - t.dim()) + t.stride())) if t is not None else (None, None)
+    return (t.data_ptr(), _lib.const_strides((0,) * (4 - t.dim()) + t.stride())) if t is not None else (None, None)
 
 
 def _norm_weight(weight, x):
