@@ -21,11 +21,16 @@
 // only K, Q, T (left operands, shared by the workgroup's waves) pass through LDS.
 //
 // Precision. The matrix cores take bf16; a float32 operand enters as three terms of 8 bits
-// (mantissa split by truncation, exactly x = x0 + x1 + x2), a float16 one as two, a bf16 one
-// as itself, and the products of terms whose orders add up to more than 2 (below 2^-24 of the
-// result) are left out. That holds states and sums at float32 accuracy at 2.7 times the rate
-// of the float32 matrix instructions (6 products for two float32 operands, 3 for a bf16 one).
-// Products that only reach 16-bit results keep the terms up to order 1 (2^-16).
+// (mantissa cut into pieces, exactly x = x0 + x1 + x2), a float16 one as two (exact), a bf16
+// one as itself, and the products of terms whose orders add up to more than 2 (two, of at most
+// 2^-22 of the factors' product each) are left out. That holds states and sums at float32
+// accuracy at 2.7 times the rate of the float32 matrix instructions (6 products for two float32
+// operands, 3 for a bf16 one). Operands formed here (P, S0, U, Y, Yk) of products that only reach
+// 16-bit results are rounded to two terms (to nearest, at most 2^-17 off, S0 2^-16), and the product
+// of two second terms (at most 2^-15) is left out: a third term would add half as many products
+// again and LDS that the kernels do not have, to results that are themselves rounded to 2^-9 or
+// 2^-12 (root mean square against 64 bits, relative to that of rounding the exact result: bf16
+// 1.00001, float16 1.0004).
 #pragma once
 
 #include "dynconv_common.hpp"
@@ -112,21 +117,52 @@ __device__ __forceinline__ float below(float x) {  // x without its first 8 sign
   return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u);
 }
 
+// The next of N terms of 4 values; x keeps what is left (exact). Three terms hold a float32 whole,
+// so they are cut off, which is the shorter chain (rounding them too: prefill of 32768 tokens 693
+// to 731 us). Two leave something out and are rounded to nearest, so that it has either sign (cut
+// off, float16 outputs came out 2^-15 too small on average; the training step of packed documents
+// 717 us so, 729 rounded, the others within 0.5 %).
+template <int N, bool LAST>
+__device__ __forceinline__ u32x2 next_term(f32x4_t& x) {
+  if constexpr (N < 3) {
+    const u32x2 w = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+    if constexpr (!LAST) x -= f32x4_t{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
+    return w;
+  } else {
+    const u32x2 w = {top2(x[0], x[1]), top2(x[2], x[3])};
+    if constexpr (!LAST) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = below(x[e]);
+    }
+    return w;
+  }
+}
+
 template <int N>
 __device__ __forceinline__ Frag<N> split8(f32x4_t a, f32x4_t b) {
   Frag<N> f;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    f.t[n] = u32x4{top2(a[0], a[1]), top2(a[2], a[3]), top2(b[0], b[1]), top2(b[2], b[3])};
-    if (n + 1 < N) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        a[e] = below(a[e]);
-        b[e] = below(b[e]);
-      }
-    }
+    const u32x2 u = n + 1 < N ? next_term<N, false>(a) : next_term<N, true>(a);
+    const u32x2 v = n + 1 < N ? next_term<N, false>(b) : next_term<N, true>(b);
+    f.t[n] = u32x4{u[0], u[1], v[0], v[1]};
   }
   return f;
+}
+// The same values in three terms and in NP: the first of three and the rest of it rounded to one.
+template <int NP>
+__device__ __forceinline__ void split8_both(Frag<3>& f, Frag<NP>& g, f32x4_t a, f32x4_t b) {
+  f = split8<3>(a, b);
+#pragma unroll
+  for (int n = 0; n < NP; ++n) g.t[n] = f.t[n];
+  if constexpr (NP == 2) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      a[e] = below(a[e]);
+      b[e] = below(b[e]);
+    }
+    g.t[1] = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+  }
 }
 
 // Row-major LDS matrices keep each 32-column block in fragment order: columns 4q .. 4q+3 at
@@ -295,13 +331,8 @@ __device__ __forceinline__ void utrap_product(f32x4_t* acc, const Trap<N>& t, co
 template <int N>
 __device__ __forceinline__ void put4(uint16_t* p, int plane, f32x4_t x) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    *reinterpret_cast<u32x2*>(p + n * plane) = u32x2{top2(x[0], x[1]), top2(x[2], x[3])};
-    if (n + 1 < N) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = below(x[e]);
-    }
-  }
+  for (int n = 0; n < N; ++n)
+    *reinterpret_cast<u32x2*>(p + n * plane) = n + 1 < N ? next_term<N, false>(x) : next_term<N, true>(x);
 }
 
 template <typename ET>
@@ -1020,13 +1051,9 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
       f32x4_t te[4], tr[4], tb[4];
       row_load<NT>(fk, sK, TK::LD, TK::PLANE, ln);
       Frag<3> sf[KB];
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(S[2 * kb], S[2 * kb + 1]);
       Frag<NP> so[KB];
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int n = 0; n < NP; ++n) so[kb].t[n] = sf[kb].t[n];
+      for (int kb = 0; kb < KB; ++kb) split8_both<NP>(sf[kb], so[kb], S[2 * kb], S[2 * kb + 1]);
       if constexpr (PAIR) hand_over<NP, KB>(lds + L::HS + cw * L::HSW, so, ln);
       row_product<2, KB>(z, fk, sK, TK::LD, TK::PLANE, sf, [&] {
         if constexpr (!STATES && !PAIR) row_load<NT>(fk, sQ, TK::LD, TK::PLANE, ln);

@@ -1,0 +1,41 @@
+"""Edges of the gated delta rule on the GPU: the split of operands into terms, vectors without an
+epsilon, a single token with strides that mean nothing."""
+import numpy as np
+import pytest
+import torch
+
+from dynamic_short_convolution_amd import dynconv_delta_bwd, dynconv_delta_fwd
+from oracle import delta_bwd, delta_fwd
+from tests.parity import to64
+from tests.test_gpu_delta import EPS, make, rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    yield
+    torch.cuda.synchronize()
+
+
+def shrink(got, ref):
+    """What share of the results is missing, on average: -<got - ref, ref> / <ref, ref>."""
+    return -float(np.sum((to64(got) - ref) * ref) / np.sum(ref * ref))
+
+
+def test_sixteen_bit_results_are_not_shrunk():
+    """Operands that only reach float16 results are held in two terms of 8 bits. Rounded to nearest,
+    what they leave out has either sign, as has the rounding of the results, which is the larger
+    (at most 2^-11 of a value, 2^-12 in the root mean square): over N results its part along them
+    is about 2^-12 / sqrt(N), with N > 2^18 2^-21, and ten of these are under 2^-17.5. Terms cut
+    off instead leave out 2^-17 of a factor on average, all of one sign, and the product of the two
+    second terms is 2^-17 on average: a product P U then lacks 3 * 2^-17, 2^-15.4."""
+    B, T, Hk, Hv, dk, dv = 2, 300, 4, 4, 128, 128
+    args = make(101, B, T, Hk, Hv, dk, dv, "f16")
+    do = rand(102, B, T, Hv, dv, dtype=torch.float16)
+    a64 = [to64(a) for a in args]
+    got = [dynconv_delta_fwd(*args, scale=0.3, qk_norm_eps=EPS), *dynconv_delta_bwd(*args, do, scale=0.3, qk_norm_eps=EPS)[:2]]
+    ref = [delta_fwd(*a64, 0.3, EPS)[0], *delta_bwd(*a64, to64(do), 0.3, EPS)[:2]]
+    lost = {n: shrink(g, r) for n, g, r in zip(("o", "dq", "dk"), got, ref)}
+    assert all(abs(x) < 2.0**-17.5 for x in lost.values()), lost
