@@ -593,6 +593,7 @@ __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
       cut = sg[t * p.ss1] != sg[(t - 1) * p.ss1];
     }
   }
+  // (rows behind the last token are zeros: no length to divide by)
   auto norms = [&](const TK& t, float* out) {
 #pragma unroll
     for (int i = 0; i < TK::N; ++i) {
@@ -603,8 +604,8 @@ __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
       for (int e = 0; e < 4; ++e) s += x[e] * x[e] + y[e] * y[e];
 #pragma unroll
       for (int m = 1; m < DK / 8; m <<= 1) s += __shfl_xor(s, m);
-      const int idx = tid + i * 256;
-      if (idx % (DK / 8) == 0) out[idx / (DK / 8)] = p.eps < 0.f ? 1.f : 1.f / sqrtf(s + p.eps);
+      const int idx = tid + i * 256, row = idx / (DK / 8);
+      if (idx % (DK / 8) == 0) out[row] = p.eps < 0.f || row >= rows ? 1.f : 1.f / sqrtf(s + p.eps);
     }
   };
   norms(tk, tok + kTokRk * C);

@@ -372,7 +372,8 @@ dynconv_status dynconv_cache_fill_varlen(const void* x, const int64_t* xs, const
  *   o_t = scale S_t^T q_t.
  *   q, k   [B,T,Hk,dk], v, o [B,T,Hv,dv] of `dtype`, strides s[0..3], s[3] == 1
  *   beta   [B,T,Hv] of `dtype`, g float32 [B,T,Hv] (log decay, normally <= 0), strides s[0..2]
- *   qk_norm_eps >= 0: q and k are divided by sqrt(|.|^2 + qk_norm_eps) first; < 0: as given
+ *   qk_norm_eps >= 0: q and k are divided by sqrt(|.|^2 + qk_norm_eps) first (the sum of squares
+ *            in float32; with 0 a row of zeros is 0 / 0); < 0: as given
  *   seq_idx  int32 [B,T] (strides ss[0..1]) or NULL: the state is reset to zero before a
  *            token whose id differs from the token's before it (document starts of packed
  *            rows); the initial state belongs to the first document of a row, the final
@@ -381,7 +382,7 @@ dynconv_status dynconv_cache_fill_varlen(const void* x, const int64_t* xs, const
  *   state_out  the same, overwritten with the state after token T-1, or NULL; may be
  *              state_in itself (same strides). T == 0 copies the state.
  * A token with beta = 0 and g = 0 leaves the state as it is (padding behind a sequence, whose
- * q, k, v have to be finite).
+ * q, k, v have to be finite, and q and k not zero when qk_norm_eps is 0).
  * g <= -128 counts as a decay to exactly zero (exp of it is 0 in float32). Tokens are worked
  * on 64 at a time: a NaN or infinity among a head's inputs can reach every output of its
  * 64-token chunk and of what follows, other documents included; other heads keep theirs.

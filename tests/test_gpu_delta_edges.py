@@ -4,10 +4,10 @@ import numpy as np
 import pytest
 import torch
 
-from dynamic_short_convolution_amd import dynconv_delta_bwd, dynconv_delta_fwd
+from dynamic_short_convolution_amd import dynconv_delta_bwd, dynconv_delta_fwd, dynconv_delta_step
 from oracle import delta_bwd, delta_fwd
 from tests.parity import to64
-from tests.test_gpu_delta import EPS, make, rand
+from tests.test_gpu_delta import EPS, TD, check, close, make, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +39,30 @@ def test_sixteen_bit_results_are_not_shrunk():
     ref = [delta_fwd(*a64, 0.3, EPS)[0], *delta_bwd(*a64, to64(do), 0.3, EPS)[:2]]
     lost = {n: shrink(g, r) for n, g, r in zip(("o", "dq", "dk"), got, ref)}
     assert all(abs(x) < 2.0**-17.5 for x in lost.values()), lost
+
+
+# ---------------------------------------------------------------------------------
+# Unit vectors without an epsilon
+# ---------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("shape", [(2, 1, 1, 2, 64, 48), (1, 63, 2, 2, 128, 32), (1, 65, 1, 2, 64, 64), (2, 130, 1, 1, 37, 51),
+                                   (1, 577, 1, 2, 40, 24)], ids=lambda s: "x".join(map(str, s)))
+def test_unit_vectors_without_epsilon(shape, dtype):
+    """qk_norm_eps = 0 with rows that are not zero: what the tokens behind the last one in its chunk
+    of 64 read as (zeros) must not be divided by their length. 577 tokens: several segments."""
+    B, T, Hk, Hv, dk, dv = shape
+    args = make(111, *shape, dtype)
+    check(args, eps=0.0, state=rand(112, B, Hv, dk, dv), dstate_out=rand(113, B, Hv, dk, dv))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_one_token_without_epsilon_is_a_step(dtype):
+    args = make(114, 2, 1, 1, 2, 64, 80, dtype)
+    S = rand(115, 2, 2, 64, 80)
+    o, last = dynconv_delta_fwd(*args, qk_norm_eps=0.0, state=S, want_state=True)
+    out = dynconv_delta_step(*[a[:, 0] for a in args], S, qk_norm_eps=0.0)
+    ro, rl = delta_fwd(*[to64(a) for a in args], 0.125, 0.0, None, to64(rand(115, 2, 2, 64, 80)))
+    for name, got, ref in (("o", o, ro), ("one step's o", out, ro[:, 0]), ("state", last, rl), ("one step's state", S, rl)):
+        close(name, got, ref, TD[dtype])
