@@ -44,7 +44,9 @@ int wide(const void* p, const int64_t* s, int n, const int64_t* e, int eb) {
   return 1;
 }
 
-dynconv_status check_sizes(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, dynconv_dtype dt) {
+dynconv_status check_sizes(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, dynconv_dtype dt,
+                           float eps = 0.f) {
+  if (eps != eps) return DYNCONV_ERR_INVALID_ARG;  // neither with a norm nor without
   if (dt != DYNCONV_F32 && dt != DYNCONV_BF16 && dt != DYNCONV_F16) return DYNCONV_ERR_INVALID_ARG;
   if (B < 0 || T < 0 || Hk < 0 || Hv < 0 || dk < 0 || dv < 0) return DYNCONV_ERR_INVALID_ARG;
   if (B == 0 || Hv == 0 || dk == 0 || dv == 0) return DYNCONV_OK;
@@ -136,7 +138,7 @@ dynconv_status dynconv_delta_fwd(const void* q, const int64_t* qs, const void* k
                                  int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, float scale,
                                  float qk_norm_eps, dynconv_dtype dtype, void* workspace, size_t workspace_bytes,
                                  void* stream) {
-  dynconv_status st = check_sizes(B, T, Hk, Hv, dk, dv, dtype);
+  dynconv_status st = check_sizes(B, T, Hk, Hv, dk, dv, dtype, qk_norm_eps);
   if (st != DYNCONV_OK) return st;
   if (empty(B, Hv, dk, dv)) return DYNCONV_OK;
   DeltaParams p{};
@@ -189,7 +191,7 @@ dynconv_status dynconv_delta_bwd(const void* q, const int64_t* qs, const void* k
                                  const int64_t* dbs, float* dstate_in, const int64_t* dsis, int64_t B, int64_t T,
                                  int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, float scale, float qk_norm_eps,
                                  dynconv_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
-  dynconv_status st = check_sizes(B, T, Hk, Hv, dk, dv, dtype);
+  dynconv_status st = check_sizes(B, T, Hk, Hv, dk, dv, dtype, qk_norm_eps);
   if (st != DYNCONV_OK) return st;
   if (empty(B, Hv, dk, dv) || T == 0) return DYNCONV_OK;
   DeltaParams p{};
@@ -244,7 +246,7 @@ dynconv_status dynconv_delta_step(const void* q, const int64_t* qs, const void* 
                                   const int64_t* bs, float* state, const int64_t* sts, void* o, const int64_t* os,
                                   int64_t B, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv, float scale,
                                   float qk_norm_eps, dynconv_dtype dtype, void* stream) {
-  dynconv_status st = check_sizes(B, 1, Hk, Hv, dk, dv, dtype);
+  dynconv_status st = check_sizes(B, 1, Hk, Hv, dk, dv, dtype, qk_norm_eps);
   if (st != DYNCONV_OK) return st;
   if (empty(B, Hv, dk, dv)) return DYNCONV_OK;
   const int eb = elem_bytes(dtype);

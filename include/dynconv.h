@@ -373,7 +373,7 @@ dynconv_status dynconv_cache_fill_varlen(const void* x, const int64_t* xs, const
  *   q, k   [B,T,Hk,dk], v, o [B,T,Hv,dv] of `dtype`, strides s[0..3], s[3] == 1
  *   beta   [B,T,Hv] of `dtype`, g float32 [B,T,Hv] (log decay, normally <= 0), strides s[0..2]
  *   qk_norm_eps >= 0: q and k are divided by sqrt(|.|^2 + qk_norm_eps) first (the sum of squares
- *            in float32; with 0 a row of zeros is 0 / 0); < 0: as given
+ *            in float32; with 0 a row of zeros is 0 / 0); < 0: as given; NaN is refused
  *   seq_idx  int32 [B,T] (strides ss[0..1]) or NULL: the state is reset to zero before a
  *            token whose id differs from the token's before it (document starts of packed
  *            rows); the initial state belongs to the first document of a row, the final
