@@ -33,6 +33,12 @@ dynconv_status check_tensor(const void* p, const int64_t* s, int n, const int64_
 constexpr int64_t kDeltaMaxTokenStride = int64_t(1) << 22;
 bool far_tokens(const int64_t* s, int64_t T) { return T > 1 && s[1] >= kDeltaMaxTokenStride; }
 
+// The token stride that the kernels get. With one token it has no meaning (0, 1 and far ones are
+// common: an expanded row, channels first, a slice of one token), but the kernels tell the chunk's rows
+// that do not exist by their offsets behind the first, which a shorter stride than a row would
+// put into it.
+int64_t token_stride(const int64_t* s, const int64_t* e) { return e[1] > 1 ? s[1] : e[3]; }
+
 // Whether the rows of a chunk lie one behind the other (no token's row overlaps the next).
 bool apart(const int64_t* s, const int64_t* e) { return e[1] <= 1 || s[1] >= e[3]; }
 
@@ -90,9 +96,9 @@ dynconv_status take_inputs(DeltaParams* p, const void* q, const int64_t* qs, con
       p->ss1 = ss[1];
     }
     p->q = q, p->k = k, p->v = v, p->g = g, p->beta = beta;
-    p->qs0 = qs[0], p->qs1 = qs[1], p->qs2 = qs[2];
-    p->ks0 = ks[0], p->ks1 = ks[1], p->ks2 = ks[2];
-    p->vs0 = vs[0], p->vs1 = vs[1], p->vs2 = vs[2];
+    p->qs0 = qs[0], p->qs1 = token_stride(qs, eq), p->qs2 = qs[2];
+    p->ks0 = ks[0], p->ks1 = token_stride(ks, eq), p->ks2 = ks[2];
+    p->vs0 = vs[0], p->vs1 = token_stride(vs, ev), p->vs2 = vs[2];
     p->gs0 = gs[0], p->gs1 = gs[1], p->gs2 = gs[2];
     p->bs0 = bs[0], p->bs1 = bs[1], p->bs2 = bs[2];
     p->vec = dk % 8 == 0 && wide(q, qs, 4, eq, eb) && wide(k, ks, 4, eq, eb) && apart(qs, eq) && apart(ks, eq) &&
@@ -151,7 +157,7 @@ dynconv_status dynconv_delta_fwd(const void* q, const int64_t* qs, const void* k
     if (far_tokens(os, T)) return DYNCONV_ERR_UNSUPPORTED;
     p.vec = p.vec && apart(os, ev);
     p.out = o;
-    p.os0 = os[0], p.os1 = os[1], p.os2 = os[2];
+    p.os0 = os[0], p.os1 = token_stride(os, ev), p.os2 = os[2];
   }
   if (state_out != nullptr) {
     if ((st = check_tensor(state_out, sos, 4, est, 4, true, true)) != DYNCONV_OK) return st;
@@ -208,10 +214,10 @@ dynconv_status dynconv_delta_bwd(const void* q, const int64_t* qs, const void* k
   if ((st = check_tensor(dbeta, dbs, 3, eg, eb, false, true)) != DYNCONV_OK) return st;
   if (far_tokens(dos, T) || far_tokens(dvs, T) || far_tokens(dqs, T) || far_tokens(dks, T)) return DYNCONV_ERR_UNSUPPORTED;
   p.dO = dO, p.dq = dq, p.dk = dk_, p.dv = dv_, p.dg = dg, p.dbeta = dbeta;
-  p.dos0 = dos[0], p.dos1 = dos[1], p.dos2 = dos[2];
-  p.dqs0 = dqs[0], p.dqs1 = dqs[1], p.dqs2 = dqs[2];
-  p.dks0 = dks[0], p.dks1 = dks[1], p.dks2 = dks[2];
-  p.dvs0 = dvs[0], p.dvs1 = dvs[1], p.dvs2 = dvs[2];
+  p.dos0 = dos[0], p.dos1 = token_stride(dos, ev), p.dos2 = dos[2];
+  p.dqs0 = dqs[0], p.dqs1 = token_stride(dqs, eq), p.dqs2 = dqs[2];
+  p.dks0 = dks[0], p.dks1 = token_stride(dks, eq), p.dks2 = dks[2];
+  p.dvs0 = dvs[0], p.dvs1 = token_stride(dvs, ev), p.dvs2 = dvs[2];
   p.dgs0 = dgs[0], p.dgs1 = dgs[1], p.dgs2 = dgs[2];
   p.dbs0 = dbs[0], p.dbs1 = dbs[1], p.dbs2 = dbs[2];
   p.vec = p.vec && dv % 8 == 0 && wide(dO, dos, 4, ev, eb) && apart(dos, ev) && apart(dvs, ev) &&

@@ -387,9 +387,9 @@ dynconv_status dynconv_cache_fill_varlen(const void* x, const int64_t* xs, const
  * on 64 at a time: a NaN or infinity among a head's inputs can reach every output of its
  * 64-token chunk and of what follows, other documents included; other heads keep theirs.
  * Limits (DYNCONV_ERR_UNSUPPORTED otherwise): dk <= 128, dv <= 65536; strides >= 0, token
- * strides (s[1]) of q, k, v, o and their gradients below 2^22 elements, B Hv ceil(dv/32) below
- * 2^23. With another size than T of 0 nothing is read or written. Inputs and outputs need
- * element alignment; rows of q, k that allow 16-byte loads are read so.
+ * strides (s[1]) of q, k, v, o and their gradients below 2^22 elements (with T == 1 they are not
+ * used), B Hv ceil(dv/32) below 2^23. With another size than T of 0 nothing is read or written.
+ * Inputs and outputs need element alignment; rows of q, k that allow 16-byte loads are read so.
  * Needs dynconv_delta_fwd_workspace_size(...) bytes of workspace. Run-to-run deterministic.
  */
 dynconv_status dynconv_delta_fwd(const void* q, const int64_t* qs, const void* k, const int64_t* ks, const void* v,

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from dynamic_short_convolution_amd import dynconv_delta_bwd, dynconv_delta_fwd, dynconv_delta_step
+from dynamic_short_convolution_amd import _lib, dynconv_delta_bwd, dynconv_delta_fwd, dynconv_delta_step
 from oracle import delta_bwd, delta_fwd
 from tests.parity import to64
 from tests.test_gpu_delta import EPS, TD, check, close, make, rand
@@ -66,3 +66,60 @@ def test_one_token_without_epsilon_is_a_step(dtype):
     ro, rl = delta_fwd(*[to64(a) for a in args], 0.125, 0.0, None, to64(rand(115, 2, 2, 64, 80)))
     for name, got, ref in (("o", o, ro), ("one step's o", out, ro[:, 0]), ("state", last, rl), ("one step's state", S, rl)):
         close(name, got, ref, TD[dtype])
+
+
+# ---------------------------------------------------------------------------------
+# One token: its stride has no meaning
+# ---------------------------------------------------------------------------------
+
+
+def one_token_strides(kind, H, d):
+    """Strides of a [B, 1, H, d] tensor: channels first, an expanded row, far apart tokens."""
+    return {"channels_first": (H * d, 1, d, 1), "expanded": (H * d, 0, d, 1), "short": (H * d, 8, d, 1),
+            "far": (H * d, 2**26, d, 1), "farther": (H * d, 2**31, d, 1)}[kind]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("kind", ["channels_first", "expanded", "short", "far", "farther"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (37, 51)])
+def test_one_token_of_any_stride(kind, dk, dv, dtype):
+    """Inputs, outputs and gradients of one token, bit for bit those of contiguous ones, inside guard
+    bands."""
+    B, H = 2, 2
+    args = make(121, B, 1, H, H, dk, dv, dtype)
+    do, state, ds = rand(122, B, 1, H, dv, dtype=TD[dtype]), rand(123, B, H, dk, dv), rand(124, B, H, dk, dv)
+
+    def view(t):
+        """A copy of t [B, 1, H, d] with such strides, between NaN."""
+        d = t.shape[-1]
+        big = torch.full((8 + B * H * d + 8,), float("nan"), dtype=t.dtype, device="cuda")
+        v = big.as_strided((B, 1, H, d), one_token_strides(kind, H, d), 8)
+        v.copy_(t)
+        return big, v
+
+    views = [view(a)[1] for a in args[:3]] + args[3:]
+    kw = dict(qk_norm_eps=EPS, state=state)
+    ref, last = dynconv_delta_fwd(*args, want_state=True, **kw)
+    big, out = view(torch.zeros_like(ref))
+    assert out.stride()[1] == one_token_strides(kind, H, dv)[1]
+    got = dynconv_delta_fwd(*views, out=out, want_state=True, **kw)
+    assert torch.equal(out, ref) and torch.equal(got[1], last) and int(torch.isfinite(big).sum()) == out.numel()
+    assert torch.equal(dynconv_delta_step(*[a[:, 0] for a in views], state.clone(), qk_norm_eps=EPS),
+                       dynconv_delta_step(*[a[:, 0] for a in args], state.clone(), qk_norm_eps=EPS))
+
+    grads = dynconv_delta_bwd(*args, do, dstate_out=ds, need_dstate=True, **kw)
+    vdo = view(do)[1]
+    same = dynconv_delta_bwd(*views, vdo, dstate_out=ds, need_dstate=True, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(grads, same))
+    # the gradients written with such strides, through the C entry point
+    sp = lambda t: (t.data_ptr(), _lib.strides(t.stride()))  # noqa: E731
+    outs = [view(torch.zeros_like(t)) for t in grads[:3]]
+    dg, db, dst = (torch.zeros_like(t) for t in grads[3:])
+    size = _lib.load().dynconv_delta_bwd_workspace_size(B, 1, H, H, dk, dv, {"f32": 0, "bf16": 1, "f16": 2}[dtype])
+    work = torch.empty(size, dtype=torch.uint8, device="cuda")
+    _lib.check("dynconv_delta_bwd", _lib.load().dynconv_delta_bwd(
+        *(x for t in views for x in sp(t)), None, None, *sp(state), *sp(vdo), *sp(ds), *(x for _, t in outs for x in sp(t)),
+        *sp(dg), *sp(db), *sp(dst), B, 1, H, H, dk, dv, dk**-0.5, EPS, {"f32": 0, "bf16": 1, "f16": 2}[dtype], work.data_ptr(), size,
+        torch.cuda.current_stream().cuda_stream))
+    assert all(torch.equal(a, b) for a, b in zip([t for _, t in outs] + [dg, db, dst], grads))
+    assert all(int(torch.isfinite(b).sum()) == t.numel() for b, t in outs)
