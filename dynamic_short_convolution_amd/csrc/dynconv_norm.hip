@@ -9,10 +9,13 @@
 // tensor and lane (8 of one element for rows that allow no wide loads), so the mean and the
 // result take one pass; longer rows are read again. The weight's gradient is kept per lane
 // over all rows of a workgroup, written as one partial row per workgroup and summed in a
-// fixed order. All sums are float32 (the partial rows' 64-bit). Times, forward / backward: 524288
-// rows of 128 with a gate, bf16, 85 / 142 us (4.7 TB/s); 32768 rows of 2048 with the residual
-// before, bf16, 93 / 146 us (5.8 / 4.6 TB/s); 5003 rows of 1537 with gate and residual, float32,
-// element by element, 23 / 31 us (5.3 / 4.9 TB/s). A large copy reaches 4.8 TB/s.
+// fixed order. Sums are float32; those of many terms, whose roundings can all fall the same way,
+// 64-bit: the partial rows', and a lane's over a longer row (up to 65536 terms; costs under 1 %).
+// Times, forward / backward: 524288 rows of 128 with a gate, bf16, 85 / 142 us (4.7 TB/s); 32768
+// rows of 2048 with the residual before, bf16, 93 / 146 us (5.8 / 4.6 TB/s); 5003 rows of 1537 with
+// gate and residual, float32, element by element, 23 / 31 us (5.3 / 4.9 TB/s); longer rows, 4096 of
+// 16384, bf16, 60 / 313 us (4.4 / 1.3 TB/s: the backward reads its rows twice and adds to its
+// partial row in memory once per row). A large copy reaches 4.8 TB/s.
 #include "dynconv_common.hpp"
 #include "dynconv_internal.hpp"
 #include "dynconv_norm_internal.hpp"
@@ -195,14 +198,14 @@ __global__ __launch_bounds__(kThreads) void k_norm_fwd(const NormParams p) {
       if (c < p.D) finish(v[i], g[i], s[i], rstd, c);
     }
   } else {
-    float ss = 0.f;
+    double ss = 0.0;
     for (int c = lane * E; c < p.D; c += LPR * E) {
       float v[E];
       value(v, c);
 #pragma unroll
-      for (int e = 0; e < E; ++e) ss += v[e] * v[e];
+      for (int e = 0; e < E; ++e) ss += double(v[e]) * double(v[e]);
     }
-    const float rstd = 1.f / sqrtf(row_sum<LPR>(ss, red) * inv + p.eps);
+    const float rstd = 1.f / sqrtf(row_sum<LPR>(float(ss), red) * inv + p.eps);
     for (int c = lane * E; c < p.D; c += LPR * E) {
       float v[E], g[E], s[E];
       value(v, c);
@@ -326,7 +329,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd(const NormParams p) {
         for (int e = 0; e < E; ++e) w[e] = 1.f;
         if (p.weight != nullptr) load<ET>(w, p.weight, c);
       };
-      float ss = 0.f, sd = 0.f;
+      double ss = 0.0, sd = 0.0;
       for (int c = lane * E; c < p.D; c += LPR * E) {
         float x[E], dy[E], z[E], w[E];
         fetch(x, dy, z, w, c);
@@ -334,12 +337,12 @@ __global__ __launch_bounds__(kThreads) void k_norm_bwd(const NormParams p) {
         for (int e = 0; e < E; ++e) {
           float dn, act, dact;
           terms(x, dy, z, w, e, dn, act, dact);
-          ss += x[e] * x[e];
-          sd += dn * x[e];
+          ss += double(x[e]) * double(x[e]);
+          sd += double(dn) * double(x[e]);
         }
       }
-      const float rstd = 1.f / sqrtf(row_sum<LPR>(ss, red[0]) * inv + p.eps);
-      const float cm = row_sum<LPR>(sd, red[1]) * inv * rstd;
+      const float rstd = 1.f / sqrtf(row_sum<LPR>(float(ss), red[0]) * inv + p.eps);
+      const float cm = row_sum<LPR>(float(sd), red[1]) * inv * rstd;
       // the partial sums of a lane's columns stay in the workgroup's own row of memory
       float* part = p.dw_part + int64_t(blockIdx.x) * p.D;
       for (int c = lane * E; c < p.D; c += LPR * E) {

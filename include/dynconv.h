@@ -453,7 +453,7 @@ dynconv_status dynconv_delta_step(const void* q, const int64_t* qs, const void* 
  *                            with a residual before
  *   weight                   [D] of `dtype`, contiguous, or NULL (ones)
  * Any D up to 2^24; element alignment (rows that allow 16-byte accesses use them). Sums are
- * float32. y and h may not be an input or each other (DYNCONV_ERR_INVALID_ARG).
+ * held to float32 accuracy for any D. y and h may not be an input or each other (DYNCONV_ERR_INVALID_ARG).
  */
 dynconv_status dynconv_norm_fwd(const void* x, const int64_t* xs, const void* weight, const void* gate,
                                 const int64_t* gs, const void* residual, const int64_t* rs, int32_t residual_after,
