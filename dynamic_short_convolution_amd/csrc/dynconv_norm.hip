@@ -11,6 +11,7 @@
 // over all rows of a workgroup, written as one partial row per workgroup and summed in a
 // fixed order. Sums are float32; those of many terms, whose roundings can all fall the same way,
 // 64-bit: the partial rows', and a lane's over a longer row (up to 65536 terms; costs under 1 %).
+// A lane's part of the weight's gradient has at most 512 rows.
 // Times, forward / backward: 524288 rows of 128 with a gate, bf16, 85 / 142 us (4.7 TB/s); 32768
 // rows of 2048 with the residual before, bf16, 93 / 146 us (5.8 / 4.6 TB/s); 5003 rows of 1537 with
 // gate and residual, float32, element by element, 23 / 31 us (5.3 / 4.9 TB/s); longer rows, 4096 of
@@ -488,7 +489,9 @@ hipError_t dispatch(const NormParams& p, dynconv_dtype dt, bool vec, bool bwd, i
 int64_t norm_bwd_blocks(int64_t rows, int64_t D, dynconv_dtype dt, bool vec) {
   const int rpb = kThreads / norm_plan(D, vec_elems(dt, vec)).lpr;
   const int64_t need = (rows + rpb - 1) / rpb;
-  return need < 1024 ? need : 1024;
+  // four workgroups per CU, and more where a lane would add over 512 rows to its float32 sums
+  const int64_t most = need > 512 * 1024 ? (need + 511) / 512 : 1024;
+  return need < most ? need : most;
 }
 
 int64_t norm_bwd_blocks_max(int64_t rows, int64_t D, dynconv_dtype dt) {

@@ -1,4 +1,4 @@
-"""Rows of the norm that are too long for the registers, up to the limit of 2^24 elements."""
+"""Long sums of the norm: rows up to the limit of 2^24 elements, and the weight gradient over many rows."""
 import numpy as np
 import pytest
 import torch
@@ -42,3 +42,15 @@ def test_longest_rows(D, dtype):
     assert np.max(np.abs(to64(dx) - rx) / (np.abs(dn) + np.max(np.abs(dn)))) <= tol
     assert np.max(np.abs(to64(dw) / rw - 1)) <= 32 * 2.0**-24  # one row: dy silu(z) n, float32 in both types
     assert np.max(np.abs(to64(dz) / rz - 1)) <= tol
+
+
+def test_weight_gradient_of_many_rows():
+    """2^27 equal rows of one element: a float32 sum of equal terms can be off by half a step of 2^-24 at
+    each addition, all the same way: for n terms by n / 2 * 2^-24 of it. A lane adds at most 512
+    (256 * 2^-24), its workgroup 16 lanes (16), the rest is in 64 bits; a term has at most 16
+    roundings."""
+    rows = 2**27
+    x = torch.ones(rows, 1, dtype=torch.bfloat16, device="cuda")
+    dy = torch.full((rows, 1), 0.8984375, dtype=torch.bfloat16, device="cuda")
+    dw = dynconv_norm_bwd(x, torch.ones(1, dtype=torch.bfloat16, device="cuda"), dy, eps=0.1)[2]
+    assert abs(float(dw) / (rows * 0.8984375 / 1.1**0.5) - 1) <= (256 + 16 + 16) * 2.0**-24
