@@ -123,3 +123,40 @@ def test_one_token_of_any_stride(kind, dk, dv, dtype):
         torch.cuda.current_stream().cuda_stream))
     assert all(torch.equal(a, b) for a, b in zip([t for _, t in outs] + [dg, db, dst], grads))
     assert all(int(torch.isfinite(b).sum()) == t.numel() for b, t in outs)
+
+
+# ---------------------------------------------------------------------------------
+# Broadcast inputs
+# ---------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (37, 51), (128, 40)])
+@pytest.mark.parametrize("shared", ["q", "k", "v", "g", "beta", "do", "state", "all"])
+def test_broadcast_inputs_are_their_copies(shared, dk, dv, dtype):
+    """Inputs with strides of 0, over sequences, tokens or heads, against contiguous copies: the same
+    values through the same kernels, so the same bits. One row of k for all tokens takes the kernels
+    for overlapping rows, whose float32 sums of the same terms may be contracted differently: each side's
+    are within 4e-6 of the largest of the exact ones (dg 1e-5), and rounding puts each off by at
+    most half a step."""
+    B, T, H = 2, 80, 2
+    args = make(131, B, T, H, H, dk, dv, dtype) + [rand(132, B, T, H, dv, dtype=TD[dtype]), rand(133, B, H, dk, dv)]
+    names = ["q", "k", "v", "g", "beta", "do", "state"]
+    over = [0, 1, 2, 2, 1, 0, 0]  # the dimension that is broadcast
+    sizes = [a.shape for a in args]
+    ex = [a.narrow(d, 0, 1).expand(s) if shared in (n, "all") else a for n, a, d, s in zip(names, args, over, sizes)]
+    full = [a.contiguous() for a in ex]
+    assert any(0 in a.stride() for a in ex)
+
+    def run(q, k, v, g, beta, do, state):
+        o, last = dynconv_delta_fwd(q, k, v, g, beta, qk_norm_eps=EPS, state=state, want_state=True)
+        return [o, last, *dynconv_delta_bwd(q, k, v, g, beta, do, qk_norm_eps=EPS, state=state, need_dstate=True)]
+
+    for name, a, b in zip(("o", "state", "dq", "dk", "dv", "dg", "dbeta", "dstate"), run(*ex), run(*full)):
+        if dk % 8 or shared not in ("k", "all"):
+            assert torch.equal(a, b), name
+            continue
+        step = 0.0 if a.dtype == torch.float32 else torch.finfo(a.dtype).eps
+        a, b = a.double(), b.double()
+        off = (a - b).abs() - step * torch.maximum(a.abs(), b.abs())
+        assert float(off.max()) <= 2 * (1e-5 if name == "dg" else 4e-6) * float(b.abs().max()), name
