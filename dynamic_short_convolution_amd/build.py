@@ -5,7 +5,10 @@ Usage: python -m dynamic_short_convolution_amd.build   (or build() from Python).
 from __future__ import annotations
 
 import concurrent.futures
+import glob
 import os
+import re
+import shutil
 import subprocess
 import sys
 
@@ -55,8 +58,7 @@ COMPILE_FLAGS = [
 
 # Sources with kernels of more than 256 registers are built without the last two flags: past 256,
 # the compiler's pass that moves VGPR-form matrix-core operands to accumulation registers has
-# crashed here, and gave wrong sums in one instantiation (float32, two value heads per key head,
-# unaligned rows). Within 256 registers, as in bfloat16, the flags change these kernels' times
+# crashed here. Within 256 registers, as in bfloat16, the flags change these kernels' times
 # by less than 2 %.
 PLAIN_MFMA_SOURCES = ("dynconv_delta_f32.hip", "dynconv_delta_bf16.hip", "dynconv_delta_f16.hip")
 
@@ -65,12 +67,59 @@ def compile_flags(src: str) -> list[str]:
     return COMPILE_FLAGS[:-2] if src in PLAIN_MFMA_SOURCES else COMPILE_FLAGS
 
 
+_VECTOR = re.compile(r"(?:v_(?!readlane|writelane|readfirstlane)|scratch_|ds_|global_|buffer_|flat_)")
+_COPY = re.compile(r"(?:v_mov_b|v_accvgpr_|scratch_)")
+_EXEC = re.compile(r"\bexec\b")
+
+
+def misplaced_vector_code(listing: str) -> list[str]:
+    """Vector instructions of an assembly listing that run under a divergent branch's execution mask
+    though they belong behind it.
+
+    The block where the lanes of a divergent branch meet begins by restoring the mask. When the
+    compiler splits a register's live range at that block it can put the copy or spill before the
+    restoring, if a scalar copy already stands there: lanes (or whole waves) that did not take the
+    branch then keep what the register or its scratch place held before. Seen with this compiler: a
+    spilled sum of the delta rule's chunk gradients (float32, 128-wide heads, two value heads per key
+    head), lost in six of eight waves, with no diagnostic."""
+    found = []
+    joins = set(re.findall(r"s_cbranch_execz (\.LBB\d+_\d+)\b", listing))
+    for m in re.finditer(r"^\s+(?:s_or_b64 exec, exec,|s_or_saveexec_b64).*$", listing, re.M):
+        start = max(listing.rfind("\n.LBB", 0, m.start()), listing.rfind("\n; %bb.", 0, m.start()))
+        if start < 0:
+            continue
+        head, *body = listing[start + 1:m.start()].split("\n")
+        lines = [t for t in (x.split(";")[0].strip() for x in body) if t and not t.startswith(".")]
+        if any(t.startswith(("s_cbranch", "s_branch")) or (_EXEC.search(t) and not re.match(r"s_and(n2)?_b64 vcc, exec", t))
+               for t in lines):
+            continue  # the mask was written since
+        vector = [t for t in lines if _VECTOR.match(t)]
+        # a block that no branch leads to may be the branch's own body: only copies and spills tell
+        if vector and (head.split(":")[0] in joins or (head.startswith(";") and all(_COPY.match(t) for t in vector))):
+            line = listing.count("\n", 0, m.start()) + 1
+            found.append(f"line {line}, {head.split(':')[0]}: {'; '.join(vector[:3])}")
+    return found
+
+
 def _compile(src: str) -> str:
-    obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-    cmd = [HIPCC, *compile_flags(src), "-c", os.path.join(CSRC, src), "-o", obj]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed for {src}:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    stem = os.path.splitext(src)[0]
+    obj, work = os.path.join(BUILD_DIR, stem + ".o"), os.path.join(BUILD_DIR, stem + ".tmp")
+    shutil.rmtree(work, ignore_errors=True)
+    os.makedirs(work)
+    try:
+        tmp = os.path.join(work, stem + ".o")
+        cmd = [HIPCC, *compile_flags(src), "-save-temps=obj", "-c", os.path.join(CSRC, src), "-o", tmp]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"hipcc failed for {src}:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+        (name,) = glob.glob(os.path.join(work, "*amdgcn*.s"))
+        with open(name) as f:
+            found = misplaced_vector_code(f.read())
+        if found:
+            raise RuntimeError(f"{src}: vector code before the execution mask is restored:\n" + "\n".join(found[:10]))
+        os.replace(tmp, obj)
+    finally:
+        shutil.rmtree(work, ignore_errors=True)
     return obj
 
 

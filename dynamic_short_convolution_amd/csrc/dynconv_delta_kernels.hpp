@@ -1575,7 +1575,8 @@ __global__ __launch_bounds__((64 * GradLds<ET, DK, ONE>::NW), (Store<ET>::NT == 
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) dP[s] = F[s] = zero4();
     if (gh > 0) __syncthreads();  // the previous head's factors are read
-    if (tid < kTokArrays * C / 4)
+    static_assert(kTokArrays * C / 4 % 64 == 0, "whole waves: no divergent branch while the sums over heads are held");
+    if (wave < kTokArrays * C / 4 / 64)
       reinterpret_cast<f32x4_t*>(tok)[tid] = reinterpret_cast<const f32x4_t*>(p.wTok + ci * (kTokArrays * C))[tid];
     f32x4_t os[4][NN], rs[4][NN], ug[4][NN];
 #pragma unroll
@@ -1730,6 +1731,9 @@ __global__ __launch_bounds__((64 * GradLds<ET, DK, ONE>::NW), (Store<ET>::NT == 
         }
         aq[mt][n] += os[mt][n];
         ak[mt][n] += ug[mt][n] - be * rs[mt][n];
+        // added here: left to itself the compiler adds at the next use, and spills up to 33 of the
+        // terms that it holds until then
+        asm volatile("" : "+v"(aq[mt][n]), "+v"(ak[mt][n]));
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
