@@ -616,8 +616,8 @@ __global__ __launch_bounds__(256) void k_delta_prep(const DeltaParams p) {
     norms(tq, tok + kTokRq * C);
   }
   if (wave == 0) {
-    // exp(-128) is 0 in float32: such a token keeps nothing of what came before it
-    if (g <= -128.f) cut = true;
+    // exp is 0 in float32 below 2^-150: such a token keeps nothing of what came before it
+    if (g <= -103.972084f) cut = true;
     if (cut) g = 0.f;
     const unsigned long long mask = __ballot(cut);
     const int cnt = __popcll(mask & ((2ull << lane) - 1ull));
@@ -1454,9 +1454,11 @@ __global__ __launch_bounds__(2 * DK) void k_delta_join(const DeltaParams p, uint
 // part along q (k) away: dq = dq' - rq q (rq q.dq'). The decay's gradient adds up all paths
 // that cross a token, dg_t = sum_{i >= t > j} X_ij + sum_{i >= t} into_i + sum_{j < t} out_j
 // + gamma <S0, dS1> with X = Y o Q K^T + Yk o K K^T, from row and column sums of the same
-// products, so that pairs on one side of t cancel exactly, into = rq scale E (q.os) - beta E
-// rk (k.rs) and out = D rk (k.ug); the cumulative sums are in 64 bits. dbeta_i = dR_i.V_i -
-// E rk (k.rs)_i + sum_j dA_ij Gam k.k. What reaches dg keeps all terms (float32).
+// products, so that pairs on one side of t cancel but for the float32 rounding of the tiles'
+// sums, and only over t's own document, so that no rounding of another one's is left in it; into =
+// rq scale E (q.os) - beta E rk (k.rs) and out = D rk (k.ug); the cumulative sums are in 64 bits.
+// dbeta_i = dR_i.V_i - E rk (k.rs)_i + sum_j dA_ij Gam k.k. What reaches dg keeps all terms
+// (float32).
 
 template <typename ET, int DK, bool ONE>
 struct GradLds {
@@ -1835,13 +1837,13 @@ __global__ __launch_bounds__((64 * GradLds<ET, DK, ONE>::NW), (Store<ET>::NT == 
         db += sum[8 * C + s * C + lane];
       }
       const double own = ahead;
+      const int n = __float_as_int(tok[kTokN * C + lane]);
 #pragma unroll
       for (int m = 1; m < 64; m <<= 1) {
         const double a = __shfl_up(ahead, m), h = __shfl_down(behind, m);
-        if (lane >= m) ahead += a;
+        if (__shfl_up(n, m) == n && lane >= m) ahead += a;
         if (lane + m < 64) behind += h;
       }
-      const int n = __float_as_int(tok[kTokN * C + lane]);
       const int before = lane == 0 ? 0 : __float_as_int(tok[kTokN * C + lane - 1]);
       const float dg = n != before ? 0.f : float(ahead - own + behind + double(through));
       if (lane < rows) {

@@ -383,7 +383,7 @@ dynconv_status dynconv_cache_fill_varlen(const void* x, const int64_t* xs, const
  *              state_in itself (same strides). T == 0 copies the state.
  * A token with beta = 0 and g = 0 leaves the state as it is (padding behind a sequence, whose
  * q, k, v have to be finite, and q and k not zero when qk_norm_eps is 0).
- * g <= -128 counts as a decay to exactly zero (exp of it is 0 in float32). Tokens are worked
+ * A g whose exp is 0 in float32 (below -103.97) is a decay to exactly zero. Tokens are worked
  * on 64 at a time: a NaN or infinity among a head's inputs can reach every output of its
  * 64-token chunk and of what follows, other documents included; other heads keep theirs.
  * Limits (DYNCONV_ERR_UNSUPPORTED otherwise): dk <= 128, dv <= 65536; strides >= 0, token

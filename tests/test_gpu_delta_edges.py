@@ -160,3 +160,31 @@ def test_broadcast_inputs_are_their_copies(shared, dk, dv, dtype):
         a, b = a.double(), b.double()
         off = (a - b).abs() - step * torch.maximum(a.abs(), b.abs())
         assert float(off.max()) <= 2 * (1e-5 if name == "dg" else 4e-6) * float(b.abs().max()), name
+
+
+# ---------------------------------------------------------------------------------
+# The decay's gradient stays in its document
+# ---------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("decay", [None, -float("inf"), -200.0, -104.0])
+def test_decay_gradient_stays_in_its_document(decay, dtype):
+    """Two documents in one row (or a token whose decay is 0 in float32 in the start's place), the second
+    without a gradient of its own: every gradient of it is 0, not what is left of the first one's
+    sums when they are taken off again."""
+    B, T, H, dk, dv, start = 1, 100, 2, 64, 64, 41
+    args = make(141, B, T, H, H, dk, dv, dtype)
+    args[3][:, 5, 0] = -104.5
+    seq = None
+    if decay is None:
+        seq = (torch.arange(T, device="cuda", dtype=torch.int32) >= start).to(torch.int32).expand(B, T).contiguous()
+    else:
+        args[3][:, start] = decay
+    do = rand(142, B, T, H, dv, dtype=TD[dtype])
+    do[:, start:] = 0.0
+    check(args, seq=seq, do=do)
+    grads = dynconv_delta_bwd(*args, do, qk_norm_eps=EPS, seq_idx=seq)
+    for name, t in zip(("dq", "dk", "dv", "dg", "dbeta"), grads):
+        assert float(t[:, :start].abs().max()) > 0.0 and float(t[:, start:].abs().max()) == 0.0, name
+    assert float(grads[3][:, 5, 0].abs().max()) == 0.0  # exp(-104.5) is 0
