@@ -7,7 +7,7 @@ import torch
 from dynamic_short_convolution_amd import _lib, dynconv_delta_bwd, dynconv_delta_fwd, dynconv_delta_step
 from oracle import delta_bwd, delta_fwd
 from tests.parity import to64
-from tests.test_gpu_delta import EPS, TD, check, close, make, rand
+from tests.test_gpu_delta import EPS, TD, check, close, documents, make, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -188,3 +188,26 @@ def test_decay_gradient_stays_in_its_document(decay, dtype):
     for name, t in zip(("dq", "dk", "dv", "dg", "dbeta"), grads):
         assert float(t[:, :start].abs().max()) > 0.0 and float(t[:, start:].abs().max()) == 0.0, name
     assert float(grads[3][:, 5, 0].abs().max()) == 0.0  # exp(-104.5) is 0
+
+
+# ---------------------------------------------------------------------------------
+# Every instantiation of the kernels
+# ---------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dk", [64, 128])
+@pytest.mark.parametrize("group", [1, 2, 3])
+@pytest.mark.parametrize("wide", [True, False], ids=["rows16", "elements"])
+@pytest.mark.parametrize("T", [100, 580], ids=["whole", "segments"])
+def test_every_instantiation(T, wide, group, dk, dtype):
+    """Each storage type, padded key width, way of loading rows, and head grouping, over one scan and
+    over segments, forwards and backwards, against the oracle."""
+    B, Hk, dv = 1, 1, 40
+    args = make(151, B, T, Hk, Hk * group, dk, dv, dtype, decay=0.3)
+    if not wide:  # one element off a 16-byte boundary
+        for i in range(3):
+            off = torch.zeros(args[i].numel() + 1, dtype=args[i].dtype, device="cuda")[1:].view(args[i].shape)
+            args[i] = off.copy_(args[i])
+    H = Hk * group
+    check(args, seq=documents(152, B, T, 70), state=rand(153, B, H, dk, dv), dstate_out=rand(154, B, H, dk, dv))
