@@ -25,12 +25,12 @@
 // one as itself, and the products of terms whose orders add up to more than 2 (two, of at most
 // 2^-22 of the factors' product each) are left out. That holds states and sums at float32
 // accuracy at 2.7 times the rate of the float32 matrix instructions (6 products for two float32
-// operands, 3 for a bf16 one). Operands formed here (P, S0, U, Y, Yk) of products that only reach
-// 16-bit results are rounded to two terms (to nearest, at most 2^-17 off, S0 2^-16), and the product
-// of two second terms (at most 2^-15) is left out: a third term would add half as many products
-// again and LDS that the kernels do not have, to results that are themselves rounded to 2^-9 or
-// 2^-12 (root mean square against 64 bits, relative to that of rounding the exact result: bf16
-// 1.00001, float16 1.0004).
+// operands, 3 for a bf16 one). Operands formed here of products that only reach 16-bit results
+// have two terms (P, U, Y, Yk rounded to nearest, at most 2^-17 off; S0 the first two of its three,
+// 2^-15), and the product of two second terms (at most 2^-15) is left out: a third term would add
+// half as many products again and LDS that the kernels do not have, to results that are themselves
+// rounded to 2^-9 or 2^-12 (root mean square against 64 bits, relative to that of rounding the exact
+// result: bf16 1.00001, float16 1.0004).
 #pragma once
 
 #include "dynconv_common.hpp"
@@ -120,8 +120,8 @@ __device__ __forceinline__ float below(float x) {  // x without its first 8 sign
 // The next of N terms of 4 values; x keeps what is left (exact). Three terms hold a float32 whole,
 // so they are cut off, which is the shorter chain (rounding them too: prefill of 32768 tokens 693
 // to 731 us). Two leave something out and are rounded to nearest, so that it has either sign (cut
-// off, float16 outputs came out 2^-15 too small on average; the training step of packed documents
-// 717 us so, 729 rounded, the others within 0.5 %).
+// off, float16 outputs came out 2^-15 too small on average, and every workload took the same time
+// within 1 %).
 template <int N, bool LAST>
 __device__ __forceinline__ u32x2 next_term(f32x4_t& x) {
   if constexpr (N < 3) {
@@ -148,21 +148,6 @@ __device__ __forceinline__ Frag<N> split8(f32x4_t a, f32x4_t b) {
     f.t[n] = u32x4{u[0], u[1], v[0], v[1]};
   }
   return f;
-}
-// The same values in three terms and in NP: the first of three and the rest of it rounded to one.
-template <int NP>
-__device__ __forceinline__ void split8_both(Frag<3>& f, Frag<NP>& g, f32x4_t a, f32x4_t b) {
-  f = split8<3>(a, b);
-#pragma unroll
-  for (int n = 0; n < NP; ++n) g.t[n] = f.t[n];
-  if constexpr (NP == 2) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      a[e] = below(a[e]);
-      b[e] = below(b[e]);
-    }
-    g.t[1] = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
-  }
 }
 
 // Row-major LDS matrices keep each 32-column block in fragment order: columns 4q .. 4q+3 at
@@ -1052,9 +1037,15 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
       f32x4_t te[4], tr[4], tb[4];
       row_load<NT>(fk, sK, TK::LD, TK::PLANE, ln);
       Frag<3> sf[KB];
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) sf[kb] = split8<3>(S[2 * kb], S[2 * kb + 1]);
+      // for the outputs the first NP of them (a second term rounded for itself: 347 us instead of 337
+      // at B8 T4096, and the same errors against 64 bits)
       Frag<NP> so[KB];
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) split8_both<NP>(sf[kb], so[kb], S[2 * kb], S[2 * kb + 1]);
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int n = 0; n < NP; ++n) so[kb].t[n] = sf[kb].t[n];
       if constexpr (PAIR) hand_over<NP, KB>(lds + L::HS + cw * L::HSW, so, ln);
       row_product<2, KB>(z, fk, sK, TK::LD, TK::PLANE, sf, [&] {
         if constexpr (!STATES && !PAIR) row_load<NT>(fk, sQ, TK::LD, TK::PLANE, ln);
