@@ -828,7 +828,7 @@ __device__ __forceinline__ ScanAt scan_at(const DeltaParams& p, uint32_t bid, in
 // 128 x 128 has 8 such waves, so a batch that fills the chip has one per SIMD, and a lone wave
 // issues an instruction about every 5 cycles. The outputs do not feed the recurrence: where LDS
 // allows (16-bit storage), a second wave on the same SIMD forms P, Q S0 and P U from the terms of
-// S0 and U that the first leaves in LDS (B8 T4096, 16 heads, bf16: 368 us with one wave, 312 with
+// S0 and U that the first leaves in LDS (B8 T4096, 16 heads, bf16: 368 us with one wave, 323 with
 // two; 0.7 GB would take 146 at the rate of a copy). What bounds it now is the chain of a chunk
 // (barriers, the terms' splits between products): the vector units are busy for 46 % of the
 // time, LDS for 45 %, the matrix units for 31 %.
@@ -995,7 +995,7 @@ __device__ __forceinline__ void delta_scan(const DeltaParams p, char* lds, uint3
     }
   }
 
-  if constexpr (PAIR) __builtin_amdgcn_s_setprio(1);  // the chain that sets the time (318 -> 312 us)
+  if constexpr (PAIR) __builtin_amdgcn_s_setprio(1);  // the chain that sets the time (2 % of it)
   f32x4_t S[DK / 16];
   if (at.seg == 0 && (MODE == kEnds || p.nSeg == 1)) {
     load_state<DK>(S, p.state_in == nullptr ? nullptr : p.state_in + b * p.sis0 + hv * p.sis1, p.sis2, p.dkn, col, ok, ln);
@@ -1348,8 +1348,8 @@ __device__ __forceinline__ void delta_back(const DeltaParams p, char* lds, uint3
 }
 
 // Both scans of the backward: the first `back` workgroups carry dS, the others S. At B8 T4096, 16
-// heads, bf16 703 us; they write 1.7 GB of images and read 0.6 GB, 480 us at the rate of a copy,
-// and the CU's vector units are busy for 39 % of the time, LDS for 31 %, the matrix units for 25 %.
+// heads, bf16 707 us; they write 1.7 GB of images and read 0.6 GB, 480 us at the rate of a copy,
+// and the CU's vector units are busy for 40 % of the time, LDS for 32 %, the matrix units for 25 %.
 template <typename ET, int DK, int NW, bool ENDS, bool VEC>
 __global__ __launch_bounds__(64 * NW, Store<ET>::NT == 1 ? 2 : 1) void k_delta_scans(const DeltaParams p, uint32_t back) {
   extern __shared__ __align__(16) char lds[];
@@ -1360,7 +1360,7 @@ __global__ __launch_bounds__(64 * NW, Store<ET>::NT == 1 ? 2 : 1) void k_delta_s
   }
 }
 
-// The forward's first pass over segments (T 32768, 16 heads: 317 us in 8 segments).
+// The forward's first pass over segments (T 32768, 16 heads: 322 us in 8 segments).
 template <typename ET, int DK, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, 2) void k_delta_ends(const DeltaParams p) {
   extern __shared__ __align__(16) char lds[];
@@ -1505,11 +1505,12 @@ struct ImageTile {
   }
 };
 
-// ONE: a single value head per key head (no sums to carry from head to head). 611 to 651 us at B8
+// ONE: a single value head per key head (no sums to carry from head to head). 611 to 667 us at B8
 // T4096, 16 heads, bf16, for 1.3 GB (270 us at the rate of a copy): the images are read once, and what
-// bounds the kernel is the latency of its phases between barriers, with two waves per SIMD (the
-// five sums of 64 x 128 take most of the registers): vector units 43 % busy, LDS 33 %, matrix
-// units 28 %.
+// bounds the kernel is the latency of its phases between barriers, five per 32 value columns
+// because S0 and dS1 take turns in LDS (69 KiB, so that two workgroups share a CU), with two waves
+// per SIMD: vector units 44 % busy, LDS 34 %, matrix units 29 %. Of the 244 registers the three
+// sums of the column loop take 96 and the images under way 52 (all of them a block ahead: 50 spilled).
 template <typename ET, int DK, bool VEC, bool ONE>
 __global__ __launch_bounds__((64 * GradLds<ET, DK, ONE>::NW), (Store<ET>::NT == 1 && ONE ? 2 : 1)) void k_delta_grad(
     const DeltaParams p) {
