@@ -59,6 +59,13 @@ EXPORTS = (
     "dynconv_norm_fwd",
     "dynconv_norm_bwd",
     "dynconv_norm_bwd_workspace_size",
+    "dynconv_scan_fwd",
+    "dynconv_scan_fwd_workspace_size",
+    "dynconv_scan_bwd",
+    "dynconv_scan_bwd_workspace_size",
+    "dynconv_scan_step",
+    "dynconv_pack8",
+    "dynconv_unpack8",
 )
 
 # Bytes of the per-GPU scratch array of dynconv_bwd_ex_noalloc (DYNCONV_NOALLOC_SCRATCH_BYTES).
@@ -166,6 +173,18 @@ _SIGNATURES["dynconv_norm_bwd"] = (
     [_vp, _i64p, _vp, _vp, _i64p, _vp, _i64p, _vp, _i64p, _i32, _f32, _vp, _i64p, _vp, _i64p, _vp, _vp, _i64p, _i64,
      _i64, _i64, _i64, _f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int)
 _SIGNATURES["dynconv_norm_bwd_workspace_size"] = ([_i64] * 4 + [ctypes.c_int], _sz)
+# gated linear scan: (pointer, strides) pairs, rate, then sizes
+_SIGNATURES["dynconv_scan_fwd"] = (  # x, decay, gate; rate; seq_idx, state_in, y, state_out; chunks
+    [_vp, _i64p] * 3 + [_vp] + [_vp, _i64p] * 4 + [_vp] + [_i64] * 3 + [ctypes.c_int, _vp, _sz, _vp], ctypes.c_int)
+_SIGNATURES["dynconv_scan_fwd_workspace_size"] = ([_i64] * 3 + [ctypes.c_int], _sz)
+_SIGNATURES["dynconv_scan_bwd"] = (  # + scales; rate; seq_idx, state_in; chunks; dy, dstate_out, dx, ddecay; drate; dgate, dstate
+    [_vp, _i64p] * 6 + [_vp] + [_vp, _i64p] * 2 + [_vp] + [_vp, _i64p] * 4 + [_vp] + [_vp, _i64p] * 2 + [_i64] * 3
+    + [ctypes.c_int, _vp, _sz, _vp], ctypes.c_int)
+_SIGNATURES["dynconv_scan_bwd_workspace_size"] = ([_i64] * 3 + [_i32, ctypes.c_int], _sz)
+_SIGNATURES["dynconv_scan_step"] = (
+    [_vp, _i64p] * 3 + [_vp] + [_vp, _i64p] * 2 + [_i64] * 2 + [ctypes.c_int, _vp], ctypes.c_int)
+_SIGNATURES["dynconv_pack8"] = ([_vp, _i64p] * 3 + [_i64] * 4 + [ctypes.c_int, _vp], ctypes.c_int)
+_SIGNATURES["dynconv_unpack8"] = _SIGNATURES["dynconv_pack8"]
 
 _lib = None
 

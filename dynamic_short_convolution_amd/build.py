@@ -37,6 +37,12 @@ SOURCES = [
     "dynconv_delta_bf16.hip",
     "dynconv_delta_f16.hip",
     "dynconv_norm.hip",
+    "dynconv_scan_abi.hip",
+    "dynconv_scan.hip",
+    "dynconv_scan_f32.hip",
+    "dynconv_scan_bf16.hip",
+    "dynconv_scan_f16.hip",
+    "dynconv_pack.hip",
 ]
 
 # -packed-fp32-ops: no v_pk_{add,mul,fma}_f32 are generated from ordinary float code.

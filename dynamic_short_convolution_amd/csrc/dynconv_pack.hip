@@ -1,0 +1,259 @@
+// Activations in 8 bits (checkpoints for a backward pass) and back, gfx950.
+//
+// Per row, every 64 channels share a step 2^e, e = floor(log2 max|x|) - 6 (at least -126): the largest
+// value is 64 to 127.99 steps, so codes round(x / step), to nearest even and cut at 127, are off by at
+// most half a step below 127.5 of them and by less than one above: 1/128 of the largest value. Multiplying
+// by a power of two is exact, so the codes do not depend on the arithmetic, and code times step fits
+// the type that was packed. A group that holds an infinity or NaN gets the scale 255 and codes 0: it reads as
+// NaN (0 times infinity), as the scale's bits 255 << 23 say without a test.
+// Memory bound: 16 bytes per lane where rows allow it, the maximum by a butterfly over the group's
+// lanes; else one element per lane and a wave per group.
+#include "dynconv_common.hpp"
+#include "dynconv_internal.hpp"
+
+namespace dynconv {
+
+namespace {
+
+constexpr int kThreads = 256, kGroup = 64;
+
+struct PackTensor {
+  const void* p;
+  int64_t s0, s1, s2;
+};
+struct PackParams {
+  PackTensor x, codes, scales;
+  int64_t items;  // rows * lanes of a row (whole groups)
+  uint32_t n1, n2, D, perRow;
+};
+
+template <int N>
+struct Bytes;
+template <>
+struct Bytes<1> {
+  typedef uint8_t T;
+};
+template <>
+struct Bytes<4> {
+  typedef uint32_t T;
+};
+template <>
+struct Bytes<8> {
+  typedef u32x2 T;
+};
+
+struct At {
+  int64_t i0;
+  uint32_t i1, i2, c;  // c: the lane's first channel
+};
+template <int E>
+__device__ __forceinline__ At place(const PackParams& p, int64_t item) {
+  At a;
+  const uint64_t row = uint64_t(item) / p.perRow;
+  a.c = uint32_t(uint64_t(item) - row * p.perRow) * E;
+  const uint32_t r = uint32_t(row);  // below 2^31
+  const uint32_t q = r / p.n2;
+  a.i2 = r - q * p.n2;
+  a.i0 = q / p.n1;
+  a.i1 = q - uint32_t(a.i0) * p.n1;
+  return a;
+}
+__device__ __forceinline__ int64_t offset(const PackTensor& t, const At& a) { return a.i0 * t.s0 + a.i1 * t.s1 + a.i2 * t.s2; }
+
+template <typename ET, int E>
+__device__ __forceinline__ void read(float (&v)[E], const PackTensor& t, int64_t off) {
+  if constexpr (E == 1) {
+    if constexpr (sizeof(ET) == 2) {
+      v[0] = Cvt<ET>::of_bits(static_cast<const uint16_t*>(t.p)[off]);
+    } else {
+      v[0] = static_cast<const float*>(t.p)[off];
+    }
+  } else {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const ET*>(t.p) + off);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(ET) == 2) {
+        v[2 * i] = Cvt<ET>::lo(w[i]), v[2 * i + 1] = Cvt<ET>::hi(w[i]);
+      } else {
+        v[i] = __uint_as_float(w[i]);
+      }
+    }
+  }
+}
+
+template <typename ET, int E>
+__global__ __launch_bounds__(kThreads) void k_pack8(const PackParams p) {
+  const int64_t item = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
+  if (item >= p.items) return;  // whole groups of lanes
+  const At a = place<E>(p, item);
+  float v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = 0.f;
+  if (a.c < p.D) read<ET, E>(v, p.x, offset(p.x, a) + a.c);
+  uint32_t top = 0;  // as integers the magnitudes keep their order, and infinities and NaN come last
+#pragma unroll
+  for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+#pragma unroll
+  for (int m = 1; m < kGroup / E; m <<= 1) top = max(top, uint32_t(__shfl_xor(int(top), m)));
+  const int biased = int(top >> 23);
+  const bool lost = biased == 255;
+  const uint32_t scale = lost ? 255u : uint32_t(max(biased - 6, 1));
+  const float inverse = lost ? 0.f : __uint_as_float((254u - scale) << 23);
+  uint32_t code[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float q = fminf(fmaxf(rintf(v[e] * inverse), -127.f), 127.f);
+    code[e] = lost ? 0u : uint32_t(int(q)) & 0xffu;
+  }
+  if (a.c >= p.D) return;
+  if (a.c % kGroup == 0)
+    const_cast<uint8_t*>(static_cast<const uint8_t*>(p.scales.p))[offset(p.scales, a) + a.c / kGroup] = uint8_t(scale);
+  typename Bytes<E>::T w;
+  if constexpr (E == 1) {
+    w = uint8_t(code[0]);
+  } else {
+    uint32_t q[E / 4];
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i)
+      q[i] = code[4 * i] | code[4 * i + 1] << 8 | code[4 * i + 2] << 16 | code[4 * i + 3] << 24;
+    if constexpr (E == 8) {
+      w = u32x2{q[0], q[1]};
+    } else {
+      w = q[0];
+    }
+  }
+  int8_t* out = const_cast<int8_t*>(static_cast<const int8_t*>(p.codes.p)) + offset(p.codes, a) + a.c;
+  *reinterpret_cast<typename Bytes<E>::T*>(out) = w;
+}
+
+template <typename ET, int E>
+__global__ __launch_bounds__(kThreads) void k_unpack8(const PackParams p) {
+  const int64_t item = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
+  if (item >= p.items) return;
+  const At a = place<E>(p, item);
+  if (a.c >= p.D) return;
+  const uint32_t scale = static_cast<const uint8_t*>(p.scales.p)[offset(p.scales, a) + a.c / kGroup];
+  const float step = __uint_as_float(scale << 23);
+  const auto w = *reinterpret_cast<const typename Bytes<E>::T*>(static_cast<const int8_t*>(p.codes.p) + offset(p.codes, a) + a.c);
+  float v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    uint32_t word;
+    if constexpr (E == 8) {
+      word = w[e / 4];
+    } else {
+      word = w;
+    }
+    v[e] = float(int8_t(word >> (8 * (e % 4)) & 0xff)) * step;
+  }
+  ET* out = const_cast<ET*>(static_cast<const ET*>(p.x.p)) + offset(p.x, a) + a.c;
+  if constexpr (E == 1) {
+    if constexpr (sizeof(ET) == 2) {
+      *reinterpret_cast<uint16_t*>(out) = Cvt<ET>::bits(v[0]);
+    } else {
+      *out = v[0];
+    }
+  } else {
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(ET) == 2) {
+        o[i] = Cvt<ET>::pack2(v[2 * i], v[2 * i + 1]);
+      } else {
+        o[i] = __float_as_uint(v[i]);
+      }
+    }
+    *reinterpret_cast<u32x4*>(out) = o;
+  }
+}
+
+template <typename ET, int E>
+hipError_t launch(PackParams p, int64_t rows, bool unpack, hipStream_t s) {
+  p.perRow = (p.D + kGroup - 1) / kGroup * (kGroup / E);
+  p.items = rows * p.perRow;
+  constexpr int64_t most = int64_t(1) << 23;  // a dimension of a launch has fewer than 2^32 threads
+  const int64_t blocks = (p.items + kThreads - 1) / kThreads;
+  const dim3 grid(unsigned(blocks < most ? blocks : most), unsigned((blocks + most - 1) / most));
+  if (unpack) {
+    hipLaunchKernelGGL((k_unpack8<ET, E>), grid, dim3(kThreads), 0, s, p);
+  } else {
+    hipLaunchKernelGGL((k_pack8<ET, E>), grid, dim3(kThreads), 0, s, p);
+  }
+  return hipGetLastError();
+}
+
+template <typename ET>
+hipError_t dispatch(const PackParams& p, int64_t rows, bool vec, bool unpack, hipStream_t s) {
+  return vec ? launch<ET, 16 / int(sizeof(ET))>(p, rows, unpack, s) : launch<ET, 1>(p, rows, unpack, s);
+}
+
+bool aligned(const void* p, int64_t a) { return (reinterpret_cast<uintptr_t>(p) % uint64_t(a)) == 0; }
+
+// A tensor [n0,n1,n2,last] of eb-byte elements, read or written in pieces of `piece` bytes where *vec.
+dynconv_status take(PackTensor* t, const void* p, const int64_t* s, const int64_t* n, int64_t last, int eb, int piece,
+                    bool output, bool* vec) {
+  if (p == nullptr || s == nullptr) return DYNCONV_ERR_INVALID_ARG;
+  if (!aligned(p, eb) || (last > 1 && s[3] != 1)) return DYNCONV_ERR_UNSUPPORTED;
+  if (!aligned(p, piece)) *vec = false;
+  for (int i = 0; i < 3; ++i) {
+    if (s[i] < 0) return DYNCONV_ERR_UNSUPPORTED;
+    if (n[i] <= 1) continue;
+    if (output && s[i] == 0) return DYNCONV_ERR_INVALID_ARG;
+    if (s[i] * eb % piece != 0) *vec = false;
+  }
+  t->p = p;
+  t->s0 = s[0], t->s1 = s[1], t->s2 = s[2];
+  return DYNCONV_OK;
+}
+
+dynconv_status run(const void* x, const int64_t* xs, const int8_t* codes, const int64_t* cs, const uint8_t* scales,
+                   const int64_t* ss, int64_t n0, int64_t n1, int64_t n2, int64_t D, dynconv_dtype dtype, bool unpack,
+                   void* stream) {
+  if (dtype != DYNCONV_F32 && dtype != DYNCONV_BF16 && dtype != DYNCONV_F16) return DYNCONV_ERR_INVALID_ARG;
+  const int64_t n[3] = {n0, n1, n2};
+  for (int64_t i : n)
+    if (i < 0) return DYNCONV_ERR_INVALID_ARG;
+  if (D < 0) return DYNCONV_ERR_INVALID_ARG;
+  for (int64_t i : n)
+    if (i > INT32_MAX) return DYNCONV_ERR_UNSUPPORTED;
+  if (D > (int64_t(1) << 24)) return DYNCONV_ERR_UNSUPPORTED;
+  if (n0 == 0 || n1 == 0 || n2 == 0 || D == 0) return DYNCONV_OK;
+  if (n0 > INT32_MAX / n1 || n0 * n1 > INT32_MAX / n2) return DYNCONV_ERR_UNSUPPORTED;
+  const int eb = dtype == DYNCONV_F32 ? 4 : 2;
+  bool vec = D * eb % 16 == 0, any = true;
+  PackParams p{};
+  dynconv_status st;
+  if ((st = take(&p.x, x, xs, n, D, eb, 16, unpack, &vec)) != DYNCONV_OK) return st;
+  if ((st = take(&p.codes, codes, cs, n, D, 1, 16 / eb, !unpack, &vec)) != DYNCONV_OK) return st;
+  if ((st = take(&p.scales, scales, ss, n, (D + kGroup - 1) / kGroup, 1, 1, !unpack, &any)) != DYNCONV_OK) return st;
+  if (x == static_cast<const void*>(codes) || x == static_cast<const void*>(scales) ||
+      static_cast<const void*>(codes) == static_cast<const void*>(scales))
+    return DYNCONV_ERR_INVALID_ARG;
+  p.n1 = uint32_t(n1), p.n2 = uint32_t(n2), p.D = uint32_t(D);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t rows = n0 * n1 * n2;
+  const hipError_t e = dtype == DYNCONV_BF16  ? dispatch<bf16_t>(p, rows, vec, unpack, s)
+                       : dtype == DYNCONV_F16 ? dispatch<f16_t>(p, rows, vec, unpack, s)
+                                              : dispatch<float>(p, rows, vec, unpack, s);
+  return e == hipSuccess ? DYNCONV_OK : record_hip_error(e);
+}
+
+}  // namespace
+
+}  // namespace dynconv
+
+extern "C" {
+
+dynconv_status dynconv_pack8(const void* x, const int64_t* xs, int8_t* codes, const int64_t* cs, uint8_t* scales,
+                             const int64_t* ss, int64_t n0, int64_t n1, int64_t n2, int64_t D, dynconv_dtype dtype,
+                             void* stream) {
+  return dynconv::run(x, xs, codes, cs, scales, ss, n0, n1, n2, D, dtype, false, stream);
+}
+
+dynconv_status dynconv_unpack8(const int8_t* codes, const int64_t* cs, const uint8_t* scales, const int64_t* ss, void* y,
+                               const int64_t* ys, int64_t n0, int64_t n1, int64_t n2, int64_t D, dynconv_dtype dtype,
+                               void* stream) {
+  return dynconv::run(y, ys, codes, cs, scales, ss, n0, n1, n2, D, dtype, true, stream);
+}
+
+}  // extern "C"

@@ -7,6 +7,7 @@ current stream, nothing else.
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 import torch
 
@@ -643,3 +644,189 @@ def dynconv_norm_bwd(x, weight, dy, gate=None, dh=None, residual_scale: float = 
             _NORM_RESIDUAL[residual_at], float(residual_scale), *_sp4(dx), *_sp4(dres), _dp(dw), *_sp4(dgate), *shape,
             float(eps), code, _dp(work), ws_bytes)
     return dx, dres, dw, dgate
+
+
+# ----------------------------------------------------------------------------------
+# Activations in 8 bits, for backward passes
+# ----------------------------------------------------------------------------------
+
+PACK8_GROUP = 64  # channels that share a scale
+
+
+class Packed8(NamedTuple):
+    """A tensor in 8 bits: int8 codes of its shape, and uint8 scales [..., ceil(D/64)] (the float32
+    exponent field of the step that 64 channels share). What dynconv_pack8 returns, and what the
+    backward calls that say so take in place of the tensor."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def _scales_shape(shape):
+    return (*shape[:-1], -(-shape[-1] // PACK8_GROUP))
+
+
+def _check_packed(name, p, shape):
+    """Checks a Packed8 operand of the given shape; returns it."""
+    _expect(f"{name}.codes", p.codes, shape, torch.int8)
+    _expect(f"{name}.scales", p.scales, _scales_shape(shape), torch.uint8)
+    return p
+
+
+def dynconv_pack8(x, out: Packed8 | None = None) -> Packed8:
+    """x (1 to 4 dimensions) in 8 bits: per row, every 64 channels are integers of -127 to 127 times
+    the power of two 2^(floor(log2 max|x|) - 6) that they share. Half the memory of 16-bit
+    activations (a quarter of float32) for what a training step keeps for its backward pass."""
+    shape = _norm_shape(x)
+    code = _dtype_code(x)
+    if out is not None:
+        _check_packed("out", out, x.shape)
+    dev = _require_device(x, *(out or ()))
+    if out is None:
+        out = Packed8(torch.empty(x.shape, dtype=torch.int8, device=dev),
+                      torch.empty(_scales_shape(x.shape), dtype=torch.uint8, device=dev))
+    _launch("dynconv_pack8", dev, *_sp4(x), *_sp4(out.codes), *_sp4(out.scales), *shape, code)
+    return out
+
+
+def dynconv_unpack8(packed: Packed8, dtype=torch.bfloat16, out=None):
+    """The values that a Packed8 stands for, as `dtype` (exact in the type that was packed)."""
+    shape = _norm_shape(packed.codes)
+    _check_packed("packed", packed, packed.codes.shape)
+    _expect("out", out, packed.codes.shape, dtype)
+    dev = _require_device(*packed, out)
+    y = torch.empty(packed.codes.shape, dtype=dtype, device=dev) if out is None else out
+    _launch("dynconv_unpack8", dev, *_sp4(packed.codes), *_sp4(packed.scales), *_sp4(y), *shape, _dtype_code(y))
+    return y
+
+
+# ----------------------------------------------------------------------------------
+# Gated linear scan
+# ----------------------------------------------------------------------------------
+
+SCAN_CHUNK = 128  # tokens between the states that dynconv_scan_fwd keeps for the backward
+
+
+def new_scan_state(B: int, D: int, device) -> torch.Tensor:
+    """A zeroed float32 [B, D] state of the gated linear scan."""
+    return torch.zeros((B, D), dtype=torch.float32, device=device)
+
+
+def _check_rate(rate, D: int):
+    _expect("rate", rate, (D,), torch.float32)
+    if rate is None:
+        raise ValueError("a rate [D] is required")
+    if D > 1 and rate.stride(0) != 1:
+        raise ValueError("rate must be contiguous")
+
+
+def _scan_shape(x, decay, gate, rate, n: int):
+    names = "[B, D]" if n == 2 else "[B, T, D]"
+    if x.dim() != n:
+        raise ValueError(f"x must be {names}; got shape {list(x.shape)}")
+    _dtype_code(x)
+    if decay is None:
+        raise ValueError(f"a decay {names} is required")
+    _expect("decay", decay, x.shape, x.dtype)
+    _expect("gate", gate, x.shape, x.dtype)
+    _check_rate(rate, x.shape[-1])
+    return x.shape
+
+
+def _chunks_shape(B: int, T: int, D: int):
+    return (B, -(-T // SCAN_CHUNK), D)
+
+
+def dynconv_scan_fwd(x, decay, rate, gate=None, seq_idx=None, state=None, want_state: bool = False,
+                     want_chunks: bool = False, out=None, state_out=None):
+    """y = h [B,T,D] of the gated linear scan of x [B,T,D]:
+
+        a_t = exp(-rate sigmoid(decay_t)),  h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(gate_t) x_t
+
+    with decay and gate (optional) of x's shape and a float32 rate [D] >= 0. With seq_idx (int32
+    [B,T]) the state restarts from zero at every document start. state: the float32 [B,D] state before
+    token 0 (default zero). Returns y; with want_state, or a state_out to write (which may be state
+    itself), (y, state after token T-1); want_chunks adds, last, the float32 states before every 128th
+    token that dynconv_scan_bwd would else recompute."""
+    B, T, D = _scan_shape(x, decay, gate, rate, 3)
+    _expect("state", state, (B, D), torch.float32)
+    _expect("state_out", state_out, (B, D), torch.float32)
+    _expect("out", out, (B, T, D), x.dtype)
+    dev = _require_device(x, decay, gate, rate, seq_idx, state, out, state_out)
+    seg = _seg_args(seq_idx, B, T) if seq_idx is not None else (None, None)
+    y = torch.empty((B, T, D), dtype=x.dtype, device=dev) if out is None else out
+    if want_state and state_out is None:
+        state_out = torch.empty((B, D), dtype=torch.float32, device=dev)
+    chunks = torch.empty(_chunks_shape(B, T, D), dtype=torch.float32, device=dev) if want_chunks else None
+    code = _dtype_code(x)
+    ws_bytes = int(_lib.load().dynconv_scan_fwd_workspace_size(B, T, D, code))
+    work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    _launch("dynconv_scan_fwd", dev, *_sp(x), *_sp(decay), *_sp(gate), _dp(rate), *seg, *_sp(state), *_sp(y),
+            *_sp(state_out), _dp(chunks), B, T, D, code, _dp(work), ws_bytes)
+    if state_out is None and chunks is None:
+        return y
+    return (y,) + ((state_out,) if state_out is not None else ()) + ((chunks,) if chunks is not None else ())
+
+
+def dynconv_scan_bwd(x, decay, rate, dy, gate=None, seq_idx=None, state=None, chunks=None, dstate_out=None,
+                     need_dstate: bool = False):
+    """(dx, ddecay, drate, dgate, dstate) of <dy, y> (+ <dstate_out, final state>) for dynconv_scan_fwd
+    with the same arguments; drate and dstate (the gradient of `state`, None unless need_dstate) are
+    float32, dgate None without a gate. chunks: what the forward returned with want_chunks; without, the states
+    are recomputed. x, decay and gate may all be Packed8: the gradients are then those at the values
+    that the codes stand for (chunks of the unpacked inputs would be others)."""
+    packed = isinstance(x, Packed8)
+    if dy.dim() != 3:
+        raise ValueError(f"dy must be [B, T, D]; got shape {list(dy.shape)}")
+    B, T, D = dy.shape
+    code = _dtype_code(dy)
+    scales = (None, None, None)
+    if packed:
+        if not isinstance(decay, Packed8) or not (gate is None or isinstance(gate, Packed8)):
+            raise ValueError("x, decay and gate are all Packed8 or none is")
+        for name, t in (("x", x), ("decay", decay), ("gate", gate)):
+            if t is not None:
+                _check_packed(name, t, dy.shape)
+        scales = (x.scales, decay.scales, gate.scales if gate is not None else None)
+        x, decay, gate = x.codes, decay.codes, gate.codes if gate is not None else None
+        _check_rate(rate, D)
+    else:
+        if isinstance(decay, Packed8) or isinstance(gate, Packed8):
+            raise ValueError("x, decay and gate are all Packed8 or none is")
+        _scan_shape(x, decay, gate, rate, 3)
+        _expect("dy", dy, x.shape, x.dtype)
+    _expect("state", state, (B, D), torch.float32)
+    _expect("dstate_out", dstate_out, (B, D), torch.float32)
+    _expect("chunks", chunks, _chunks_shape(B, T, D), torch.float32)
+    if chunks is not None and not chunks.is_contiguous():
+        raise ValueError("chunks must be contiguous")
+    dev = _require_device(x, decay, gate, *scales, rate, dy, seq_idx, state, chunks, dstate_out)
+    seg = _seg_args(seq_idx, B, T) if seq_idx is not None else (None, None)
+
+    def new():
+        return torch.empty((B, T, D), dtype=dy.dtype, device=dev)
+
+    dx, da, dgate = new(), new(), new() if gate is not None else None
+    drate = torch.empty((D,), dtype=torch.float32, device=dev)
+    dstate = torch.empty((B, D), dtype=torch.float32, device=dev) if need_dstate else None
+    ws_bytes = int(_lib.load().dynconv_scan_bwd_workspace_size(B, T, D, int(chunks is not None), code))
+    work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    _launch("dynconv_scan_bwd", dev, *_sp(x), *_sp(decay), *_sp(gate), *(a for t in scales for a in _sp(t)), _dp(rate),
+            *seg, *_sp(state), _dp(chunks), *_sp(dy), *_sp(dstate_out), *_sp(dx), *_sp(da), _dp(drate), *_sp(dgate),
+            *_sp(dstate), B, T, D, code, _dp(work), ws_bytes)
+    return dx, da, drate, dgate, dstate
+
+
+def dynconv_scan_step(x, decay, rate, state, gate=None, out=None):
+    """y [B,D] of one token of every sequence (x, decay, gate [B,D], float32 rate [D]); state (float32
+    [B,D]) is updated in place."""
+    B, D = _scan_shape(x, decay, gate, rate, 2)
+    if state is None:
+        raise ValueError("a state [B, D] is required")
+    _expect("state", state, (B, D), torch.float32)
+    _expect("out", out, (B, D), x.dtype)
+    dev = _require_device(x, decay, gate, rate, state, out)
+    y = torch.empty((B, D), dtype=x.dtype, device=dev) if out is None else out
+    _launch("dynconv_scan_step", dev, *_sp(x), *_sp(decay), *_sp(gate), _dp(rate), *_sp(state), *_sp(y), B, D,
+            _dtype_code(x))
+    return y

@@ -483,6 +483,91 @@ dynconv_status dynconv_norm_bwd(const void* x, const int64_t* xs, const void* we
 
 size_t dynconv_norm_bwd_workspace_size(int64_t n0, int64_t n1, int64_t n2, int64_t D, dynconv_dtype dtype);
 
+/*
+ * Gated linear scan: the recurrence per channel that a linear-recurrent layer puts behind its
+ * convolution. With s_t = sigmoid(decay_t):
+ *   a_t = exp(-rate s_t),  h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(gate_t) x_t,  y_t = h_t.
+ *   x, decay, gate, y  [B,T,D] of `dtype`, strides s[0..2] (elements, >= 0, s[2] == 1); gate may be
+ *             NULL (a factor of 1)
+ *   rate      float32 [D], contiguous, >= 0 (a negative one gives NaN)
+ *   seq_idx   int32 [B,T] (strides ss[0..1]) or NULL: the state restarts from zero at a token whose id
+ *             differs from the one's before it; the initial state belongs to a row's first document,
+ *             the final state to its last
+ *   state_in  float32 [B,D] (strides [0..1], last 1) or NULL (zero)
+ *   state_out the same, overwritten with the state after token T-1, or NULL; may be state_in itself
+ *             (same strides). T == 0 copies the state.
+ *   chunks    float32 [B, ceil(T/128), D], contiguous, overwritten with the state before every 128th
+ *             token (0, 128, ...), for the backward; or NULL
+ * The states are float32 whatever the `dtype`. A NaN or infinity stays in its channel and document.
+ * Limits (DYNCONV_ERR_UNSUPPORTED otherwise): D <= 2^24, B ceil(D/64) < 2^22; token strides below 2^22
+ * elements (with T == 1 they are not used). Element alignment; two channels at a time where D and
+ * all strides are even and the pointers aligned to two elements.
+ * Few channels and long sequences need dynconv_scan_fwd_workspace_size(...) bytes of workspace
+ * (aligned to 8; 0 for most calls). Run-to-run deterministic.
+ */
+dynconv_status dynconv_scan_fwd(const void* x, const int64_t* xs, const void* decay, const int64_t* as, const void* gate,
+                                const int64_t* gs, const float* rate, const int32_t* seq_idx, const int64_t* ss,
+                                const float* state_in, const int64_t* sis, void* y, const int64_t* ys, float* state_out,
+                                const int64_t* sos, float* chunks, int64_t B, int64_t T, int64_t D, dynconv_dtype dtype,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+size_t dynconv_scan_fwd_workspace_size(int64_t B, int64_t T, int64_t D, dynconv_dtype dtype);
+
+/*
+ * Backward of dynconv_scan_fwd given dy [B,T,D] and, optionally, the gradient of the final state
+ * (dstate_out float32 [B,D], or NULL):
+ *   x, decay, gate  the forward's; or, with scales, int8 codes of them as dynconv_pack8 writes them
+ *              (x_scales, decay_scales and, with a gate, gate_scales: uint8 [B,T,ceil(D/64)], strides
+ *              [0..2], last 1; all or none): the gradients are then those at the values the codes stand for
+ *   chunks     what the forward wrote, or NULL: the states are then recomputed from the inputs (one
+ *              more reading of x, decay and gate; state_in is only used here)
+ *   dx, ddecay, dgate  [B,T,D] of `dtype`; dgate is required with a gate
+ *   drate      float32 [D], overwritten (sums in 64 bits in a fixed order)
+ *   dstate_in  float32 [B,D], the gradient of the initial state, or NULL to skip
+ * Where sqrt(1 - a^2) is 0 in float32 (rate or s of 0) its derivative is taken as 0. Without tokens
+ * drate is zero and dstate_in a copy of dstate_out. Needs dynconv_scan_bwd_workspace_size(...) bytes
+ * (aligned to 8; with_chunks: whether chunks are given).
+ */
+dynconv_status dynconv_scan_bwd(const void* x, const int64_t* xs, const void* decay, const int64_t* as, const void* gate,
+                                const int64_t* gs, const uint8_t* x_scales, const int64_t* xcs,
+                                const uint8_t* decay_scales, const int64_t* acs, const uint8_t* gate_scales,
+                                const int64_t* gcs, const float* rate, const int32_t* seq_idx, const int64_t* ss,
+                                const float* state_in, const int64_t* sis, const float* chunks, const void* dy,
+                                const int64_t* dys, const float* dstate_out, const int64_t* dsos, void* dx,
+                                const int64_t* dxs, void* ddecay, const int64_t* das, float* drate, void* dgate,
+                                const int64_t* dgs, float* dstate_in, const int64_t* dsis, int64_t B, int64_t T,
+                                int64_t D, dynconv_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+size_t dynconv_scan_bwd_workspace_size(int64_t B, int64_t T, int64_t D, int32_t with_chunks, dynconv_dtype dtype);
+
+/*
+ * One decoding step of the gated linear scan: one token of every sequence, the state updated in
+ * place. x, decay, gate, y [B,D] of `dtype`, strides s[0..1] (s[1] == 1); state float32 [B,D].
+ */
+dynconv_status dynconv_scan_step(const void* x, const int64_t* xs, const void* decay, const int64_t* as,
+                                 const void* gate, const int64_t* gs, const float* rate, float* state,
+                                 const int64_t* sts, void* y, const int64_t* ys, int64_t B, int64_t D,
+                                 dynconv_dtype dtype, void* stream);
+
+/*
+ * Activations in 8 bits: what a training step keeps for its backward pass. Every 64 channels of a row
+ * share a step, the power of two 2^(floor(log2 max|x|) - 6) (at least 2^-126); a value is an integer code
+ * of -127 to 127 (nearest, ties to even) times the step. Off by at most 2^-7 of the group's largest
+ * value; a group with a NaN or infinity reads back as NaN, whole.
+ *   x       [n0,n1,n2,D] of `dtype`, strides s[0..3] (s[3] == 1)
+ *   codes   int8 of the same shape, strides cs[0..3] (cs[3] == 1)
+ *   scales  uint8 [n0,n1,n2,ceil(D/64)], strides ss[0..3] (ss[3] == 1): the step's float32 exponent field
+ * dynconv_unpack8 writes code times step, which `dtype` holds exactly when it is the type that was
+ * packed (or float32). Backward calls that take scales read the codes themselves.
+ */
+dynconv_status dynconv_pack8(const void* x, const int64_t* xs, int8_t* codes, const int64_t* cs, uint8_t* scales,
+                             const int64_t* ss, int64_t n0, int64_t n1, int64_t n2, int64_t D, dynconv_dtype dtype,
+                             void* stream);
+
+dynconv_status dynconv_unpack8(const int8_t* codes, const int64_t* cs, const uint8_t* scales, const int64_t* ss, void* y,
+                               const int64_t* ys, int64_t n0, int64_t n1, int64_t n2, int64_t D, dynconv_dtype dtype,
+                               void* stream);
+
 #ifdef __cplusplus
 }
 #endif
