@@ -64,8 +64,8 @@ EXPORTS = (
     "dynconv_scan_bwd",
     "dynconv_scan_bwd_workspace_size",
     "dynconv_scan_step",
-    "dynconv_pack8",
-    "dynconv_unpack8",
+    "dynconv_pack",
+    "dynconv_unpack",
 )
 
 # Bytes of the per-GPU scratch array of dynconv_bwd_ex_noalloc (DYNCONV_NOALLOC_SCRATCH_BYTES).
@@ -183,8 +183,8 @@ _SIGNATURES["dynconv_scan_bwd"] = (  # + scales; rate; seq_idx, state_in; chunks
 _SIGNATURES["dynconv_scan_bwd_workspace_size"] = ([_i64] * 3 + [_i32, ctypes.c_int], _sz)
 _SIGNATURES["dynconv_scan_step"] = (
     [_vp, _i64p] * 3 + [_vp] + [_vp, _i64p] * 2 + [_i64] * 2 + [ctypes.c_int, _vp], ctypes.c_int)
-_SIGNATURES["dynconv_pack8"] = ([_vp, _i64p] * 3 + [_i64] * 4 + [ctypes.c_int, _vp], ctypes.c_int)
-_SIGNATURES["dynconv_unpack8"] = _SIGNATURES["dynconv_pack8"]
+_SIGNATURES["dynconv_pack"] = ([_vp, _i64p] * 3 + [_i64] * 4 + [ctypes.c_int, _vp], ctypes.c_int)
+_SIGNATURES["dynconv_unpack"] = _SIGNATURES["dynconv_pack"]
 
 _lib = None
 

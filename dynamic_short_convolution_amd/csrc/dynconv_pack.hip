@@ -244,13 +244,13 @@ dynconv_status run(const void* x, const int64_t* xs, const int8_t* codes, const 
 
 extern "C" {
 
-dynconv_status dynconv_pack8(const void* x, const int64_t* xs, int8_t* codes, const int64_t* cs, uint8_t* scales,
+dynconv_status dynconv_pack(const void* x, const int64_t* xs, int8_t* codes, const int64_t* cs, uint8_t* scales,
                              const int64_t* ss, int64_t n0, int64_t n1, int64_t n2, int64_t D, dynconv_dtype dtype,
                              void* stream) {
   return dynconv::run(x, xs, codes, cs, scales, ss, n0, n1, n2, D, dtype, false, stream);
 }
 
-dynconv_status dynconv_unpack8(const int8_t* codes, const int64_t* cs, const uint8_t* scales, const int64_t* ss, void* y,
+dynconv_status dynconv_unpack(const int8_t* codes, const int64_t* cs, const uint8_t* scales, const int64_t* ss, void* y,
                                const int64_t* ys, int64_t n0, int64_t n1, int64_t n2, int64_t D, dynconv_dtype dtype,
                                void* stream) {
   return dynconv::run(y, ys, codes, cs, scales, ss, n0, n1, n2, D, dtype, true, stream);

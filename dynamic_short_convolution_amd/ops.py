@@ -685,7 +685,7 @@ def dynconv_pack8(x, out: Packed8 | None = None) -> Packed8:
     if out is None:
         out = Packed8(torch.empty(x.shape, dtype=torch.int8, device=dev),
                       torch.empty(_scales_shape(x.shape), dtype=torch.uint8, device=dev))
-    _launch("dynconv_pack8", dev, *_sp4(x), *_sp4(out.codes), *_sp4(out.scales), *shape, code)
+    _launch("dynconv_pack", dev, *_sp4(x), *_sp4(out.codes), *_sp4(out.scales), *shape, code)
     return out
 
 
@@ -696,7 +696,7 @@ def dynconv_unpack8(packed: Packed8, dtype=torch.bfloat16, out=None):
     _expect("out", out, packed.codes.shape, dtype)
     dev = _require_device(*packed, out)
     y = torch.empty(packed.codes.shape, dtype=dtype, device=dev) if out is None else out
-    _launch("dynconv_unpack8", dev, *_sp4(packed.codes), *_sp4(packed.scales), *_sp4(y), *shape, _dtype_code(y))
+    _launch("dynconv_unpack", dev, *_sp4(packed.codes), *_sp4(packed.scales), *_sp4(y), *shape, _dtype_code(y))
     return y
 
 

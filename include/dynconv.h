@@ -516,7 +516,7 @@ size_t dynconv_scan_fwd_workspace_size(int64_t B, int64_t T, int64_t D, dynconv_
 /*
  * Backward of dynconv_scan_fwd given dy [B,T,D] and, optionally, the gradient of the final state
  * (dstate_out float32 [B,D], or NULL):
- *   x, decay, gate  the forward's; or, with scales, int8 codes of them as dynconv_pack8 writes them
+ *   x, decay, gate  the forward's; or, with scales, int8 codes of them as dynconv_pack writes them
  *              (x_scales, decay_scales and, with a gate, gate_scales: uint8 [B,T,ceil(D/64)], strides
  *              [0..2], last 1; all or none): the gradients are then those at the values the codes stand for
  *   chunks     what the forward wrote, or NULL: the states are then recomputed from the inputs (one
@@ -557,14 +557,14 @@ dynconv_status dynconv_scan_step(const void* x, const int64_t* xs, const void* d
  *   x       [n0,n1,n2,D] of `dtype`, strides s[0..3] (s[3] == 1)
  *   codes   int8 of the same shape, strides cs[0..3] (cs[3] == 1)
  *   scales  uint8 [n0,n1,n2,ceil(D/64)], strides ss[0..3] (ss[3] == 1): the step's float32 exponent field
- * dynconv_unpack8 writes code times step, which `dtype` holds exactly when it is the type that was
+ * dynconv_unpack writes code times step, which `dtype` holds exactly when it is the type that was
  * packed (or float32). Backward calls that take scales read the codes themselves.
  */
-dynconv_status dynconv_pack8(const void* x, const int64_t* xs, int8_t* codes, const int64_t* cs, uint8_t* scales,
+dynconv_status dynconv_pack(const void* x, const int64_t* xs, int8_t* codes, const int64_t* cs, uint8_t* scales,
                              const int64_t* ss, int64_t n0, int64_t n1, int64_t n2, int64_t D, dynconv_dtype dtype,
                              void* stream);
 
-dynconv_status dynconv_unpack8(const int8_t* codes, const int64_t* cs, const uint8_t* scales, const int64_t* ss, void* y,
+dynconv_status dynconv_unpack(const int8_t* codes, const int64_t* cs, const uint8_t* scales, const int64_t* ss, void* y,
                                const int64_t* ys, int64_t n0, int64_t n1, int64_t n2, int64_t D, dynconv_dtype dtype,
                                void* stream);
 
