@@ -66,6 +66,10 @@ EXPORTS = (
     "dynconv_scan_step",
     "dynconv_pack",
     "dynconv_unpack",
+    "dynconv_groupnorm_fwd",
+    "dynconv_groupnorm_fwd_workspace_size",
+    "dynconv_groupnorm_bwd",
+    "dynconv_groupnorm_bwd_workspace_size",
 )
 
 # Bytes of the per-GPU scratch array of dynconv_bwd_ex_noalloc (DYNCONV_NOALLOC_SCRATCH_BYTES).
@@ -185,6 +189,16 @@ _SIGNATURES["dynconv_scan_step"] = (
     [_vp, _i64p] * 3 + [_vp] + [_vp, _i64p] * 2 + [_i64] * 2 + [ctypes.c_int, _vp], ctypes.c_int)
 _SIGNATURES["dynconv_pack"] = ([_vp, _i64p] * 3 + [_i64] * 4 + [ctypes.c_int, _vp], ctypes.c_int)
 _SIGNATURES["dynconv_unpack"] = _SIGNATURES["dynconv_pack"]
+# group norm: x (and scales), weight, bias, gate, lengths, ..., then sizes, over_sequence, silu, eps
+_group_sizes = [_i64] * 4 + [_i32, _i32]
+_SIGNATURES["dynconv_groupnorm_fwd"] = (
+    [_vp, _i64p, _vp, _vp, _vp, _i64p, _vp, _vp, _i64p, _vp] + _group_sizes + [_f32, ctypes.c_int, _vp, _sz, _vp],
+    ctypes.c_int)
+_SIGNATURES["dynconv_groupnorm_fwd_workspace_size"] = (_group_sizes + [ctypes.c_int], _sz)
+_SIGNATURES["dynconv_groupnorm_bwd"] = (
+    [_vp, _i64p, _vp, _i64p, _vp, _vp, _vp, _i64p, _vp, _vp, _vp, _i64p, _vp, _i64p, _vp, _vp, _vp, _i64p] + _group_sizes
+    + [_f32, ctypes.c_int, _vp, _sz, _vp], ctypes.c_int)
+_SIGNATURES["dynconv_groupnorm_bwd_workspace_size"] = (_group_sizes + [ctypes.c_int], _sz)
 
 _lib = None
 

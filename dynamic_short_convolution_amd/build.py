@@ -43,6 +43,10 @@ SOURCES = [
     "dynconv_scan_bf16.hip",
     "dynconv_scan_f16.hip",
     "dynconv_pack.hip",
+    "dynconv_groupnorm.hip",
+    "dynconv_groupnorm_f32.hip",
+    "dynconv_groupnorm_bf16.hip",
+    "dynconv_groupnorm_f16.hip",
 ]
 
 # -packed-fp32-ops: no v_pk_{add,mul,fma}_f32 are generated from ordinary float code.

@@ -1,0 +1,13 @@
+// The group norm's kernels for bf16 storage.
+#include "dynconv_groupnorm_kernels.hpp"
+
+namespace dynconv {
+
+hipError_t group_tokens_bf16(const GroupParams& p, bool vec, bool packed, bool bwd, hipStream_t s) {
+  return group::tokens<bf16_t>(p, vec, packed, bwd, s);
+}
+hipError_t group_sequences_bf16(const GroupParams& p, bool vec, bool packed, GroupStage stage, hipStream_t s) {
+  return group::sequences<bf16_t>(p, vec, packed, stage, s);
+}
+
+}  // namespace dynconv

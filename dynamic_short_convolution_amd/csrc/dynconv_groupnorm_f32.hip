@@ -1,0 +1,13 @@
+// The group norm's kernels for f32 storage.
+#include "dynconv_groupnorm_kernels.hpp"
+
+namespace dynconv {
+
+hipError_t group_tokens_f32(const GroupParams& p, bool vec, bool packed, bool bwd, hipStream_t s) {
+  return group::tokens<float>(p, vec, packed, bwd, s);
+}
+hipError_t group_sequences_f32(const GroupParams& p, bool vec, bool packed, GroupStage stage, hipStream_t s) {
+  return group::sequences<float>(p, vec, packed, stage, s);
+}
+
+}  // namespace dynconv

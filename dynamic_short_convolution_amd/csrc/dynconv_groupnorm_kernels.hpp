@@ -1,0 +1,759 @@
+// Group norm, channels last, with weight, bias, SiLU and a SiLU gate, gfx950: kernels, compiled once per
+// storage type.
+//
+//   n = (x - mean) / sqrt(var + eps),  z = n w + b,  y = act(z) silu(gate),  act = SiLU or none
+//   dz = dy silu(gate) act'(z),  dn = dz w,  dx = (dn - mean(dn) - n mean(dn n)) / sqrt(var + eps),
+//   dw = sum dz n,  db = sum dz,  dgate = dy act(z) silu'(gate)
+// The means run over the Cg channels of a group, of one token or of all tokens of a sequence.
+#pragma once
+
+#include <type_traits>
+
+#include "dynconv_common.hpp"
+#include "dynconv_groupnorm_internal.hpp"
+
+namespace dynconv {
+
+namespace group {
+
+constexpr int kThreads = 256;
+constexpr int kScaleGroup = 64;
+
+struct i8_t {
+  int8_t bits;
+};
+
+// E consecutive elements (16 bytes of the storage type, or one); codes of 8 bits as integers.
+template <typename ET, int E>
+__device__ __forceinline__ void load(float (&v)[E], const void* base, int64_t off) {
+  const ET* p = static_cast<const ET*>(base) + off;
+  if constexpr (E == 1) {
+    if constexpr (sizeof(ET) == 1) {
+      v[0] = float(*reinterpret_cast<const int8_t*>(p));
+    } else if constexpr (sizeof(ET) == 2) {
+      v[0] = Cvt<ET>::of_bits(*reinterpret_cast<const uint16_t*>(p));
+    } else {
+      v[0] = *p;
+    }
+  } else if constexpr (sizeof(ET) == 1) {
+    uint32_t w[E / 4];
+    if constexpr (E == 8) {
+      const u32x2 q = *reinterpret_cast<const u32x2*>(p);
+      w[0] = q[0], w[1] = q[1];
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = float(int8_t(w[i / 4] >> (8 * (i % 4)) & 0xff));
+  } else {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(ET) == 2) {
+        v[2 * i] = Cvt<ET>::lo(w[i]), v[2 * i + 1] = Cvt<ET>::hi(w[i]);
+      } else {
+        v[i] = __uint_as_float(w[i]);
+      }
+    }
+  }
+}
+template <typename ET, int E>
+__device__ __forceinline__ void store(const float (&v)[E], const void* base, int64_t off) {
+  ET* p = const_cast<ET*>(static_cast<const ET*>(base)) + off;
+  if constexpr (E == 1) {
+    if constexpr (sizeof(ET) == 2) {
+      *reinterpret_cast<uint16_t*>(p) = Cvt<ET>::bits(v[0]);
+    } else {
+      *p = v[0];
+    }
+  } else {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(ET) == 2) {
+        w[i] = Cvt<ET>::pack2(v[2 * i], v[2 * i + 1]);
+      } else {
+        w[i] = __float_as_uint(v[i]);
+      }
+    }
+    *reinterpret_cast<u32x4*>(p) = w;
+  }
+}
+
+// A token's E channels from c (of x: in 8 bits with their scale; E channels share one).
+template <typename IT, int E>
+__device__ __forceinline__ void load_x(float (&v)[E], const GroupTensor& t, int64_t b, int64_t tok, int64_t c) {
+  load<IT, E>(v, t.p, b * t.s0 + tok * t.s1 + c);
+  if constexpr (sizeof(IT) == 1) {
+    const float step = __uint_as_float(uint32_t(t.sc[b * t.c0 + tok * t.c1 + c / kScaleGroup]) << 23);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] *= step;
+  }
+}
+
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
+}
+
+// y of one element.
+__device__ __forceinline__ float value(float n, float w, float b, bool silu, bool gated, float g) {
+  float z = __builtin_fmaf(n, w, b);
+  if (silu) z *= sigmoid(z);
+  if (gated) z *= g * sigmoid(g);
+  return z;
+}
+// dz of one element, and the gate's gradient.
+__device__ __forceinline__ float slope(float n, float w, float b, bool silu, bool gated, float g, float dy, float& dgate) {
+  const float z = __builtin_fmaf(n, w, b);
+  float act = z, d = 1.f;
+  if (silu) {
+    const float s = sigmoid(z);
+    act = z * s;
+    d = s * (1.f + z * (1.f - s));
+  }
+  if (gated) {
+    const float s = sigmoid(g);
+    dgate = dy * act * (s * (1.f + g * (1.f - s)));
+    dy *= g * s;
+  }
+  return dy * d;
+}
+
+// Sum over the LPR lanes of a row, in every one of them. `red`: 4 floats per call site.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x, float* red) {
+#pragma unroll
+  for (int m = 1; m < (LPR < 64 ? LPR : 64); m <<= 1) x += __shfl_xor(x, m);
+  if constexpr (LPR == 256) {
+    __syncthreads();  // the previous sum is read
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = (red[0] + red[1]) + (red[2] + red[3]);
+  }
+  return x;
+}
+template <int LPR>
+__device__ __forceinline__ double row_sum(double x, double* red) {
+#pragma unroll
+  for (int m = 1; m < (LPR < 64 ? LPR : 64); m <<= 1) x += __shfl_xor(x, m);
+  if constexpr (LPR == 256) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = (red[0] + red[1]) + (red[2] + red[3]);
+  }
+  return x;
+}
+
+// ---------------------------------------------------------------------------------
+// Per token. A row (one group of one token) belongs to the fewest lanes that hold it in one 16-byte
+// load each, up to a wave, then 2 or 4 loads, then a workgroup: each input is read once, the mean
+// and the squares around it are two sums over registers. Longer rows are read again.
+// ---------------------------------------------------------------------------------
+template <typename ET, int E, int LPR, int NV>
+__global__ __launch_bounds__(kThreads) void k_group_fwd(const GroupParams p) {
+  __shared__ float red[2][4];
+  __shared__ double dred[2][4];
+  const int lane = threadIdx.x % LPR;
+  const int64_t row = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR;
+  const int64_t rows = int64_t(p.B) * p.T * p.G;
+  if (row >= rows) return;  // whole rows; with 256 lanes a whole workgroup
+  const int64_t token = row / p.G, b = token / p.T, t = token - b * p.T;
+  const int c0 = int(row - token * p.G) * p.Cg;
+  const bool gated = p.gate.p != nullptr, silu = p.silu != 0;
+  const float inv = 1.f / float(p.Cg);
+  const int64_t ox = b * p.x.s0 + t * p.x.s1 + c0, og = b * p.gate.s0 + t * p.gate.s1 + c0;
+  const int64_t oy = b * p.y.s0 + t * p.y.s1 + c0;
+  auto finish = [&](const float (&x)[E], const float (&g)[E], const float (&w)[E], const float (&bi)[E], float mean,
+                    float rstd, int c) {
+    float y[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = value((x[e] - mean) * rstd, w[e], bi[e], silu, gated, g[e]);
+    store<ET>(y, p.y.p, oy + c);
+  };
+  if constexpr (NV > 0) {
+    float x[NV][E], g[NV][E], w[NV][E], bi[NV][E];
+    int cc[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {  // lanes past the row read its start and drop it
+      const int c = (lane + i * LPR) * E;
+      cc[i] = c < p.Cg ? c : 0;
+      load<ET>(x[i], p.x.p, ox + cc[i]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) w[i][e] = 1.f, bi[i][e] = 0.f;
+    }
+    if (gated) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) load<ET>(g[i], p.gate.p, og + cc[i]);
+    }
+    if (p.weight != nullptr) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) load<ET>(w[i], p.weight, c0 + cc[i]);
+    }
+    if (p.bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) load<ET>(bi[i], p.bias, c0 + cc[i]);
+    }
+    float sum = 0.f, sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((lane + i * LPR) * E < p.Cg) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum += x[i][e];
+      }
+    const float mean = row_sum<LPR>(sum, red[0]) * inv;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((lane + i * LPR) * E < p.Cg) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sq += (x[i][e] - mean) * (x[i][e] - mean);
+      }
+    const float rstd = 1.f / sqrtf(row_sum<LPR>(sq, red[1]) * inv + p.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((lane + i * LPR) * E < p.Cg) finish(x[i], g[i], w[i], bi[i], mean, rstd, cc[i]);
+  } else {
+    double sum = 0.0, sq = 0.0;  // 64 bits: of any number of channels, and no difference of two of them loses the variance
+    for (int c = lane * E; c < p.Cg; c += LPR * E) {
+      float x[E];
+      load<ET>(x, p.x.p, ox + c);
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum += double(x[e]), sq += double(x[e]) * double(x[e]);
+    }
+    const double mean = row_sum<LPR>(sum, dred[0]) / p.Cg;
+    const double var = row_sum<LPR>(sq, dred[1]) / p.Cg - mean * mean;
+    const float rstd = 1.f / sqrtf((var < 0.0 ? 0.f : float(var)) + p.eps);
+    for (int c = lane * E; c < p.Cg; c += LPR * E) {
+      float x[E], g[E], w[E], bi[E];
+      load<ET>(x, p.x.p, ox + c);
+      if (gated) load<ET>(g, p.gate.p, og + c);
+#pragma unroll
+      for (int e = 0; e < E; ++e) w[e] = 1.f, bi[e] = 0.f;
+      if (p.weight != nullptr) load<ET>(w, p.weight, c0 + c);
+      if (p.bias != nullptr) load<ET>(bi, p.bias, c0 + c);
+      finish(x, g, w, bi, float(mean), rstd, c);
+    }
+  }
+}
+
+// A workgroup takes gpw neighbouring groups of tpw tokens at a time, a lane the same channels
+// every time, so the sums of the weight's and the bias's gradient stay in its registers; they leave
+// as one partial row per workgroup.
+template <typename ET, int E, int LPR, int NV, bool PACKED>
+__global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
+  using IT = std::conditional_t<PACKED, i8_t, ET>;
+  constexpr int NA = NV > 0 ? NV : 1;
+  __shared__ float red[4][4];
+  __shared__ double dred[4][4];
+  extern __shared__ float fold[];  // NV > 0: [tpw][gpw Cg]
+  const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+  const int tsub = slot / p.gpw, gsub = slot - tsub * p.gpw;
+  const int gi = blockIdx.y * p.gpw + gsub;
+  const bool mine = tsub < p.tpw && gi < p.G;
+  const int c0 = (mine ? gi : 0) * p.Cg;
+  const bool gated = p.gate.p != nullptr, silu = p.silu != 0;
+  const float inv = 1.f / float(p.Cg);
+  const int64_t tokens = int64_t(p.B) * p.T;
+  float dw[NA][E], db[NA][E], w[NA][E], bi[NA][E];
+  int cc[NA];
+#pragma unroll
+  for (int i = 0; i < NA; ++i) {
+    const int c = (lane + i * LPR) * E;
+    cc[i] = c < p.Cg ? c : 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) dw[i][e] = 0.f, db[i][e] = 0.f, w[i][e] = 1.f, bi[i][e] = 0.f;
+    if constexpr (NV > 0) {
+      if (p.weight != nullptr) load<ET>(w[i], p.weight, c0 + cc[i]);
+      if (p.bias != nullptr) load<ET>(bi[i], p.bias, c0 + cc[i]);
+    }
+  }
+  bool first = true;
+  for (int64_t tok0 = int64_t(blockIdx.x) * p.tpw; tok0 < tokens; tok0 += int64_t(gridDim.x) * p.tpw) {
+    const bool have = mine && tok0 + tsub < tokens;
+    const int64_t token = have ? tok0 + tsub : tokens - 1;
+    const int64_t b = token / p.T, t = token - b * p.T;
+    const int64_t og = b * p.gate.s0 + t * p.gate.s1 + c0, ody = b * p.dy.s0 + t * p.dy.s1 + c0;
+    const int64_t odx = b * p.dx.s0 + t * p.dx.s1 + c0, odg = b * p.dgate.s0 + t * p.dgate.s1 + c0;
+    if constexpr (NV > 0) {
+      float x[NV][E], dy[NV][E], g[NV][E];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        load_x<IT, E>(x[i], p.x, b, t, c0 + cc[i]);
+        load<ET>(dy[i], p.dy.p, ody + cc[i]);
+      }
+      if (gated) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) load<ET>(g[i], p.gate.p, og + cc[i]);
+      }
+      float sum = 0.f, sq = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if ((lane + i * LPR) * E < p.Cg) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) sum += x[i][e];
+        }
+      const float mean = row_sum<LPR>(sum, red[0]) * inv;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if ((lane + i * LPR) * E < p.Cg) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) sq += (x[i][e] - mean) * (x[i][e] - mean);
+        }
+      const float rstd = 1.f / sqrtf(row_sum<LPR>(sq, red[1]) * inv + p.eps);
+      float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if ((lane + i * LPR) * E < p.Cg) {
+          float dz[E], dg[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            x[i][e] = (x[i][e] - mean) * rstd;
+            dg[e] = 0.f;
+            dz[e] = slope(x[i][e], w[i][e], bi[i][e], silu, gated, g[i][e], dy[i][e], dg[e]);
+            dy[i][e] = dz[e] * w[i][e];
+            s1 += dy[i][e];
+            s2 += dy[i][e] * x[i][e];
+          }
+          if (have) {
+            if (gated) store<ET>(dg, p.dgate.p, odg + cc[i]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) dw[i][e] += dz[e] * x[i][e], db[i][e] += dz[e];
+          }
+        }
+      s1 = row_sum<LPR>(s1, red[2]) * inv;
+      s2 = row_sum<LPR>(s2, red[3]) * inv;
+      if (have) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if ((lane + i * LPR) * E < p.Cg) {
+            float dx[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) dx[e] = rstd * (dy[i][e] - s1 - x[i][e] * s2);
+            store<ET>(dx, p.dx.p, odx + cc[i]);
+          }
+      }
+    } else {
+      double sum = 0.0, sq = 0.0;
+      for (int c = lane * E; c < p.Cg; c += LPR * E) {
+        float x[E];
+        load_x<IT, E>(x, p.x, b, t, c0 + c);
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum += double(x[e]), sq += double(x[e]) * double(x[e]);
+      }
+      const double dmean = row_sum<LPR>(sum, dred[0]) / p.Cg;
+      const double var = row_sum<LPR>(sq, dred[1]) / p.Cg - dmean * dmean;
+      const float mean = float(dmean), rstd = 1.f / sqrtf((var < 0.0 ? 0.f : float(var)) + p.eps);
+      auto point = [&](int c, float (&n)[E], float (&dn)[E], float (&dz)[E], float (&dg)[E]) {
+        float wv[E], bv[E], g[E];
+        load_x<IT, E>(n, p.x, b, t, c0 + c);
+        load<ET>(dn, p.dy.p, ody + c);
+        if (gated) load<ET>(g, p.gate.p, og + c);
+#pragma unroll
+        for (int e = 0; e < E; ++e) wv[e] = 1.f, bv[e] = 0.f;
+        if (p.weight != nullptr) load<ET>(wv, p.weight, c0 + c);
+        if (p.bias != nullptr) load<ET>(bv, p.bias, c0 + c);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          n[e] = (n[e] - mean) * rstd;
+          dg[e] = 0.f;
+          dz[e] = slope(n[e], wv[e], bv[e], silu, gated, g[e], dn[e], dg[e]);
+          dn[e] = dz[e] * wv[e];
+        }
+      };
+      double s1 = 0.0, s2 = 0.0;
+      for (int c = lane * E; c < p.Cg; c += LPR * E) {
+        float n[E], dn[E], dz[E], dg[E];
+        point(c, n, dn, dz, dg);
+#pragma unroll
+        for (int e = 0; e < E; ++e) s1 += double(dn[e]), s2 += double(dn[e]) * double(n[e]);
+      }
+      const float m1 = float(row_sum<LPR>(s1, dred[2]) / p.Cg), m2 = float(row_sum<LPR>(s2, dred[3]) / p.Cg);
+      // the partial sums of a lane's columns stay in the workgroup's own rows of memory
+      float* part = p.colpart != nullptr ? p.colpart + int64_t(blockIdx.x) * 2 * p.C + c0 : nullptr;
+      for (int c = lane * E; c < p.Cg && have; c += LPR * E) {
+        float n[E], dn[E], dz[E], dg[E], dx[E];
+        point(c, n, dn, dz, dg);
+#pragma unroll
+        for (int e = 0; e < E; ++e) dx[e] = rstd * (dn[e] - m1 - n[e] * m2);
+        store<ET>(dx, p.dx.p, odx + c);
+        if (gated) store<ET>(dg, p.dgate.p, odg + c);
+        if (part != nullptr) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            part[c + e] = first ? dz[e] * n[e] : part[c + e] + dz[e] * n[e];
+            part[p.C + c + e] = first ? dz[e] : part[p.C + c + e] + dz[e];
+          }
+        }
+      }
+    }
+    first = false;
+  }
+  if constexpr (NV > 0) {
+    if (p.colpart == nullptr) return;
+    float* part = p.colpart + int64_t(blockIdx.x) * 2 * p.C;
+    if (p.tpw == 1) {
+      if (!mine) return;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if ((lane + i * LPR) * E < p.Cg) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            part[c0 + cc[i] + e] = dw[i][e];
+            part[p.C + c0 + cc[i] + e] = db[i][e];
+          }
+        }
+      return;
+    }
+    const int width = p.gpw * p.Cg;
+    for (int which = 0; which < 2; ++which) {
+      __syncthreads();
+      if (mine) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if ((lane + i * LPR) * E < p.Cg) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) fold[tsub * width + gsub * p.Cg + cc[i] + e] = which ? db[i][e] : dw[i][e];
+          }
+      }
+      __syncthreads();
+      for (int c = threadIdx.x; c < width; c += kThreads) {
+        if (int(blockIdx.y) * width + c >= p.C) break;
+        float s = 0.f;
+        for (int q = 0; q < p.tpw; ++q) s += fold[q * width + c];
+        part[which * p.C + blockIdx.y * width + c] = s;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// Over the tokens of a sequence. A workgroup owns gpb whole groups (or part of the columns of a
+// wide one at a time) of a run of tokens; a lane keeps its channels and goes along the tokens, tps
+// of them side by side. x is read twice: once for the sums, once for the result.
+// ---------------------------------------------------------------------------------
+struct Place {
+  int b, g0, t0, t1, n, tsub, l, z;  // t0..t1: its tokens, of n that exist; l: lane of the token
+  bool on;
+};
+__device__ __forceinline__ Place place(const GroupParams& p) {
+  Place q;
+  q.z = blockIdx.y;
+  q.b = int(blockIdx.x) / p.nChunk;
+  const int k = int(blockIdx.x) - q.b * p.nChunk;
+  q.g0 = q.z * p.gpb;
+  q.n = p.lengths != nullptr ? min(max(p.lengths[q.b], 0), p.T) : p.T;
+  q.t0 = k * p.chunk;
+  q.t1 = min(p.T, q.t0 + p.chunk);
+  q.tsub = threadIdx.x / p.lpt;
+  q.l = threadIdx.x - q.tsub * p.lpt;
+  q.on = q.tsub < p.tps;
+  return q;
+}
+constexpr int kAhead = 4;  // tokens whose loads a lane has under way
+
+// Sums over the lanes of each of a workgroup's groups: v[i] of thread (tsub, l), channels from l E.
+// The result of group g is in out[g][i] for every thread after the call.
+template <int N, int E>
+__device__ __forceinline__ void group_sums(const GroupParams& p, const Place& q, const double (&v)[N], double* red,
+                                           double* out) {
+  const int lanes = p.gpb > 1 ? p.Cg / E : p.lpt;  // lanes of a group and token
+  int per = 1;  // threads that add up one group
+  while (per * 2 * p.gpb <= kThreads) per *= 2;
+  const int g = threadIdx.x / per, j = threadIdx.x - g * per;
+  for (int i = 0; i < N; ++i) {
+    __syncthreads();
+    red[threadIdx.x] = q.on ? v[i] : 0.0;
+    __syncthreads();
+    double s = 0.0;
+    if (g < p.gpb)
+      for (int e = j; e < lanes * p.tps; e += per) s += red[(e / lanes) * p.lpt + g * lanes + e % lanes];
+    for (int h = per / 2; h > 0; h /= 2) {
+      __syncthreads();
+      red[threadIdx.x] = s;
+      __syncthreads();
+      if (j < h) s += red[threadIdx.x + h];
+    }
+    if (g < p.gpb && j == 0) out[g * N + i] = s;
+  }
+  __syncthreads();
+}
+
+template <typename ET, int E, bool PACKED>
+__global__ __launch_bounds__(kThreads) void k_group_stats(const GroupParams p) {
+  using IT = std::conditional_t<PACKED, i8_t, ET>;
+  __shared__ double red[kThreads], out[kThreads * 2];
+  const Place q = place(p);
+  const int c0 = q.g0 * p.Cg, cEnd = min(p.C, c0 + p.gpb * p.Cg), end = min(q.t1, q.n);
+  double v[2] = {0.0, 0.0};  // 64 bits: the squares' sum is good for the variance of any offset that float32 holds
+  for (int c = c0 + q.l * E; q.on && c < cEnd; c += p.lpt * E) {
+    for (int t = q.t0 + q.tsub; t < end; t += kAhead * p.tps) {
+      float x[kAhead][E];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) load_x<IT, E>(x[u], p.x, q.b, min(t + u * p.tps, end - 1), c);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (t + u * p.tps < end) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[0] += double(x[u][e]), v[1] += double(x[u][e]) * double(x[u][e]);
+        }
+    }
+  }
+  group_sums<2, E>(p, q, v, red, out);
+  double* part = p.part + int64_t(blockIdx.x) * p.G * 2;
+  for (int i = threadIdx.x; i < p.gpb * 2; i += kThreads)
+    if (q.g0 + i / 2 < p.G) part[q.g0 * 2 + i] = out[i];
+}
+
+template <typename ET, int E>
+__global__ __launch_bounds__(kThreads) void k_group_apply(const GroupParams p) {
+  const Place q = place(p);
+  if (!q.on) return;
+  const int c0 = q.g0 * p.Cg, cEnd = min(p.C, c0 + p.gpb * p.Cg);
+  const bool gated = p.gate.p != nullptr, silu = p.silu != 0;
+  for (int c = c0 + q.l * E; c < cEnd; c += p.lpt * E) {
+    float w[E], bi[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) w[e] = 1.f, bi[e] = 0.f;
+    if (p.weight != nullptr) load<ET>(w, p.weight, c);
+    if (p.bias != nullptr) load<ET>(bi, p.bias, c);
+    const float* st = p.stats + (int64_t(q.b) * p.G + c / p.Cg) * 2;
+    const float mean = st[0], rstd = st[1];
+    for (int t = q.t0 + q.tsub; t < q.t1; t += kAhead * p.tps) {
+      float x[kAhead][E], g[kAhead][E];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) load_x<ET, E>(x[u], p.x, q.b, min(t + u * p.tps, q.t1 - 1), c);
+      if (gated) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          load<ET>(g[u], p.gate.p, q.b * p.gate.s0 + min(t + u * p.tps, q.t1 - 1) * p.gate.s1 + c);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int tok = t + u * p.tps;
+        if (tok >= q.t1) break;
+        float y[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          y[e] = tok < q.n ? value((x[u][e] - mean) * rstd, w[e], bi[e], silu, gated, g[u][e]) : 0.f;
+        store<ET>(y, p.y.p, q.b * p.y.s0 + tok * p.y.s1 + c);
+      }
+    }
+  }
+}
+
+// Column sums of dz n and dz over a workgroup's tokens.
+template <typename ET, int E, bool PACKED>
+__global__ __launch_bounds__(kThreads) void k_group_columns(const GroupParams p) {
+  using IT = std::conditional_t<PACKED, i8_t, ET>;
+  __shared__ float fold[kThreads][E + 1];
+  const Place q = place(p);
+  const int c0 = q.g0 * p.Cg, cEnd = min(p.C, c0 + p.gpb * p.Cg), end = min(q.t1, q.n);
+  const bool gated = p.gate.p != nullptr, silu = p.silu != 0;
+  float* part = p.colpart + int64_t(blockIdx.x) * 2 * p.C;
+  for (int cb = c0; cb < cEnd; cb += p.lpt * E) {
+    const int c = cb + q.l * E;
+    const bool on = q.on && c < cEnd;
+    float dw[E], db[E], w[E], bi[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) dw[e] = 0.f, db[e] = 0.f, w[e] = 1.f, bi[e] = 0.f;
+    if (on) {
+      if (p.weight != nullptr) load<ET>(w, p.weight, c);
+      if (p.bias != nullptr) load<ET>(bi, p.bias, c);
+      const float* st = p.stats + (int64_t(q.b) * p.G + c / p.Cg) * 2;
+      const float mean = st[0], rstd = st[1];
+      for (int t = q.t0 + q.tsub; t < end; t += kAhead * p.tps) {
+        float x[kAhead][E], dy[kAhead][E], g[kAhead][E];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int64_t tok = min(t + u * p.tps, end - 1);
+          load_x<IT, E>(x[u], p.x, q.b, tok, c);
+          load<ET>(dy[u], p.dy.p, q.b * p.dy.s0 + tok * p.dy.s1 + c);
+        }
+        if (gated) {
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u)
+            load<ET>(g[u], p.gate.p, q.b * p.gate.s0 + min(t + u * p.tps, end - 1) * p.gate.s1 + c);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (t + u * p.tps < end) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              const float n = (x[u][e] - mean) * rstd;
+              float dg;
+              const float dz = slope(n, w[e], bi[e], silu, gated, g[u][e], dy[u][e], dg);
+              dw[e] += dz * n;
+              db[e] += dz;
+            }
+          }
+      }
+    }
+    for (int which = 0; which < 2; ++which) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < E; ++e) fold[threadIdx.x][e] = which ? db[e] : dw[e];
+      __syncthreads();
+      if (q.tsub == 0 && on) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          float s = 0.f;
+          for (int r = 0; r < p.tps; ++r) s += fold[r * p.lpt + q.l][e];
+          part[which * p.C + c + e] = s;
+        }
+      }
+    }
+  }
+}
+
+// dx (and dgate) of a workgroup's tokens from the sequence's column sums.
+template <typename ET, int E, bool PACKED>
+__global__ __launch_bounds__(kThreads) void k_group_gradient(const GroupParams p) {
+  using IT = std::conditional_t<PACKED, i8_t, ET>;
+  __shared__ double red[kThreads], out[kThreads * 2];
+  const Place q = place(p);
+  const int c0 = q.g0 * p.Cg, cEnd = min(p.C, c0 + p.gpb * p.Cg);
+  const bool gated = p.gate.p != nullptr, silu = p.silu != 0;
+  // mean(dn n) and mean(dn) of each group: the column sums with the weight on them
+  double v[2] = {0.0, 0.0};
+  if (q.on && q.tsub == 0)
+    for (int c = c0 + q.l * E; c < cEnd; c += p.lpt * E) {
+      float w[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) w[e] = 1.f;
+      if (p.weight != nullptr) load<ET>(w, p.weight, c);
+      const float* cs = p.colsum + int64_t(q.b) * 2 * p.C + c;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[0] += double(w[e]) * double(cs[e]), v[1] += double(w[e]) * double(cs[p.C + e]);
+    }
+  group_sums<2, E>(p, q, v, red, out);
+  if (!q.on) return;
+  const double inv = q.n > 0 ? 1.0 / (double(q.n) * p.Cg) : 0.0;
+  for (int c = c0 + q.l * E; c < cEnd; c += p.lpt * E) {
+    float w[E], bi[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) w[e] = 1.f, bi[e] = 0.f;
+    if (p.weight != nullptr) load<ET>(w, p.weight, c);
+    if (p.bias != nullptr) load<ET>(bi, p.bias, c);
+    const int g = c / p.Cg;
+    const float* st = p.stats + (int64_t(q.b) * p.G + g) * 2;
+    const float mean = st[0], rstd = st[1];
+    const float m2 = float(out[(g - q.g0) * 2] * inv), m1 = float(out[(g - q.g0) * 2 + 1] * inv);
+    for (int t = q.t0 + q.tsub; t < q.t1; t += kAhead * p.tps) {
+      float x[kAhead][E], dy[kAhead][E], gt[kAhead][E];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int64_t tok = min(t + u * p.tps, q.t1 - 1);
+        load_x<IT, E>(x[u], p.x, q.b, tok, c);
+        load<ET>(dy[u], p.dy.p, q.b * p.dy.s0 + tok * p.dy.s1 + c);
+      }
+      if (gated) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          load<ET>(gt[u], p.gate.p, q.b * p.gate.s0 + min(t + u * p.tps, q.t1 - 1) * p.gate.s1 + c);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int tok = t + u * p.tps;
+        if (tok >= q.t1) break;
+        const bool real = tok < q.n;
+        float dx[E], dg[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float n = (x[u][e] - mean) * rstd;
+          dg[e] = 0.f;
+          const float dz = slope(n, w[e], bi[e], silu, gated, gt[u][e], dy[u][e], dg[e]);
+          dx[e] = real ? rstd * (dz * w[e] - m1 - n * m2) : 0.f;
+          dg[e] = real ? dg[e] : 0.f;
+        }
+        store<ET>(dx, p.dx.p, q.b * p.dx.s0 + tok * p.dx.s1 + c);
+        if (gated) store<ET>(dg, p.dgate.p, q.b * p.dgate.s0 + tok * p.dgate.s1 + c);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------------
+template <typename ET, int E, int LPR, int NV>
+hipError_t tokens_nv(const GroupParams& p, bool packed, bool bwd, hipStream_t s) {
+  constexpr int rpb = kThreads / LPR;
+  if (!bwd) {
+    constexpr int64_t most = int64_t(1) << 23;  // a dimension of a launch has fewer than 2^32 threads
+    const int64_t blocks = (int64_t(p.B) * p.T * p.G + rpb - 1) / rpb;
+    const dim3 grid(unsigned(blocks < most ? blocks : most), unsigned((blocks + most - 1) / most));
+    hipLaunchKernelGGL((k_group_fwd<ET, E, LPR, NV>), grid, dim3(kThreads), 0, s, p);
+    return hipGetLastError();
+  }
+  int32_t gpw, tpw;
+  const dim3 grid(unsigned(group_token_blocks(int64_t(p.B) * p.T, p.G, p.Cg, E, &gpw, &tpw)),
+                  unsigned((p.G + gpw - 1) / gpw));
+  const size_t lds = NV > 0 && tpw > 1 ? size_t(tpw) * size_t(gpw) * size_t(p.Cg) * sizeof(float) : 0;
+  GroupParams q = p;
+  q.gpw = gpw;
+  q.tpw = tpw;
+  if (packed) {
+    hipLaunchKernelGGL((k_group_bwd<ET, E, LPR, NV, true>), grid, dim3(kThreads), lds, s, q);
+  } else {
+    hipLaunchKernelGGL((k_group_bwd<ET, E, LPR, NV, false>), grid, dim3(kThreads), lds, s, q);
+  }
+  return hipGetLastError();
+}
+
+template <typename ET, int E>
+hipError_t tokens_e(const GroupParams& p, bool packed, bool bwd, hipStream_t s) {
+  const GroupPlan pl = group_plan(p.Cg, E);
+  if constexpr (E > 1) {
+    if (pl.lpr == 4) return tokens_nv<ET, E, 4, 1>(p, packed, bwd, s);
+    if (pl.lpr == 8) return tokens_nv<ET, E, 8, 1>(p, packed, bwd, s);
+    if (pl.lpr == 32) return tokens_nv<ET, E, 32, 1>(p, packed, bwd, s);
+  }
+  if (pl.lpr == 16) return tokens_nv<ET, E, 16, 1>(p, packed, bwd, s);
+  if (pl.lpr == 64) {
+    if (pl.nv == 1) return tokens_nv<ET, E, 64, 1>(p, packed, bwd, s);
+    if (pl.nv == 2) return tokens_nv<ET, E, 64, 2>(p, packed, bwd, s);
+    return tokens_nv<ET, E, 64, 4>(p, packed, bwd, s);
+  }
+  if (pl.nv == 2) return tokens_nv<ET, E, 256, 2>(p, packed, bwd, s);
+  if (pl.nv == 4) return tokens_nv<ET, E, 256, 4>(p, packed, bwd, s);
+  return tokens_nv<ET, E, 256, 0>(p, packed, bwd, s);
+}
+
+template <typename ET>
+hipError_t tokens(const GroupParams& p, bool vec, bool packed, bool bwd, hipStream_t s) {
+  return vec ? tokens_e<ET, 16 / int(sizeof(ET))>(p, packed, bwd, s) : tokens_e<ET, 1>(p, packed, bwd, s);
+}
+
+template <typename ET, int E>
+hipError_t sequences_e(const GroupParams& p, bool packed, GroupStage stage, hipStream_t s) {
+  const dim3 grid(unsigned(p.B) * unsigned(p.nChunk), unsigned((p.G + p.gpb - 1) / p.gpb)), block(kThreads);
+  if (stage == kGroupStats) {
+    if (packed) {
+      hipLaunchKernelGGL((k_group_stats<ET, E, true>), grid, block, 0, s, p);
+    } else {
+      hipLaunchKernelGGL((k_group_stats<ET, E, false>), grid, block, 0, s, p);
+    }
+  } else if (stage == kGroupApply) {
+    hipLaunchKernelGGL((k_group_apply<ET, E>), grid, block, 0, s, p);
+  } else if (stage == kGroupColumns) {
+    if (packed) {
+      hipLaunchKernelGGL((k_group_columns<ET, E, true>), grid, block, 0, s, p);
+    } else {
+      hipLaunchKernelGGL((k_group_columns<ET, E, false>), grid, block, 0, s, p);
+    }
+  } else if (packed) {
+    hipLaunchKernelGGL((k_group_gradient<ET, E, true>), grid, block, 0, s, p);
+  } else {
+    hipLaunchKernelGGL((k_group_gradient<ET, E, false>), grid, block, 0, s, p);
+  }
+  return hipGetLastError();
+}
+
+template <typename ET>
+hipError_t sequences(const GroupParams& p, bool vec, bool packed, GroupStage stage, hipStream_t s) {
+  return vec ? sequences_e<ET, 16 / int(sizeof(ET))>(p, packed, stage, s) : sequences_e<ET, 1>(p, packed, stage, s);
+}
+
+}  // namespace group
+
+}  // namespace dynconv

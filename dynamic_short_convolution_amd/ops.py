@@ -830,3 +830,96 @@ def dynconv_scan_step(x, decay, rate, state, gate=None, out=None):
     _launch("dynconv_scan_step", dev, *_sp(x), *_sp(decay), *_sp(gate), _dp(rate), *_sp(state), *_sp(y), B, D,
             _dtype_code(x))
     return y
+
+
+# ----------------------------------------------------------------------------------
+# Group norm, channels last
+# ----------------------------------------------------------------------------------
+
+
+def _sp3(t):
+    """(pointer, three strides) of a tensor of 2 or 3 dimensions, or two NULLs."""
+    return (t.data_ptr(), _lib.const_strides((0,) * (3 - t.dim()) + t.stride())) if t is not None else (None, None)
+
+
+def _group_args(shape, dtype, groups, weight, bias, gate, activation, over, lengths, stats):
+    """Checks what both directions share; returns ((B, T, C), over sequences, SiLU)."""
+    if over not in ("token", "sequence"):
+        raise ValueError(f"over is 'token' or 'sequence'; got {over!r}")
+    sequence = over == "sequence"
+    if len(shape) != 3 and (sequence or len(shape) != 2):
+        raise ValueError(f"x must be [B, T, C]{'' if sequence else ' or [tokens, C]'}; got shape {list(shape)}")
+    if activation not in (None, "silu"):
+        raise ValueError(f"activation is 'silu' or None; got {activation!r}")
+    B, T, C = (1,) * (3 - len(shape)) + tuple(shape)
+    if groups < 1 or C % groups != 0:
+        raise ValueError(f"groups = {groups} must be a positive divisor of C = {C}")
+    for name, t in (("weight", weight), ("bias", bias)):
+        _expect(name, t, (C,), dtype)
+        if t is not None and C > 1 and t.stride(0) != 1:
+            raise ValueError(f"{name} must be contiguous")
+    _expect("gate", gate, shape, dtype)
+    if not sequence and (lengths is not None or stats is not None):
+        raise ValueError("lengths and stats go with over='sequence'")
+    _expect("lengths", lengths, (B,), torch.int32)
+    _expect("stats", stats, (B, groups, 2), torch.float32)
+    for name, t in (("lengths", lengths), ("stats", stats)):
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    return (B, T, C), int(sequence), int(activation == "silu")
+
+
+def dynconv_groupnorm_fwd(x, groups: int, weight=None, bias=None, gate=None, activation: str | None = None,
+                          over: str = "token", lengths=None, eps: float = 1e-5, want_stats: bool = False, out=None):
+    """y = act(n * weight + bias) * silu(gate) with n = (x - mean) / sqrt(var + eps) over the C / groups
+    neighbouring channels of each group of x [B,T,C] (or [tokens,C]): of each token (over="token"), or of all
+    tokens of a sequence (over="sequence"). weight, bias [C] and gate (x's shape) are optional; act is
+    SiLU with activation="silu", else nothing. Over sequences, lengths (int32 [B], 0 to T) says how many tokens
+    of each count; y is 0 behind them. With want_stats returns (y, stats) for dynconv_groupnorm_bwd: float32
+    [B,groups,2] over sequences, None per token (there the backward has the group in registers)."""
+    code = _dtype_code(x)
+    (B, T, C), seq, silu = _group_args(x.shape, x.dtype, groups, weight, bias, gate, activation, over, lengths, None)
+    _expect("out", out, x.shape, x.dtype)
+    dev = _require_device(x, weight, bias, gate, lengths, out)
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+    # a sequence without tokens, or none at all: nothing is launched that would write them
+    stats = (torch.zeros if B * T * C == 0 else torch.empty)((B, groups, 2), dtype=torch.float32, device=dev) if want_stats and seq else None
+    ws_bytes = int(_lib.load().dynconv_groupnorm_fwd_workspace_size(B, T, C, groups, 1, int(stats is not None), code)) if seq else 0
+    work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    _launch("dynconv_groupnorm_fwd", dev, *_sp3(x), _dp(weight), _dp(bias), *_sp3(gate), _dp(lengths), *_sp3(y), _dp(stats),
+            B, T, C, groups, seq, silu, float(eps), code, _dp(work), ws_bytes)
+    return (y, stats) if want_stats else y
+
+
+def dynconv_groupnorm_bwd(x, groups: int, dy, weight=None, bias=None, gate=None, activation: str | None = None,
+                          over: str = "token", lengths=None, eps: float = 1e-5, stats=None):
+    """(dx, dweight, dbias, dgate) of <dy, y> for dynconv_groupnorm_fwd with the same arguments, None where
+    there is no such input; dweight and dbias are float32 [C]. x may be a Packed8 of what the forward took:
+    the gradients are then those at the values it stands for (pass no stats, which would be the unpacked
+    x's). stats: what the forward returned with want_stats; recomputed without."""
+    code = _dtype_code(dy)
+    scales = None
+    if isinstance(x, Packed8):
+        _check_packed("x", x, dy.shape)
+        x, scales = x
+    else:
+        _expect("x", x, dy.shape, dy.dtype)
+    (B, T, C), seq, silu = _group_args(dy.shape, dy.dtype, groups, weight, bias, gate, activation, over, lengths, stats)
+    dev = _require_device(x, scales, dy, weight, bias, gate, lengths, stats)
+
+    def new():
+        return torch.empty(dy.shape, dtype=dy.dtype, device=dev)
+
+    def column():
+        return torch.empty((C,), dtype=torch.float32, device=dev)
+
+    dx, dgate = new(), new() if gate is not None else None
+    dw, db = column() if weight is not None else None, column() if bias is not None else None
+    ws_bytes = 0
+    if seq or dw is not None or db is not None:
+        ws_bytes = int(_lib.load().dynconv_groupnorm_bwd_workspace_size(B, T, C, groups, seq, int(stats is not None), code))
+    work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    _launch("dynconv_groupnorm_bwd", dev, *_sp3(x), *_sp3(scales), _dp(weight), _dp(bias), *_sp3(gate), _dp(lengths),
+            _dp(stats), *_sp3(dy), *_sp3(dx), _dp(dw), _dp(db), *_sp3(dgate), B, T, C, groups, seq, silu, float(eps), code,
+            _dp(work), ws_bytes)
+    return dx, dw, db, dgate

@@ -568,6 +568,52 @@ dynconv_status dynconv_unpack(const int8_t* codes, const int64_t* cs, const uint
                                const int64_t* ys, int64_t n0, int64_t n1, int64_t n2, int64_t D, dynconv_dtype dtype,
                                void* stream);
 
+/*
+ * Group norm, channels last, with weight, bias, SiLU and a SiLU gate:
+ *   n = (x - mean) / sqrt(var + eps),  y = act(n weight + bias) silu(gate)
+ * The mean and the variance run over the C/groups neighbouring channels of a group: of each token, or
+ * (over_sequence != 0) of all tokens of a sequence. act is SiLU with silu != 0, else nothing.
+ *   x, gate, y    [B,T,C] of `dtype`, strides s[0..2] (elements, >= 0, s[2] == 1); gate may be NULL (1)
+ *   weight, bias  [C] of `dtype`, contiguous, or NULL (ones, zeros)
+ *   lengths       int32 [B], contiguous, or NULL (T); over sequences only: the tokens of a sequence,
+ *                 cut to 0..T. Tokens behind them are not in the statistics, and their y is 0.
+ *   stats         float32 [B,groups,2], overwritten with mean and 1 / sqrt(var + eps) (0, 0 for a
+ *                 sequence without tokens) for the backward, or NULL; over sequences only
+ * Sums over a sequence are held in 64 bits, those over a token's group in 32 (in 64 for groups longer than
+ * the registers take). C up to 2^19, B below 2^23, B T below 2^31. Element alignment; 16 bytes at a time where
+ * C/groups, all strides and pointers allow it. Over sequences needs
+ * dynconv_groupnorm_fwd_workspace_size(...) bytes (aligned to 8), per token none. Run-to-run deterministic.
+ */
+dynconv_status dynconv_groupnorm_fwd(const void* x, const int64_t* xs, const void* weight, const void* bias,
+                                     const void* gate, const int64_t* gs, const int32_t* lengths, void* y,
+                                     const int64_t* ys, float* stats, int64_t B, int64_t T, int64_t C, int64_t groups,
+                                     int32_t over_sequence, int32_t silu, float eps, dynconv_dtype dtype,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+size_t dynconv_groupnorm_fwd_workspace_size(int64_t B, int64_t T, int64_t C, int64_t groups, int32_t over_sequence,
+                                            int32_t with_stats, dynconv_dtype dtype);
+
+/*
+ * Backward of dynconv_groupnorm_fwd given dy:
+ *   x        the forward's, or, with x_scales (uint8 [B,T,ceil(C/64)], strides xcs[0..2], last 1), its int8
+ *            codes as dynconv_pack writes them: the gradients are then those at the values they stand for
+ *   stats    what the forward wrote, or NULL: recomputed from x (over sequences only)
+ *   dx       [B,T,C] of `dtype`; 0 behind a sequence's tokens
+ *   dweight, dbias  float32 [C], overwritten, or NULL to skip (without tokens zero)
+ *   dgate    required with a gate; 0 behind a sequence's tokens
+ * Needs dynconv_groupnorm_bwd_workspace_size(...) bytes (aligned to 8; per token only for dweight or dbias).
+ */
+dynconv_status dynconv_groupnorm_bwd(const void* x, const int64_t* xs, const uint8_t* x_scales, const int64_t* xcs,
+                                     const void* weight, const void* bias, const void* gate, const int64_t* gs,
+                                     const int32_t* lengths, const float* stats, const void* dy, const int64_t* dys,
+                                     void* dx, const int64_t* dxs, float* dweight, float* dbias, void* dgate,
+                                     const int64_t* dgs, int64_t B, int64_t T, int64_t C, int64_t groups,
+                                     int32_t over_sequence, int32_t silu, float eps, dynconv_dtype dtype,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+size_t dynconv_groupnorm_bwd_workspace_size(int64_t B, int64_t T, int64_t C, int64_t groups, int32_t over_sequence,
+                                            int32_t with_stats, dynconv_dtype dtype);
+
 #ifdef __cplusplus
 }
 #endif
