@@ -15,7 +15,7 @@ namespace {
 int elem_bytes(dynconv_dtype dt) { return dt == DYNCONV_F32 ? 4 : 2; }
 bool aligned(const void* p, int64_t a) { return (reinterpret_cast<uintptr_t>(p) % uint64_t(a)) == 0; }
 
-// The kernels address a tile's 256 rows with 32-bit byte offsets.
+// The kernels address a tile's 128 rows with 32-bit byte offsets.
 constexpr int64_t kScanMaxTokenStride = int64_t(1) << 22;
 
 struct Sizes {
@@ -36,11 +36,12 @@ dynconv_status take(ScanTensor* t, const void* p, const int64_t* s, const Sizes&
   if (p == nullptr || s == nullptr) return DYNCONV_ERR_INVALID_ARG;
   if (!aligned(p, eb) || (z.D > 1 && s[2] != 1) || s[0] < 0 || s[1] < 0) return DYNCONV_ERR_UNSUPPORTED;
   if (z.T > 1 && s[1] >= kScanMaxTokenStride) return DYNCONV_ERR_UNSUPPORTED;
-  if (output && ((z.B > 1 && s[0] == 0) || (z.T > 1 && s[1] == 0))) return DYNCONV_ERR_INVALID_ARG;
+  // an output's rows have places of their own (the kernels drop rows that do not exist by their offsets)
+  if (output && ((z.B > 1 && s[0] == 0) || (z.T > 1 && s[1] < z.D))) return DYNCONV_ERR_INVALID_ARG;
   if (!aligned(p, 2 * eb) || (z.B > 1 && s[0] % 2 != 0) || (z.T > 1 && s[1] % 2 != 0)) *vec = 1;
   t->p = p;
   t->s0 = s[0];
-  t->s1 = z.T > 1 ? s[1] : 0;
+  t->s1 = z.T > 1 ? s[1] : z.D;  // of a single token it has no meaning
   return DYNCONV_OK;
 }
 
@@ -81,13 +82,10 @@ bool any_equal(const void* out, std::initializer_list<const void*> others) {
 
 size_t rounded(size_t n) { return (n + 255) / 256 * 256; }
 
-void set_segments(ScanParams* p, const Sizes& z, int tile) {
-  p->segTiles = scan_segment_tiles(z.B, z.D, z.T, tile);
-  p->nSeg = scan_segments(z.T, p->segTiles, tile);
-}
+int32_t segments(const Sizes& z) { return scan_segments(z.T, scan_segment_tiles(z.B, z.D, z.T)); }
 
-size_t maps_bytes(const Sizes& z, int tile) {
-  const int32_t n = scan_segments(z.T, scan_segment_tiles(z.B, z.D, z.T, tile), tile);
+size_t maps_bytes(const Sizes& z) {
+  const int32_t n = segments(z);
   return n > 1 ? rounded(size_t(z.B) * size_t(n) * size_t(z.D) * sizeof(float2)) : 0;
 }
 
@@ -101,11 +99,9 @@ struct BwdSpace {
   size_t total() const { return drate + maps + chunks; }
 };
 BwdSpace bwd_space(const Sizes& z, bool given) {
-  const int32_t n = scan_segments(z.T, scan_segment_tiles(z.B, z.D, z.T, kScanTileBwd), kScanTileBwd);
   BwdSpace w;
-  w.drate = rounded(size_t(z.B) * size_t(n) * size_t(z.D) * sizeof(float));
-  const size_t f = given ? 0 : maps_bytes(z, kScanTile), b = maps_bytes(z, kScanTileBwd);
-  w.maps = f > b ? f : b;
+  w.drate = rounded(size_t(z.B) * size_t(segments(z)) * size_t(z.D) * sizeof(float));
+  w.maps = maps_bytes(z);
   w.chunks = given ? 0 : chunks_bytes(z);
   return w;
 }
@@ -125,7 +121,7 @@ extern "C" {
 size_t dynconv_scan_fwd_workspace_size(int64_t B, int64_t T, int64_t D, dynconv_dtype dtype) {
   const Sizes z{B, T, D};
   if (check_sizes(z, dtype) != DYNCONV_OK || B == 0 || T == 0 || D == 0) return 0;
-  return maps_bytes(z, kScanTile);
+  return maps_bytes(z);
 }
 
 dynconv_status dynconv_scan_fwd(const void* x, const int64_t* xs, const void* decay, const int64_t* as, const void* gate,
@@ -165,8 +161,8 @@ dynconv_status dynconv_scan_fwd(const void* x, const int64_t* xs, const void* de
   p.state_out = state_out, p.sos = state_out != nullptr ? sos[0] : 0;
   p.chunks = chunks;
   p.B = int32_t(B), p.T = int32_t(T), p.D = int32_t(D);
-  set_segments(&p, z, kScanTile);
-  const size_t need = maps_bytes(z, kScanTile);
+  p.segTiles = scan_segment_tiles(B, D, T), p.nSeg = segments(z);
+  const size_t need = maps_bytes(z);
   if (need != 0 && (workspace == nullptr || workspace_bytes < need)) return DYNCONV_ERR_WORKSPACE;
   if (need != 0 && !aligned(workspace, 8)) return DYNCONV_ERR_UNSUPPORTED;
   p.maps = static_cast<float2*>(workspace);
@@ -243,17 +239,16 @@ dynconv_status dynconv_scan_bwd(const void* x, const int64_t* xs, const void* de
   p.drate_part = reinterpret_cast<float*>(at);
   p.maps = reinterpret_cast<float2*>(at + w.drate);
   p.B = int32_t(B), p.T = int32_t(T), p.D = int32_t(D);
+  p.segTiles = scan_segment_tiles(B, D, T), p.nSeg = segments(z);
   hipError_t e;
   if (chunks != nullptr) {
     p.chunks = const_cast<float*>(chunks);
   } else {
     p.chunks = reinterpret_cast<float*>(at + w.drate + w.maps);
-    set_segments(&p, z, kScanTile);
     if ((e = run_fwd(p, dtype, vec, packed, s)) != hipSuccess) return done(e);
   }
   p.dstate_out = dstate_out, p.dsos = dstate_out != nullptr ? dsos[0] : 0;
   p.dstate = dstate_in, p.dsis = dstate_in != nullptr ? dsis[0] : 0;
-  set_segments(&p, z, kScanTileBwd);
   e = dtype == DYNCONV_BF16  ? scan_bwd_bf16(p, vec, packed, s)
       : dtype == DYNCONV_F16 ? scan_bwd_f16(p, vec, packed, s)
                              : scan_bwd_f32(p, vec, packed, s);

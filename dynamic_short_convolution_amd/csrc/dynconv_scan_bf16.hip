@@ -3,7 +3,7 @@
 
 namespace dynconv {
 
-hipError_t scan_fwd_bf16(const ScanParams& p, int vec, bool packed, hipStream_t s) { return scan::fwd<bf16_t>(p, vec, packed, s); }
-hipError_t scan_bwd_bf16(const ScanParams& p, int vec, bool packed, hipStream_t s) { return scan::bwd<bf16_t>(p, vec, packed, s); }
+hipError_t scan_fwd_bf16(const ScanParams& p, int vec, bool packed, hipStream_t s) { return scan::run<bf16_t>(p, vec, packed, false, s); }
+hipError_t scan_bwd_bf16(const ScanParams& p, int vec, bool packed, hipStream_t s) { return scan::run<bf16_t>(p, vec, packed, true, s); }
 
 }  // namespace dynconv

@@ -3,7 +3,7 @@
 
 namespace dynconv {
 
-hipError_t scan_fwd_f32(const ScanParams& p, int vec, bool packed, hipStream_t s) { return scan::fwd<float>(p, vec, packed, s); }
-hipError_t scan_bwd_f32(const ScanParams& p, int vec, bool packed, hipStream_t s) { return scan::bwd<float>(p, vec, packed, s); }
+hipError_t scan_fwd_f32(const ScanParams& p, int vec, bool packed, hipStream_t s) { return scan::run<float>(p, vec, packed, false, s); }
+hipError_t scan_bwd_f32(const ScanParams& p, int vec, bool packed, hipStream_t s) { return scan::run<float>(p, vec, packed, true, s); }
 
 }  // namespace dynconv

@@ -10,12 +10,11 @@
 namespace dynconv {
 
 constexpr int kScanCols = 64;    // channels of a workgroup, and of one scale of an operand in 8 bits
-constexpr int kScanWaves = 16;   // waves of a workgroup, one after the other along the tokens
+constexpr int kScanWaves = 8;    // waves of a workgroup, one after the other along the tokens
+constexpr int kScanElems = 16;   // elements of a tile per lane: 16 tokens of one channel or 8 of two
+constexpr int kScanTile = kScanWaves * kScanElems;  // tokens of a workgroup's tile
 constexpr int kScanChunk = 128;  // tokens between two kept states
-// Tokens of a workgroup's tile: 16 (forward) or 8 (backward) elements per lane, whatever the lane's width.
-constexpr int kScanTile = kScanWaves * 16;
-constexpr int kScanTileBwd = kScanWaves * 8;
-static_assert(kScanTileBwd == kScanChunk && kScanTile % kScanChunk == 0, "kept states start tiles");
+static_assert(kScanTile == kScanChunk, "kept states start tiles");
 
 // Activation [B,T,D] (channels adjacent); sc: the scales of an operand in 8 bits, [B,T,ceil(D/64)].
 struct ScanTensor {
@@ -46,22 +45,22 @@ struct ScanParams {
   // s - 1. Backward: place nSeg - 1 the gradient from behind the last token, place s those of
   // segment s + 1, in reverse.
   float2* maps;
-  int32_t B, T, D, nSeg, segTiles;  // segTiles: tiles of the direction's size per segment
+  int32_t B, T, D, nSeg, segTiles;  // segTiles: tiles per segment
 };
 
 // Tiles per segment. A workgroup walks its tiles one behind the other; with few (sequence, 64
 // channels) pairs the CUs would idle, so the sequence is cut, at the price of a first pass that
 // reads the inputs of the maps once more.
-inline int32_t scan_segment_tiles(int64_t B, int64_t D, int64_t T, int tile) {
-  const int64_t blocks = B * ((D + kScanCols - 1) / kScanCols), tiles = (T + tile - 1) / tile;
+inline int32_t scan_segment_tiles(int64_t B, int64_t D, int64_t T) {
+  const int64_t blocks = B * ((D + kScanCols - 1) / kScanCols), tiles = (T + kScanTile - 1) / kScanTile;
   int64_t want = blocks > 0 ? 256 / blocks : 1;  // one workgroup per CU
   if (want < 2 || tiles < 4) return int32_t(tiles > 0 ? tiles : 1);
   if (want > tiles / 2) want = tiles / 2;
   if (want > 32) want = 32;
   return int32_t((tiles + want - 1) / want);
 }
-inline int32_t scan_segments(int64_t T, int32_t segTiles, int tile) {
-  const int64_t tiles = (T + tile - 1) / tile;
+inline int32_t scan_segments(int64_t T, int32_t segTiles) {
+  const int64_t tiles = (T + kScanTile - 1) / kScanTile;
   return int32_t(tiles > 0 ? (tiles + segTiles - 1) / segTiles : 1);
 }
 

@@ -117,13 +117,15 @@ __device__ __forceinline__ Decay decay_of(float s, float rate) {
   return d;
 }
 
+constexpr uint32_t kNowhere = 0x80000000u;  // an offset behind every buffer's range
+
 // Where a lane stands: its channels, its lane group's run of tokens.
 template <int V>
 struct Lane {
   static constexpr int kLanes = kScanCols / V;  // lanes side by side over the channels
   int wave, group, run, chl;                    // run: index of the lane group's run in the tile
   bool ok;                                      // the channels exist
-  uint32_t ch;                                  // first channel within the block, one that exists
+  int cg;                                       // the first of them, or the tensor's last
   __device__ __forceinline__ Lane(int D, int c0) {
     const int lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -131,59 +133,95 @@ struct Lane {
     run = wave * V + group;
     chl = (lane % kLanes) * V;
     ok = c0 + chl < D;
-    ch = ok ? chl : D - V - c0;
+    cg = ok ? c0 + chl : D - V;
   }
 };
 
-// A run's rows of one operand. Rows behind the last token repeat it.
+// A tile's rows of one tensor through buffer instructions: a uniform descriptor per tile whose range
+// ends with the last row that exists, the lane's place in its first row as vector offset, the row as
+// scalar offset (both count for the range), so rows and channels that do not exist read as zero and
+// are not written, without a branch or an address per row.
+template <typename ET, int V, int L>
+struct Place {
+  uint32_t off, pitch;
+  __device__ __forceinline__ Place(const ScanTensor& t, const Lane<V>& me) {
+    pitch = uint32_t(t.s1) * uint32_t(sizeof(ET));
+    off = me.ok ? uint32_t(me.run * L) * pitch + uint32_t(me.chl) * uint32_t(sizeof(ET)) : kNowhere;
+  }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const ScanTensor& t, int b, int t0, int c0, int last, int D) const {
+    const char* base = static_cast<const char*>(t.p) + (b * t.s0 + t0 * t.s1 + c0) * int64_t(sizeof(ET));
+    const uint32_t range = uint32_t(last) * pitch + uint32_t(min(D - c0, kScanCols)) * uint32_t(sizeof(ET));
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, int(range), 0x00027000);
+  }
+};
+
+// A run's rows of one operand.
 template <typename ET, int V, int L>
 struct Rows {
   typedef Elems<ET, V> E;
   typename E::W w[L];
-  uint8_t sc[sizeof(ET) == 1 ? L : 1];
 
-  // Tile rows start at token t0; `last` is the tile's last row that exists.
-  __device__ __forceinline__ void load(const ScanTensor& t, int b, int t0, int c0, int run, uint32_t ch, int last) {
-    const char* base = static_cast<const char*>(t.p) + (b * t.s0 + t0 * t.s1 + c0) * int64_t(sizeof(ET));
-    const uint32_t pitch = uint32_t(t.s1) * uint32_t(sizeof(ET));
-    const uint32_t end = uint32_t(last) * pitch + ch * uint32_t(sizeof(ET));
-    uint32_t off = uint32_t(run * L) * pitch + ch * uint32_t(sizeof(ET));
+  __device__ __forceinline__ void load(const Place<ET, V, L>& at, __amdgpu_buffer_rsrc_t r) {
 #pragma unroll
     for (int j = 0; j < L; ++j) {
-      w[j] = *reinterpret_cast<const typename E::W*>(base + (run * L + j < last ? off : end));
-      off += pitch;
-    }
-    if constexpr (sizeof(ET) == 1) {
-      const uint8_t* sb = t.sc + (b * t.c0 + t0 * t.c1 + c0 / kScanCols);
-      const uint32_t sp = uint32_t(t.c1);
-#pragma unroll
-      for (int j = 0; j < L; ++j) sc[j] = sb[uint32_t(min(run * L + j, last)) * sp];
-    }
-  }
-  __device__ __forceinline__ void get(int j, float (&v)[V]) const {
-    E::get(w[j], v);
-    if constexpr (sizeof(ET) == 1) {
-      const float scale = __uint_as_float(uint32_t(sc[j]) << 23);
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] *= scale;
+      const int row = int(uint32_t(j) * at.pitch);
+      if constexpr (sizeof(w[0]) == 1) {
+        w[j] = __builtin_amdgcn_raw_buffer_load_b8(r, int(at.off), row, 0);
+      } else if constexpr (sizeof(w[0]) == 2) {
+        w[j] = __builtin_amdgcn_raw_buffer_load_b16(r, int(at.off), row, 0);
+      } else if constexpr (sizeof(w[0]) == 4) {
+        w[j] = __builtin_amdgcn_raw_buffer_load_b32(r, int(at.off), row, 0);
+      } else {
+        w[j] = __builtin_amdgcn_raw_buffer_load_b64(r, int(at.off), row, 0);
+      }
     }
   }
+  __device__ __forceinline__ void get(int j, float (&v)[V]) const { E::get(w[j], v); }
 };
 
 template <typename ET, int V, int L>
-__device__ __forceinline__ void store_row(const ScanTensor& t, int b, int t0, int c0, int run, int j, uint32_t ch,
-                                          const float (&v)[V]) {
-  char* base = static_cast<char*>(const_cast<void*>(t.p)) + (b * t.s0 + t0 * t.s1 + c0) * int64_t(sizeof(ET));
-  const uint32_t off = uint32_t(run * L + j) * uint32_t(t.s1) * uint32_t(sizeof(ET)) + ch * uint32_t(sizeof(ET));
-  *reinterpret_cast<typename Elems<ET, V>::W*>(base + off) = Elems<ET, V>::put(v);
+__device__ __forceinline__ void store_row(const Place<ET, V, L>& at, __amdgpu_buffer_rsrc_t r, int j, const float (&v)[V]) {
+  const auto w = Elems<ET, V>::put(v);
+  const int row = int(uint32_t(j) * at.pitch);
+  if constexpr (sizeof(w) == 2) {
+    __builtin_amdgcn_raw_buffer_store_b16(w, r, int(at.off), row, 0);
+  } else if constexpr (sizeof(w) == 4) {
+    __builtin_amdgcn_raw_buffer_store_b32(w, r, int(at.off), row, 0);
+  } else {
+    __builtin_amdgcn_raw_buffer_store_b64(w, r, int(at.off), row, 0);
+  }
 }
 
+// The scales of a tile's operands in 8 bits: a thread loads one of (operand, token), one tile before
+// they are put into LDS, which is one tile before their use.
+struct Scales {
+  uint32_t held;
+  __device__ __forceinline__ void load(const ScanParams& p, int b, int t0, int c0, int last) {
+    const int which = threadIdx.x / kScanTile, row = min(int(threadIdx.x % kScanTile), last);
+    const ScanTensor& t = which == 0 ? p.x : which == 1 ? p.decay : p.gate;
+    held = 0;
+    if (which < 3 && t.sc != nullptr) held = t.sc[b * t.c0 + (t0 + row) * t.c1 + c0 / kScanCols];
+  }
+  __device__ __forceinline__ void put(uint8_t (&to)[3][kScanTile]) const {
+    const int which = threadIdx.x / kScanTile;
+    if (which < 3) to[which][threadIdx.x % kScanTile] = uint8_t(held);
+  }
+};
+template <int L>
+struct RunScales {  // of a run's L tokens
+  uint32_t w[L / 4];
+  __device__ __forceinline__ void get(const uint8_t (&from)[kScanTile], int run) {
+#pragma unroll
+    for (int i = 0; i < L / 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(&from[run * L + 4 * i]);
+  }
+  __device__ __forceinline__ float step(int j) const { return __uint_as_float((w[j / 4] >> (8 * (j % 4)) & 0xffu) << 23); }
+};
+
 // Document starts of a tile as a bit per token, one tile ahead of their use.
-template <int TILE>
 struct Starts {
-  static constexpr int kWords = TILE / 64;
+  static constexpr int kWords = kScanTile / 64;
   static __device__ __forceinline__ void make(const ScanParams& p, int b, int t0, uint64_t* bits) {
-    if (threadIdx.x < TILE) {
+    if (threadIdx.x < kScanTile) {
       const int t = t0 + int(threadIdx.x);
       bool first = false;
       if (t > 0 && t < p.T) {
@@ -200,25 +238,53 @@ struct Starts {
   }
 };
 
-// h -> A h + H. A of zero (a document start, or a decay to nothing) forgets what came before, a
-// NaN of another document too.
-__device__ __forceinline__ float through(float A, float H, float h) { return A == 0.f ? H : __builtin_fmaf(A, h, H); }
+// h -> A h + H. With documents an A of zero (their start, or a decay to nothing) forgets what came
+// before, a NaN of another document too.
+template <bool DOCS>
+__device__ __forceinline__ float through(float A, float H, float h) {
+  const float r = __builtin_fmaf(A, h, H);
+  return DOCS ? (A == 0.f ? H : r) : r;
+}
+template <bool DOCS>
+__device__ __forceinline__ float chain(float A, float B) {  // of two maps' factors
+  return DOCS ? (A == 0.f ? 0.f : A * B) : A * B;
+}
+
+// The maps of the waves in LDS, read in pieces of a lane's channels.
+template <int V>
+__device__ __forceinline__ void read_map(const float (&m)[kScanCols], int chl, float (&v)[V]) {
+  if constexpr (V == 2) {
+    const float2 f = *reinterpret_cast<const float2*>(&m[chl]);
+    v[0] = f.x, v[1] = f.y;
+  } else {
+    v[0] = m[chl];
+  }
+}
+template <int V>
+__device__ __forceinline__ void write_map(float (&m)[kScanCols], int chl, const float (&v)[V]) {
+  if constexpr (V == 2) {
+    *reinterpret_cast<float2*>(&m[chl]) = float2{v[0], v[1]};
+  } else {
+    m[chl] = v[0];
+  }
+}
 
 // ---------------------------------------------------------------------------------
 // Forward. MAPS: only the map of the segment, into p.maps; with segment 0 the initial state too.
 // ---------------------------------------------------------------------------------
-template <typename ET, int V, bool PACKED, bool MAPS>
-__global__ __launch_bounds__(kThreads) void k_scan_fwd(const ScanParams p) {
+template <typename ET, int V, bool PACKED, bool DOCS, bool MAPS>
+__global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
   using IT = std::conditional_t<PACKED, i8_t, ET>;
-  constexpr int L = 16 / V;
-  __shared__ float maps[2][kScanWaves][kScanCols][2];
-  __shared__ uint64_t starts[2][Starts<kScanTile>::kWords];
+  constexpr int L = kScanElems / V;
+  __shared__ float maps[2][2][kScanWaves][kScanCols];  // [tile & 1][A, H]
+  __shared__ uint64_t starts[2][Starts::kWords];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[2][3][kScanTile];
   const int nCols = (p.D + kScanCols - 1) / kScanCols;
   const int b = int(blockIdx.x) / nCols, c0 = (int(blockIdx.x) - b * nCols) * kScanCols, seg = blockIdx.y;
   const Lane<V> me(p.D, c0);
-  const bool gated = p.gate.p != nullptr, docs = p.seg != nullptr;
+  const bool gated = p.gate.p != nullptr;
   float rate[V], carry[V], total[V];
-  const int cg = c0 + int(me.ch);
+  const int cg = me.cg;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     rate[i] = p.rate[cg + i];
@@ -233,7 +299,7 @@ __global__ __launch_bounds__(kThreads) void k_scan_fwd(const ScanParams p) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float2 f = m[int64_t(q) * p.D + i];
-        carry[i] = through(f.x, f.y, carry[i]);
+        carry[i] = through<DOCS>(f.x, f.y, carry[i]);
       }
     }
   } else if (p.nSeg == 1 && p.state_in != nullptr) {
@@ -242,40 +308,59 @@ __global__ __launch_bounds__(kThreads) void k_scan_fwd(const ScanParams p) {
   }
   const int nTiles = (p.T + kScanTile - 1) / kScanTile;
   const int k0 = seg * p.segTiles, k1 = min(nTiles, k0 + p.segTiles);
-  Rows<IT, V, L> rx, ra, rg;
-  auto fetch = [&](int k) {
-    const int t0 = k * kScanTile, last = min(p.T - t0, kScanTile) - 1;
-    rx.load(p.x, b, t0, c0, me.run, me.ch, last);
-    ra.load(p.decay, b, t0, c0, me.run, me.ch, last);
-    if (gated) rg.load(p.gate, b, t0, c0, me.run, me.ch, last);
+  Rows<IT, V, L> rx[2], ra[2], rg[2];
+  const Place<IT, V, L> px(p.x, me), pa(p.decay, me), pg(p.gate, me);
+  const Place<ET, V, L> py(p.y, me);
+  Scales sc;
+  auto last_of = [&](int k) { return min(p.T - k * kScanTile, kScanTile) - 1; };
+  auto fetch = [&](int k, Rows<IT, V, L>& x, Rows<IT, V, L>& a, Rows<IT, V, L>& g) {
+    const int t0 = k * kScanTile, last = last_of(k);
+    x.load(px, px.rows(p.x, b, t0, c0, last, p.D));
+    a.load(pa, pa.rows(p.decay, b, t0, c0, last, p.D));
+    if (gated) g.load(pg, pg.rows(p.gate, b, t0, c0, last, p.D));
   };
-  fetch(k0);
-  if (docs) {
-    Starts<kScanTile>::make(p, b, k0 * kScanTile, starts[k0 & 1]);
-    __syncthreads();
+  if constexpr (PACKED) {
+    sc.load(p, b, k0 * kScanTile, c0, last_of(k0));
+    sc.put(scales[k0 & 1]);
+    if (k0 + 1 < k1) sc.load(p, b, (k0 + 1) * kScanTile, c0, last_of(k0 + 1));
   }
-  for (int k = k0; k < k1; ++k) {
-    const int t0 = k * kScanTile, last = min(p.T - t0, kScanTile) - 1;
+  fetch(k0, rx[0], ra[0], rg[0]);
+  if (k0 + 1 < k1) fetch(k0 + 1, rx[1], ra[1], rg[1]);
+  if constexpr (DOCS) Starts::make(p, b, k0 * kScanTile, starts[k0 & 1]);
+  if constexpr (DOCS || PACKED) __syncthreads();
+
+  auto tile = [&](int k, Rows<IT, V, L>& cx, Rows<IT, V, L>& ca, Rows<IT, V, L>& cgt) {
+    const int t0 = k * kScanTile, last = last_of(k);
     float a[L][V], u[L][V];
+    RunScales<L> sx, sa, sg;
+    if constexpr (PACKED) {
+      sx.get(scales[k & 1][0], me.run);
+      sa.get(scales[k & 1][1], me.run);
+      sg.get(scales[k & 1][2], me.run);
+    }
 #pragma unroll
     for (int j = 0; j < L; ++j) {
       float x[V], r[V], g[V];
-      rx.get(j, x);
-      ra.get(j, r);
-#pragma unroll
-      for (int i = 0; i < V; ++i) g[i] = 1.f;
-      if (gated) {
-        rg.get(j, g);
-#pragma unroll
-        for (int i = 0; i < V; ++i) g[i] = sigmoid(g[i]);
-      }
+      cx.get(j, x);
+      ca.get(j, r);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const Decay d = decay_of(sigmoid(r[i]), rate[i]);
-        a[j][i] = d.a;
-        u[j][i] = d.b * g[i] * x[i];
+        if constexpr (PACKED) x[i] *= sx.step(j), r[i] *= sa.step(j);
+        const float s = sigmoid(r[i]);
+        const float q = rate[i] * s;
+        a[j][i] = __builtin_amdgcn_exp2f(q * -kLog2e);
+        u[j][i] = x[i] * __builtin_amdgcn_sqrtf(one_minus_exp(2.f * q, a[j][i] * a[j][i]));
+      }
+      if (gated) {
+        cgt.get(j, g);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if constexpr (PACKED) g[i] *= sg.step(j);
+          u[j][i] *= sigmoid(g[i]);
+        }
       }
     }
+    if (k + 2 < k1) fetch(k + 2, cx, ca, cgt);
     if (last < kScanTile - 1) {  // tokens that do not exist leave the state as it is
 #pragma unroll
       for (int j = 0; j < L; ++j)
@@ -285,36 +370,25 @@ __global__ __launch_bounds__(kThreads) void k_scan_fwd(const ScanParams p) {
           u[j][i] = me.run * L + j > last ? 0.f : u[j][i];
         }
     }
-    if (docs) {
-      const uint32_t m = Starts<kScanTile>::of_run(starts[k & 1], me.run, L);
+    if constexpr (DOCS) {
+      const uint32_t m = Starts::of_run(starts[k & 1], me.run, L);
 #pragma unroll
       for (int j = 0; j < L; ++j)
 #pragma unroll
         for (int i = 0; i < V; ++i) a[j][i] = m >> j & 1 ? 0.f : a[j][i];
     }
-    if (k + 1 < k1) fetch(k + 1);
     float A[V], H[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) A[i] = a[0][i], H[i] = u[0][i];
-    if (docs) {
 #pragma unroll
-      for (int j = 1; j < L; ++j)
+    for (int j = 1; j < L; ++j)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          H[i] = through(a[j][i], u[j][i], H[i]);
-          A[i] = a[j][i] == 0.f ? 0.f : a[j][i] * A[i];
-        }
-    } else {
-#pragma unroll
-      for (int j = 1; j < L; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          H[i] = __builtin_fmaf(a[j][i], H[i], u[j][i]);
-          A[i] *= a[j][i];
-        }
-    }
+      for (int i = 0; i < V; ++i) {
+        H[i] = through<DOCS>(a[j][i], u[j][i], H[i]);
+        A[i] = chain<DOCS>(a[j][i], A[i]);
+      }
     // the wave's map: its lane groups' one behind the other
-    float pA[V], pH[V];  // the map of the lane groups before this one
+    float pA[V], pH[V];  // the map of the lane group before this one
 #pragma unroll
     for (int i = 0; i < V; ++i) pA[i] = 1.f, pH[i] = 0.f;
     if constexpr (V == 2) {
@@ -325,52 +399,61 @@ __global__ __launch_bounds__(kThreads) void k_scan_fwd(const ScanParams p) {
         const float A1 = me.group ? A[i] : oA, H1 = me.group ? H[i] : oH;
         pA[i] = me.group ? A0 : 1.f;
         pH[i] = me.group ? H0 : 0.f;
-        A[i] = A1 == 0.f ? 0.f : A1 * A0;
-        H[i] = through(A1, H1, H0);
+        A[i] = chain<DOCS>(A1, A0);
+        H[i] = through<DOCS>(A1, H1, H0);
       }
     }
     if (me.group == 0) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        maps[k & 1][me.wave][me.chl + i][0] = A[i];
-        maps[k & 1][me.wave][me.chl + i][1] = H[i];
+      write_map<V>(maps[k & 1][0][me.wave], me.chl, A);
+      write_map<V>(maps[k & 1][1][me.wave], me.chl, H);
+    }
+    if (k + 1 < k1) {
+      if constexpr (DOCS) Starts::make(p, b, (k + 1) * kScanTile, starts[(k + 1) & 1]);
+      if constexpr (PACKED) {
+        sc.put(scales[(k + 1) & 1]);
+        if (k + 2 < k1) sc.load(p, b, (k + 2) * kScanTile, c0, last_of(k + 2));
       }
     }
-    if (docs && k + 1 < k1) Starts<kScanTile>::make(p, b, (k + 1) * kScanTile, starts[(k + 1) & 1]);
-    __syncthreads();  // the other half's readers are past it: they read it before the barrier before
+    __syncthreads();  // what is overwritten next was read before the barrier before
+    if constexpr (!MAPS) {
+      if (p.chunks != nullptr && me.wave == 0 && me.group == 0 && me.ok) {
+        float* out = p.chunks + (int64_t(b) * nTiles + k) * p.D + cg;
+#pragma unroll
+        for (int i = 0; i < V; ++i) out[i] = carry[i];
+      }
+    }
     float h[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = 0.f;
-#pragma unroll 4
+    for (int i = 0; i < V; ++i) h[i] = carry[i];
+#pragma unroll
     for (int w = 0; w < kScanWaves; ++w) {
+      float fA[V], fH[V];
+      read_map<V>(maps[k & 1][0][w], me.chl, fA);
+      read_map<V>(maps[k & 1][1][w], me.chl, fH);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if (w == me.wave) h[i] = carry[i];
-        const float fA = maps[k & 1][w][me.chl + i][0], fH = maps[k & 1][w][me.chl + i][1];
-        carry[i] = through(fA, fH, carry[i]);
-        if constexpr (MAPS) total[i] = fA == 0.f ? 0.f : fA * total[i];
+        carry[i] = through<DOCS>(fA[i], fH[i], carry[i]);
+        if (w < kScanWaves - 1) h[i] = w < me.wave ? carry[i] : h[i];
+        if constexpr (MAPS) total[i] = chain<DOCS>(fA[i], total[i]);
       }
     }
     if constexpr (!MAPS) {
-      const int row = me.run * L;
-      if (p.chunks != nullptr && me.group == 0 && row % kScanChunk == 0 && row <= last && me.ok) {
-        const int nC = (p.T + kScanChunk - 1) / kScanChunk;
-        float* out = p.chunks + (int64_t(b) * nC + (t0 + row) / kScanChunk) * p.D + cg;
-#pragma unroll
-        for (int i = 0; i < V; ++i) out[i] = h[i];
-      }
       if (p.y.p != nullptr) {
+        const __amdgpu_buffer_rsrc_t ry = py.rows(p.y, b, t0, c0, last, p.D);
 #pragma unroll
-        for (int i = 0; i < V; ++i) h[i] = through(pA[i], pH[i], h[i]);
+        for (int i = 0; i < V; ++i) h[i] = through<DOCS>(pA[i], pH[i], h[i]);
 #pragma unroll
         for (int j = 0; j < L; ++j) {
 #pragma unroll
-          for (int i = 0; i < V; ++i)
-            h[i] = docs ? through(a[j][i], u[j][i], h[i]) : __builtin_fmaf(a[j][i], h[i], u[j][i]);
-          if (me.ok && row + j <= last) store_row<ET, V, L>(p.y, b, t0, c0, me.run, j, me.ch, h);
+          for (int i = 0; i < V; ++i) h[i] = through<DOCS>(a[j][i], u[j][i], h[i]);
+          store_row(py, ry, j, h);
         }
       }
     }
+  };
+  for (int k = k0; k < k1; k += 2) {
+    tile(k, rx[0], ra[0], rg[0]);
+    if (k + 1 < k1) tile(k + 1, rx[1], ra[1], rg[1]);
   }
   if (!me.ok || threadIdx.x >= Lane<V>::kLanes) return;
   if constexpr (MAPS) {
@@ -389,18 +472,19 @@ __global__ __launch_bounds__(kThreads) void k_scan_fwd(const ScanParams p) {
 // ---------------------------------------------------------------------------------
 // Backward, tiles from the last to the first. MAPS: only the segment's map of e.
 // ---------------------------------------------------------------------------------
-template <typename ET, int V, bool PACKED, bool MAPS>
-__global__ __launch_bounds__(kThreads) void k_scan_bwd(const ScanParams p) {
+template <typename ET, int V, bool PACKED, bool DOCS, bool MAPS>
+__global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
   using IT = std::conditional_t<PACKED, i8_t, ET>;
-  constexpr int L = 8 / V;
-  __shared__ float maps[2][kScanWaves][kScanCols][MAPS ? 2 : 3];
-  __shared__ uint64_t starts[2][Starts<kScanTileBwd>::kWords];
+  constexpr int L = kScanElems / V;
+  __shared__ float maps[2][MAPS ? 2 : 3][kScanWaves][kScanCols];  // [tile & 1][A, E, H]
+  __shared__ uint64_t starts[2][Starts::kWords];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[2][3][kScanTile];
   const int nCols = (p.D + kScanCols - 1) / kScanCols;
   const int b = int(blockIdx.x) / nCols, c0 = (int(blockIdx.x) - b * nCols) * kScanCols;
   const int seg = int(blockIdx.y) + (MAPS ? 1 : 0);
   const Lane<V> me(p.D, c0);
-  const bool gated = p.gate.p != nullptr, docs = p.seg != nullptr;
-  const int cg = c0 + int(me.ch);
+  const bool gated = p.gate.p != nullptr;
+  const int cg = me.cg, row = me.run * L;
   float rate[V], carry[V], total[V];
   double drate[V];
 #pragma unroll
@@ -418,47 +502,62 @@ __global__ __launch_bounds__(kThreads) void k_scan_bwd(const ScanParams p) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float2 f = m[int64_t(q) * p.D + i];
-        carry[i] = through(f.x, f.y, carry[i]);
+        carry[i] = through<DOCS>(f.x, f.y, carry[i]);
       }
     }
   } else if (p.nSeg == 1 && p.dstate_out != nullptr) {
 #pragma unroll
     for (int i = 0; i < V; ++i) carry[i] = p.dstate_out[b * p.dsos + cg + i];
   }
-  const int nTiles = (p.T + kScanTileBwd - 1) / kScanTileBwd;
+  const int nTiles = (p.T + kScanTile - 1) / kScanTile;
   const int k0 = seg * p.segTiles, k1 = min(nTiles, k0 + p.segTiles);
   Rows<IT, V, L> rx, ra, rg;
   Rows<ET, V, L> rd;
+  const Place<IT, V, L> px(p.x, me), pa(p.decay, me), pg(p.gate, me);
+  const Place<ET, V, L> pd(p.dy, me), pdx(p.dx, me), pda(p.ddecay, me), pdg(p.dgate, me);
+  Scales sc;
   float kept[V];
+  auto last_of = [&](int k) { return min(p.T - k * kScanTile, kScanTile) - 1; };
   auto fetch = [&](int k) {
-    const int t0 = k * kScanTileBwd, last = min(p.T - t0, kScanTileBwd) - 1;
-    ra.load(p.decay, b, t0, c0, me.run, me.ch, last);
-    rd.load(p.dy, b, t0, c0, me.run, me.ch, last);
+    const int t0 = k * kScanTile, last = last_of(k);
+    ra.load(pa, pa.rows(p.decay, b, t0, c0, last, p.D));
+    rd.load(pd, pd.rows(p.dy, b, t0, c0, last, p.D));
     if constexpr (!MAPS) {
-      rx.load(p.x, b, t0, c0, me.run, me.ch, last);
-      if (gated) rg.load(p.gate, b, t0, c0, me.run, me.ch, last);
+      rx.load(px, px.rows(p.x, b, t0, c0, last, p.D));
+      if (gated) rg.load(pg, pg.rows(p.gate, b, t0, c0, last, p.D));
       const float* c = p.chunks + (int64_t(b) * nTiles + k) * p.D + cg;
 #pragma unroll
       for (int i = 0; i < V; ++i) kept[i] = c[i];
     }
   };
-  fetch(k1 - 1);
-  if (docs) {
-    Starts<kScanTileBwd>::make(p, b, (k1 - 1) * kScanTileBwd, starts[(k1 - 1) & 1]);
-    __syncthreads();
+  if constexpr (PACKED) {
+    sc.load(p, b, (k1 - 1) * kScanTile, c0, last_of(k1 - 1));
+    sc.put(scales[(k1 - 1) & 1]);
+    if (k1 - 1 > k0) sc.load(p, b, (k1 - 2) * kScanTile, c0, last_of(k1 - 2));
   }
+  fetch(k1 - 1);
+  if constexpr (DOCS) Starts::make(p, b, (k1 - 1) * kScanTile, starts[(k1 - 1) & 1]);
+  if constexpr (DOCS || PACKED) __syncthreads();
   for (int k = k1 - 1; k >= k0; --k) {
-    const int t0 = k * kScanTileBwd, last = min(p.T - t0, kScanTileBwd) - 1;
-    const int row = me.run * L;
-    float a[L][V], s[L][V], rb[L][V], b_[L][V], sg[L][V], x[L][V], hb[L][V], dy[L][V];
-    float hk[V];
+    const int t0 = k * kScanTile, last = last_of(k);
+    // f: what passes a token (a, or 0 where it starts a document); w = b sigmoid(gate); c = sigmoid(gate) a^2 / b
+    float a[L][V], s[L][V], w[L][V], c[L][V], sg[L][V], x[L][V], hb[L][V], dy[L][V], hk[V];
+    RunScales<L> sx, sa, sgt;
+    if constexpr (PACKED) {
+      sx.get(scales[k & 1][0], me.run);
+      sa.get(scales[k & 1][1], me.run);
+      sgt.get(scales[k & 1][2], me.run);
+    }
 #pragma unroll
     for (int j = 0; j < L; ++j) {
       float r[V];
       ra.get(j, r);
       rd.get(j, dy[j]);
 #pragma unroll
-      for (int i = 0; i < V; ++i) s[j][i] = sigmoid(r[i]);
+      for (int i = 0; i < V; ++i) {
+        if constexpr (PACKED) r[i] *= sa.step(j);
+        s[j][i] = sigmoid(r[i]);
+      }
       if constexpr (!MAPS) {
         rx.get(j, x[j]);
 #pragma unroll
@@ -466,19 +565,25 @@ __global__ __launch_bounds__(kThreads) void k_scan_bwd(const ScanParams p) {
         if (gated) {
           rg.get(j, sg[j]);
 #pragma unroll
-          for (int i = 0; i < V; ++i) sg[j][i] = sigmoid(sg[j][i]);
+          for (int i = 0; i < V; ++i) {
+            if constexpr (PACKED) sg[j][i] *= sgt.step(j);
+            sg[j][i] = sigmoid(sg[j][i]);
+          }
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+          if constexpr (PACKED) x[j][i] *= sx.step(j);
           const Decay d = decay_of(s[j][i], rate[i]);
-          a[j][i] = d.a, rb[j][i] = d.rb, b_[j][i] = d.b;
+          a[j][i] = d.a;
+          w[j][i] = d.b * sg[j][i];
+          c[j][i] = d.a * d.a * d.rb * sg[j][i];
         }
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) a[j][i] = __builtin_amdgcn_exp2f(rate[i] * s[j][i] * -kLog2e);
       }
     }
-    if (last < kScanTileBwd - 1) {
+    if (last < kScanTile - 1) {
 #pragma unroll
       for (int j = 0; j < L; ++j)
 #pragma unroll
@@ -489,18 +594,17 @@ __global__ __launch_bounds__(kThreads) void k_scan_bwd(const ScanParams p) {
           if constexpr (!MAPS) {
             s[j][i] = gone ? 0.f : s[j][i];
             x[j][i] = gone ? 0.f : x[j][i];
-            b_[j][i] = gone ? 0.f : b_[j][i];
-            rb[j][i] = gone ? 0.f : rb[j][i];
-            sg[j][i] = gone ? 0.f : sg[j][i];
+            w[j][i] = gone ? 0.f : w[j][i];
+            c[j][i] = gone ? 0.f : c[j][i];
           }
         }
     }
-    uint32_t first = 0;  // tokens that start a document: nothing passes through them, forwards or backwards
-    if (docs) first = Starts<kScanTileBwd>::of_run(starts[k & 1], me.run, L);
 #pragma unroll
     for (int i = 0; i < V; ++i) hk[i] = MAPS ? 0.f : kept[i];
     if (k > k0) fetch(k - 1);
-    auto pass = [&](int j, int i) { return first >> j & 1 ? 0.f : a[j][i]; };
+    uint32_t first = 0;  // tokens that start a document: nothing passes through them, forwards or backwards
+    if constexpr (DOCS) first = Starts::of_run(starts[k & 1], me.run, L);
+    auto pass = [&](int j, int i) { return DOCS && (first >> j & 1) ? 0.f : a[j][i]; };
     float A[V], H[V], E[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) A[i] = 1.f, H[i] = 0.f, E[i] = 0.f;
@@ -509,17 +613,17 @@ __global__ __launch_bounds__(kThreads) void k_scan_bwd(const ScanParams p) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float f = pass(j, i);
-        A[i] = f == 0.f ? 0.f : f * A[i];
-        if constexpr (!MAPS) H[i] = through(f, b_[j][i] * sg[j][i] * x[j][i], H[i]);
+        A[i] = chain<DOCS>(f, A[i]);
+        if constexpr (!MAPS) {
+          hb[j][i] = w[j][i] * x[j][i];
+          H[i] = through<DOCS>(f, hb[j][i], H[i]);
+        }
       }
 #pragma unroll
     for (int j = L - 1; j >= 0; --j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float f = pass(j, i);
-        E[i] = f == 0.f ? 0.f : f * (dy[j][i] + E[i]);
-      }
-    float pA[V], pH[V], pE[V];  // A: the other lane group's; H before this one, E behind it
+      for (int i = 0; i < V; ++i) E[i] = chain<DOCS>(pass(j, i), dy[j][i] + E[i]);
+    float pA[V], pH[V], pE[V];  // of the other lane group
 #pragma unroll
     for (int i = 0; i < V; ++i) pA[i] = 1.f, pH[i] = 0.f, pE[i] = 0.f;
     if constexpr (V == 2) {
@@ -530,63 +634,71 @@ __global__ __launch_bounds__(kThreads) void k_scan_bwd(const ScanParams p) {
         const float E0 = me.group ? oE : E[i], E1 = me.group ? E[i] : oE;
         pA[i] = oA;
         pE[i] = oE;
-        A[i] = A0 == 0.f || A1 == 0.f ? 0.f : A1 * A0;
-        E[i] = through(A0, E0, E1);
+        A[i] = chain<DOCS>(A1, A0);
+        E[i] = through<DOCS>(A0, E0, E1);
         if constexpr (!MAPS) {
           const float oH = __shfl_xor(H[i], 32);
           const float H0 = me.group ? oH : H[i], H1 = me.group ? H[i] : oH;
           pH[i] = oH;
-          H[i] = through(A1, H1, H0);
+          H[i] = through<DOCS>(A1, H1, H0);
         }
       }
     }
     if (me.group == 0) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        maps[k & 1][me.wave][me.chl + i][0] = A[i];
-        maps[k & 1][me.wave][me.chl + i][1] = E[i];
-        if constexpr (!MAPS) maps[k & 1][me.wave][me.chl + i][2] = H[i];
+      write_map<V>(maps[k & 1][0][me.wave], me.chl, A);
+      write_map<V>(maps[k & 1][1][me.wave], me.chl, E);
+      if constexpr (!MAPS) write_map<V>(maps[k & 1][2][me.wave], me.chl, H);
+    }
+    if (k > k0) {
+      if constexpr (DOCS) Starts::make(p, b, (k - 1) * kScanTile, starts[(k - 1) & 1]);
+      if constexpr (PACKED) {
+        sc.put(scales[(k - 1) & 1]);
+        if (k - 1 > k0) sc.load(p, b, (k - 2) * kScanTile, c0, last_of(k - 2));
       }
     }
-    if (docs && k > k0) Starts<kScanTileBwd>::make(p, b, (k - 1) * kScanTileBwd, starts[(k - 1) & 1]);
     __syncthreads();
     float e[V], h[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) e[i] = 0.f, h[i] = hk[i];
-#pragma unroll 4
-    for (int w = kScanWaves - 1; w >= 0; --w) {
+    for (int i = 0; i < V; ++i) e[i] = carry[i], h[i] = hk[i];
+#pragma unroll 2
+    for (int q = kScanWaves - 1; q >= 0; --q) {
+      float fA[V], fE[V];
+      read_map<V>(maps[k & 1][0][q], me.chl, fA);
+      read_map<V>(maps[k & 1][1][q], me.chl, fE);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if (w == me.wave) e[i] = carry[i];
-        const float fA = maps[k & 1][w][me.chl + i][0], fE = maps[k & 1][w][me.chl + i][1];
-        carry[i] = through(fA, fE, carry[i]);
-        if constexpr (MAPS) total[i] = fA == 0.f ? 0.f : fA * total[i];
+        carry[i] = through<DOCS>(fA[i], fE[i], carry[i]);
+        e[i] = q > me.wave ? carry[i] : e[i];
+        if constexpr (MAPS) total[i] = chain<DOCS>(fA[i], total[i]);
       }
     }
     if constexpr (!MAPS) {
-#pragma unroll 1
-      for (int w = 0; w < me.wave; ++w) {
+#pragma unroll 2
+      for (int q = 0; q < kScanWaves; ++q) {
+        float fA[V], fH[V];
+        read_map<V>(maps[k & 1][0][q], me.chl, fA);
+        read_map<V>(maps[k & 1][2][q], me.chl, fH);
 #pragma unroll
-        for (int i = 0; i < V; ++i) h[i] = through(maps[k & 1][w][me.chl + i][0], maps[k & 1][w][me.chl + i][2], h[i]);
+        for (int i = 0; i < V; ++i) h[i] = q < me.wave ? through<DOCS>(fA[i], fH[i], h[i]) : h[i];
       }
       if constexpr (V == 2) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          if (me.group) {
-            h[i] = through(pA[i], pH[i], h[i]);
-          } else {
-            e[i] = through(pA[i], pE[i], e[i]);
-          }
+          const float hn = through<DOCS>(pA[i], pH[i], h[i]), en = through<DOCS>(pA[i], pE[i], e[i]);
+          h[i] = me.group ? hn : h[i];
+          e[i] = me.group ? e[i] : en;
         }
       }
 #pragma unroll
       for (int j = 0; j < L; ++j)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float f = pass(j, i);
-          hb[j][i] = f == 0.f ? 0.f : h[i];
-          h[i] = through(f, b_[j][i] * sg[j][i] * x[j][i], h[i]);
+          const float f = pass(j, i), before = DOCS ? (f == 0.f ? 0.f : h[i]) : h[i];
+          h[i] = through<DOCS>(f, hb[j][i], h[i]);
+          hb[j][i] = before;
         }
+      const __amdgpu_buffer_rsrc_t rdx = pdx.rows(p.dx, b, t0, c0, last, p.D), rda = pda.rows(p.ddecay, b, t0, c0, last, p.D);
+      const __amdgpu_buffer_rsrc_t rdg = pdg.rows(p.dgate, b, t0, c0, last, p.D);
       float sum[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) sum[i] = 0.f;
@@ -596,20 +708,17 @@ __global__ __launch_bounds__(kThreads) void k_scan_bwd(const ScanParams p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const float dh = dy[j][i] + e[i];
-          const float dhs = dh * sg[j][i];
-          dx[i] = dhs * b_[j][i];
+          dx[i] = dh * w[j][i];
           dg[i] = dx[i] * x[j][i] * (1.f - sg[j][i]);
           const float ad = a[j][i] * dh;
-          const float dl = s[j][i] * __builtin_fmaf(ad, hb[j][i], -(a[j][i] * a[j][i]) * rb[j][i] * dhs * x[j][i]);
+          const float dl = s[j][i] * __builtin_fmaf(ad, hb[j][i], -c[j][i] * dh * x[j][i]);
           sum[i] -= dl;
           dr[i] = -rate[i] * dl * (1.f - s[j][i]);
-          e[i] = first >> j & 1 ? 0.f : ad;
+          e[i] = DOCS && (first >> j & 1) ? 0.f : ad;
         }
-        if (me.ok && row + j <= last) {
-          store_row<ET, V, L>(p.dx, b, t0, c0, me.run, j, me.ch, dx);
-          store_row<ET, V, L>(p.ddecay, b, t0, c0, me.run, j, me.ch, dr);
-          if (gated) store_row<ET, V, L>(p.dgate, b, t0, c0, me.run, j, me.ch, dg);
-        }
+        store_row(pdx, rdx, j, dx);
+        store_row(pda, rda, j, dr);
+        if (gated) store_row(pdg, rdg, j, dg);
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) drate[i] += double(sum[i]);  // 64 bits: of any number of tiles
@@ -636,7 +745,7 @@ __global__ __launch_bounds__(kThreads) void k_scan_bwd(const ScanParams p) {
     if (int(threadIdx.x) < kScanCols && c0 + int(threadIdx.x) < p.D) {
       double t = 0.0;
 #pragma unroll
-      for (int w = 0; w < kScanWaves; ++w) t += sums[w][threadIdx.x];
+      for (int q = 0; q < kScanWaves; ++q) t += sums[q][threadIdx.x];
       p.drate_part[(int64_t(b) * p.nSeg + seg) * p.D + c0 + threadIdx.x] = float(t);
     }
     if (p.dstate != nullptr && k0 == 0 && me.ok && int(threadIdx.x) < Lane<V>::kLanes) {
@@ -646,43 +755,37 @@ __global__ __launch_bounds__(kThreads) void k_scan_bwd(const ScanParams p) {
   }
 }
 
-template <typename ET, int V, bool PACKED>
-hipError_t launch_fwd(const ScanParams& p, hipStream_t s) {
+template <typename ET, int V, bool PACKED, bool DOCS>
+hipError_t launch(const ScanParams& p, bool bwd, hipStream_t s) {
   const unsigned blocks = unsigned((p.D + kScanCols - 1) / kScanCols) * unsigned(p.B);
+  const dim3 first(blocks, unsigned(p.nSeg - 1)), all(blocks, unsigned(p.nSeg));
   if (p.nSeg > 1) {
-    hipLaunchKernelGGL((k_scan_fwd<ET, V, PACKED, true>), dim3(blocks, unsigned(p.nSeg - 1)), dim3(kThreads),
-                       0, s, p);
+    if (bwd) {
+      hipLaunchKernelGGL((k_scan_bwd<ET, V, PACKED, DOCS, true>), first, dim3(kThreads), 0, s, p);
+    } else {
+      hipLaunchKernelGGL((k_scan_fwd<ET, V, PACKED, DOCS, true>), first, dim3(kThreads), 0, s, p);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((k_scan_fwd<ET, V, PACKED, false>), dim3(blocks, unsigned(p.nSeg)), dim3(kThreads), 0, s,
-                     p);
-  return hipGetLastError();
-}
-
-template <typename ET, int V, bool PACKED>
-hipError_t launch_bwd(const ScanParams& p, hipStream_t s) {
-  const unsigned blocks = unsigned((p.D + kScanCols - 1) / kScanCols) * unsigned(p.B);
-  if (p.nSeg > 1) {
-    hipLaunchKernelGGL((k_scan_bwd<ET, V, PACKED, true>), dim3(blocks, unsigned(p.nSeg - 1)), dim3(kThreads),
-                       0, s, p);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  if (bwd) {
+    hipLaunchKernelGGL((k_scan_bwd<ET, V, PACKED, DOCS, false>), all, dim3(kThreads), 0, s, p);
+  } else {
+    hipLaunchKernelGGL((k_scan_fwd<ET, V, PACKED, DOCS, false>), all, dim3(kThreads), 0, s, p);
   }
-  hipLaunchKernelGGL((k_scan_bwd<ET, V, PACKED, false>), dim3(blocks, unsigned(p.nSeg)), dim3(kThreads), 0, s,
-                     p);
   return hipGetLastError();
 }
 
-template <typename ET>
-hipError_t fwd(const ScanParams& p, int vec, bool packed, hipStream_t s) {
-  if (vec == 2) return packed ? launch_fwd<ET, 2, true>(p, s) : launch_fwd<ET, 2, false>(p, s);
-  return packed ? launch_fwd<ET, 1, true>(p, s) : launch_fwd<ET, 1, false>(p, s);
+template <typename ET, int V>
+hipError_t launch_v(const ScanParams& p, bool packed, bool bwd, hipStream_t s) {
+  const bool docs = p.seg != nullptr;
+  if (packed) return docs ? launch<ET, V, true, true>(p, bwd, s) : launch<ET, V, true, false>(p, bwd, s);
+  return docs ? launch<ET, V, false, true>(p, bwd, s) : launch<ET, V, false, false>(p, bwd, s);
 }
+
 template <typename ET>
-hipError_t bwd(const ScanParams& p, int vec, bool packed, hipStream_t s) {
-  if (vec == 2) return packed ? launch_bwd<ET, 2, true>(p, s) : launch_bwd<ET, 2, false>(p, s);
-  return packed ? launch_bwd<ET, 1, true>(p, s) : launch_bwd<ET, 1, false>(p, s);
+hipError_t run(const ScanParams& p, int vec, bool packed, bool bwd, hipStream_t s) {
+  return vec == 2 ? launch_v<ET, 2>(p, packed, bwd, s) : launch_v<ET, 1>(p, packed, bwd, s);
 }
 
 }  // namespace scan
