@@ -30,7 +30,7 @@ __global__ __launch_bounds__(kStepThreads) void k_scan_step(const ScanStepParams
   if (p.gate != nullptr) E::get(at(p.gate, p.gs), g);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const scan::Decay d = scan::decay_of(scan::sigmoid(r[v]), p.rate[c + v]);
+    const scan::Decay d = scan::decay_of(scan::sigmoid(r[v]), p.rate[c + v] * scan::kLog2e);
     y[v] = __builtin_fmaf(d.a, st[v], d.b * (p.gate != nullptr ? scan::sigmoid(g[v]) : 1.f) * x[v]);
   }
 #pragma unroll

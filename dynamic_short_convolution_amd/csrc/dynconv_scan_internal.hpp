@@ -55,8 +55,8 @@ inline int32_t scan_segment_tiles(int64_t B, int64_t D, int64_t T) {
   const int64_t blocks = B * ((D + kScanCols - 1) / kScanCols), tiles = (T + kScanTile - 1) / kScanTile;
   int64_t want = blocks > 0 ? 256 / blocks : 1;  // one workgroup per CU
   if (want < 2 || tiles < 4) return int32_t(tiles > 0 ? tiles : 1);
-  if (want > tiles / 2) want = tiles / 2;
-  if (want > 32) want = 32;
+  if (want > tiles) want = tiles;
+  if (want > 64) want = 64;
   return int32_t((tiles + want - 1) / want);
 }
 inline int32_t scan_segments(int64_t T, int32_t segTiles) {

@@ -26,6 +26,7 @@ namespace scan {
 
 constexpr int kThreads = kScanWaves * 64;
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kAhead = 8;  // segments' maps whose loads are under way at a time
 
 // Words that hold N bytes.
 template <int N>
@@ -91,28 +92,31 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -kLog2e));
 }
 
-// (1 - e^-z) for z >= 0. Below a half the difference would cancel: a polynomial for (1 - e^-z) / z,
-// interpolated at the six Chebyshev points of [0, 0.5] (5e-8 of the value in float32).
-__device__ __forceinline__ float one_minus_exp(float z, float ez) {
-  float p = -0x1.267e62p-10f;
-  p = __builtin_fmaf(p, z, 0x1.0c5b76p-7f);
-  p = __builtin_fmaf(p, z, -0x1.550898p-5f);
-  p = __builtin_fmaf(p, z, 0x1.55531cp-3f);
-  p = __builtin_fmaf(p, z, -0x1.fffff4p-2f);
-  p = __builtin_fmaf(p, z, 1.f);
-  return z < 0.5f ? p * z : 1.f - ez;
+// 1 - a^2 for a = 2^-v, v >= 0. At small v the difference would cancel: a polynomial for
+// (1 - 2^-2v) / v, interpolated at the six Chebyshev points of [0, 0.36] (1.2e-7 of the value in float32);
+// above, a^2 is at most 0.61.
+__device__ __forceinline__ float one_minus_square(float v, float a) {
+  float p = -0x1.0563dcp-7f;
+  p = __builtin_fmaf(p, v, 0x1.57861ep-5f);
+  p = __builtin_fmaf(p, v, -0x1.3ae43ap-3f);
+  p = __builtin_fmaf(p, v, 0x1.c6ad9cp-2f);
+  p = __builtin_fmaf(p, v, -0x1.ebfbd4p-1f);
+  p = __builtin_fmaf(p, v, 0x1.62e430p+0f);
+  float small = p * v, large = __builtin_fmaf(-a, a, 1.f);
+  asm("" : "+v"(small), "+v"(large));  // both formed: without this the compiler makes a divergent branch of every element
+  return v < 0.36f ? small : large;
 }
 
-// One token's decay and input scale: a, 1/b (0 where b is 0) and b.
+// One token's decay and input scale: a, 1/b (0 where b is 0) and b. rate: in units of log 2.
 struct Decay {
   float a, rb, b;
 };
 __device__ __forceinline__ Decay decay_of(float s, float rate) {
-  const float g = rate * s;  // -log a
+  const float v = rate * s;  // -log2 a
   Decay d;
-  d.a = __builtin_amdgcn_exp2f(g * -kLog2e);
-  const float q = one_minus_exp(2.f * g, d.a * d.a);
-  d.rb = q > 0.f ? __builtin_amdgcn_rsqf(q) : q;  // q of a NaN stays one
+  d.a = __builtin_amdgcn_exp2f(-v);
+  const float q = one_minus_square(v, d.a);
+  d.rb = q == 0.f ? 0.f : __builtin_amdgcn_rsqf(q);
   d.b = q * d.rb;
   return d;
 }
@@ -287,7 +291,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
   const int cg = me.cg;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    rate[i] = p.rate[cg + i];
+    rate[i] = p.rate[cg + i] * kLog2e;
     carry[i] = 0.f;
     total[i] = 1.f;
   }
@@ -295,12 +299,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
     const float2* m = p.maps + (int64_t(b) * p.nSeg) * p.D + cg;
 #pragma unroll
     for (int i = 0; i < V; ++i) carry[i] = m[i].y;
-    for (int q = 1; q <= seg; ++q) {
+    for (int q0 = 1; q0 <= seg; q0 += kAhead) {
+      float2 f[kAhead][V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float2 f = m[int64_t(q) * p.D + i];
-        carry[i] = through<DOCS>(f.x, f.y, carry[i]);
-      }
+      for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[q][i] = m[int64_t(min(q0 + q, seg)) * p.D + i];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+        for (int i = 0; i < V; ++i) carry[i] = q0 + q <= seg ? through<DOCS>(f[q][i].x, f[q][i].y, carry[i]) : carry[i];
     }
   } else if (p.nSeg == 1 && p.state_in != nullptr) {
 #pragma unroll
@@ -347,9 +355,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
       for (int i = 0; i < V; ++i) {
         if constexpr (PACKED) x[i] *= sx.step(j), r[i] *= sa.step(j);
         const float s = sigmoid(r[i]);
-        const float q = rate[i] * s;
-        a[j][i] = __builtin_amdgcn_exp2f(q * -kLog2e);
-        u[j][i] = x[i] * __builtin_amdgcn_sqrtf(one_minus_exp(2.f * q, a[j][i] * a[j][i]));
+        const float v = rate[i] * s;
+        a[j][i] = __builtin_amdgcn_exp2f(-v);
+        u[j][i] = x[i] * __builtin_amdgcn_sqrtf(one_minus_square(v, a[j][i]));
       }
       if (gated) {
         cgt.get(j, g);
@@ -489,7 +497,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
   double drate[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    rate[i] = p.rate[cg + i];
+    rate[i] = p.rate[cg + i] * kLog2e;
     carry[i] = 0.f;
     total[i] = 1.f;
     drate[i] = 0.0;
@@ -498,12 +506,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
     const float2* m = p.maps + (int64_t(b) * p.nSeg) * p.D + cg;
 #pragma unroll
     for (int i = 0; i < V; ++i) carry[i] = m[int64_t(p.nSeg - 1) * p.D + i].y;
-    for (int q = p.nSeg - 2; q >= seg; --q) {
+    for (int q0 = p.nSeg - 2; q0 >= seg; q0 -= kAhead) {
+      float2 f[kAhead][V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float2 f = m[int64_t(q) * p.D + i];
-        carry[i] = through<DOCS>(f.x, f.y, carry[i]);
-      }
+      for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[q][i] = m[int64_t(max(q0 - q, seg)) * p.D + i];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+        for (int i = 0; i < V; ++i) carry[i] = q0 - q >= seg ? through<DOCS>(f[q][i].x, f[q][i].y, carry[i]) : carry[i];
     }
   } else if (p.nSeg == 1 && p.dstate_out != nullptr) {
 #pragma unroll
@@ -580,7 +592,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) a[j][i] = __builtin_amdgcn_exp2f(rate[i] * s[j][i] * -kLog2e);
+        for (int i = 0; i < V; ++i) a[j][i] = __builtin_amdgcn_exp2f(-(rate[i] * s[j][i]));
       }
     }
     if (last < kScanTile - 1) {
@@ -699,9 +711,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
         }
       const __amdgpu_buffer_rsrc_t rdx = pdx.rows(p.dx, b, t0, c0, last, p.D), rda = pda.rows(p.ddecay, b, t0, c0, last, p.D);
       const __amdgpu_buffer_rsrc_t rdg = pdg.rows(p.dgate, b, t0, c0, last, p.D);
-      float sum[V];
+      float sum[V], back[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum[i] = 0.f;
+      for (int i = 0; i < V; ++i) sum[i] = 0.f, back[i] = rate[i] * -0.693147180559945309417f;  // of log 2
 #pragma unroll
       for (int j = L - 1; j >= 0; --j) {
         float dx[V], dr[V], dg[V];
@@ -713,7 +725,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
           const float ad = a[j][i] * dh;
           const float dl = s[j][i] * __builtin_fmaf(ad, hb[j][i], -c[j][i] * dh * x[j][i]);
           sum[i] -= dl;
-          dr[i] = -rate[i] * dl * (1.f - s[j][i]);
+          dr[i] = back[i] * dl * (1.f - s[j][i]);
           e[i] = DOCS && (first >> j & 1) ? 0.f : ad;
         }
         store_row(pdx, rdx, j, dx);
