@@ -87,12 +87,12 @@ hipError_t group_sum(const float* part, int64_t n, int64_t C, int64_t batches, f
 GroupPlan group_plan(int64_t Cg, int E) {
   const int64_t loads = (Cg + E - 1) / E;  // of the row
   if (E > 1) {
-    if (loads <= 4) return {4, 1};
-    if (loads <= 8) return {8, 1};
+    for (int lpr : {4, 8, 16, 32, 64})
+      if (loads <= lpr) return {lpr, 1};
+  } else {
+    if (loads <= 32) return {16, 2};
+    if (loads <= 64) return {16, 4};
   }
-  if (loads <= 16) return {16, 1};
-  if (E > 1 && loads <= 32) return {32, 1};
-  if (loads <= 64) return {64, 1};
   if (loads <= 128) return {64, 2};
   if (loads <= 256) return {64, 4};
   if (loads <= 512) return {256, 2};
@@ -100,14 +100,16 @@ GroupPlan group_plan(int64_t Cg, int E) {
   return {256, 0};
 }
 
-int64_t group_token_blocks(int64_t tokens, int64_t G, int64_t Cg, int E, int32_t* gpw, int32_t* tpw) {
+int64_t group_token_blocks(int64_t tokens, int64_t G, int64_t Cg, int E, bool bwd, int32_t* gpw, int32_t* tpw) {
   const int64_t rpb = kThreads / group_plan(Cg, E).lpr;
   *gpw = int32_t(G < rpb ? G : rpb);
   *tpw = int32_t(rpb / *gpw);
   const int64_t need = (tokens + *tpw - 1) / *tpw, across = (G + *gpw - 1) / *gpw;
-  // four workgroups per CU, and more where a lane would add over 512 rows to its float32 sums
-  int64_t most = across < 1024 ? 1024 / across : 1;
-  if ((need + 511) / 512 > most) most = (need + 511) / 512;
+  // Workgroups per CU: eight in the forward; four in the backward, each of which leaves a row of
+  // partial sums, and more where a lane would add over 512 rows to its float32 sums.
+  const int64_t all = bwd ? 1024 : 2048;
+  int64_t most = across < all ? all / across : 1;
+  if (bwd && (need + 511) / 512 > most) most = (need + 511) / 512;
   return need < most ? need : most;
 }
 
@@ -194,7 +196,7 @@ Space space(const Sizes& z, int E, bool bwd, bool stats) {
   const GroupParams p = sized(z, E);
   if (!z.sequence) {
     int32_t gpw, tpw;
-    if (bwd) w.colpart = rounded(size_t(group_token_blocks(z.B * z.T, z.G, p.Cg, E, &gpw, &tpw)) * 2 * size_t(z.C) * sizeof(float));
+    if (bwd) w.colpart = rounded(size_t(group_token_blocks(z.B * z.T, z.G, p.Cg, E, true, &gpw, &tpw)) * 2 * size_t(z.C) * sizeof(float));
     return w;
   }
   const size_t rows = size_t(z.B) * size_t(p.nChunk);
@@ -357,7 +359,7 @@ dynconv_status dynconv_groupnorm_bwd(const void* x, const int64_t* xs, const uin
     int32_t gpw, tpw;
     e = tokens(p, dtype, vec, packed, true, s);
     if (e == hipSuccess && params)
-      e = group_sum(p.colpart, group_token_blocks(B * T, groups, p.Cg, vec ? E : 1, &gpw, &tpw), C, 1, dweight, dbias, 0, s);
+      e = group_sum(p.colpart, group_token_blocks(B * T, groups, p.Cg, vec ? E : 1, true, &gpw, &tpw), C, 1, dweight, dbias, 0, s);
     return done(e);
   }
   if (stats != nullptr) {

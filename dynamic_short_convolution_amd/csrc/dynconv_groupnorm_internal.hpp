@@ -30,7 +30,7 @@ struct GroupParams {
   int32_t B, T, C, G, Cg;
   int32_t silu;
   float eps;
-  // Backward over tokens: groups and tokens that a workgroup works on at a time.
+  // Per token: groups and tokens that a workgroup works on at a time.
   int32_t gpw, tpw;
   // Sequences: groups of a workgroup, lanes of a token, tokens at a time, tokens of a workgroup.
   int32_t gpb, lpt, tps, chunk, nChunk;
@@ -41,8 +41,8 @@ struct GroupPlan {
   int lpr, nv;
 };
 GroupPlan group_plan(int64_t Cg, int E);
-// Workgroups along the tokens of the backward over tokens (rows of partial sums).
-int64_t group_token_blocks(int64_t tokens, int64_t G, int64_t Cg, int E, int32_t* gpw, int32_t* tpw);
+// Workgroups along the tokens, each with one row of partial sums in the backward.
+int64_t group_token_blocks(int64_t tokens, int64_t G, int64_t Cg, int E, bool bwd, int32_t* gpw, int32_t* tpw);
 // Sets gpb, lpt, tps, chunk and nChunk.
 void group_sequence_plan(GroupParams* p, int E);
 

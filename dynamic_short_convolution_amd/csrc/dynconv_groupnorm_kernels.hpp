@@ -119,11 +119,27 @@ __device__ __forceinline__ float slope(float n, float w, float b, bool silu, boo
   return dy * d;
 }
 
-// Sum over the LPR lanes of a row, in every one of them. `red`: 4 floats per call site.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+// Sum over the LPR lanes of a row, in every one of them, without LDS up to a wave: lanes 1 and 2 apart
+// within a quad, 4 and 8 apart by mirrors (whose quads and halves are equal by then), 16 and 32
+// apart by swaps. `red`: 4 floats per call site.
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x, float* red) {
-#pragma unroll
-  for (int m = 1; m < (LPR < 64 ? LPR : 64); m <<= 1) x += __shfl_xor(x, m);
+  x += dpp<0xB1>(x);
+  x += dpp<0x4E>(x);
+  if constexpr (LPR >= 8) x += dpp<0x141>(x);
+  if constexpr (LPR >= 16) x += dpp<0x140>(x);
+  if constexpr (LPR >= 32) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  }
+  if constexpr (LPR >= 64) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  }
   if constexpr (LPR == 256) {
     __syncthreads();  // the previous sum is read
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
@@ -147,98 +163,123 @@ __device__ __forceinline__ double row_sum(double x, double* red) {
 
 // ---------------------------------------------------------------------------------
 // Per token. A row (one group of one token) belongs to the fewest lanes that hold it in one 16-byte
-// load each, up to a wave, then 2 or 4 loads, then a workgroup: each input is read once, the mean
-// and the squares around it are two sums over registers. Longer rows are read again.
+// load each (rows without such loads: in at most 4 of one element), up to a wave, then 2 or 4 loads,
+// then a workgroup: each input is read once, the mean and the squares around it are two sums over
+// registers. Longer rows are read again. A workgroup takes gpw neighbouring groups of tpw tokens at a
+// time, a lane the same channels every time, the next tokens' loads under way meanwhile.
 // ---------------------------------------------------------------------------------
+struct Token {
+  int64_t b, t;
+};
+__device__ __forceinline__ Token token_at(const GroupParams& p, int64_t token) {
+  if (p.B == 1) return {0, token};
+  const uint32_t b = uint32_t(token) / uint32_t(p.T);  // below 2^31 tokens
+  return {b, int64_t(uint32_t(token) - b * uint32_t(p.T))};
+}
+
 template <typename ET, int E, int LPR, int NV>
 __global__ __launch_bounds__(kThreads) void k_group_fwd(const GroupParams p) {
+  constexpr int NA = NV > 0 ? NV : 1;
   __shared__ float red[2][4];
   __shared__ double dred[2][4];
-  const int lane = threadIdx.x % LPR;
-  const int64_t row = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR;
-  const int64_t rows = int64_t(p.B) * p.T * p.G;
-  if (row >= rows) return;  // whole rows; with 256 lanes a whole workgroup
-  const int64_t token = row / p.G, b = token / p.T, t = token - b * p.T;
-  const int c0 = int(row - token * p.G) * p.Cg;
+  const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+  const int tsub = slot / p.gpw, gsub = slot - tsub * p.gpw;
+  const int gi = blockIdx.y * p.gpw + gsub;
+  const bool mine = tsub < p.tpw && gi < p.G;
+  const int c0 = (mine ? gi : 0) * p.Cg;
   const bool gated = p.gate.p != nullptr, silu = p.silu != 0;
   const float inv = 1.f / float(p.Cg);
-  const int64_t ox = b * p.x.s0 + t * p.x.s1 + c0, og = b * p.gate.s0 + t * p.gate.s1 + c0;
-  const int64_t oy = b * p.y.s0 + t * p.y.s1 + c0;
+  const int64_t tokens = int64_t(p.B) * p.T, step = int64_t(gridDim.x) * p.tpw;
   auto finish = [&](const float (&x)[E], const float (&g)[E], const float (&w)[E], const float (&bi)[E], float mean,
-                    float rstd, int c) {
+                    float rstd, int64_t off) {
     float y[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) y[e] = value((x[e] - mean) * rstd, w[e], bi[e], silu, gated, g[e]);
-    store<ET>(y, p.y.p, oy + c);
+    store<ET>(y, p.y.p, off);
   };
   if constexpr (NV > 0) {
-    float x[NV][E], g[NV][E], w[NV][E], bi[NV][E];
-    int cc[NV];
+    float w[NA][E], bi[NA][E], nx[NA][E], ng[NA][E];
+    int cc[NA];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {  // lanes past the row read its start and drop it
       const int c = (lane + i * LPR) * E;
-      cc[i] = c < p.Cg ? c : 0;
-      load<ET>(x[i], p.x.p, ox + cc[i]);
+      cc[i] = c0 + (c < p.Cg ? c : 0);
 #pragma unroll
       for (int e = 0; e < E; ++e) w[i][e] = 1.f, bi[i][e] = 0.f;
+      if (p.weight != nullptr) load<ET>(w[i], p.weight, cc[i]);
+      if (p.bias != nullptr) load<ET>(bi[i], p.bias, cc[i]);
     }
-    if (gated) {
+    auto fetch = [&](int64_t tok) {
+      const Token q = token_at(p, tok < tokens ? tok : tokens - 1);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) load<ET>(g[i], p.gate.p, og + cc[i]);
-    }
-    if (p.weight != nullptr) {
+      for (int i = 0; i < NV; ++i) load<ET>(nx[i], p.x.p, q.b * p.x.s0 + q.t * p.x.s1 + cc[i]);
+      if (gated) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) load<ET>(w[i], p.weight, c0 + cc[i]);
-    }
-    if (p.bias != nullptr) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) load<ET>(bi[i], p.bias, c0 + cc[i]);
-    }
-    float sum = 0.f, sq = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if ((lane + i * LPR) * E < p.Cg) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum += x[i][e];
+        for (int i = 0; i < NV; ++i) load<ET>(ng[i], p.gate.p, q.b * p.gate.s0 + q.t * p.gate.s1 + cc[i]);
       }
-    const float mean = row_sum<LPR>(sum, red[0]) * inv;
+    };
+    int64_t tok0 = int64_t(blockIdx.x) * p.tpw;
+    fetch(tok0 + tsub);
+    for (; tok0 < tokens; tok0 += step) {
+      float x[NV][E], g[NV][E];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if ((lane + i * LPR) * E < p.Cg) {
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < E; ++e) sq += (x[i][e] - mean) * (x[i][e] - mean);
+        for (int e = 0; e < E; ++e) x[i][e] = nx[i][e], g[i][e] = ng[i][e];
+      if (tok0 + step < tokens) fetch(tok0 + step + tsub);
+      float sum = 0.f, sq = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if ((lane + i * LPR) * E < p.Cg) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) sum += x[i][e];
+        }
+      const float mean = row_sum<LPR>(sum, red[0]) * inv;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if ((lane + i * LPR) * E < p.Cg) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) sq += (x[i][e] - mean) * (x[i][e] - mean);
+        }
+      const float rstd = 1.f / sqrtf(row_sum<LPR>(sq, red[1]) * inv + p.eps);
+      if (mine && tok0 + tsub < tokens) {
+        const Token q = token_at(p, tok0 + tsub);
+        const int64_t oy = q.b * p.y.s0 + q.t * p.y.s1;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if ((lane + i * LPR) * E < p.Cg) finish(x[i], g[i], w[i], bi[i], mean, rstd, oy + cc[i]);
       }
-    const float rstd = 1.f / sqrtf(row_sum<LPR>(sq, red[1]) * inv + p.eps);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if ((lane + i * LPR) * E < p.Cg) finish(x[i], g[i], w[i], bi[i], mean, rstd, cc[i]);
+    }
   } else {
-    double sum = 0.0, sq = 0.0;  // 64 bits: of any number of channels, and no difference of two of them loses the variance
-    for (int c = lane * E; c < p.Cg; c += LPR * E) {
-      float x[E];
-      load<ET>(x, p.x.p, ox + c);
+    for (int64_t token = blockIdx.x; token < tokens; token += step) {  // one group of one token at a time
+      const Token q = token_at(p, token);
+      const int64_t ox = q.b * p.x.s0 + q.t * p.x.s1 + c0, og = q.b * p.gate.s0 + q.t * p.gate.s1 + c0;
+      double sum = 0.0, sq = 0.0;  // 64 bits: of any number of channels, and no difference of two of them loses the variance
+      for (int c = lane * E; c < p.Cg; c += LPR * E) {
+        float x[E];
+        load<ET>(x, p.x.p, ox + c);
 #pragma unroll
-      for (int e = 0; e < E; ++e) sum += double(x[e]), sq += double(x[e]) * double(x[e]);
-    }
-    const double mean = row_sum<LPR>(sum, dred[0]) / p.Cg;
-    const double var = row_sum<LPR>(sq, dred[1]) / p.Cg - mean * mean;
-    const float rstd = 1.f / sqrtf((var < 0.0 ? 0.f : float(var)) + p.eps);
-    for (int c = lane * E; c < p.Cg; c += LPR * E) {
-      float x[E], g[E], w[E], bi[E];
-      load<ET>(x, p.x.p, ox + c);
-      if (gated) load<ET>(g, p.gate.p, og + c);
+        for (int e = 0; e < E; ++e) sum += double(x[e]), sq += double(x[e]) * double(x[e]);
+      }
+      const double mean = row_sum<LPR>(sum, dred[0]) / p.Cg;
+      const double var = row_sum<LPR>(sq, dred[1]) / p.Cg - mean * mean;
+      const float rstd = 1.f / sqrtf((var < 0.0 ? 0.f : float(var)) + p.eps);
+      for (int c = lane * E; c < p.Cg; c += LPR * E) {
+        float x[E], g[E], w[E], bi[E];
+        load<ET>(x, p.x.p, ox + c);
+        if (gated) load<ET>(g, p.gate.p, og + c);
 #pragma unroll
-      for (int e = 0; e < E; ++e) w[e] = 1.f, bi[e] = 0.f;
-      if (p.weight != nullptr) load<ET>(w, p.weight, c0 + c);
-      if (p.bias != nullptr) load<ET>(bi, p.bias, c0 + c);
-      finish(x, g, w, bi, float(mean), rstd, c);
+        for (int e = 0; e < E; ++e) w[e] = 1.f, bi[e] = 0.f;
+        if (p.weight != nullptr) load<ET>(w, p.weight, c0 + c);
+        if (p.bias != nullptr) load<ET>(bi, p.bias, c0 + c);
+        finish(x, g, w, bi, float(mean), rstd, q.b * p.y.s0 + q.t * p.y.s1 + c0 + c);
+      }
     }
   }
 }
 
-// A workgroup takes gpw neighbouring groups of tpw tokens at a time, a lane the same channels
-// every time, so the sums of the weight's and the bias's gradient stay in its registers; they leave
-// as one partial row per workgroup.
+// The sums of the weight's and the bias's gradient stay in a lane's registers and leave as one partial row per
+// workgroup.
 template <typename ET, int E, int LPR, int NV, bool PACKED>
 __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
   using IT = std::conditional_t<PACKED, i8_t, ET>;
@@ -268,23 +309,34 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
     }
   }
   bool first = true;
-  for (int64_t tok0 = int64_t(blockIdx.x) * p.tpw; tok0 < tokens; tok0 += int64_t(gridDim.x) * p.tpw) {
+  const int64_t step = int64_t(gridDim.x) * p.tpw;
+  float nx[NA][E], ndy[NA][E], ng[NA][E];
+  auto fetch = [&](int64_t tok) {
+    const Token q = token_at(p, tok < tokens ? tok : tokens - 1);
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      load_x<IT, E>(nx[i], p.x, q.b, q.t, c0 + cc[i]);
+      load<ET>(ndy[i], p.dy.p, q.b * p.dy.s0 + q.t * p.dy.s1 + c0 + cc[i]);
+    }
+    if (gated) {
+#pragma unroll
+      for (int i = 0; i < NA; ++i) load<ET>(ng[i], p.gate.p, q.b * p.gate.s0 + q.t * p.gate.s1 + c0 + cc[i]);
+    }
+  };
+  if constexpr (NV > 0) fetch(int64_t(blockIdx.x) * p.tpw + tsub);
+  for (int64_t tok0 = int64_t(blockIdx.x) * p.tpw; tok0 < tokens; tok0 += step) {
     const bool have = mine && tok0 + tsub < tokens;
-    const int64_t token = have ? tok0 + tsub : tokens - 1;
-    const int64_t b = token / p.T, t = token - b * p.T;
+    const Token here = token_at(p, have ? tok0 + tsub : tokens - 1);
+    const int64_t b = here.b, t = here.t;
     const int64_t og = b * p.gate.s0 + t * p.gate.s1 + c0, ody = b * p.dy.s0 + t * p.dy.s1 + c0;
     const int64_t odx = b * p.dx.s0 + t * p.dx.s1 + c0, odg = b * p.dgate.s0 + t * p.dgate.s1 + c0;
     if constexpr (NV > 0) {
       float x[NV][E], dy[NV][E], g[NV][E];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        load_x<IT, E>(x[i], p.x, b, t, c0 + cc[i]);
-        load<ET>(dy[i], p.dy.p, ody + cc[i]);
-      }
-      if (gated) {
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) load<ET>(g[i], p.gate.p, og + cc[i]);
-      }
+        for (int e = 0; e < E; ++e) x[i][e] = nx[i][e], dy[i][e] = ndy[i][e], g[i][e] = ng[i][e];
+      if (tok0 + step < tokens) fetch(tok0 + step + tsub);
       float sum = 0.f, sq = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -677,21 +729,14 @@ __global__ __launch_bounds__(kThreads) void k_group_gradient(const GroupParams p
 // ---------------------------------------------------------------------------------
 template <typename ET, int E, int LPR, int NV>
 hipError_t tokens_nv(const GroupParams& p, bool packed, bool bwd, hipStream_t s) {
-  constexpr int rpb = kThreads / LPR;
+  GroupParams q = p;
+  const int64_t blocks = group_token_blocks(int64_t(p.B) * p.T, p.G, p.Cg, E, bwd, &q.gpw, &q.tpw);
+  const dim3 grid(unsigned(blocks), unsigned((p.G + q.gpw - 1) / q.gpw));
   if (!bwd) {
-    constexpr int64_t most = int64_t(1) << 23;  // a dimension of a launch has fewer than 2^32 threads
-    const int64_t blocks = (int64_t(p.B) * p.T * p.G + rpb - 1) / rpb;
-    const dim3 grid(unsigned(blocks < most ? blocks : most), unsigned((blocks + most - 1) / most));
-    hipLaunchKernelGGL((k_group_fwd<ET, E, LPR, NV>), grid, dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_group_fwd<ET, E, LPR, NV>), grid, dim3(kThreads), 0, s, q);
     return hipGetLastError();
   }
-  int32_t gpw, tpw;
-  const dim3 grid(unsigned(group_token_blocks(int64_t(p.B) * p.T, p.G, p.Cg, E, &gpw, &tpw)),
-                  unsigned((p.G + gpw - 1) / gpw));
-  const size_t lds = NV > 0 && tpw > 1 ? size_t(tpw) * size_t(gpw) * size_t(p.Cg) * sizeof(float) : 0;
-  GroupParams q = p;
-  q.gpw = gpw;
-  q.tpw = tpw;
+  const size_t lds = NV > 0 && q.tpw > 1 ? size_t(q.tpw) * size_t(q.gpw) * size_t(p.Cg) * sizeof(float) : 0;
   if (packed) {
     hipLaunchKernelGGL((k_group_bwd<ET, E, LPR, NV, true>), grid, dim3(kThreads), lds, s, q);
   } else {
@@ -706,14 +751,13 @@ hipError_t tokens_e(const GroupParams& p, bool packed, bool bwd, hipStream_t s) 
   if constexpr (E > 1) {
     if (pl.lpr == 4) return tokens_nv<ET, E, 4, 1>(p, packed, bwd, s);
     if (pl.lpr == 8) return tokens_nv<ET, E, 8, 1>(p, packed, bwd, s);
+    if (pl.lpr == 16) return tokens_nv<ET, E, 16, 1>(p, packed, bwd, s);
     if (pl.lpr == 32) return tokens_nv<ET, E, 32, 1>(p, packed, bwd, s);
+    if (pl.lpr == 64 && pl.nv == 1) return tokens_nv<ET, E, 64, 1>(p, packed, bwd, s);
+  } else {
+    if (pl.lpr == 16) return pl.nv == 2 ? tokens_nv<ET, E, 16, 2>(p, packed, bwd, s) : tokens_nv<ET, E, 16, 4>(p, packed, bwd, s);
   }
-  if (pl.lpr == 16) return tokens_nv<ET, E, 16, 1>(p, packed, bwd, s);
-  if (pl.lpr == 64) {
-    if (pl.nv == 1) return tokens_nv<ET, E, 64, 1>(p, packed, bwd, s);
-    if (pl.nv == 2) return tokens_nv<ET, E, 64, 2>(p, packed, bwd, s);
-    return tokens_nv<ET, E, 64, 4>(p, packed, bwd, s);
-  }
+  if (pl.lpr == 64) return pl.nv == 2 ? tokens_nv<ET, E, 64, 2>(p, packed, bwd, s) : tokens_nv<ET, E, 64, 4>(p, packed, bwd, s);
   if (pl.nv == 2) return tokens_nv<ET, E, 256, 2>(p, packed, bwd, s);
   if (pl.nv == 4) return tokens_nv<ET, E, 256, 4>(p, packed, bwd, s);
   return tokens_nv<ET, E, 256, 0>(p, packed, bwd, s);

@@ -23,9 +23,31 @@ struct PackTensor {
 };
 struct PackParams {
   PackTensor x, codes, scales;
-  int64_t items;  // rows * lanes of a row (whole groups)
-  uint32_t n1, n2, D, perRow;
+  uint32_t rows, n1, n2, D;
+  uint32_t lanes, perBlock, rowBlocks;  // lanes of a row (whole groups); of a workgroup's; rows' workgroups
+  bool flat;                            // the rows of every tensor are n2 apart by one stride
 };
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xf, 0xf, true));
+}
+// The largest of N (8, 16 or 64) neighbouring lanes, in each of them: lanes 1 and 2 apart within a quad, 4
+// and 8 apart by mirrors, 16 and 32 apart by swaps.
+template <int N>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  v = max(v, dpp<0xB1>(v));
+  v = max(v, dpp<0x4E>(v));
+  v = max(v, dpp<0x141>(v));
+  if constexpr (N >= 16) v = max(v, dpp<0x140>(v));
+  if constexpr (N >= 64) {
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max(b[0], b[1]);
+  }
+  return v;
+}
 
 template <int N>
 struct Bytes;
@@ -42,23 +64,28 @@ struct Bytes<8> {
   typedef u32x2 T;
 };
 
-struct At {
-  int64_t i0;
-  uint32_t i1, i2, c;  // c: the lane's first channel
-};
-template <int E>
-__device__ __forceinline__ At place(const PackParams& p, int64_t item) {
-  At a;
-  const uint64_t row = uint64_t(item) / p.perRow;
-  a.c = uint32_t(uint64_t(item) - row * p.perRow) * E;
-  const uint32_t r = uint32_t(row);  // below 2^31
-  const uint32_t q = r / p.n2;
-  a.i2 = r - q * p.n2;
-  a.i0 = q / p.n1;
-  a.i1 = q - uint32_t(a.i0) * p.n1;
-  return a;
+__device__ __forceinline__ int64_t offset(const PackParams& p, const PackTensor& t, uint32_t row) {
+  if (p.flat) return int64_t(row) * t.s2;
+  const uint32_t q = row / p.n2, i0 = q / p.n1;
+  return int64_t(i0) * t.s0 + int64_t(q - i0 * p.n1) * t.s1 + int64_t(row - q * p.n2) * t.s2;
 }
-__device__ __forceinline__ int64_t offset(const PackTensor& t, const At& a) { return a.i0 * t.s0 + a.i1 * t.s1 + a.i2 * t.s2; }
+
+// A lane's place: its columns, and the rows that it goes through.
+template <int E>
+struct Walk {
+  uint32_t c, row, step;
+  bool on;
+  __device__ __forceinline__ explicit Walk(const PackParams& p) {
+    const uint32_t cb = blockIdx.x / p.rowBlocks, rb = blockIdx.x - cb * p.rowBlocks;
+    const uint32_t side = kThreads / p.perBlock, sub = threadIdx.x / p.perBlock;  // rows side by side
+    const uint32_t l = cb * p.perBlock + threadIdx.x - sub * p.perBlock;
+    c = l * E;
+    on = sub < side && l < p.lanes;
+    row = rb * side + sub;
+    step = p.rowBlocks * side;
+  }
+};
+constexpr int kAhead = 4;  // rows whose loads a lane has under way
 
 template <typename ET, int E>
 __device__ __forceinline__ void read(float (&v)[E], const PackTensor& t, int64_t off) {
@@ -83,97 +110,120 @@ __device__ __forceinline__ void read(float (&v)[E], const PackTensor& t, int64_t
 
 template <typename ET, int E>
 __global__ __launch_bounds__(kThreads) void k_pack8(const PackParams p) {
-  const int64_t item = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
-  if (item >= p.items) return;  // whole groups of lanes
-  const At a = place<E>(p, item);
-  float v[E];
+  const Walk<E> me(p);
+  if (!me.on) return;  // whole groups of lanes
+  for (uint32_t row = me.row; row < p.rows; row += kAhead * me.step) {
+    float v[kAhead][E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = 0.f;
-  if (a.c < p.D) read<ET, E>(v, p.x, offset(p.x, a) + a.c);
-  uint32_t top = 0;  // as integers the magnitudes keep their order, and infinities and NaN come last
+    for (int u = 0; u < kAhead; ++u) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+      for (int e = 0; e < E; ++e) v[u][e] = 0.f;
+      const uint32_t r = row + u * me.step;  // below 2^31 + 4 * 2^20
+      if (me.c < p.D) read<ET, E>(v[u], p.x, offset(p, p.x, r < p.rows ? r : row) + me.c);
+    }
 #pragma unroll
-  for (int m = 1; m < kGroup / E; m <<= 1) top = max(top, uint32_t(__shfl_xor(int(top), m)));
-  const int biased = int(top >> 23);
-  const bool lost = biased == 255;
-  const uint32_t scale = lost ? 255u : uint32_t(max(biased - 6, 1));
-  const float inverse = lost ? 0.f : __uint_as_float((254u - scale) << 23);
-  uint32_t code[E];
+    for (int u = 0; u < kAhead; ++u) {
+      const uint32_t r = row + u * me.step;
+      if (r >= p.rows) break;
+      uint32_t top = 0;  // as integers the magnitudes keep their order, and infinities and NaN come last
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float q = fminf(fmaxf(rintf(v[e] * inverse), -127.f), 127.f);
-    code[e] = lost ? 0u : uint32_t(int(q)) & 0xffu;
-  }
-  if (a.c >= p.D) return;
-  if (a.c % kGroup == 0)
-    const_cast<uint8_t*>(static_cast<const uint8_t*>(p.scales.p))[offset(p.scales, a) + a.c / kGroup] = uint8_t(scale);
-  typename Bytes<E>::T w;
-  if constexpr (E == 1) {
-    w = uint8_t(code[0]);
-  } else {
-    uint32_t q[E / 4];
+      for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(v[u][e]) & 0x7fffffffu);
+      top = group_max<kGroup / E>(top);
+      const int biased = int(top >> 23);
+      const bool lost = biased == 255;
+      const uint32_t scale = lost ? 255u : uint32_t(max(biased - 6, 1));
+      const float inverse = lost ? 0.f : __uint_as_float((254u - scale) << 23);
+      uint32_t code[E];
 #pragma unroll
-    for (int i = 0; i < E / 4; ++i)
-      q[i] = code[4 * i] | code[4 * i + 1] << 8 | code[4 * i + 2] << 16 | code[4 * i + 3] << 24;
-    if constexpr (E == 8) {
-      w = u32x2{q[0], q[1]};
-    } else {
-      w = q[0];
+      for (int e = 0; e < E; ++e) {
+        const float q = fminf(fmaxf(rintf(v[u][e] * inverse), -127.f), 127.f);
+        code[e] = lost ? 0u : uint32_t(int(q)) & 0xffu;
+      }
+      if (me.c >= p.D) continue;
+      if (me.c % kGroup == 0)
+        const_cast<uint8_t*>(static_cast<const uint8_t*>(p.scales.p))[offset(p, p.scales, r) + me.c / kGroup] = uint8_t(scale);
+      typename Bytes<E>::T w;
+      if constexpr (E == 1) {
+        w = uint8_t(code[0]);
+      } else {
+        uint32_t q[E / 4];
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i)
+          q[i] = code[4 * i] | code[4 * i + 1] << 8 | code[4 * i + 2] << 16 | code[4 * i + 3] << 24;
+        if constexpr (E == 8) {
+          w = u32x2{q[0], q[1]};
+        } else {
+          w = q[0];
+        }
+      }
+      int8_t* out = const_cast<int8_t*>(static_cast<const int8_t*>(p.codes.p)) + offset(p, p.codes, r) + me.c;
+      *reinterpret_cast<typename Bytes<E>::T*>(out) = w;
     }
   }
-  int8_t* out = const_cast<int8_t*>(static_cast<const int8_t*>(p.codes.p)) + offset(p.codes, a) + a.c;
-  *reinterpret_cast<typename Bytes<E>::T*>(out) = w;
 }
 
 template <typename ET, int E>
 __global__ __launch_bounds__(kThreads) void k_unpack8(const PackParams p) {
-  const int64_t item = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
-  if (item >= p.items) return;
-  const At a = place<E>(p, item);
-  if (a.c >= p.D) return;
-  const uint32_t scale = static_cast<const uint8_t*>(p.scales.p)[offset(p.scales, a) + a.c / kGroup];
-  const float step = __uint_as_float(scale << 23);
-  const auto w = *reinterpret_cast<const typename Bytes<E>::T*>(static_cast<const int8_t*>(p.codes.p) + offset(p.codes, a) + a.c);
-  float v[E];
+  typedef typename Bytes<E>::T Word;
+  const Walk<E> me(p);
+  if (!me.on || me.c >= p.D) return;
+  for (uint32_t row = me.row; row < p.rows; row += kAhead * me.step) {
+    Word w[kAhead];
+    uint32_t scale[kAhead];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    uint32_t word;
-    if constexpr (E == 8) {
-      word = w[e / 4];
-    } else {
-      word = w;
+    for (int u = 0; u < kAhead; ++u) {
+      const uint32_t r = row + u * me.step, s = r < p.rows ? r : row;
+      w[u] = *reinterpret_cast<const Word*>(static_cast<const int8_t*>(p.codes.p) + offset(p, p.codes, s) + me.c);
+      scale[u] = static_cast<const uint8_t*>(p.scales.p)[offset(p, p.scales, s) + me.c / kGroup];
     }
-    v[e] = float(int8_t(word >> (8 * (e % 4)) & 0xff)) * step;
-  }
-  ET* out = const_cast<ET*>(static_cast<const ET*>(p.x.p)) + offset(p.x, a) + a.c;
-  if constexpr (E == 1) {
-    if constexpr (sizeof(ET) == 2) {
-      *reinterpret_cast<uint16_t*>(out) = Cvt<ET>::bits(v[0]);
-    } else {
-      *out = v[0];
-    }
-  } else {
-    u32x4 o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(ET) == 2) {
-        o[i] = Cvt<ET>::pack2(v[2 * i], v[2 * i + 1]);
+    for (int u = 0; u < kAhead; ++u) {
+      const uint32_t r = row + u * me.step;
+      if (r >= p.rows) break;
+      const float step = __uint_as_float(scale[u] << 23);
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        uint32_t word;
+        if constexpr (E == 8) {
+          word = w[u][e / 4];
+        } else {
+          word = w[u];
+        }
+        v[e] = float(int8_t(word >> (8 * (e % 4)) & 0xff)) * step;
+      }
+      ET* out = const_cast<ET*>(static_cast<const ET*>(p.x.p)) + offset(p, p.x, r) + me.c;
+      if constexpr (E == 1) {
+        if constexpr (sizeof(ET) == 2) {
+          *reinterpret_cast<uint16_t*>(out) = Cvt<ET>::bits(v[0]);
+        } else {
+          *out = v[0];
+        }
       } else {
-        o[i] = __float_as_uint(v[i]);
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (sizeof(ET) == 2) {
+            o[i] = Cvt<ET>::pack2(v[2 * i], v[2 * i + 1]);
+          } else {
+            o[i] = __float_as_uint(v[i]);
+          }
+        }
+        *reinterpret_cast<u32x4*>(out) = o;
       }
     }
-    *reinterpret_cast<u32x4*>(out) = o;
   }
 }
 
 template <typename ET, int E>
-hipError_t launch(PackParams p, int64_t rows, bool unpack, hipStream_t s) {
-  p.perRow = (p.D + kGroup - 1) / kGroup * (kGroup / E);
-  p.items = rows * p.perRow;
-  constexpr int64_t most = int64_t(1) << 23;  // a dimension of a launch has fewer than 2^32 threads
-  const int64_t blocks = (p.items + kThreads - 1) / kThreads;
-  const dim3 grid(unsigned(blocks < most ? blocks : most), unsigned((blocks + most - 1) / most));
+hipError_t launch(PackParams p, bool unpack, hipStream_t s) {
+  p.lanes = (p.D + kGroup - 1) / kGroup * (kGroup / E);
+  p.perBlock = p.lanes < kThreads ? p.lanes : kThreads;
+  const uint32_t colBlocks = (p.lanes + p.perBlock - 1) / p.perBlock, side = kThreads / p.perBlock;
+  // eight workgroups per CU, each with at least its first rows
+  const uint32_t need = uint32_t((uint64_t(p.rows) + side - 1) / side), most = colBlocks < 2048 ? 2048 / colBlocks : 1;
+  p.rowBlocks = need < most ? need : most;
+  const dim3 grid(colBlocks * p.rowBlocks);
   if (unpack) {
     hipLaunchKernelGGL((k_unpack8<ET, E>), grid, dim3(kThreads), 0, s, p);
   } else {
@@ -183,8 +233,8 @@ hipError_t launch(PackParams p, int64_t rows, bool unpack, hipStream_t s) {
 }
 
 template <typename ET>
-hipError_t dispatch(const PackParams& p, int64_t rows, bool vec, bool unpack, hipStream_t s) {
-  return vec ? launch<ET, 16 / int(sizeof(ET))>(p, rows, unpack, s) : launch<ET, 1>(p, rows, unpack, s);
+hipError_t dispatch(const PackParams& p, bool vec, bool unpack, hipStream_t s) {
+  return vec ? launch<ET, 16 / int(sizeof(ET))>(p, unpack, s) : launch<ET, 1>(p, unpack, s);
 }
 
 bool aligned(const void* p, int64_t a) { return (reinterpret_cast<uintptr_t>(p) % uint64_t(a)) == 0; }
@@ -204,6 +254,23 @@ dynconv_status take(PackTensor* t, const void* p, const int64_t* s, const int64_
   t->p = p;
   t->s0 = s[0], t->s1 = s[1], t->s2 = s[2];
   return DYNCONV_OK;
+}
+
+// Whether t's rows follow each other by the stride of the last dimension of more than one, which becomes s2.
+bool flat(PackTensor* t, const int64_t* n) {
+  const int64_t s[3] = {t->s0, t->s1, t->s2};
+  int64_t step = 0, count = 1;
+  for (int i = 2; i >= 0; --i) {
+    if (n[i] <= 1) continue;
+    if (count == 1) {
+      step = s[i];
+    } else if (s[i] != step * count) {
+      return false;
+    }
+    count *= n[i];
+  }
+  t->s2 = step;
+  return true;
 }
 
 dynconv_status run(const void* x, const int64_t* xs, const int8_t* codes, const int64_t* cs, const uint8_t* scales,
@@ -231,10 +298,11 @@ dynconv_status run(const void* x, const int64_t* xs, const int8_t* codes, const 
     return DYNCONV_ERR_INVALID_ARG;
   p.n1 = uint32_t(n1), p.n2 = uint32_t(n2), p.D = uint32_t(D);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const int64_t rows = n0 * n1 * n2;
-  const hipError_t e = dtype == DYNCONV_BF16  ? dispatch<bf16_t>(p, rows, vec, unpack, s)
-                       : dtype == DYNCONV_F16 ? dispatch<f16_t>(p, rows, vec, unpack, s)
-                                              : dispatch<float>(p, rows, vec, unpack, s);
+  p.rows = uint32_t(n0 * n1 * n2);
+  p.flat = flat(&p.x, n) && flat(&p.codes, n) && flat(&p.scales, n);
+  const hipError_t e = dtype == DYNCONV_BF16  ? dispatch<bf16_t>(p, vec, unpack, s)
+                       : dtype == DYNCONV_F16 ? dispatch<f16_t>(p, vec, unpack, s)
+                                              : dispatch<float>(p, vec, unpack, s);
   return e == hipSuccess ? DYNCONV_OK : record_hip_error(e);
 }
 

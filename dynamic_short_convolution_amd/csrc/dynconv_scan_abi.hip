@@ -47,7 +47,7 @@ dynconv_status take(ScanTensor* t, const void* p, const int64_t* s, const Sizes&
 
 dynconv_status take_scales(ScanTensor* t, const uint8_t* p, const int64_t* s, const Sizes& z) {
   if (p == nullptr || s == nullptr) return DYNCONV_ERR_INVALID_ARG;
-  if (s[0] < 0 || s[1] < 0 || (z.D > kScanCols && s[2] != 1)) return DYNCONV_ERR_UNSUPPORTED;
+  if (s[0] < 0 || s[1] < 0 || (z.D > kScanScaleCols && s[2] != 1)) return DYNCONV_ERR_UNSUPPORTED;
   if (z.T > 1 && s[1] >= kScanMaxTokenStride) return DYNCONV_ERR_UNSUPPORTED;
   t->sc = p;
   t->c0 = s[0];

@@ -127,6 +127,7 @@ constexpr uint32_t kNowhere = 0x80000000u;  // an offset behind every buffer's r
 template <int V>
 struct Lane {
   static constexpr int kLanes = kScanCols / V;  // lanes side by side over the channels
+  static constexpr int kGroups = 64 / kLanes;
   int wave, group, run, chl;                    // run: index of the lane group's run in the tile
   bool ok;                                      // the channels exist
   int cg;                                       // the first of them, or the tensor's last
@@ -134,7 +135,7 @@ struct Lane {
     const int lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     group = lane / kLanes;
-    run = wave * V + group;
+    run = wave * kGroups + group;
     chl = (lane % kLanes) * V;
     ok = c0 + chl < D;
     cg = ok ? c0 + chl : D - V;
@@ -204,7 +205,7 @@ struct Scales {
     const int which = threadIdx.x / kScanTile, row = min(int(threadIdx.x % kScanTile), last);
     const ScanTensor& t = which == 0 ? p.x : which == 1 ? p.decay : p.gate;
     held = 0;
-    if (which < 3 && t.sc != nullptr) held = t.sc[b * t.c0 + (t0 + row) * t.c1 + c0 / kScanCols];
+    if (which < 3 && t.sc != nullptr) held = t.sc[b * t.c0 + (t0 + row) * t.c1 + c0 / kScanScaleCols];
   }
   __device__ __forceinline__ void put(uint8_t (&to)[3][kScanTile]) const {
     const int which = threadIdx.x / kScanTile;
@@ -252,6 +253,35 @@ __device__ __forceinline__ float through(float A, float H, float h) {
 template <bool DOCS>
 __device__ __forceinline__ float chain(float A, float B) {  // of two maps' factors
   return DOCS ? (A == 0.f ? 0.f : A * B) : A * B;
+}
+
+// Of the lane groups of a wave, one behind the other: the maps (A, H) become those of the group and all
+// before it (or, REVERSE, behind it), and (pA, pH) those without its own.
+template <int V, bool DOCS, bool REVERSE>
+__device__ __forceinline__ void scan_groups(const Lane<V>& me, float (&A)[V], float (&H)[V], float (&pA)[V], float (&pH)[V]) {
+  constexpr int kLanes = Lane<V>::kLanes, kGroups = Lane<V>::kGroups;
+  auto from = [&](float v, int d) { return REVERSE ? __shfl_down(v, d * kLanes) : __shfl_up(v, d * kLanes); };
+  const int rank = REVERSE ? kGroups - 1 - me.group : me.group;
+#pragma unroll
+  for (int d = 1; d < kGroups; d *= 2) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float oA = from(A[i], d), oH = from(H[i], d);
+      const float h = through<DOCS>(A[i], H[i], oH), a = chain<DOCS>(A[i], oA);
+      H[i] = rank >= d ? h : H[i];
+      A[i] = rank >= d ? a : A[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    pA[i] = 1.f;
+    pH[i] = 0.f;
+    if constexpr (kGroups > 1) {
+      const float oA = from(A[i], 1), oH = from(H[i], 1);
+      pA[i] = rank > 0 ? oA : 1.f;
+      pH[i] = rank > 0 ? oH : 0.f;
+    }
+  }
 }
 
 // The maps of the waves in LDS, read in pieces of a lane's channels.
@@ -395,23 +425,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
         H[i] = through<DOCS>(a[j][i], u[j][i], H[i]);
         A[i] = chain<DOCS>(a[j][i], A[i]);
       }
-    // the wave's map: its lane groups' one behind the other
-    float pA[V], pH[V];  // the map of the lane group before this one
-#pragma unroll
-    for (int i = 0; i < V; ++i) pA[i] = 1.f, pH[i] = 0.f;
-    if constexpr (V == 2) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float oA = __shfl_xor(A[i], 32), oH = __shfl_xor(H[i], 32);
-        const float A0 = me.group ? oA : A[i], H0 = me.group ? oH : H[i];
-        const float A1 = me.group ? A[i] : oA, H1 = me.group ? H[i] : oH;
-        pA[i] = me.group ? A0 : 1.f;
-        pH[i] = me.group ? H0 : 0.f;
-        A[i] = chain<DOCS>(A1, A0);
-        H[i] = through<DOCS>(A1, H1, H0);
-      }
-    }
-    if (me.group == 0) {
+    float pA[V], pH[V];  // the map of the lane groups before this one
+    scan_groups<V, DOCS, false>(me, A, H, pA, pH);
+    if (me.group == Lane<V>::kGroups - 1) {
       write_map<V>(maps[k & 1][0][me.wave], me.chl, A);
       write_map<V>(maps[k & 1][1][me.wave], me.chl, H);
     }
@@ -423,13 +439,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
       }
     }
     __syncthreads();  // what is overwritten next was read before the barrier before
-    if constexpr (!MAPS) {
-      if (p.chunks != nullptr && me.wave == 0 && me.group == 0 && me.ok) {
-        float* out = p.chunks + (int64_t(b) * nTiles + k) * p.D + cg;
-#pragma unroll
-        for (int i = 0; i < V; ++i) out[i] = carry[i];
-      }
-    }
     float h[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) h[i] = carry[i];
@@ -446,6 +455,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
       }
     }
     if constexpr (!MAPS) {
+      const int row = me.run * L;
+      if (p.chunks != nullptr && me.group == 0 && row % kScanChunk == 0 && row <= last && me.ok) {
+        const int nC = (p.T + kScanChunk - 1) / kScanChunk;
+        float* out = p.chunks + (int64_t(b) * nC + (t0 + row) / kScanChunk) * p.D + cg;
+#pragma unroll
+        for (int i = 0; i < V; ++i) out[i] = h[i];
+      }
       if (p.y.p != nullptr) {
         const __amdgpu_buffer_rsrc_t ry = py.rows(p.y, b, t0, c0, last, p.D);
 #pragma unroll
@@ -635,31 +651,17 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
     for (int j = L - 1; j >= 0; --j)
 #pragma unroll
       for (int i = 0; i < V; ++i) E[i] = chain<DOCS>(pass(j, i), dy[j][i] + E[i]);
-    float pA[V], pH[V], pE[V];  // of the other lane group
+    float pA[V], pH[V], rA[V], rE[V], B[V];  // the maps of the lane groups before and behind this one
 #pragma unroll
-    for (int i = 0; i < V; ++i) pA[i] = 1.f, pH[i] = 0.f, pE[i] = 0.f;
-    if constexpr (V == 2) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float oA = __shfl_xor(A[i], 32), oE = __shfl_xor(E[i], 32);
-        const float A0 = me.group ? oA : A[i], A1 = me.group ? A[i] : oA;
-        const float E0 = me.group ? oE : E[i], E1 = me.group ? E[i] : oE;
-        pA[i] = oA;
-        pE[i] = oE;
-        A[i] = chain<DOCS>(A1, A0);
-        E[i] = through<DOCS>(A0, E0, E1);
-        if constexpr (!MAPS) {
-          const float oH = __shfl_xor(H[i], 32);
-          const float H0 = me.group ? oH : H[i], H1 = me.group ? H[i] : oH;
-          pH[i] = oH;
-          H[i] = through<DOCS>(A1, H1, H0);
-        }
-      }
-    }
+    for (int i = 0; i < V; ++i) B[i] = A[i];
+    scan_groups<V, DOCS, true>(me, B, E, rA, rE);
     if (me.group == 0) {
-      write_map<V>(maps[k & 1][0][me.wave], me.chl, A);
+      write_map<V>(maps[k & 1][0][me.wave], me.chl, B);
       write_map<V>(maps[k & 1][1][me.wave], me.chl, E);
-      if constexpr (!MAPS) write_map<V>(maps[k & 1][2][me.wave], me.chl, H);
+    }
+    if constexpr (!MAPS) {
+      scan_groups<V, DOCS, false>(me, A, H, pA, pH);
+      if (me.group == Lane<V>::kGroups - 1) write_map<V>(maps[k & 1][2][me.wave], me.chl, H);
     }
     if (k > k0) {
       if constexpr (DOCS) Starts::make(p, b, (k - 1) * kScanTile, starts[(k - 1) & 1]);
@@ -693,13 +695,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) h[i] = q < me.wave ? through<DOCS>(fA[i], fH[i], h[i]) : h[i];
       }
-      if constexpr (V == 2) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float hn = through<DOCS>(pA[i], pH[i], h[i]), en = through<DOCS>(pA[i], pE[i], e[i]);
-          h[i] = me.group ? hn : h[i];
-          e[i] = me.group ? e[i] : en;
-        }
+      for (int i = 0; i < V; ++i) {
+        h[i] = through<DOCS>(pA[i], pH[i], h[i]);
+        e[i] = through<DOCS>(rA[i], rE[i], e[i]);
       }
 #pragma unroll
       for (int j = 0; j < L; ++j)
@@ -750,7 +749,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
     __shared__ double sums[kScanWaves][kScanCols];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if constexpr (V == 2) drate[i] += __shfl_xor(drate[i], 32);
+#pragma unroll
+      for (int m = Lane<V>::kLanes; m < 64; m *= 2) drate[i] += __shfl_xor(drate[i], m);
       if (me.group == 0) sums[me.wave][me.chl + i] = drate[i];
     }
     __syncthreads();
