@@ -86,13 +86,8 @@ hipError_t group_sum(const float* part, int64_t n, int64_t C, int64_t batches, f
 
 GroupPlan group_plan(int64_t Cg, int E) {
   const int64_t loads = (Cg + E - 1) / E;  // of the row
-  if (E > 1) {
-    for (int lpr : {4, 8, 16, 32, 64})
-      if (loads <= lpr) return {lpr, 1};
-  } else {
-    if (loads <= 32) return {16, 2};
-    if (loads <= 64) return {16, 4};
-  }
+  for (int lpr : {4, 8, 16, 32, 64})
+    if (loads <= lpr) return {lpr, 1};
   if (loads <= 128) return {64, 2};
   if (loads <= 256) return {64, 4};
   if (loads <= 512) return {256, 2};
@@ -115,6 +110,7 @@ int64_t group_token_blocks(int64_t tokens, int64_t G, int64_t Cg, int E, bool bw
 
 void group_sequence_plan(GroupParams* p, int E) {
   const int lanes = (p->Cg + E - 1) / E;
+  p->lpg = lanes;
   p->gpb = lanes >= kThreads ? 1 : (p->G < kThreads / lanes ? p->G : kThreads / lanes);
   p->lpt = lanes >= kThreads ? kThreads : p->gpb * lanes;
   p->tps = kThreads / p->lpt;
@@ -152,21 +148,21 @@ dynconv_status check_sizes(const Sizes& z, dynconv_dtype dt, float eps) {
 bool empty(const Sizes& z) { return z.B == 0 || z.T == 0 || z.C == 0; }
 
 dynconv_status take(GroupTensor* t, const void* p, const int64_t* s, const Sizes& z, int eb, int piece, bool output,
-                    bool* vec) {
+                    bool* whole) {
   if (p == nullptr || s == nullptr) return DYNCONV_ERR_INVALID_ARG;
   if (!aligned(p, eb) || (z.C > 1 && s[2] != 1) || s[0] < 0 || s[1] < 0) return DYNCONV_ERR_UNSUPPORTED;
   if (output && ((z.B > 1 && s[0] == 0) || (z.T > 1 && s[1] == 0))) return DYNCONV_ERR_INVALID_ARG;
-  if (!aligned(p, piece) || (z.B > 1 && s[0] * eb % piece != 0) || (z.T > 1 && s[1] * eb % piece != 0)) *vec = false;
+  if (!aligned(p, piece) || (z.B > 1 && s[0] * eb % piece != 0) || (z.T > 1 && s[1] * eb % piece != 0)) *whole = false;
   t->p = p;
   t->s0 = s[0];
   t->s1 = s[1];
   return DYNCONV_OK;
 }
 
-dynconv_status take_vector(const void* w, int eb, bool* vec) {
+dynconv_status take_vector(const void* w, int eb, bool* whole) {
   if (w == nullptr) return DYNCONV_OK;
   if (!aligned(w, eb)) return DYNCONV_ERR_UNSUPPORTED;
-  if (!aligned(w, 16)) *vec = false;
+  if (!aligned(w, 16)) *whole = false;
   return DYNCONV_OK;
 }
 
@@ -208,27 +204,21 @@ Space space(const Sizes& z, int E, bool bwd, bool stats) {
   }
   return w;
 }
-size_t space_max(const Sizes& z, dynconv_dtype dt, bool bwd, bool stats) {
-  const size_t a = space(z, 1, bwd, stats).total();
-  const int E = 16 / elem_bytes(dt);
-  const size_t b = z.C / z.G % E == 0 ? space(z, E, bwd, stats).total() : 0;
-  return a > b ? a : b;
-}
 
-hipError_t tokens(const GroupParams& p, dynconv_dtype dt, bool vec, bool packed, bool bwd, hipStream_t s) {
-  return dt == DYNCONV_BF16  ? group_tokens_bf16(p, vec, packed, bwd, s)
-         : dt == DYNCONV_F16 ? group_tokens_f16(p, vec, packed, bwd, s)
-                             : group_tokens_f32(p, vec, packed, bwd, s);
+hipError_t tokens(const GroupParams& p, dynconv_dtype dt, bool whole, bool packed, bool bwd, hipStream_t s) {
+  return dt == DYNCONV_BF16  ? group_tokens_bf16(p, whole, packed, bwd, s)
+         : dt == DYNCONV_F16 ? group_tokens_f16(p, whole, packed, bwd, s)
+                             : group_tokens_f32(p, whole, packed, bwd, s);
 }
-hipError_t sequences(const GroupParams& p, dynconv_dtype dt, bool vec, bool packed, GroupStage stage, hipStream_t s) {
-  return dt == DYNCONV_BF16  ? group_sequences_bf16(p, vec, packed, stage, s)
-         : dt == DYNCONV_F16 ? group_sequences_f16(p, vec, packed, stage, s)
-                             : group_sequences_f32(p, vec, packed, stage, s);
+hipError_t sequences(const GroupParams& p, dynconv_dtype dt, bool whole, bool packed, GroupStage stage, hipStream_t s) {
+  return dt == DYNCONV_BF16  ? group_sequences_bf16(p, whole, packed, stage, s)
+         : dt == DYNCONV_F16 ? group_sequences_f16(p, whole, packed, stage, s)
+                             : group_sequences_f32(p, whole, packed, stage, s);
 }
 
 // Mean and scale of every (sequence, group) into p.stats.
-hipError_t statistics(const GroupParams& p, dynconv_dtype dt, bool vec, bool packed, hipStream_t s) {
-  const hipError_t e = sequences(p, dt, vec, packed, kGroupStats, s);
+hipError_t statistics(const GroupParams& p, dynconv_dtype dt, bool whole, bool packed, hipStream_t s) {
+  const hipError_t e = sequences(p, dt, whole, packed, kGroupStats, s);
   if (e != hipSuccess) return e;
   const int64_t waves = int64_t(p.B) * p.G;
   hipLaunchKernelGGL(k_group_finish, dim3(unsigned((waves + 3) / 4)), dim3(kThreads), 0, s, p);
@@ -249,7 +239,7 @@ size_t dynconv_groupnorm_fwd_workspace_size(int64_t B, int64_t T, int64_t C, int
                                             int32_t with_stats, dynconv_dtype dtype) {
   const Sizes z{B, T, C, groups, over_sequence != 0};
   if (check_sizes(z, dtype, 0.f) != DYNCONV_OK || empty(z)) return 0;
-  return space_max(z, dtype, false, with_stats != 0);
+  return space(z, 16 / elem_bytes(dtype), false, with_stats != 0).total();
 }
 
 dynconv_status dynconv_groupnorm_fwd(const void* x, const int64_t* xs, const void* weight, const void* bias,
@@ -263,29 +253,29 @@ dynconv_status dynconv_groupnorm_fwd(const void* x, const int64_t* xs, const voi
   if (!z.sequence && (lengths != nullptr || stats != nullptr)) return DYNCONV_ERR_INVALID_ARG;
   if (empty(z)) return DYNCONV_OK;
   const int eb = elem_bytes(dtype), E = 16 / eb;
-  bool vec = C / groups % E == 0;
+  bool whole = C / groups % E == 0;
   GroupTensor tx{}, tg{}, ty{};
-  if ((st = take(&tx, x, xs, z, eb, 16, false, &vec)) != DYNCONV_OK) return st;
-  if (gate != nullptr && (st = take(&tg, gate, gs, z, eb, 16, false, &vec)) != DYNCONV_OK) return st;
-  if ((st = take(&ty, y, ys, z, eb, 16, true, &vec)) != DYNCONV_OK) return st;
-  if ((st = take_vector(weight, eb, &vec)) != DYNCONV_OK || (st = take_vector(bias, eb, &vec)) != DYNCONV_OK) return st;
+  if ((st = take(&tx, x, xs, z, eb, 16, false, &whole)) != DYNCONV_OK) return st;
+  if (gate != nullptr && (st = take(&tg, gate, gs, z, eb, 16, false, &whole)) != DYNCONV_OK) return st;
+  if ((st = take(&ty, y, ys, z, eb, 16, true, &whole)) != DYNCONV_OK) return st;
+  if ((st = take_vector(weight, eb, &whole)) != DYNCONV_OK || (st = take_vector(bias, eb, &whole)) != DYNCONV_OK) return st;
   if (!aligned(lengths, 4) || !aligned(stats, 4)) return DYNCONV_ERR_UNSUPPORTED;
   if (any_equal(y, {x, weight, bias, gate, lengths, stats}) || any_equal(stats, {x, weight, bias, gate, lengths}))
     return DYNCONV_ERR_INVALID_ARG;
-  GroupParams p = sized(z, vec ? E : 1);
+  GroupParams p = sized(z, E);
   p.x = tx, p.gate = tg, p.y = ty;
   p.weight = weight, p.bias = bias, p.lengths = lengths;
   p.silu = silu != 0;
   p.eps = eps;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (!z.sequence) return done(tokens(p, dtype, vec, false, false, s));
-  const Space w = space(z, vec ? E : 1, false, stats != nullptr);
+  if (!z.sequence) return done(tokens(p, dtype, whole, false, false, s));
+  const Space w = space(z, E, false, stats != nullptr);
   if (workspace == nullptr || workspace_bytes < w.total()) return DYNCONV_ERR_WORKSPACE;
   if (!aligned(workspace, 8)) return DYNCONV_ERR_UNSUPPORTED;
   p.part = static_cast<double*>(workspace);
   p.stats = stats != nullptr ? stats : reinterpret_cast<float*>(static_cast<char*>(workspace) + w.part);
-  hipError_t e = statistics(p, dtype, vec, false, s);
-  if (e == hipSuccess) e = sequences(p, dtype, vec, false, kGroupApply, s);
+  hipError_t e = statistics(p, dtype, whole, false, s);
+  if (e == hipSuccess) e = sequences(p, dtype, whole, false, kGroupApply, s);
   return done(e);
 }
 
@@ -293,7 +283,7 @@ size_t dynconv_groupnorm_bwd_workspace_size(int64_t B, int64_t T, int64_t C, int
                                             int32_t with_stats, dynconv_dtype dtype) {
   const Sizes z{B, T, C, groups, over_sequence != 0};
   if (check_sizes(z, dtype, 0.f) != DYNCONV_OK || empty(z)) return 0;
-  return space_max(z, dtype, true, with_stats != 0);
+  return space(z, 16 / elem_bytes(dtype), true, with_stats != 0).total();
 }
 
 dynconv_status dynconv_groupnorm_bwd(const void* x, const int64_t* xs, const uint8_t* x_scales, const int64_t* xcs,
@@ -321,10 +311,10 @@ dynconv_status dynconv_groupnorm_bwd(const void* x, const int64_t* xs, const uin
     return done(group_sum(nullptr, 0, C, 1, dweight, dbias, 0, s));
   }
   const int eb = elem_bytes(dtype), E = 16 / eb;
-  bool vec = C / groups % E == 0;
+  bool whole = C / groups % E == 0;
   const bool packed = x_scales != nullptr;
   GroupTensor tx{}, tg{}, tdy{}, tdx{}, tdg{};
-  if ((st = take(&tx, x, xs, z, packed ? 1 : eb, packed ? E : 16, false, &vec)) != DYNCONV_OK) return st;
+  if ((st = take(&tx, x, xs, z, packed ? 1 : eb, packed ? E : 16, false, &whole)) != DYNCONV_OK) return st;
   if (packed) {
     if (xcs == nullptr) return DYNCONV_ERR_INVALID_ARG;
     if (xcs[0] < 0 || xcs[1] < 0 || (C > 64 && xcs[2] != 1)) return DYNCONV_ERR_UNSUPPORTED;
@@ -332,20 +322,20 @@ dynconv_status dynconv_groupnorm_bwd(const void* x, const int64_t* xs, const uin
     tx.c0 = xcs[0];
     tx.c1 = xcs[1];
   }
-  if (gate != nullptr && (st = take(&tg, gate, gs, z, eb, 16, false, &vec)) != DYNCONV_OK) return st;
-  if ((st = take(&tdy, dy, dys, z, eb, 16, false, &vec)) != DYNCONV_OK) return st;
-  if ((st = take(&tdx, dx, dxs, z, eb, 16, true, &vec)) != DYNCONV_OK) return st;
+  if (gate != nullptr && (st = take(&tg, gate, gs, z, eb, 16, false, &whole)) != DYNCONV_OK) return st;
+  if ((st = take(&tdy, dy, dys, z, eb, 16, false, &whole)) != DYNCONV_OK) return st;
+  if ((st = take(&tdx, dx, dxs, z, eb, 16, true, &whole)) != DYNCONV_OK) return st;
   if ((gate != nullptr) != (dgate != nullptr)) return DYNCONV_ERR_INVALID_ARG;
-  if (gate != nullptr && (st = take(&tdg, dgate, dgs, z, eb, 16, true, &vec)) != DYNCONV_OK) return st;
-  if ((st = take_vector(weight, eb, &vec)) != DYNCONV_OK || (st = take_vector(bias, eb, &vec)) != DYNCONV_OK) return st;
+  if (gate != nullptr && (st = take(&tdg, dgate, dgs, z, eb, 16, true, &whole)) != DYNCONV_OK) return st;
+  if ((st = take_vector(weight, eb, &whole)) != DYNCONV_OK || (st = take_vector(bias, eb, &whole)) != DYNCONV_OK) return st;
   if (!aligned(lengths, 4) || !aligned(stats, 4)) return DYNCONV_ERR_UNSUPPORTED;
-  GroupParams p = sized(z, vec ? E : 1);
+  GroupParams p = sized(z, E);
   p.x = tx, p.gate = tg, p.dy = tdy, p.dx = tdx, p.dgate = tdg;
   p.weight = weight, p.bias = bias, p.lengths = lengths;
   p.silu = silu != 0;
   p.eps = eps;
   const bool params = dweight != nullptr || dbias != nullptr;
-  const Space w = space(z, vec ? E : 1, true, stats != nullptr);
+  const Space w = space(z, E, true, stats != nullptr);
   char* at = static_cast<char*>(workspace);
   if (z.sequence || params) {
     if (workspace == nullptr || workspace_bytes < w.total()) return DYNCONV_ERR_WORKSPACE;
@@ -357,21 +347,21 @@ dynconv_status dynconv_groupnorm_bwd(const void* x, const int64_t* xs, const uin
   hipError_t e;
   if (!z.sequence) {
     int32_t gpw, tpw;
-    e = tokens(p, dtype, vec, packed, true, s);
+    e = tokens(p, dtype, whole, packed, true, s);
     if (e == hipSuccess && params)
-      e = group_sum(p.colpart, group_token_blocks(B * T, groups, p.Cg, vec ? E : 1, true, &gpw, &tpw), C, 1, dweight, dbias, 0, s);
+      e = group_sum(p.colpart, group_token_blocks(B * T, groups, p.Cg, E, true, &gpw, &tpw), C, 1, dweight, dbias, 0, s);
     return done(e);
   }
   if (stats != nullptr) {
     p.stats = const_cast<float*>(stats);
   } else {
     p.stats = reinterpret_cast<float*>(at + w.part);
-    if ((e = statistics(p, dtype, vec, packed, s)) != hipSuccess) return done(e);
+    if ((e = statistics(p, dtype, whole, packed, s)) != hipSuccess) return done(e);
   }
-  e = sequences(p, dtype, vec, packed, kGroupColumns, s);
+  e = sequences(p, dtype, whole, packed, kGroupColumns, s);
   if (e == hipSuccess) e = group_sum(p.colpart, p.nChunk, C, B, p.colsum, p.colsum + C, 2 * C, s);
   if (e == hipSuccess && params) e = group_sum(p.colsum, B, C, 1, dweight, dbias, 0, s);
-  if (e == hipSuccess) e = sequences(p, dtype, vec, packed, kGroupGradient, s);
+  if (e == hipSuccess) e = sequences(p, dtype, whole, packed, kGroupGradient, s);
   return done(e);
 }
 

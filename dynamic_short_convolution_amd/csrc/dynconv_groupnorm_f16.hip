@@ -3,11 +3,11 @@
 
 namespace dynconv {
 
-hipError_t group_tokens_f16(const GroupParams& p, bool vec, bool packed, bool bwd, hipStream_t s) {
-  return group::tokens<f16_t>(p, vec, packed, bwd, s);
+hipError_t group_tokens_f16(const GroupParams& p, bool whole, bool packed, bool bwd, hipStream_t s) {
+  return group::tokens<f16_t>(p, whole, packed, bwd, s);
 }
-hipError_t group_sequences_f16(const GroupParams& p, bool vec, bool packed, GroupStage stage, hipStream_t s) {
-  return group::sequences<f16_t>(p, vec, packed, stage, s);
+hipError_t group_sequences_f16(const GroupParams& p, bool whole, bool packed, GroupStage stage, hipStream_t s) {
+  return group::sequences<f16_t>(p, whole, packed, stage, s);
 }
 
 }  // namespace dynconv

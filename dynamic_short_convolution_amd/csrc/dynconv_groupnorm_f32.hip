@@ -3,11 +3,11 @@
 
 namespace dynconv {
 
-hipError_t group_tokens_f32(const GroupParams& p, bool vec, bool packed, bool bwd, hipStream_t s) {
-  return group::tokens<float>(p, vec, packed, bwd, s);
+hipError_t group_tokens_f32(const GroupParams& p, bool whole, bool packed, bool bwd, hipStream_t s) {
+  return group::tokens<float>(p, whole, packed, bwd, s);
 }
-hipError_t group_sequences_f32(const GroupParams& p, bool vec, bool packed, GroupStage stage, hipStream_t s) {
-  return group::sequences<float>(p, vec, packed, stage, s);
+hipError_t group_sequences_f32(const GroupParams& p, bool whole, bool packed, GroupStage stage, hipStream_t s) {
+  return group::sequences<float>(p, whole, packed, stage, s);
 }
 
 }  // namespace dynconv

@@ -23,50 +23,58 @@ struct i8_t {
   int8_t bits;
 };
 
-// E consecutive elements (16 bytes of the storage type, or one); codes of 8 bits as integers.
-template <typename ET, int E>
-__device__ __forceinline__ void load(float (&v)[E], const void* base, int64_t off) {
+// Words of a piece at the alignment of its elements (global memory takes 16 bytes at any).
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef u32x2 __attribute__((aligned(1))) u32x2_any;
+typedef uint32_t __attribute__((aligned(1))) u32_any;
+
+// A piece: E consecutive elements, 16 bytes of the storage type (codes of 8 bits as integers). WHOLE:
+// aligned, all of them a row's; else the first n are, the others read as zero and are not written.
+template <typename ET, int E, bool WHOLE>
+__device__ __forceinline__ void load(float (&v)[E], const void* base, int64_t off, int n) {
   const ET* p = static_cast<const ET*>(base) + off;
-  if constexpr (E == 1) {
+  if (WHOLE || n >= E) {
     if constexpr (sizeof(ET) == 1) {
-      v[0] = float(*reinterpret_cast<const int8_t*>(p));
-    } else if constexpr (sizeof(ET) == 2) {
-      v[0] = Cvt<ET>::of_bits(*reinterpret_cast<const uint16_t*>(p));
-    } else {
-      v[0] = *p;
-    }
-  } else if constexpr (sizeof(ET) == 1) {
-    uint32_t w[E / 4];
-    if constexpr (E == 8) {
-      const u32x2 q = *reinterpret_cast<const u32x2*>(p);
-      w[0] = q[0], w[1] = q[1];
-    } else {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
-    }
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = float(int8_t(w[i / 4] >> (8 * (i % 4)) & 0xff));
-  } else {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(ET) == 2) {
-        v[2 * i] = Cvt<ET>::lo(w[i]), v[2 * i + 1] = Cvt<ET>::hi(w[i]);
+      uint32_t w[E / 4];
+      if constexpr (E == 8) {
+        const u32x2 q = WHOLE ? *reinterpret_cast<const u32x2*>(p) : *reinterpret_cast<const u32x2_any*>(p);
+        w[0] = q[0], w[1] = q[1];
       } else {
-        v[i] = __uint_as_float(w[i]);
+        w[0] = WHOLE ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const u32_any*>(p);
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = float(int8_t(w[i / 4] >> (8 * (i % 4)) & 0xff));
+    } else {
+      const u32x4 w = WHOLE ? *reinterpret_cast<const u32x4*>(p) : *reinterpret_cast<const u32x4_any*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(ET) == 2) {
+          v[2 * i] = Cvt<ET>::lo(w[i]), v[2 * i + 1] = Cvt<ET>::hi(w[i]);
+        } else {
+          v[i] = __uint_as_float(w[i]);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      v[e] = 0.f;
+      if (e < n) {
+        if constexpr (sizeof(ET) == 1) {
+          v[e] = float(*reinterpret_cast<const int8_t*>(p + e));
+        } else if constexpr (sizeof(ET) == 2) {
+          v[e] = Cvt<ET>::of_bits(*reinterpret_cast<const uint16_t*>(p + e));
+        } else {
+          v[e] = p[e];
+        }
       }
     }
   }
 }
-template <typename ET, int E>
-__device__ __forceinline__ void store(const float (&v)[E], const void* base, int64_t off) {
+template <typename ET, int E, bool WHOLE>
+__device__ __forceinline__ void store(const float (&v)[E], const void* base, int64_t off, int n) {
   ET* p = const_cast<ET*>(static_cast<const ET*>(base)) + off;
-  if constexpr (E == 1) {
-    if constexpr (sizeof(ET) == 2) {
-      *reinterpret_cast<uint16_t*>(p) = Cvt<ET>::bits(v[0]);
-    } else {
-      *p = v[0];
-    }
-  } else {
+  if (WHOLE || n >= E) {
     u32x4 w;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -76,18 +84,36 @@ __device__ __forceinline__ void store(const float (&v)[E], const void* base, int
         w[i] = __float_as_uint(v[i]);
       }
     }
-    *reinterpret_cast<u32x4*>(p) = w;
+    if constexpr (WHOLE) {
+      *reinterpret_cast<u32x4*>(p) = w;
+    } else {
+      *reinterpret_cast<u32x4_any*>(p) = w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (e < n) {
+        if constexpr (sizeof(ET) == 2) {
+          *reinterpret_cast<uint16_t*>(p + e) = Cvt<ET>::bits(v[e]);
+        } else {
+          p[e] = v[e];
+        }
+      }
   }
 }
 
-// A token's E channels from c (of x: in 8 bits with their scale; E channels share one).
-template <typename IT, int E>
-__device__ __forceinline__ void load_x(float (&v)[E], const GroupTensor& t, int64_t b, int64_t tok, int64_t c) {
-  load<IT, E>(v, t.p, b * t.s0 + tok * t.s1 + c);
+// A token's piece of x from channel c on; in 8 bits with its scale (of WHOLE pieces one, else up to two).
+template <typename IT, int E, bool WHOLE>
+__device__ __forceinline__ void load_x(float (&v)[E], const GroupTensor& t, int64_t b, int64_t tok, int64_t c, int n) {
+  load<IT, E, WHOLE>(v, t.p, b * t.s0 + tok * t.s1 + c, n);
   if constexpr (sizeof(IT) == 1) {
-    const float step = __uint_as_float(uint32_t(t.sc[b * t.c0 + tok * t.c1 + c / kScaleGroup]) << 23);
+    if (!WHOLE && n <= 0) return;
+    const uint8_t* sc = t.sc + (b * t.c0 + tok * t.c1);
+    const float step = __uint_as_float(uint32_t(sc[c / kScaleGroup]) << 23);
+    const int64_t end = WHOLE ? c : c + (n < E ? n : E) - 1;
+    const float next = WHOLE ? step : __uint_as_float(uint32_t(sc[end / kScaleGroup]) << 23);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] *= step;
+    for (int e = 0; e < E; ++e) v[e] *= WHOLE || (c + e) / kScaleGroup == c / kScaleGroup ? step : next;
   }
 }
 
@@ -163,8 +189,7 @@ __device__ __forceinline__ double row_sum(double x, double* red) {
 
 // ---------------------------------------------------------------------------------
 // Per token. A row (one group of one token) belongs to the fewest lanes that hold it in one 16-byte
-// load each (rows without such loads: in at most 4 of one element), up to a wave, then 2 or 4 loads,
-// then a workgroup: each input is read once, the mean and the squares around it are two sums over
+// piece each, up to a wave, then 2 or 4 pieces, then a workgroup: each input is read once, the mean and the squares around it are two sums over
 // registers. Longer rows are read again. A workgroup takes gpw neighbouring groups of tpw tokens at a
 // time, a lane the same channels every time, the next tokens' loads under way meanwhile.
 // ---------------------------------------------------------------------------------
@@ -177,7 +202,7 @@ __device__ __forceinline__ Token token_at(const GroupParams& p, int64_t token) {
   return {b, int64_t(uint32_t(token) - b * uint32_t(p.T))};
 }
 
-template <typename ET, int E, int LPR, int NV>
+template <typename ET, int E, bool WHOLE, int LPR, int NV>
 __global__ __launch_bounds__(kThreads) void k_group_fwd(const GroupParams p) {
   constexpr int NA = NV > 0 ? NV : 1;
   __shared__ float red[2][4];
@@ -191,31 +216,32 @@ __global__ __launch_bounds__(kThreads) void k_group_fwd(const GroupParams p) {
   const float inv = 1.f / float(p.Cg);
   const int64_t tokens = int64_t(p.B) * p.T, step = int64_t(gridDim.x) * p.tpw;
   auto finish = [&](const float (&x)[E], const float (&g)[E], const float (&w)[E], const float (&bi)[E], float mean,
-                    float rstd, int64_t off) {
+                    float rstd, int64_t off, int n) {
     float y[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) y[e] = value((x[e] - mean) * rstd, w[e], bi[e], silu, gated, g[e]);
-    store<ET>(y, p.y.p, off);
+    store<ET, E, WHOLE>(y, p.y.p, off, n);
   };
   if constexpr (NV > 0) {
     float w[NA][E], bi[NA][E], nx[NA][E], ng[NA][E];
-    int cc[NA];
+    int cc[NA], nn[NA];  // first channel and channels that exist; lanes past the row read its start (or nothing) and drop it
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {  // lanes past the row read its start and drop it
+    for (int i = 0; i < NV; ++i) {
       const int c = (lane + i * LPR) * E;
+      nn[i] = p.Cg - c;
       cc[i] = c0 + (c < p.Cg ? c : 0);
 #pragma unroll
       for (int e = 0; e < E; ++e) w[i][e] = 1.f, bi[i][e] = 0.f;
-      if (p.weight != nullptr) load<ET>(w[i], p.weight, cc[i]);
-      if (p.bias != nullptr) load<ET>(bi[i], p.bias, cc[i]);
+      if (p.weight != nullptr) load<ET, E, WHOLE>(w[i], p.weight, cc[i], nn[i]);
+      if (p.bias != nullptr) load<ET, E, WHOLE>(bi[i], p.bias, cc[i], nn[i]);
     }
     auto fetch = [&](int64_t tok) {
       const Token q = token_at(p, tok < tokens ? tok : tokens - 1);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) load<ET>(nx[i], p.x.p, q.b * p.x.s0 + q.t * p.x.s1 + cc[i]);
+      for (int i = 0; i < NV; ++i) load<ET, E, WHOLE>(nx[i], p.x.p, q.b * p.x.s0 + q.t * p.x.s1 + cc[i], nn[i]);
       if (gated) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) load<ET>(ng[i], p.gate.p, q.b * p.gate.s0 + q.t * p.gate.s1 + cc[i]);
+        for (int i = 0; i < NV; ++i) load<ET, E, WHOLE>(ng[i], p.gate.p, q.b * p.gate.s0 + q.t * p.gate.s1 + cc[i], nn[i]);
       }
     };
     int64_t tok0 = int64_t(blockIdx.x) * p.tpw;
@@ -230,16 +256,16 @@ __global__ __launch_bounds__(kThreads) void k_group_fwd(const GroupParams p) {
       float sum = 0.f, sq = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if ((lane + i * LPR) * E < p.Cg) {
+        if (nn[i] > 0) {
 #pragma unroll
           for (int e = 0; e < E; ++e) sum += x[i][e];
         }
       const float mean = row_sum<LPR>(sum, red[0]) * inv;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if ((lane + i * LPR) * E < p.Cg) {
+        if (nn[i] > 0) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) sq += (x[i][e] - mean) * (x[i][e] - mean);
+          for (int e = 0; e < E; ++e) sq += WHOLE || e < nn[i] ? (x[i][e] - mean) * (x[i][e] - mean) : 0.f;
         }
       const float rstd = 1.f / sqrtf(row_sum<LPR>(sq, red[1]) * inv + p.eps);
       if (mine && tok0 + tsub < tokens) {
@@ -247,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void k_group_fwd(const GroupParams p) {
         const int64_t oy = q.b * p.y.s0 + q.t * p.y.s1;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if ((lane + i * LPR) * E < p.Cg) finish(x[i], g[i], w[i], bi[i], mean, rstd, oy + cc[i]);
+          if (nn[i] > 0) finish(x[i], g[i], w[i], bi[i], mean, rstd, oy + cc[i], nn[i]);
       }
     }
   } else {
@@ -257,7 +283,7 @@ __global__ __launch_bounds__(kThreads) void k_group_fwd(const GroupParams p) {
       double sum = 0.0, sq = 0.0;  // 64 bits: of any number of channels, and no difference of two of them loses the variance
       for (int c = lane * E; c < p.Cg; c += LPR * E) {
         float x[E];
-        load<ET>(x, p.x.p, ox + c);
+        load<ET, E, WHOLE>(x, p.x.p, ox + c, p.Cg - c);
 #pragma unroll
         for (int e = 0; e < E; ++e) sum += double(x[e]), sq += double(x[e]) * double(x[e]);
       }
@@ -266,13 +292,14 @@ __global__ __launch_bounds__(kThreads) void k_group_fwd(const GroupParams p) {
       const float rstd = 1.f / sqrtf((var < 0.0 ? 0.f : float(var)) + p.eps);
       for (int c = lane * E; c < p.Cg; c += LPR * E) {
         float x[E], g[E], w[E], bi[E];
-        load<ET>(x, p.x.p, ox + c);
-        if (gated) load<ET>(g, p.gate.p, og + c);
+        const int n = p.Cg - c;
+        load<ET, E, WHOLE>(x, p.x.p, ox + c, n);
+        if (gated) load<ET, E, WHOLE>(g, p.gate.p, og + c, n);
 #pragma unroll
         for (int e = 0; e < E; ++e) w[e] = 1.f, bi[e] = 0.f;
-        if (p.weight != nullptr) load<ET>(w, p.weight, c0 + c);
-        if (p.bias != nullptr) load<ET>(bi, p.bias, c0 + c);
-        finish(x, g, w, bi, float(mean), rstd, q.b * p.y.s0 + q.t * p.y.s1 + c0 + c);
+        if (p.weight != nullptr) load<ET, E, WHOLE>(w, p.weight, c0 + c, n);
+        if (p.bias != nullptr) load<ET, E, WHOLE>(bi, p.bias, c0 + c, n);
+        finish(x, g, w, bi, float(mean), rstd, q.b * p.y.s0 + q.t * p.y.s1 + c0 + c, n);
       }
     }
   }
@@ -280,7 +307,7 @@ __global__ __launch_bounds__(kThreads) void k_group_fwd(const GroupParams p) {
 
 // The sums of the weight's and the bias's gradient stay in a lane's registers and leave as one partial row per
 // workgroup.
-template <typename ET, int E, int LPR, int NV, bool PACKED>
+template <typename ET, int E, bool WHOLE, int LPR, int NV, bool PACKED>
 __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
   using IT = std::conditional_t<PACKED, i8_t, ET>;
   constexpr int NA = NV > 0 ? NV : 1;
@@ -296,16 +323,17 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
   const float inv = 1.f / float(p.Cg);
   const int64_t tokens = int64_t(p.B) * p.T;
   float dw[NA][E], db[NA][E], w[NA][E], bi[NA][E];
-  int cc[NA];
+  int cc[NA], nn[NA];
 #pragma unroll
   for (int i = 0; i < NA; ++i) {
     const int c = (lane + i * LPR) * E;
+    nn[i] = p.Cg - c;
     cc[i] = c < p.Cg ? c : 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[i][e] = 0.f, db[i][e] = 0.f, w[i][e] = 1.f, bi[i][e] = 0.f;
     if constexpr (NV > 0) {
-      if (p.weight != nullptr) load<ET>(w[i], p.weight, c0 + cc[i]);
-      if (p.bias != nullptr) load<ET>(bi[i], p.bias, c0 + cc[i]);
+      if (p.weight != nullptr) load<ET, E, WHOLE>(w[i], p.weight, c0 + cc[i], nn[i]);
+      if (p.bias != nullptr) load<ET, E, WHOLE>(bi[i], p.bias, c0 + cc[i], nn[i]);
     }
   }
   bool first = true;
@@ -315,12 +343,12 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
     const Token q = token_at(p, tok < tokens ? tok : tokens - 1);
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
-      load_x<IT, E>(nx[i], p.x, q.b, q.t, c0 + cc[i]);
-      load<ET>(ndy[i], p.dy.p, q.b * p.dy.s0 + q.t * p.dy.s1 + c0 + cc[i]);
+      load_x<IT, E, WHOLE>(nx[i], p.x, q.b, q.t, c0 + cc[i], nn[i]);
+      load<ET, E, WHOLE>(ndy[i], p.dy.p, q.b * p.dy.s0 + q.t * p.dy.s1 + c0 + cc[i], nn[i]);
     }
     if (gated) {
 #pragma unroll
-      for (int i = 0; i < NA; ++i) load<ET>(ng[i], p.gate.p, q.b * p.gate.s0 + q.t * p.gate.s1 + c0 + cc[i]);
+      for (int i = 0; i < NA; ++i) load<ET, E, WHOLE>(ng[i], p.gate.p, q.b * p.gate.s0 + q.t * p.gate.s1 + c0 + cc[i], nn[i]);
     }
   };
   if constexpr (NV > 0) fetch(int64_t(blockIdx.x) * p.tpw + tsub);
@@ -340,22 +368,22 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
       float sum = 0.f, sq = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if ((lane + i * LPR) * E < p.Cg) {
+        if (nn[i] > 0) {
 #pragma unroll
           for (int e = 0; e < E; ++e) sum += x[i][e];
         }
       const float mean = row_sum<LPR>(sum, red[0]) * inv;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if ((lane + i * LPR) * E < p.Cg) {
+        if (nn[i] > 0) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) sq += (x[i][e] - mean) * (x[i][e] - mean);
+          for (int e = 0; e < E; ++e) sq += WHOLE || e < nn[i] ? (x[i][e] - mean) * (x[i][e] - mean) : 0.f;
         }
       const float rstd = 1.f / sqrtf(row_sum<LPR>(sq, red[1]) * inv + p.eps);
       float s1 = 0.f, s2 = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if ((lane + i * LPR) * E < p.Cg) {
+        if (nn[i] > 0) {
           float dz[E], dg[E];
 #pragma unroll
           for (int e = 0; e < E; ++e) {
@@ -367,7 +395,7 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
             s2 += dy[i][e] * x[i][e];
           }
           if (have) {
-            if (gated) store<ET>(dg, p.dgate.p, odg + cc[i]);
+            if (gated) store<ET, E, WHOLE>(dg, p.dgate.p, odg + cc[i], nn[i]);
 #pragma unroll
             for (int e = 0; e < E; ++e) dw[i][e] += dz[e] * x[i][e], db[i][e] += dz[e];
           }
@@ -377,18 +405,18 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
       if (have) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if ((lane + i * LPR) * E < p.Cg) {
+          if (nn[i] > 0) {
             float dx[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) dx[e] = rstd * (dy[i][e] - s1 - x[i][e] * s2);
-            store<ET>(dx, p.dx.p, odx + cc[i]);
+            store<ET, E, WHOLE>(dx, p.dx.p, odx + cc[i], nn[i]);
           }
       }
     } else {
       double sum = 0.0, sq = 0.0;
       for (int c = lane * E; c < p.Cg; c += LPR * E) {
         float x[E];
-        load_x<IT, E>(x, p.x, b, t, c0 + c);
+        load_x<IT, E, WHOLE>(x, p.x, b, t, c0 + c, p.Cg - c);
 #pragma unroll
         for (int e = 0; e < E; ++e) sum += double(x[e]), sq += double(x[e]) * double(x[e]);
       }
@@ -397,13 +425,14 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
       const float mean = float(dmean), rstd = 1.f / sqrtf((var < 0.0 ? 0.f : float(var)) + p.eps);
       auto point = [&](int c, float (&n)[E], float (&dn)[E], float (&dz)[E], float (&dg)[E]) {
         float wv[E], bv[E], g[E];
-        load_x<IT, E>(n, p.x, b, t, c0 + c);
-        load<ET>(dn, p.dy.p, ody + c);
-        if (gated) load<ET>(g, p.gate.p, og + c);
+        const int have = p.Cg - c;
+        load_x<IT, E, WHOLE>(n, p.x, b, t, c0 + c, have);
+        load<ET, E, WHOLE>(dn, p.dy.p, ody + c, have);
+        if (gated) load<ET, E, WHOLE>(g, p.gate.p, og + c, have);
 #pragma unroll
         for (int e = 0; e < E; ++e) wv[e] = 1.f, bv[e] = 0.f;
-        if (p.weight != nullptr) load<ET>(wv, p.weight, c0 + c);
-        if (p.bias != nullptr) load<ET>(bv, p.bias, c0 + c);
+        if (p.weight != nullptr) load<ET, E, WHOLE>(wv, p.weight, c0 + c, have);
+        if (p.bias != nullptr) load<ET, E, WHOLE>(bv, p.bias, c0 + c, have);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           n[e] = (n[e] - mean) * rstd;
@@ -427,11 +456,12 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
         point(c, n, dn, dz, dg);
 #pragma unroll
         for (int e = 0; e < E; ++e) dx[e] = rstd * (dn[e] - m1 - n[e] * m2);
-        store<ET>(dx, p.dx.p, odx + c);
-        if (gated) store<ET>(dg, p.dgate.p, odg + c);
+        store<ET, E, WHOLE>(dx, p.dx.p, odx + c, p.Cg - c);
+        if (gated) store<ET, E, WHOLE>(dg, p.dgate.p, odg + c, p.Cg - c);
         if (part != nullptr) {
 #pragma unroll
           for (int e = 0; e < E; ++e) {
+            if (!WHOLE && c + e >= p.Cg) break;
             part[c + e] = first ? dz[e] * n[e] : part[c + e] + dz[e] * n[e];
             part[p.C + c + e] = first ? dz[e] : part[p.C + c + e] + dz[e];
           }
@@ -447,9 +477,10 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
       if (!mine) return;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if ((lane + i * LPR) * E < p.Cg) {
+        if (nn[i] > 0) {
 #pragma unroll
           for (int e = 0; e < E; ++e) {
+            if (!WHOLE && e >= nn[i]) break;
             part[c0 + cc[i] + e] = dw[i][e];
             part[p.C + c0 + cc[i] + e] = db[i][e];
           }
@@ -462,9 +493,10 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
       if (mine) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if ((lane + i * LPR) * E < p.Cg) {
+          if (nn[i] > 0) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) fold[tsub * width + gsub * p.Cg + cc[i] + e] = which ? db[i][e] : dw[i][e];
+            for (int e = 0; e < E; ++e)
+              if (WHOLE || e < nn[i]) fold[tsub * width + gsub * p.Cg + cc[i] + e] = which ? db[i][e] : dw[i][e];
           }
       }
       __syncthreads();
@@ -484,31 +516,46 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
 // of them side by side. x is read twice: once for the sums, once for the result.
 // ---------------------------------------------------------------------------------
 struct Place {
-  int b, g0, t0, t1, n, tsub, l, z;  // t0..t1: its tokens, of n that exist; l: lane of the token
+  int b, g0, t0, t1, n, tsub, l;  // t0..t1: its tokens, of n that exist; l: lane of the token
+  int g, c;                       // the lane's group, and its first channel there
   bool on;
 };
+template <int E>
 __device__ __forceinline__ Place place(const GroupParams& p) {
   Place q;
-  q.z = blockIdx.y;
   q.b = int(blockIdx.x) / p.nChunk;
   const int k = int(blockIdx.x) - q.b * p.nChunk;
-  q.g0 = q.z * p.gpb;
+  q.g0 = blockIdx.y * p.gpb;
   q.n = p.lengths != nullptr ? min(max(p.lengths[q.b], 0), p.T) : p.T;
   q.t0 = k * p.chunk;
   q.t1 = min(p.T, q.t0 + p.chunk);
   q.tsub = threadIdx.x / p.lpt;
   q.l = threadIdx.x - q.tsub * p.lpt;
-  q.on = q.tsub < p.tps;
+  const int gl = q.l / p.lpg;  // 0 where a group has all lanes
+  q.g = q.g0 + (p.gpb > 1 ? gl : 0);
+  q.c = (p.gpb > 1 ? q.l - gl * p.lpg : q.l) * E;
+  q.on = q.tsub < p.tps && q.g < p.G;
   return q;
 }
 constexpr int kAhead = 4;  // tokens whose loads a lane has under way
 
-// Sums over the lanes of each of a workgroup's groups: v[i] of thread (tsub, l), channels from l E.
+// Zeros for the lane's tokens from `end` on (those behind the sequence; nothing of theirs is read).
+template <typename ET, int E, bool WHOLE>
+__device__ __forceinline__ void zero_tokens(const GroupTensor& out, const GroupParams& p, const Place& q, int end, int c, int n) {
+  float zero[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) zero[e] = 0.f;
+  int t = q.t0 + q.tsub;
+  if (t < end) t += (end - t + p.tps - 1) / p.tps * p.tps;
+  for (; t < q.t1; t += p.tps) store<ET, E, WHOLE>(zero, out.p, q.b * out.s0 + t * out.s1 + c, n);
+}
+
+// Sums over the lanes of each of a workgroup's groups: v[i] of thread (tsub, l).
 // The result of group g is in out[g][i] for every thread after the call.
-template <int N, int E>
+template <int N>
 __device__ __forceinline__ void group_sums(const GroupParams& p, const Place& q, const double (&v)[N], double* red,
                                            double* out) {
-  const int lanes = p.gpb > 1 ? p.Cg / E : p.lpt;  // lanes of a group and token
+  const int lanes = p.gpb > 1 ? p.lpg : p.lpt;  // lanes of a group and token
   int per = 1;  // threads that add up one group
   while (per * 2 * p.gpb <= kThreads) per *= 2;
   const int g = threadIdx.x / per, j = threadIdx.x - g * per;
@@ -530,18 +577,19 @@ __device__ __forceinline__ void group_sums(const GroupParams& p, const Place& q,
   __syncthreads();
 }
 
-template <typename ET, int E, bool PACKED>
+template <typename ET, int E, bool WHOLE, bool PACKED>
 __global__ __launch_bounds__(kThreads) void k_group_stats(const GroupParams p) {
   using IT = std::conditional_t<PACKED, i8_t, ET>;
   __shared__ double red[kThreads], out[kThreads * 2];
-  const Place q = place(p);
-  const int c0 = q.g0 * p.Cg, cEnd = min(p.C, c0 + p.gpb * p.Cg), end = min(q.t1, q.n);
+  const Place q = place<E>(p);
+  const int end = min(q.t1, q.n);
   double v[2] = {0.0, 0.0};  // 64 bits: the squares' sum is good for the variance of any offset that float32 holds
-  for (int c = c0 + q.l * E; q.on && c < cEnd; c += p.lpt * E) {
+  for (int cl = q.c; q.on && cl < p.Cg; cl += p.lpt * E) {
+    const int c = q.g * p.Cg + cl, n = p.Cg - cl;
     for (int t = q.t0 + q.tsub; t < end; t += kAhead * p.tps) {
       float x[kAhead][E];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) load_x<IT, E>(x[u], p.x, q.b, min(t + u * p.tps, end - 1), c);
+      for (int u = 0; u < kAhead; ++u) load_x<IT, E, WHOLE>(x[u], p.x, q.b, min(t + u * p.tps, end - 1), c, n);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
         if (t + u * p.tps < end) {
@@ -550,91 +598,93 @@ __global__ __launch_bounds__(kThreads) void k_group_stats(const GroupParams p) {
         }
     }
   }
-  group_sums<2, E>(p, q, v, red, out);
+  group_sums<2>(p, q, v, red, out);
   double* part = p.part + int64_t(blockIdx.x) * p.G * 2;
   for (int i = threadIdx.x; i < p.gpb * 2; i += kThreads)
     if (q.g0 + i / 2 < p.G) part[q.g0 * 2 + i] = out[i];
 }
 
-template <typename ET, int E>
+template <typename ET, int E, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void k_group_apply(const GroupParams p) {
-  const Place q = place(p);
+  const Place q = place<E>(p);
   if (!q.on) return;
-  const int c0 = q.g0 * p.Cg, cEnd = min(p.C, c0 + p.gpb * p.Cg);
+  const int end = min(q.t1, q.n);
   const bool gated = p.gate.p != nullptr, silu = p.silu != 0;
-  for (int c = c0 + q.l * E; c < cEnd; c += p.lpt * E) {
+  for (int cl = q.c; cl < p.Cg; cl += p.lpt * E) {
+    const int c = q.g * p.Cg + cl, n = p.Cg - cl;
     float w[E], bi[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) w[e] = 1.f, bi[e] = 0.f;
-    if (p.weight != nullptr) load<ET>(w, p.weight, c);
-    if (p.bias != nullptr) load<ET>(bi, p.bias, c);
-    const float* st = p.stats + (int64_t(q.b) * p.G + c / p.Cg) * 2;
+    if (p.weight != nullptr) load<ET, E, WHOLE>(w, p.weight, c, n);
+    if (p.bias != nullptr) load<ET, E, WHOLE>(bi, p.bias, c, n);
+    const float* st = p.stats + (int64_t(q.b) * p.G + q.g) * 2;
     const float mean = st[0], rstd = st[1];
-    for (int t = q.t0 + q.tsub; t < q.t1; t += kAhead * p.tps) {
+    int t = q.t0 + q.tsub;
+    for (; t < end; t += kAhead * p.tps) {
       float x[kAhead][E], g[kAhead][E];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) load_x<ET, E>(x[u], p.x, q.b, min(t + u * p.tps, q.t1 - 1), c);
+      for (int u = 0; u < kAhead; ++u) load_x<ET, E, WHOLE>(x[u], p.x, q.b, min(t + u * p.tps, end - 1), c, n);
       if (gated) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-          load<ET>(g[u], p.gate.p, q.b * p.gate.s0 + min(t + u * p.tps, q.t1 - 1) * p.gate.s1 + c);
+          load<ET, E, WHOLE>(g[u], p.gate.p, q.b * p.gate.s0 + min(t + u * p.tps, end - 1) * p.gate.s1 + c, n);
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const int tok = t + u * p.tps;
-        if (tok >= q.t1) break;
+        if (tok >= end) break;
         float y[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          y[e] = tok < q.n ? value((x[u][e] - mean) * rstd, w[e], bi[e], silu, gated, g[u][e]) : 0.f;
-        store<ET>(y, p.y.p, q.b * p.y.s0 + tok * p.y.s1 + c);
+        for (int e = 0; e < E; ++e) y[e] = value((x[u][e] - mean) * rstd, w[e], bi[e], silu, gated, g[u][e]);
+        store<ET, E, WHOLE>(y, p.y.p, q.b * p.y.s0 + tok * p.y.s1 + c, n);
       }
     }
+    zero_tokens<ET, E, WHOLE>(p.y, p, q, end, c, n);
   }
 }
 
 // Column sums of dz n and dz over a workgroup's tokens.
-template <typename ET, int E, bool PACKED>
+template <typename ET, int E, bool WHOLE, bool PACKED>
 __global__ __launch_bounds__(kThreads) void k_group_columns(const GroupParams p) {
   using IT = std::conditional_t<PACKED, i8_t, ET>;
   __shared__ float fold[kThreads][E + 1];
-  const Place q = place(p);
-  const int c0 = q.g0 * p.Cg, cEnd = min(p.C, c0 + p.gpb * p.Cg), end = min(q.t1, q.n);
+  const Place q = place<E>(p);
+  const int end = min(q.t1, q.n);
   const bool gated = p.gate.p != nullptr, silu = p.silu != 0;
   float* part = p.colpart + int64_t(blockIdx.x) * 2 * p.C;
-  for (int cb = c0; cb < cEnd; cb += p.lpt * E) {
-    const int c = cb + q.l * E;
-    const bool on = q.on && c < cEnd;
+  for (int cb = 0; cb < p.Cg; cb += p.lpt * E) {  // once, but for groups wider than the workgroup
+    const int cl = q.c + cb, c = q.g * p.Cg + cl, n = p.Cg - cl;
+    const bool on = q.on && n > 0;
     float dw[E], db[E], w[E], bi[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[e] = 0.f, db[e] = 0.f, w[e] = 1.f, bi[e] = 0.f;
     if (on) {
-      if (p.weight != nullptr) load<ET>(w, p.weight, c);
-      if (p.bias != nullptr) load<ET>(bi, p.bias, c);
-      const float* st = p.stats + (int64_t(q.b) * p.G + c / p.Cg) * 2;
+      if (p.weight != nullptr) load<ET, E, WHOLE>(w, p.weight, c, n);
+      if (p.bias != nullptr) load<ET, E, WHOLE>(bi, p.bias, c, n);
+      const float* st = p.stats + (int64_t(q.b) * p.G + q.g) * 2;
       const float mean = st[0], rstd = st[1];
       for (int t = q.t0 + q.tsub; t < end; t += kAhead * p.tps) {
         float x[kAhead][E], dy[kAhead][E], g[kAhead][E];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           const int64_t tok = min(t + u * p.tps, end - 1);
-          load_x<IT, E>(x[u], p.x, q.b, tok, c);
-          load<ET>(dy[u], p.dy.p, q.b * p.dy.s0 + tok * p.dy.s1 + c);
+          load_x<IT, E, WHOLE>(x[u], p.x, q.b, tok, c, n);
+          load<ET, E, WHOLE>(dy[u], p.dy.p, q.b * p.dy.s0 + tok * p.dy.s1 + c, n);
         }
         if (gated) {
 #pragma unroll
           for (int u = 0; u < kAhead; ++u)
-            load<ET>(g[u], p.gate.p, q.b * p.gate.s0 + min(t + u * p.tps, end - 1) * p.gate.s1 + c);
+            load<ET, E, WHOLE>(g[u], p.gate.p, q.b * p.gate.s0 + min(t + u * p.tps, end - 1) * p.gate.s1 + c, n);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
           if (t + u * p.tps < end) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-              const float n = (x[u][e] - mean) * rstd;
+              const float norm = (x[u][e] - mean) * rstd;
               float dg;
-              const float dz = slope(n, w[e], bi[e], silu, gated, g[u][e], dy[u][e], dg);
-              dw[e] += dz * n;
+              const float dz = slope(norm, w[e], bi[e], silu, gated, g[u][e], dy[u][e], dg);
+              dw[e] += dz * norm;
               db[e] += dz;
             }
           }
@@ -648,6 +698,7 @@ __global__ __launch_bounds__(kThreads) void k_group_columns(const GroupParams p)
       if (q.tsub == 0 && on) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
+          if (!WHOLE && e >= n) break;
           float s = 0.f;
           for (int r = 0; r < p.tps; ++r) s += fold[r * p.lpt + q.l][e];
           part[which * p.C + c + e] = s;
@@ -658,144 +709,147 @@ __global__ __launch_bounds__(kThreads) void k_group_columns(const GroupParams p)
 }
 
 // dx (and dgate) of a workgroup's tokens from the sequence's column sums.
-template <typename ET, int E, bool PACKED>
+template <typename ET, int E, bool WHOLE, bool PACKED>
 __global__ __launch_bounds__(kThreads) void k_group_gradient(const GroupParams p) {
   using IT = std::conditional_t<PACKED, i8_t, ET>;
   __shared__ double red[kThreads], out[kThreads * 2];
-  const Place q = place(p);
-  const int c0 = q.g0 * p.Cg, cEnd = min(p.C, c0 + p.gpb * p.Cg);
+  const Place q = place<E>(p);
+  const int end = min(q.t1, q.n);
   const bool gated = p.gate.p != nullptr, silu = p.silu != 0;
   // mean(dn n) and mean(dn) of each group: the column sums with the weight on them
   double v[2] = {0.0, 0.0};
   if (q.on && q.tsub == 0)
-    for (int c = c0 + q.l * E; c < cEnd; c += p.lpt * E) {
+    for (int cl = q.c; cl < p.Cg; cl += p.lpt * E) {
+      const int c = q.g * p.Cg + cl, n = p.Cg - cl;
       float w[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) w[e] = 1.f;
-      if (p.weight != nullptr) load<ET>(w, p.weight, c);
+      if (p.weight != nullptr) load<ET, E, WHOLE>(w, p.weight, c, n);
       const float* cs = p.colsum + int64_t(q.b) * 2 * p.C + c;
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[0] += double(w[e]) * double(cs[e]), v[1] += double(w[e]) * double(cs[p.C + e]);
+      for (int e = 0; e < E; ++e)
+        if (WHOLE || e < n) v[0] += double(w[e]) * double(cs[e]), v[1] += double(w[e]) * double(cs[p.C + e]);
     }
-  group_sums<2, E>(p, q, v, red, out);
+  group_sums<2>(p, q, v, red, out);
   if (!q.on) return;
   const double inv = q.n > 0 ? 1.0 / (double(q.n) * p.Cg) : 0.0;
-  for (int c = c0 + q.l * E; c < cEnd; c += p.lpt * E) {
+  for (int cl = q.c; cl < p.Cg; cl += p.lpt * E) {
+    const int c = q.g * p.Cg + cl, n = p.Cg - cl;
     float w[E], bi[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) w[e] = 1.f, bi[e] = 0.f;
-    if (p.weight != nullptr) load<ET>(w, p.weight, c);
-    if (p.bias != nullptr) load<ET>(bi, p.bias, c);
-    const int g = c / p.Cg;
-    const float* st = p.stats + (int64_t(q.b) * p.G + g) * 2;
+    if (p.weight != nullptr) load<ET, E, WHOLE>(w, p.weight, c, n);
+    if (p.bias != nullptr) load<ET, E, WHOLE>(bi, p.bias, c, n);
+    const float* st = p.stats + (int64_t(q.b) * p.G + q.g) * 2;
     const float mean = st[0], rstd = st[1];
-    const float m2 = float(out[(g - q.g0) * 2] * inv), m1 = float(out[(g - q.g0) * 2 + 1] * inv);
-    for (int t = q.t0 + q.tsub; t < q.t1; t += kAhead * p.tps) {
+    const float m2 = float(out[(q.g - q.g0) * 2] * inv), m1 = float(out[(q.g - q.g0) * 2 + 1] * inv);
+    for (int t = q.t0 + q.tsub; t < end; t += kAhead * p.tps) {
       float x[kAhead][E], dy[kAhead][E], gt[kAhead][E];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int64_t tok = min(t + u * p.tps, q.t1 - 1);
-        load_x<IT, E>(x[u], p.x, q.b, tok, c);
-        load<ET>(dy[u], p.dy.p, q.b * p.dy.s0 + tok * p.dy.s1 + c);
+        const int64_t tok = min(t + u * p.tps, end - 1);
+        load_x<IT, E, WHOLE>(x[u], p.x, q.b, tok, c, n);
+        load<ET, E, WHOLE>(dy[u], p.dy.p, q.b * p.dy.s0 + tok * p.dy.s1 + c, n);
       }
       if (gated) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-          load<ET>(gt[u], p.gate.p, q.b * p.gate.s0 + min(t + u * p.tps, q.t1 - 1) * p.gate.s1 + c);
+          load<ET, E, WHOLE>(gt[u], p.gate.p, q.b * p.gate.s0 + min(t + u * p.tps, end - 1) * p.gate.s1 + c, n);
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const int tok = t + u * p.tps;
-        if (tok >= q.t1) break;
-        const bool real = tok < q.n;
+        if (tok >= end) break;
         float dx[E], dg[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const float n = (x[u][e] - mean) * rstd;
+          const float norm = (x[u][e] - mean) * rstd;
           dg[e] = 0.f;
-          const float dz = slope(n, w[e], bi[e], silu, gated, gt[u][e], dy[u][e], dg[e]);
-          dx[e] = real ? rstd * (dz * w[e] - m1 - n * m2) : 0.f;
-          dg[e] = real ? dg[e] : 0.f;
+          const float dz = slope(norm, w[e], bi[e], silu, gated, gt[u][e], dy[u][e], dg[e]);
+          dx[e] = rstd * (dz * w[e] - m1 - norm * m2);
         }
-        store<ET>(dx, p.dx.p, q.b * p.dx.s0 + tok * p.dx.s1 + c);
-        if (gated) store<ET>(dg, p.dgate.p, q.b * p.dgate.s0 + tok * p.dgate.s1 + c);
+        store<ET, E, WHOLE>(dx, p.dx.p, q.b * p.dx.s0 + tok * p.dx.s1 + c, n);
+        if (gated) store<ET, E, WHOLE>(dg, p.dgate.p, q.b * p.dgate.s0 + tok * p.dgate.s1 + c, n);
       }
     }
+    zero_tokens<ET, E, WHOLE>(p.dx, p, q, end, c, n);
+    if (gated) zero_tokens<ET, E, WHOLE>(p.dgate, p, q, end, c, n);
   }
 }
 
 // ---------------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------------
-template <typename ET, int E, int LPR, int NV>
+template <typename ET, int E, bool WHOLE, int LPR, int NV>
 hipError_t tokens_nv(const GroupParams& p, bool packed, bool bwd, hipStream_t s) {
   GroupParams q = p;
   const int64_t blocks = group_token_blocks(int64_t(p.B) * p.T, p.G, p.Cg, E, bwd, &q.gpw, &q.tpw);
   const dim3 grid(unsigned(blocks), unsigned((p.G + q.gpw - 1) / q.gpw));
   if (!bwd) {
-    hipLaunchKernelGGL((k_group_fwd<ET, E, LPR, NV>), grid, dim3(kThreads), 0, s, q);
+    hipLaunchKernelGGL((k_group_fwd<ET, E, WHOLE, LPR, NV>), grid, dim3(kThreads), 0, s, q);
     return hipGetLastError();
   }
   const size_t lds = NV > 0 && q.tpw > 1 ? size_t(q.tpw) * size_t(q.gpw) * size_t(p.Cg) * sizeof(float) : 0;
   if (packed) {
-    hipLaunchKernelGGL((k_group_bwd<ET, E, LPR, NV, true>), grid, dim3(kThreads), lds, s, q);
+    hipLaunchKernelGGL((k_group_bwd<ET, E, WHOLE, LPR, NV, true>), grid, dim3(kThreads), lds, s, q);
   } else {
-    hipLaunchKernelGGL((k_group_bwd<ET, E, LPR, NV, false>), grid, dim3(kThreads), lds, s, q);
+    hipLaunchKernelGGL((k_group_bwd<ET, E, WHOLE, LPR, NV, false>), grid, dim3(kThreads), lds, s, q);
   }
   return hipGetLastError();
 }
 
-template <typename ET, int E>
+template <typename ET, bool WHOLE>
 hipError_t tokens_e(const GroupParams& p, bool packed, bool bwd, hipStream_t s) {
+  constexpr int E = 16 / int(sizeof(ET));
   const GroupPlan pl = group_plan(p.Cg, E);
-  if constexpr (E > 1) {
-    if (pl.lpr == 4) return tokens_nv<ET, E, 4, 1>(p, packed, bwd, s);
-    if (pl.lpr == 8) return tokens_nv<ET, E, 8, 1>(p, packed, bwd, s);
-    if (pl.lpr == 16) return tokens_nv<ET, E, 16, 1>(p, packed, bwd, s);
-    if (pl.lpr == 32) return tokens_nv<ET, E, 32, 1>(p, packed, bwd, s);
-    if (pl.lpr == 64 && pl.nv == 1) return tokens_nv<ET, E, 64, 1>(p, packed, bwd, s);
-  } else {
-    if (pl.lpr == 16) return pl.nv == 2 ? tokens_nv<ET, E, 16, 2>(p, packed, bwd, s) : tokens_nv<ET, E, 16, 4>(p, packed, bwd, s);
+  if (pl.lpr == 4) return tokens_nv<ET, E, WHOLE, 4, 1>(p, packed, bwd, s);
+  if (pl.lpr == 8) return tokens_nv<ET, E, WHOLE, 8, 1>(p, packed, bwd, s);
+  if (pl.lpr == 16) return tokens_nv<ET, E, WHOLE, 16, 1>(p, packed, bwd, s);
+  if (pl.lpr == 32) return tokens_nv<ET, E, WHOLE, 32, 1>(p, packed, bwd, s);
+  if (pl.lpr == 64) {
+    if (pl.nv == 1) return tokens_nv<ET, E, WHOLE, 64, 1>(p, packed, bwd, s);
+    if (pl.nv == 2) return tokens_nv<ET, E, WHOLE, 64, 2>(p, packed, bwd, s);
+    return tokens_nv<ET, E, WHOLE, 64, 4>(p, packed, bwd, s);
   }
-  if (pl.lpr == 64) return pl.nv == 2 ? tokens_nv<ET, E, 64, 2>(p, packed, bwd, s) : tokens_nv<ET, E, 64, 4>(p, packed, bwd, s);
-  if (pl.nv == 2) return tokens_nv<ET, E, 256, 2>(p, packed, bwd, s);
-  if (pl.nv == 4) return tokens_nv<ET, E, 256, 4>(p, packed, bwd, s);
-  return tokens_nv<ET, E, 256, 0>(p, packed, bwd, s);
+  if (pl.nv == 2) return tokens_nv<ET, E, WHOLE, 256, 2>(p, packed, bwd, s);
+  if (pl.nv == 4) return tokens_nv<ET, E, WHOLE, 256, 4>(p, packed, bwd, s);
+  return tokens_nv<ET, E, WHOLE, 256, 0>(p, packed, bwd, s);
 }
 
 template <typename ET>
-hipError_t tokens(const GroupParams& p, bool vec, bool packed, bool bwd, hipStream_t s) {
-  return vec ? tokens_e<ET, 16 / int(sizeof(ET))>(p, packed, bwd, s) : tokens_e<ET, 1>(p, packed, bwd, s);
+hipError_t tokens(const GroupParams& p, bool whole, bool packed, bool bwd, hipStream_t s) {
+  return whole ? tokens_e<ET, true>(p, packed, bwd, s) : tokens_e<ET, false>(p, packed, bwd, s);
 }
 
-template <typename ET, int E>
+template <typename ET, bool WHOLE>
 hipError_t sequences_e(const GroupParams& p, bool packed, GroupStage stage, hipStream_t s) {
+  constexpr int E = 16 / int(sizeof(ET));
   const dim3 grid(unsigned(p.B) * unsigned(p.nChunk), unsigned((p.G + p.gpb - 1) / p.gpb)), block(kThreads);
   if (stage == kGroupStats) {
     if (packed) {
-      hipLaunchKernelGGL((k_group_stats<ET, E, true>), grid, block, 0, s, p);
+      hipLaunchKernelGGL((k_group_stats<ET, E, WHOLE, true>), grid, block, 0, s, p);
     } else {
-      hipLaunchKernelGGL((k_group_stats<ET, E, false>), grid, block, 0, s, p);
+      hipLaunchKernelGGL((k_group_stats<ET, E, WHOLE, false>), grid, block, 0, s, p);
     }
   } else if (stage == kGroupApply) {
-    hipLaunchKernelGGL((k_group_apply<ET, E>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((k_group_apply<ET, E, WHOLE>), grid, block, 0, s, p);
   } else if (stage == kGroupColumns) {
     if (packed) {
-      hipLaunchKernelGGL((k_group_columns<ET, E, true>), grid, block, 0, s, p);
+      hipLaunchKernelGGL((k_group_columns<ET, E, WHOLE, true>), grid, block, 0, s, p);
     } else {
-      hipLaunchKernelGGL((k_group_columns<ET, E, false>), grid, block, 0, s, p);
+      hipLaunchKernelGGL((k_group_columns<ET, E, WHOLE, false>), grid, block, 0, s, p);
     }
   } else if (packed) {
-    hipLaunchKernelGGL((k_group_gradient<ET, E, true>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((k_group_gradient<ET, E, WHOLE, true>), grid, block, 0, s, p);
   } else {
-    hipLaunchKernelGGL((k_group_gradient<ET, E, false>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((k_group_gradient<ET, E, WHOLE, false>), grid, block, 0, s, p);
   }
   return hipGetLastError();
 }
 
 template <typename ET>
-hipError_t sequences(const GroupParams& p, bool vec, bool packed, GroupStage stage, hipStream_t s) {
-  return vec ? sequences_e<ET, 16 / int(sizeof(ET))>(p, packed, stage, s) : sequences_e<ET, 1>(p, packed, stage, s);
+hipError_t sequences(const GroupParams& p, bool whole, bool packed, GroupStage stage, hipStream_t s) {
+  return whole ? sequences_e<ET, true>(p, packed, stage, s) : sequences_e<ET, false>(p, packed, stage, s);
 }
 
 }  // namespace group

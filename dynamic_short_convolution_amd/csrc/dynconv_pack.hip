@@ -6,8 +6,10 @@
 // by a power of two is exact, so the codes do not depend on the arithmetic, and code times step fits
 // the type that was packed. A group that holds an infinity or NaN gets the scale 255 and codes 0: it reads as
 // NaN (0 times infinity), as the scale's bits 255 << 23 say without a test.
-// Memory bound: 16 bytes per lane where rows allow it, the maximum by a butterfly over the group's
-// lanes; else one element per lane and a wave per group.
+// Memory bound: 16 bytes of the row per lane (at any alignment of its elements), the maximum by a butterfly
+// over the group's lanes, four rows' loads of a lane under way at a time.
+#include <type_traits>
+
 #include "dynconv_common.hpp"
 #include "dynconv_internal.hpp"
 
@@ -15,7 +17,7 @@ namespace dynconv {
 
 namespace {
 
-constexpr int kThreads = 256, kGroup = 64;
+constexpr int kThreads = 256, kGroup = 64;  // kGroup: channels that share a step
 
 struct PackTensor {
   const void* p;
@@ -32,36 +34,30 @@ template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
   return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xf, 0xf, true));
 }
-// The largest of N (8, 16 or 64) neighbouring lanes, in each of them: lanes 1 and 2 apart within a quad, 4
-// and 8 apart by mirrors, 16 and 32 apart by swaps.
+// The largest of N (8 or 16) neighbouring lanes, in each of them: lanes 1 and 2 apart within a quad, 4 and 8
+// apart by mirrors.
 template <int N>
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {
   v = max(v, dpp<0xB1>(v));
   v = max(v, dpp<0x4E>(v));
   v = max(v, dpp<0x141>(v));
   if constexpr (N >= 16) v = max(v, dpp<0x140>(v));
-  if constexpr (N >= 64) {
-    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    v = max(a[0], a[1]);
-    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    v = max(b[0], b[1]);
-  }
   return v;
 }
 
-template <int N>
-struct Bytes;
-template <>
-struct Bytes<1> {
-  typedef uint8_t T;
-};
-template <>
-struct Bytes<4> {
+// Words of a piece at the alignment of its elements (global memory takes 16 bytes at any).
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef u32x2 __attribute__((aligned(1))) u32x2_any;
+typedef uint32_t __attribute__((aligned(1))) u32_any;
+template <int E, bool WHOLE>
+struct Codes {
   typedef uint32_t T;
+  typedef std::conditional_t<WHOLE, uint32_t, u32_any> At;
 };
-template <>
-struct Bytes<8> {
+template <bool WHOLE>
+struct Codes<8, WHOLE> {
   typedef u32x2 T;
+  typedef std::conditional_t<WHOLE, u32x2, u32x2_any> At;
 };
 
 __device__ __forceinline__ int64_t offset(const PackParams& p, const PackTensor& t, uint32_t row) {
@@ -87,16 +83,12 @@ struct Walk {
 };
 constexpr int kAhead = 4;  // rows whose loads a lane has under way
 
-template <typename ET, int E>
-__device__ __forceinline__ void read(float (&v)[E], const PackTensor& t, int64_t off) {
-  if constexpr (E == 1) {
-    if constexpr (sizeof(ET) == 2) {
-      v[0] = Cvt<ET>::of_bits(static_cast<const uint16_t*>(t.p)[off]);
-    } else {
-      v[0] = static_cast<const float*>(t.p)[off];
-    }
-  } else {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const ET*>(t.p) + off);
+// A piece: E consecutive elements. WHOLE: aligned, all of them the row's; else its first n are.
+template <typename ET, int E, bool WHOLE>
+__device__ __forceinline__ void read(float (&v)[E], const PackTensor& t, int64_t off, int n) {
+  const ET* p = static_cast<const ET*>(t.p) + off;
+  if (WHOLE || n >= E) {
+    const u32x4 w = WHOLE ? *reinterpret_cast<const u32x4*>(p) : *reinterpret_cast<const u32x4_any*>(p);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (sizeof(ET) == 2) {
@@ -105,10 +97,20 @@ __device__ __forceinline__ void read(float (&v)[E], const PackTensor& t, int64_t
         v[i] = __uint_as_float(w[i]);
       }
     }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (e < n) {
+        if constexpr (sizeof(ET) == 2) {
+          v[e] = Cvt<ET>::of_bits(*reinterpret_cast<const uint16_t*>(p + e));
+        } else {
+          v[e] = p[e];
+        }
+      }
   }
 }
 
-template <typename ET, int E>
+template <typename ET, int E, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void k_pack8(const PackParams p) {
   const Walk<E> me(p);
   if (!me.on) return;  // whole groups of lanes
@@ -119,7 +121,7 @@ __global__ __launch_bounds__(kThreads) void k_pack8(const PackParams p) {
 #pragma unroll
       for (int e = 0; e < E; ++e) v[u][e] = 0.f;
       const uint32_t r = row + u * me.step;  // below 2^31 + 4 * 2^20
-      if (me.c < p.D) read<ET, E>(v[u], p.x, offset(p, p.x, r < p.rows ? r : row) + me.c);
+      if (me.c < p.D) read<ET, E, WHOLE>(v[u], p.x, offset(p, p.x, r < p.rows ? r : row) + me.c, int(p.D - me.c));
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -142,29 +144,32 @@ __global__ __launch_bounds__(kThreads) void k_pack8(const PackParams p) {
       if (me.c >= p.D) continue;
       if (me.c % kGroup == 0)
         const_cast<uint8_t*>(static_cast<const uint8_t*>(p.scales.p))[offset(p, p.scales, r) + me.c / kGroup] = uint8_t(scale);
-      typename Bytes<E>::T w;
-      if constexpr (E == 1) {
-        w = uint8_t(code[0]);
-      } else {
+      int8_t* out = const_cast<int8_t*>(static_cast<const int8_t*>(p.codes.p)) + offset(p, p.codes, r) + me.c;
+      if (WHOLE || me.c + E <= p.D) {
         uint32_t q[E / 4];
 #pragma unroll
         for (int i = 0; i < E / 4; ++i)
           q[i] = code[4 * i] | code[4 * i + 1] << 8 | code[4 * i + 2] << 16 | code[4 * i + 3] << 24;
+        typename Codes<E, WHOLE>::T w;
         if constexpr (E == 8) {
           w = u32x2{q[0], q[1]};
         } else {
           w = q[0];
         }
+        *reinterpret_cast<typename Codes<E, WHOLE>::At*>(out) = w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (me.c + e < p.D) out[e] = int8_t(code[e]);
       }
-      int8_t* out = const_cast<int8_t*>(static_cast<const int8_t*>(p.codes.p)) + offset(p, p.codes, r) + me.c;
-      *reinterpret_cast<typename Bytes<E>::T*>(out) = w;
     }
   }
 }
 
-template <typename ET, int E>
+template <typename ET, int E, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void k_unpack8(const PackParams p) {
-  typedef typename Bytes<E>::T Word;
+  typedef typename Codes<E, WHOLE>::T Word;
+  typedef typename Codes<E, WHOLE>::At WordAt;
   const Walk<E> me(p);
   if (!me.on || me.c >= p.D) return;
   for (uint32_t row = me.row; row < p.rows; row += kAhead * me.step) {
@@ -173,7 +178,20 @@ __global__ __launch_bounds__(kThreads) void k_unpack8(const PackParams p) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const uint32_t r = row + u * me.step, s = r < p.rows ? r : row;
-      w[u] = *reinterpret_cast<const Word*>(static_cast<const int8_t*>(p.codes.p) + offset(p, p.codes, s) + me.c);
+      const int8_t* in = static_cast<const int8_t*>(p.codes.p) + offset(p, p.codes, s) + me.c;
+      if (WHOLE || me.c + E <= p.D) {
+        w[u] = *reinterpret_cast<const WordAt*>(in);
+      } else {
+        uint32_t q[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (me.c + e < p.D) q[e / 4] |= uint32_t(uint8_t(in[e])) << (8 * (e % 4));
+        if constexpr (E == 8) {
+          w[u] = u32x2{q[0], q[1]};
+        } else {
+          w[u] = q[0];
+        }
+      }
       scale[u] = static_cast<const uint8_t*>(p.scales.p)[offset(p, p.scales, s) + me.c / kGroup];
     }
 #pragma unroll
@@ -193,13 +211,7 @@ __global__ __launch_bounds__(kThreads) void k_unpack8(const PackParams p) {
         v[e] = float(int8_t(word >> (8 * (e % 4)) & 0xff)) * step;
       }
       ET* out = const_cast<ET*>(static_cast<const ET*>(p.x.p)) + offset(p, p.x, r) + me.c;
-      if constexpr (E == 1) {
-        if constexpr (sizeof(ET) == 2) {
-          *reinterpret_cast<uint16_t*>(out) = Cvt<ET>::bits(v[0]);
-        } else {
-          *out = v[0];
-        }
-      } else {
+      if (WHOLE || me.c + E <= p.D) {
         u32x4 o;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -209,14 +221,29 @@ __global__ __launch_bounds__(kThreads) void k_unpack8(const PackParams p) {
             o[i] = __float_as_uint(v[i]);
           }
         }
-        *reinterpret_cast<u32x4*>(out) = o;
+        if constexpr (WHOLE) {
+          *reinterpret_cast<u32x4*>(out) = o;
+        } else {
+          *reinterpret_cast<u32x4_any*>(out) = o;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (me.c + e < p.D) {
+            if constexpr (sizeof(ET) == 2) {
+              *reinterpret_cast<uint16_t*>(out + e) = Cvt<ET>::bits(v[e]);
+            } else {
+              out[e] = v[e];
+            }
+          }
       }
     }
   }
 }
 
-template <typename ET, int E>
+template <typename ET, bool WHOLE>
 hipError_t launch(PackParams p, bool unpack, hipStream_t s) {
+  constexpr int E = 16 / int(sizeof(ET));
   p.lanes = (p.D + kGroup - 1) / kGroup * (kGroup / E);
   p.perBlock = p.lanes < kThreads ? p.lanes : kThreads;
   const uint32_t colBlocks = (p.lanes + p.perBlock - 1) / p.perBlock, side = kThreads / p.perBlock;
@@ -225,31 +252,31 @@ hipError_t launch(PackParams p, bool unpack, hipStream_t s) {
   p.rowBlocks = need < most ? need : most;
   const dim3 grid(colBlocks * p.rowBlocks);
   if (unpack) {
-    hipLaunchKernelGGL((k_unpack8<ET, E>), grid, dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_unpack8<ET, E, WHOLE>), grid, dim3(kThreads), 0, s, p);
   } else {
-    hipLaunchKernelGGL((k_pack8<ET, E>), grid, dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_pack8<ET, E, WHOLE>), grid, dim3(kThreads), 0, s, p);
   }
   return hipGetLastError();
 }
 
 template <typename ET>
-hipError_t dispatch(const PackParams& p, bool vec, bool unpack, hipStream_t s) {
-  return vec ? launch<ET, 16 / int(sizeof(ET))>(p, unpack, s) : launch<ET, 1>(p, unpack, s);
+hipError_t dispatch(const PackParams& p, bool whole, bool unpack, hipStream_t s) {
+  return whole ? launch<ET, true>(p, unpack, s) : launch<ET, false>(p, unpack, s);
 }
 
 bool aligned(const void* p, int64_t a) { return (reinterpret_cast<uintptr_t>(p) % uint64_t(a)) == 0; }
 
-// A tensor [n0,n1,n2,last] of eb-byte elements, read or written in pieces of `piece` bytes where *vec.
+// A tensor [n0,n1,n2,last] of eb-byte elements, read or written in pieces of `piece` bytes where *whole.
 dynconv_status take(PackTensor* t, const void* p, const int64_t* s, const int64_t* n, int64_t last, int eb, int piece,
-                    bool output, bool* vec) {
+                    bool output, bool* whole) {
   if (p == nullptr || s == nullptr) return DYNCONV_ERR_INVALID_ARG;
   if (!aligned(p, eb) || (last > 1 && s[3] != 1)) return DYNCONV_ERR_UNSUPPORTED;
-  if (!aligned(p, piece)) *vec = false;
+  if (!aligned(p, piece)) *whole = false;
   for (int i = 0; i < 3; ++i) {
     if (s[i] < 0) return DYNCONV_ERR_UNSUPPORTED;
     if (n[i] <= 1) continue;
     if (output && s[i] == 0) return DYNCONV_ERR_INVALID_ARG;
-    if (s[i] * eb % piece != 0) *vec = false;
+    if (s[i] * eb % piece != 0) *whole = false;
   }
   t->p = p;
   t->s0 = s[0], t->s1 = s[1], t->s2 = s[2];
@@ -287,11 +314,11 @@ dynconv_status run(const void* x, const int64_t* xs, const int8_t* codes, const 
   if (n0 == 0 || n1 == 0 || n2 == 0 || D == 0) return DYNCONV_OK;
   if (n0 > INT32_MAX / n1 || n0 * n1 > INT32_MAX / n2) return DYNCONV_ERR_UNSUPPORTED;
   const int eb = dtype == DYNCONV_F32 ? 4 : 2;
-  bool vec = D * eb % 16 == 0, any = true;
+  bool whole = D * eb % 16 == 0, any = true;
   PackParams p{};
   dynconv_status st;
-  if ((st = take(&p.x, x, xs, n, D, eb, 16, unpack, &vec)) != DYNCONV_OK) return st;
-  if ((st = take(&p.codes, codes, cs, n, D, 1, 16 / eb, !unpack, &vec)) != DYNCONV_OK) return st;
+  if ((st = take(&p.x, x, xs, n, D, eb, 16, unpack, &whole)) != DYNCONV_OK) return st;
+  if ((st = take(&p.codes, codes, cs, n, D, 1, 16 / eb, !unpack, &whole)) != DYNCONV_OK) return st;
   if ((st = take(&p.scales, scales, ss, n, (D + kGroup - 1) / kGroup, 1, 1, !unpack, &any)) != DYNCONV_OK) return st;
   if (x == static_cast<const void*>(codes) || x == static_cast<const void*>(scales) ||
       static_cast<const void*>(codes) == static_cast<const void*>(scales))
@@ -300,9 +327,9 @@ dynconv_status run(const void* x, const int64_t* xs, const int8_t* codes, const 
   const hipStream_t s = static_cast<hipStream_t>(stream);
   p.rows = uint32_t(n0 * n1 * n2);
   p.flat = flat(&p.x, n) && flat(&p.codes, n) && flat(&p.scales, n);
-  const hipError_t e = dtype == DYNCONV_BF16  ? dispatch<bf16_t>(p, vec, unpack, s)
-                       : dtype == DYNCONV_F16 ? dispatch<f16_t>(p, vec, unpack, s)
-                                              : dispatch<float>(p, vec, unpack, s);
+  const hipError_t e = dtype == DYNCONV_BF16  ? dispatch<bf16_t>(p, whole, unpack, s)
+                       : dtype == DYNCONV_F16 ? dispatch<f16_t>(p, whole, unpack, s)
+                                              : dispatch<float>(p, whole, unpack, s);
   return e == hipSuccess ? DYNCONV_OK : record_hip_error(e);
 }
 
