@@ -115,12 +115,17 @@ void group_sequence_plan(GroupParams* p, int E) {
   p->lpt = lanes >= kThreads ? kThreads : p->gpb * lanes;
   p->tps = kThreads / p->lpt;
   const int64_t across = int64_t(p->B) * ((p->G + p->gpb - 1) / p->gpb);
-  // four workgroups per CU; at least 32 tokens per lane, so that the column sums' rows stay few
-  const int64_t want = across < 1024 ? 1024 / across : 1;
-  int64_t chunk = (int64_t(p->T) + want - 1) / want;
-  if (chunk < 32 * p->tps) chunk = 32 * p->tps;
-  p->chunk = int32_t(chunk);
-  p->nChunk = int32_t((p->T + chunk - 1) / chunk);
+  // Workgroups per CU: sixteen (with sequences of other lengths many have nothing to do), in the
+  // gradient's two passes four, each of which leaves a row of column sums or begins with a sum over the groups.
+  auto cut = [&](int64_t all, int least, int32_t* chunk, int32_t* n) {
+    const int64_t want = across < all ? all / across : 1;
+    int64_t c = (int64_t(p->T) + want - 1) / want;
+    if (c < least * p->tps) c = least * p->tps;
+    *chunk = int32_t(c);
+    *n = int32_t((p->T + c - 1) / c);
+  };
+  cut(4096, 8, &p->chunk, &p->nChunk);
+  cut(1024, 32, &p->gradChunk, &p->nGradChunk);
 }
 
 namespace {
@@ -195,11 +200,10 @@ Space space(const Sizes& z, int E, bool bwd, bool stats) {
     if (bwd) w.colpart = rounded(size_t(group_token_blocks(z.B * z.T, z.G, p.Cg, E, true, &gpw, &tpw)) * 2 * size_t(z.C) * sizeof(float));
     return w;
   }
-  const size_t rows = size_t(z.B) * size_t(p.nChunk);
-  if (!(bwd && stats)) w.part = rounded(rows * size_t(z.G) * 2 * sizeof(double));
+  if (!(bwd && stats)) w.part = rounded(size_t(z.B) * size_t(p.nChunk) * size_t(z.G) * 2 * sizeof(double));
   if (!stats) w.stats = rounded(size_t(z.B) * size_t(z.G) * 2 * sizeof(float));
   if (bwd) {
-    w.colpart = rounded(rows * 2 * size_t(z.C) * sizeof(float));
+    w.colpart = rounded(size_t(z.B) * size_t(p.nGradChunk) * 2 * size_t(z.C) * sizeof(float));
     w.colsum = rounded(size_t(z.B) * 2 * size_t(z.C) * sizeof(float));
   }
   return w;
@@ -359,7 +363,7 @@ dynconv_status dynconv_groupnorm_bwd(const void* x, const int64_t* xs, const uin
     if ((e = statistics(p, dtype, whole, packed, s)) != hipSuccess) return done(e);
   }
   e = sequences(p, dtype, whole, packed, kGroupColumns, s);
-  if (e == hipSuccess) e = group_sum(p.colpart, p.nChunk, C, B, p.colsum, p.colsum + C, 2 * C, s);
+  if (e == hipSuccess) e = group_sum(p.colpart, p.nGradChunk, C, B, p.colsum, p.colsum + C, 2 * C, s);
   if (e == hipSuccess && params) e = group_sum(p.colsum, B, C, 1, dweight, dbias, 0, s);
   if (e == hipSuccess) e = sequences(p, dtype, whole, packed, kGroupGradient, s);
   return done(e);

@@ -32,8 +32,9 @@ struct GroupParams {
   float eps;
   // Per token: groups and tokens that a workgroup works on at a time.
   int32_t gpw, tpw;
-  // Sequences: groups of a workgroup, lanes of a group and of a token, tokens at a time, tokens of a workgroup.
-  int32_t gpb, lpg, lpt, tps, chunk, nChunk;
+  // Sequences: groups of a workgroup, lanes of a group and of a token, tokens at a time, tokens of a workgroup
+  // (and how many such chunks) in the forward's passes and in the gradient's.
+  int32_t gpb, lpg, lpt, tps, chunk, nChunk, gradChunk, nGradChunk;
 };
 
 // Lanes per row and vectors per lane (nv 0: the looping form) of a group of Cg channels.
@@ -43,7 +44,7 @@ struct GroupPlan {
 GroupPlan group_plan(int64_t Cg, int E);
 // Workgroups along the tokens, each with one row of partial sums in the backward.
 int64_t group_token_blocks(int64_t tokens, int64_t G, int64_t Cg, int E, bool bwd, int32_t* gpw, int32_t* tpw);
-// Sets gpb, lpg, lpt, tps, chunk and nChunk.
+// Sets gpb to nGradChunk.
 void group_sequence_plan(GroupParams* p, int E);
 
 hipError_t group_tokens_f32(const GroupParams&, bool whole, bool packed, bool bwd, hipStream_t);

@@ -537,7 +537,7 @@ __device__ __forceinline__ Place place(const GroupParams& p) {
   q.on = q.tsub < p.tps && q.g < p.G;
   return q;
 }
-constexpr int kAhead = 4;  // tokens whose loads a lane has under way
+constexpr int kAhead = 4, kAheadGrad = 2;  // tokens whose loads a lane has under way
 
 // Zeros for the lane's tokens from `end` on (those behind the sequence; nothing of theirs is read).
 template <typename ET, int E, bool WHOLE>
@@ -663,21 +663,21 @@ __global__ __launch_bounds__(kThreads) void k_group_columns(const GroupParams p)
       if (p.bias != nullptr) load<ET, E, WHOLE>(bi, p.bias, c, n);
       const float* st = p.stats + (int64_t(q.b) * p.G + q.g) * 2;
       const float mean = st[0], rstd = st[1];
-      for (int t = q.t0 + q.tsub; t < end; t += kAhead * p.tps) {
-        float x[kAhead][E], dy[kAhead][E], g[kAhead][E];
+      for (int t = q.t0 + q.tsub; t < end; t += kAheadGrad * p.tps) {
+        float x[kAheadGrad][E], dy[kAheadGrad][E], g[kAheadGrad][E];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
+        for (int u = 0; u < kAheadGrad; ++u) {
           const int64_t tok = min(t + u * p.tps, end - 1);
           load_x<IT, E, WHOLE>(x[u], p.x, q.b, tok, c, n);
           load<ET, E, WHOLE>(dy[u], p.dy.p, q.b * p.dy.s0 + tok * p.dy.s1 + c, n);
         }
         if (gated) {
 #pragma unroll
-          for (int u = 0; u < kAhead; ++u)
+          for (int u = 0; u < kAheadGrad; ++u)
             load<ET, E, WHOLE>(g[u], p.gate.p, q.b * p.gate.s0 + min(t + u * p.tps, end - 1) * p.gate.s1 + c, n);
         }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
+        for (int u = 0; u < kAheadGrad; ++u)
           if (t + u * p.tps < end) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -743,21 +743,21 @@ __global__ __launch_bounds__(kThreads) void k_group_gradient(const GroupParams p
     const float* st = p.stats + (int64_t(q.b) * p.G + q.g) * 2;
     const float mean = st[0], rstd = st[1];
     const float m2 = float(out[(q.g - q.g0) * 2] * inv), m1 = float(out[(q.g - q.g0) * 2 + 1] * inv);
-    for (int t = q.t0 + q.tsub; t < end; t += kAhead * p.tps) {
-      float x[kAhead][E], dy[kAhead][E], gt[kAhead][E];
+    for (int t = q.t0 + q.tsub; t < end; t += kAheadGrad * p.tps) {
+      float x[kAheadGrad][E], dy[kAheadGrad][E], gt[kAheadGrad][E];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
+      for (int u = 0; u < kAheadGrad; ++u) {
         const int64_t tok = min(t + u * p.tps, end - 1);
         load_x<IT, E, WHOLE>(x[u], p.x, q.b, tok, c, n);
         load<ET, E, WHOLE>(dy[u], p.dy.p, q.b * p.dy.s0 + tok * p.dy.s1 + c, n);
       }
       if (gated) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
+        for (int u = 0; u < kAheadGrad; ++u)
           load<ET, E, WHOLE>(gt[u], p.gate.p, q.b * p.gate.s0 + min(t + u * p.tps, end - 1) * p.gate.s1 + c, n);
       }
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
+      for (int u = 0; u < kAheadGrad; ++u) {
         const int tok = t + u * p.tps;
         if (tok >= end) break;
         float dx[E], dg[E];
@@ -822,8 +822,9 @@ hipError_t tokens(const GroupParams& p, bool whole, bool packed, bool bwd, hipSt
 }
 
 template <typename ET, bool WHOLE>
-hipError_t sequences_e(const GroupParams& p, bool packed, GroupStage stage, hipStream_t s) {
+hipError_t sequences_e(GroupParams p, bool packed, GroupStage stage, hipStream_t s) {
   constexpr int E = 16 / int(sizeof(ET));
+  if (stage == kGroupColumns || stage == kGroupGradient) p.chunk = p.gradChunk, p.nChunk = p.nGradChunk;
   const dim3 grid(unsigned(p.B) * unsigned(p.nChunk), unsigned((p.G + p.gpb - 1) / p.gpb)), block(kThreads);
   if (stage == kGroupStats) {
     if (packed) {
