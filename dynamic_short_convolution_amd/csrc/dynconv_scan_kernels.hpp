@@ -68,9 +68,10 @@ struct Elems {  // V adjacent elements of a storage type
       } else {
         v[0] = Cvt<ET>::lo(w), v[1] = Cvt<ET>::hi(w);
       }
-    } else {
-      v[0] = float(int8_t(w & 0xff));
-      if constexpr (V == 2) v[1] = float(int8_t(w >> 8));
+    } else {  // codes plus 128
+      const uint32_t u = uint32_t(w) ^ 0x8080u;
+      v[0] = float(u & 0xffu);
+      if constexpr (V == 2) v[1] = float(u >> 8 & 0xffu);
     }
   }
   static __device__ __forceinline__ W put(const float (&v)[V]) {
@@ -88,9 +89,9 @@ struct Elems {  // V adjacent elements of a storage type
   }
 };
 
-__device__ __forceinline__ float sigmoid(float z) {
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -kLog2e));
-}
+// 1 / (1 + 2^e): the sigmoid of -e log 2.
+__device__ __forceinline__ float sigmoid_of(float e) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(e)); }
+__device__ __forceinline__ float sigmoid(float z) { return sigmoid_of(z * -kLog2e); }
 
 // 1 - a^2 for a = 2^-v, v >= 0. At small v the difference would cancel: a polynomial for
 // (1 - 2^-2v) / v, interpolated at the six Chebyshev points of [0, 0.36] (1.2e-7 of the value in float32);
@@ -197,9 +198,10 @@ __device__ __forceinline__ void store_row(const Place<ET, V, L>& at, __amdgpu_bu
   }
 }
 
-// The scales of a tile's operands in 8 bits: a thread loads one of (operand, token), one tile before
-// they are put into LDS, which is one tile before their use.
-struct Scales {
+// The steps of a tile's operands in 8 bits (those of decay and gate times -log2 e, as the exponential of
+// their sigmoid takes them): a thread loads one of (operand, token), one tile before they are put into
+// LDS, which is one tile before their use.
+struct Steps {
   uint32_t held;
   __device__ __forceinline__ void load(const ScanParams& p, int b, int t0, int c0, int last) {
     const int which = threadIdx.x / kScanTile, row = min(int(threadIdx.x % kScanTile), last);
@@ -207,20 +209,14 @@ struct Scales {
     held = 0;
     if (which < 3 && t.sc != nullptr) held = t.sc[b * t.c0 + (t0 + row) * t.c1 + c0 / kScanScaleCols];
   }
-  __device__ __forceinline__ void put(uint8_t (&to)[3][kScanTile]) const {
+  __device__ __forceinline__ void put(float (&to)[3][kScanTile]) const {
     const int which = threadIdx.x / kScanTile;
-    if (which < 3) to[which][threadIdx.x % kScanTile] = uint8_t(held);
+    const float step = __uint_as_float(held << 23);
+    if (which < 3) to[which][threadIdx.x % kScanTile] = which == 0 ? step : step * -kLog2e;
   }
 };
-template <int L>
-struct RunScales {  // of a run's L tokens
-  uint32_t w[L / 4];
-  __device__ __forceinline__ void get(const uint8_t (&from)[kScanTile], int run) {
-#pragma unroll
-    for (int i = 0; i < L / 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(&from[run * L + 4 * i]);
-  }
-  __device__ __forceinline__ float step(int j) const { return __uint_as_float((w[j / 4] >> (8 * (j % 4)) & 0xffu) << 23); }
-};
+// A code plus 128 times a step, the 128 taken off: (code step) rounded once.
+__device__ __forceinline__ float held_value(float biased, float step) { return __builtin_fmaf(biased, step, -128.f * step); }
 
 // Document starts of a tile as a bit per token, one tile ahead of their use.
 struct Starts {
@@ -312,7 +308,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
   constexpr int L = kScanElems / V;
   __shared__ float maps[2][2][kScanWaves][kScanCols];  // [tile & 1][A, H]
   __shared__ uint64_t starts[2][Starts::kWords];
-  __shared__ __attribute__((aligned(16))) uint8_t scales[2][3][kScanTile];
+  __shared__ __attribute__((aligned(16))) float steps[PACKED ? 2 : 1][3][PACKED ? kScanTile : 1];
   const int nCols = (p.D + kScanCols - 1) / kScanCols;
   const int b = int(blockIdx.x) / nCols, c0 = (int(blockIdx.x) - b * nCols) * kScanCols, seg = blockIdx.y;
   const Lane<V> me(p.D, c0);
@@ -349,7 +345,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
   Rows<IT, V, L> rx[2], ra[2], rg[2];
   const Place<IT, V, L> px(p.x, me), pa(p.decay, me), pg(p.gate, me);
   const Place<ET, V, L> py(p.y, me);
-  Scales sc;
+  Steps sc;
   auto last_of = [&](int k) { return min(p.T - k * kScanTile, kScanTile) - 1; };
   auto fetch = [&](int k, Rows<IT, V, L>& x, Rows<IT, V, L>& a, Rows<IT, V, L>& g) {
     const int t0 = k * kScanTile, last = last_of(k);
@@ -359,7 +355,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
   };
   if constexpr (PACKED) {
     sc.load(p, b, k0 * kScanTile, c0, last_of(k0));
-    sc.put(scales[k0 & 1]);
+    sc.put(steps[k0 & 1]);
     if (k0 + 1 < k1) sc.load(p, b, (k0 + 1) * kScanTile, c0, last_of(k0 + 1));
   }
   fetch(k0, rx[0], ra[0], rg[0]);
@@ -370,12 +366,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
   auto tile = [&](int k, Rows<IT, V, L>& cx, Rows<IT, V, L>& ca, Rows<IT, V, L>& cgt) {
     const int t0 = k * kScanTile, last = last_of(k);
     float a[L][V], u[L][V];
-    RunScales<L> sx, sa, sg;
-    if constexpr (PACKED) {
-      sx.get(scales[k & 1][0], me.run);
-      sa.get(scales[k & 1][1], me.run);
-      sg.get(scales[k & 1][2], me.run);
-    }
+    auto step = [&](int which, int j) { return PACKED ? steps[k & 1][which][me.run * L + j] : 0.f; };
 #pragma unroll
     for (int j = 0; j < L; ++j) {
       float x[V], r[V], g[V];
@@ -383,8 +374,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
       ca.get(j, r);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if constexpr (PACKED) x[i] *= sx.step(j), r[i] *= sa.step(j);
-        const float s = sigmoid(r[i]);
+        if constexpr (PACKED) x[i] = held_value(x[i], step(0, j)), r[i] = held_value(r[i], step(1, j));
+        const float s = PACKED ? sigmoid_of(r[i]) : sigmoid(r[i]);
         const float v = rate[i] * s;
         a[j][i] = __builtin_amdgcn_exp2f(-v);
         u[j][i] = x[i] * __builtin_amdgcn_sqrtf(one_minus_square(v, a[j][i]));
@@ -393,8 +384,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
         cgt.get(j, g);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          if constexpr (PACKED) g[i] *= sg.step(j);
-          u[j][i] *= sigmoid(g[i]);
+          u[j][i] *= PACKED ? sigmoid_of(held_value(g[i], step(2, j))) : sigmoid(g[i]);
         }
       }
     }
@@ -434,7 +424,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
     if (k + 1 < k1) {
       if constexpr (DOCS) Starts::make(p, b, (k + 1) * kScanTile, starts[(k + 1) & 1]);
       if constexpr (PACKED) {
-        sc.put(scales[(k + 1) & 1]);
+        sc.put(steps[(k + 1) & 1]);
         if (k + 2 < k1) sc.load(p, b, (k + 2) * kScanTile, c0, last_of(k + 2));
       }
     }
@@ -502,7 +492,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
   constexpr int L = kScanElems / V;
   __shared__ float maps[2][MAPS ? 2 : 3][kScanWaves][kScanCols];  // [tile & 1][A, E, H]
   __shared__ uint64_t starts[2][Starts::kWords];
-  __shared__ __attribute__((aligned(16))) uint8_t scales[2][3][kScanTile];
+  __shared__ __attribute__((aligned(16))) float steps[PACKED ? 2 : 1][3][PACKED ? kScanTile : 1];
   const int nCols = (p.D + kScanCols - 1) / kScanCols;
   const int b = int(blockIdx.x) / nCols, c0 = (int(blockIdx.x) - b * nCols) * kScanCols;
   const int seg = int(blockIdx.y) + (MAPS ? 1 : 0);
@@ -543,7 +533,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
   Rows<ET, V, L> rd;
   const Place<IT, V, L> px(p.x, me), pa(p.decay, me), pg(p.gate, me);
   const Place<ET, V, L> pd(p.dy, me), pdx(p.dx, me), pda(p.ddecay, me), pdg(p.dgate, me);
-  Scales sc;
+  Steps sc;
   float kept[V];
   auto last_of = [&](int k) { return min(p.T - k * kScanTile, kScanTile) - 1; };
   auto fetch = [&](int k) {
@@ -560,7 +550,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
   };
   if constexpr (PACKED) {
     sc.load(p, b, (k1 - 1) * kScanTile, c0, last_of(k1 - 1));
-    sc.put(scales[(k1 - 1) & 1]);
+    sc.put(steps[(k1 - 1) & 1]);
     if (k1 - 1 > k0) sc.load(p, b, (k1 - 2) * kScanTile, c0, last_of(k1 - 2));
   }
   fetch(k1 - 1);
@@ -570,12 +560,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
     const int t0 = k * kScanTile, last = last_of(k);
     // f: what passes a token (a, or 0 where it starts a document); w = b sigmoid(gate); c = sigmoid(gate) a^2 / b
     float a[L][V], s[L][V], w[L][V], c[L][V], sg[L][V], x[L][V], hb[L][V], dy[L][V], hk[V];
-    RunScales<L> sx, sa, sgt;
-    if constexpr (PACKED) {
-      sx.get(scales[k & 1][0], me.run);
-      sa.get(scales[k & 1][1], me.run);
-      sgt.get(scales[k & 1][2], me.run);
-    }
+    auto step = [&](int which, int j) { return PACKED ? steps[k & 1][which][me.run * L + j] : 0.f; };
 #pragma unroll
     for (int j = 0; j < L; ++j) {
       float r[V];
@@ -583,8 +568,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
       rd.get(j, dy[j]);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if constexpr (PACKED) r[i] *= sa.step(j);
-        s[j][i] = sigmoid(r[i]);
+        s[j][i] = PACKED ? sigmoid_of(held_value(r[i], step(1, j))) : sigmoid(r[i]);
       }
       if constexpr (!MAPS) {
         rx.get(j, x[j]);
@@ -594,13 +578,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
           rg.get(j, sg[j]);
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            if constexpr (PACKED) sg[j][i] *= sgt.step(j);
-            sg[j][i] = sigmoid(sg[j][i]);
+            sg[j][i] = PACKED ? sigmoid_of(held_value(sg[j][i], step(2, j))) : sigmoid(sg[j][i]);
           }
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          if constexpr (PACKED) x[j][i] *= sx.step(j);
+          if constexpr (PACKED) x[j][i] = held_value(x[j][i], step(0, j));
           const Decay d = decay_of(s[j][i], rate[i]);
           a[j][i] = d.a;
           w[j][i] = d.b * sg[j][i];
@@ -666,7 +649,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
     if (k > k0) {
       if constexpr (DOCS) Starts::make(p, b, (k - 1) * kScanTile, starts[(k - 1) & 1]);
       if constexpr (PACKED) {
-        sc.put(scales[(k - 1) & 1]);
+        sc.put(steps[(k - 1) & 1]);
         if (k - 1 > k0) sc.load(p, b, (k - 2) * kScanTile, c0, last_of(k - 2));
       }
     }
