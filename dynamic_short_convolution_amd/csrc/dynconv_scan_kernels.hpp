@@ -154,9 +154,14 @@ struct Place {
     pitch = uint32_t(t.s1) * uint32_t(sizeof(ET));
     off = me.ok ? uint32_t(me.run * L) * pitch + uint32_t(me.chl) * uint32_t(sizeof(ET)) : kNowhere;
   }
-  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const ScanTensor& t, int b, int t0, int c0, int last, int D) const {
-    const char* base = static_cast<const char*>(t.p) + (b * t.s0 + t0 * t.s1 + c0) * int64_t(sizeof(ET));
-    const uint32_t range = uint32_t(last) * pitch + uint32_t(min(D - c0, kScanCols)) * uint32_t(sizeof(ET));
+  // Of tile k of k0 .. k1 - 1, or (another one, or no tensor) an empty range. Accesses without a branch
+  // around them: where paths with and without loads meet, the compiler has to wait as if the later
+  // ones had not been issued, which would undo the loads ahead.
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const ScanTensor& t, int b, int k, int k0, int k1, int c0, int T, int D) const {
+    const char* base = static_cast<const char*>(t.p) + (b * t.s0 + int64_t(k) * kScanTile * t.s1 + c0) * int64_t(sizeof(ET));
+    const int last = min(T - k * kScanTile, kScanTile) - 1;
+    uint32_t range = uint32_t(last) * pitch + uint32_t(min(D - c0, kScanCols)) * uint32_t(sizeof(ET));
+    if (t.p == nullptr || k < k0 || k >= k1) range = 0;
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, int(range), 0x00027000);
   }
 };
@@ -203,11 +208,13 @@ __device__ __forceinline__ void store_row(const Place<ET, V, L>& at, __amdgpu_bu
 // LDS, which is one tile before their use.
 struct Steps {
   uint32_t held;
-  __device__ __forceinline__ void load(const ScanParams& p, int b, int t0, int c0, int last) {
-    const int which = threadIdx.x / kScanTile, row = min(int(threadIdx.x % kScanTile), last);
-    const ScanTensor& t = which == 0 ? p.x : which == 1 ? p.decay : p.gate;
-    held = 0;
-    if (which < 3 && t.sc != nullptr) held = t.sc[b * t.c0 + (t0 + row) * t.c1 + c0 / kScanScaleCols];
+  __device__ __forceinline__ void load(const ScanParams& p, int b, int k, int c0) {
+    const int which = threadIdx.x / kScanTile;
+    const int64_t row = min(k * kScanTile + int(threadIdx.x % kScanTile), p.T - 1);
+    const uint8_t* sc = p.x.sc + (b * p.x.c0 + row * p.x.c1);
+    if (which == 1) sc = p.decay.sc + (b * p.decay.c0 + row * p.decay.c1);
+    if (which == 2 && p.gate.sc != nullptr) sc = p.gate.sc + (b * p.gate.c0 + row * p.gate.c1);
+    held = sc[c0 / kScanScaleCols];
   }
   __device__ __forceinline__ void put(float (&to)[3][kScanTile]) const {
     const int which = threadIdx.x / kScanTile;
@@ -218,20 +225,22 @@ struct Steps {
 // A code plus 128 times a step, the 128 taken off: (code step) rounded once.
 __device__ __forceinline__ float held_value(float biased, float step) { return __builtin_fmaf(biased, step, -128.f * step); }
 
-// Document starts of a tile as a bit per token, one tile ahead of their use.
+// Document starts of a tile as a bit per token: a thread loads a token's id and the one before, one tile
+// before the bits are put into LDS, which is one tile before their use.
 struct Starts {
   static constexpr int kWords = kScanTile / 64;
-  static __device__ __forceinline__ void make(const ScanParams& p, int b, int t0, uint64_t* bits) {
-    if (threadIdx.x < kScanTile) {
-      const int t = t0 + int(threadIdx.x);
-      bool first = false;
-      if (t > 0 && t < p.T) {
-        const int32_t* s = p.seg + b * p.ss0 + t * p.ss1;
-        first = s[0] != s[-p.ss1];
-      }
-      const uint64_t m = __ballot(first);
-      if ((threadIdx.x & 63) == 0) bits[threadIdx.x >> 6] = m;
-    }
+  int32_t id, before;
+  bool counts;
+  __device__ __forceinline__ void load(const ScanParams& p, int b, int k) {
+    const int t = k * kScanTile + int(threadIdx.x % kScanTile), at = min(t, p.T - 1);
+    const int32_t* s = p.seg + b * p.ss0;
+    id = s[at * p.ss1];
+    before = s[max(at - 1, 0) * p.ss1];
+    counts = t < p.T;  // token 0 differs from no id before it
+  }
+  __device__ __forceinline__ void put(uint64_t* bits) const {
+    const uint64_t m = __ballot(counts && id != before);
+    if (threadIdx.x < kScanTile && (threadIdx.x & 63) == 0) bits[threadIdx.x >> 6] = m;
   }
   // The L bits of a run that lies in one word.
   static __device__ __forceinline__ uint32_t of_run(const uint64_t* bits, int run, int L) {
@@ -346,30 +355,35 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
   const Place<IT, V, L> px(p.x, me), pa(p.decay, me), pg(p.gate, me);
   const Place<ET, V, L> py(p.y, me);
   Steps sc;
-  auto last_of = [&](int k) { return min(p.T - k * kScanTile, kScanTile) - 1; };
+  Starts first;
   auto fetch = [&](int k, Rows<IT, V, L>& x, Rows<IT, V, L>& a, Rows<IT, V, L>& g) {
-    const int t0 = k * kScanTile, last = last_of(k);
-    x.load(px, px.rows(p.x, b, t0, c0, last, p.D));
-    a.load(pa, pa.rows(p.decay, b, t0, c0, last, p.D));
-    if (gated) g.load(pg, pg.rows(p.gate, b, t0, c0, last, p.D));
+    x.load(px, px.rows(p.x, b, k, k0, k1, c0, p.T, p.D));
+    a.load(pa, pa.rows(p.decay, b, k, k0, k1, c0, p.T, p.D));
+    g.load(pg, pg.rows(p.gate, b, k, k0, k1, c0, p.T, p.D));
   };
   if constexpr (PACKED) {
-    sc.load(p, b, k0 * kScanTile, c0, last_of(k0));
+    sc.load(p, b, k0, c0);
     sc.put(steps[k0 & 1]);
-    if (k0 + 1 < k1) sc.load(p, b, (k0 + 1) * kScanTile, c0, last_of(k0 + 1));
+    sc.load(p, b, k0 + 1, c0);
+  }
+  if constexpr (DOCS) {
+    first.load(p, b, k0);
+    first.put(starts[k0 & 1]);
+    first.load(p, b, k0 + 1);
   }
   fetch(k0, rx[0], ra[0], rg[0]);
-  if (k0 + 1 < k1) fetch(k0 + 1, rx[1], ra[1], rg[1]);
-  if constexpr (DOCS) Starts::make(p, b, k0 * kScanTile, starts[k0 & 1]);
+  __builtin_amdgcn_sched_barrier(0);  // the loads return in order: those of the first tile first
+  fetch(k0 + 1, rx[1], ra[1], rg[1]);
+  __builtin_amdgcn_sched_barrier(0);
   if constexpr (DOCS || PACKED) __syncthreads();
 
   auto tile = [&](int k, Rows<IT, V, L>& cx, Rows<IT, V, L>& ca, Rows<IT, V, L>& cgt) {
-    const int t0 = k * kScanTile, last = last_of(k);
+    const int t0 = k * kScanTile, last = min(p.T - t0, kScanTile) - 1;
     float a[L][V], u[L][V];
     auto step = [&](int which, int j) { return PACKED ? steps[k & 1][which][me.run * L + j] : 0.f; };
 #pragma unroll
     for (int j = 0; j < L; ++j) {
-      float x[V], r[V], g[V];
+      float x[V], r[V];
       cx.get(j, x);
       ca.get(j, r);
 #pragma unroll
@@ -380,15 +394,17 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
         a[j][i] = __builtin_amdgcn_exp2f(-v);
         u[j][i] = x[i] * __builtin_amdgcn_sqrtf(one_minus_square(v, a[j][i]));
       }
-      if (gated) {
+    }
+    if (gated) {  // one branch: between branches the tokens' chains could not be interleaved
+#pragma unroll
+      for (int j = 0; j < L; ++j) {
+        float g[V];
         cgt.get(j, g);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          u[j][i] *= PACKED ? sigmoid_of(held_value(g[i], step(2, j))) : sigmoid(g[i]);
-        }
+        for (int i = 0; i < V; ++i) u[j][i] *= PACKED ? sigmoid_of(held_value(g[i], step(2, j))) : sigmoid(g[i]);
       }
     }
-    if (k + 2 < k1) fetch(k + 2, cx, ca, cgt);
+    fetch(k + 2, cx, ca, cgt);
     if (last < kScanTile - 1) {  // tokens that do not exist leave the state as it is
 #pragma unroll
       for (int j = 0; j < L; ++j)
@@ -421,12 +437,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
       write_map<V>(maps[k & 1][0][me.wave], me.chl, A);
       write_map<V>(maps[k & 1][1][me.wave], me.chl, H);
     }
-    if (k + 1 < k1) {
-      if constexpr (DOCS) Starts::make(p, b, (k + 1) * kScanTile, starts[(k + 1) & 1]);
-      if constexpr (PACKED) {
-        sc.put(steps[(k + 1) & 1]);
-        if (k + 2 < k1) sc.load(p, b, (k + 2) * kScanTile, c0, last_of(k + 2));
-      }
+    if constexpr (DOCS) {
+      first.put(starts[(k + 1) & 1]);
+      first.load(p, b, k + 2);
+    }
+    if constexpr (PACKED) {
+      sc.put(steps[(k + 1) & 1]);
+      sc.load(p, b, k + 2, c0);
     }
     __syncthreads();  // what is overwritten next was read before the barrier before
     float h[V];
@@ -452,22 +469,22 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) out[i] = h[i];
       }
-      if (p.y.p != nullptr) {
-        const __amdgpu_buffer_rsrc_t ry = py.rows(p.y, b, t0, c0, last, p.D);
+      const __amdgpu_buffer_rsrc_t ry = py.rows(p.y, b, k, k0, k1, c0, p.T, p.D);  // empty where only the states are wanted
 #pragma unroll
-        for (int i = 0; i < V; ++i) h[i] = through<DOCS>(pA[i], pH[i], h[i]);
+      for (int i = 0; i < V; ++i) h[i] = through<DOCS>(pA[i], pH[i], h[i]);
 #pragma unroll
-        for (int j = 0; j < L; ++j) {
+      for (int j = 0; j < L; ++j) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) h[i] = through<DOCS>(a[j][i], u[j][i], h[i]);
-          store_row(py, ry, j, h);
-        }
+        for (int i = 0; i < V; ++i) h[i] = through<DOCS>(a[j][i], u[j][i], h[i]);
+        store_row(py, ry, j, h);
       }
     }
   };
-  for (int k = k0; k < k1; k += 2) {
+  for (int k = k0;; k += 2) {
     tile(k, rx[0], ra[0], rg[0]);
-    if (k + 1 < k1) tile(k + 1, rx[1], ra[1], rg[1]);
+    if (k + 1 >= k1) break;
+    tile(k + 1, rx[1], ra[1], rg[1]);
+    if (k + 2 >= k1) break;
   }
   if (!me.ok || threadIdx.x >= Lane<V>::kLanes) return;
   if constexpr (MAPS) {
@@ -534,30 +551,33 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
   const Place<IT, V, L> px(p.x, me), pa(p.decay, me), pg(p.gate, me);
   const Place<ET, V, L> pd(p.dy, me), pdx(p.dx, me), pda(p.ddecay, me), pdg(p.dgate, me);
   Steps sc;
+  Starts begin;
   float kept[V];
-  auto last_of = [&](int k) { return min(p.T - k * kScanTile, kScanTile) - 1; };
   auto fetch = [&](int k) {
-    const int t0 = k * kScanTile, last = last_of(k);
-    ra.load(pa, pa.rows(p.decay, b, t0, c0, last, p.D));
-    rd.load(pd, pd.rows(p.dy, b, t0, c0, last, p.D));
+    ra.load(pa, pa.rows(p.decay, b, k, k0, k1, c0, p.T, p.D));
+    rd.load(pd, pd.rows(p.dy, b, k, k0, k1, c0, p.T, p.D));
     if constexpr (!MAPS) {
-      rx.load(px, px.rows(p.x, b, t0, c0, last, p.D));
-      if (gated) rg.load(pg, pg.rows(p.gate, b, t0, c0, last, p.D));
-      const float* c = p.chunks + (int64_t(b) * nTiles + k) * p.D + cg;
+      rx.load(px, px.rows(p.x, b, k, k0, k1, c0, p.T, p.D));
+      rg.load(pg, pg.rows(p.gate, b, k, k0, k1, c0, p.T, p.D));
+      const float* c = p.chunks + (int64_t(b) * nTiles + max(k, k0)) * p.D + cg;
 #pragma unroll
       for (int i = 0; i < V; ++i) kept[i] = c[i];
     }
   };
   if constexpr (PACKED) {
-    sc.load(p, b, (k1 - 1) * kScanTile, c0, last_of(k1 - 1));
+    sc.load(p, b, k1 - 1, c0);
     sc.put(steps[(k1 - 1) & 1]);
-    if (k1 - 1 > k0) sc.load(p, b, (k1 - 2) * kScanTile, c0, last_of(k1 - 2));
+    sc.load(p, b, max(k1 - 2, k0), c0);
+  }
+  if constexpr (DOCS) {
+    begin.load(p, b, k1 - 1);
+    begin.put(starts[(k1 - 1) & 1]);
+    begin.load(p, b, max(k1 - 2, k0));
   }
   fetch(k1 - 1);
-  if constexpr (DOCS) Starts::make(p, b, (k1 - 1) * kScanTile, starts[(k1 - 1) & 1]);
   if constexpr (DOCS || PACKED) __syncthreads();
   for (int k = k1 - 1; k >= k0; --k) {
-    const int t0 = k * kScanTile, last = last_of(k);
+    const int t0 = k * kScanTile, last = min(p.T - t0, kScanTile) - 1;
     // f: what passes a token (a, or 0 where it starts a document); w = b sigmoid(gate); c = sigmoid(gate) a^2 / b
     float a[L][V], s[L][V], w[L][V], c[L][V], sg[L][V], x[L][V], hb[L][V], dy[L][V], hk[V];
     auto step = [&](int which, int j) { return PACKED ? steps[k & 1][which][me.run * L + j] : 0.f; };
@@ -573,25 +593,31 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
       if constexpr (!MAPS) {
         rx.get(j, x[j]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) sg[j][i] = 1.f;
-        if (gated) {
-          rg.get(j, sg[j]);
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            sg[j][i] = PACKED ? sigmoid_of(held_value(sg[j][i], step(2, j))) : sigmoid(sg[j][i]);
-          }
-        }
-#pragma unroll
         for (int i = 0; i < V; ++i) {
           if constexpr (PACKED) x[j][i] = held_value(x[j][i], step(0, j));
           const Decay d = decay_of(s[j][i], rate[i]);
           a[j][i] = d.a;
-          w[j][i] = d.b * sg[j][i];
-          c[j][i] = d.a * d.a * d.rb * sg[j][i];
+          w[j][i] = d.b;
+          c[j][i] = d.a * d.a * d.rb;
+          sg[j][i] = 1.f;
         }
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) a[j][i] = __builtin_amdgcn_exp2f(-(rate[i] * s[j][i]));
+      }
+    }
+    if constexpr (!MAPS) {
+      if (gated) {  // one branch: between branches the tokens' chains could not be interleaved
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+          rg.get(j, sg[j]);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            sg[j][i] = PACKED ? sigmoid_of(held_value(sg[j][i], step(2, j))) : sigmoid(sg[j][i]);
+            w[j][i] *= sg[j][i];
+            c[j][i] *= sg[j][i];
+          }
+        }
       }
     }
     if (last < kScanTile - 1) {
@@ -612,7 +638,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) hk[i] = MAPS ? 0.f : kept[i];
-    if (k > k0) fetch(k - 1);
+    fetch(k - 1);
     uint32_t first = 0;  // tokens that start a document: nothing passes through them, forwards or backwards
     if constexpr (DOCS) first = Starts::of_run(starts[k & 1], me.run, L);
     auto pass = [&](int j, int i) { return DOCS && (first >> j & 1) ? 0.f : a[j][i]; };
@@ -646,12 +672,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
       scan_groups<V, DOCS, false>(me, A, H, pA, pH);
       if (me.group == Lane<V>::kGroups - 1) write_map<V>(maps[k & 1][2][me.wave], me.chl, H);
     }
-    if (k > k0) {
-      if constexpr (DOCS) Starts::make(p, b, (k - 1) * kScanTile, starts[(k - 1) & 1]);
-      if constexpr (PACKED) {
-        sc.put(steps[(k - 1) & 1]);
-        if (k - 1 > k0) sc.load(p, b, (k - 2) * kScanTile, c0, last_of(k - 2));
-      }
+    if constexpr (DOCS) {
+      begin.put(starts[(k - 1) & 1]);
+      begin.load(p, b, max(k - 2, k0));
+    }
+    if constexpr (PACKED) {
+      sc.put(steps[(k - 1) & 1]);
+      sc.load(p, b, max(k - 2, k0), c0);
     }
     __syncthreads();
     float e[V], h[V];
@@ -691,8 +718,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
           h[i] = through<DOCS>(f, hb[j][i], h[i]);
           hb[j][i] = before;
         }
-      const __amdgpu_buffer_rsrc_t rdx = pdx.rows(p.dx, b, t0, c0, last, p.D), rda = pda.rows(p.ddecay, b, t0, c0, last, p.D);
-      const __amdgpu_buffer_rsrc_t rdg = pdg.rows(p.dgate, b, t0, c0, last, p.D);
+      const __amdgpu_buffer_rsrc_t rdx = pdx.rows(p.dx, b, k, k0, k1, c0, p.T, p.D);
+      const __amdgpu_buffer_rsrc_t rda = pda.rows(p.ddecay, b, k, k0, k1, c0, p.T, p.D);
+      const __amdgpu_buffer_rsrc_t rdg = pdg.rows(p.dgate, b, k, k0, k1, c0, p.T, p.D);
       float sum[V], back[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) sum[i] = 0.f, back[i] = rate[i] * -0.693147180559945309417f;  // of log 2
@@ -712,7 +740,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
         }
         store_row(pdx, rdx, j, dx);
         store_row(pda, rda, j, dr);
-        if (gated) store_row(pdg, rdg, j, dg);
+        store_row(pdg, rdg, j, dg);
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) drate[i] += double(sum[i]);  // 64 bits: of any number of tiles
