@@ -309,7 +309,9 @@ __device__ __forceinline__ void write_map(float (&m)[kScanCols], int chl, const 
 }
 
 // ---------------------------------------------------------------------------------
-// Forward. MAPS: only the map of the segment, into p.maps; with segment 0 the initial state too.
+// Forward. MAPS: only the map of the segment, into p.maps; with segment 0 the initial state too. That pass
+// goes from the last tile to the first, so that what it read last, which the memory-side cache still
+// holds, is what the pass behind it reads first.
 // ---------------------------------------------------------------------------------
 template <typename ET, int V, bool PACKED, bool DOCS, bool MAPS>
 __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
@@ -356,31 +358,35 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
   const Place<ET, V, L> py(p.y, me);
   Steps sc;
   Starts first;
-  auto fetch = [&](int k, Rows<IT, V, L>& x, Rows<IT, V, L>& a, Rows<IT, V, L>& g) {
+  const int n = k1 - k0;
+  auto order = [&](int i) { return MAPS ? k1 - 1 - i : k0 + i; };  // the tile of turn i
+  auto real = [&](int i) { return order(min(i, n - 1)); };
+  auto fetch = [&](int i, Rows<IT, V, L>& x, Rows<IT, V, L>& a, Rows<IT, V, L>& g) {
+    const int k = order(i);
     x.load(px, px.rows(p.x, b, k, k0, k1, c0, p.T, p.D));
     a.load(pa, pa.rows(p.decay, b, k, k0, k1, c0, p.T, p.D));
     g.load(pg, pg.rows(p.gate, b, k, k0, k1, c0, p.T, p.D));
   };
   if constexpr (PACKED) {
-    sc.load(p, b, k0, c0);
-    sc.put(steps[k0 & 1]);
-    sc.load(p, b, k0 + 1, c0);
+    sc.load(p, b, real(0), c0);
+    sc.put(steps[0]);
+    sc.load(p, b, real(1), c0);
   }
   if constexpr (DOCS) {
-    first.load(p, b, k0);
-    first.put(starts[k0 & 1]);
-    first.load(p, b, k0 + 1);
+    first.load(p, b, real(0));
+    first.put(starts[0]);
+    first.load(p, b, real(1));
   }
-  fetch(k0, rx[0], ra[0], rg[0]);
+  fetch(0, rx[0], ra[0], rg[0]);
   __builtin_amdgcn_sched_barrier(0);  // the loads return in order: those of the first tile first
-  fetch(k0 + 1, rx[1], ra[1], rg[1]);
+  fetch(1, rx[1], ra[1], rg[1]);
   __builtin_amdgcn_sched_barrier(0);
   if constexpr (DOCS || PACKED) __syncthreads();
 
-  auto tile = [&](int k, Rows<IT, V, L>& cx, Rows<IT, V, L>& ca, Rows<IT, V, L>& cgt) {
-    const int t0 = k * kScanTile, last = min(p.T - t0, kScanTile) - 1;
+  auto tile = [&](int i, Rows<IT, V, L>& cx, Rows<IT, V, L>& ca, Rows<IT, V, L>& cgt) {
+    const int k = order(i), t0 = k * kScanTile, last = min(p.T - t0, kScanTile) - 1, half = i & 1;
     float a[L][V], u[L][V];
-    auto step = [&](int which, int j) { return PACKED ? steps[k & 1][which][me.run * L + j] : 0.f; };
+    auto step = [&](int which, int j) { return PACKED ? steps[half][which][me.run * L + j] : 0.f; };
 #pragma unroll
     for (int j = 0; j < L; ++j) {
       float x[V], r[V];
@@ -404,7 +410,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
         for (int i = 0; i < V; ++i) u[j][i] *= PACKED ? sigmoid_of(held_value(g[i], step(2, j))) : sigmoid(g[i]);
       }
     }
-    fetch(k + 2, cx, ca, cgt);
+    fetch(i + 2, cx, ca, cgt);
     if (last < kScanTile - 1) {  // tokens that do not exist leave the state as it is
 #pragma unroll
       for (int j = 0; j < L; ++j)
@@ -415,7 +421,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
         }
     }
     if constexpr (DOCS) {
-      const uint32_t m = Starts::of_run(starts[k & 1], me.run, L);
+      const uint32_t m = Starts::of_run(starts[half], me.run, L);
 #pragma unroll
       for (int j = 0; j < L; ++j)
 #pragma unroll
@@ -434,31 +440,44 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
     float pA[V], pH[V];  // the map of the lane groups before this one
     scan_groups<V, DOCS, false>(me, A, H, pA, pH);
     if (me.group == Lane<V>::kGroups - 1) {
-      write_map<V>(maps[k & 1][0][me.wave], me.chl, A);
-      write_map<V>(maps[k & 1][1][me.wave], me.chl, H);
+      write_map<V>(maps[half][0][me.wave], me.chl, A);
+      write_map<V>(maps[half][1][me.wave], me.chl, H);
     }
     if constexpr (DOCS) {
-      first.put(starts[(k + 1) & 1]);
-      first.load(p, b, k + 2);
+      first.put(starts[half ^ 1]);
+      first.load(p, b, real(i + 2));
     }
     if constexpr (PACKED) {
-      sc.put(steps[(k + 1) & 1]);
-      sc.load(p, b, k + 2, c0);
+      sc.put(steps[half ^ 1]);
+      sc.load(p, b, real(i + 2), c0);
     }
     __syncthreads();  // what is overwritten next was read before the barrier before
     float h[V];
+    if constexpr (MAPS) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = carry[i];
+      for (int q = kScanWaves - 1; q >= 0; --q) {
+        float fA[V], fH[V];
+        read_map<V>(maps[half][0][q], me.chl, fA);
+        read_map<V>(maps[half][1][q], me.chl, fH);
 #pragma unroll
-    for (int w = 0; w < kScanWaves; ++w) {
-      float fA[V], fH[V];
-      read_map<V>(maps[k & 1][0][w], me.chl, fA);
-      read_map<V>(maps[k & 1][1][w], me.chl, fH);
+        for (int c = 0; c < V; ++c) {
+          carry[c] = through<DOCS>(total[c], carry[c], fH[c]);
+          total[c] = chain<DOCS>(total[c], fA[c]);
+        }
+      }
+    } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        carry[i] = through<DOCS>(fA[i], fH[i], carry[i]);
-        if (w < kScanWaves - 1) h[i] = w < me.wave ? carry[i] : h[i];
-        if constexpr (MAPS) total[i] = chain<DOCS>(fA[i], total[i]);
+      for (int c = 0; c < V; ++c) h[c] = carry[c];
+#pragma unroll
+      for (int q = 0; q < kScanWaves; ++q) {
+        float fA[V], fH[V];
+        read_map<V>(maps[half][0][q], me.chl, fA);
+        read_map<V>(maps[half][1][q], me.chl, fH);
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          carry[c] = through<DOCS>(fA[c], fH[c], carry[c]);
+          if (q < kScanWaves - 1) h[c] = q < me.wave ? carry[c] : h[c];
+        }
       }
     }
     if constexpr (!MAPS) {
@@ -480,11 +499,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
       }
     }
   };
-  for (int k = k0;; k += 2) {
-    tile(k, rx[0], ra[0], rg[0]);
-    if (k + 1 >= k1) break;
-    tile(k + 1, rx[1], ra[1], rg[1]);
-    if (k + 2 >= k1) break;
+  for (int i = 0;; i += 2) {
+    tile(i, rx[0], ra[0], rg[0]);
+    if (i + 1 >= n) break;
+    tile(i + 1, rx[1], ra[1], rg[1]);
+    if (i + 2 >= n) break;
   }
   if (!me.ok || threadIdx.x >= Lane<V>::kLanes) return;
   if constexpr (MAPS) {
@@ -501,7 +520,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
 }
 
 // ---------------------------------------------------------------------------------
-// Backward, tiles from the last to the first. MAPS: only the segment's map of e.
+// Backward, tiles from the last to the first. MAPS: only the segment's map of e, from the first to the last.
 // ---------------------------------------------------------------------------------
 template <typename ET, int V, bool PACKED, bool DOCS, bool MAPS>
 __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
@@ -545,7 +564,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
     for (int i = 0; i < V; ++i) carry[i] = p.dstate_out[b * p.dsos + cg + i];
   }
   const int nTiles = (p.T + kScanTile - 1) / kScanTile;
-  const int k0 = seg * p.segTiles, k1 = min(nTiles, k0 + p.segTiles);
+  const int k0 = seg * p.segTiles, k1 = min(nTiles, k0 + p.segTiles), n = k1 - k0;
+  auto order = [&](int i) { return MAPS ? k0 + i : k1 - 1 - i; };  // the tile of turn i
+  auto real = [&](int i) { return order(min(i, n - 1)); };
   Rows<IT, V, L> rx, ra, rg;
   Rows<ET, V, L> rd;
   const Place<IT, V, L> px(p.x, me), pa(p.decay, me), pg(p.gate, me);
@@ -553,34 +574,35 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
   Steps sc;
   Starts begin;
   float kept[V];
-  auto fetch = [&](int k) {
+  auto fetch = [&](int i) {
+    const int k = order(i);
     ra.load(pa, pa.rows(p.decay, b, k, k0, k1, c0, p.T, p.D));
     rd.load(pd, pd.rows(p.dy, b, k, k0, k1, c0, p.T, p.D));
     if constexpr (!MAPS) {
       rx.load(px, px.rows(p.x, b, k, k0, k1, c0, p.T, p.D));
       rg.load(pg, pg.rows(p.gate, b, k, k0, k1, c0, p.T, p.D));
-      const float* c = p.chunks + (int64_t(b) * nTiles + max(k, k0)) * p.D + cg;
+      const float* c = p.chunks + (int64_t(b) * nTiles + real(i)) * p.D + cg;
 #pragma unroll
-      for (int i = 0; i < V; ++i) kept[i] = c[i];
+      for (int v = 0; v < V; ++v) kept[v] = c[v];
     }
   };
   if constexpr (PACKED) {
-    sc.load(p, b, k1 - 1, c0);
-    sc.put(steps[(k1 - 1) & 1]);
-    sc.load(p, b, max(k1 - 2, k0), c0);
+    sc.load(p, b, real(0), c0);
+    sc.put(steps[0]);
+    sc.load(p, b, real(1), c0);
   }
   if constexpr (DOCS) {
-    begin.load(p, b, k1 - 1);
-    begin.put(starts[(k1 - 1) & 1]);
-    begin.load(p, b, max(k1 - 2, k0));
+    begin.load(p, b, real(0));
+    begin.put(starts[0]);
+    begin.load(p, b, real(1));
   }
-  fetch(k1 - 1);
+  fetch(0);
   if constexpr (DOCS || PACKED) __syncthreads();
-  for (int k = k1 - 1; k >= k0; --k) {
-    const int t0 = k * kScanTile, last = min(p.T - t0, kScanTile) - 1;
+  for (int turn = 0; turn < n; ++turn) {
+    const int k = order(turn), t0 = k * kScanTile, last = min(p.T - t0, kScanTile) - 1, half = turn & 1;
     // f: what passes a token (a, or 0 where it starts a document); w = b sigmoid(gate); c = sigmoid(gate) a^2 / b
     float a[L][V], s[L][V], w[L][V], c[L][V], sg[L][V], x[L][V], hb[L][V], dy[L][V], hk[V];
-    auto step = [&](int which, int j) { return PACKED ? steps[k & 1][which][me.run * L + j] : 0.f; };
+    auto step = [&](int which, int j) { return PACKED ? steps[half][which][me.run * L + j] : 0.f; };
 #pragma unroll
     for (int j = 0; j < L; ++j) {
       float r[V];
@@ -638,9 +660,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) hk[i] = MAPS ? 0.f : kept[i];
-    fetch(k - 1);
+    fetch(turn + 1);
     uint32_t first = 0;  // tokens that start a document: nothing passes through them, forwards or backwards
-    if constexpr (DOCS) first = Starts::of_run(starts[k & 1], me.run, L);
+    if constexpr (DOCS) first = Starts::of_run(starts[half], me.run, L);
     auto pass = [&](int j, int i) { return DOCS && (first >> j & 1) ? 0.f : a[j][i]; };
     float A[V], H[V], E[V];
 #pragma unroll
@@ -665,43 +687,56 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
     for (int i = 0; i < V; ++i) B[i] = A[i];
     scan_groups<V, DOCS, true>(me, B, E, rA, rE);
     if (me.group == 0) {
-      write_map<V>(maps[k & 1][0][me.wave], me.chl, B);
-      write_map<V>(maps[k & 1][1][me.wave], me.chl, E);
+      write_map<V>(maps[half][0][me.wave], me.chl, B);
+      write_map<V>(maps[half][1][me.wave], me.chl, E);
     }
     if constexpr (!MAPS) {
       scan_groups<V, DOCS, false>(me, A, H, pA, pH);
-      if (me.group == Lane<V>::kGroups - 1) write_map<V>(maps[k & 1][2][me.wave], me.chl, H);
+      if (me.group == Lane<V>::kGroups - 1) write_map<V>(maps[half][2][me.wave], me.chl, H);
     }
     if constexpr (DOCS) {
-      begin.put(starts[(k - 1) & 1]);
-      begin.load(p, b, max(k - 2, k0));
+      begin.put(starts[half ^ 1]);
+      begin.load(p, b, real(turn + 2));
     }
     if constexpr (PACKED) {
-      sc.put(steps[(k - 1) & 1]);
-      sc.load(p, b, max(k - 2, k0), c0);
+      sc.put(steps[half ^ 1]);
+      sc.load(p, b, real(turn + 2), c0);
     }
     __syncthreads();
     float e[V], h[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) e[i] = carry[i], h[i] = hk[i];
+    if constexpr (MAPS) {
 #pragma unroll 2
-    for (int q = kScanWaves - 1; q >= 0; --q) {
-      float fA[V], fE[V];
-      read_map<V>(maps[k & 1][0][q], me.chl, fA);
-      read_map<V>(maps[k & 1][1][q], me.chl, fE);
+      for (int q = 0; q < kScanWaves; ++q) {
+        float fA[V], fE[V];
+        read_map<V>(maps[half][0][q], me.chl, fA);
+        read_map<V>(maps[half][1][q], me.chl, fE);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        carry[i] = through<DOCS>(fA[i], fE[i], carry[i]);
-        e[i] = q > me.wave ? carry[i] : e[i];
-        if constexpr (MAPS) total[i] = chain<DOCS>(fA[i], total[i]);
+        for (int i = 0; i < V; ++i) {
+          carry[i] = through<DOCS>(total[i], carry[i], fE[i]);
+          total[i] = chain<DOCS>(total[i], fA[i]);
+        }
+      }
+    } else {
+#pragma unroll 2
+      for (int q = kScanWaves - 1; q >= 0; --q) {
+        float fA[V], fE[V];
+        read_map<V>(maps[half][0][q], me.chl, fA);
+        read_map<V>(maps[half][1][q], me.chl, fE);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          carry[i] = through<DOCS>(fA[i], fE[i], carry[i]);
+          e[i] = q > me.wave ? carry[i] : e[i];
+        }
       }
     }
     if constexpr (!MAPS) {
 #pragma unroll 2
       for (int q = 0; q < kScanWaves; ++q) {
         float fA[V], fH[V];
-        read_map<V>(maps[k & 1][0][q], me.chl, fA);
-        read_map<V>(maps[k & 1][2][q], me.chl, fH);
+        read_map<V>(maps[half][0][q], me.chl, fA);
+        read_map<V>(maps[half][2][q], me.chl, fH);
 #pragma unroll
         for (int i = 0; i < V; ++i) h[i] = q < me.wave ? through<DOCS>(fA[i], fH[i], h[i]) : h[i];
       }
