@@ -13,7 +13,7 @@ constexpr int kThreads = 256;
 
 // mean and 1 / sqrt(var + eps) of a (sequence, group) from its chunks' sums: a wave each, in a fixed order.
 __global__ __launch_bounds__(kThreads) void k_group_finish(const GroupParams p) {
-  const int64_t i = int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64;
+  const int64_t i = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * (kThreads / 64) + threadIdx.x / 64;
   if (i >= int64_t(p.B) * p.G) return;
   const int lane = threadIdx.x & 63, b = int(i / p.G), g = int(i - int64_t(b) * p.G);
   double sum = 0.0, sq = 0.0;
@@ -224,8 +224,10 @@ hipError_t sequences(const GroupParams& p, dynconv_dtype dt, bool whole, bool pa
 hipError_t statistics(const GroupParams& p, dynconv_dtype dt, bool whole, bool packed, hipStream_t s) {
   const hipError_t e = sequences(p, dt, whole, packed, kGroupStats, s);
   if (e != hipSuccess) return e;
-  const int64_t waves = int64_t(p.B) * p.G;
-  hipLaunchKernelGGL(k_group_finish, dim3(unsigned((waves + 3) / 4)), dim3(kThreads), 0, s, p);
+  constexpr int64_t most = int64_t(1) << 23;  // a dimension of a launch has fewer than 2^32 threads
+  const int64_t blocks = (int64_t(p.B) * p.G + kThreads / 64 - 1) / (kThreads / 64);
+  const dim3 grid(unsigned(blocks < most ? blocks : most), unsigned((blocks + most - 1) / most));
+  hipLaunchKernelGGL(k_group_finish, grid, dim3(kThreads), 0, s, p);
   return hipGetLastError();
 }
 

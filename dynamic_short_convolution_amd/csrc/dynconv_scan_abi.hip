@@ -249,10 +249,12 @@ dynconv_status dynconv_scan_bwd(const void* x, const int64_t* xs, const void* de
   }
   p.dstate_out = dstate_out, p.dsos = dstate_out != nullptr ? dsos[0] : 0;
   p.dstate = dstate_in, p.dsis = dstate_in != nullptr ? dsis[0] : 0;
+  const int64_t rows = int64_t(B) * p.nSeg;  // of drate's partial sums; a single one is the result
+  if (rows == 1) p.drate_part = drate;
   e = dtype == DYNCONV_BF16  ? scan_bwd_bf16(p, vec, packed, s)
       : dtype == DYNCONV_F16 ? scan_bwd_f16(p, vec, packed, s)
                              : scan_bwd_f32(p, vec, packed, s);
-  if (e == hipSuccess) e = norm_dweight(p.drate_part, int64_t(B) * p.nSeg, p.D, drate, s);
+  if (e == hipSuccess && rows > 1) e = norm_dweight(p.drate_part, rows, p.D, drate, s);
   return done(e);
 }
 

@@ -7,6 +7,7 @@ current stream, nothing else.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -646,6 +647,12 @@ def dynconv_norm_bwd(x, weight, dy, gate=None, dh=None, residual_scale: float = 
     return dx, dres, dw, dgate
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(fn: str, *sizes) -> int:
+    """A workspace query of the C ABI (a function of its arguments alone): 1 us less per repeated call."""
+    return int(getattr(_lib.load(), fn)(*sizes))
+
+
 # ----------------------------------------------------------------------------------
 # Activations in 8 bits, for backward passes
 # ----------------------------------------------------------------------------------
@@ -759,7 +766,7 @@ def dynconv_scan_fwd(x, decay, rate, gate=None, seq_idx=None, state=None, want_s
         state_out = torch.empty((B, D), dtype=torch.float32, device=dev)
     chunks = torch.empty(_chunks_shape(B, T, D), dtype=torch.float32, device=dev) if want_chunks else None
     code = _dtype_code(x)
-    ws_bytes = int(_lib.load().dynconv_scan_fwd_workspace_size(B, T, D, code))
+    ws_bytes = _workspace_bytes("dynconv_scan_fwd_workspace_size", B, T, D, code)
     work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
     _launch("dynconv_scan_fwd", dev, *_sp(x), *_sp(decay), *_sp(gate), _dp(rate), *seg, *_sp(state), *_sp(y),
             *_sp(state_out), _dp(chunks), B, T, D, code, _dp(work), ws_bytes)
@@ -809,7 +816,7 @@ def dynconv_scan_bwd(x, decay, rate, dy, gate=None, seq_idx=None, state=None, ch
     dx, da, dgate = new(), new(), new() if gate is not None else None
     drate = torch.empty((D,), dtype=torch.float32, device=dev)
     dstate = torch.empty((B, D), dtype=torch.float32, device=dev) if need_dstate else None
-    ws_bytes = int(_lib.load().dynconv_scan_bwd_workspace_size(B, T, D, int(chunks is not None), code))
+    ws_bytes = _workspace_bytes("dynconv_scan_bwd_workspace_size", B, T, D, int(chunks is not None), code)
     work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
     _launch("dynconv_scan_bwd", dev, *_sp(x), *_sp(decay), *_sp(gate), *(a for t in scales for a in _sp(t)), _dp(rate),
             *seg, *_sp(state), _dp(chunks), *_sp(dy), *_sp(dstate_out), *_sp(dx), *_sp(da), _dp(drate), *_sp(dgate),
@@ -884,7 +891,7 @@ def dynconv_groupnorm_fwd(x, groups: int, weight=None, bias=None, gate=None, act
     y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
     # a sequence without tokens, or none at all: nothing is launched that would write them
     stats = (torch.zeros if B * T * C == 0 else torch.empty)((B, groups, 2), dtype=torch.float32, device=dev) if want_stats and seq else None
-    ws_bytes = int(_lib.load().dynconv_groupnorm_fwd_workspace_size(B, T, C, groups, 1, int(stats is not None), code)) if seq else 0
+    ws_bytes = _workspace_bytes("dynconv_groupnorm_fwd_workspace_size", B, T, C, groups, 1, int(stats is not None), code) if seq else 0
     work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
     _launch("dynconv_groupnorm_fwd", dev, *_sp3(x), _dp(weight), _dp(bias), *_sp3(gate), _dp(lengths), *_sp3(y), _dp(stats),
             B, T, C, groups, seq, silu, float(eps), code, _dp(work), ws_bytes)
@@ -917,7 +924,7 @@ def dynconv_groupnorm_bwd(x, groups: int, dy, weight=None, bias=None, gate=None,
     dw, db = column() if weight is not None else None, column() if bias is not None else None
     ws_bytes = 0
     if seq or dw is not None or db is not None:
-        ws_bytes = int(_lib.load().dynconv_groupnorm_bwd_workspace_size(B, T, C, groups, seq, int(stats is not None), code))
+        ws_bytes = _workspace_bytes("dynconv_groupnorm_bwd_workspace_size", B, T, C, groups, seq, int(stats is not None), code)
     work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
     _launch("dynconv_groupnorm_bwd", dev, *_sp3(x), *_sp3(scales), _dp(weight), _dp(bias), *_sp3(gate), _dp(lengths),
             _dp(stats), *_sp3(dy), *_sp3(dx), _dp(dw), _dp(db), *_sp3(dgate), B, T, C, groups, seq, silu, float(eps), code,
