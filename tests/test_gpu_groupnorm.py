@@ -379,3 +379,15 @@ def test_refusals():
                 dict(groups=4, lengths=torch.ones(2, dtype=torch.int32, device="cuda"))):
         with pytest.raises(ValueError):
             dc.dynconv_groupnorm_fwd(x, **bad)
+
+
+def test_more_groups_than_one_dimension_of_a_launch():
+    """2^26 (sequence, group) pairs: the waves that finish their statistics are more than 2^32 threads."""
+    B, groups = 2**20 + 3, 64
+    x = torch.ones(B, 1, 2 * groups, dtype=torch.bfloat16, device="cuda")
+    x[..., 1::2] = 3.0
+    x[-5:] = rand(160, 5, 1, 2 * groups, dtype=torch.bfloat16)
+    y = dc.dynconv_groupnorm_fwd(x, groups, over="sequence")
+    ref = groupnorm_fwd(to64(x[-8:]), groups, over="sequence")
+    near("last rows", y[-8:], ref, bounds(to64(x[-8:]), groups, np.zeros((8, 1, 2 * groups)), over="sequence")[0])
+    assert bool((y[:-5, :, 0::2] == y[0, 0, 0]).all()) and bool((y[:-5, :, 1::2] == y[0, 0, 1]).all())

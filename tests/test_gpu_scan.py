@@ -427,3 +427,25 @@ def test_refusals():
         dc.dynconv_scan_step(s["x"][:, 0], s["decay"][:, 0], s["rate"], s["state"], out=s["x"][:, 0])
     with pytest.raises(DynconvError, match="UNSUPPORTED"):
         dc.dynconv_pack8(rand(221, 64, 4).t())
+
+
+def test_many_short_sequences():
+    B, T, D = 70001, 2, 64
+    s, dy, _ = inputs(B, T, D, "bf16", True, 0, True, seed=230)
+    y, last = dc.dynconv_scan_fwd(**s, want_state=True)
+    g = dc.dynconv_scan_bwd(**s, dy=dy, need_dstate=True)
+    pick = slice(B - 40, B)
+    part = {n: t if n == "rate" or t is None else t[pick] for n, t in s.items()}
+    args = tuple(opt(part[n]) for n in ("x", "decay", "rate", "gate"))
+    bound = fwd_bound(*args, None, to64(part["state"]))
+    ry, rlast = scan_fwd(*args, None, to64(part["state"]))
+    near("y", y[pick], ry, bound)
+    near("state", last[pick], rlast, bound[:, -1])
+    ref, bounds = scan_bwd(*args, to64(dy[pick]), None, to64(part["state"])), bwd_bounds(*args, to64(dy[pick]), None, to64(part["state"]))
+    for name, i in (("dx", 0), ("ddecay", 1), ("dgate", 3), ("dstate", 4)):
+        near(name, g[i][pick], ref[i], bounds[i])
+
+
+def test_long_narrow_sequence_of_all_segments():
+    s, dy, dlast = inputs(1, 40000, 3, "f32", True, 5000, True, seed=240)
+    check(s, dy, dlast)
