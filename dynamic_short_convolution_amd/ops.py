@@ -32,11 +32,12 @@ def _require_device(*ts):
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
+        i = t.get_device()  # -1 on the CPU; half the time of comparing device objects
+        if i < 0:
             raise RuntimeError("libdynconv runs on the GPU only: got a CPU tensor")
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
+            dev, first = t.device, i
+        elif i != first:
             raise RuntimeError("all tensors must be on the same device")
     return dev
 
@@ -761,13 +762,13 @@ def dynconv_scan_fwd(x, decay, rate, gate=None, seq_idx=None, state=None, want_s
     _expect("out", out, (B, T, D), x.dtype)
     dev = _require_device(x, decay, gate, rate, seq_idx, state, out, state_out)
     seg = _seg_args(seq_idx, B, T) if seq_idx is not None else (None, None)
-    y = torch.empty((B, T, D), dtype=x.dtype, device=dev) if out is None else out
+    y = x.new_empty((B, T, D)) if out is None else out
     if want_state and state_out is None:
         state_out = torch.empty((B, D), dtype=torch.float32, device=dev)
     chunks = torch.empty(_chunks_shape(B, T, D), dtype=torch.float32, device=dev) if want_chunks else None
     code = _dtype_code(x)
     ws_bytes = _workspace_bytes("dynconv_scan_fwd_workspace_size", B, T, D, code)
-    work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    work = y.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
     _launch("dynconv_scan_fwd", dev, *_sp(x), *_sp(decay), *_sp(gate), _dp(rate), *seg, *_sp(state), *_sp(y),
             *_sp(state_out), _dp(chunks), B, T, D, code, _dp(work), ws_bytes)
     if state_out is None and chunks is None:
@@ -811,13 +812,13 @@ def dynconv_scan_bwd(x, decay, rate, dy, gate=None, seq_idx=None, state=None, ch
     seg = _seg_args(seq_idx, B, T) if seq_idx is not None else (None, None)
 
     def new():
-        return torch.empty((B, T, D), dtype=dy.dtype, device=dev)
+        return dy.new_empty((B, T, D))
 
     dx, da, dgate = new(), new(), new() if gate is not None else None
     drate = torch.empty((D,), dtype=torch.float32, device=dev)
     dstate = torch.empty((B, D), dtype=torch.float32, device=dev) if need_dstate else None
     ws_bytes = _workspace_bytes("dynconv_scan_bwd_workspace_size", B, T, D, int(chunks is not None), code)
-    work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    work = dy.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
     _launch("dynconv_scan_bwd", dev, *_sp(x), *_sp(decay), *_sp(gate), *(a for t in scales for a in _sp(t)), _dp(rate),
             *seg, *_sp(state), _dp(chunks), *_sp(dy), *_sp(dstate_out), *_sp(dx), *_sp(da), _dp(drate), *_sp(dgate),
             *_sp(dstate), B, T, D, code, _dp(work), ws_bytes)
@@ -833,7 +834,7 @@ def dynconv_scan_step(x, decay, rate, state, gate=None, out=None):
     _expect("state", state, (B, D), torch.float32)
     _expect("out", out, (B, D), x.dtype)
     dev = _require_device(x, decay, gate, rate, state, out)
-    y = torch.empty((B, D), dtype=x.dtype, device=dev) if out is None else out
+    y = x.new_empty((B, D)) if out is None else out
     _launch("dynconv_scan_step", dev, *_sp(x), *_sp(decay), *_sp(gate), _dp(rate), *_sp(state), *_sp(y), B, D,
             _dtype_code(x))
     return y
@@ -888,11 +889,11 @@ def dynconv_groupnorm_fwd(x, groups: int, weight=None, bias=None, gate=None, act
     (B, T, C), seq, silu = _group_args(x.shape, x.dtype, groups, weight, bias, gate, activation, over, lengths, None)
     _expect("out", out, x.shape, x.dtype)
     dev = _require_device(x, weight, bias, gate, lengths, out)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+    y = x.new_empty(x.shape) if out is None else out
     # a sequence without tokens, or none at all: nothing is launched that would write them
     stats = (torch.zeros if B * T * C == 0 else torch.empty)((B, groups, 2), dtype=torch.float32, device=dev) if want_stats and seq else None
     ws_bytes = _workspace_bytes("dynconv_groupnorm_fwd_workspace_size", B, T, C, groups, 1, int(stats is not None), code) if seq else 0
-    work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    work = y.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
     _launch("dynconv_groupnorm_fwd", dev, *_sp3(x), _dp(weight), _dp(bias), *_sp3(gate), _dp(lengths), *_sp3(y), _dp(stats),
             B, T, C, groups, seq, silu, float(eps), code, _dp(work), ws_bytes)
     return (y, stats) if want_stats else y
@@ -915,7 +916,7 @@ def dynconv_groupnorm_bwd(x, groups: int, dy, weight=None, bias=None, gate=None,
     dev = _require_device(x, scales, dy, weight, bias, gate, lengths, stats)
 
     def new():
-        return torch.empty(dy.shape, dtype=dy.dtype, device=dev)
+        return dy.new_empty(dy.shape)
 
     def column():
         return torch.empty((C,), dtype=torch.float32, device=dev)
@@ -925,7 +926,7 @@ def dynconv_groupnorm_bwd(x, groups: int, dy, weight=None, bias=None, gate=None,
     ws_bytes = 0
     if seq or dw is not None or db is not None:
         ws_bytes = _workspace_bytes("dynconv_groupnorm_bwd_workspace_size", B, T, C, groups, seq, int(stats is not None), code)
-    work = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+    work = dy.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
     _launch("dynconv_groupnorm_bwd", dev, *_sp3(x), *_sp3(scales), _dp(weight), _dp(bias), *_sp3(gate), _dp(lengths),
             _dp(stats), *_sp3(dy), *_sp3(dx), _dp(dw), _dp(db), *_sp3(dgate), B, T, C, groups, seq, silu, float(eps), code,
             _dp(work), ws_bytes)
