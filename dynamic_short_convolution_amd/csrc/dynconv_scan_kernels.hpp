@@ -309,12 +309,15 @@ __device__ __forceinline__ void write_map(float (&m)[kScanCols], int chl, const 
 }
 
 // ---------------------------------------------------------------------------------
-// Forward. MAPS: only the map of the segment, into p.maps; with segment 0 the initial state too. That pass
+// Forward: the outputs (and the kept and last states), the kept states alone (for a backward that has to
+// recompute them), or only the map of the segment, into p.maps; with segment 0 the initial state too. That pass
 // goes from the last tile to the first, so that what it read last, which the memory-side cache still
 // holds, is what the pass behind it reads first.
 // ---------------------------------------------------------------------------------
-template <typename ET, int V, bool PACKED, bool DOCS, bool MAPS>
+enum Want { kOutputs, kStates, kMaps };
+template <typename ET, int V, bool PACKED, bool DOCS, Want WANT>
 __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
+  constexpr bool MAPS = WANT == kMaps;
   using IT = std::conditional_t<PACKED, i8_t, ET>;
   constexpr int L = kScanElems / V;
   __shared__ float maps[2][2][kScanWaves][kScanCols];  // [tile & 1][A, H]
@@ -488,7 +491,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) out[i] = h[i];
       }
-      const __amdgpu_buffer_rsrc_t ry = py.rows(p.y, b, k, k0, k1, c0, p.T, p.D);  // empty where only the states are wanted
+    }
+    if constexpr (WANT == kOutputs) {
+      const __amdgpu_buffer_rsrc_t ry = py.rows(p.y, b, k, k0, k1, c0, p.T, p.D);
 #pragma unroll
       for (int i = 0; i < V; ++i) h[i] = through<DOCS>(pA[i], pH[i], h[i]);
 #pragma unroll
@@ -821,15 +826,17 @@ hipError_t launch(const ScanParams& p, bool bwd, hipStream_t s) {
     if (bwd) {
       hipLaunchKernelGGL((k_scan_bwd<ET, V, PACKED, DOCS, true>), first, dim3(kThreads), 0, s, p);
     } else {
-      hipLaunchKernelGGL((k_scan_fwd<ET, V, PACKED, DOCS, true>), first, dim3(kThreads), 0, s, p);
+      hipLaunchKernelGGL((k_scan_fwd<ET, V, PACKED, DOCS, kMaps>), first, dim3(kThreads), 0, s, p);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (bwd) {
     hipLaunchKernelGGL((k_scan_bwd<ET, V, PACKED, DOCS, false>), all, dim3(kThreads), 0, s, p);
-  } else {
-    hipLaunchKernelGGL((k_scan_fwd<ET, V, PACKED, DOCS, false>), all, dim3(kThreads), 0, s, p);
+  } else if (p.y.p == nullptr) {
+    hipLaunchKernelGGL((k_scan_fwd<ET, V, PACKED, DOCS, kStates>), all, dim3(kThreads), 0, s, p);
+  } else if constexpr (!PACKED) {  // the forward of packed inputs only serves the backward
+    hipLaunchKernelGGL((k_scan_fwd<ET, V, PACKED, DOCS, kOutputs>), all, dim3(kThreads), 0, s, p);
   }
   return hipGetLastError();
 }
