@@ -7,7 +7,6 @@ current stream, nothing else.
 from __future__ import annotations
 
 import ctypes
-import functools
 from typing import NamedTuple
 
 import torch
@@ -648,10 +647,47 @@ def dynconv_norm_bwd(x, weight, dy, gate=None, dh=None, residual_scale: float = 
     return dx, dres, dw, dgate
 
 
-@functools.lru_cache(maxsize=4096)
-def _workspace_bytes(fn: str, *sizes) -> int:
-    """A workspace query of the C ABI (a function of its arguments alone): 1 us less per repeated call."""
+# ----------------------------------------------------------------------------------
+# Plans: what a call needs besides pointers
+# ----------------------------------------------------------------------------------
+
+_PLANS: dict = {}
+
+
+def _plan(make, extra: tuple, *tensors):
+    """make(*extra, *tensors) checks a call's arguments and returns its sizes and stride arrays (not to be
+    written): once for all calls whose tensors have these shapes, strides and types, which takes 5 to 8 us
+    less than every time."""
+    key = (make, extra, *[None if t is None else (t.shape, t.stride(), t.dtype) for t in tensors])
+    plan = _PLANS.get(key)
+    if plan is None:
+        plan = make(*extra, *tensors)
+        if len(_PLANS) >= 4096:
+            _PLANS.clear()
+        _PLANS[key] = plan
+    return plan
+
+
+def _st(t, n: int | None = None):
+    """Stride array of a tensor (of n dimensions, leading ones of stride 0 added), or NULL."""
+    return None if t is None else _lib.const_strides((0,) * (0 if n is None else n - t.dim()) + t.stride())
+
+
+def _dense(shape, n: int | None = None):
+    """Stride array of a new tensor of this shape."""
+    strides, step = [], 1
+    for size in reversed(shape):
+        strides.append(step)
+        step *= max(size, 1)
+    return _lib.const_strides((0,) * (0 if n is None else n - len(shape)) + tuple(reversed(strides)))
+
+
+def _workspace(fn: str, *sizes) -> int:
     return int(getattr(_lib.load(), fn)(*sizes))
+
+
+def _seq_strides(seq_idx, B: int, T: int):
+    return None if seq_idx is None else _seg_args(seq_idx, B, T)[1]
 
 
 # ----------------------------------------------------------------------------------
@@ -674,37 +710,50 @@ def _scales_shape(shape):
     return (*shape[:-1], -(-shape[-1] // PACK8_GROUP))
 
 
-def _check_packed(name, p, shape):
-    """Checks a Packed8 operand of the given shape; returns it."""
-    _expect(f"{name}.codes", p.codes, shape, torch.int8)
-    _expect(f"{name}.scales", p.scales, _scales_shape(shape), torch.uint8)
-    return p
+def _check_packed(name, codes, scales, shape):
+    _expect(f"{name}.codes", codes, shape, torch.int8)
+    _expect(f"{name}.scales", scales, _scales_shape(shape), torch.uint8)
+
+
+def _pack_plan(x, codes, scales):
+    sizes, code = _norm_shape(x), _dtype_code(x)
+    if codes is not None:
+        _check_packed("out", codes, scales, x.shape)
+    shape = _scales_shape(x.shape)
+    return (shape, _st(x, 4), _dense(x.shape, 4) if codes is None else _st(codes, 4),
+            _dense(shape, 4) if scales is None else _st(scales, 4), (*sizes, code))
 
 
 def dynconv_pack8(x, out: Packed8 | None = None) -> Packed8:
     """x (1 to 4 dimensions) in 8 bits: per row, every 64 channels are integers of -127 to 127 times
     the power of two 2^(floor(log2 max|x|) - 6) that they share. Half the memory of 16-bit
     activations (a quarter of float32) for what a training step keeps for its backward pass."""
-    shape = _norm_shape(x)
-    code = _dtype_code(x)
-    if out is not None:
-        _check_packed("out", out, x.shape)
-    dev = _require_device(x, *(out or ()))
+    codes, scales = (None, None) if out is None else out
+    shape, xs, cs, ss, sizes = _plan(_pack_plan, (), x, codes, scales)
+    dev = _require_device(x, codes, scales)
     if out is None:
-        out = Packed8(torch.empty(x.shape, dtype=torch.int8, device=dev),
-                      torch.empty(_scales_shape(x.shape), dtype=torch.uint8, device=dev))
-    _launch("dynconv_pack", dev, *_sp4(x), *_sp4(out.codes), *_sp4(out.scales), *shape, code)
+        out = Packed8(x.new_empty(x.shape, dtype=torch.int8), x.new_empty(shape, dtype=torch.uint8))
+        codes, scales = out
+    _launch("dynconv_pack", dev, x.data_ptr(), xs, codes.data_ptr(), cs, scales.data_ptr(), ss, *sizes)
     return out
+
+
+def _unpack_plan(dtype, codes, scales, out):
+    sizes = _norm_shape(codes)
+    _check_packed("packed", codes, scales, codes.shape)
+    _expect("out", out, codes.shape, dtype)
+    if dtype not in _DTYPE:
+        raise TypeError(f"unsupported dtype {dtype}; use float32, bfloat16 or float16")
+    return _st(codes, 4), _st(scales, 4), _dense(codes.shape, 4) if out is None else _st(out, 4), (*sizes, _DTYPE[dtype])
 
 
 def dynconv_unpack8(packed: Packed8, dtype=torch.bfloat16, out=None):
     """The values that a Packed8 stands for, as `dtype` (exact in the type that was packed)."""
-    shape = _norm_shape(packed.codes)
-    _check_packed("packed", packed, packed.codes.shape)
-    _expect("out", out, packed.codes.shape, dtype)
-    dev = _require_device(*packed, out)
-    y = torch.empty(packed.codes.shape, dtype=dtype, device=dev) if out is None else out
-    _launch("dynconv_unpack", dev, *_sp4(packed.codes), *_sp4(packed.scales), *_sp4(y), *shape, _dtype_code(y))
+    codes, scales = packed
+    cs, ss, ys, sizes = _plan(_unpack_plan, (dtype,), codes, scales, out)
+    dev = _require_device(codes, scales, out)
+    y = codes.new_empty(codes.shape, dtype=dtype) if out is None else out
+    _launch("dynconv_unpack", dev, codes.data_ptr(), cs, scales.data_ptr(), ss, y.data_ptr(), ys, *sizes)
     return y
 
 
@@ -738,11 +787,22 @@ def _scan_shape(x, decay, gate, rate, n: int):
     _expect("decay", decay, x.shape, x.dtype)
     _expect("gate", gate, x.shape, x.dtype)
     _check_rate(rate, x.shape[-1])
-    return x.shape
+    return tuple(x.shape)
 
 
 def _chunks_shape(B: int, T: int, D: int):
     return (B, -(-T // SCAN_CHUNK), D)
+
+
+def _scan_fwd_plan(x, decay, rate, gate, seq_idx, state, state_out, out):
+    B, T, D = _scan_shape(x, decay, gate, rate, 3)
+    _expect("state", state, (B, D), torch.float32)
+    _expect("state_out", state_out, (B, D), torch.float32)
+    _expect("out", out, (B, T, D), x.dtype)
+    code = _dtype_code(x)
+    return ((B, T, D), _chunks_shape(B, T, D), code, _workspace("dynconv_scan_fwd_workspace_size", B, T, D, code), _st(x),
+            _st(decay), _st(gate), _seq_strides(seq_idx, B, T), _st(state), _dense((B, T, D)) if out is None else _st(out),
+            _dense((B, D)) if state_out is None else _st(state_out))
 
 
 def dynconv_scan_fwd(x, decay, rate, gate=None, seq_idx=None, state=None, want_state: bool = False,
@@ -756,24 +816,43 @@ def dynconv_scan_fwd(x, decay, rate, gate=None, seq_idx=None, state=None, want_s
     token 0 (default zero). Returns y; with want_state, or a state_out to write (which may be state
     itself), (y, state after token T-1); want_chunks adds, last, the float32 states before every 128th
     token that dynconv_scan_bwd would else recompute."""
-    B, T, D = _scan_shape(x, decay, gate, rate, 3)
-    _expect("state", state, (B, D), torch.float32)
-    _expect("state_out", state_out, (B, D), torch.float32)
-    _expect("out", out, (B, T, D), x.dtype)
+    shape, kept, code, ws_bytes, xs, as_, gs, ss, sis, ys, sos = _plan(_scan_fwd_plan, (), x, decay, rate, gate, seq_idx,
+                                                                       state, state_out, out)
     dev = _require_device(x, decay, gate, rate, seq_idx, state, out, state_out)
-    seg = _seg_args(seq_idx, B, T) if seq_idx is not None else (None, None)
-    y = x.new_empty((B, T, D)) if out is None else out
+    y = x.new_empty(shape) if out is None else out
     if want_state and state_out is None:
-        state_out = torch.empty((B, D), dtype=torch.float32, device=dev)
-    chunks = torch.empty(_chunks_shape(B, T, D), dtype=torch.float32, device=dev) if want_chunks else None
-    code = _dtype_code(x)
-    ws_bytes = _workspace_bytes("dynconv_scan_fwd_workspace_size", B, T, D, code)
-    work = y.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
-    _launch("dynconv_scan_fwd", dev, *_sp(x), *_sp(decay), *_sp(gate), _dp(rate), *seg, *_sp(state), *_sp(y),
-            *_sp(state_out), _dp(chunks), B, T, D, code, _dp(work), ws_bytes)
+        state_out = rate.new_empty((shape[0], shape[2]))
+    chunks = rate.new_empty(kept) if want_chunks else None
+    work = x.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
+    _launch("dynconv_scan_fwd", dev, x.data_ptr(), xs, decay.data_ptr(), as_, _dp(gate), gs, rate.data_ptr(), _dp(seq_idx),
+            ss, _dp(state), sis, y.data_ptr(), ys, _dp(state_out), sos, _dp(chunks), *shape, code, _dp(work), ws_bytes)
     if state_out is None and chunks is None:
         return y
     return (y,) + ((state_out,) if state_out is not None else ()) + ((chunks,) if chunks is not None else ())
+
+
+def _scan_bwd_plan(packed, x, x_scales, decay, decay_scales, gate, gate_scales, rate, dy, seq_idx, state, chunks, dstate_out):
+    if dy.dim() != 3:
+        raise ValueError(f"dy must be [B, T, D]; got shape {list(dy.shape)}")
+    B, T, D = dy.shape
+    code = _dtype_code(dy)
+    if packed:
+        _check_packed("x", x, x_scales, dy.shape)
+        _check_packed("decay", decay, decay_scales, dy.shape)
+        if gate is not None:
+            _check_packed("gate", gate, gate_scales, dy.shape)
+        _check_rate(rate, D)
+    else:
+        _scan_shape(x, decay, gate, rate, 3)
+        _expect("dy", dy, x.shape, x.dtype)
+    _expect("state", state, (B, D), torch.float32)
+    _expect("dstate_out", dstate_out, (B, D), torch.float32)
+    _expect("chunks", chunks, _chunks_shape(B, T, D), torch.float32)
+    if chunks is not None and not chunks.is_contiguous():
+        raise ValueError("chunks must be contiguous")
+    ws_bytes = _workspace("dynconv_scan_bwd_workspace_size", B, T, D, int(chunks is not None), code)
+    return ((B, T, D), code, ws_bytes, _st(x), _st(decay), _st(gate), _st(x_scales), _st(decay_scales), _st(gate_scales),
+            _seq_strides(seq_idx, B, T), _st(state), _st(dy), _st(dstate_out), _dense((B, T, D)), _dense((B, D)))
 
 
 def dynconv_scan_bwd(x, decay, rate, dy, gate=None, seq_idx=None, state=None, chunks=None, dstate_out=None,
@@ -784,70 +863,47 @@ def dynconv_scan_bwd(x, decay, rate, dy, gate=None, seq_idx=None, state=None, ch
     are recomputed. x, decay and gate may all be Packed8: the gradients are then those at the values
     that the codes stand for (chunks of the unpacked inputs would be others)."""
     packed = isinstance(x, Packed8)
-    if dy.dim() != 3:
-        raise ValueError(f"dy must be [B, T, D]; got shape {list(dy.shape)}")
-    B, T, D = dy.shape
-    code = _dtype_code(dy)
-    scales = (None, None, None)
-    if packed:
-        if not isinstance(decay, Packed8) or not (gate is None or isinstance(gate, Packed8)):
-            raise ValueError("x, decay and gate are all Packed8 or none is")
-        for name, t in (("x", x), ("decay", decay), ("gate", gate)):
-            if t is not None:
-                _check_packed(name, t, dy.shape)
-        scales = (x.scales, decay.scales, gate.scales if gate is not None else None)
-        x, decay, gate = x.codes, decay.codes, gate.codes if gate is not None else None
-        _check_rate(rate, D)
-    else:
-        if isinstance(decay, Packed8) or isinstance(gate, Packed8):
-            raise ValueError("x, decay and gate are all Packed8 or none is")
-        _scan_shape(x, decay, gate, rate, 3)
-        _expect("dy", dy, x.shape, x.dtype)
-    _expect("state", state, (B, D), torch.float32)
-    _expect("dstate_out", dstate_out, (B, D), torch.float32)
-    _expect("chunks", chunks, _chunks_shape(B, T, D), torch.float32)
-    if chunks is not None and not chunks.is_contiguous():
-        raise ValueError("chunks must be contiguous")
-    dev = _require_device(x, decay, gate, *scales, rate, dy, seq_idx, state, chunks, dstate_out)
-    seg = _seg_args(seq_idx, B, T) if seq_idx is not None else (None, None)
-
-    def new():
-        return dy.new_empty((B, T, D))
-
-    dx, da, dgate = new(), new(), new() if gate is not None else None
-    drate = torch.empty((D,), dtype=torch.float32, device=dev)
-    dstate = torch.empty((B, D), dtype=torch.float32, device=dev) if need_dstate else None
-    ws_bytes = _workspace_bytes("dynconv_scan_bwd_workspace_size", B, T, D, int(chunks is not None), code)
+    if packed != isinstance(decay, Packed8) or (gate is not None and packed != isinstance(gate, Packed8)):
+        raise ValueError("x, decay and gate are all Packed8 or none is")
+    (x, xc), (decay, ac) = (x, decay) if packed else ((x, None), (decay, None))
+    gate, gc = gate if packed and gate is not None else (gate, None)
+    shape, code, ws_bytes, xs, as_, gs, xcs, acs, gcs, ss, sis, dys, dsos, new, newst = _plan(
+        _scan_bwd_plan, (packed,), x, xc, decay, ac, gate, gc, rate, dy, seq_idx, state, chunks, dstate_out)
+    dev = _require_device(x, xc, decay, ac, gate, gc, rate, dy, seq_idx, state, chunks, dstate_out)
+    dx, da, dgate = dy.new_empty(shape), dy.new_empty(shape), dy.new_empty(shape) if gate is not None else None
+    drate = rate.new_empty(shape[2:])
+    dstate = rate.new_empty((shape[0], shape[2])) if need_dstate else None
     work = dy.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
-    _launch("dynconv_scan_bwd", dev, *_sp(x), *_sp(decay), *_sp(gate), *(a for t in scales for a in _sp(t)), _dp(rate),
-            *seg, *_sp(state), _dp(chunks), *_sp(dy), *_sp(dstate_out), *_sp(dx), *_sp(da), _dp(drate), *_sp(dgate),
-            *_sp(dstate), B, T, D, code, _dp(work), ws_bytes)
+    _launch("dynconv_scan_bwd", dev, x.data_ptr(), xs, decay.data_ptr(), as_, _dp(gate), gs, _dp(xc), xcs, _dp(ac), acs,
+            _dp(gc), gcs, rate.data_ptr(), _dp(seq_idx), ss, _dp(state), sis, _dp(chunks), dy.data_ptr(), dys, _dp(dstate_out),
+            dsos, dx.data_ptr(), new, da.data_ptr(), new, drate.data_ptr(), _dp(dgate), new, _dp(dstate), newst, *shape, code,
+            _dp(work), ws_bytes)
     return dx, da, drate, dgate, dstate
 
 
-def dynconv_scan_step(x, decay, rate, state, gate=None, out=None):
-    """y [B,D] of one token of every sequence (x, decay, gate [B,D], float32 rate [D]); state (float32
-    [B,D]) is updated in place."""
+def _scan_step_plan(x, decay, rate, state, gate, out):
     B, D = _scan_shape(x, decay, gate, rate, 2)
     if state is None:
         raise ValueError("a state [B, D] is required")
     _expect("state", state, (B, D), torch.float32)
     _expect("out", out, (B, D), x.dtype)
+    return _st(x), _st(decay), _st(gate), _st(state), _dense((B, D)) if out is None else _st(out), (B, D, _dtype_code(x))
+
+
+def dynconv_scan_step(x, decay, rate, state, gate=None, out=None):
+    """y [B,D] of one token of every sequence (x, decay, gate [B,D], float32 rate [D]); state (float32
+    [B,D]) is updated in place."""
+    xs, as_, gs, sts, ys, sizes = _plan(_scan_step_plan, (), x, decay, rate, state, gate, out)
     dev = _require_device(x, decay, gate, rate, state, out)
-    y = x.new_empty((B, D)) if out is None else out
-    _launch("dynconv_scan_step", dev, *_sp(x), *_sp(decay), *_sp(gate), _dp(rate), *_sp(state), *_sp(y), B, D,
-            _dtype_code(x))
+    y = x.new_empty(x.shape) if out is None else out
+    _launch("dynconv_scan_step", dev, x.data_ptr(), xs, decay.data_ptr(), as_, _dp(gate), gs, rate.data_ptr(),
+            state.data_ptr(), sts, y.data_ptr(), ys, *sizes)
     return y
 
 
 # ----------------------------------------------------------------------------------
 # Group norm, channels last
 # ----------------------------------------------------------------------------------
-
-
-def _sp3(t):
-    """(pointer, three strides) of a tensor of 2 or 3 dimensions, or two NULLs."""
-    return (t.data_ptr(), _lib.const_strides((0,) * (3 - t.dim()) + t.stride())) if t is not None else (None, None)
 
 
 def _group_args(shape, dtype, groups, weight, bias, gate, activation, over, lengths, stats):
@@ -877,6 +933,15 @@ def _group_args(shape, dtype, groups, weight, bias, gate, activation, over, leng
     return (B, T, C), int(sequence), int(activation == "silu")
 
 
+def _group_fwd_plan(groups, activation, over, eps, want_stats, x, weight, bias, gate, lengths, out):
+    code = _dtype_code(x)
+    (B, T, C), seq, silu = _group_args(x.shape, x.dtype, groups, weight, bias, gate, activation, over, lengths, None)
+    _expect("out", out, x.shape, x.dtype)
+    ws_bytes = _workspace("dynconv_groupnorm_fwd_workspace_size", B, T, C, groups, seq, int(want_stats), code)
+    return ((B, groups, 2) if want_stats and seq else None, B * T * C == 0, ws_bytes, _st(x, 3), _st(gate, 3),
+            _dense(x.shape, 3) if out is None else _st(out, 3), (B, T, C, groups, seq, silu, float(eps), code))
+
+
 def dynconv_groupnorm_fwd(x, groups: int, weight=None, bias=None, gate=None, activation: str | None = None,
                           over: str = "token", lengths=None, eps: float = 1e-5, want_stats: bool = False, out=None):
     """y = act(n * weight + bias) * silu(gate) with n = (x - mean) / sqrt(var + eps) over the C / groups
@@ -885,18 +950,31 @@ def dynconv_groupnorm_fwd(x, groups: int, weight=None, bias=None, gate=None, act
     SiLU with activation="silu", else nothing. Over sequences, lengths (int32 [B], 0 to T) says how many tokens
     of each count; y is 0 behind them. With want_stats returns (y, stats) for dynconv_groupnorm_bwd: float32
     [B,groups,2] over sequences, None per token (there the backward has the group in registers)."""
-    code = _dtype_code(x)
-    (B, T, C), seq, silu = _group_args(x.shape, x.dtype, groups, weight, bias, gate, activation, over, lengths, None)
-    _expect("out", out, x.shape, x.dtype)
+    kept, nothing, ws_bytes, xs, gs, ys, sizes = _plan(_group_fwd_plan, (groups, activation, over, eps, want_stats), x, weight,
+                                                       bias, gate, lengths, out)
     dev = _require_device(x, weight, bias, gate, lengths, out)
     y = x.new_empty(x.shape) if out is None else out
-    # a sequence without tokens, or none at all: nothing is launched that would write them
-    stats = (torch.zeros if B * T * C == 0 else torch.empty)((B, groups, 2), dtype=torch.float32, device=dev) if want_stats and seq else None
-    ws_bytes = _workspace_bytes("dynconv_groupnorm_fwd_workspace_size", B, T, C, groups, 1, int(stats is not None), code) if seq else 0
-    work = y.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
-    _launch("dynconv_groupnorm_fwd", dev, *_sp3(x), _dp(weight), _dp(bias), *_sp3(gate), _dp(lengths), *_sp3(y), _dp(stats),
-            B, T, C, groups, seq, silu, float(eps), code, _dp(work), ws_bytes)
+    stats = None
+    if kept is not None:  # without a token nothing is launched that would write them
+        stats = (torch.zeros if nothing else torch.empty)(kept, dtype=torch.float32, device=dev)
+    work = x.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
+    _launch("dynconv_groupnorm_fwd", dev, x.data_ptr(), xs, _dp(weight), _dp(bias), _dp(gate), gs, _dp(lengths), y.data_ptr(),
+            ys, _dp(stats), *sizes, _dp(work), ws_bytes)
     return (y, stats) if want_stats else y
+
+
+def _group_bwd_plan(groups, activation, over, eps, x, scales, dy, weight, bias, gate, lengths, stats):
+    code = _dtype_code(dy)
+    if scales is not None:
+        _check_packed("x", x, scales, dy.shape)
+    else:
+        _expect("x", x, dy.shape, dy.dtype)
+    (B, T, C), seq, silu = _group_args(dy.shape, dy.dtype, groups, weight, bias, gate, activation, over, lengths, stats)
+    ws_bytes = 0
+    if seq or weight is not None or bias is not None:
+        ws_bytes = _workspace("dynconv_groupnorm_bwd_workspace_size", B, T, C, groups, seq, int(stats is not None), code)
+    return ((C,), ws_bytes, _st(x, 3), _st(scales, 3), _st(gate, 3), _st(dy, 3), _dense(dy.shape, 3),
+            (B, T, C, groups, seq, silu, float(eps), code))
 
 
 def dynconv_groupnorm_bwd(x, groups: int, dy, weight=None, bias=None, gate=None, activation: str | None = None,
@@ -905,29 +983,13 @@ def dynconv_groupnorm_bwd(x, groups: int, dy, weight=None, bias=None, gate=None,
     there is no such input; dweight and dbias are float32 [C]. x may be a Packed8 of what the forward took:
     the gradients are then those at the values it stands for (pass no stats, which would be the unpacked
     x's). stats: what the forward returned with want_stats; recomputed without."""
-    code = _dtype_code(dy)
-    scales = None
-    if isinstance(x, Packed8):
-        _check_packed("x", x, dy.shape)
-        x, scales = x
-    else:
-        _expect("x", x, dy.shape, dy.dtype)
-    (B, T, C), seq, silu = _group_args(dy.shape, dy.dtype, groups, weight, bias, gate, activation, over, lengths, stats)
+    x, scales = x if isinstance(x, Packed8) else (x, None)
+    column, ws_bytes, xs, xcs, gs, dys, new, sizes = _plan(_group_bwd_plan, (groups, activation, over, eps), x, scales, dy,
+                                                           weight, bias, gate, lengths, stats)
     dev = _require_device(x, scales, dy, weight, bias, gate, lengths, stats)
-
-    def new():
-        return dy.new_empty(dy.shape)
-
-    def column():
-        return torch.empty((C,), dtype=torch.float32, device=dev)
-
-    dx, dgate = new(), new() if gate is not None else None
-    dw, db = column() if weight is not None else None, column() if bias is not None else None
-    ws_bytes = 0
-    if seq or dw is not None or db is not None:
-        ws_bytes = _workspace_bytes("dynconv_groupnorm_bwd_workspace_size", B, T, C, groups, seq, int(stats is not None), code)
+    dx, dgate = dy.new_empty(dy.shape), dy.new_empty(dy.shape) if gate is not None else None
+    dw, db = (None if t is None else dy.new_empty(column, dtype=torch.float32) for t in (weight, bias))
     work = dy.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
-    _launch("dynconv_groupnorm_bwd", dev, *_sp3(x), *_sp3(scales), _dp(weight), _dp(bias), *_sp3(gate), _dp(lengths),
-            _dp(stats), *_sp3(dy), *_sp3(dx), _dp(dw), _dp(db), *_sp3(dgate), B, T, C, groups, seq, silu, float(eps), code,
-            _dp(work), ws_bytes)
+    _launch("dynconv_groupnorm_bwd", dev, x.data_ptr(), xs, _dp(scales), xcs, _dp(weight), _dp(bias), _dp(gate), gs, _dp(lengths),
+            _dp(stats), dy.data_ptr(), dys, dx.data_ptr(), new, _dp(dw), _dp(db), _dp(dgate), new, *sizes, _dp(work), ws_bytes)
     return dx, dw, db, dgate
