@@ -26,7 +26,7 @@ dynconv_status check_sizes(const Sizes& z, dynconv_dtype dt) {
   if (dt != DYNCONV_F32 && dt != DYNCONV_BF16 && dt != DYNCONV_F16) return DYNCONV_ERR_INVALID_ARG;
   if (z.B < 0 || z.T < 0 || z.D < 0) return DYNCONV_ERR_INVALID_ARG;
   if (z.B > INT32_MAX || z.T > INT32_MAX - 65536 || z.D > (int64_t(1) << 24)) return DYNCONV_ERR_UNSUPPORTED;
-  // one workgroup of 1024 threads per (sequence, 64 channels), a launch has fewer than 2^32 threads
+  // one workgroup of 512 threads per (sequence, 64 channels), a launch has fewer than 2^32 threads
   if (z.B * ((z.D + kScanCols - 1) / kScanCols) >= (int64_t(1) << 22)) return DYNCONV_ERR_UNSUPPORTED;
   return DYNCONV_OK;
 }
@@ -41,7 +41,7 @@ dynconv_status take(ScanTensor* t, const void* p, const int64_t* s, const Sizes&
   if (!aligned(p, 2 * eb) || (z.B > 1 && s[0] % 2 != 0) || (z.T > 1 && s[1] % 2 != 0)) *vec = 1;
   t->p = p;
   t->s0 = s[0];
-  t->s1 = z.T > 1 ? s[1] : z.D;  // of a single token it has no meaning
+  t->s1 = z.T > 1 ? s[1] : kScanCols;  // a single token's is not used: any that puts the next row out of the range
   return DYNCONV_OK;
 }
 

@@ -12,7 +12,7 @@ namespace dynconv {
 constexpr int kScanCols = 64;    // channels of a workgroup
 constexpr int kScanScaleCols = 64;  // channels that share a scale of an operand in 8 bits
 constexpr int kScanWaves = 8;    // waves of a workgroup, one after the other along the tokens
-constexpr int kScanElems = 16;    // elements of a tile per lane: 8 tokens of one channel or 4 of two
+constexpr int kScanElems = 16;   // elements of a tile per lane: 16 tokens of one channel or 8 of two
 constexpr int kScanTile = kScanWaves * kScanElems * 64 / kScanCols;  // tokens of a workgroup's tile
 constexpr int kScanChunk = 128;  // tokens between two kept states
 static_assert(kScanTile == kScanChunk, "kept states start tiles");

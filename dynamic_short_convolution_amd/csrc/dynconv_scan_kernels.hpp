@@ -484,10 +484,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
       }
     }
     if constexpr (!MAPS) {
-      const int row = me.run * L;
-      if (p.chunks != nullptr && me.group == 0 && row % kScanChunk == 0 && row <= last && me.ok) {
-        const int nC = (p.T + kScanChunk - 1) / kScanChunk;
-        float* out = p.chunks + (int64_t(b) * nC + (t0 + row) / kScanChunk) * p.D + cg;
+      if (p.chunks != nullptr && me.run == 0 && me.ok) {
+        float* out = p.chunks + (int64_t(b) * nTiles + k) * p.D + cg;
 #pragma unroll
         for (int i = 0; i < V; ++i) out[i] = h[i];
       }
@@ -647,7 +645,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
         }
       }
     }
-    if (last < kScanTile - 1) {
+    if (last < kScanTile - 1) {  // tokens that do not exist leave h and e as they are
 #pragma unroll
       for (int j = 0; j < L; ++j)
 #pragma unroll
@@ -656,10 +654,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
           a[j][i] = gone ? 1.f : a[j][i];
           dy[j][i] = gone ? 0.f : dy[j][i];
           if constexpr (!MAPS) {
-            s[j][i] = gone ? 0.f : s[j][i];
             x[j][i] = gone ? 0.f : x[j][i];
             w[j][i] = gone ? 0.f : w[j][i];
-            c[j][i] = gone ? 0.f : c[j][i];
           }
         }
     }
@@ -774,7 +770,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
           dg[i] = dx[i] * x[j][i] * (1.f - sg[j][i]);
           const float ad = a[j][i] * dh;
           const float dl = s[j][i] * __builtin_fmaf(ad, hb[j][i], -c[j][i] * dh * x[j][i]);
-          sum[i] -= dl;
+          sum[i] -= row + j > last ? 0.f : dl;  // of a token that does not exist it may be 0 times infinity
           dr[i] = back[i] * dl * (1.f - s[j][i]);
           e[i] = DOCS && (first >> j & 1) ? 0.f : ad;
         }

@@ -220,6 +220,22 @@ def test_nan_stays_in_its_channel_and_document(dtype, bad):
         s[name][0, 200, 5] = keep
 
 
+@pytest.mark.parametrize("docs", [0, 3])
+@pytest.mark.parametrize("T", [5, 128, 200])
+def test_infinity_in_the_last_token(T, docs):
+    """dl of that token is the infinity dh sigmoid(gate) x a^2 / b, the others are finite: drate is infinite, with
+    a tile's rows behind the last token and without."""
+    s, _, _ = inputs(2, T, 3, "f32", True, docs, True, seed=45)
+    s["x"][1, T - 1, 1] = float("inf")
+    dx, ddecay, drate, dgate, dstate = dc.dynconv_scan_bwd(**s, dy=torch.ones(2, T, 3, device="cuda"), need_dstate=True)
+    assert drate[1].item() == float("inf") and torch.isfinite(drate[[0, 2]]).all()
+    for t in (ddecay, dgate):
+        assert t[1, T - 1, 1].isinf()
+        t[1, T - 1, 1] = 0.0
+        assert torch.isfinite(t).all()
+    assert torch.isfinite(dx).all() and torch.isfinite(dstate).all()
+
+
 @pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 63), ("f32", 130), ("f16", 100)])
 def test_strided_views_inside_guard_bands(dtype, D):
     td = TD[dtype]
@@ -274,6 +290,24 @@ def test_one_token_of_any_stride():
     assert torch.equal(dc.dynconv_scan_fwd(**v), dc.dynconv_scan_fwd(**s))
     for a, b in zip(dc.dynconv_scan_bwd(**v, dy=dy), dc.dynconv_scan_bwd(**s, dy=dy)):
         assert (a is None and b is None) or torch.equal(a, b)
+
+
+def test_a_single_token_of_the_widest_rows():
+    """2^24 channels of float32: both directions at the first, the last and some channels between."""
+    D = 2**24
+    g = torch.Generator(device="cuda").manual_seed(15)
+    x, decay, dy = (torch.randn(1, 1, D, device="cuda", generator=g) for _ in range(3))
+    rate, state = torch.rand(D, device="cuda", generator=g), torch.randn(1, D, device="cuda", generator=g)
+    at = np.r_[0:64, 2**20 - 3:2**20 + 3, D - 64:D]
+    part = [to64(t[..., at]) for t in (x, decay, rate, dy, state)]
+    px, pd, pr, pdy, ps = part
+    near("y", dc.dynconv_scan_fwd(x, decay, rate, state=state)[..., at], scan_fwd(px, pd, pr, state=ps)[0],
+         fwd_bound(px, pd, pr, state=ps))
+    got = dc.dynconv_scan_bwd(x, decay, rate, dy, state=state, need_dstate=True)
+    ref, bounds = scan_bwd(px, pd, pr, None, pdy, state=ps), bwd_bounds(px, pd, pr, None, pdy, state=ps)
+    for name, t, r, b in zip(("dx", "ddecay", "drate", "dgate", "dstate"), got, ref, bounds):
+        if t is not None:
+            near(name, t[..., at], r, b)
 
 
 def test_offsets_past_32_bits():

@@ -12,8 +12,9 @@ TILE, COLS, WAVES, ELEMS, NOWHERE, WRAP = 128, 64, 8, 16, 0x80000000, 2**32
 
 
 def accesses(T, D, s1, eb, V, k, c0):
-    """(tokens, channels) inside the range of tile k, and whether any piece straddles its end; T == 1 keeps D as stride."""
-    pitch = (s1 if T > 1 else D) * eb
+    """(tokens, channels) inside the range of tile k, and whether any piece straddles its end; a single
+    token's rows are taken to be 64 elements apart."""
+    pitch = (s1 if T > 1 else COLS) * eb
     last = min(T - k * TILE, TILE) - 1
     limit = last * pitch + min(D - c0, COLS) * eb
     assert pitch < WRAP and 0 < limit < 2**31
@@ -50,7 +51,7 @@ def test_rows_that_do_not_exist_are_dropped(T, D, pad, V, eb):
             got, torn, last = accesses(T, D, s1, eb, V, k, c0)
             assert not torn
             for row, ch, at in got:
-                assert row <= last and at == (row * (s1 if T > 1 else D) + ch) * eb
+                assert row <= last and at == (row * s1 + ch) * eb
                 seen[k * TILE + row, c0 + ch:c0 + ch + V] += 1
     assert (seen == 1).all()
 
@@ -71,6 +72,15 @@ def test_farthest_rows_do_not_wrap():
     """Token strides just below the limit of 2^22 elements, float32."""
     got, torn, last = accesses(TILE, COLS, 2**22 - 2, 4, 2, 0, 0)
     assert not torn and last == TILE - 1 and len(got) == TILE * COLS // 2
+
+
+@pytest.mark.parametrize("eb", [1, 2, 4])
+@pytest.mark.parametrize("V", [1, 2])
+def test_a_single_token_of_the_widest_rows(V, eb):
+    """2^24 channels: with the width as stride the offsets of float32 rows from the 64th on would come round to the first."""
+    for c0 in (0, 2**24 - COLS):
+        got, torn, _ = accesses(1, 2**24, 0, eb, V, 0, c0)
+        assert not torn and sorted(at for _, _, at in got) == [i * eb for i in range(0, COLS, V)]
 
 
 def test_a_planted_mistake_is_seen():
