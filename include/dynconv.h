@@ -500,8 +500,8 @@ size_t dynconv_norm_bwd_workspace_size(int64_t n0, int64_t n1, int64_t n2, int64
  *             token (0, 128, ...), for the backward; or NULL
  * The states are float32 whatever the `dtype`. A NaN or infinity stays in its channel and document.
  * Limits (DYNCONV_ERR_UNSUPPORTED otherwise): D <= 2^24, B ceil(D/64) < 2^22; token strides below 2^22
- * elements (with T == 1 they are not used). Element alignment; two channels at a time where D and
- * all strides are even and the pointers aligned to two elements.
+ * elements (with T == 1 they are not used). Element alignment; 16-bit types go two channels at a time where
+ * D and all strides are even and the pointers aligned to two elements.
  * Few channels and long sequences need dynconv_scan_fwd_workspace_size(...) bytes of workspace
  * (aligned to 8; 0 for most calls). Run-to-run deterministic.
  */
