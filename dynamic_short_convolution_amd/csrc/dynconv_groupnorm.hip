@@ -84,12 +84,15 @@ hipError_t group_sum(const float* part, int64_t n, int64_t C, int64_t batches, f
 
 }  // namespace
 
+// The fewest lanes that hold a row in one piece each (groups of 16 bf16 channels on 4 lanes instead of 2: forward 91
+// us, not 52); then more pieces per lane, as far as the backward's registers go: 2048 bf16 channels on 64 lanes of
+// 4 pieces took 190 us, on 256 lanes of one 107 (4882 tokens of 8 sequences, 40 million elements).
 GroupPlan group_plan(int64_t Cg, int E) {
   const int64_t loads = (Cg + E - 1) / E;  // of the row
-  for (int lpr : {4, 8, 16, 32, 64})
+  for (int lpr : {1, 2, 4, 8, 16, 32, 64})
     if (loads <= lpr) return {lpr, 1};
   if (loads <= 128) return {64, 2};
-  if (loads <= 256) return {64, 4};
+  if (loads <= 256) return E == 8 ? GroupPlan{256, 1} : GroupPlan{64, 4};
   if (loads <= 512) return {256, 2};
   if (loads <= 1024) return {256, 4};
   return {256, 0};
@@ -116,7 +119,9 @@ void group_sequence_plan(GroupParams* p, int E) {
   p->tps = kThreads / p->lpt;
   const int64_t across = int64_t(p->B) * ((p->G + p->gpb - 1) / p->gpb);
   // Workgroups per CU: sixteen (with sequences of other lengths many have nothing to do), in the
-  // gradient's two passes four, each of which leaves a row of column sums or begins with a sum over the groups.
+  // gradient's two passes four, each of which leaves a row of column sums or begins with a sum over the
+  // groups. Such a row is paid for by 32 of a lane's tokens, by 8 where there would be fewer than two workgroups
+  // per CU (8 sequences of 610 tokens, one group of 8192 bf16 channels: 191 us, with 32 always 329).
   auto cut = [&](int64_t all, int least, int32_t* chunk, int32_t* n) {
     const int64_t want = across < all ? all / across : 1;
     int64_t c = (int64_t(p->T) + want - 1) / want;
@@ -125,7 +130,7 @@ void group_sequence_plan(GroupParams* p, int E) {
     *n = int32_t((p->T + c - 1) / c);
   };
   cut(4096, 8, &p->chunk, &p->nChunk);
-  cut(1024, 32, &p->gradChunk, &p->nGradChunk);
+  cut(1024, across * (p->T / (32 * p->tps)) >= 512 ? 32 : 8, &p->gradChunk, &p->nGradChunk);
 }
 
 namespace {

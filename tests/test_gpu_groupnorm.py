@@ -161,6 +161,29 @@ def test_over_sequences(shape, groups, lengths, gated, silu, dtype):
     check(shape, groups, dtype, gated, silu, over="sequence", lengths=lengths)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("over", ["token", "sequence"])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("width,groups", [(1, 5), (2, 64), (3, 9), (4, 16), (5, 7), (7, 64), (8, 32), (9, 300), (11, 3), (15, 5), (16, 64), (17, 3),
+                                          (31, 2), (33, 5), (1101, 2), (2049, 1), (4100, 1)])
+def test_every_last_piece(width, groups, packed, over, dtype):
+    """Groups shorter than a piece of 16 bytes, of some pieces, and with a last one that reaches back into the one before."""
+    check((2, 41, width * groups), groups, dtype, True, True, over=over, packed=packed, seed=20,
+          lengths=[41, 30] if over == "sequence" else None)
+
+
+@pytest.mark.parametrize("over", ["token", "sequence"])
+def test_elements_of_two_pieces_are_written_the_same(over):
+    """Repeated calls give the same bits, those of elements that two lanes write among them."""
+    x, dy, gate = (rand(i, 3, 900, 27 * 57, dtype=torch.bfloat16) for i in (21, 22, 23))
+    w = rand(24, 27 * 57, dtype=torch.bfloat16)
+    kw = dict(weight=w, bias=w, gate=gate, activation="silu", over=over)
+    first = (dc.dynconv_groupnorm_fwd(x, 27, **kw), *dc.dynconv_groupnorm_bwd(x, 27, dy, **kw))
+    for _ in range(10):
+        again = (dc.dynconv_groupnorm_fwd(x, 27, **kw), *dc.dynconv_groupnorm_bwd(x, 27, dy, **kw))
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_long_sequences(dtype):
     check((2, 5000, 128), 4, dtype, False, True, over="sequence", lengths=[5000, 4097])
