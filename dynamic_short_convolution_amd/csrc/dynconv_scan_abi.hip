@@ -82,10 +82,15 @@ bool any_equal(const void* out, std::initializer_list<const void*> others) {
 
 size_t rounded(size_t n) { return (n + 255) / 256 * 256; }
 
-int32_t segments(const Sizes& z) { return scan_segments(z.T, scan_segment_tiles(z.B, z.D, z.T)); }
+int32_t segments(const Sizes& z, bool bwd) { return scan_segments(z.T, scan_segment_tiles(z.B, z.D, z.T, bwd)); }
+void cut(ScanParams* p, const Sizes& z, bool bwd) {
+  p->segTiles = scan_segment_tiles(z.B, z.D, z.T, bwd);
+  p->nSeg = scan_segments(z.T, p->segTiles);
+}
 
-size_t maps_bytes(const Sizes& z) {
-  const int32_t n = segments(z);
+// The backward's hold the forward's too, which is cut into as many segments or none.
+size_t maps_bytes(const Sizes& z, bool bwd) {
+  const int32_t n = segments(z, bwd);
   return n > 1 ? rounded(size_t(z.B) * size_t(n) * size_t(z.D) * sizeof(float2)) : 0;
 }
 
@@ -100,8 +105,8 @@ struct BwdSpace {
 };
 BwdSpace bwd_space(const Sizes& z, bool given) {
   BwdSpace w;
-  w.drate = rounded(size_t(z.B) * size_t(segments(z)) * size_t(z.D) * sizeof(float));
-  w.maps = maps_bytes(z);
+  w.drate = rounded(size_t(z.B) * size_t(segments(z, true)) * size_t(z.D) * sizeof(float));
+  w.maps = maps_bytes(z, true);
   w.chunks = given ? 0 : chunks_bytes(z);
   return w;
 }
@@ -121,7 +126,7 @@ extern "C" {
 size_t dynconv_scan_fwd_workspace_size(int64_t B, int64_t T, int64_t D, dynconv_dtype dtype) {
   const Sizes z{B, T, D};
   if (check_sizes(z, dtype) != DYNCONV_OK || B == 0 || T == 0 || D == 0) return 0;
-  return maps_bytes(z);
+  return maps_bytes(z, false);
 }
 
 dynconv_status dynconv_scan_fwd(const void* x, const int64_t* xs, const void* decay, const int64_t* as, const void* gate,
@@ -161,8 +166,8 @@ dynconv_status dynconv_scan_fwd(const void* x, const int64_t* xs, const void* de
   p.state_out = state_out, p.sos = state_out != nullptr ? sos[0] : 0;
   p.chunks = chunks;
   p.B = int32_t(B), p.T = int32_t(T), p.D = int32_t(D);
-  p.segTiles = scan_segment_tiles(B, D, T), p.nSeg = segments(z);
-  const size_t need = maps_bytes(z);
+  cut(&p, z, false);
+  const size_t need = maps_bytes(z, false);
   if (need != 0 && (workspace == nullptr || workspace_bytes < need)) return DYNCONV_ERR_WORKSPACE;
   if (need != 0 && !aligned(workspace, 8)) return DYNCONV_ERR_UNSUPPORTED;
   p.maps = static_cast<float2*>(workspace);
@@ -239,7 +244,7 @@ dynconv_status dynconv_scan_bwd(const void* x, const int64_t* xs, const void* de
   p.drate_part = reinterpret_cast<float*>(at);
   p.maps = reinterpret_cast<float2*>(at + w.drate);
   p.B = int32_t(B), p.T = int32_t(T), p.D = int32_t(D);
-  p.segTiles = scan_segment_tiles(B, D, T), p.nSeg = segments(z);
+  cut(&p, z, false);
   hipError_t e;
   if (chunks != nullptr) {
     p.chunks = const_cast<float*>(chunks);
@@ -247,6 +252,7 @@ dynconv_status dynconv_scan_bwd(const void* x, const int64_t* xs, const void* de
     p.chunks = reinterpret_cast<float*>(at + w.drate + w.maps);
     if ((e = run_fwd(p, dtype, vec, packed, s)) != hipSuccess) return done(e);
   }
+  cut(&p, z, true);
   p.dstate_out = dstate_out, p.dsos = dstate_out != nullptr ? dsos[0] : 0;
   p.dstate = dstate_in, p.dsis = dstate_in != nullptr ? dsis[0] : 0;
   const int64_t rows = int64_t(B) * p.nSeg;  // of drate's partial sums; a single one is the result

@@ -51,11 +51,14 @@ struct ScanParams {
 
 // Tiles per segment. A workgroup walks its tiles one behind the other; with few (sequence, 64
 // channels) pairs the CUs would idle, so the sequence is cut, at the price of a first pass that
-// reads the inputs of the maps once more.
-inline int32_t scan_segment_tiles(int64_t B, int64_t D, int64_t T) {
+// reads the inputs of the maps once more: all three of the forward, two of the backward's four, which therefore
+// is cut into two already (bf16, whole / cut, us: 128 pairs of 7812 tokens 176 / 180 forward and 326 / 242
+// backward, of 2048 tokens 47 / 50 and 83 / 67; 85 pairs of 11764 tokens into three 245 / 170 and 456 / 227;
+// 32 of 31250 into eight 658 / 183 and 1215 / 255, into four 328 / 423, into sixteen 201 / 267).
+inline int32_t scan_segment_tiles(int64_t B, int64_t D, int64_t T, bool bwd) {
   const int64_t blocks = B * ((D + kScanCols - 1) / kScanCols), tiles = (T + kScanTile - 1) / kScanTile;
   int64_t want = blocks > 0 ? 256 / blocks : 1;  // one workgroup per CU
-  if (want < 2 || tiles < 4) return int32_t(tiles > 0 ? tiles : 1);
+  if (want < (bwd ? 2 : 3) || tiles < 4) return int32_t(tiles > 0 ? tiles : 1);
   if (want > tiles) want = tiles;
   if (want > 64) want = 64;
   return int32_t((tiles + want - 1) / want);
