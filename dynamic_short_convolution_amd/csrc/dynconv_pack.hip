@@ -66,10 +66,15 @@ __device__ __forceinline__ int64_t offset(const PackParams& p, const PackTensor&
   return int64_t(i0) * t.s0 + int64_t(q - i0 * p.n1) * t.s1 + int64_t(row - q * p.n2) * t.s2;
 }
 
-// A lane's place: its columns, and the rows that it goes through.
-template <int E>
+// A lane's place: its columns, and the rows that it goes through. Where pieces are not WHOLE, a row's last one
+// begins early enough to end with it, so that it is read and written with 16 bytes as well: its first `skip`
+// columns are the piece's before it too (40 million bf16 elements in rows of 100: 28 us, with the last piece element by
+// element 90; rows of 515 36 and 77). Only rows shorter than a piece go element by element (n < E).
+template <int E, bool WHOLE>
 struct Walk {
-  uint32_t c, row, step;
+  uint32_t c, row, step;  // c: its own first column
+  uint32_t from, skip;    // where its piece begins
+  int n;                  // elements of a piece, the same for all lanes
   bool on;
   __device__ __forceinline__ explicit Walk(const PackParams& p) {
     const uint32_t cb = blockIdx.x / p.rowBlocks, rb = blockIdx.x - cb * p.rowBlocks;
@@ -77,43 +82,53 @@ struct Walk {
     const uint32_t l = cb * p.perBlock + threadIdx.x - sub * p.perBlock;
     c = l * E;
     on = sub < side && l < p.lanes;
+    n = WHOLE || p.D >= E ? E : int(p.D);
+    from = WHOLE || c >= p.D || p.D < E ? c : min(c, p.D - E);
+    skip = c - from;
     row = rb * side + sub;
     step = p.rowBlocks * side;
   }
 };
 constexpr int kAhead = 4;  // rows whose loads a lane has under way
 
-// A piece: E consecutive elements. WHOLE: aligned, all of them the row's; else its first n are.
+// A piece: E consecutive elements (WHOLE: aligned), or the n of a shorter row.
 template <typename ET, int E, bool WHOLE>
 __device__ __forceinline__ void read(float (&v)[E], const PackTensor& t, int64_t off, int n) {
-  const ET* p = static_cast<const ET*>(t.p) + off;
-  if (WHOLE || n >= E) {
-    const u32x4 w = WHOLE ? *reinterpret_cast<const u32x4*>(p) : *reinterpret_cast<const u32x4_any*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(ET) == 2) {
-        v[2 * i] = Cvt<ET>::lo(w[i]), v[2 * i + 1] = Cvt<ET>::hi(w[i]);
-      } else {
-        v[i] = __uint_as_float(w[i]);
-      }
+  typedef typename std::conditional<sizeof(ET) == 2, uint16_t, uint32_t>::type Bits;
+  const Bits* p = static_cast<const Bits*>(t.p) + off;
+  u32x4 w;
+  if (WHOLE || n == E) {
+    w = WHOLE ? *reinterpret_cast<const u32x4*>(p) : *reinterpret_cast<const u32x4_any*>(p);
+  } else {  // into the words by shifts: registers have no index
+    uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+    for (int e = 0; e < n; ++e) {
+      const uint64_t b = uint64_t(p[e]) << (e % (E / 2) * int(8 * sizeof(ET)));
+      lo |= e < E / 2 ? b : 0;
+      hi |= e < E / 2 ? 0 : b;
     }
-  } else {
+    w = u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+  }
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (e < n) {
-        if constexpr (sizeof(ET) == 2) {
-          v[e] = Cvt<ET>::of_bits(*reinterpret_cast<const uint16_t*>(p + e));
-        } else {
-          v[e] = p[e];
-        }
-      }
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(ET) == 2) {
+      v[2 * i] = Cvt<ET>::lo(w[i]), v[2 * i + 1] = Cvt<ET>::hi(w[i]);
+    } else {
+      v[i] = __uint_as_float(w[i]);
+    }
   }
 }
 
 template <typename ET, int E, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void k_pack8(const PackParams p) {
-  const Walk<E> me(p);
+  const Walk<E, WHOLE> me(p);
   if (!me.on) return;  // whole groups of lanes
+  // A last piece that is alone in its group of channels shares columns with another group's, whose codes
+  // have another step: it leaves them to that one and stores its own byte by byte.
+  const bool lone = !WHOLE && p.D % kGroup < E;
+  const bool wide = WHOLE || (me.n == E && !(lone && me.skip > 0));
+  int8_t* out = const_cast<int8_t*>(static_cast<const int8_t*>(p.codes.p)) + me.from;
+  uint8_t* sc = const_cast<uint8_t*>(static_cast<const uint8_t*>(p.scales.p)) + me.c / kGroup;
   for (uint32_t row = me.row; row < p.rows; row += kAhead * me.step) {
     float v[kAhead][E];
 #pragma unroll
@@ -121,15 +136,16 @@ __global__ __launch_bounds__(kThreads) void k_pack8(const PackParams p) {
 #pragma unroll
       for (int e = 0; e < E; ++e) v[u][e] = 0.f;
       const uint32_t r = row + u * me.step;  // below 2^31 + 4 * 2^20
-      if (me.c < p.D) read<ET, E, WHOLE>(v[u], p.x, offset(p, p.x, r < p.rows ? r : row) + me.c, int(p.D - me.c));
+      if (me.c < p.D) read<ET, E, WHOLE>(v[u], p.x, offset(p, p.x, r < p.rows ? r : row) + me.from, me.n);
     }
+    uint32_t q[kAhead][2];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const uint32_t r = row + u * me.step;
       if (r >= p.rows) break;
       uint32_t top = 0;  // as integers the magnitudes keep their order, and infinities and NaN come last
 #pragma unroll
-      for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(v[u][e]) & 0x7fffffffu);
+      for (int e = 0; e < E; ++e) top = max(top, lone && uint32_t(e) < me.skip ? 0u : __float_as_uint(v[u][e]) & 0x7fffffffu);
       top = group_max<kGroup / E>(top);
       const int biased = int(top >> 23);
       const bool lost = biased == 255;
@@ -138,31 +154,33 @@ __global__ __launch_bounds__(kThreads) void k_pack8(const PackParams p) {
       uint32_t code[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float q = fminf(fmaxf(rintf(v[u][e] * inverse), -127.f), 127.f);
-        code[e] = lost ? 0u : uint32_t(int(q)) & 0xffu;
+        const float c = fminf(fmaxf(rintf(v[u][e] * inverse), -127.f), 127.f);
+        code[e] = lost ? 0u : uint32_t(int(c)) & 0xffu;
       }
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i)
+        q[u][i] = code[4 * i] | code[4 * i + 1] << 8 | code[4 * i + 2] << 16 | code[4 * i + 3] << 24;
       if (me.c >= p.D) continue;
-      if (me.c % kGroup == 0)
-        const_cast<uint8_t*>(static_cast<const uint8_t*>(p.scales.p))[offset(p, p.scales, r) + me.c / kGroup] = uint8_t(scale);
-      int8_t* out = const_cast<int8_t*>(static_cast<const int8_t*>(p.codes.p)) + offset(p, p.codes, r) + me.c;
-      if (WHOLE || me.c + E <= p.D) {
-        uint32_t q[E / 4];
-#pragma unroll
-        for (int i = 0; i < E / 4; ++i)
-          q[i] = code[4 * i] | code[4 * i + 1] << 8 | code[4 * i + 2] << 16 | code[4 * i + 3] << 24;
-        typename Codes<E, WHOLE>::T w;
-        if constexpr (E == 8) {
-          w = u32x2{q[0], q[1]};
-        } else {
-          w = q[0];
-        }
-        *reinterpret_cast<typename Codes<E, WHOLE>::At*>(out) = w;
+      if (me.c % kGroup == 0) sc[offset(p, p.scales, r)] = uint8_t(scale);
+      typename Codes<E, WHOLE>::T w;
+      if constexpr (E == 8) {
+        w = u32x2{q[u][0], q[u][1]};
       } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (me.c + e < p.D) out[e] = int8_t(code[e]);
+        w = q[u][0];
       }
+      if (wide) *reinterpret_cast<typename Codes<E, WHOLE>::At*>(out + offset(p, p.codes, r)) = w;
     }
+    if constexpr (!WHOLE)
+      if (!wide && me.c < p.D)
+#pragma unroll 1
+        for (int e = int(me.skip); e < me.n; ++e)
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            const uint32_t r = row + u * me.step;
+            if (r >= p.rows) break;
+            const uint64_t bytes = E == 8 ? uint64_t(q[u][1]) << 32 | q[u][0] : q[u][0];
+            out[offset(p, p.codes, r) + e] = int8_t(uint8_t(bytes >> (8 * e)));
+          }
   }
 }
 
@@ -170,35 +188,37 @@ template <typename ET, int E, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void k_unpack8(const PackParams p) {
   typedef typename Codes<E, WHOLE>::T Word;
   typedef typename Codes<E, WHOLE>::At WordAt;
-  const Walk<E> me(p);
+  const Walk<E, WHOLE> me(p);
   if (!me.on || me.c >= p.D) return;
   for (uint32_t row = me.row; row < p.rows; row += kAhead * me.step) {
     Word w[kAhead];
-    uint32_t scale[kAhead];
+    uint32_t scale[kAhead], next[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const uint32_t r = row + u * me.step, s = r < p.rows ? r : row;
-      const int8_t* in = static_cast<const int8_t*>(p.codes.p) + offset(p, p.codes, s) + me.c;
-      if (WHOLE || me.c + E <= p.D) {
+      const int8_t* in = static_cast<const int8_t*>(p.codes.p) + offset(p, p.codes, s) + me.from;
+      if (WHOLE || me.n == E) {
         w[u] = *reinterpret_cast<const WordAt*>(in);
       } else {
         uint32_t q[2] = {0, 0};
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          if (me.c + e < p.D) q[e / 4] |= uint32_t(uint8_t(in[e])) << (8 * (e % 4));
+          if (e < me.n) q[e / 4] |= uint32_t(uint8_t(in[e])) << (8 * (e % 4));
         if constexpr (E == 8) {
           w[u] = u32x2{q[0], q[1]};
         } else {
           w[u] = q[0];
         }
       }
-      scale[u] = static_cast<const uint8_t*>(p.scales.p)[offset(p, p.scales, s) + me.c / kGroup];
+      const uint8_t* sc = static_cast<const uint8_t*>(p.scales.p) + offset(p, p.scales, s);
+      scale[u] = sc[me.from / kGroup];
+      if constexpr (!WHOLE) next[u] = sc[me.c / kGroup];
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const uint32_t r = row + u * me.step;
       if (r >= p.rows) break;
-      const float step = __uint_as_float(scale[u] << 23);
+      const float step = __uint_as_float(scale[u] << 23), own = WHOLE ? step : __uint_as_float(next[u] << 23);
       float v[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -208,10 +228,10 @@ __global__ __launch_bounds__(kThreads) void k_unpack8(const PackParams p) {
         } else {
           word = w[u];
         }
-        v[e] = float(int8_t(word >> (8 * (e % 4)) & 0xff)) * step;
+        v[e] = float(int8_t(word >> (8 * (e % 4)) & 0xff)) * (WHOLE || uint32_t(e) < me.skip ? step : own);
       }
-      ET* out = const_cast<ET*>(static_cast<const ET*>(p.x.p)) + offset(p, p.x, r) + me.c;
-      if (WHOLE || me.c + E <= p.D) {
+      ET* out = const_cast<ET*>(static_cast<const ET*>(p.x.p)) + offset(p, p.x, r) + me.from;
+      if (WHOLE || me.n == E) {
         u32x4 o;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -229,7 +249,7 @@ __global__ __launch_bounds__(kThreads) void k_unpack8(const PackParams p) {
       } else {
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          if (me.c + e < p.D) {
+          if (e < me.n) {
             if constexpr (sizeof(ET) == 2) {
               *reinterpret_cast<uint16_t*>(out + e) = Cvt<ET>::bits(v[e]);
             } else {

@@ -425,6 +425,24 @@ def test_pack8_of_extremes(dtype):
     assert bool(back[3, 64:].isnan().all()) and float(back[3, :64].abs().max()) == 0.0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_pack8_of_every_width(dtype):
+    """Rows shorter than a piece, last pieces that reach back (also into another group), and what stands beside the rows.
+    Some float16 groups hold an infinity: they read as NaN."""
+    td = TD[dtype]
+    for D in [*range(1, 140), 191, 193, 257, 515, 1000, 1025, 16385]:
+        x = rand(220 + D, 9, D, dtype=td) * torch.exp(4 * rand(221 + D, 9, 1)).to(td)
+        codes, held = pack8(to64(x))[0], held8(to64(x))
+        for off in (0, 3):
+            guard = torch.full((9, D + 16 + off), 77, dtype=torch.int8, device="cuda")
+            p = dc.dynconv_pack8(x, out=dc.Packed8(guard[:, off:off + D], torch.zeros(9, -(-D // 64), dtype=torch.uint8, device="cuda")))
+            assert np.array_equal(to64(p.codes), codes), (D, off)
+            out = torch.full((9, D + 16 + off), 5.0, dtype=td, device="cuda")
+            assert np.array_equal(to64(dc.dynconv_unpack8(p, td, out=out[:, off:off + D])), held, equal_nan=True), (D, off)
+            guard[:, off:off + D], out[:, off:off + D] = 77, 5.0
+            assert bool((guard == 77).all()) and bool((out == 5.0).all()), (D, off)
+
+
 def test_pack8_views_and_empty():
     x = rand(210, 6, 5, 130, dtype=torch.bfloat16)
     want = dc.dynconv_pack8(x)
