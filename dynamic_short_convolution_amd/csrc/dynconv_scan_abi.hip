@@ -31,14 +31,17 @@ dynconv_status check_sizes(const Sizes& z, dynconv_dtype dt) {
   return DYNCONV_OK;
 }
 
-// An activation [B,T,D] of eb-byte elements; clears *vec when two channels at a time are not aligned.
-dynconv_status take(ScanTensor* t, const void* p, const int64_t* s, const Sizes& z, int eb, bool output, int* vec) {
+// An activation [B,T,D] of eb-byte elements; clears *vec when two channels at a time are not aligned, sets
+// *shared when 64 channels of a row are not whole 128-byte lines.
+dynconv_status take(ScanTensor* t, const void* p, const int64_t* s, const Sizes& z, int eb, bool output, int* vec,
+                    bool* shared) {
   if (p == nullptr || s == nullptr) return DYNCONV_ERR_INVALID_ARG;
   if (!aligned(p, eb) || (z.D > 1 && s[2] != 1) || s[0] < 0 || s[1] < 0) return DYNCONV_ERR_UNSUPPORTED;
   if (z.T > 1 && s[1] >= kScanMaxTokenStride) return DYNCONV_ERR_UNSUPPORTED;
   // an output's rows have places of their own (the kernels drop rows that do not exist by their offsets)
   if (output && ((z.B > 1 && s[0] == 0) || (z.T > 1 && s[1] < z.D))) return DYNCONV_ERR_INVALID_ARG;
   if (!aligned(p, 2 * eb) || (z.B > 1 && s[0] % 2 != 0) || (z.T > 1 && s[1] % 2 != 0)) *vec = 1;
+  if (eb == 1 || !aligned(p, 128) || (z.B > 1 && s[0] * eb % 128 != 0) || (z.T > 1 && s[1] * eb % 128 != 0)) *shared = true;
   t->p = p;
   t->s0 = s[0];
   t->s1 = z.T > 1 ? s[1] : kScanCols;  // a single token's is not used: any that puts the next row out of the range
@@ -150,10 +153,10 @@ dynconv_status dynconv_scan_fwd(const void* x, const int64_t* xs, const void* de
     if (state_out == nullptr || state_out == state_in) return DYNCONV_OK;
     return done(scan_copy_state(state_in, state_in != nullptr ? sis[0] : 0, state_out, sos[0], int32_t(B), int32_t(D), s));
   }
-  if ((st = take(&p.x, x, xs, z, eb, false, &vec)) != DYNCONV_OK) return st;
-  if ((st = take(&p.decay, decay, as, z, eb, false, &vec)) != DYNCONV_OK) return st;
-  if (gate != nullptr && (st = take(&p.gate, gate, gs, z, eb, false, &vec)) != DYNCONV_OK) return st;
-  if ((st = take(&p.y, y, ys, z, eb, true, &vec)) != DYNCONV_OK) return st;
+  if ((st = take(&p.x, x, xs, z, eb, false, &vec, &p.shared)) != DYNCONV_OK) return st;
+  if ((st = take(&p.decay, decay, as, z, eb, false, &vec, &p.shared)) != DYNCONV_OK) return st;
+  if (gate != nullptr && (st = take(&p.gate, gate, gs, z, eb, false, &vec, &p.shared)) != DYNCONV_OK) return st;
+  if ((st = take(&p.y, y, ys, z, eb, true, &vec, &p.shared)) != DYNCONV_OK) return st;
   if ((st = take_seg(&p, seq_idx, ss)) != DYNCONV_OK) return st;
   if (rate == nullptr) return DYNCONV_ERR_INVALID_ARG;
   if (!aligned(rate, 4) || (chunks != nullptr && !aligned(chunks, 4))) return DYNCONV_ERR_UNSUPPORTED;
@@ -221,19 +224,19 @@ dynconv_status dynconv_scan_bwd(const void* x, const int64_t* xs, const void* de
   if (packed != (decay_scales != nullptr) || (packed && gate != nullptr) != (gate_scales != nullptr))
     return DYNCONV_ERR_INVALID_ARG;
   const int ib = packed ? 1 : eb;
-  if ((st = take(&p.x, x, xs, z, ib, false, &vec)) != DYNCONV_OK) return st;
-  if ((st = take(&p.decay, decay, as, z, ib, false, &vec)) != DYNCONV_OK) return st;
-  if (gate != nullptr && (st = take(&p.gate, gate, gs, z, ib, false, &vec)) != DYNCONV_OK) return st;
+  if ((st = take(&p.x, x, xs, z, ib, false, &vec, &p.shared)) != DYNCONV_OK) return st;
+  if ((st = take(&p.decay, decay, as, z, ib, false, &vec, &p.shared)) != DYNCONV_OK) return st;
+  if (gate != nullptr && (st = take(&p.gate, gate, gs, z, ib, false, &vec, &p.shared)) != DYNCONV_OK) return st;
   if (packed) {
     if ((st = take_scales(&p.x, x_scales, xcs, z)) != DYNCONV_OK) return st;
     if ((st = take_scales(&p.decay, decay_scales, acs, z)) != DYNCONV_OK) return st;
     if (gate != nullptr && (st = take_scales(&p.gate, gate_scales, gcs, z)) != DYNCONV_OK) return st;
   }
-  if ((st = take(&p.dy, dy, dys, z, eb, false, &vec)) != DYNCONV_OK) return st;
-  if ((st = take(&p.dx, dx, dxs, z, eb, true, &vec)) != DYNCONV_OK) return st;
-  if ((st = take(&p.ddecay, ddecay, das, z, eb, true, &vec)) != DYNCONV_OK) return st;
+  if ((st = take(&p.dy, dy, dys, z, eb, false, &vec, &p.shared)) != DYNCONV_OK) return st;
+  if ((st = take(&p.dx, dx, dxs, z, eb, true, &vec, &p.shared)) != DYNCONV_OK) return st;
+  if ((st = take(&p.ddecay, ddecay, das, z, eb, true, &vec, &p.shared)) != DYNCONV_OK) return st;
   if ((gate != nullptr) != (dgate != nullptr)) return DYNCONV_ERR_INVALID_ARG;
-  if (gate != nullptr && (st = take(&p.dgate, dgate, dgs, z, eb, true, &vec)) != DYNCONV_OK) return st;
+  if (gate != nullptr && (st = take(&p.dgate, dgate, dgs, z, eb, true, &vec, &p.shared)) != DYNCONV_OK) return st;
   if ((st = take_seg(&p, seq_idx, ss)) != DYNCONV_OK) return st;
   const BwdSpace w = bwd_space(z, chunks != nullptr);
   if (workspace == nullptr || workspace_bytes < w.total()) return DYNCONV_ERR_WORKSPACE;
@@ -277,9 +280,10 @@ dynconv_status dynconv_scan_step(const void* x, const int64_t* xs, const void* d
   ScanStepParams p{};
   auto row = [&](const void* t, const int64_t* s, bool output, int64_t* stride) {
     ScanTensor out;
+    bool shared;
     if (t == nullptr || s == nullptr) return dynconv_status(DYNCONV_ERR_INVALID_ARG);
     const int64_t s3[3] = {s[0], 0, s[1]};
-    const dynconv_status r = take(&out, t, s3, z, eb, output, &vec);
+    const dynconv_status r = take(&out, t, s3, z, eb, output, &vec, &shared);
     *stride = s[0];
     return r;
   };

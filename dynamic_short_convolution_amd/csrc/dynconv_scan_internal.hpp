@@ -47,6 +47,7 @@ struct ScanParams {
   // segment s + 1, in reverse.
   float2* maps;
   int32_t B, T, D, nSeg, segTiles;  // segTiles: tiles per segment
+  bool shared;                      // workgroups side by side share 128-byte lines of a tensor
 };
 
 // Tiles per segment. A workgroup walks its tiles one behind the other; with few (sequence, 64

@@ -124,6 +124,15 @@ __device__ __forceinline__ Decay decay_of(float s, float rate) {
 
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset behind every buffer's range
 
+// The (sequence, 64 channels) pair of a workgroup. Where the 64 channels of a row are not whole 128-byte lines,
+// workgroups side by side share lines, so they go to one XCD and its L2 (64 sequences of 2000 tokens, 500 channels,
+// bf16: forward 117 us, apart 147, backward 216 and 311; 8 of 4096 x 2048 from 8-bit inputs 551 and 558 in all).
+// Else they go to the XCDs in turn (8 sequences of 1953 tokens, 4096 channels: forward 123 us, in one XCD 131,
+// backward 214 and 229).
+__device__ __forceinline__ int block_at(const ScanParams& p) {
+  return int(p.shared ? xcd_logical_block(blockIdx.x, gridDim.x) : blockIdx.x);
+}
+
 // Where a lane stands: its channels, its lane group's run of tokens.
 template <int V>
 struct Lane {
@@ -324,7 +333,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
   __shared__ uint64_t starts[2][Starts::kWords];
   __shared__ __attribute__((aligned(16))) float steps[PACKED ? 2 : 1][3][PACKED ? kScanTile : 1];
   const int nCols = (p.D + kScanCols - 1) / kScanCols;
-  const int b = int(blockIdx.x) / nCols, c0 = (int(blockIdx.x) - b * nCols) * kScanCols, seg = blockIdx.y;
+  const int at = block_at(p), b = at / nCols, c0 = (at - b * nCols) * kScanCols, seg = blockIdx.y;
   const Lane<V> me(p.D, c0);
   const bool gated = p.gate.p != nullptr;
   float rate[V], carry[V], total[V];
@@ -533,7 +542,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
   __shared__ uint64_t starts[2][Starts::kWords];
   __shared__ __attribute__((aligned(16))) float steps[PACKED ? 2 : 1][3][PACKED ? kScanTile : 1];
   const int nCols = (p.D + kScanCols - 1) / kScanCols;
-  const int b = int(blockIdx.x) / nCols, c0 = (int(blockIdx.x) - b * nCols) * kScanCols;
+  const int at = block_at(p), b = at / nCols, c0 = (at - b * nCols) * kScanCols;
   const int seg = int(blockIdx.y) + (MAPS ? 1 : 0);
   const Lane<V> me(p.D, c0);
   const bool gated = p.gate.p != nullptr;
