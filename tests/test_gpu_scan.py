@@ -98,6 +98,17 @@ def test_segments_of_long_sequences(dtype, shape, docs):
     check(*inputs(*shape, dtype, True, docs, True, seed=20))
 
 
+@pytest.mark.parametrize("dtype,docs", [("bf16", 0), ("f32", 20)])
+@pytest.mark.parametrize("shape", [(128, 515, 3), (16, 641, 500)], ids=str)
+def test_only_the_backward_is_cut(shape, dtype, docs):
+    """128 workgroups: the forward, which the backward may repeat, runs whole."""
+    assert dc._lib.load().dynconv_scan_fwd_workspace_size(*shape, 0) == 0
+    B, T, D = shape
+    one = dc._lib.load().dynconv_scan_bwd_workspace_size(B, T, D, 1, 0)
+    assert one >= 2 * B * D * 4 + 2 * B * D * 8  # two segments' partial sums and maps
+    check(*inputs(*shape, dtype, True, docs, True, seed=25))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("docs", [0, 9])
 @pytest.mark.parametrize("shape", [(1, 1, 3), (2, 130, 64), (1, 300, 129), (2, 257, 200), (1, 2100, 66)], ids=str)
