@@ -595,29 +595,48 @@ __device__ __forceinline__ void zero_tokens(const GroupTensor& out, const GroupP
   for (; t < q.t1; t += p.tps) store<ET, E, WHOLE>(zero, out.p, q.b * out.s0 + t * out.s1 + c, n);
 }
 
-// Sums over the lanes of each of a workgroup's groups: v[i] of thread (tsub, l).
-// The result of group g is in out[g][i] for every thread after the call.
+// Sums over the lanes of each of a workgroup's groups: v[i] of thread (tsub, l). The result of group g is in
+// out[g][i] for every thread after the call. red: N values per thread. As many neighbouring threads as there
+// are (a power of two) add up a group, in a wave without LDS.
 template <int N>
 __device__ __forceinline__ void group_sums(const GroupParams& p, const Place& q, const double (&v)[N], double* red,
                                            double* out) {
   const int lanes = p.gpb > 1 ? p.lpg : p.lpt;  // lanes of a group and token
-  int per = 1;  // threads that add up one group
+  int per = 1;
   while (per * 2 * p.gpb <= kThreads) per *= 2;
   const int g = threadIdx.x / per, j = threadIdx.x - g * per;
-  for (int i = 0; i < N; ++i) {
-    __syncthreads();
-    red[threadIdx.x] = q.on ? v[i] : 0.0;
-    __syncthreads();
-    double s = 0.0;
-    if (g < p.gpb)
-      for (int e = j; e < lanes * p.tps; e += per) s += red[(e / lanes) * p.lpt + g * lanes + e % lanes];
-    for (int h = per / 2; h > 0; h /= 2) {
-      __syncthreads();
-      red[threadIdx.x] = s;
-      __syncthreads();
-      if (j < h) s += red[threadIdx.x + h];
+#pragma unroll
+  for (int i = 0; i < N; ++i) red[i * kThreads + threadIdx.x] = q.on ? v[i] : 0.0;
+  __syncthreads();
+  double s[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] = 0.0;
+  if (g < p.gpb)
+    for (int e = j; e < lanes * p.tps; e += per) {
+      const int at = (e / lanes) * p.lpt + g * lanes + e % lanes;
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] += red[i * kThreads + at];
     }
-    if (g < p.gpb && j == 0) out[g * N + i] = s;
+  for (int m = 1; m < per && m < 64; m *= 2) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] += __shfl_xor(s[i], m);
+  }
+  if (per > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) red[i * kThreads + (threadIdx.x >> 6)] = s[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      s[i] = 0.0;
+      for (int w = 0; w < per / 64; ++w) s[i] += red[i * kThreads + g * (per / 64) + w];
+    }
+  }
+  if (g < p.gpb && j == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[g * N + i] = s[i];
   }
   __syncthreads();
 }
@@ -625,7 +644,7 @@ __device__ __forceinline__ void group_sums(const GroupParams& p, const Place& q,
 template <typename ET, int E, bool WHOLE, bool PACKED>
 __global__ __launch_bounds__(kThreads) void k_group_stats(const GroupParams p) {
   using IT = std::conditional_t<PACKED, i8_t, ET>;
-  __shared__ double red[kThreads], out[kThreads * 2];
+  __shared__ double red[kThreads * 2], out[kThreads * 2];
   const Place q = place<E>(p);
   const int end = min(q.t1, q.n);
   typedef Piece<E, WHOLE> P;
@@ -768,7 +787,7 @@ __global__ __launch_bounds__(kThreads) void k_group_columns(const GroupParams p)
 template <typename ET, int E, bool WHOLE, bool PACKED>
 __global__ __launch_bounds__(kThreads) void k_group_gradient(const GroupParams p) {
   using IT = std::conditional_t<PACKED, i8_t, ET>;
-  __shared__ double red[kThreads], out[kThreads * 2];
+  __shared__ double red[kThreads * 2], out[kThreads * 2];
   const Place q = place<E>(p);
   const int end = min(q.t1, q.n);
   const bool gated = p.gate.p != nullptr, silu = p.silu != 0;
