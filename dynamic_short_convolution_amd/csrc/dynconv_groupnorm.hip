@@ -132,8 +132,9 @@ void group_sequence_plan(GroupParams* p, int E) {
   // Workgroups per CU: eight (four are 5 % better where all have work, and 5 % worse where half of the tokens of a
   // batch do not exist: 8 sequences of 2048 bf16 channels, both directions 174 and 184 us), in the
   // gradient's two passes four, each of which leaves a row of column sums or begins with a sum over the
-  // groups. Such a row is paid for by 32 of a lane's tokens, by 8 where there would be fewer than two workgroups
-  // per CU (8 sequences of 610 tokens, one group of 8192 bf16 channels: 191 us, with 32 always 329).
+  // groups. Such a row is paid for by 16 of a lane's tokens (27 groups of 57 bf16 channels, 26000 tokens: 187 us,
+  // with 32 212; 64 groups of 16 137 and 147), by 8 where there would be fewer than two workgroups per CU (8
+  // sequences of 610 tokens, one group of 8192: 191, with 16 231, with 32 328).
   auto cut = [&](int64_t all, int least, int32_t* chunk, int32_t* n) {
     const int64_t want = across < all ? all / across : 1;
     int64_t c = (int64_t(p->T) + want - 1) / want;
@@ -142,7 +143,7 @@ void group_sequence_plan(GroupParams* p, int E) {
     *n = int32_t((p->T + c - 1) / c);
   };
   cut(2048, 8, &p->chunk, &p->nChunk);
-  cut(1024, across * (p->T / (32 * p->tps)) >= 512 ? 32 : 8, &p->gradChunk, &p->nGradChunk);
+  cut(1024, across * (p->T / (16 * p->tps)) >= 512 ? 16 : 8, &p->gradChunk, &p->nGradChunk);
 }
 
 namespace {
