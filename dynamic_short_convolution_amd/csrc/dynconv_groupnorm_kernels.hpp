@@ -557,8 +557,9 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
 // wide one at a time) of a run of tokens; a lane keeps its channels and goes along the tokens, tps
 // of them side by side. x is read twice: once for the sums, once for the result; the backward reads x and dy for
 // the column sums, from which the groups' means follow, and again for the result. Bound by memory: 8
-// sequences of 0 to 4096 tokens (half of them in all), 32 groups of 64, bf16: sums 26 us, result 34 to 36, column
-// sums 43 to 45, gradient 52 to 55 (3.7 to 4.8 TB/s), three small sums 18.
+// sequences of 0 to 4096 tokens (half of them in all), 32 groups of 64, bf16: sums 26 to 29 us, result 36 to 38, column
+// sums 43 to 45, gradient 52 to 54 (2.4 to 5 TB/s), three small sums 17. With float32 in place of float64 sums the
+// first pass takes as long.
 // ---------------------------------------------------------------------------------
 struct Place {
   int b, g0, t0, t1, n, tsub, l;  // t0..t1: its tokens, of n that exist; l: lane of the token
