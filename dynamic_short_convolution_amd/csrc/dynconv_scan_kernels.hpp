@@ -115,7 +115,9 @@ __device__ __forceinline__ float one_minus_square(float v, float a) {
   return v < 0.36f ? small : large;
 }
 
-// One token's decay and input scale: a, 1/b (0 where b is 0) and b. rate: in units of log 2.
+// One token's decay and input scale: a, 1/b (0 where b is 0) and b. rate: in units of log 2. The instructions of
+// roots and reciprocals take a denormal as zero, so b of a denormal 1 - a^2 is 0, as the forward's root has it, and
+// 1/b must not become infinite.
 struct Decay {
   float a, rb, b;
 };
@@ -124,7 +126,7 @@ __device__ __forceinline__ Decay decay_of(float s, float rate) {
   Decay d;
   d.a = __builtin_amdgcn_exp2f(-v);
   const float q = one_minus_square(v, d.a);
-  d.rb = q == 0.f ? 0.f : __builtin_amdgcn_rsqf(q);
+  d.rb = __builtin_fabsf(q) < 0x1p-126f ? 0.f : __builtin_amdgcn_rsqf(q);
   d.b = q * d.rb;
   return d;
 }

@@ -524,9 +524,9 @@ size_t dynconv_scan_fwd_workspace_size(int64_t B, int64_t T, int64_t D, dynconv_
  *   dx, ddecay, dgate  [B,T,D] of `dtype`; dgate is required with a gate
  *   drate      float32 [D], overwritten (sums in 64 bits in a fixed order)
  *   dstate_in  float32 [B,D], the gradient of the initial state, or NULL to skip
- * Where sqrt(1 - a^2) is 0 in float32 (rate or s of 0) its derivative is taken as 0. Without tokens
- * drate is zero and dstate_in a copy of dstate_out. Needs dynconv_scan_bwd_workspace_size(...) bytes
- * (aligned to 8; with_chunks: whether chunks are given).
+ * Where 1 - a^2 is below 2^-126 (rate or s of nearly 0) it counts as 0, here as in the other calls, and the
+ * derivative of its root as 0. Without tokens drate is zero and dstate_in a copy of dstate_out. Needs
+ * dynconv_scan_bwd_workspace_size(...) bytes (aligned to 8; with_chunks: whether chunks are given).
  */
 dynconv_status dynconv_scan_bwd(const void* x, const int64_t* xs, const void* decay, const int64_t* as, const void* gate,
                                 const int64_t* gs, const uint8_t* x_scales, const int64_t* xcs,
