@@ -273,9 +273,11 @@ __device__ __forceinline__ float through(float A, float H, float h) {
   const float r = __builtin_fmaf(A, h, H);
   return DOCS ? (A == 0.f ? H : r) : r;
 }
+// The product of two maps' factors: what either of them forgets is forgotten, whatever the other one is (the factors of
+// a run serve both directions, in which a NaN is before or behind the document start).
 template <bool DOCS>
-__device__ __forceinline__ float chain(float A, float B) {  // of two maps' factors
-  return DOCS ? (A == 0.f ? 0.f : A * B) : A * B;
+__device__ __forceinline__ float chain(float A, float B) {
+  return DOCS ? (A == 0.f || B == 0.f ? 0.f : A * B) : A * B;
 }
 
 // Of the lane groups of a wave, one behind the other: the maps (A, H) become those of the group and all
@@ -703,7 +705,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
 #pragma unroll
     for (int j = L - 1; j >= 0; --j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) E[i] = chain<DOCS>(pass(j, i), dy[j][i] + E[i]);
+      for (int i = 0; i < V; ++i) {
+        const float f = pass(j, i), dh = dy[j][i] + E[i];
+        E[i] = DOCS && f == 0.f ? 0.f : f * dh;
+      }
     float pA[V], pH[V], rA[V], rE[V], B[V];  // the maps of the lane groups before and behind this one
 #pragma unroll
     for (int i = 0; i < V; ++i) B[i] = A[i];

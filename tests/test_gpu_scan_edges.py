@@ -82,3 +82,50 @@ def test_nearly_closed_decay_gates_backward(kept, dtype):
     # drate's terms sqrt(sigmoid / (2 rate)) dh sg x of such tokens: below 2^-63 / rate
     lim = (up * np.abs(x)).sum((0, 1)) * B_OFF / rate
     near("drate", got[2][:28], ref[2][:28], bounds[2][:28] + lim[:28])
+
+
+# ---------------------------------------------------------------------------------
+# NaN and infinities with documents
+# ---------------------------------------------------------------------------------
+
+
+def with_documents(B, T, D, dtype, starts, seed, scale=1.0):
+    s, dy, dlast = inputs(B, T, D, dtype, True, 0, True, seed=seed)
+    seq = torch.zeros(B, T, dtype=torch.int32)
+    for t in starts:
+        seq[:, t:] += 1
+    s["seq_idx"] = seq.cuda()
+    s["rate"] *= scale
+    return s, dy, dlast
+
+
+def both(s, dy, dlast):
+    y, last, chunks = dc.dynconv_scan_fwd(**s, want_state=True, want_chunks=True)
+    kw = dict(dy=dy, dstate_out=dlast, need_dstate=True)
+    return (y, last), [dc.dynconv_scan_bwd(**s, chunks=c, **kw) for c in (chunks, None)]
+
+
+# one and two channels per lane (runs of 16 and 8 tokens); cut into segments, or too many workgroups for that
+SHAPES = [("f32", 1, 600, 70), ("bf16", 1, 600, 70), ("bf16", 1, 600, 65), ("f16", 140, 300, 64), ("f32", 140, 300, 64)]
+
+
+@pytest.mark.parametrize("dtype,B,T,D", SHAPES, ids=str)
+@pytest.mark.parametrize("start,end,at", [(146, 290, 148), (144, 290, 151), (128, 290, 135), (36, 290, 40), (146, 150, 148), (130, 146, 145),
+                                          (146, 290, 146), (256, 290, 257)])
+def test_nan_in_the_run_of_its_documents_start(dtype, B, T, D, start, end, at):
+    """Nothing of it reaches another document or channel, forwards or backwards, kept states or none."""
+    s, dy, dlast = with_documents(B, T, D, dtype, (start, end), 310)
+    clean, cg = both(s, dy, dlast)
+    hit = torch.zeros(B, T, D, dtype=torch.bool, device="cuda")
+    hit[0, start:end, 5] = True
+    for t in (s["x"], s["decay"], s["gate"], dy):
+        keep = t[0, at, 5].clone()
+        t[0, at, 5] = float("nan")
+        (y, last), grads = both(s, dy, dlast)
+        t[0, at, 5] = keep
+        assert torch.equal(y[~hit], clean[0][~hit]) and torch.equal(last, clean[1])
+        for got, want in zip(grads, cg):
+            for i in (0, 1, 3):
+                assert torch.equal(got[i][~hit], want[i][~hit]), GRADS[i]
+            assert torch.equal(got[4], want[4])
+            assert torch.equal(got[2][:5], want[2][:5]) and torch.equal(got[2][6:], want[2][6:])
