@@ -266,18 +266,20 @@ struct Starts {
   }
 };
 
-// h -> A h + H. With documents an A of zero (their start, or a decay to nothing) forgets what came
-// before, a NaN of another document too.
+// h -> A h + H. With documents a factor of -0 marks a map that holds a document's start: it forgets what came before,
+// a NaN of another document too. Decays are positive, so a product of them that underflows is +0 and lets a NaN or
+// infinity of its own document through.
+__device__ __forceinline__ bool forgets(float A) { return __float_as_uint(A) == 0x80000000u; }
 template <bool DOCS>
 __device__ __forceinline__ float through(float A, float H, float h) {
   const float r = __builtin_fmaf(A, h, H);
-  return DOCS ? (A == 0.f ? H : r) : r;
+  return DOCS && forgets(A) ? H : r;
 }
 // The product of two maps' factors: what either of them forgets is forgotten, whatever the other one is (the factors of
 // a run serve both directions, in which a NaN is before or behind the document start).
 template <bool DOCS>
 __device__ __forceinline__ float chain(float A, float B) {
-  return DOCS ? (A == 0.f || B == 0.f ? 0.f : A * B) : A * B;
+  return DOCS && (forgets(A) || forgets(B)) ? -0.f : A * B;
 }
 
 // Of the lane groups of a wave, one behind the other: the maps (A, H) become those of the group and all
@@ -450,7 +452,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
 #pragma unroll
       for (int j = 0; j < L; ++j)
 #pragma unroll
-        for (int i = 0; i < V; ++i) a[j][i] = m >> j & 1 ? 0.f : a[j][i];
+        for (int i = 0; i < V; ++i) a[j][i] = m >> j & 1 ? -0.f : a[j][i];
     }
     float A[V], H[V];
 #pragma unroll
@@ -687,7 +689,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
     fetch(turn + 1);
     uint32_t first = 0;  // tokens that start a document: nothing passes through them, forwards or backwards
     if constexpr (DOCS) first = Starts::of_run(starts[half], me.run, L);
-    auto pass = [&](int j, int i) { return DOCS && (first >> j & 1) ? 0.f : a[j][i]; };
+    auto pass = [&](int j, int i) { return DOCS && (first >> j & 1) ? -0.f : a[j][i]; };
     float A[V], H[V], E[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) A[i] = 1.f, H[i] = 0.f, E[i] = 0.f;
@@ -707,7 +709,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float f = pass(j, i), dh = dy[j][i] + E[i];
-        E[i] = DOCS && f == 0.f ? 0.f : f * dh;
+        E[i] = DOCS && forgets(f) ? 0.f : f * dh;
       }
     float pA[V], pH[V], rA[V], rE[V], B[V];  // the maps of the lane groups before and behind this one
 #pragma unroll
@@ -776,7 +778,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
       for (int j = 0; j < L; ++j)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float f = pass(j, i), before = DOCS ? (f == 0.f ? 0.f : h[i]) : h[i];
+          const float f = pass(j, i), before = DOCS && forgets(f) ? 0.f : h[i];
           h[i] = through<DOCS>(f, hb[j][i], h[i]);
           hb[j][i] = before;
         }

@@ -129,3 +129,29 @@ def test_nan_in_the_run_of_its_documents_start(dtype, B, T, D, start, end, at):
                 assert torch.equal(got[i][~hit], want[i][~hit]), GRADS[i]
             assert torch.equal(got[4], want[4])
             assert torch.equal(got[2][:5], want[2][:5]) and torch.equal(got[2][6:], want[2][6:])
+
+
+@pytest.mark.parametrize("dtype,B,T,D", SHAPES, ids=str)
+@pytest.mark.parametrize("documents", [True, False])
+def test_infinity_stays_through_its_document(dtype, B, T, D, documents):
+    """Decays of about a half, whose product over a tile underflows to zero: the state behind an infinity is not finite
+    to the document's end, the gradients before one not from its start, with document ids and without."""
+    starts, at = (20, 290), 33
+    s, dy, dlast = with_documents(B, T, D, dtype, starts, 320, scale=6.0)
+    s["rate"] = torch.clamp(s["rate"], 1.0, 4.0)
+    assert 0.0 < float(torch.exp(-s["rate"].max())) < 0.1
+    first, end = starts
+    if not documents:
+        s["seq_idx"], first, end = None, 0, T
+    s["x"][0, at, 5] = float("inf")
+    (y, last), grads = both(s, dy, dlast)
+    assert not bool(torch.isfinite(y[0, at:end, 5]).any())
+    assert bool(torch.isfinite(last[0, 5])) == documents
+    for g in grads:  # through h_{t-1}
+        assert not bool(torch.isfinite(g[1][0, at + 1:end, 5]).any()) and not bool(torch.isfinite(g[2][5]))
+    s["x"][0, at, 5] = 1.0
+    back = end - 7
+    dy[0, back, 5] = float("inf")
+    for g in both(s, dy, dlast)[1]:
+        assert not bool(torch.isfinite(g[0][0, first:back + 1, 5]).any())
+        assert bool(torch.isfinite(g[4][0, 5])) == documents
