@@ -75,10 +75,9 @@ struct Elems {  // V adjacent elements of a storage type
       } else {
         v[0] = Cvt<ET>::lo(w), v[1] = Cvt<ET>::hi(w);
       }
-    } else {  // codes plus 128
-      const uint32_t u = uint32_t(w) ^ 0x8080u;
-      v[0] = float(u & 0xffu);
-      if constexpr (V == 2) v[1] = float(u >> 8 & 0xffu);
+    } else {  // codes
+      v[0] = float(int32_t(uint32_t(w) << 24) >> 24);
+      if constexpr (V == 2) v[1] = float(int32_t(uint32_t(w) << 16) >> 24);
     }
   }
   static __device__ __forceinline__ W put(const float (&v)[V]) {
@@ -240,9 +239,6 @@ struct Steps {
     if (which < 3) to[which][threadIdx.x % kScanTile] = which == 0 ? step : step * -kLog2e;
   }
 };
-// A code plus 128 times a step, the 128 taken off: (code step) rounded once.
-__device__ __forceinline__ float held_value(float biased, float step) { return __builtin_fmaf(biased, step, -128.f * step); }
-
 // Document starts of a tile as a bit per token: a thread loads a token's id and the one before, one tile
 // before the bits are put into LDS, which is one tile before their use.
 struct Starts {
@@ -421,7 +417,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
       ca.get(j, r);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if constexpr (PACKED) x[i] = held_value(x[i], step(0, j)), r[i] = held_value(r[i], step(1, j));
+        if constexpr (PACKED) x[i] *= step(0, j), r[i] *= step(1, j);
         const float s = PACKED ? sigmoid_of(r[i]) : sigmoid(r[i]);
         const float v = rate[i] * s;
         a[j][i] = __builtin_amdgcn_exp2f(-v);
@@ -434,7 +430,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
         float g[V];
         cgt.get(j, g);
 #pragma unroll
-        for (int i = 0; i < V; ++i) u[j][i] *= PACKED ? sigmoid_of(held_value(g[i], step(2, j))) : sigmoid(g[i]);
+        for (int i = 0; i < V; ++i) u[j][i] *= PACKED ? sigmoid_of(g[i] * step(2, j)) : sigmoid(g[i]);
       }
     }
     fetch(i + 2, cx, ca, cgt);
@@ -638,13 +634,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
       rd.get(j, dy[j]);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        s[j][i] = PACKED ? sigmoid_of(held_value(r[i], step(1, j))) : sigmoid(r[i]);
+        s[j][i] = PACKED ? sigmoid_of(r[i] * step(1, j)) : sigmoid(r[i]);
       }
       if constexpr (!MAPS) {
         rx.get(j, x[j]);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          if constexpr (PACKED) x[j][i] = held_value(x[j][i], step(0, j));
+          if constexpr (PACKED) x[j][i] *= step(0, j);
           const Decay d = decay_of(s[j][i], rate[i]);
           a[j][i] = d.a;
           w[j][i] = d.b;
@@ -663,7 +659,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
           rg.get(j, sg[j]);
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            sg[j][i] = PACKED ? sigmoid_of(held_value(sg[j][i], step(2, j))) : sigmoid(sg[j][i]);
+            sg[j][i] = PACKED ? sigmoid_of(sg[j][i] * step(2, j)) : sigmoid(sg[j][i]);
             w[j][i] *= sg[j][i];
             c[j][i] *= sg[j][i];
           }

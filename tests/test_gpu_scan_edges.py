@@ -155,3 +155,30 @@ def test_infinity_stays_through_its_document(dtype, B, T, D, documents):
     for g in both(s, dy, dlast)[1]:
         assert not bool(torch.isfinite(g[0][0, first:back + 1, 5]).any())
         assert bool(torch.isfinite(g[4][0, 5])) == documents
+
+
+# ---------------------------------------------------------------------------------
+# Codes of the largest values
+# ---------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 65])
+def test_codes_of_values_past_2_to_127(dtype, D):
+    """Their steps are 2^121, 128 of which no float32 holds."""
+    s, dy, dlast = inputs(2, 40, D, dtype, True, 0, True, seed=330)
+    s["x"][0, 3, 7], s["x"][1, 9, 11] = 1.5 * 2.0**127, -1.25 * 2.0**127
+    s["gate"][0, 3, 7] = s["gate"][1, 9, 11] = -9.0
+    s["decay"][0, 11, 9], s["decay"][1, 30, 2], s["decay"][1, 31, 2] = 1.5 * 2.0**127, -1.5 * 2.0**127, 2.0**127
+    s["gate"][1, 20, 1], s["gate"][0, 20, 1] = 1.75 * 2.0**127, -1.0 * 2.0**127
+    dy = dy * 2.0**-20
+    dlast = dlast * 2.0**-20
+    packed = {n: dc.dynconv_pack8(s[n]) for n in ("x", "decay", "gate")}
+    held = [held8(to64(s[n])) for n in ("x", "decay", "gate")]
+    args = (held[0], held[1], to64(s["rate"]), held[2])
+    rest = (to64(dy), None, to64(s["state"]), to64(dlast))
+    with np.errstate(over="ignore"):
+        ref, bounds = scan_bwd(*args, *rest), bwd_bounds(*args, *rest)
+    got = dc.dynconv_scan_bwd(**{**s, **packed}, dy=dy, dstate_out=dlast, need_dstate=True)
+    for name, g, r, b in zip(GRADS, got, ref, bounds):
+        near(name, g, r, b)
