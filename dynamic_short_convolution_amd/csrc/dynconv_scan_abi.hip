@@ -223,6 +223,7 @@ dynconv_status dynconv_scan_bwd(const void* x, const int64_t* xs, const void* de
   // x, decay and gate are all of `dtype` or all in 8 bits
   if (packed != (decay_scales != nullptr) || (packed && gate != nullptr) != (gate_scales != nullptr))
     return DYNCONV_ERR_INVALID_ARG;
+  if (packed && chunks != nullptr) return DYNCONV_ERR_INVALID_ARG;  // the forward's states are of other inputs
   const int ib = packed ? 1 : eb;
   if ((st = take(&p.x, x, xs, z, ib, false, &vec, &p.shared)) != DYNCONV_OK) return st;
   if ((st = take(&p.decay, decay, as, z, ib, false, &vec, &p.shared)) != DYNCONV_OK) return st;

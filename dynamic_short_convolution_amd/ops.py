@@ -842,6 +842,8 @@ def _scan_bwd_plan(packed, x, x_scales, decay, decay_scales, gate, gate_scales, 
         if gate is not None:
             _check_packed("gate", gate, gate_scales, dy.shape)
         _check_rate(rate, D)
+        if chunks is not None:
+            raise ValueError("chunks do not go with Packed8 inputs: they are the states of the unpacked ones")
     else:
         _scan_shape(x, decay, gate, rate, 3)
         _expect("dy", dy, x.shape, x.dtype)
@@ -861,7 +863,7 @@ def dynconv_scan_bwd(x, decay, rate, dy, gate=None, seq_idx=None, state=None, ch
     with the same arguments; drate and dstate (the gradient of `state`, None unless need_dstate) are
     float32, dgate None without a gate. chunks: what the forward returned with want_chunks; without, the states
     are recomputed. x, decay and gate may all be Packed8: the gradients are then those at the values
-    that the codes stand for (chunks of the unpacked inputs would be others)."""
+    that the codes stand for, and no chunks are taken."""
     packed = isinstance(x, Packed8)
     if packed != isinstance(decay, Packed8) or (gate is not None and packed != isinstance(gate, Packed8)):
         raise ValueError("x, decay and gate are all Packed8 or none is")

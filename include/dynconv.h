@@ -520,7 +520,8 @@ size_t dynconv_scan_fwd_workspace_size(int64_t B, int64_t T, int64_t D, dynconv_
  *              (x_scales, decay_scales and, with a gate, gate_scales: uint8 [B,T,ceil(D/64)], strides
  *              [0..2], last 1; all or none): the gradients are then those at the values the codes stand for
  *   chunks     what the forward wrote, or NULL: the states are then recomputed from the inputs (one
- *              more reading of x, decay and gate; state_in is only used here)
+ *              more reading of x, decay and gate; state_in is only used here). NULL with scales
+ *              (DYNCONV_ERR_INVALID_ARG otherwise): the forward's states are of other inputs
  *   dx, ddecay, dgate  [B,T,D] of `dtype`; dgate is required with a gate
  *   drate      float32 [D], overwritten (sums in 64 bits in a fixed order)
  *   dstate_in  float32 [B,D], the gradient of the initial state, or NULL to skip
