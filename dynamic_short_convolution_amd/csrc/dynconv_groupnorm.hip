@@ -321,6 +321,7 @@ dynconv_status dynconv_groupnorm_bwd(const void* x, const int64_t* xs, const uin
   dynconv_status st = check_sizes(z, dtype, eps);
   if (st != DYNCONV_OK) return st;
   if (!z.sequence && (lengths != nullptr || stats != nullptr)) return DYNCONV_ERR_INVALID_ARG;
+  if (x_scales != nullptr && stats != nullptr) return DYNCONV_ERR_INVALID_ARG;  // the forward's are of another x
   if (C == 0) return DYNCONV_OK;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (!aligned(dweight, 4) || !aligned(dbias, 4)) return DYNCONV_ERR_UNSUPPORTED;

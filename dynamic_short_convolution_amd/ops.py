@@ -969,6 +969,8 @@ def _group_bwd_plan(groups, activation, over, eps, x, scales, dy, weight, bias, 
     code = _dtype_code(dy)
     if scales is not None:
         _check_packed("x", x, scales, dy.shape)
+        if stats is not None:
+            raise ValueError("stats do not go with a Packed8 x: they are those of the unpacked one")
     else:
         _expect("x", x, dy.shape, dy.dtype)
     (B, T, C), seq, silu = _group_args(dy.shape, dy.dtype, groups, weight, bias, gate, activation, over, lengths, stats)
@@ -983,8 +985,8 @@ def dynconv_groupnorm_bwd(x, groups: int, dy, weight=None, bias=None, gate=None,
                           over: str = "token", lengths=None, eps: float = 1e-5, stats=None):
     """(dx, dweight, dbias, dgate) of <dy, y> for dynconv_groupnorm_fwd with the same arguments, None where
     there is no such input; dweight and dbias are float32 [C]. x may be a Packed8 of what the forward took:
-    the gradients are then those at the values it stands for (pass no stats, which would be the unpacked
-    x's). stats: what the forward returned with want_stats; recomputed without."""
+    the gradients are then those at the values it stands for, and no stats are taken. stats: what the forward
+    returned with want_stats; recomputed without."""
     x, scales = x if isinstance(x, Packed8) else (x, None)
     column, ws_bytes, xs, xcs, gs, dys, new, sizes = _plan(_group_bwd_plan, (groups, activation, over, eps), x, scales, dy,
                                                            weight, bias, gate, lengths, stats)

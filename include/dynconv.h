@@ -598,7 +598,8 @@ size_t dynconv_groupnorm_fwd_workspace_size(int64_t B, int64_t T, int64_t C, int
  * Backward of dynconv_groupnorm_fwd given dy:
  *   x        the forward's, or, with x_scales (uint8 [B,T,ceil(C/64)], strides xcs[0..2], last 1), its int8
  *            codes as dynconv_pack writes them: the gradients are then those at the values they stand for
- *   stats    what the forward wrote, or NULL: recomputed from x (over sequences only)
+ *   stats    what the forward wrote, or NULL: recomputed from x (over sequences only). NULL with x_scales
+ *            (DYNCONV_ERR_INVALID_ARG otherwise): the forward's are of another x
  *   dx       [B,T,C] of `dtype`; 0 behind a sequence's tokens
  *   dweight, dbias  float32 [C], overwritten, or NULL to skip (without tokens zero)
  *   dgate    required with a gate; 0 behind a sequence's tokens

@@ -16,3 +16,11 @@ def test_scan_kept_states_do_not_go_with_codes(lib):  # noqa: F811
     packed = dc.Packed8(torch.zeros(2, 3, 8, dtype=torch.int8), torch.zeros(2, 3, 1, dtype=torch.uint8))
     with pytest.raises(ValueError, match="chunks"):
         dc.dynconv_scan_bwd(packed, packed, rate, x, chunks=torch.zeros(2, 1, 8))
+
+
+def test_groupnorm_statistics_do_not_go_with_codes(lib):  # noqa: F811
+    assert gbwd(lib, xc=XC, seq=1) == WORKSPACE
+    assert gbwd(lib, xc=XC, seq=1, st=SO) == INVALID
+    packed = dc.Packed8(torch.zeros(2, 3, 8, dtype=torch.int8), torch.zeros(2, 3, 1, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="stats"):
+        dc.dynconv_groupnorm_bwd(packed, 2, torch.zeros(2, 3, 8), over="sequence", stats=torch.zeros(2, 2, 2))
