@@ -134,16 +134,18 @@ void group_sequence_plan(GroupParams* p, int E) {
   // gradient's two passes four, each of which leaves a row of column sums or begins with a sum over the
   // groups. Such a row is paid for by 16 of a lane's tokens (27 groups of 57 bf16 channels, 26000 tokens: 187 us,
   // with 32 212; 64 groups of 16 137 and 147), by 8 where there would be fewer than two workgroups per CU (8
-  // sequences of 610 tokens, one group of 8192: 191, with 16 231, with 32 328).
-  auto cut = [&](int64_t all, int least, int32_t* chunk, int32_t* n) {
+  // sequences of 610 tokens, one group of 8192: 191, with 16 231, with 32 328). A lane adds up to `most` tokens to its sums:
+  // any number in 64 bits, 512 to the gradient's float32 sums.
+  auto cut = [&](int64_t all, int least, int64_t most, int32_t* chunk, int32_t* n) {
     const int64_t want = across < all ? all / across : 1;
     int64_t c = (int64_t(p->T) + want - 1) / want;
     if (c < least * p->tps) c = least * p->tps;
+    if (c > most * p->tps) c = most * p->tps;
     *chunk = int32_t(c);
     *n = int32_t((p->T + c - 1) / c);
   };
-  cut(2048, 8, &p->chunk, &p->nChunk);
-  cut(1024, across * (p->T / (16 * p->tps)) >= 512 ? 16 : 8, &p->gradChunk, &p->nGradChunk);
+  cut(2048, 8, INT32_MAX, &p->chunk, &p->nChunk);
+  cut(1024, across * (p->T / (16 * p->tps)) >= 512 ? 16 : 8, 512, &p->gradChunk, &p->nGradChunk);
 }
 
 namespace {

@@ -580,8 +580,8 @@ dynconv_status dynconv_unpack(const int8_t* codes, const int64_t* cs, const uint
  *                 cut to 0..T. Tokens behind them are not in the statistics, and their y is 0.
  *   stats         float32 [B,groups,2], overwritten with mean and 1 / sqrt(var + eps) (0, 0 for a
  *                 sequence without tokens) for the backward, or NULL; over sequences only
- * Sums over a sequence are held in 64 bits, those over a token's group in 32 (in 64 for groups longer than
- * the registers take). C up to 2^19, B below 2^23, B T below 2^31. Element alignment; 16 bytes at a time where
+ * The statistics' sums over a sequence are held in 64 bits, those over a token's group in 32 (in 64 for groups longer
+ * than the registers take). C up to 2^19, B below 2^23, B T below 2^31. Element alignment; 16 bytes at a time where
  * C/groups, all strides and pointers allow it. Over sequences needs
  * dynconv_groupnorm_fwd_workspace_size(...) bytes (aligned to 8), per token none. Run-to-run deterministic.
  */
@@ -603,6 +603,8 @@ size_t dynconv_groupnorm_fwd_workspace_size(int64_t B, int64_t T, int64_t C, int
  *   dx       [B,T,C] of `dtype`; 0 behind a sequence's tokens
  *   dweight, dbias  float32 [C], overwritten, or NULL to skip (without tokens zero)
  *   dgate    required with a gate; 0 behind a sequence's tokens
+ * The sums over tokens, from which over sequences the groups' means of the gradient follow too, are held in 32 bits
+ * over a workgroup's tokens, at most 512 of each lane, and in 64 over the workgroups.
  * Needs dynconv_groupnorm_bwd_workspace_size(...) bytes (aligned to 8; per token only for dweight or dbias).
  */
 dynconv_status dynconv_groupnorm_bwd(const void* x, const int64_t* xs, const uint8_t* x_scales, const int64_t* xcs,
