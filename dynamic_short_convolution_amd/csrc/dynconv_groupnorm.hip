@@ -38,7 +38,8 @@ __global__ __launch_bounds__(kThreads) void k_group_finish(const GroupParams p) 
     sum += __shfl_xor(sum, m);
     sq += __shfl_xor(sq, m);
   }
-  const int n = p.lengths != nullptr ? min(max(p.lengths[b], 0), p.T) : p.T;
+  int n = p.lengths != nullptr ? min(max(p.lengths[b], 0), p.T) : p.T;
+  if (p.Cg == 0) n = 0;  // no channels
   if (lane != 0) return;
   const double count = double(n) * p.Cg;
   const double mean = n > 0 ? sum / count : 0.0, var = n > 0 ? sq / count - mean * mean : 0.0;
@@ -240,15 +241,17 @@ hipError_t sequences(const GroupParams& p, dynconv_dtype dt, bool whole, bool pa
                              : group_sequences_f32(p, whole, packed, stage, s);
 }
 
-// Mean and scale of every (sequence, group) into p.stats.
-hipError_t statistics(const GroupParams& p, dynconv_dtype dt, bool whole, bool packed, hipStream_t s) {
-  const hipError_t e = sequences(p, dt, whole, packed, kGroupStats, s);
-  if (e != hipSuccess) return e;
+// Mean and scale of every (sequence, group) into p.stats, from the chunks' sums.
+hipError_t finish(const GroupParams& p, hipStream_t s) {
   constexpr int64_t most = int64_t(1) << 23;  // a dimension of a launch has fewer than 2^32 threads
   const int64_t blocks = (int64_t(p.B) * p.G + kThreads / 64 - 1) / (kThreads / 64);
   const dim3 grid(unsigned(blocks < most ? blocks : most), unsigned((blocks + most - 1) / most));
   hipLaunchKernelGGL(k_group_finish, grid, dim3(kThreads), 0, s, p);
   return hipGetLastError();
+}
+hipError_t statistics(const GroupParams& p, dynconv_dtype dt, bool whole, bool packed, hipStream_t s) {
+  const hipError_t e = sequences(p, dt, whole, packed, kGroupStats, s);
+  return e == hipSuccess ? finish(p, s) : e;
 }
 
 dynconv_status done(hipError_t e) { return e == hipSuccess ? DYNCONV_OK : record_hip_error(e); }
@@ -277,8 +280,15 @@ dynconv_status dynconv_groupnorm_fwd(const void* x, const int64_t* xs, const voi
   dynconv_status st = check_sizes(z, dtype, eps);
   if (st != DYNCONV_OK) return st;
   if (!z.sequence && (lengths != nullptr || stats != nullptr)) return DYNCONV_ERR_INVALID_ARG;
-  if (empty(z)) return DYNCONV_OK;
   const int eb = elem_bytes(dtype), E = 16 / eb;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (empty(z)) {  // the statistics of sequences without tokens
+    if (stats == nullptr || B == 0) return DYNCONV_OK;
+    if (!aligned(stats, 4) || groups > kMaxC) return DYNCONV_ERR_UNSUPPORTED;
+    GroupParams p{};
+    p.B = int32_t(B), p.G = int32_t(groups), p.Cg = int32_t(C / groups), p.stats = stats;
+    return done(finish(p, s));
+  }
   bool whole = C / groups % E == 0;
   GroupTensor tx{}, tg{}, ty{};
   if ((st = take(&tx, x, xs, z, eb, 16, false, &whole)) != DYNCONV_OK) return st;
@@ -293,7 +303,6 @@ dynconv_status dynconv_groupnorm_fwd(const void* x, const int64_t* xs, const voi
   p.weight = weight, p.bias = bias, p.lengths = lengths;
   p.silu = silu != 0;
   p.eps = eps;
-  const hipStream_t s = static_cast<hipStream_t>(stream);
   if (!z.sequence) return done(tokens(p, dtype, whole, false, false, s));
   const Space w = space(z, E, false, stats != nullptr);
   if (workspace == nullptr || workspace_bytes < w.total()) return DYNCONV_ERR_WORKSPACE;

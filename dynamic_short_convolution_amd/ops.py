@@ -940,7 +940,7 @@ def _group_fwd_plan(groups, activation, over, eps, want_stats, x, weight, bias, 
     (B, T, C), seq, silu = _group_args(x.shape, x.dtype, groups, weight, bias, gate, activation, over, lengths, None)
     _expect("out", out, x.shape, x.dtype)
     ws_bytes = _workspace("dynconv_groupnorm_fwd_workspace_size", B, T, C, groups, seq, int(want_stats), code)
-    return ((B, groups, 2) if want_stats and seq else None, B * T * C == 0, ws_bytes, _st(x, 3), _st(gate, 3),
+    return ((B, groups, 2) if want_stats and seq else None, ws_bytes, _st(x, 3), _st(gate, 3),
             _dense(x.shape, 3) if out is None else _st(out, 3), (B, T, C, groups, seq, silu, float(eps), code))
 
 
@@ -952,13 +952,11 @@ def dynconv_groupnorm_fwd(x, groups: int, weight=None, bias=None, gate=None, act
     SiLU with activation="silu", else nothing. Over sequences, lengths (int32 [B], 0 to T) says how many tokens
     of each count; y is 0 behind them. With want_stats returns (y, stats) for dynconv_groupnorm_bwd: float32
     [B,groups,2] over sequences, None per token (there the backward has the group in registers)."""
-    kept, nothing, ws_bytes, xs, gs, ys, sizes = _plan(_group_fwd_plan, (groups, activation, over, eps, want_stats), x, weight,
-                                                       bias, gate, lengths, out)
+    kept, ws_bytes, xs, gs, ys, sizes = _plan(_group_fwd_plan, (groups, activation, over, eps, want_stats), x, weight, bias,
+                                              gate, lengths, out)
     dev = _require_device(x, weight, bias, gate, lengths, out)
     y = x.new_empty(x.shape) if out is None else out
-    stats = None
-    if kept is not None:  # without a token nothing is launched that would write them
-        stats = (torch.zeros if nothing else torch.empty)(kept, dtype=torch.float32, device=dev)
+    stats = torch.empty(kept, dtype=torch.float32, device=dev) if kept is not None else None
     work = x.new_empty(ws_bytes, dtype=torch.uint8) if ws_bytes else None
     _launch("dynconv_groupnorm_fwd", dev, x.data_ptr(), xs, _dp(weight), _dp(bias), _dp(gate), gs, _dp(lengths), y.data_ptr(),
             ys, _dp(stats), *sizes, _dp(work), ws_bytes)

@@ -30,3 +30,14 @@ def test_column_sums_of_many_long_sequences():
     dy = torch.full((1, 1, C), c, device="cuda").expand(B, T, C)
     dbias = dc.dynconv_groupnorm_bwd(x, C, dy, weight=torch.ones(C, device="cuda"), bias=torch.zeros(C, device="cuda"), over="sequence")[2]
     assert (np.abs(to64(dbias) - B * T * c) <= (48 + 512) * U * B * T * c).all()
+
+
+def test_statistics_without_tokens_from_the_entry_point():
+    """T of 0: mean 0 and factor 0 of every sequence and group."""
+    x = torch.zeros(1, dtype=torch.bfloat16, device="cuda")
+    for B, C, groups in ((3, 64, 4), (2, 0, 5)):
+        stats = torch.full((B, groups, 2), float("nan"), device="cuda")
+        s = _lib.strides((64, 64, 1))
+        st = _lib.load().dynconv_groupnorm_fwd(x.data_ptr(), s, None, None, None, None, None, x.data_ptr(), s, stats.data_ptr(), B, 0, C, groups,
+                                               1, 0, 1e-5, 1, None, 0, torch.cuda.current_stream().cuda_stream)
+        assert st == 0 and float(stats.abs().max()) == 0.0
