@@ -98,6 +98,9 @@ struct Elems {  // V adjacent elements of a storage type
 // 1 / (1 + 2^e): the sigmoid of -e log 2.
 __device__ __forceinline__ float sigmoid_of(float e) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(e)); }
 __device__ __forceinline__ float sigmoid(float z) { return sigmoid_of(z * -kLog2e); }
+// 1 - s for s = 1 / (1 + p), without the difference, of which nothing is left for an open gate: p s, and 1 where p is
+// infinite and s 0 (of infinity times 0, a NaN, the minimum is its other operand; where p is a NaN, s is one too).
+__device__ __forceinline__ float rest_of(float p, float s) { return fminf(p * s, 1.f); }
 
 // 1 - a^2 for a = 2^-v, v >= 0. At small v the difference would cancel: a polynomial for
 // (1 - 2^-2v) / v, interpolated at the six Chebyshev points of [0, 0.36] (1.2e-7 of the value in float32);
@@ -624,44 +627,46 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
   if constexpr (DOCS || PACKED) __syncthreads();
   for (int turn = 0; turn < n; ++turn) {
     const int k = order(turn), t0 = k * kScanTile, last = min(p.T - t0, kScanTile) - 1, half = turn & 1;
-    // f: what passes a token (a, or 0 where it starts a document); w = b sigmoid(gate); c = sigmoid(gate) a^2 / b
-    float a[L][V], s[L][V], w[L][V], c[L][V], sg[L][V], x[L][V], hb[L][V], dy[L][V], hk[V];
+    // s = sigmoid(decay), sr = 1 - s; w = b sigmoid(gate); c = sigmoid(gate) x a^2 / b; xg = x (1 - sigmoid(gate)); hb: the
+    // inputs b sigmoid(gate) x, then the states before the tokens
+    float a[L][V], s[L][V], sr[L][V], w[L][V], c[L][V], xg[L][V], x[L][V], hb[L][V], dy[L][V], hk[V];
     auto step = [&](int which, int j) { return PACKED ? steps[half][which][me.run * L + j] : 0.f; };
 #pragma unroll
     for (int j = 0; j < L; ++j) {
       float r[V];
       ra.get(j, r);
       rd.get(j, dy[j]);
+      if constexpr (!MAPS) rx.get(j, x[j]);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        s[j][i] = PACKED ? sigmoid_of(r[i] * step(1, j)) : sigmoid(r[i]);
-      }
-      if constexpr (!MAPS) {
-        rx.get(j, x[j]);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
+        const float pe = __builtin_amdgcn_exp2f(r[i] * (PACKED ? step(1, j) : -kLog2e));
+        s[j][i] = __builtin_amdgcn_rcpf(1.f + pe);
+        if constexpr (!MAPS) {
           if constexpr (PACKED) x[j][i] *= step(0, j);
+          sr[j][i] = rest_of(pe, s[j][i]);
           const Decay d = decay_of(s[j][i], rate[i]);
           a[j][i] = d.a;
           w[j][i] = d.b;
           c[j][i] = d.a * d.a * d.rb;
-          sg[j][i] = 1.f;
+          xg[j][i] = 0.f;
+        } else {
+          a[j][i] = __builtin_amdgcn_exp2f(-(rate[i] * s[j][i]));
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) a[j][i] = __builtin_amdgcn_exp2f(-(rate[i] * s[j][i]));
       }
     }
     if constexpr (!MAPS) {
       if (gated) {  // one branch: between branches the tokens' chains could not be interleaved
 #pragma unroll
         for (int j = 0; j < L; ++j) {
-          rg.get(j, sg[j]);
+          float g[V];
+          rg.get(j, g);
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            sg[j][i] = PACKED ? sigmoid_of(sg[j][i] * step(2, j)) : sigmoid(sg[j][i]);
-            w[j][i] *= sg[j][i];
-            c[j][i] *= sg[j][i];
+            const float pg = __builtin_amdgcn_exp2f(g[i] * (PACKED ? step(2, j) : -kLog2e));
+            const float sg = __builtin_amdgcn_rcpf(1.f + pg);
+            w[j][i] *= sg;
+            c[j][i] *= sg;
+            xg[j][i] = rest_of(pg, sg);
           }
         }
       }
@@ -682,10 +687,25 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) hk[i] = MAPS ? 0.f : kept[i];
+    if constexpr (!MAPS) {
+#pragma unroll
+      for (int j = 0; j < L; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {  // x itself is not kept
+          hb[j][i] = w[j][i] * x[j][i];
+          c[j][i] *= x[j][i];
+          xg[j][i] *= x[j][i];
+        }
+    }
     fetch(turn + 1);
     uint32_t first = 0;  // tokens that start a document: nothing passes through them, forwards or backwards
     if constexpr (DOCS) first = Starts::of_run(starts[half], me.run, L);
-    auto pass = [&](int j, int i) { return DOCS && (first >> j & 1) ? -0.f : a[j][i]; };
+    if constexpr (DOCS) {
+#pragma unroll
+      for (int j = 0; j < L; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[j][i] = first >> j & 1 ? -0.f : a[j][i];
+    }
     float A[V], H[V], E[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) A[i] = 1.f, H[i] = 0.f, E[i] = 0.f;
@@ -693,10 +713,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
     for (int j = 0; j < L; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float f = pass(j, i);
+        const float f = a[j][i];
         A[i] = chain<DOCS>(f, A[i]);
         if constexpr (!MAPS) {
-          hb[j][i] = w[j][i] * x[j][i];
           H[i] = through<DOCS>(f, hb[j][i], H[i]);
         }
       }
@@ -704,7 +723,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
     for (int j = L - 1; j >= 0; --j)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float f = pass(j, i), dh = dy[j][i] + E[i];
+        const float f = a[j][i], dh = dy[j][i] + E[i];
         E[i] = DOCS && forgets(f) ? 0.f : f * dh;
       }
     float pA[V], pH[V], rA[V], rE[V], B[V];  // the maps of the lane groups before and behind this one
@@ -774,7 +793,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
       for (int j = 0; j < L; ++j)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float f = pass(j, i), before = DOCS && forgets(f) ? 0.f : h[i];
+          const float f = a[j][i], before = DOCS && forgets(f) ? 0.f : h[i];
           h[i] = through<DOCS>(f, hb[j][i], h[i]);
           hb[j][i] = before;
         }
@@ -791,11 +810,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
         for (int i = 0; i < V; ++i) {
           const float dh = dy[j][i] + e[i];
           dx[i] = dh * w[j][i];
-          dg[i] = dx[i] * x[j][i] * (1.f - sg[j][i]);
+          dg[i] = dx[i] * xg[j][i];
           const float ad = a[j][i] * dh;
-          const float dl = s[j][i] * __builtin_fmaf(ad, hb[j][i], -c[j][i] * dh * x[j][i]);
+          const float dl = s[j][i] * __builtin_fmaf(ad, hb[j][i], -c[j][i] * dh);
           sum[i] -= row + j > last ? 0.f : dl;  // of a token that does not exist it may be 0 times infinity
-          dr[i] = back[i] * dl * (1.f - s[j][i]);
+          dr[i] = back[i] * dl * sr[j][i];
           e[i] = DOCS && (first >> j & 1) ? 0.f : ad;
         }
         store_row(pdx, rdx, j, dx);

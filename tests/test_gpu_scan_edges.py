@@ -182,3 +182,32 @@ def test_codes_of_values_past_2_to_127(dtype, D):
     got = dc.dynconv_scan_bwd(**{**s, **packed}, dy=dy, dstate_out=dlast, need_dstate=True)
     for name, g, r, b in zip(GRADS, got, ref, bounds):
         near(name, g, r, b)
+
+
+# ---------------------------------------------------------------------------------
+# Open gates
+# ---------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("kept", ["whole", "8 bits"])
+def test_gradients_of_open_gates(kept, dtype):
+    """ddecay and dgate carry the factors 1 - sigmoid, which are small for open gates: the bounds of the others times
+    them, and (|z| + 6) u of their own."""
+    s, dy, dlast = inputs(2, 260, 66, dtype, True, 30, True, seed=340)
+    s["decay"][:, :, :40] = torch.linspace(4.0, 20.0, 40).to(TD[dtype]).cuda()
+    s["gate"][:, :, 20:] = torch.linspace(4.0, 20.0, 46).to(TD[dtype]).cuda()
+    x, decay, gate = (to64(s[n]) for n in ("x", "decay", "gate"))
+    given = dict(s)
+    if kept == "8 bits":
+        given.update({n: dc.dynconv_pack8(s[n]) for n in ("x", "decay", "gate")})
+        x, decay, gate = held8(x), held8(decay), held8(gate)
+    rest = (to64(dy), s["seq_idx"].cpu().numpy(), to64(s["state"]), to64(dlast))
+    args = (x, decay, to64(s["rate"]), gate)
+    ref, bounds = scan_bwd(*args, *rest), bwd_bounds(*args, *rest)
+    got = dc.dynconv_scan_bwd(**given, dy=dy, dstate_out=dlast, need_dstate=True)
+    for i, z in ((1, decay), (3, gate)):
+        own = (np.abs(z) + 6) * U
+        near(GRADS[i], got[i], ref[i], bounds[i] / (1.0 + np.exp(z)) * (1 + own) + own * np.abs(ref[i]))
+    for i in (0, 2, 4):
+        near(GRADS[i], got[i], ref[i], bounds[i])
