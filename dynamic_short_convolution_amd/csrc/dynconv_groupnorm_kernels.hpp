@@ -168,11 +168,11 @@ template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
 }
-// Sum over the LPR lanes of a row, in every one of them, without LDS up to a wave: lanes 1 and 2 apart
+// Sums over the LPR lanes of a row, in every one of them, without LDS up to a wave: lanes 1 and 2 apart
 // within a quad, 4 and 8 apart by mirrors (whose quads and halves are equal by then), 16 and 32
-// apart by swaps. `red`: 4 floats per call site.
+// apart by swaps. `red`: one array per call site.
 template <int LPR>
-__device__ __forceinline__ float row_sum(float x, float* red) {
+__device__ __forceinline__ float wave_sum(float x) {
   if constexpr (LPR >= 2) x += dpp<0xB1>(x);
   if constexpr (LPR >= 4) x += dpp<0x4E>(x);
   if constexpr (LPR >= 8) x += dpp<0x141>(x);
@@ -185,13 +185,22 @@ __device__ __forceinline__ float row_sum(float x, float* red) {
     const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
   }
-  if constexpr (LPR == 256) {
-    __syncthreads();  // the previous sum is read
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = (red[0] + red[1]) + (red[2] + red[3]);
-  }
   return x;
+}
+template <int LPR, int N>
+__device__ __forceinline__ void row_sums(float (&x)[N], float (&red)[N][4]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = wave_sum<LPR>(x[i]);
+  if constexpr (LPR == 256) {
+    __syncthreads();  // the previous sums are read
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) red[i][threadIdx.x >> 6] = x[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = (red[i][0] + red[i][1]) + (red[i][2] + red[i][3]);
+  }
 }
 template <int LPR>
 __device__ __forceinline__ double row_sum(double x, double* red) {
@@ -224,10 +233,46 @@ __device__ __forceinline__ Token token_at(const GroupParams& p, int64_t token) {
   return {b, int64_t(uint32_t(token) - b * uint32_t(p.T))};
 }
 
+// A row's deviations from its mean, in place of x, and what turns them into n = d rstd + shift. A first mean
+// is off by some roundings of itself, which is much beside a small deviation (1100 channels of 1000.1 made n 0.02 instead of
+// 0); the mean of the deviations from it is off by as many roundings of that.
+struct Norm {
+  float rstd, shift;
+};
+template <int E, bool WHOLE, int LPR, int NV>
+__device__ __forceinline__ Norm normalise(float (&x)[NV][E], const int (&skip)[NV], int n, float inv, float eps, float (&red1)[1][4],
+                                          float (&red2)[2][4]) {
+  typedef Piece<E, WHOLE> P;
+  float sum[1] = {0.f};
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (skip[i] < E) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum[0] += P::counts(e, skip[i], n) ? x[i][e] : 0.f;
+    }
+  row_sums<LPR>(sum, red1);
+  const float mean = sum[0] * inv;
+  float of[2] = {0.f, 0.f};  // the deviations, their squares
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (skip[i] < E) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        x[i][e] -= mean;
+        const float d = P::counts(e, skip[i], n) ? x[i][e] : 0.f;
+        of[0] += d, of[1] += d * d;
+      }
+    }
+  row_sums<LPR>(of, red2);
+  const float off = of[0] * inv, var = of[1] * inv - off * off;
+  const float rstd = 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);
+  return {rstd, -off * rstd};
+}
+
 template <typename ET, int E, bool WHOLE, int LPR, int NV>
 __global__ __launch_bounds__(kThreads) void k_group_fwd(const GroupParams p) {
   constexpr int NA = NV > 0 ? NV : 1;
-  __shared__ float red[2][4];
+  __shared__ float red1[1][4], red2[2][4];
   __shared__ double dred[2][4];
   const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
   const int tsub = slot / p.gpw, gsub = slot - tsub * p.gpw;
@@ -239,11 +284,10 @@ __global__ __launch_bounds__(kThreads) void k_group_fwd(const GroupParams p) {
   const bool gated = p.gate.p != nullptr, silu = p.silu != 0;
   const float inv = 1.f / float(p.Cg);
   const int64_t tokens = int64_t(p.B) * p.T, step = int64_t(gridDim.x) * p.tpw;
-  auto finish = [&](const float (&x)[E], const float (&g)[E], const float (&w)[E], const float (&bi)[E], float mean,
-                    float rstd, int64_t off) {
+  auto finish = [&](const float (&d)[E], const float (&g)[E], const float (&w)[E], const float (&bi)[E], Norm at, int64_t off) {
     float y[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = value((x[e] - mean) * rstd, w[e], bi[e], silu, gated, g[e]);
+    for (int e = 0; e < E; ++e) y[e] = value(__builtin_fmaf(d[e], at.rstd, at.shift), w[e], bi[e], silu, gated, g[e]);
     store<ET, E, WHOLE>(y, p.y.p, off, n);
   };
   if constexpr (NV > 0) {
@@ -278,27 +322,13 @@ __global__ __launch_bounds__(kThreads) void k_group_fwd(const GroupParams p) {
 #pragma unroll
         for (int e = 0; e < E; ++e) x[i][e] = nx[i][e], g[i][e] = ng[i][e];
       if (tok0 + step < tokens) fetch(tok0 + step + tsub);
-      float sum = 0.f, sq = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (skip[i] < E) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) sum += P::counts(e, skip[i], n) ? x[i][e] : 0.f;
-        }
-      const float mean = row_sum<LPR>(sum, red[0]) * inv;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (skip[i] < E) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) sq += P::counts(e, skip[i], n) ? (x[i][e] - mean) * (x[i][e] - mean) : 0.f;
-        }
-      const float rstd = 1.f / sqrtf(row_sum<LPR>(sq, red[1]) * inv + p.eps);
+      const Norm norm = normalise<E, WHOLE, LPR, NV>(x, skip, n, inv, p.eps, red1, red2);
       if (mine && tok0 + tsub < tokens) {
         const Token q = token_at(p, tok0 + tsub);
         const int64_t oy = q.b * p.y.s0 + q.t * p.y.s1;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if (skip[i] < E) finish(x[i], g[i], w[i], bi[i], mean, rstd, oy + cc[i]);
+          if (skip[i] < E) finish(x[i], g[i], w[i], bi[i], norm, oy + cc[i]);
       }
     }
   } else {
@@ -328,7 +358,9 @@ __global__ __launch_bounds__(kThreads) void k_group_fwd(const GroupParams p) {
         for (int e = 0; e < E; ++e) w[e] = 1.f, bi[e] = 0.f;
         if (p.weight != nullptr) load<ET, E, WHOLE>(w, p.weight, c0 + c, n);
         if (p.bias != nullptr) load<ET, E, WHOLE>(bi, p.bias, c0 + c, n);
-        finish(x, g, w, bi, float(mean), rstd, q.b * p.y.s0 + q.t * p.y.s1 + c0 + c);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] -= float(mean);
+        finish(x, g, w, bi, Norm{rstd, 0.f}, q.b * p.y.s0 + q.t * p.y.s1 + c0 + c);
       }
     }
   }
@@ -340,7 +372,7 @@ template <typename ET, int E, bool WHOLE, int LPR, int NV, bool PACKED>
 __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
   using IT = std::conditional_t<PACKED, i8_t, ET>;
   constexpr int NA = NV > 0 ? NV : 1;
-  __shared__ float red[4][4];
+  __shared__ float red1[1][4], red2[2][2][4];
   __shared__ double dred[4][4];
   extern __shared__ float fold[];  // NV > 0: [tpw][gpw Cg]
   const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
@@ -397,35 +429,21 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
 #pragma unroll
         for (int e = 0; e < E; ++e) x[i][e] = nx[i][e], dy[i][e] = ndy[i][e], g[i][e] = ng[i][e];
       if (tok0 + step < tokens) fetch(tok0 + step + tsub);
-      float sum = 0.f, sq = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (skip[i] < E) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) sum += P::counts(e, skip[i], n) ? x[i][e] : 0.f;
-        }
-      const float mean = row_sum<LPR>(sum, red[0]) * inv;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (skip[i] < E) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) sq += P::counts(e, skip[i], n) ? (x[i][e] - mean) * (x[i][e] - mean) : 0.f;
-        }
-      const float rstd = 1.f / sqrtf(row_sum<LPR>(sq, red[1]) * inv + p.eps);
-      float s1 = 0.f, s2 = 0.f;
+      const Norm at = normalise<E, WHOLE, LPR, NV>(x, skip, n, inv, p.eps, red1, red2[0]);
+      float m[2] = {0.f, 0.f};  // of dn, of dn n
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (skip[i] < E) {
           float dz[E], dg[E];
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            x[i][e] = (x[i][e] - mean) * rstd;
+            x[i][e] = __builtin_fmaf(x[i][e], at.rstd, at.shift);
             dg[e] = 0.f;
             dz[e] = slope(x[i][e], w[i][e], bi[i][e], silu, gated, g[i][e], dy[i][e], dg[e]);
             dy[i][e] = dz[e] * w[i][e];
             const bool counts = P::counts(e, skip[i], n);
-            s1 += counts ? dy[i][e] : 0.f;
-            s2 += counts ? dy[i][e] * x[i][e] : 0.f;
+            m[0] += counts ? dy[i][e] : 0.f;
+            m[1] += counts ? dy[i][e] * x[i][e] : 0.f;
           }
           if (have) {
             if (gated) store<ET, E, WHOLE>(dg, p.dgate.p, odg + cc[i], n);
@@ -433,15 +451,15 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
             for (int e = 0; e < E; ++e) dw[i][e] += dz[e] * x[i][e], db[i][e] += dz[e];
           }
         }
-      s1 = row_sum<LPR>(s1, red[2]) * inv;
-      s2 = row_sum<LPR>(s2, red[3]) * inv;
+      row_sums<LPR>(m, red2[1]);
+      m[0] *= inv, m[1] *= inv;
       if (have) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
           if (skip[i] < E) {
             float dx[E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) dx[e] = rstd * (dy[i][e] - s1 - x[i][e] * s2);
+            for (int e = 0; e < E; ++e) dx[e] = at.rstd * (dy[i][e] - m[0] - x[i][e] * m[1]);
             store<ET, E, WHOLE>(dx, p.dx.p, odx + cc[i], n);
           }
       }

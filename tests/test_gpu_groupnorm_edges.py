@@ -41,3 +41,28 @@ def test_statistics_without_tokens_from_the_entry_point():
         st = _lib.load().dynconv_groupnorm_fwd(x.data_ptr(), s, None, None, None, None, None, x.data_ptr(), s, stats.data_ptr(), B, 0, C, groups,
                                                1, 0, 1e-5, 1, None, 0, torch.cuda.current_stream().cuda_stream)
         assert st == 0 and float(stats.abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("width", [3, 57, 64, 100, 515, 1100, 2050, 4100, 9000])
+@pytest.mark.parametrize("over", ["token", "sequence"])
+def test_groups_without_deviation(width, over, dtype):
+    """n is (x - mean) / sqrt(eps): a mean off by one rounding of 1000 makes it 0.02. The first mean may be off by 48 u of
+    1000, the mean of the deviations from it by 48 u of that. The variance over 64-bit sums is off by some 2^-53 of
+    1000^2, eight of which are (1000^2 / eps) 2^-50 / 2 of its root."""
+    td = TD[dtype]
+    x = torch.full((2, 3, 2 * width), 1000.0, dtype=td, device="cuda")
+    if dtype == "f32":
+        x += 0.1
+    dy = rand(2, 2, 3, 2 * width, dtype=td)
+    allowed = 50 * U * (50 * U * 1000.1) / np.sqrt(1e-5)
+    y = dc.dynconv_groupnorm_fwd(x, 2, over=over)
+    assert float(y.abs().max()) <= allowed
+    # dx is then (dy - mean(dy)) / sqrt(eps)
+    dx = to64(dc.dynconv_groupnorm_bwd(x, 2, dy, over=over)[0])
+    d = to64(dy).reshape(2, 3, 2, width)
+    m = d.mean(-1 if over == "token" else (1, 3), keepdims=True)
+    ref = ((d - m) / np.sqrt(1e-5)).reshape(dx.shape)
+    size = np.abs(d).max() / np.sqrt(1e-5)
+    half = {"f32": U, "bf16": 2.0**-8, "f16": 2.0**-11}[dtype]
+    assert (np.abs(dx - ref) <= (200 * U + 1000.1**2 / 1e-5 * 2.0**-51) * size + 1.01 * half * np.abs(ref)).all()
