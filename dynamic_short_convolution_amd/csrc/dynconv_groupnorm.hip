@@ -97,8 +97,11 @@ hipError_t group_sum(const float* part, int64_t n, int64_t C, int64_t batches, f
 }  // namespace
 
 // The fewest lanes that hold a row in one piece each (groups of 16 bf16 channels on 4 lanes instead of 2: forward 91
-// us, not 52); then more pieces per lane, as far as the backward's registers go: 2048 bf16 channels on 64 lanes of
-// 4 pieces took 190 us, on 256 lanes of one 107 (4882 tokens of 8 sequences, 40 million elements).
+// us, not 52): 2048 bf16 channels on 64 lanes of 4 pieces took the backward 190 us, on 256 lanes of one 107 (40
+// million elements). Then more pieces per lane, which the backward pays for with its registers: two pieces on 256 lanes
+// take 200 to 215 of them (4096 channels 120 us, the ragged 2050 244), four 370 to 398, one wave per SIMD (8192 channels
+// 225, 4100 396); longer rows are read twice, with the column sums added to memory token by token (10001 channels 474,
+// 20000 429). The forward of the same takes 48 to 108.
 GroupPlan group_plan(int64_t Cg, int E) {
   const int64_t loads = (Cg + E - 1) / E;  // of the row
   for (int lpr : {1, 2, 4, 8, 16, 32, 64})

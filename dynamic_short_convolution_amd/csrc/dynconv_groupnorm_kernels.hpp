@@ -221,8 +221,9 @@ __device__ __forceinline__ double row_sum(double x, double* red) {
 // squares around it are two sums over registers. Longer rows are read again. A workgroup takes gpw
 // neighbouring groups of tpw tokens at a time, a lane the same channels every time, the next tokens' loads under
 // way meanwhile (those after them too: 230 us against 232, and 50 against 45 for ragged float32 groups).
-// Bound by memory: 32768 tokens of 16 groups of 128 with gate, bf16, forward 91 to 103 us (3.9 to 4.4 TB/s),
-// backward 130 to 150 (4.5 to 5.2); 5003 tokens of 27 groups of 57, float32, 17 and 25 us (3.6 and 3.7).
+// Bound by memory: 32768 tokens of 16 groups of 128 with gate, bf16, forward 94 to 109 us (3.7 to 4.3 TB/s),
+// backward 132 to 155 (4.3 to 5.1), from 8-bit x 130 to 152; 5003 tokens of 27 groups of 57, float32, 17 and 25 us (3.6
+// and 3.7).
 // ---------------------------------------------------------------------------------
 struct Token {
   int64_t b, t;
@@ -575,8 +576,9 @@ __global__ __launch_bounds__(kThreads) void k_group_bwd(const GroupParams p) {
 // wide one at a time) of a run of tokens; a lane keeps its channels and goes along the tokens, tps
 // of them side by side. x is read twice: once for the sums, once for the result; the backward reads x and dy for
 // the column sums, from which the groups' means follow, and again for the result. Bound by memory: 8
-// sequences of 0 to 4096 tokens (half of them in all), 32 groups of 64, bf16: sums 26 to 29 us, result 36 to 38, column
-// sums 43 to 45, gradient 52 to 54 (2.4 to 5 TB/s), three small sums 17. With float32 in place of float64 sums the
+// sequences of 0 to 4096 tokens (half of them in all), 32 groups of 64, bf16: sums 25 to 28 us, result 36 to 38, column
+// sums 43 to 45, gradient 50 to 54 (2.4 to 5 TB/s), three small sums 17; from 8-bit x sums 19, column sums 47, gradient
+// 52 to 54. With float32 in place of float64 sums the
 // first pass takes as long.
 // ---------------------------------------------------------------------------------
 struct Place {

@@ -15,10 +15,10 @@
 //
 // What bounds it is the time that its loads take to come: one workgroup per CU (its registers: 8 waves of up to
 // 256) reads 128-byte pieces of rows that lie a row apart. The forward has two tiles' loads under way, the
-// backward one. 8 sequences of 4096 tokens, 2048 channels, bf16 (537 MB forward, 940 MB backward): 133 to
-// 137 us (3.9 to 4.0 TB/s; the same reads and writes with a sum in place of the scan take 118 to 122, however
-// wide, deep or many the loads, and one after the other through memory 96), backward 206 to 220 us (4.3
-// to 4.6 TB/s). Vector units are busy 47 % of the forward's time and 58 % of the backward's. Both directions
+// backward one. 8 sequences of 4096 tokens, 2048 channels, bf16 (537 MB forward, 940 MB backward): 128 to
+// 134 us (4.0 to 4.2 TB/s; the same reads and writes with a sum in place of the scan take 118 to 122, however
+// wide, deep or many the loads, and one after the other through memory 96), backward 206 to 226 us (4.2
+// to 4.6 TB/s). Vector units are busy 48 % of the forward's time and 60 % of the backward's. Both directions
 // when they took 342 us: with 32 channels per workgroup 438, with 16 waves of 8 elements per lane 394.
 #pragma once
 
@@ -333,9 +333,10 @@ __device__ __forceinline__ void write_map(float (&m)[kScanCols], int chl, const 
 // Forward: the outputs (and the kept and last states), the kept states alone (for a backward that has to
 // recompute them), or only the map of the segment, into p.maps; with segment 0 the initial state too. That pass
 // goes from the last tile to the first, so that what it read last, which the memory-side cache still
-// holds, is what the pass behind it reads first (32768 tokens of 2048 channels, 8 segments: 105 us and then
-// 118; the other way round 216 in all, now 210). The states alone, from 8-bit inputs of 8 x 4096 x 2048: 108 us (a
-// training step of 554 us; with the outputs' variant, its stores switched off at run time, 565).
+// holds, is what the pass behind it reads first (32768 tokens of 2048 channels, 8 segments: 96 to 106 us and then
+// 111 to 119; a call 209, the other way round 216 where it took 210). The states alone of 8 x 4096 x 2048: from 8-bit
+// inputs 97 to 105 us, from bf16 113 to 119 (the outputs' variant, its stores switched off at run time, made a training
+// step from 8-bit inputs 565 us that takes 554 with this one).
 // ---------------------------------------------------------------------------------
 enum Want { kOutputs, kStates, kMaps };
 template <typename ET, int V, bool PACKED, bool DOCS, Want WANT>
@@ -547,7 +548,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_fwd(const ScanParams p) {
 
 // ---------------------------------------------------------------------------------
 // Backward, tiles from the last to the first. MAPS: only the segment's map of e, from the first to the last.
-// From 8-bit inputs 197 to 211 us where 16-bit ones take 206 to 220 (8 x 4096 x 2048): the writes remain.
+// From 8-bit inputs 202 to 215 us where 16-bit ones take 206 to 226 (8 x 4096 x 2048): the writes remain.
 // ---------------------------------------------------------------------------------
 template <typename ET, int V, bool PACKED, bool DOCS, bool MAPS>
 __global__ __launch_bounds__(kThreads, 2) void k_scan_bwd(const ScanParams p) {
@@ -885,10 +886,11 @@ hipError_t launch_docs(const ScanParams& p, bool bwd, hipStream_t s) {
   return p.seg != nullptr ? launch<ET, V, PACKED, true>(p, bwd, s) : launch<ET, V, PACKED, false>(p, bwd, s);
 }
 
-// Two channels per lane where vec allows (8 sequences of 4096 tokens, 2048 channels: bf16 forward 130 us, with
-// one 135, backward 228 and 244), but float32 inputs go one per lane: 64 lanes' 4 bytes are whole rows of a
-// tile as well, and the backward with documents would not fit its registers (390 us, with two 519; the others
-// are the same within 1 %). With inputs in 8 bits two again (395 us, with one 410).
+// Two channels per lane where vec allows (calls of 8 sequences of 4096 tokens, 2048 channels, bf16, with documents:
+// forward 137 us, with one 146, backward 237 and 245; from 8-bit inputs 351 and 373), but float32 inputs go one per
+// lane: 64 lanes' 4 bytes are whole rows of a tile as well, and the backward with two would not fit its registers (8
+// sequences of 2048 tokens: 200 us, with two 227, with documents 211 and 314; forward 116 and 113, 120 and 114). With
+// float32 inputs in 8 bits two again (191 us, with one 198).
 template <typename ET>
 hipError_t run(const ScanParams& p, int vec, bool packed, bool bwd, hipStream_t s) {
   if (packed) return vec == 2 ? launch_docs<ET, 2, true>(p, bwd, s) : launch_docs<ET, 1, true>(p, bwd, s);
