@@ -265,7 +265,8 @@ __device__ __forceinline__ Norm normalise(float (&x)[NV][E], const int (&skip)[N
       }
     }
   row_sums<LPR>(of, red2);
-  const float off = of[0] * inv, var = of[1] * inv - off * off;
+  // one rounding: where the squares are past float32, the variance is infinite (n is 0) and not the difference of two
+  const float off = of[0] * inv, var = __builtin_fmaf(-off, off, of[1] * inv);
   const float rstd = 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);
   return {rstd, -off * rstd};
 }

@@ -66,3 +66,13 @@ def test_groups_without_deviation(width, over, dtype):
     size = np.abs(d).max() / np.sqrt(1e-5)
     half = {"f32": U, "bf16": 2.0**-8, "f16": 2.0**-11}[dtype]
     assert (np.abs(dx - ref) <= (200 * U + 1000.1**2 / 1e-5 * 2.0**-51) * size + 1.01 * half * np.abs(ref)).all()
+
+
+@pytest.mark.parametrize("width", [57, 64, 515, 2050])
+def test_squares_past_float32(width):
+    """Per token the variance of such values is infinite in float32: n is 0, not NaN, whatever the mean is off by."""
+    x = rand(3, 2, 3, 2 * width) * 1e33 + 1e33
+    w, b = rand(4, 2 * width), rand(5, 2 * width)
+    assert torch.equal(dc.dynconv_groupnorm_fwd(x, 2, w, b), b.expand(2, 3, 2 * width))
+    dx, dw, db, _ = dc.dynconv_groupnorm_bwd(x, 2, torch.ones_like(x), w, b)
+    assert float(dx.abs().max()) == 0.0 == float(dw.abs().max()) and bool((db == 6.0).all())
